@@ -16,7 +16,9 @@
  * Conventions shared by every entry point
  *   - All tensors are float32, C-contiguous, in DEVICE memory owned by the
  *     caller; positions are int32 in device memory.  (kvs_decode_step_host
- *     is the exception: its inputs and result are in host memory.)  The
+ *     is the exception: its inputs and result are in host memory.  The
+ *     paged-cache and logit entry points also take 16-bit types and row
+ *     strides, each as it says.)  The
  *     library never allocates, frees or synchronises; it does not keep
  *     pointers after a call returns.
  *   - Layouts (M sequences, H = num_heads query heads, Hkv = num_kv_heads,
@@ -72,9 +74,15 @@ typedef enum kvs_status {
   KVS_ERR_POSITION = 7,    /* device: a position outside [0, max_len) */
   KVS_ERR_TIMEOUT = 8,     /* device: a bounded pipeline wait expired */
   KVS_ERR_SLOT = 9,        /* device: a cache slot outside [0, num_slots) */
-  KVS_ERR_MEMORY = 10      /* the device could not provide memory the library
+  KVS_ERR_MEMORY = 10,     /* the device could not provide memory the library
                               itself holds (kvs_flash_decode_static) */
+  KVS_ERR_PAGE = 11,       /* device: a page number outside [0, num_pages) */
+  KVS_ERR_ROWS = 12        /* device: row offsets that decrease, leave
+                              [0, num_rows], or span more than max_new rows */
 } kvs_status;
+
+/* Element types of the paged-cache and logit entry points. */
+typedef enum kvs_dtype { KVS_F32 = 0, KVS_F16 = 1, KVS_BF16 = 2 } kvs_dtype;
 
 /* A cudaStream_t, passed as an opaque pointer so this header needs no CUDA
  * include. */
@@ -511,6 +519,205 @@ int kvs_prefill_attention(const float *q, const float *k, const float *v,
                           float *out, int num_heads, int seq_len, int head_dim,
                           int causal, void *workspace, size_t workspace_bytes,
                           int *d_status, kvs_stream_t stream);
+
+/*
+ * A paged KV cache: the rows of all sequences in pages of page_size rows,
+ * handed to sequences in any order (the layout of one page is that of the
+ * dense cache of the other entry points, [Hkv][rows][D]).
+ */
+typedef struct kvs_paged_cache {
+  void *k_pages, *v_pages; /* device, 16-byte aligned: [num_pages][Hkv][page_size][D] */
+  int32_t num_pages;       /* >= 1; num_pages * Hkv * page_size < 2^31 */
+  int32_t page_size;       /* rows of a page: a power of two, 16 or more */
+  int32_t num_kv_heads;
+  int32_t head_dim;        /* 64 or 128 */
+  int32_t dtype;           /* kvs_dtype of the pages, and of q, k, v and out */
+} kvs_paged_cache;
+
+/*
+ * A ragged batch over a paged cache: sequence i has n_i = row_offsets[i + 1]
+ * - row_offsets[i] new tokens (0, 1 or more: a prompt, a chunk of one, a
+ * decode step) at positions p_i .. p_i + n_i - 1, p_i = positions[i].  Row
+ * row_offsets[i] + t of q, k, v and out belongs to its token t.  Row j of
+ * its cache is row j % page_size of page page_table[i][j / page_size].
+ * Rows of q, k, v and out outside every [row_offsets[i], row_offsets[i + 1])
+ * are neither read nor written.  Table entries past the last page that a
+ * sequence's rows reach are not read.
+ *
+ * Checked on the device, per sequence, with the first error in d_status:
+ *   KVS_ERR_ROWS      row_offsets[i] <= row_offsets[i + 1] does not hold, or
+ *                     they leave [0, num_rows], or n_i > max_new; nothing is
+ *                     written for the sequence
+ *   KVS_ERR_POSITION  n_i > 0 and p_i < 0 or p_i + n_i > max_pages * page_size
+ *   KVS_ERR_PAGE      a page number needed is outside [0, num_pages)
+ */
+typedef struct kvs_paged_batch {
+  const int32_t *positions;   /* device [M] */
+  const int32_t *row_offsets; /* device [M + 1] */
+  const int32_t *page_table;  /* device [M][max_pages] */
+  int32_t num_seqs;           /* M >= 0 */
+  int32_t num_rows;           /* rows of q, k, v and out, >= 0 */
+  int32_t max_new;            /* the largest n_i that may occur, >= 1 */
+  int32_t max_pages;          /* >= 1; max_pages * page_size < 2^31 */
+} kvs_paged_batch;
+
+/*
+ * kvs_rope_scatter_paged -- what precedes the attention of a step: rotary
+ * positions on the new tokens' queries and keys, and the new K and V rows
+ * written into the pages, in ONE launch.
+ *
+ * For the token at position P (32 bits, exact), pair j of a head, 0 <= j <
+ * rot_dim / 2, with t = P * inv_freq[j] (the angle is reduced exactly, so far
+ * positions keep full precision), c = scale * cos t, s = scale * sin t:
+ *     (a, b) -> (a c - b s, b c + a s)
+ * where (a, b) are elements (j, j + rot_dim / 2) of the head, or (2j, 2j + 1)
+ * when interleaved != 0.  Elements rot_dim.. are copied.  Rotated q goes to
+ * q_out, rotated k and plain v to row P of the token's sequence in the pages.
+ * Computed in float32 and rounded once to the type.  No other page row is
+ * written; a page shared by two sequences must not be written by both.
+ *
+ *   q, k, v    in   rows [num_rows] of [H][D], [Hkv][D], [Hkv][D], each row
+ *                   contiguous, rows *_stride elements apart (so that q, k and
+ *                   v can be column blocks of one matrix); 16-byte aligned
+ *                   pointers and row strides
+ *   q_out      out  rows of [H][D], q_out_stride elements apart; may be q
+ *                   itself with q's stride, else must not overlap the inputs
+ *   inv_freq   in   [rot_dim / 2] float32, device (kvs_rope_frequencies makes
+ *                   them); finite, |inv_freq| <= 1e6
+ *   rot_dim         even, 0 .. head_dim
+ *   scale           factor of the rotated part (1 without length scaling)
+ * A token with a bad position or page has no page row written; its q_out
+ * row is NaN (bad position) or still the rotated q (bad page).
+ * Errors: NULL, DIMS, UNSUPPORTED, ALIGN, LAUNCH on the host; ROWS,
+ * POSITION, PAGE via d_status.
+ */
+int kvs_rope_scatter_paged(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                           const void *v, int64_t v_stride, void *q_out, int64_t q_out_stride,
+                           const kvs_paged_cache *cache, const kvs_paged_batch *batch,
+                           const float *inv_freq, int num_heads, int rot_dim, int interleaved,
+                           float scale, int *d_status, kvs_stream_t stream);
+
+/*
+ * kvs_rope_frequencies -- the table of inverse frequencies (HOST memory) and
+ * the scale that kvs_rope_scatter_paged takes, for w_j = base^(-2j / rot_dim):
+ *   KVS_ROPE_PLAIN    w_j
+ *   KVS_ROPE_LINEAR   w_j / factor (positions compressed by factor)
+ *   KVS_ROPE_NTK      w_j with base * factor^(rot_dim / (rot_dim - 2)): the
+ *                     slowest pair compressed by factor, the fastest kept
+ *   KVS_ROPE_YARN     pairs that turn more than `fast` times over
+ *                     original_len positions keep w_j, those that turn less
+ *                     than `slow` times take w_j / factor, a linear ramp over
+ *                     the pair index between; scale = 0.1 ln(factor) + 1
+ *   KVS_ROPE_BANDS    as YARN, with the ramp linear in the number of turns,
+ *                     and scale 1
+ * scale is 1 where nothing else is said.  Computed in double, rounded once.
+ *   inv_freq  out  float[rot_dim / 2], host
+ *   scale     out  float, host (nullable)
+ *   base > 0; factor >= 1 (not read by PLAIN); original_len > 0 and
+ *   0 < slow < fast (read by YARN and BANDS only); NTK: rot_dim >= 4
+ * Errors: DIMS (rot_dim < 2 or odd, an unknown kind, a value out of range),
+ * NULL.
+ */
+typedef enum kvs_rope_kind {
+  KVS_ROPE_PLAIN = 0,
+  KVS_ROPE_LINEAR = 1,
+  KVS_ROPE_NTK = 2,
+  KVS_ROPE_YARN = 3,
+  KVS_ROPE_BANDS = 4
+} kvs_rope_kind;
+
+int kvs_rope_frequencies(int rot_dim, double base, int kind, double factor, double original_len,
+                         double slow, double fast, float *inv_freq, float *scale);
+
+/*
+ * kvs_paged_attention -- attention of every sequence's new tokens over its
+ * paged cache, the rows of those tokens included (kvs_rope_scatter_paged, or
+ * the caller, has written them): for token t of sequence i and query head h
+ * (kv head g = h / G),
+ *     out[row][h][:] = softmax_j( q[row][h] . k_j[g] / sqrt(D) ) applied to
+ *     v_j[g], j = 0 .. p_i + t.
+ * One call serves prompts, chunks of prompts and decode steps together.
+ * Every live K and V row must be finite; cache rows past a sequence's last
+ * new token are never used, whatever they hold.  Products of 16-bit types
+ * accumulate in float32, the softmax runs in float32 with its weights
+ * rounded to the type before the product with v; float32 inputs keep float32
+ * accuracy throughout.
+ *
+ *   q, out     rows [num_rows] of [H][D], the strides in elements between
+ *              rows, 16-byte aligned pointers and row strides; out must not
+ *              overlap q
+ *   workspace  device scratch of >= kvs_paged_attention_workspace_bytes
+ *              bytes, 256-byte aligned; as for kvs_flash_decode (no
+ *              initialisation, not shared by calls that can overlap, the
+ *              epoch rule for captured graphs after a KVS_ERR_TIMEOUT)
+ * The rows of a sequence with a bad position are NaN; where a sequence needs
+ * a bad page, the rows that attend it are NaN and its other rows may be.
+ * Errors: NULL, DIMS, UNSUPPORTED (also H / Hkv > 8), ALIGN, WORKSPACE,
+ * LAUNCH on the host; ROWS, POSITION, PAGE, TIMEOUT via d_status.
+ */
+size_t kvs_paged_attention_workspace_bytes(int num_heads, int num_kv_heads, int head_dim,
+                                           int max_new);
+
+int kvs_paged_attention(const void *q, int64_t q_stride, const kvs_paged_cache *cache,
+                        const kvs_paged_batch *batch, void *out, int64_t out_stride,
+                        int num_heads, void *workspace, size_t workspace_bytes, int *d_status,
+                        kvs_stream_t stream);
+
+/*
+ * kvs_process_logits -- what happens between the model's logits and the
+ * choice of a token: penalties for repeated tokens, biases and a grammar
+ * mask, and the greedy token of the result, in ONE launch.  For row m and
+ * token id j, in float32 and in this order:
+ *     x = logits[m][j]
+ *     j in row m's history:           x = x > 0 ? x / r : x * r   (r = repetition[m])
+ *     c = times j was generated:      x -= frequency[m] * c
+ *     c > 0:                          x -= presence[m]
+ *     each of row m's biases on j:    x += value (in list order)
+ *     j forbidden by row m's mask:    x = -inf
+ * out[m][j] is x rounded to the type, and token_ids[m] the argmax of out[m]
+ * by kvs_argmax's rule (smallest index of the largest value, NaN never, 0
+ * where nothing is above -inf).
+ * Row m's history is history[history_offsets[m] .. history_offsets[m + 1]):
+ * its first prompt_lens[m] entries are the prompt (they count as seen, not
+ * as generated), the rest was generated.  Ids outside [0, vocab_size) in a
+ * history or a bias list are ignored.
+ */
+typedef struct kvs_logit_rules {
+  const int32_t *history;         /* device, or NULL: no history, no penalties */
+  const int32_t *history_offsets; /* device [M + 1], with history */
+  const int32_t *prompt_lens;     /* device [M], or NULL: nothing is prompt */
+  const float *repetition;        /* device [M], or NULL: 1 */
+  const float *presence;          /* device [M], or NULL: 0 */
+  const float *frequency;         /* device [M], or NULL: 0 */
+  const int32_t *bias_ids;        /* device, or NULL: no biases */
+  const float *bias_values;       /* device, with bias_ids */
+  const int32_t *bias_offsets;    /* device [M + 1], with bias_ids */
+  const uint32_t *mask;           /* device [mask_count][ceil(vocab / 32)], bit j % 32 of word
+                                     j / 32 set: j allowed; or NULL: no masks */
+  const int32_t *mask_rows;       /* device [M]: row m's mask, negative: none; or NULL: mask m */
+  int32_t history_len;            /* entries of history, >= 0 */
+  int32_t bias_len;               /* entries of bias_ids and bias_values, >= 0 */
+  int32_t mask_count;             /* rows of mask (>= M where mask_rows is NULL) */
+} kvs_logit_rules;
+
+/*
+ *   logits     in   [M] rows of vocab_size elements of `dtype`, logits_stride
+ *                   elements apart (>= vocab_size), element-aligned
+ *   out        out  rows out_stride elements apart; may be logits itself with
+ *                   its stride, else must not overlap it; or NULL: only the
+ *                   tokens are wanted
+ *   token_ids  out  [M] int32, device, or NULL (then out is required)
+ *   rules      in   HOST struct of device pointers
+ * An offset pair that decreases or leaves [0, *_len] is KVS_ERR_ROWS via
+ * d_status, a mask row at or past mask_count KVS_ERR_PAGE; that list or mask
+ * counts as empty (no history, no biases, no mask).
+ * Errors: DIMS (M < 0, vocab_size < 1, a stride or length too small), NULL,
+ * ALIGN, UNSUPPORTED (dtype; a vocabulary of more than 2^19 tokens), LAUNCH.
+ * M = 0 enqueues nothing.
+ */
+int kvs_process_logits(const void *logits, int64_t logits_stride, void *out, int64_t out_stride,
+                       int dtype, int M, int vocab_size, const kvs_logit_rules *rules,
+                       int32_t *token_ids, int *d_status, kvs_stream_t stream);
 
 /*
  * Kernel schedule of kvs_flash_decode, kvs_decode_step (and so of the

@@ -9,4 +9,6 @@ from .binding import (EXPORTS, kvs_argmax, kvs_prefill_attention, KVS_SCHEDULE_A
                       kvs_flash_decode_static, step_io,
                       kvs_flash_decode_workspace_bytes, kvs_get_schedule, kvs_kv_scatter,
                       kvs_prepare, kvs_schedule_for, prefill_workspace, kvs_set_schedule, kvs_step_graph_create, lib, strerror,
-                      workspace)
+                      workspace, PagedBatch, PagedCache, kvs_paged_attention, kvs_process_logits,
+                      kvs_rope_frequencies, kvs_rope_scatter_paged, paged_attention_workspace,
+                      KVS_ROPE_BANDS, KVS_ROPE_LINEAR, KVS_ROPE_NTK, KVS_ROPE_PLAIN, KVS_ROPE_YARN)

@@ -29,6 +29,15 @@ KVS_ERR_POSITION = 7
 KVS_ERR_TIMEOUT = 8
 KVS_ERR_SLOT = 9
 KVS_ERR_MEMORY = 10
+KVS_ERR_PAGE = 11
+KVS_ERR_ROWS = 12
+
+# kvs_dtype values
+KVS_F32, KVS_F16, KVS_BF16 = 0, 1, 2
+_DTYPES = {torch.float32: KVS_F32, torch.float16: KVS_F16, torch.bfloat16: KVS_BF16}
+
+# kvs_rope_kind values (kvs_rope_frequencies)
+KVS_ROPE_PLAIN, KVS_ROPE_LINEAR, KVS_ROPE_NTK, KVS_ROPE_YARN, KVS_ROPE_BANDS = range(5)
 
 # Every symbol include/kvsdecode.h declares.
 EXPORTS = ("kvs_kv_scatter", "kvs_choose_chunk_size", "kvs_flash_decode_workspace_bytes",
@@ -38,7 +47,9 @@ EXPORTS = ("kvs_kv_scatter", "kvs_choose_chunk_size", "kvs_flash_decode_workspac
            "kvs_decode_step_slots", "kvs_argmax", "kvs_prefill_attention",
            "kvs_prefill_workspace_bytes", "kvs_step_io_bytes", "kvs_decode_step_host",
            "kvs_set_wait_limit_ns", "kvs_step_io_layout", "kvs_decode_step_host_io",
-           "kvs_step_graph_io_layout", "kvs_step_graph_create_host_io")
+           "kvs_step_graph_io_layout", "kvs_step_graph_create_host_io", "kvs_rope_scatter_paged",
+           "kvs_rope_frequencies", "kvs_paged_attention_workspace_bytes", "kvs_paged_attention",
+           "kvs_process_logits")
 
 # Default bound on each pipeline wait of the kernels (kvs_set_wait_limit_ns).
 KVS_WAIT_LIMIT_DEFAULT_NS = 2_000_000_000
@@ -57,6 +68,9 @@ _lib = None
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _SZ = ctypes.c_size_t
+_L = ctypes.c_int64
+_F = ctypes.c_float
+_D = ctypes.c_double
 
 
 class KvsError(RuntimeError):
@@ -132,6 +146,17 @@ def lib() -> ctypes.CDLL:
                                                   _P, _SZ, _P, _P]
             L.kvs_set_wait_limit_ns.restype = _I
             L.kvs_set_wait_limit_ns.argtypes = [ctypes.c_uint64, ctypes.POINTER(ctypes.c_uint64)]
+            L.kvs_rope_scatter_paged.restype = _I
+            L.kvs_rope_scatter_paged.argtypes = [_P, _L, _P, _L, _P, _L, _P, _L, _P, _P, _P, _I,
+                                                 _I, _I, _F, _P, _P]
+            L.kvs_rope_frequencies.restype = _I
+            L.kvs_rope_frequencies.argtypes = [_I, _D, _I, _D, _D, _D, _D, _P, _P]
+            L.kvs_paged_attention_workspace_bytes.restype = _SZ
+            L.kvs_paged_attention_workspace_bytes.argtypes = [_I, _I, _I, _I]
+            L.kvs_paged_attention.restype = _I
+            L.kvs_paged_attention.argtypes = [_P, _L, _P, _P, _P, _L, _I, _P, _SZ, _P, _P]
+            L.kvs_process_logits.restype = _I
+            L.kvs_process_logits.argtypes = [_P, _L, _P, _L, _I, _I, _I, _P, _P, _P, _P]
             L.kvs_strerror.restype = ctypes.c_char_p
             L.kvs_strerror.argtypes = [_I]
             _lib = L
@@ -568,3 +593,236 @@ def kvs_step_graph_create(q, k_rows, v_rows, positions, k_cache, v_cache, out, c
         ctypes.byref(handle))
     _check(rc, "kvs_step_graph_create")
     return StepGraph(handle, (q, k_rows, v_rows, positions, k_cache, v_cache, out, workspace))
+
+
+class _PagedCacheStruct(ctypes.Structure):
+    _fields_ = [("k_pages", _P), ("v_pages", _P), ("num_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class _PagedBatchStruct(ctypes.Structure):
+    _fields_ = [("positions", _P), ("row_offsets", _P), ("page_table", _P),
+                ("num_seqs", ctypes.c_int32), ("num_rows", ctypes.c_int32),
+                ("max_new", ctypes.c_int32), ("max_pages", ctypes.c_int32)]
+
+
+class _LogitRulesStruct(ctypes.Structure):
+    _fields_ = [(n, _P) for n in ("history", "history_offsets", "prompt_lens", "repetition",
+                                  "presence", "frequency", "bias_ids", "bias_values",
+                                  "bias_offsets", "mask", "mask_rows")] + \
+               [(n, ctypes.c_int32) for n in ("history_len", "bias_len", "mask_count")]
+
+
+class PagedCache:
+    """A paged KV cache, checked once: k_pages and v_pages [num_pages, Hkv, page_size, D]
+    (float32, float16 or bfloat16, contiguous, CUDA)."""
+
+    def __init__(self, k_pages, v_pages):
+        for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
+            if not (t.is_cuda and t.dtype in _DTYPES and t.dim() == 4 and t.is_contiguous()):
+                raise TypeError(f"{name}: need a contiguous CUDA tensor [num_pages, Hkv, page_size, "
+                                f"D] of float32, float16 or bfloat16, got {tuple(t.shape)} "
+                                f"{t.dtype} {t.device}")
+        if k_pages.shape != v_pages.shape or k_pages.dtype != v_pages.dtype or \
+                k_pages.device != v_pages.device:
+            raise ValueError("PagedCache: k_pages and v_pages differ in shape, type or device")
+        self.k_pages, self.v_pages = k_pages, v_pages
+        self.dtype, self.device_index = k_pages.dtype, k_pages.get_device()
+        self.num_pages, self.num_kv_heads, self.page_size, self.head_dim = k_pages.shape
+        self._struct = _PagedCacheStruct(k_pages.data_ptr(), v_pages.data_ptr(), self.num_pages,
+                                         self.page_size, self.num_kv_heads, self.head_dim,
+                                         _DTYPES[k_pages.dtype])
+        self._addr = ctypes.addressof(self._struct)
+
+
+class PagedBatch:
+    """A ragged batch over a paged cache, checked once: positions [M], row_offsets [M + 1] and
+    page_table [M, max_pages] (int32, contiguous, CUDA).  Update the tensors' contents between
+    calls, not their addresses; num_rows (rows of q, k, v and out) and max_new (the largest
+    number of new tokens of a sequence) are the caller's, since the offsets are on the device."""
+
+    def __init__(self, positions, row_offsets, page_table, num_rows, max_new):
+        p, o = _i32(positions, "positions"), _i32(row_offsets, "row_offsets")
+        if not (page_table.is_cuda and page_table.dtype == torch.int32 and
+                page_table.dim() == 2 and page_table.is_contiguous()):
+            raise TypeError("page_table: need a contiguous int32 CUDA matrix [M, max_pages]")
+        M = positions.numel()
+        if row_offsets.numel() != M + 1 or page_table.shape[0] != M:
+            raise ValueError("PagedBatch: positions [M], row_offsets [M + 1] and page_table "
+                             "[M, max_pages] disagree on M")
+        if not positions.get_device() == row_offsets.get_device() == page_table.get_device():
+            raise ValueError("PagedBatch: tensors on different devices")
+        self.positions, self.row_offsets, self.page_table = positions, row_offsets, page_table
+        self.num_seqs, self.num_rows, self.max_new = M, int(num_rows), int(max_new)
+        self.device_index = positions.get_device()
+        self._struct = _PagedBatchStruct(p, o, page_table.data_ptr(), M, self.num_rows,
+                                         self.max_new, page_table.shape[1])
+        self._addr = ctypes.addressof(self._struct)
+
+
+def _call_device(t: torch.Tensor, where: str) -> int:
+    """The current device, which the call's tensors (t is one) must be on."""
+    dev = t.get_device()
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"{where}: the tensors are on device {dev}, which is not the current one")
+    return dev
+
+
+def _call_stream(stream, dev: int) -> int:
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return _stream(stream)
+
+
+def _rows(t: torch.Tensor, name: str, rows: int, heads: int, D: int, dtype, dev: int):
+    """Pointer and row stride of a [rows, heads, D] tensor whose rows are contiguous."""
+    if t.dtype != dtype or t.get_device() != dev or t.shape != (rows, heads, D):
+        raise TypeError(f"{name}: need a {dtype} tensor [{rows}, {heads}, {D}] on device {dev}, got "
+                        f"{tuple(t.shape)} {t.dtype} {t.device}")
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (s1 != D and heads > 1):
+        raise TypeError(f"{name}: the [heads, D] rows must be contiguous, got strides {t.stride()}")
+    return t.data_ptr(), s0 if rows > 1 else heads * D
+
+
+def _same_device(cache, batch, dev, where):
+    if cache.device_index != dev or batch.device_index != dev:
+        raise ValueError(f"{where}: cache, batch and tensors on different devices")
+
+
+def kvs_rope_frequencies(rot_dim, base=10000.0, kind=KVS_ROPE_PLAIN, factor=1.0, original_len=0.0,
+                         slow=1.0, fast=32.0, device=None):
+    """(inv_freq, scale): the frequency table of kvs_rope_scatter_paged (float32 [rot_dim / 2] on
+    the device) and the factor it goes with, for a length-scaling rule KVS_ROPE_*."""
+    table = torch.empty(max(rot_dim // 2, 1), dtype=torch.float32)
+    scale = ctypes.c_float(1.0)
+    _check(lib().kvs_rope_frequencies(int(rot_dim), float(base), int(kind), float(factor),
+                                      float(original_len), float(slow), float(fast),
+                                      table.data_ptr(), ctypes.addressof(scale)),
+           "kvs_rope_frequencies")
+    return table.to(device or "cuda"), scale.value
+
+
+def kvs_rope_scatter_paged(q, k, v, q_out, cache, batch, inv_freq, interleaved=False, scale=1.0,
+                           d_status=None, stream=None):
+    """Rotary positions on q [num_rows, H, D] and k [num_rows, Hkv, D] of a PagedBatch: rotated q
+    to q_out (q itself is fine), rotated k and plain v into the pages of a PagedCache.  Rows may
+    be strided (column blocks of one matrix).  The head's first 2 * inv_freq.numel() elements
+    turn, the rest is copied."""
+    dev = _call_device(q, "kvs_rope_scatter_paged")
+    _same_device(cache, batch, dev, "kvs_rope_scatter_paged")
+    N, D, Hkv, dt = batch.num_rows, cache.head_dim, cache.num_kv_heads, cache.dtype
+    H = q.shape[1] if q.dim() == 3 else -1
+    if inv_freq.dtype != torch.float32 or inv_freq.get_device() != dev or inv_freq.dim() != 1 or \
+            not inv_freq.is_contiguous():
+        raise TypeError("inv_freq: need a contiguous float32 vector on the tensors' device")
+    qp, qs = _rows(q, "q", N, H, D, dt, dev)
+    kp, ks = _rows(k, "k", N, Hkv, D, dt, dev)
+    vp, vs = _rows(v, "v", N, Hkv, D, dt, dev)
+    op, os_ = _rows(q_out, "q_out", N, H, D, dt, dev)
+    rc = lib().kvs_rope_scatter_paged(qp, qs, kp, ks, vp, vs, op, os_, cache._addr, batch._addr,
+                                      inv_freq.data_ptr(), H, 2 * inv_freq.numel(),
+                                      1 if interleaved else 0, scale, _status_ptr(d_status),
+                                      _call_stream(stream, dev))
+    if rc != KVS_OK:
+        raise KvsError(rc, "kvs_rope_scatter_paged")
+    return q_out
+
+
+def paged_attention_workspace(cache, batch, num_heads, device=None):
+    """A device byte buffer large enough for kvs_paged_attention (allocated by torch)."""
+    n = int(lib().kvs_paged_attention_workspace_bytes(num_heads, cache.num_kv_heads,
+                                                      cache.head_dim, batch.max_new))
+    if n == 0:
+        raise KvsError(KVS_ERR_DIMS, "kvs_paged_attention_workspace_bytes")
+    return torch.empty(n, dtype=torch.uint8, device=device or cache.k_pages.device)
+
+
+def kvs_paged_attention(q, cache, batch, out, workspace=None, d_status=None, stream=None):
+    """out [num_rows, H, D] = attention of every new token of a PagedBatch over its sequence's
+    pages, rows 0 .. its own position."""
+    dev = _call_device(q, "kvs_paged_attention")
+    _same_device(cache, batch, dev, "kvs_paged_attention")
+    if workspace is None:
+        raise ValueError("kvs_paged_attention: pass a workspace (see "
+                         "binding.paged_attention_workspace)")
+    H = q.shape[1] if q.dim() == 3 else -1
+    qp, qs = _rows(q, "q", batch.num_rows, H, cache.head_dim, cache.dtype, dev)
+    op, os_ = _rows(out, "out", batch.num_rows, H, cache.head_dim, cache.dtype, dev)
+    rc = lib().kvs_paged_attention(qp, qs, cache._addr, batch._addr, op, os_, H,
+                                   workspace.data_ptr(), workspace.nbytes,
+                                   _status_ptr(d_status), _call_stream(stream, dev))
+    if rc != KVS_OK:
+        raise KvsError(rc, "kvs_paged_attention")
+    return out
+
+
+def _vector(t, name, dtype, n, dev):
+    """Pointer of a contiguous vector of n entries (n None: any), 0 for None."""
+    if t is None:
+        return 0
+    if t.dtype != dtype or t.get_device() != dev or t.dim() != 1 or not t.is_contiguous() or \
+            (n is not None and t.numel() != n):
+        raise TypeError(f"{name}: need a contiguous {dtype} vector{'' if n is None else f' of {n}'} "
+                        f"on the logits' device, got {tuple(t.shape)} {t.dtype} {t.device}")
+    return t.data_ptr()
+
+
+def kvs_process_logits(logits, out=None, token_ids=None, history=None, history_offsets=None,
+                       prompt_lens=None, repetition=None, presence=None, frequency=None,
+                       bias_ids=None, bias_values=None, bias_offsets=None, mask=None,
+                       mask_rows=None, d_status=None, stream=None):
+    """Penalties, biases and grammar masks on logits [M, V] (float32, float16 or bfloat16; rows may
+    be strided) into out (logits itself is fine; None: only the tokens), and the greedy token of
+    the result into token_ids (int32 [M], made when None).  Returns token_ids."""
+    dt = _DTYPES.get(logits.dtype)
+    if dt is None or not logits.is_cuda or logits.dim() != 2 or \
+            (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise TypeError("logits: need a CUDA matrix [M, V] of float32, float16 or bfloat16 with "
+                        "contiguous rows")
+    dev = _call_device(logits, "kvs_process_logits")
+    M, V = logits.shape
+    ls = logits.stride(0) if M > 1 else V
+    op, os_ = 0, 0
+    if out is not None:
+        if out.dtype != logits.dtype or out.shape != logits.shape or out.get_device() != dev or \
+                (V > 1 and out.stride(1) != 1):
+            raise TypeError("out: need a matrix like logits")
+        op, os_ = out.data_ptr(), out.stride(0) if M > 1 else V
+    if token_ids is None:
+        token_ids = torch.empty(M, dtype=torch.int32, device=logits.device)
+    if (history is None) != (history_offsets is None):
+        raise ValueError("kvs_process_logits: history and history_offsets come together")
+    if len({bias_ids is None, bias_values is None, bias_offsets is None}) > 1:
+        raise ValueError("kvs_process_logits: bias_ids, bias_values and bias_offsets come together")
+    nh = nb = nm = 0
+    i32, f32 = torch.int32, torch.float32
+    if history is not None:
+        nh = history.numel()
+    if bias_ids is not None:
+        nb = bias_ids.numel()
+    mp = 0
+    if mask is not None:
+        if mask.dtype != i32 or mask.get_device() != dev or mask.dim() != 2 or \
+                mask.shape[1] != (V + 31) // 32 or not mask.is_contiguous():
+            raise TypeError("mask: need a contiguous int32 matrix [masks, ceil(V / 32)] on the "
+                            "logits' device")
+        mp, nm = mask.data_ptr(), mask.shape[0]
+    rules = _LogitRulesStruct(
+        _vector(history, "history", i32, None, dev),
+        _vector(history_offsets, "history_offsets", i32, M + 1, dev),
+        _vector(prompt_lens, "prompt_lens", i32, M, dev),
+        _vector(repetition, "repetition", f32, M, dev),
+        _vector(presence, "presence", f32, M, dev),
+        _vector(frequency, "frequency", f32, M, dev),
+        _vector(bias_ids, "bias_ids", i32, None, dev),
+        _vector(bias_values, "bias_values", f32, nb, dev),
+        _vector(bias_offsets, "bias_offsets", i32, M + 1, dev), mp,
+        _vector(mask_rows, "mask_rows", i32, M, dev), nh, nb, nm)
+    rc = lib().kvs_process_logits(logits.data_ptr(), ls, op, os_, dt, M, V,
+                                  ctypes.addressof(rules), _vector(token_ids, "token_ids", i32, M, dev),
+                                  _status_ptr(d_status), _call_stream(stream, dev))
+    if rc != KVS_OK:
+        raise KvsError(rc, "kvs_process_logits")
+    return token_ids

@@ -2,7 +2,9 @@
 // host, the chunk-size rule, workspace sizing, and dispatch to the kernel
 // launchers.  Nothing here allocates, frees or synchronises.
 
+#include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <cstdint>
 #include <mutex>
 
@@ -99,6 +101,8 @@ const char *kvs_strerror(int status) {
     case KVS_ERR_TIMEOUT: return "a bounded device pipeline wait expired";
     case KVS_ERR_SLOT: return "a cache slot is outside [0, num_slots)";
     case KVS_ERR_MEMORY: return "the device could not provide the library's own buffer";
+    case KVS_ERR_PAGE: return "a page or mask number is out of range";
+    case KVS_ERR_ROWS: return "row offsets decrease or leave their list";
     default: return "unknown kvs status";
   }
 }
@@ -421,6 +425,173 @@ int kvs_prefill_attention(const float *q, const float *k, const float *v, float 
                              workspace, d_status, reinterpret_cast<cudaStream_t>(stream));
 }
 
+// Shape checks of a paged cache and batch (no device memory is looked at).
+static int check_paged(const kvs_paged_cache *cache, const kvs_paged_batch *batch, int num_heads) {
+  if (!cache || !batch) return KVS_ERR_NULL;
+  const int Hkv = cache->num_kv_heads;
+  if (cache->num_pages < 1 || cache->page_size < 1 || Hkv < 1 || num_heads < 1 ||
+      num_heads % Hkv != 0 || batch->num_seqs < 0 || batch->num_rows < 0 || batch->max_new < 1 ||
+      batch->max_pages < 1)
+    return KVS_ERR_DIMS;
+  if (cache->dtype != KVS_F32 && cache->dtype != KVS_F16 && cache->dtype != KVS_BF16)
+    return KVS_ERR_UNSUPPORTED;
+  if (!head_dim_supported(cache->head_dim) || num_heads / Hkv > 8) return KVS_ERR_UNSUPPORTED;
+  if (cache->page_size < 16 || (cache->page_size & (cache->page_size - 1)) != 0)
+    return KVS_ERR_UNSUPPORTED;
+  // rows of the pages and of one sequence are counted in 32 bits
+  if ((int64_t)cache->num_pages * Hkv > 0x7fffffffll / cache->page_size ||
+      (int64_t)batch->max_pages > 0x7fffffffll / cache->page_size)
+    return KVS_ERR_DIMS;
+  return KVS_OK;
+}
+
+// Pointers of a paged cache and batch with work in it.
+static int check_paged_pointers(const kvs_paged_cache *cache, const kvs_paged_batch *batch) {
+  if (!cache->k_pages || !cache->v_pages || !batch->positions || !batch->row_offsets ||
+      !batch->page_table)
+    return KVS_ERR_NULL;
+  if (!aligned(cache->k_pages, 16) || !aligned(cache->v_pages, 16) ||
+      !aligned(batch->positions, 4) || !aligned(batch->row_offsets, 4) ||
+      !aligned(batch->page_table, 4))
+    return KVS_ERR_ALIGN;
+  return KVS_OK;
+}
+
+// Rows of `row` elements of `dtype`, `stride` elements apart.
+static int check_rows(const void *p, int64_t stride, int64_t row, int dtype) {
+  if (!p) return KVS_ERR_NULL;
+  if (stride < row) return KVS_ERR_DIMS;
+  if (!aligned(p, 16) || stride * (dtype == KVS_F32 ? 4 : 2) % 16 != 0) return KVS_ERR_ALIGN;
+  return KVS_OK;
+}
+
+static kvs::PagedArgs paged_args(const kvs_paged_cache *cache, const kvs_paged_batch *batch) {
+  int shift = 0;
+  while ((1 << shift) < cache->page_size) ++shift;
+  return kvs::PagedArgs{batch->positions, batch->row_offsets, batch->page_table,
+                        batch->num_seqs,  batch->num_rows,    batch->max_new,
+                        batch->max_pages, shift,              cache->num_pages};
+}
+
+int kvs_rope_scatter_paged(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                           const void *v, int64_t v_stride, void *q_out, int64_t q_out_stride,
+                           const kvs_paged_cache *cache, const kvs_paged_batch *batch,
+                           const float *inv_freq, int num_heads, int rot_dim, int interleaved,
+                           float scale, int *d_status, kvs_stream_t stream) {
+  int rc = check_paged(cache, batch, num_heads);
+  if (rc != KVS_OK) return rc;
+  const int D = cache->head_dim, Hkv = cache->num_kv_heads, dtype = cache->dtype;
+  if (rot_dim < 0 || rot_dim > D || rot_dim % 2 != 0) return KVS_ERR_DIMS;
+  if (batch->num_seqs == 0 || batch->num_rows == 0) return KVS_OK;
+  rc = check_paged_pointers(cache, batch);
+  if (rc == KVS_OK) rc = check_rows(q, q_stride, (int64_t)num_heads * D, dtype);
+  if (rc == KVS_OK) rc = check_rows(k, k_stride, (int64_t)Hkv * D, dtype);
+  if (rc == KVS_OK) rc = check_rows(v, v_stride, (int64_t)Hkv * D, dtype);
+  if (rc == KVS_OK) rc = check_rows(q_out, q_out_stride, (int64_t)num_heads * D, dtype);
+  if (rc != KVS_OK) return rc;
+  if (rot_dim > 0 && !inv_freq) return KVS_ERR_NULL;
+  if (!aligned(inv_freq, 4)) return KVS_ERR_ALIGN;
+  return kvs::launch_rope_scatter(q, q_stride, k, k_stride, v, v_stride, q_out, q_out_stride,
+                                  cache->k_pages, cache->v_pages, paged_args(cache, batch),
+                                  inv_freq, num_heads, Hkv, D, dtype, rot_dim, interleaved ? 1 : 0,
+                                  scale, d_status, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int kvs_rope_frequencies(int rot_dim, double base, int kind, double factor, double original_len,
+                         double slow, double fast, float *inv_freq, float *scale) {
+  const bool ramp = kind == KVS_ROPE_YARN || kind == KVS_ROPE_BANDS;
+  if (rot_dim < 2 || rot_dim % 2 != 0 || kind < KVS_ROPE_PLAIN || kind > KVS_ROPE_BANDS ||
+      !(base > 0.0) || (kind != KVS_ROPE_PLAIN && !(factor >= 1.0)) ||
+      (ramp && (!(original_len > 0.0) || !(slow > 0.0) || !(fast > slow))) ||
+      (kind == KVS_ROPE_NTK && rot_dim < 4))
+    return KVS_ERR_DIMS;
+  if (!inv_freq) return KVS_ERR_NULL;
+  const double two_pi = 6.28318530717958647693;
+  if (kind == KVS_ROPE_NTK) base *= std::pow(factor, (double)rot_dim / (rot_dim - 2));
+  // YARN's ramp runs over the pair index, from the (fractional) pair that
+  // turns `fast` times over original_len positions to the one that turns
+  // `slow` times, both rounded outwards and kept inside the head
+  auto pair_of = [&](double turns) {
+    return rot_dim * std::log(original_len / (turns * two_pi)) / (2.0 * std::log(base));
+  };
+  double first = 0.0, last = 0.0;
+  if (kind == KVS_ROPE_YARN) {
+    first = std::max(0.0, std::floor(pair_of(fast)));
+    last = std::min(rot_dim - 1.0, std::ceil(pair_of(slow)));
+    if (last <= first) last = first + 0.001;
+  }
+  for (int j = 0; j < rot_dim / 2; ++j) {
+    double w = std::pow(base, -2.0 * j / rot_dim);
+    double keep = 1.0;  // share of w kept, the rest is w / factor
+    if (kind == KVS_ROPE_LINEAR) keep = 0.0;
+    if (kind == KVS_ROPE_YARN) keep = 1.0 - std::min(1.0, std::max(0.0, (j - first) / (last - first)));
+    if (kind == KVS_ROPE_BANDS)
+      keep = std::min(1.0, std::max(0.0, (original_len * w / two_pi - slow) / (fast - slow)));
+    if (kind == KVS_ROPE_LINEAR || ramp) w = keep * w + (1.0 - keep) * w / factor;
+    inv_freq[j] = (float)w;
+  }
+  if (scale) *scale = kind == KVS_ROPE_YARN ? (float)(0.1 * std::log(factor) + 1.0) : 1.f;
+  return KVS_OK;
+}
+
+size_t kvs_paged_attention_workspace_bytes(int num_heads, int num_kv_heads, int head_dim,
+                                           int max_new) {
+  if (num_heads < 1 || num_kv_heads < 1 || num_heads % num_kv_heads != 0 || max_new < 1 ||
+      !head_dim_supported(head_dim) || num_heads / num_kv_heads > 8)
+    return 0;
+  return kvs::paged_attention_workspace_bytes(num_heads, num_kv_heads, head_dim, max_new);
+}
+
+int kvs_paged_attention(const void *q, int64_t q_stride, const kvs_paged_cache *cache,
+                        const kvs_paged_batch *batch, void *out, int64_t out_stride,
+                        int num_heads, void *workspace, size_t workspace_bytes, int *d_status,
+                        kvs_stream_t stream) {
+  int rc = check_paged(cache, batch, num_heads);
+  if (rc != KVS_OK) return rc;
+  if (batch->num_seqs == 0 || batch->num_rows == 0) return KVS_OK;
+  const int D = cache->head_dim;
+  rc = check_paged_pointers(cache, batch);
+  if (rc == KVS_OK) rc = check_rows(q, q_stride, (int64_t)num_heads * D, cache->dtype);
+  if (rc == KVS_OK) rc = check_rows(out, out_stride, (int64_t)num_heads * D, cache->dtype);
+  if (rc != KVS_OK) return rc;
+  if (!workspace) return KVS_ERR_WORKSPACE;
+  if (!aligned(workspace, 256)) return KVS_ERR_ALIGN;
+  if (workspace_bytes < kvs::paged_attention_workspace_bytes(num_heads, cache->num_kv_heads, D,
+                                                             batch->max_new))
+    return KVS_ERR_WORKSPACE;
+  return kvs::launch_paged_attention(q, q_stride, *cache, paged_args(cache, batch), out,
+                                     out_stride, num_heads, workspace, d_status,
+                                     reinterpret_cast<cudaStream_t>(stream));
+}
+
+int kvs_process_logits(const void *logits, int64_t logits_stride, void *out, int64_t out_stride,
+                       int dtype, int M, int vocab_size, const kvs_logit_rules *rules,
+                       int32_t *token_ids, int *d_status, kvs_stream_t stream) {
+  if (M < 0 || vocab_size < 1) return KVS_ERR_DIMS;
+  if (dtype != KVS_F32 && dtype != KVS_F16 && dtype != KVS_BF16) return KVS_ERR_UNSUPPORTED;
+  if (vocab_size > (1 << 19)) return KVS_ERR_UNSUPPORTED;
+  if (M == 0) return KVS_OK;
+  if (!logits || !rules || (!out && !token_ids)) return KVS_ERR_NULL;
+  if (logits_stride < vocab_size || (out && out_stride < vocab_size)) return KVS_ERR_DIMS;
+  const uintptr_t size = dtype == KVS_F32 ? 4 : 2;
+  if (!aligned(logits, size) || !aligned(out, size) || !aligned(token_ids, 4)) return KVS_ERR_ALIGN;
+  const kvs_logit_rules &r = *rules;
+  if (r.history && !r.history_offsets) return KVS_ERR_NULL;
+  if (r.bias_ids && (!r.bias_values || !r.bias_offsets)) return KVS_ERR_NULL;
+  if (r.history_len < 0 || r.history_len > (1 << 29) || r.bias_len < 0 ||
+      (r.mask && r.mask_count < (r.mask_rows ? 1 : M)))
+    return KVS_ERR_DIMS;
+  for (const void *p : {(const void *)r.history, (const void *)r.history_offsets,
+                        (const void *)r.prompt_lens, (const void *)r.repetition,
+                        (const void *)r.presence, (const void *)r.frequency,
+                        (const void *)r.bias_ids, (const void *)r.bias_values,
+                        (const void *)r.bias_offsets, (const void *)r.mask,
+                        (const void *)r.mask_rows})
+    if (!aligned(p, 4)) return KVS_ERR_ALIGN;
+  return kvs::launch_logits(logits, logits_stride, out, out_stride, dtype, M, vocab_size, r,
+                            token_ids, d_status, reinterpret_cast<cudaStream_t>(stream));
+}
+
 int kvs_set_schedule(int schedule) {
   if (schedule != KVS_SCHEDULE_AUTO && schedule != KVS_SCHEDULE_PERSISTENT &&
       schedule != KVS_SCHEDULE_CLUSTER)
@@ -441,6 +612,7 @@ int kvs_set_wait_limit_ns(uint64_t ns, uint64_t *previous) {
   int rc = kvs::set_wait_limit_step(ns);
   if (rc == KVS_OK) rc = kvs::set_wait_limit_cluster(ns);
   if (rc == KVS_OK) rc = kvs::set_wait_limit_prefill(ns);
+  if (rc == KVS_OK) rc = kvs::set_wait_limit_paged(ns);
   if (rc != KVS_OK) return rc;
   if (previous) *previous = g_limit[dev].load();
   g_limit[dev].store(ns);

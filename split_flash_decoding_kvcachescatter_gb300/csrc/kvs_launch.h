@@ -146,6 +146,30 @@ size_t prefill_workspace_bytes(int H, int S, int D);
 int launch_prefill(const float *q, const float *k, const float *v, float *out, int H, int S, int D,
                    int causal, void *workspace, int *d_status, cudaStream_t stream);
 
+// A ragged batch over a paged cache (kvs_paged_batch) as the kernels see it.
+struct PagedArgs {
+  const int32_t *positions, *row_offsets, *page_table;
+  int M, num_rows, max_new, max_pages, page_shift, num_pages;
+};
+
+// Rotary positions + scatter into the pages, one launch (num_rows >= 1).
+int launch_rope_scatter(const void *q, long long q_stride, const void *k, long long k_stride,
+                        const void *v, long long v_stride, void *q_out, long long q_out_stride,
+                        void *k_pages, void *v_pages, const PagedArgs &b, const float *inv_freq,
+                        int H, int Hkv, int D, int dtype, int rot, int interleaved, float scale,
+                        int *d_status, cudaStream_t stream);
+
+// Penalties, biases, mask and greedy token of M logit rows, one launch.
+int launch_logits(const void *logits, long long logits_stride, void *out, long long out_stride,
+                  int dtype, int M, int V, const kvs_logit_rules &rules, int32_t *ids,
+                  int *d_status, cudaStream_t stream);
+
+// Attention of a ragged batch over a paged cache.
+size_t paged_attention_workspace_bytes(int H, int Hkv, int D, int max_new);
+int launch_paged_attention(const void *q, long long q_stride, const kvs_paged_cache &cache,
+                           const PagedArgs &b, void *out, long long out_stride, int H,
+                           void *workspace, int *d_status, cudaStream_t stream);
+
 // Sets the step kernel's attributes for (H / Hkv, D) on the current device
 // (done on first use anyway; a stream capture calls it beforehand).
 int prepare_step_kernel(int H, int Hkv, int D);
@@ -172,5 +196,6 @@ bool poll_waits();
 int set_wait_limit_step(uint64_t ns);
 int set_wait_limit_cluster(uint64_t ns);
 int set_wait_limit_prefill(uint64_t ns);
+int set_wait_limit_paged(uint64_t ns);
 
 }  // namespace kvs

@@ -1,0 +1,218 @@
+// rope_scatter.cu -- rotary positions on a ragged batch's new queries and
+// keys, and the new K and V rows written into a paged cache, in one launch.
+//
+// Mathematics: pair j of a head at position P turns by t = P w_j.  t matters
+// modulo a full turn only, so the kernel keeps w_j / 2 pi as a 64-bit binary
+// fraction of a turn (one double product a thread and pair) and multiplies
+// it by P in wrapping 64-bit integers: the reduction is exact, where a
+// float32 product P w_j would be off by 2^-24 P w_j radians (0.008 at
+// position 131072).  The top 32 bits of the fraction go to sincospi.
+//
+// Bound: bytes (each row of q, k, v read once and written once).  A block
+// takes one token, or a slice of its heads when tokens are few: it puts the
+// token's rot_dim / 2 (cos, sin) pairs in shared memory once for all heads,
+// then each thread moves up to kItems pair vectors (two 16-byte loads each
+// with the half layout), all loads issued before the first is used.
+
+#include "kvs_paged.cuh"
+
+namespace kvs {
+
+namespace {
+
+constexpr int kRopeThreads = 128;
+constexpr int kRopeItems = 3;
+
+struct RopeArgs {
+  const void *q, *k, *v;
+  void *q_out, *k_pages, *v_pages;
+  long long q_stride, k_stride, v_stride, q_out_stride;
+  const float *inv_freq;
+  int H, Hkv, D, rot;
+  float scale;
+};
+
+// Index of the sequence whose rows hold `row`, by one warp (every lane gets
+// it): the number of sequences that end at or before it.
+__device__ __forceinline__ int warp_find_seq(const PagedArgs &b, int row, int lane) {
+  int n = 0;
+  for (int i = lane; i < b.M; i += 32) n += __ldca(b.row_offsets + i + 1) <= row;
+  return __reduce_add_sync(0xffffffffu, n);
+}
+
+// grid (num_rows, slices).  VE: elements of a vector; IL: interleaved pairs.
+template <typename T, int VE, bool IL>
+__global__ void __launch_bounds__(kRopeThreads)
+    rope_scatter_kernel(RopeArgs a, PagedArgs b, int *d_status) {
+  __shared__ float2 cs[64];
+  grid_dependency_wait();
+  allow_dependent_launch();
+  const int tid = threadIdx.x;
+  const int row = blockIdx.x;
+  if (blockIdx.y == 0)  // the status of every sequence, spread over the blocks
+    for (int i = row * kRopeThreads + tid; i < b.M; i += gridDim.x * kRopeThreads) {
+      const int err = paged_seq(b, i).err;
+      if (err != KVS_OK) record_status(d_status, err);
+    }
+  const int i = warp_find_seq(b, row, tid & 31);
+  if (i >= b.M) return;  // a row behind the last sequence
+  const PagedSeq s = paged_seq(b, i);
+  if (s.err == KVS_ERR_ROWS || row < s.row0 || row >= s.row0 + s.n) return;
+  const bool bad_pos = s.err != KVS_OK;
+  const int pos = s.p + (row - s.row0);
+  int page = -1;
+  if (!bad_pos) {
+    page = __ldca(b.page_table + (size_t)i * b.max_pages + (pos >> b.page_shift));
+    if ((unsigned)page >= (unsigned)b.num_pages) {
+      if (tid == 0) record_status(d_status, KVS_ERR_PAGE);
+      page = -1;
+    }
+  }
+  for (int j = tid; j < a.rot / 2; j += kRopeThreads) {
+    // turns per position, modulo 1, in units of 2^-64
+    double f = (double)a.inv_freq[j] * 0.15915494309189533577;  // 1 / 2 pi
+    f -= floor(f);
+    const unsigned long long turn = __double2ull_rn(f * 18446744073709551616.0) *
+                                    (unsigned long long)(unsigned)pos;
+    // signed 32-bit fraction of a half turn's angle: t / pi in [-1, 1)
+    const float x = (float)(int)(unsigned)(turn >> 32) * 4.656612873077393e-10f;  // 2^-31
+    float sn, c;
+    sincospif(x, &sn, &c);
+    cs[j] = make_float2(c * a.scale, sn * a.scale);
+  }
+  __syncthreads();
+  const int half = a.rot / 2;
+  // vectors of a rotated head: pair vectors first, then those copied
+  const int npair = IL ? a.rot / VE : half / VE;
+  const int per_head = npair + (a.D - a.rot) / VE;
+  const int nrot = (a.H + a.Hkv) * per_head;
+  const int total = nrot + a.Hkv * (a.D / VE);
+  const int slot = pos & ((1 << b.page_shift) - 1);
+  const T *q = static_cast<const T *>(a.q) + (long long)row * a.q_stride;
+  const T *k = static_cast<const T *>(a.k) + (long long)row * a.k_stride;
+  const T *v = static_cast<const T *>(a.v) + (long long)row * a.v_stride;
+  T *qo = static_cast<T *>(a.q_out) + (long long)row * a.q_out_stride;
+  const size_t head_rows = (size_t)1 << b.page_shift;
+  // row of kv head g in the page
+  const size_t page_row = (size_t)(page < 0 ? 0 : page) * a.Hkv * head_rows + slot;
+  T *kp = static_cast<T *>(a.k_pages) + page_row * a.D;
+  T *vp = static_cast<T *>(a.v_pages) + page_row * a.D;
+  const int step = kRopeThreads * gridDim.y;
+  for (int base = blockIdx.y * kRopeThreads + tid; base < total; base += kRopeItems * step) {
+    Vec<T, VE> x[kRopeItems], y[kRopeItems];
+    T *dst[kRopeItems];
+    int j0[kRopeItems];  // first pair (rotated) or -1 (copied), -2: nothing
+#pragma unroll
+    for (int u = 0; u < kRopeItems; ++u) {
+      const int it = base + u * step;
+      j0[u] = -2;
+      if (it >= total) continue;
+      const T *src;
+      if (it < nrot) {
+        const int h = it / per_head;
+        const int w = it - h * per_head;
+        const bool is_q = h < a.H;
+        src = is_q ? q + h * a.D : k + (h - a.H) * a.D;
+        dst[u] = is_q ? qo + h * a.D : page < 0 ? nullptr : kp + (size_t)(h - a.H) * head_rows * a.D;
+        if (w < npair) {
+          j0[u] = IL ? w * (VE / 2) : w * VE;
+          src += w * VE;
+          if (dst[u]) dst[u] += w * VE;
+          if (!IL) y[u] = vec_load<T, VE>(src + half);
+        } else {
+          j0[u] = -1;
+          src += a.rot + (w - npair) * VE;
+          if (dst[u]) dst[u] += a.rot + (w - npair) * VE;
+        }
+      } else {
+        const int e = (it - nrot) * VE;
+        const int g = e / a.D;
+        src = v + e;
+        dst[u] = page < 0 ? nullptr : vp + (size_t)g * head_rows * a.D + (e - g * a.D);
+        j0[u] = -1;
+      }
+      x[u] = vec_load<T, VE>(src);
+    }
+#pragma unroll
+    for (int u = 0; u < kRopeItems; ++u) {
+      if (j0[u] == -2 || dst[u] == nullptr) continue;
+      if (bad_pos) {  // (page is -1, so this is q_out)
+        const T nan = from_f32<T>(__int_as_float(0x7fc00000));
+#pragma unroll
+        for (int e = 0; e < VE; ++e) x[u].e[e] = y[u].e[e] = nan;
+      } else if (j0[u] >= 0) {
+        if (IL) {
+#pragma unroll
+          for (int e = 0; e + 1 < VE; e += 2) {
+            const float2 t = cs[j0[u] + e / 2];
+            const float p = to_f32(x[u].e[e]), r = to_f32(x[u].e[e + 1]);
+            x[u].e[e] = from_f32<T>(p * t.x - r * t.y);
+            x[u].e[e + 1] = from_f32<T>(r * t.x + p * t.y);
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < VE; ++e) {
+            const float2 t = cs[j0[u] + e];
+            const float p = to_f32(x[u].e[e]), r = to_f32(y[u].e[e]);
+            x[u].e[e] = from_f32<T>(p * t.x - r * t.y);
+            y[u].e[e] = from_f32<T>(r * t.x + p * t.y);
+          }
+        }
+      }
+      vec_store<T, VE>(dst[u], x[u]);
+      if (!IL && j0[u] >= 0) vec_store<T, VE>(dst[u] + half, y[u]);
+    }
+  }
+}
+
+template <typename T, int VE, bool IL>
+int launch_rope(const RopeArgs &a, const PagedArgs &b, int *d_status, cudaStream_t stream) {
+  const int sms = device_sm_count();
+  if (sms <= 0) return KVS_ERR_LAUNCH;
+  const int total = (a.H + a.Hkv) * ((IL ? a.rot / VE : a.rot / 2 / VE) + (a.D - a.rot) / VE) +
+                    a.Hkv * (a.D / VE);
+  // Few tokens: a token's vectors are split over blocks until every SM has
+  // one block or a thread has one vector left.
+  const int most = (total + kRopeThreads - 1) / kRopeThreads;
+  const int want = (2 * sms + b.num_rows - 1) / b.num_rows;
+  const int slices = want < 1 ? 1 : want < most ? want : most;
+  const cudaError_t e =
+      launch_pdl(rope_scatter_kernel<T, VE, IL>, dim3((unsigned)b.num_rows, (unsigned)slices),
+                 dim3(kRopeThreads), 0, stream, a, b, d_status);
+  return e == cudaSuccess ? KVS_OK : KVS_ERR_LAUNCH;
+}
+
+// The widest vector (16 bytes at most) that the head splits into: it must
+// divide the rotated half (half layout) or the rotated part (interleaved).
+template <typename T>
+int dispatch_rope(const RopeArgs &a, const PagedArgs &b, int interleaved, int *d_status,
+                  cudaStream_t stream) {
+  constexpr int kMost = 16 / sizeof(T);
+  const int n = interleaved ? a.rot : a.rot / 2;
+  if (n % kMost == 0)
+    return interleaved ? launch_rope<T, kMost, true>(a, b, d_status, stream)
+                       : launch_rope<T, kMost, false>(a, b, d_status, stream);
+  if (kMost == 8 && n % 4 == 0)
+    return interleaved ? launch_rope<T, 4, true>(a, b, d_status, stream)
+                       : launch_rope<T, 4, false>(a, b, d_status, stream);
+  if (n % 2 == 0)
+    return interleaved ? launch_rope<T, 2, true>(a, b, d_status, stream)
+                       : launch_rope<T, 2, false>(a, b, d_status, stream);
+  return launch_rope<T, 1, false>(a, b, d_status, stream);  // (interleaved: rot is even)
+}
+
+}  // namespace
+
+int launch_rope_scatter(const void *q, long long q_stride, const void *k, long long k_stride,
+                        const void *v, long long v_stride, void *q_out, long long q_out_stride,
+                        void *k_pages, void *v_pages, const PagedArgs &b, const float *inv_freq,
+                        int H, int Hkv, int D, int dtype, int rot, int interleaved, float scale,
+                        int *d_status, cudaStream_t stream) {
+  const RopeArgs a{q,        k,        v,   q_out, k_pages, v_pages, q_stride, k_stride,
+                   v_stride, q_out_stride, inv_freq, H,     Hkv,     D,       rot,      scale};
+  if (dtype == KVS_F32) return dispatch_rope<float>(a, b, interleaved, d_status, stream);
+  if (dtype == KVS_F16) return dispatch_rope<__half>(a, b, interleaved, d_status, stream);
+  return dispatch_rope<__nv_bfloat16>(a, b, interleaved, d_status, stream);
+}
+
+}  // namespace kvs
