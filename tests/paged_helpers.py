@@ -16,6 +16,24 @@ def half_step(dtype):
     return torch.finfo(dtype).eps / 2
 
 
+def least_step(dtype):
+    """Largest error of one rounding below the type's normal range, where its numbers are
+    evenly spaced (float16: below 2^-14, 2^-24 apart, so 2^-25)."""
+    info = torch.finfo(dtype)
+    return info.smallest_normal * info.eps / 2
+
+
+def within(got, ref, bound, where=""):
+    """Every element of got within bound of ref (64 bits), with the worst one told."""
+    over = (got.double() - ref).abs() - bound
+    if not bool((over <= 0).all()):  # (NaN fails too)
+        at = int(torch.nan_to_num(over, nan=float("inf")).argmax())
+        raise AssertionError(
+            f"{where}: {int((~(over <= 0)).sum())} of {over.numel()} outside; at {at}: "
+            f"{float(got.flatten()[at])!r} for {float(ref.flatten()[at])!r}, bound "
+            f"{float(bound.expand_as(ref).reshape(-1)[at]):.3g}")
+
+
 class Paged:
     """A batch of sequences (n new tokens from position p each) over pages in
     shuffled order.  Pages' rows that hold no live key are NaN, and so are the
@@ -102,16 +120,13 @@ class Paged:
             rel += (3 * 2.0 ** -21 if f32 else u) + (L * 2.0 ** -25 if self.dtype == torch.float16 else 0)
             rel += ((3 * L / 8 if f32 else L / 16) + L / 8 + 64) * 2.0 ** -23
             out[a:a + n] = o
-            bound[a:a + n] = rel * vmax + u * (o.abs() + rel * vmax) + 1e-30
+            bound[a:a + n] = rel * vmax + u * (o.abs() + rel * vmax) + least_step(self.dtype)
         return out, bound
 
     def check(self, got, where=""):
         ref, bound = self.reference()
         assert int(self.status.item()) == 0, where
-        err = (got.double() - ref).abs()
-        assert torch.isfinite(got).all(), f"{where}: not finite"
-        worst = (err - bound).max()
-        assert worst <= 0, f"{where}: {float((err / bound.clamp_min(1e-30)).max()):.2f} of the bound"
+        within(got, ref, bound, where)
 
 
 def row_of(offsets, r):
