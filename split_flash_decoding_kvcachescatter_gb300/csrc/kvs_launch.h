@@ -146,6 +146,12 @@ size_t prefill_workspace_bytes(int H, int S, int D);
 int launch_prefill(const float *q, const float *k, const float *v, float *out, int H, int S, int D,
                    int causal, void *workspace, int *d_status, cudaStream_t stream);
 
+// Grid bound of the paged attention kernels (one block an SM); their
+// workspaces hold partials for that many blocks.
+constexpr int kPagedMaxBlocks = 192;
+// Floats of one partial: RT rows of (m, l), then RT x D accumulators.
+constexpr size_t paged_slot_floats(int RT, int D) { return (size_t)RT * (D + 2); }
+
 // A ragged batch over a paged cache (kvs_paged_batch) as the kernels see it.
 struct PagedArgs {
   const int32_t *positions, *row_offsets, *page_table;
@@ -169,6 +175,12 @@ size_t paged_attention_workspace_bytes(int H, int Hkv, int D, int max_new);
 int launch_paged_attention(const void *q, long long q_stride, const kvs_paged_cache &cache,
                            const PagedArgs &b, void *out, long long out_stride, int H,
                            void *workspace, int *d_status, cudaStream_t stream);
+
+// The tensor-core variant for chunks (float16 and bfloat16 pages).
+size_t paged_chunk_workspace_bytes(int D);
+int launch_paged_chunk(const void *q, long long q_stride, const kvs_paged_cache &cache,
+                       const PagedArgs &b, void *out, long long out_stride, int H,
+                       void *workspace, int *d_status, cudaStream_t stream);
 
 // Sets the step kernel's attributes for (H / Hkv, D) on the current device
 // (done on first use anyway; a stream capture calls it beforehand).
@@ -197,5 +209,6 @@ int set_wait_limit_step(uint64_t ns);
 int set_wait_limit_cluster(uint64_t ns);
 int set_wait_limit_prefill(uint64_t ns);
 int set_wait_limit_paged(uint64_t ns);
+int set_wait_limit_chunk(uint64_t ns);
 
 }  // namespace kvs

@@ -86,4 +86,145 @@ __device__ __forceinline__ void vec_store(T *p, const Vec<T, N> &v) {
   }
 }
 
+// ---- the line of cost rows ------------------------------------------------
+// What fixes the line: kv heads, tokens of a row tile, fixed price of a unit,
+// keys of a tile, the shortest column worth a block.
+struct Line {
+  int Hkv, TT, fix, KT, min_column;
+};
+
+// Sequence with n tokens from position p, TT tokens a row tile: Rn row tiles;
+// unit (rt, g) attends p + min(n, (rt + 1) TT) keys.
+struct SeqCost {
+  int p, n, Rn, TT, fix;
+  __device__ SeqCost(const PagedSeq &s, const Line &ln)
+      : p(s.p), n(s.err == KVS_OK ? s.n : 0), Rn(0), TT(ln.TT), fix(ln.fix) {
+    Rn = (n + TT - 1) / TT;
+  }
+  __device__ int keys(int rt) const { return p + min(n, (rt + 1) * TT); }
+  // cost rows of one kv head's units before row tile rt (rt < Rn)
+  __device__ long long before(int rt) const {
+    return (long long)rt * (p + fix) + (long long)TT * ((long long)rt * (rt + 1) / 2);
+  }
+  __device__ long long head_total() const {
+    return n > 0 ? before(Rn - 1) + p + n + fix : 0;
+  }
+};
+
+// A unit of the line: sequence i, row tile rt, kv head g, first cost row base.
+struct Unit {
+  int i, rt, g;
+  long long base;
+};
+
+struct PagedPlan {
+  long long R;   // cost rows in all
+  long long P;   // columns in use
+  Unit first;    // the unit that holds this block's first cost row
+};
+
+__device__ __forceinline__ long long column_start(long long R, long long P, long long b) {
+  return R * b / P;
+}
+// Column holding cost row x: the largest b with R * b / P <= x.
+__device__ __forceinline__ int column_at(long long x, long long R, long long P) {
+  const long long c = (x * P + P - 1) / R;
+  return (int)(c < P - 1 ? c : P - 1);
+}
+
+// Warp-cooperative; every lane returns the plan.
+static __device__ PagedPlan warp_plan(const PagedArgs &a, const Line &ln, int blocks, int b, int lane) {
+  PagedPlan pl{0, 1, {a.M, 0, 0, 0}};
+  long long sum = 0;
+  for (int i = lane; i < a.M; i += 32) sum += SeqCost(paged_seq(a, i), ln).head_total();
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  pl.R = sum * ln.Hkv;
+  if (pl.R == 0) return pl;
+  // short lines use fewer columns, so that one holds work worth a block
+  pl.P = max(1ll, min((long long)blocks, pl.R / ln.min_column));
+  if (b >= pl.P) return pl;
+  const long long x0 = column_start(pl.R, pl.P, b);
+  long long base = 0;
+  for (int i0 = 0; i0 < a.M; i0 += 32) {
+    const int i = i0 + lane;
+    long long mine = 0;
+    if (i < a.M) mine = SeqCost(paged_seq(a, i), ln).head_total() * ln.Hkv;
+    long long inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += v;
+    }
+    const bool hit = mine > 0 && x0 >= base + inc - mine && x0 < base + inc;
+    const unsigned ballot = __ballot_sync(0xffffffffu, hit);
+    if (ballot) {
+      const int src = __ffs(ballot) - 1;
+      const long long sb = __shfl_sync(0xffffffffu, base + inc - mine, src);
+      pl.first.i = i0 + src;
+      const SeqCost c(paged_seq(a, pl.first.i), ln);
+      const long long off = x0 - sb;
+      int lo = 0, hi = c.Rn - 1;  // the last row tile that starts at or before off
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (c.before(mid) * ln.Hkv <= off) lo = mid;
+        else hi = mid - 1;
+      }
+      const long long tile_base = c.before(lo) * ln.Hkv;
+      const long long span = c.keys(lo) + ln.fix;
+      pl.first.rt = lo;
+      pl.first.g = (int)((off - tile_base) / span);
+      pl.first.base = sb + tile_base + pl.first.g * span;
+      return pl;
+    }
+    base += __shfl_sync(0xffffffffu, inc, 31);
+  }
+  return pl;
+}
+
+// Everything a warp needs to know about a unit.
+struct UnitInfo {
+  PagedSeq s;
+  int keys, nt;     // keys it attends, its tiles
+  int t_lo, t_hi;   // tiles of this block
+  int tok0, ntok;   // tokens of the row tile (within the sequence)
+  long long k0;     // cost row where tile 0 starts
+};
+
+// Of nt tiles of KT keys, the first one at cost row k0: how many start before x.
+__device__ __forceinline__ int tiles_before(long long x, long long k0, int nt, int KT) {
+  const long long d = x - k0;
+  return d <= 0 ? 0 : (int)min((long long)nt, (d + KT - 1) / KT);
+}
+
+__device__ __forceinline__ UnitInfo unit_info(const PagedArgs &a, const Unit &u, const Line &ln,
+                                              long long x0, long long x1) {
+  UnitInfo f;
+  f.s = paged_seq(a, u.i);
+  const SeqCost c(f.s, ln);
+  f.keys = c.keys(u.rt);
+  f.nt = (f.keys + ln.KT - 1) / ln.KT;
+  f.tok0 = u.rt * ln.TT;
+  f.ntok = min(ln.TT, c.n - f.tok0);
+  f.k0 = u.base + ln.fix;
+  f.t_lo = tiles_before(x0, f.k0, f.nt, ln.KT);
+  f.t_hi = tiles_before(x1, f.k0, f.nt, ln.KT);
+  return f;
+}
+
+// The unit after u; false past the last sequence.
+__device__ __forceinline__ bool next_unit(const PagedArgs &a, Unit &u, const UnitInfo &f,
+                                          const Line &ln) {
+  u.base += f.keys + ln.fix;
+  if (++u.g < ln.Hkv) return true;
+  u.g = 0;
+  if ((++u.rt) * ln.TT < f.s.n) return true;
+  u.rt = 0;
+  for (++u.i; u.i < a.M; ++u.i) {
+    const PagedSeq s = paged_seq(a, u.i);
+    if (s.err == KVS_OK && s.n > 0) return true;
+  }
+  return false;
+}
+
 }  // namespace kvs

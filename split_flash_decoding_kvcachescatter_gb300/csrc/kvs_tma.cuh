@@ -32,24 +32,44 @@ static inline TensorMapEncode tensor_map_encoder() {
   return fn;
 }
 
-// Map over `rows` rows of D elements (contiguous): a copy takes box_rows rows
-// whole, cut into column blocks of 128 bytes: shared memory gets
-// [D * size / 128][box_rows][128 bytes], 16-byte pieces swizzled by the row
-// (piece c of row r at c ^ (r % 8)).  Coordinates (0, row, 0).
+// Map over `rows` rows of D elements (contiguous), cut into column blocks of
+// 128 bytes: a copy of box_rows rows and `blocks` column blocks fills
+// [blocks][box_rows][128 bytes] of shared memory, 16-byte pieces swizzled by
+// the row (piece c of row r at c ^ (r % 8)).  Coordinates (0, row, block).
 static inline int make_row_map(CUtensorMap *map, const void *base, uint64_t rows, int D, int dtype,
-                               int box_rows) {
+                               int box_rows, int blocks) {
   const TensorMapEncode enc = tensor_map_encoder();
   if (!enc) return KVS_ERR_LAUNCH;
   const int size = dtype == KVS_F32 ? 4 : 2;
   const cuuint64_t dims[3] = {(cuuint64_t)(128 / size), rows, (cuuint64_t)(D * size / 128)};
   const cuuint64_t strides[2] = {(cuuint64_t)D * size, 128};
-  const cuuint32_t box[3] = {(cuuint32_t)(128 / size), (cuuint32_t)box_rows,
-                             (cuuint32_t)(D * size / 128)};
+  const cuuint32_t box[3] = {(cuuint32_t)(128 / size), (cuuint32_t)box_rows, (cuuint32_t)blocks};
   const cuuint32_t es[3] = {1, 1, 1};
   const CUtensorMapDataType type = dtype == KVS_F32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                                    : dtype == KVS_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                                       : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   const CUresult r = enc(map, type, 3, const_cast<void *>(base), dims, strides, box, es,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? KVS_OK : KVS_ERR_LAUNCH;
+}
+
+// Map over rows of [heads][D] 16-bit elements, row_stride elements apart: a
+// copy takes box_heads heads of box_rows rows, one column block of 64
+// elements, as [box_rows][box_heads][128 bytes], swizzled likewise.
+// Coordinates (0, head, row, block).
+static inline int make_q_map(CUtensorMap *map, const void *base, uint64_t rows, int64_t row_stride,
+                             int heads, int D, int dtype, int box_rows, int box_heads) {
+  const TensorMapEncode enc = tensor_map_encoder();
+  if (!enc) return KVS_ERR_LAUNCH;
+  const cuuint64_t dims[4] = {64, (cuuint64_t)heads, rows, (cuuint64_t)(D / 64)};
+  const cuuint64_t strides[3] = {(cuuint64_t)D * 2, (cuuint64_t)row_stride * 2, 128};
+  const cuuint32_t box[4] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_rows, 1};
+  const cuuint32_t es[4] = {1, 1, 1, 1};
+  const CUresult r = enc(map,
+                         dtype == KVS_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                          : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                         4, const_cast<void *>(base), dims, strides, box, es,
                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? KVS_OK : KVS_ERR_LAUNCH;

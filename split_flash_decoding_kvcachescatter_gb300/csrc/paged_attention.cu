@@ -22,7 +22,8 @@
 // column blocks moved by tensor-map copies of 16 rows, each looked up in the
 // page table); the WR warps of a group take 16 rows each.  Small row tiles
 // (RT = 16, a decode step) run WK = 4, WR = 1 -- the keys are split over the
-// warps, whose states merge in shared memory; larger ones WK = 1, WR = 8.
+// warps, whose states merge in shared memory; larger ones WK = 1, WR = 7 (eight warps in all,
+// so that a thread may have 255 registers).
 //
 // Products run on mma.sync (16 rows: an M = 128 tcgen05 tile would be seven
 // eighths padding): m16n8k16 for the 16-bit types; float32 as three TF32
@@ -30,6 +31,7 @@
 // product.  A 32-key tile of a decode step costs a warp about 900 cycles for
 // 16 KB where HBM delivers 23 bytes a cycle an SM, so four warps keep ahead.
 
+#include <algorithm>
 #include <cmath>
 #include <mutex>
 #include <type_traits>
@@ -42,7 +44,6 @@ namespace kvs {
 
 namespace {
 
-constexpr int kPagedMaxBlocks = 192;  // grid bound (one block an SM)
 constexpr int kUnitCost = 64;         // cost rows that stand for a unit's fixed price
 constexpr int kPagedMaxDevices = 64;
 
@@ -76,142 +77,8 @@ struct PagedGeo {
 // Workspace: 256 bytes (epoch), a counter per block, then per block two
 // partial slots (0: a unit begun in an earlier column, 1: one begun here and
 // not finished), each RT float2 (m, l) and RT x D floats.
-__host__ __device__ inline size_t paged_slot_floats(int RT, int D) { return (size_t)RT * (D + 2); }
 inline size_t paged_ws_bytes(int RT, int D) {
   return 256 + (size_t)kPagedMaxBlocks * 8 + 2 * (size_t)kPagedMaxBlocks * paged_slot_floats(RT, D) * 4;
-}
-
-// ---- the line of cost rows ------------------------------------------------
-// Sequence with n tokens from position p, TT tokens a row tile: Rn row tiles;
-// unit (rt, g) attends p + min(n, (rt + 1) TT) keys.
-struct SeqCost {
-  int p, n, Rn, TT;
-  __device__ SeqCost(const PagedSeq &s, int tt)
-      : p(s.p), n(s.err == KVS_OK ? s.n : 0), Rn(0), TT(tt) {
-    Rn = (n + TT - 1) / TT;
-  }
-  __device__ int keys(int rt) const { return p + min(n, (rt + 1) * TT); }
-  // cost rows of one kv head's units before row tile rt (rt < Rn)
-  __device__ long long before(int rt) const {
-    return (long long)rt * (p + kUnitCost) + (long long)TT * ((long long)rt * (rt + 1) / 2);
-  }
-  __device__ long long head_total() const {
-    return n > 0 ? before(Rn - 1) + p + n + kUnitCost : 0;
-  }
-};
-
-// A unit of the line: sequence i, row tile rt, kv head g, first cost row base.
-struct Unit {
-  int i, rt, g;
-  long long base;
-};
-
-struct PagedPlan {
-  long long R;   // cost rows in all
-  long long P;   // columns in use
-  Unit first;    // the unit that holds this block's first cost row
-};
-
-__device__ __forceinline__ long long column_start(long long R, long long P, long long b) {
-  return R * b / P;
-}
-// Column holding cost row x: the largest b with R * b / P <= x.
-__device__ __forceinline__ int column_at(long long x, long long R, long long P) {
-  const long long c = (x * P + P - 1) / R;
-  return (int)(c < P - 1 ? c : P - 1);
-}
-
-// Warp-cooperative; every lane returns the plan.
-__device__ PagedPlan warp_plan(const PagedArgs &a, int Hkv, int TT, int blocks, int b,
-                               int min_column, int lane) {
-  PagedPlan pl{0, 1, {a.M, 0, 0, 0}};
-  long long sum = 0;
-  for (int i = lane; i < a.M; i += 32) sum += SeqCost(paged_seq(a, i), TT).head_total();
-#pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  pl.R = sum * Hkv;
-  if (pl.R == 0) return pl;
-  // short lines use fewer columns, so that one holds work worth a block
-  pl.P = max(1ll, min((long long)blocks, pl.R / min_column));
-  if (b >= pl.P) return pl;
-  const long long x0 = column_start(pl.R, pl.P, b);
-  long long base = 0;
-  for (int i0 = 0; i0 < a.M; i0 += 32) {
-    const int i = i0 + lane;
-    long long mine = 0;
-    if (i < a.M) mine = SeqCost(paged_seq(a, i), TT).head_total() * Hkv;
-    long long inc = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long v = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += v;
-    }
-    const bool hit = mine > 0 && x0 >= base + inc - mine && x0 < base + inc;
-    const unsigned ballot = __ballot_sync(0xffffffffu, hit);
-    if (ballot) {
-      const int src = __ffs(ballot) - 1;
-      const long long sb = __shfl_sync(0xffffffffu, base + inc - mine, src);
-      pl.first.i = i0 + src;
-      const SeqCost c(paged_seq(a, pl.first.i), TT);
-      const long long off = x0 - sb;
-      int lo = 0, hi = c.Rn - 1;  // the last row tile that starts at or before off
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (c.before(mid) * Hkv <= off) lo = mid;
-        else hi = mid - 1;
-      }
-      const long long tile_base = c.before(lo) * Hkv;
-      const long long span = c.keys(lo) + kUnitCost;
-      pl.first.rt = lo;
-      pl.first.g = (int)((off - tile_base) / span);
-      pl.first.base = sb + tile_base + pl.first.g * span;
-      return pl;
-    }
-    base += __shfl_sync(0xffffffffu, inc, 31);
-  }
-  return pl;
-}
-
-// Everything a warp needs to know about a unit.
-struct UnitInfo {
-  PagedSeq s;
-  int keys, nt;     // keys it attends, its tiles
-  int t_lo, t_hi;   // tiles of this block
-  int tok0, ntok;   // tokens of the row tile (within the sequence)
-};
-
-__device__ __forceinline__ UnitInfo unit_info(const PagedArgs &a, const Unit &u, int TT, int KT,
-                                              long long x0, long long x1) {
-  UnitInfo f;
-  f.s = paged_seq(a, u.i);
-  const SeqCost c(f.s, TT);
-  f.keys = c.keys(u.rt);
-  f.nt = (f.keys + KT - 1) / KT;
-  f.tok0 = u.rt * TT;
-  f.ntok = min(TT, c.n - f.tok0);
-  const long long k0 = u.base + kUnitCost;
-  auto first_tile = [&](long long x) {  // tiles that start before cost row x
-    const long long d = x - k0;
-    return d <= 0 ? 0 : (int)min((long long)f.nt, (d + KT - 1) / KT);
-  };
-  f.t_lo = first_tile(x0);
-  f.t_hi = first_tile(x1);
-  return f;
-}
-
-// The unit after u; false past the last sequence.
-__device__ __forceinline__ bool next_unit(const PagedArgs &a, Unit &u, const UnitInfo &f, int Hkv,
-                                          int TT) {
-  u.base += f.keys + kUnitCost;
-  if (++u.g < Hkv) return true;
-  u.g = 0;
-  if ((++u.rt) * TT < f.s.n) return true;
-  u.rt = 0;
-  for (++u.i; u.i < a.M; ++u.i) {
-    const PagedSeq s = paged_seq(a, u.i);
-    if (s.err == KVS_OK && s.n > 0) return true;
-  }
-  return false;
 }
 
 __device__ __forceinline__ float ex2f(float x) {
@@ -355,6 +222,11 @@ struct WarpRows {
 #pragma unroll
       for (int e = 0; e < 4; ++e) s[j][e] = 0.f;
     if constexpr (F32) {
+      float small[NT][4];
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) small[j][e] = 0.f;
 #pragma unroll
       for (int c = 0; c < D / 16; ++c) {  // 16 columns: block c / 2, half c % 2
         uint32_t ah[2][4], al[2][4];      // two k steps of 8
@@ -366,6 +238,8 @@ struct WarpRows {
                        al[e2][u]);
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
+          // (the small products gather apart: the tensor cores truncate each
+          // sum, so a long chain of additions would lose its last bits)
           const int row = 8 * j + key_of_col<true>(lane >> 2);
           const int pc = ((lane & 3) + 4 * (c & 1)) ^ (row & 7);
           const float4 kv = lds_f4(sk + (c >> 1) * 2048 + row * 128 + pc * 16);
@@ -376,12 +250,16 @@ struct WarpRows {
           split_tf32(kv.w, bh[3], bl[3]);
 #pragma unroll
           for (int e2 = 0; e2 < 2; ++e2) {
-            mma_tf32(s[j], al[e2], bh[2 * e2], bh[2 * e2 + 1]);
-            mma_tf32(s[j], ah[e2], bl[2 * e2], bl[2 * e2 + 1]);
+            mma_tf32(small[j], al[e2], bh[2 * e2], bh[2 * e2 + 1]);
+            mma_tf32(small[j], ah[e2], bl[2 * e2], bl[2 * e2 + 1]);
             mma_tf32(s[j], ah[e2], bh[2 * e2], bh[2 * e2 + 1]);
           }
         }
       }
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[j][e] += small[j][e];
     } else {
       const int row = (lane & 7) + ((lane >> 4) << 3);
 #pragma unroll
@@ -432,7 +310,7 @@ struct WarpRows {
       for (int j = 0; j < NT; ++j) t += s[j][2 * hh] + s[j][2 * hh + 1];
       l[hh] = l[hh] * alpha[hh] + t;  // this lane's columns; summed over the lanes at the end
     }
-    if (__any_sync(0xffffffffu, moved)) {
+    if (!F32 && __any_sync(0xffffffffu, moved)) {
 #pragma unroll
       for (int j = 0; j < D / 8; ++j)
 #pragma unroll
@@ -440,18 +318,29 @@ struct WarpRows {
     }
     // ---- weights times V ----
     if constexpr (F32) {
+      // a tile's products gather in registers of their own and join the
+      // accumulator by one rounded addition a tile (the tensor cores truncate
+      // each sum: over thousands of keys that would add up)
+      uint32_t ph[NT][4], plo[NT][4];  // a0: row, key 2q; a1: row + 8; a2, a3: column 2q + 1's key
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
-        uint32_t ph[4], plo[4];  // a0: row, key 2q; a1: row + 8; a2, a3: the key of column 2q + 1
-        split_tf32(s[j][0], ph[0], plo[0]);
-        split_tf32(s[j][2], ph[1], plo[1]);
-        split_tf32(s[j][1], ph[2], plo[2]);
-        split_tf32(s[j][3], ph[3], plo[3]);
-        const int r0 = 8 * j + key_of_col<true>(2 * (lane & 3));
-        const int r1 = 8 * j + key_of_col<true>(2 * (lane & 3) + 1);
-        const int n = lane >> 2;
+        split_tf32(s[j][0], ph[j][0], plo[j][0]);
+        split_tf32(s[j][2], ph[j][1], plo[j][1]);
+        split_tf32(s[j][1], ph[j][2], plo[j][2]);
+        split_tf32(s[j][3], ph[j][3], plo[j][3]);
+      }
+      const int n = lane >> 2;
 #pragma unroll
-        for (int b = 0; b < D / 32; ++b) {
+      for (int b = 0; b < D / 32; ++b) {
+        float t[4][4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) t[e][k] = 0.f;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          const int r0 = 8 * j + key_of_col<true>(2 * (lane & 3));
+          const int r1 = 8 * j + key_of_col<true>(2 * (lane & 3) + 1);
           const float4 v0 = lds_f4(sv + b * 2048 + r0 * 128 + (n ^ (r0 & 7)) * 16);
           const float4 v1 = lds_f4(sv + b * 2048 + r1 * 128 + (n ^ (r1 & 7)) * 16);
           const float e0[4] = {v0.x, v0.y, v0.z, v0.w}, e1[4] = {v1.x, v1.y, v1.z, v1.w};
@@ -460,11 +349,15 @@ struct WarpRows {
             uint32_t h0, l0, h1, l1;
             split_tf32(e0[e], h0, l0);
             split_tf32(e1[e], h1, l1);
-            mma_tf32(o[b * 4 + e], plo, h0, h1);
-            mma_tf32(o[b * 4 + e], ph, l0, l1);
-            mma_tf32(o[b * 4 + e], ph, h0, h1);
+            mma_tf32(t[e], plo[j], h0, h1);
+            mma_tf32(t[e], ph[j], l0, l1);
+            mma_tf32(t[e], ph[j], h0, h1);
           }
         }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) o[b * 4 + e][k] = fmaf(o[b * 4 + e][k], alpha[k >> 1], t[e][k]);
       }
     } else {
       const int row = (lane & 7) + (((lane >> 3) & 1) << 3);
@@ -554,7 +447,7 @@ __global__ void __launch_bounds__((WK * WR + 1) * 32, 1)
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int b = blockIdx.x;
-  const int TT = C::RT / G;
+  const Line ln{Hkv, C::RT / G, kUnitCost, C::KT, min_column};
   if (threadIdx.x == 0) {
     prefetch_map(&kmap);
     prefetch_map(&vmap);
@@ -582,7 +475,7 @@ __global__ void __launch_bounds__((WK * WR + 1) * 32, 1)
   const unsigned tag = launch_tag(host_tag, __ldcg(epoch));
   __syncthreads();
   allow_dependent_launch();
-  const PagedPlan pl = warp_plan(pa, Hkv, TT, gridDim.x, b, min_column, lane);
+  const PagedPlan pl = warp_plan(pa, ln, gridDim.x, b, lane);
   if (pl.R == 0 || b >= pl.P) return;
   const long long x0 = column_start(pl.R, pl.P, b), x1 = column_start(pl.R, pl.P, b + 1);
   Unit u = pl.first;
@@ -597,7 +490,7 @@ __global__ void __launch_bounds__((WK * WR + 1) * 32, 1)
     bool ok = true;
     constexpr int NP = C::KT / 16;  // 16-row pieces of a tile
     do {
-      const UnitInfo f = unit_info(pa, u, TT, C::KT, x0, x1);
+      const UnitInfo f = unit_info(pa, u, ln, x0, x1);
       const int32_t *table = pa.page_table + (size_t)u.i * pa.max_pages;
       // the page of piece c of the tiles from t_lo on: a lane looks up 32
       // pieces ahead at a time
@@ -643,7 +536,7 @@ __global__ void __launch_bounds__((WK * WR + 1) * 32, 1)
         for (int r = 0; r < WK; ++r) use[r] += r == ring;
       }
       if (!ok) break;
-      if (!next_unit(pa, u, f, Hkv, TT)) break;
+      if (!next_unit(pa, u, f, ln)) break;
     } while (u.base < x1);
     if (lane == 0) {
       if (!ok) give_up(abort, d_status, epoch);
@@ -677,7 +570,7 @@ __global__ void __launch_bounds__((WK * WR + 1) * 32, 1)
   const float nan = __int_as_float(0x7fc00000);
   WarpRows<T, D> w;
   do {
-    const UnitInfo f = unit_info(pa, u, TT, C::KT, x0, x1);
+    const UnitInfo f = unit_info(pa, u, ln, x0, x1);
     if (f.t_lo < f.t_hi) {
       const int rows = f.ntok * G;
       const bool any_rows = 16 * wr < rows;  // (a warp past the rows only keeps the ring going)
@@ -810,8 +703,7 @@ __global__ void __launch_bounds__((WK * WR + 1) * 32, 1)
         if (!consumers_barrier()) return;  // (also: the merge buffers may be written again)
       }
       if (!whole) {
-        const long long k0 = u.base + kUnitCost;
-        const int b1 = column_at(k0, pl.R, pl.P);  // the block of the unit's tile 0
+        const int b1 = column_at(f.k0, pl.R, pl.P);  // the block of the unit's tile 0
         if (threadIdx.x == 0) {
           const unsigned add = (unsigned)(f.t_hi - f.t_lo);
           const unsigned before = tagged_add(counters + b1, add, tag, d_status, epoch);
@@ -827,10 +719,8 @@ __global__ void __launch_bounds__((WK * WR + 1) * 32, 1)
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
             float ls = 0.f, mx = neg_inf_f();
             for (int c = b1; c < (int)pl.P; ++c) {
-              const long long s0 = column_start(pl.R, pl.P, c) - k0;
-              const long long s1 = column_start(pl.R, pl.P, c + 1) - k0;
-              const int lo = s0 <= 0 ? 0 : (int)min((long long)f.nt, (s0 + C::KT - 1) / C::KT);
-              const int hi = s1 <= 0 ? 0 : (int)min((long long)f.nt, (s1 + C::KT - 1) / C::KT);
+              const int lo = tiles_before(column_start(pl.R, pl.P, c), f.k0, f.nt, C::KT);
+              const int hi = tiles_before(column_start(pl.R, pl.P, c + 1), f.k0, f.nt, C::KT);
               if (lo >= f.nt) break;
               if (lo >= hi) continue;
               const float *ps = slots + (2 * (size_t)c + (lo == 0 ? 1 : 0)) * paged_slot_floats(C::RT, D);
@@ -854,7 +744,7 @@ __global__ void __launch_bounds__((WK * WR + 1) * 32, 1)
         }
       }
     }
-    if (!next_unit(pa, u, f, Hkv, TT)) break;
+    if (!next_unit(pa, u, f, ln)) break;
   } while (u.base < x1);
 }
 
@@ -886,8 +776,10 @@ int launch_stream(const void *q, long long q_stride, const kvs_paged_cache &cach
   if (sms <= 0) return KVS_ERR_LAUNCH;
   CUtensorMap kmap, vmap;
   const uint64_t rows = (uint64_t)cache.num_pages * cache.num_kv_heads * cache.page_size;
-  int rc = make_row_map(&kmap, cache.k_pages, rows, D, cache.dtype, 16);
-  if (rc == KVS_OK) rc = make_row_map(&vmap, cache.v_pages, rows, D, cache.dtype, 16);
+  int rc = make_row_map(&kmap, cache.k_pages, rows, D, cache.dtype, 16,
+                        D * (int)sizeof(T) / 128);
+  if (rc == KVS_OK) rc = make_row_map(&vmap, cache.v_pages, rows, D, cache.dtype, 16,
+                        D * (int)sizeof(T) / 128);
   if (rc != KVS_OK) return rc;
   const int Hkv = cache.num_kv_heads;
   const int grid = sms < kPagedMaxBlocks ? sms : kPagedMaxBlocks;
@@ -909,8 +801,12 @@ int dispatch_rows(const void *q, long long q_stride, const kvs_paged_cache &cach
   if ((long long)pa.max_new * (H / cache.num_kv_heads) <= 16)
     return launch_stream<T, D, 4, 1>(q, q_stride, cache, pa, out, out_stride, H, workspace,
                                      d_status, stream);
-  return launch_stream<T, D, 1, 8>(q, q_stride, cache, pa, out, out_stride, H, workspace, d_status,
-                                   stream);
+  if constexpr (std::is_same<T, float>::value)
+    return launch_stream<T, D, 1, 7>(q, q_stride, cache, pa, out, out_stride, H, workspace,
+                                     d_status, stream);
+  else
+    return launch_paged_chunk(q, q_stride, cache, pa, out, out_stride, H, workspace, d_status,
+                              stream);
 }
 
 }  // namespace
@@ -924,7 +820,8 @@ int set_wait_limit_paged(uint64_t ns) {
 }
 
 size_t paged_attention_workspace_bytes(int H, int Hkv, int D, int max_new) {
-  return paged_ws_bytes((long long)max_new * (H / Hkv) <= 16 ? 16 : 128, D);
+  if ((long long)max_new * (H / Hkv) <= 16) return paged_ws_bytes(16, D);
+  return std::max(paged_ws_bytes(128, D), paged_chunk_workspace_bytes(D));
 }
 
 int launch_paged_attention(const void *q, long long q_stride, const kvs_paged_cache &cache,

@@ -1,0 +1,737 @@
+// paged_chunk.cu -- attention of chunks of new tokens over a paged KV cache
+// on the 5th-generation tensor cores (tcgen05), float16 and bfloat16.
+//
+// Mathematics and split: as paged_attention.cu (flash attention over a key
+// axis cut into equal cost columns, pieces of a unit merged by the block
+// that completes it).  A unit is two tiles A and B of TT = 128 / G whole
+// tokens with the G query heads of their kv head, so that both share every
+// K and V tile of 128 keys: per key tile a block reads 64 KB (D = 128) for
+// four products of 128 x 128 x 128, 2048 tensor-core cycles.
+//
+// Block (12 warps, one block an SM):
+//   warps 0-3, 4-7  softmax of tile A and of tile B: thread t owns row t,
+//                   which is TMEM lane t
+//   warp 8          issues the products: S_x = Q_x K^T (operands in shared
+//                   memory, K-major), O_x += P_x V (P from TMEM, V as the
+//                   copies leave it: head elements contiguous, which is the
+//                   MN-major operand, so nothing is transposed)
+//   warp 9          copies: Q by tensor maps over (head element, head of the
+//                   group, row), K and V page by page, two stages each
+//   warps 10-11     none (they make the register split whole)
+// TMEM columns: S_A [0, 128), S_B [128, 256), O_A and O_B behind, P_x in 16
+// bits over the first half of S_x.
+//
+// The issuing thread runs on events: it polls tile A and tile B in turn and
+// issues whatever is ready (P V once the softmax has written P, the next S
+// once P V has read it), so one tile's products fill the other's softmax.
+//
+// The softmax keeps a reference maximum that moves only when a row's maximum
+// grows by more than 2^8, so P and O are rarely rescaled; the weights are
+// rounded to the type for the product, their sum is taken in float32 before.
+
+#include <cmath>
+#include <mutex>
+#include <type_traits>
+
+#include "kvs_paged.cuh"
+#include "kvs_tags.cuh"
+#include "kvs_tcgen05.cuh"
+#include "kvs_tma.cuh"
+
+namespace kvs {
+
+namespace {
+
+constexpr int kCM = 128;                 // rows of a tile (MMA M)
+constexpr int kCN = 128;                 // keys of a tile
+constexpr int kCMmaWarp = 8, kCCopyWarp = 9;
+constexpr int kCThreads = 12 * 32;
+constexpr int kCFix = 128;               // fixed price of a unit, in cost rows
+constexpr float kCRescale = 8.f;
+constexpr uint32_t kCTmemCols = 512;
+constexpr int kCMaxDevices = 64;
+
+template <int D>
+struct CGeo {
+  static constexpr int NB = D / 64;               // 128-byte column blocks of a row
+  static constexpr int BLK = 128 * 128;           // bytes of a block of 128 rows
+  static constexpr int TILE = NB * BLK;           // one tile of Q, K or V
+  static constexpr int KS = 2, VS = 2;            // stages
+  static constexpr int OFF_Q = 0;                 // Q_A, Q_B
+  static constexpr int OFF_K = 2 * TILE;
+  static constexpr int OFF_V = OFF_K + KS * TILE;
+  static constexpr int OFF_BAR = OFF_V + VS * TILE;
+  // q, qfree, kfull[KS], kfree[KS], vfull[VS], vfree[VS], vpart, sfull[2],
+  // pfull[2], pvdone[2], odone[2], wg[2], final
+  static constexpr int NBAR = 2 + 2 * KS + 2 * VS + 1 + 10 + 1;
+  static constexpr int OFF_TMEM = OFF_BAR + NBAR * 8;
+  static constexpr int OFF_MISC = OFF_TMEM + 8;   // abort, last[2], bad[4], pad
+  static constexpr int NEED = OFF_MISC + 32;
+  // all 512 TMEM columns are this block's: more than half of the SM's shared
+  // memory keeps a second block away
+  static constexpr int SMEM = NEED > 116 * 1024 ? NEED : 116 * 1024;
+  static_assert(SMEM <= 227 * 1024, "one block per SM must fit");
+};
+
+// Shared-memory descriptor, 128-byte swizzle (tile bases 1024-byte aligned).
+// K-major: stride byte offset between 8-row groups; MN-major: leading byte
+// offset between 64-element blocks, stride byte offset between groups of 8 k.
+__device__ __forceinline__ uint64_t desc_sw128(const void *p, uint32_t lbo, uint32_t sbo) {
+  return smem_desc(p, lbo, sbo) | ((uint64_t)2 << 61);
+}
+
+// kind::f16 with FP32 accumulation: A and B both FP16 or both BF16.
+template <typename T>
+constexpr uint32_t idesc16(int M, int N, bool b_mn_major) {
+  const uint32_t bf = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
+  return idesc_f16_f32(M, N) | bf << 7 | bf << 10 | (b_mn_major ? 1u << 16 : 0u);
+}
+
+template <typename T>
+__device__ __forceinline__ uint32_t pack_pair(float a, float b) {
+  if constexpr (std::is_same<T, __half>::value) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+  } else {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+  }
+}
+
+// x * f for two packed values, f a power of two (exact above the subnormals).
+template <typename T>
+__device__ __forceinline__ uint32_t scale_pair(uint32_t x, float f) {
+  if constexpr (std::is_same<T, __half>::value) {
+    const __half2 v = __hmul2(*reinterpret_cast<const __half2 *>(&x), __float2half2_rn(f));
+    return *reinterpret_cast<const uint32_t *>(&v);
+  } else {
+    const __nv_bfloat162 v =
+        __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&x), __float2bfloat162_rn(f));
+    return *reinterpret_cast<const uint32_t *>(&v);
+  }
+}
+
+// Box of 64 elements x R rows of one column block (coordinates element, row,
+// block) and the Q box (element, head, row, block).
+__device__ __forceinline__ void tma_block(void *dst, const CUtensorMap *map, int row, int blk,
+                                          uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_addr(dst)),
+      "l"(map), "r"(0), "r"(row), "r"(blk), "r"(smem_addr(bar))
+      : "memory");
+}
+__device__ __forceinline__ void tma_q(void *dst, const CUtensorMap *map, int head, int row, int blk,
+                                      uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_addr(dst)),
+      "l"(map), "r"(0), "r"(head), "r"(row), "r"(blk), "r"(smem_addr(bar))
+      : "memory");
+}
+
+// The two tiles of a unit: tokens, key tiles that each attends, and those of
+// this block's column.
+struct CTile {
+  int tok0, ntok, nt, lo, hi;
+};
+
+template <typename T, int D, bool kPoll>
+__global__ void __launch_bounds__(kCThreads, 1)
+    paged_chunk_kernel(T *__restrict__ out, long long out_stride, PagedArgs pa,
+                       const __grid_constant__ CUtensorMap qmap,
+                       const __grid_constant__ CUtensorMap kmap,
+                       const __grid_constant__ CUtensorMap vmap, int G, int Hkv, int box_shift,
+                       float sl2, unsigned char *ws, unsigned host_tag, int *d_status) {
+  using C = CGeo<D>;
+  constexpr int KS = C::KS, VS = C::VS;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
+  uint64_t *bar_q = bars;            // Q of the unit landed
+  uint64_t *qfree = bar_q + 1;       // the unit's S products done (commit)
+  uint64_t *kfull = qfree + 1;       // [KS]
+  uint64_t *kfree = kfull + KS;      // [KS] the S products of a stage done (commit)
+  uint64_t *vfull = kfree + KS;      // [VS]
+  uint64_t *vfree = vfull + VS;      // [VS] the P V products of a stage done (commit)
+  uint64_t *vpart = vfree + VS;      // a V tile that ends past the last key landed
+  uint64_t *sfull = vpart + 1;       // [2] S_x ready (commit)
+  uint64_t *pfull = sfull + 2;       // [2] P_x written, O_x rescaled (128 arrivals)
+  uint64_t *pvdone = pfull + 2;      // [2] P V_x done (commit)
+  uint64_t *odone = pvdone + 2;      // [2] the unit's last P V_x done (commit)
+  uint64_t *wgbar = odone + 2;       // [2] the warps of a warpgroup
+  uint64_t *final = wgbar + 2;       // every product of the block done (commit)
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_TMEM);
+  volatile int *abort = reinterpret_cast<volatile int *>(smem + C::OFF_MISC);
+  volatile int *s_last = abort + 1;  // [2]
+  volatile int *s_bad = abort + 3;   // [4] a bad page in the unit of round rd, at rd % 4
+  unsigned *epoch = reinterpret_cast<unsigned *>(ws);
+  unsigned long long *counters = reinterpret_cast<unsigned long long *>(ws + 256);
+  float *slots = reinterpret_cast<float *>(ws + 256 + (size_t)kPagedMaxBlocks * 16);
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int b = blockIdx.x;
+  const int TT = kCM / G;  // tokens of a tile
+  const Line ln{Hkv, 2 * TT, kCFix, kCN, kCN + kCFix};
+
+  if (threadIdx.x == 0) {
+    prefetch_map(&qmap);
+    prefetch_map(&kmap);
+    prefetch_map(&vmap);
+    for (int j = 0; j < C::NBAR; ++j) mbar_init(&bars[j], 1);
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&pfull[x], kCM);
+      mbar_init(&wgbar[x], 4);
+    }
+    *abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0) {
+    tmem_alloc(tmem_slot, kCTmemCols);
+    tmem_relinquish();
+  }
+  grid_dependency_wait();
+  // bad sequences: status, and NaN rows where the rows are known
+  for (int i = b; i < pa.M; i += gridDim.x) {
+    const PagedSeq s = paged_seq(pa, i);
+    if (s.err != KVS_OK) {
+      if (threadIdx.x == 0) record_status(d_status, s.err);
+      const T nan = from_f32<T>(__int_as_float(0x7fc00000));
+      for (int r = 0; r < s.n; ++r)
+        for (int e = threadIdx.x; e < Hkv * G * D; e += kCThreads)
+          out[(long long)(s.row0 + r) * out_stride + e] = nan;
+    }
+  }
+  const unsigned tag = launch_tag(host_tag, __ldcg(epoch));
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  allow_dependent_launch();
+  const uint32_t tmem = *tmem_slot;
+  const PagedPlan pl = warp_plan(pa, ln, gridDim.x, b, lane);
+  const bool work = pl.R > 0 && b < pl.P;
+  const long long x0 = work ? column_start(pl.R, pl.P, b) : 0;
+  const long long x1 = work ? column_start(pl.R, pl.P, b + 1) : 0;
+  Unit u = pl.first;
+  bool more = work;
+  auto tile_of = [&](const UnitInfo &f, int x) {
+    CTile t;
+    t.tok0 = f.tok0 + x * TT;
+    t.ntok = min(TT, f.ntok - x * TT);
+    t.nt = t.ntok > 0 ? (f.s.p + t.tok0 + t.ntok + kCN - 1) / kCN : 0;
+    t.lo = min(f.t_lo, t.nt);
+    t.hi = min(f.t_hi, t.nt);
+    return t;
+  };
+  // the next unit of the column with work in it; false at its end
+  auto advance = [&](const UnitInfo &f) { more = next_unit(pa, u, f, ln) && u.base < x1; };
+
+  if (warp == kCCopyWarp) {
+    // ======================= copies ==========================================
+    int nk = 0, nv = 0;  // K and V tiles issued
+    int nq = 0, npart = 0;
+    bool ok = true, part_failed = false;
+    const int R = 1 << box_shift;          // rows of a copy
+    const int pieces = kCN >> box_shift;   // copies of a tile's column block
+    const uint32_t piece_bytes = (uint32_t)R * 128;
+    while (more && ok) {
+      const UnitInfo f = unit_info(pa, u, ln, x0, x1);
+      if (f.t_lo < f.t_hi) {
+        const int32_t *table = pa.page_table + (size_t)u.i * pa.max_pages;
+        const int L = f.s.p + f.s.n;
+        if (nq > 0 && !(ok = __all_sync(0xffffffffu, mbar_wait<kPoll>(qfree, (uint32_t)(nq - 1) & 1u, abort))))
+          break;
+        if (lane == 0) {
+          s_bad[nq & 3] = 0;
+          const int tiles = f.ntok > TT ? 2 : 1;
+          mbar_arrive_expect_tx(bar_q, (uint32_t)(tiles * C::NB * TT * G * 128));
+          for (int x = 0; x < tiles; ++x)
+            for (int blk = 0; blk < C::NB; ++blk)
+              tma_q(smem + C::OFF_Q + x * C::TILE + blk * C::BLK, &qmap, u.g * G,
+                    f.s.row0 + f.tok0 + x * TT, blk, bar_q);
+        }
+        ++nq;
+        __syncwarp();
+        for (int n = f.t_lo; n < f.t_hi; ++n) {
+          // lane: column block lane / pieces, piece lane % pieces of the tile
+          const int piece = lane & (pieces - 1);
+          const int blk = lane / pieces;
+          const int key = n * kCN + piece * R;
+          const int live_pieces = min(pieces, (L - n * kCN + R - 1) / R);
+          const bool mine = blk < C::NB && piece < live_pieces;
+          int page = mine ? __ldca(table + (key >> pa.page_shift)) : 0;
+          if ((unsigned)page >= (unsigned)pa.num_pages) {
+            record_status(d_status, KVS_ERR_PAGE);
+            s_bad[(nq - 1) & 3] = 1;
+            page = 0;
+          }
+          const int row = ((page * Hkv + u.g) << pa.page_shift) + (key & ((1 << pa.page_shift) - 1));
+          const uint32_t bytes = (uint32_t)(C::NB * live_pieces) * piece_bytes;
+          unsigned char *part = smem + blk * C::BLK + piece * R * 128;
+          const int ks = nk % KS, vs = nv % VS;
+          if (nk >= KS && !(ok = __all_sync(0xffffffffu, mbar_wait<kPoll>(&kfree[ks], (uint32_t)((nk - KS) / KS) & 1u, abort))))
+            break;
+          if (lane == 0) mbar_arrive_expect_tx(&kfull[ks], bytes);
+          __syncwarp();
+          if (mine) tma_block(part + C::OFF_K + ks * C::TILE, &kmap, row, blk, &kfull[ks]);
+          ++nk;
+          if (nv >= VS && !(ok = __all_sync(0xffffffffu, mbar_wait<kPoll>(&vfree[vs], (uint32_t)((nv - VS) / VS) & 1u, abort))))
+            break;
+          // a V tile that ends past the last key: its other rows hold anything
+          // (their weights are zero, but 0 x NaN is not), so they are zeroed
+          // before the products may read it
+          const int left = L - n * kCN;
+          uint64_t *bar = left < kCN ? vpart : &vfull[vs];
+          if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
+          __syncwarp();
+          if (mine) tma_block(part + C::OFF_V + vs * C::TILE, &vmap, row, blk, bar);
+          ++nv;
+          if (left < kCN) {
+            ++npart;
+            if (!(ok = __all_sync(0xffffffffu, mbar_wait<kPoll>(vpart, (uint32_t)(npart - 1) & 1u, abort)))) {
+              part_failed = true;
+              break;
+            }
+            unsigned char *v = smem + C::OFF_V + vs * C::TILE;
+            for (int e = lane; e < (kCN - left) * 8 * C::NB; e += 32) {
+              const int r = left + (e >> 3) / C::NB, bb = (e >> 3) % C::NB;
+              *reinterpret_cast<uint4 *>(v + bb * C::BLK + r * 128 + (e & 7) * 16) = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_shared();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&vfull[vs]);
+          }
+        }
+      }
+      if (ok) advance(f);
+    }
+    if (lane == 0) {
+      if (!ok) give_up(abort, d_status, epoch);
+      // every copy issued lands before the block can exit
+      if (nq > 0) mbar_wait_drain(bar_q, (uint32_t)(nq - 1) & 1u);
+      for (int j = (nk > KS ? nk - KS : 0); j < nk; ++j)
+        mbar_wait_drain(&kfull[j % KS], (uint32_t)(j / KS) & 1u);
+      // a V tile counted on vpart completes vfull only once its tail is zeroed
+      if (npart > 0) mbar_wait_drain(vpart, (uint32_t)(npart - 1) & 1u);
+      for (int j = (nv > VS ? nv - VS : 0); j < nv - (part_failed ? 1 : 0); ++j)
+        mbar_wait_drain(&vfull[j % VS], (uint32_t)(j / VS) & 1u);
+    }
+    __syncwarp();
+  } else if (warp == kCMmaWarp) {
+    // ======================= tensor-core work ================================
+    if (lane == 0) {
+      const uint64_t dq = desc_sw128(smem + C::OFF_Q, 16, 1024);
+      const uint64_t dk = desc_sw128(smem + C::OFF_K, 16, 1024);
+      const uint64_t dv = desc_sw128(smem + C::OFF_V, C::BLK, 1024);
+      constexpr uint64_t kTileStep = C::TILE >> 4;
+      constexpr uint32_t kIdS = idesc16<T>(kCM, kCN, false);
+      constexpr uint32_t kIdO = idesc16<T>(kCM, D, true);
+      int gt = 0;                 // K (and V) tiles of the earlier units
+      int sdone[2] = {0, 0};      // S_x products of the earlier units (pfull, pvdone phases)
+      int nq = 0;
+      bool ok = true;
+      uint32_t out_commits = 0;   // a bit per x: a commit on pvdone[x] not yet waited for
+      const uint64_t limit = kPoll ? (uint64_t)g_wait_limit_ns : kWaitLimitNs;
+      while (more && ok) {
+        const UnitInfo f = unit_info(pa, u, ln, x0, x1);
+        if (f.t_lo < f.t_hi) {
+          const CTile ta = tile_of(f, 0), tb = tile_of(f, 1);
+          const int n_x[2] = {ta.hi - ta.lo, tb.hi - tb.lo};  // products of each tile
+          const int n_all = f.t_hi - f.t_lo;                  // K and V tiles of the unit
+          // (a tile attends the first n_x of them; key tiles that only B attends come last)
+          int s_next[2] = {0, 0}, pv_next[2] = {0, 0};
+          int k_done = 0, v_done = 0;  // stages released
+          int k_in = 0, v_in = 0;      // stages known to have landed
+          bool have_q = false;
+          uint64_t t0 = global_timer_ns();
+          uint32_t idle = 0;
+          while (k_done < n_all || v_done < n_all) {
+            bool did = false;
+            if (!have_q) {
+              have_q = mbar_test_wait(bar_q, (uint32_t)nq & 1u);
+              if (have_q) tc_fence_after();
+            }
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              // P V_x(j): P_x(j) is written and V(j) has landed
+              const int j = pv_next[x];
+              if (j < s_next[x] && mbar_test_wait(&pfull[x], (uint32_t)(sdone[x] + j) & 1u)) {
+                bool in = j < v_in;
+                if (!in) {
+                  const int gv = gt + j;
+                  in = mbar_test_wait(&vfull[gv % VS], (uint32_t)(gv / VS) & 1u);
+                  if (in) v_in = j + 1;
+                }
+                if (in) {
+                  tc_fence_after();
+                  const uint64_t bv = dv + (uint64_t)((gt + j) % VS) * kTileStep;
+                  const uint32_t d = tmem + 2 * kCN + x * D, a = tmem + x * kCN;
+#pragma unroll
+                  for (int ks = 0; ks < kCN / 16; ++ks)
+                    mma_f16_ts(d, a + ks * 8, bv + 128 * ks, kIdO, (j > 0 || ks > 0) ? 1u : 0u);
+                  if (j + 1 == n_x[x]) mma_commit(&odone[x]);
+                  mma_commit(&pvdone[x]);
+                  out_commits |= 1u << x;
+                  pv_next[x] = j + 1;
+                  did = true;
+                }
+              }
+              // S_x(i): P V_x(i - 1) is done with P_x, and K(i) has landed
+              const int i = s_next[x];
+              if (have_q && i < n_x[x] && i == pv_next[x]) {
+                if (out_commits >> x & 1u) {
+                  if (mbar_test_wait(&pvdone[x], (uint32_t)(sdone[x] + i - 1) & 1u))
+                    out_commits &= ~(1u << x);
+                }
+                if (!(out_commits >> x & 1u)) {
+                  bool in = i < k_in;
+                  if (!in) {
+                    const int gk = gt + i;
+                    in = mbar_test_wait(&kfull[gk % KS], (uint32_t)(gk / KS) & 1u);
+                    if (in) k_in = i + 1;
+                  }
+                  if (in) {
+                    tc_fence_after();
+                    const uint64_t a = dq + (x ? kTileStep : 0);
+                    const uint64_t bk = dk + (uint64_t)((gt + i) % KS) * kTileStep;
+                    const uint32_t d = tmem + x * kCN;
+#pragma unroll
+                    for (int ks = 0; ks < D / 16; ++ks) {
+                      const uint64_t at = (uint64_t)(ks >> 2) * (C::BLK >> 4) + (ks & 3) * 2;
+                      mma_f16(d, a + at, bk + at, kIdS, ks > 0 ? 1u : 0u);
+                    }
+                    mma_commit(&sfull[x]);
+                    s_next[x] = i + 1;
+                    did = true;
+                  }
+                }
+              }
+            }
+            if (did) {
+              // stages whose last product is issued: their commit frees them
+              while (k_done < n_all && (s_next[0] > k_done || k_done >= n_x[0]) &&
+                     (s_next[1] > k_done || k_done >= n_x[1])) {
+                mma_commit(&kfree[(gt + k_done) % KS]);
+                if (++k_done == n_all) mma_commit(qfree);
+              }
+              while (v_done < n_all && (pv_next[0] > v_done || v_done >= n_x[0]) &&
+                     (pv_next[1] > v_done || v_done >= n_x[1])) {
+                mma_commit(&vfree[(gt + v_done) % VS]);
+                ++v_done;
+              }
+              idle = 0;
+            } else {
+              // nothing was ready: bounded polling
+              if (idle == 0) t0 = global_timer_ns();
+              if ((++idle & (kPoll ? 0u : 255u)) == 0) {
+                if (*abort || global_timer_ns() - t0 > limit) {
+                  ok = false;
+                  break;
+                }
+              }
+            }
+          }
+          if (!ok) break;
+          gt += n_all;
+          sdone[0] += n_x[0];
+          sdone[1] += n_x[1];
+          ++nq;
+        }
+        advance(f);
+      }
+      if (!ok) give_up(abort, d_status, epoch);
+      // every product issued finishes before the block frees the tensor memory
+      mma_commit(final);
+      mbar_wait_drain(final, 0u);
+    }
+    __syncwarp();
+  } else if (warp < 8) {
+    // ======================= softmax of tile x ===============================
+    const int x = warp >> 2;
+    const int t = threadIdx.x & 127;
+    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t tm_s = tmem + lane_base + x * kCN;
+    const uint32_t tm_o = tmem + lane_base + 2 * kCN + x * D;
+    const float nan = __int_as_float(0x7fc00000);
+    int sb = 0;  // S_x products of the earlier units
+    int ob = 0;  // earlier units with products of tile x
+    int nq = 0;  // earlier units
+    uint32_t wphase = 0;
+    bool failed = false;
+    auto wg_barrier = [&]() -> bool {  // the warpgroup's four warps, bounded
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&wgbar[x]);
+      const bool got = __all_sync(0xffffffffu, mbar_wait<kPoll>(&wgbar[x], wphase, abort));
+      wphase ^= 1u;
+      return got;
+    };
+    while (more && !failed) {
+      const UnitInfo f = unit_info(pa, u, ln, x0, x1);
+      if (f.t_lo < f.t_hi) {
+        const CTile tl = tile_of(f, x);
+        const int rows = tl.ntok * G;
+        const bool live = t < rows;
+        const int tok = live ? t / G : tl.ntok - 1;
+        const int last = f.s.p + tl.tok0 + tok;  // the row's last key
+        const int first_last = f.s.p + tl.tok0;  // the tile's first row's
+        float m = neg_inf_f(), l = 0.f;
+        for (int n = tl.lo; n < tl.hi; ++n) {
+          const uint32_t ph = (uint32_t)(sb + n - tl.lo) & 1u;
+          if (!__all_sync(0xffffffffu, mbar_wait<kPoll>(&sfull[x], ph, abort))) {
+            failed = true;
+            break;
+          }
+          tc_fence_after();
+          const int key0 = n * kCN;
+          const bool masked = key0 + kCN - 1 > first_last;
+          float m_ref = m;
+          float lt = 0.f;
+#pragma unroll 1
+          for (int ch = 0; ch < 2; ++ch) {
+            float r[64];
+            tmem_ld64(tm_s + ch * 64, r);
+            tmem_wait_ld();
+            if (masked) {
+              const int lim = last - (key0 + ch * 64);  // keys 0..lim of the chunk are attended
+#pragma unroll
+              for (int v = 0; v < 64; ++v) r[v] = v <= lim ? r[v] : neg_inf_f();
+            }
+            float mx[32];
+#pragma unroll
+            for (int v = 0; v < 32; ++v) mx[v] = fmaxf(r[v], r[v + 32]);
+#pragma unroll
+            for (int w = 16; w >= 1; w >>= 1) {
+#pragma unroll
+              for (int v = 0; v < w; ++v) mx[v] = fmaxf(mx[v], mx[v + w]);
+            }
+            const float cm = mx[0] * sl2;
+            const float m_prev = m_ref;
+            if (cm > m_ref + kCRescale) m_ref = cm;
+            if (ch > 0 && __any_sync(0xffffffffu, m_ref != m_prev)) {  // rare
+              const float fac = (m_ref != m_prev) ? ex2(m_prev - m_ref) : 1.f;
+              lt *= fac;
+              uint32_t w0[32];
+              tmem_wait_st();  // chunk 0's P has landed
+              tmem_ld32u(tm_s, w0);
+              tmem_wait_ld();
+#pragma unroll
+              for (int v = 0; v < 32; ++v) w0[v] = scale_pair<T>(w0[v], fac);
+              tmem_st32u(tm_s, w0);
+            }
+            const float mb = (m_ref == neg_inf_f()) ? 0.f : m_ref;
+            uint32_t w[32];
+            float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+            const float2 sl2x2 = make_float2(sl2, sl2), nmb2 = make_float2(-mb, -mb);
+#pragma unroll
+            for (int v = 0; v < 32; ++v) {
+              const float2 x2 = __ffma2_rn(make_float2(r[2 * v], r[2 * v + 1]), sl2x2, nmb2);
+              const float p0 = ex2(x2.x), p1 = ex2(x2.y);
+              ls[v & 1] = __fadd2_rn(ls[v & 1], make_float2(p0, p1));
+              w[v] = pack_pair<T>(p0, p1);
+            }
+            lt += (ls[0].x + ls[1].x) + (ls[0].y + ls[1].y);
+            tmem_st32u(tm_s + ch * 32, w);
+          }
+          // (rows that do not exist hold anything: they never ask for a rescale)
+          const float alpha = (m == neg_inf_f() || !live) ? 1.f : ex2(m - m_ref);
+          if (n > tl.lo && __any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              float r[32];
+              tmem_ld32(tm_o + c * 32, r);
+              tmem_wait_ld();
+#pragma unroll
+              for (int v = 0; v < 32; ++v) r[v] *= alpha;
+              tmem_st32(tm_o + c * 32, r);
+            }
+          }
+          l = l * alpha + lt;
+          m = m_ref;
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(&pfull[x]);
+        }
+        if (failed) break;
+        sb += tl.hi - tl.lo;
+        if (tl.lo < tl.hi) {
+          if (!__all_sync(0xffffffffu, mbar_wait<kPoll>(&odone[x], (uint32_t)ob & 1u, abort))) {
+            failed = true;
+            break;
+          }
+          ++ob;
+          tc_fence_after();
+          if (s_bad[nq & 3]) l = nan;
+          const bool whole = tl.hi - tl.lo == tl.nt;
+          const long long row0 = f.s.row0 + tl.tok0;
+          if (whole) {
+            const float inv = 1.f / l;
+            T *orow = out + (row0 + tok) * out_stride + (long long)(u.g * G + (t - tok * G)) * D;
+#pragma unroll 1
+            for (int ch = 0; ch < D / 32; ++ch) {
+              float o[32];
+              tmem_ld32(tm_o + ch * 32, o);
+              tmem_wait_ld();
+              if (live) {
+                uint4 *o4 = reinterpret_cast<uint4 *>(orow + ch * 32);
+#pragma unroll
+                for (int v = 0; v < 4; ++v)
+                  o4[v] = make_uint4(pack_pair<T>(o[8 * v] * inv, o[8 * v + 1] * inv),
+                                     pack_pair<T>(o[8 * v + 2] * inv, o[8 * v + 3] * inv),
+                                     pack_pair<T>(o[8 * v + 4] * inv, o[8 * v + 5] * inv),
+                                     pack_pair<T>(o[8 * v + 6] * inv, o[8 * v + 7] * inv));
+              }
+            }
+          } else {
+            auto slot_of = [&](int c, int lo) {
+              return slots + ((2 * (size_t)c + (lo == 0 ? 1 : 0)) * 2 + x) * paged_slot_floats(kCM, D);
+            };
+            float *sl = slot_of(b, tl.lo);
+#pragma unroll 1
+            for (int ch = 0; ch < D / 32; ++ch) {
+              float o[32];
+              tmem_ld32(tm_o + ch * 32, o);
+              tmem_wait_ld();
+              if (live) {
+                float4 *o4 = reinterpret_cast<float4 *>(sl + 2 * kCM + (size_t)t * D + ch * 32);
+#pragma unroll
+                for (int v = 0; v < 8; ++v)
+                  __stcg(o4 + v, make_float4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]));
+              }
+            }
+            if (live) __stcg(reinterpret_cast<float2 *>(sl) + t, make_float2(m, l));
+            __threadfence();  // the partial is visible GPU-wide before it counts
+            if (!wg_barrier()) {
+              failed = true;
+              break;
+            }
+            const int b1 = column_at(f.k0, pl.R, pl.P);  // the block of the unit's tile 0
+            if (t == 0) {
+              const unsigned add = (unsigned)(tl.hi - tl.lo);
+              unsigned long long *ctr = counters + 2 * b1 + x;
+              const unsigned before = tagged_add(ctr, add, tag, d_status, epoch);
+              const bool fin = before != 0xffffffffu && before + add == (unsigned)tl.nt;
+              if (fin) *ctr = 0ull;  // a replayed graph uses the same tag again
+              s_last[x] = fin;
+            }
+            if (!wg_barrier()) {
+              failed = true;
+              break;
+            }
+            if (s_last[x]) {
+              __threadfence();
+              for (int e = t; e < rows * (D / 4); e += kCM) {
+                const int r = e / (D / 4), d = (e - r * (D / 4)) * 4;
+                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+                float ls = 0.f, mx = neg_inf_f();
+                for (int c = b1; c < (int)pl.P; ++c) {
+                  const int lo = tiles_before(column_start(pl.R, pl.P, c), f.k0, tl.nt, kCN);
+                  const int hi = tiles_before(column_start(pl.R, pl.P, c + 1), f.k0, tl.nt, kCN);
+                  if (lo >= tl.nt) break;
+                  if (lo >= hi) continue;
+                  const float *ps = slot_of(c, lo);
+                  const float2 ml = __ldcg(reinterpret_cast<const float2 *>(ps) + r);
+                  const float4 v = __ldcg(reinterpret_cast<const float4 *>(ps + 2 * kCM + (size_t)r * D + d));
+                  const float mn = fmaxf(mx, ml.x);
+                  const float mz = mn == neg_inf_f() ? 0.f : mn;
+                  const float wa = ex2(mx - mz), wb = ex2(ml.x - mz);
+                  acc.x = acc.x * wa + v.x * wb;
+                  acc.y = acc.y * wa + v.y * wb;
+                  acc.z = acc.z * wa + v.z * wb;
+                  acc.w = acc.w * wa + v.w * wb;
+                  ls = ls * wa + ml.y * wb;
+                  mx = mn;
+                }
+                const float inv = 1.f / ls;
+                const int tk = r / G;
+                T *p = out + (row0 + tk) * out_stride + (long long)(u.g * G + (r - tk * G)) * D + d;
+                *reinterpret_cast<uint2 *>(p) = make_uint2(pack_pair<T>(acc.x * inv, acc.y * inv),
+                                                           pack_pair<T>(acc.z * inv, acc.w * inv));
+              }
+            }
+          }
+        }
+        ++nq;
+      }
+      if (!failed) advance(f);
+    }
+    if (failed && lane == 0) give_up(abort, d_status, epoch);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) tmem_dealloc(tmem, kCTmemCols);
+}
+
+template <typename T, int D>
+int launch_chunk(const void *q, long long q_stride, const kvs_paged_cache &cache,
+                 const PagedArgs &pa, void *out, long long out_stride, int H, void *workspace,
+                 int *d_status, cudaStream_t stream) {
+  using C = CGeo<D>;
+  static bool configured[kCMaxDevices] = {false};
+  static std::mutex mu;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kCMaxDevices) return KVS_ERR_LAUNCH;
+  {
+    std::lock_guard<std::mutex> lk(mu);
+    if (!configured[dev]) {
+      for (auto kern : {paged_chunk_kernel<T, D, false>, paged_chunk_kernel<T, D, true>}) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) !=
+            cudaSuccess) {
+          cudaGetLastError();
+          return KVS_ERR_LAUNCH;
+        }
+      }
+      configured[dev] = true;
+    }
+  }
+  const int sms = device_sm_count();
+  if (sms <= 0) return KVS_ERR_LAUNCH;
+  const int Hkv = cache.num_kv_heads, G = H / Hkv;
+  CUtensorMap qmap, kmap, vmap;
+  const uint64_t rows = (uint64_t)cache.num_pages * Hkv * cache.page_size;
+  const int box_shift = pa.page_shift < 7 ? pa.page_shift : 7;
+  int rc = make_row_map(&kmap, cache.k_pages, rows, D, cache.dtype, 1 << box_shift, 1);
+  if (rc == KVS_OK) rc = make_row_map(&vmap, cache.v_pages, rows, D, cache.dtype, 1 << box_shift, 1);
+  if (rc == KVS_OK)
+    rc = make_q_map(&qmap, q, pa.num_rows, q_stride, H, D, cache.dtype, kCM / G, G);
+  if (rc != KVS_OK) return rc;
+  const int grid = sms < kPagedMaxBlocks ? sms : kPagedMaxBlocks;
+  const float sl2 = (float)(1.4426950408889634074 / std::sqrt((double)D));
+  const cudaError_t e = launch_pdl(
+      poll_waits() ? paged_chunk_kernel<T, D, true> : paged_chunk_kernel<T, D, false>, dim3(grid),
+      dim3(kCThreads), C::SMEM, stream, static_cast<T *>(out), out_stride, pa, qmap, kmap, vmap, G,
+      Hkv, box_shift, sl2, static_cast<unsigned char *>(workspace), fresh_tag(), d_status);
+  return e == cudaSuccess ? KVS_OK : KVS_ERR_LAUNCH;
+}
+
+}  // namespace
+
+int set_wait_limit_chunk(uint64_t ns) {
+  if (set_unit_wait_limit(ns) != cudaSuccess) {
+    cudaGetLastError();
+    return KVS_ERR_LAUNCH;
+  }
+  return KVS_OK;
+}
+
+// Workspace: 256 bytes (epoch), two counters a block (tiles A and B), then
+// per block two units' partials (begun earlier, not finished), each two tiles.
+size_t paged_chunk_workspace_bytes(int D) {
+  return 256 + (size_t)kPagedMaxBlocks * 16 +
+         4 * (size_t)kPagedMaxBlocks * paged_slot_floats(kCM, D) * 4;
+}
+
+int launch_paged_chunk(const void *q, long long q_stride, const kvs_paged_cache &cache,
+                       const PagedArgs &pa, void *out, long long out_stride, int H,
+                       void *workspace, int *d_status, cudaStream_t stream) {
+#define KVS_CHUNK(T)                                                                            \
+  return cache.head_dim == 64                                                                   \
+             ? launch_chunk<T, 64>(q, q_stride, cache, pa, out, out_stride, H, workspace,       \
+                                   d_status, stream)                                            \
+             : launch_chunk<T, 128>(q, q_stride, cache, pa, out, out_stride, H, workspace,      \
+                                    d_status, stream)
+  if (cache.dtype == KVS_F16) KVS_CHUNK(__half);
+  if (cache.dtype == KVS_BF16) KVS_CHUNK(__nv_bfloat16);
+#undef KVS_CHUNK
+  return KVS_ERR_UNSUPPORTED;
+}
+
+}  // namespace kvs
