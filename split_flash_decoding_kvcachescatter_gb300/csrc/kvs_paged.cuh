@@ -227,4 +227,50 @@ __device__ __forceinline__ bool next_unit(const PagedArgs &a, Unit &u, const Uni
   return false;
 }
 
+// Four accumulator columns of one row, merged over a unit's pieces in column
+// order: block b1's piece began the unit (its slot 2 b1 + 1), those of blocks
+// b1 + 1 .. b2 continue it (slots 2 b).  A slot of `stride` floats has the
+// row's (m, l) at float2 `r` and its accumulators at float `at`.  Pieces are
+// taken eight at a time, all loads of a batch before the first is used, so a
+// batch costs one L2 round trip.
+static __device__ __noinline__ void merge_pieces(const float *slots, size_t stride, int at,
+                                                    int r, int b1, int b2, float4 &acc, float &l) {
+  constexpr int kBatch = 8;
+  acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  l = 0.f;
+  float m = neg_inf_f();
+  for (int c = b1; c <= b2; c += kBatch) {
+    float2 ml[kBatch];
+    float4 v[kBatch];
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      if (c + j <= b2) {
+        const float *ps = slots + (2 * (size_t)(c + j) + (c + j == b1 ? 1 : 0)) * stride;
+        ml[j] = __ldcg(reinterpret_cast<const float2 *>(ps) + r);
+        v[j] = __ldcg(reinterpret_cast<const float4 *>(ps + at));
+      }
+    }
+    float mn = m;
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j)
+      if (c + j <= b2) mn = fmaxf(mn, ml[j].x);
+    const float mz = mn == neg_inf_f() ? 0.f : mn;
+    const float w = exp2f(m - mz);
+    acc = make_float4(acc.x * w, acc.y * w, acc.z * w, acc.w * w);
+    l *= w;
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      if (c + j <= b2) {
+        const float wj = exp2f(ml[j].x - mz);
+        acc.x = fmaf(wj, v[j].x, acc.x);
+        acc.y = fmaf(wj, v[j].y, acc.y);
+        acc.z = fmaf(wj, v[j].z, acc.z);
+        acc.w = fmaf(wj, v[j].w, acc.w);
+        l = fmaf(wj, ml[j].y, l);  // (a NaN sum stays one also under a zero weight)
+      }
+    }
+    m = mn;
+  }
+}
+
 }  // namespace kvs

@@ -17,8 +17,8 @@
 // of kvs_tags.cuh; no block waits for another).  Everything is derived on the device from
 // the positions and offsets, so a captured graph follows them.
 //
-// Block: one producer warp and WK * WR consumer warps.  WK key groups have a
-// ring of stages each (a stage: K and V of one tile, swizzled 128-byte
+// Block: WK * WR consumer warps and a producer warp for each of WK key
+// groups.  A key group has a ring of stages (a stage: K and V of one tile, swizzled 128-byte
 // column blocks moved by tensor-map copies of 16 rows, each looked up in the
 // page table); the WR warps of a group take 16 rows each.  Small row tiles
 // (RT = 16, a decode step) run WK = 4, WR = 1 -- the keys are split over the
@@ -68,7 +68,7 @@ struct PagedGeo {
   static constexpr int OFF_BAD = OFF_BAR + (2 * WK * S + 1) * 8;  // int [WK][S]
   static constexpr int OFF_MISC = OFF_BAD + WK * S * 4;           // abort, last, tag, pad
   static constexpr int SMEM = OFF_MISC + 16;
-  static constexpr int THREADS = (NW + 1) * 32;
+  static constexpr int THREADS = (NW + WK) * 32;  // a producer warp a ring
   static_assert(WK == 1 || WR == 1, "keys or rows over the warps");
   static_assert(S >= 2, "two stages at least");
   static_assert(SMEM <= 227 * 1024, "one block per SM must fit");
@@ -162,9 +162,11 @@ template <typename T, int D>
 struct WarpRows {
   static constexpr bool F32 = std::is_same<T, float>::value;
   static constexpr int KT = F32 ? 16 : 32;
-  static constexpr int NQ = F32 ? D / 2 : D / 4;  // registers of q
+  // float32: q stays in L1 (its fragments would take 64 of the 255 registers)
+  static constexpr int NQ = F32 ? 1 : D / 4;
 
   uint32_t qf[NQ];
+  const T *qrow[2];  // float32: this lane's two rows of q, nullptr where there is none
   float o[D / 8][4];
   float m[2], l[2];
   int lane;
@@ -187,16 +189,7 @@ struct WarpRows {
       const T *src = q + (long long)(f.s.row0 + f.tok0 + tok) * q_stride +
                      (long long)(g * G + (live ? x - tok * G : 0)) * D;
       if constexpr (F32) {
-        // registers [block of 32][half of 16][row half][4]
-#pragma unroll
-        for (int c = 0; c < D / 16; ++c) {
-          const float4 v = live ? __ldcg(reinterpret_cast<const float4 *>(src + 16 * c + 4 * (lane & 3)))
-                                : make_float4(0.f, 0.f, 0.f, 0.f);
-          qf[(c * 2 + hh) * 4 + 0] = __float_as_uint(v.x);
-          qf[(c * 2 + hh) * 4 + 1] = __float_as_uint(v.y);
-          qf[(c * 2 + hh) * 4 + 2] = __float_as_uint(v.z);
-          qf[(c * 2 + hh) * 4 + 3] = __float_as_uint(v.w);
-        }
+        qrow[hh] = live ? src + 4 * (lane & 3) : nullptr;
       } else {
         // registers [k step of 16][a0 a1 a2 a3]: a0, a1 rows, a2, a3 k + 8
 #pragma unroll
@@ -229,13 +222,16 @@ struct WarpRows {
         for (int e = 0; e < 4; ++e) small[j][e] = 0.f;
 #pragma unroll
       for (int c = 0; c < D / 16; ++c) {  // 16 columns: block c / 2, half c % 2
-        uint32_t ah[2][4], al[2][4];      // two k steps of 8
+        uint32_t ah[2][4], al[2][4];      // two k steps of 8: a0: row, even; a1: row + 8; a2, a3: odd
 #pragma unroll
-        for (int e2 = 0; e2 < 2; ++e2)
-#pragma unroll
-          for (int u = 0; u < 4; ++u)  // a0: row, even; a1: row + 8; a2, a3: odd
-            split_tf32(__uint_as_float(qf[(c * 2 + (u & 1)) * 4 + 2 * e2 + (u >> 1)]), ah[e2][u],
-                       al[e2][u]);
+        for (int hh = 0; hh < 2; ++hh) {
+          const float4 v = qrow[hh] ? __ldca(reinterpret_cast<const float4 *>(qrow[hh] + 16 * c))
+                                    : make_float4(0.f, 0.f, 0.f, 0.f);
+          split_tf32(v.x, ah[0][hh], al[0][hh]);
+          split_tf32(v.y, ah[0][2 + hh], al[0][2 + hh]);
+          split_tf32(v.z, ah[1][hh], al[1][hh]);
+          split_tf32(v.w, ah[1][2 + hh], al[1][2 + hh]);
+        }
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
           // (the small products gather apart: the tensor cores truncate each
@@ -427,7 +423,7 @@ __device__ __forceinline__ void store4(T *p, float4 v) {
 
 // ---- the kernel ---------------------------------------------------------------
 template <typename T, int D, int WK, int WR, bool kPoll>
-__global__ void __launch_bounds__((WK * WR + 1) * 32, 1)
+__global__ void __launch_bounds__((WK * WR + WK) * 32, 1)
     paged_stream_kernel(const T *__restrict__ q, long long q_stride, T *__restrict__ out,
                         long long out_stride, PagedArgs pa,
                         const __grid_constant__ CUtensorMap kmap,
@@ -480,45 +476,37 @@ __global__ void __launch_bounds__((WK * WR + 1) * 32, 1)
   const long long x0 = column_start(pl.R, pl.P, b), x1 = column_start(pl.R, pl.P, b + 1);
   Unit u = pl.first;
 
-  if (warp == C::NW) {
-    // ======================= producer =======================================
+  if (warp >= C::NW) {
+    // ======================= producer of ring kw ==============================
+    // (one warp for all rings issued a tile in about 1000 cycles: half the
+    // rate at which HBM could fill them)
     // a decode step reads a row once; row tiles of a chunk share them through L2
     const uint64_t policy = WR == 1 ? policy_evict_first() : policy_evict_normal();
-    uint32_t use[WK];  // tiles put in each ring
-#pragma unroll
-    for (int r = 0; r < WK; ++r) use[r] = 0;
+    const int ring = warp - C::NW;
+    uint32_t n = 0;  // tiles put in the ring
     bool ok = true;
     constexpr int NP = C::KT / 16;  // 16-row pieces of a tile
+    constexpr int AHEAD = 32 / NP;  // tiles whose pages one look-up finds
+    const int piece = lane % NP;    // lanes 0..NP-1: K pieces, NP..2NP-1: V pieces
     do {
       const UnitInfo f = unit_info(pa, u, ln, x0, x1);
       const int32_t *table = pa.page_table + (size_t)u.i * pa.max_pages;
-      // the page of piece c of the tiles from t_lo on: a lane looks up 32
-      // pieces ahead at a time
-      int page = 0, page_base = -1;
-      for (int t = f.t_lo; t < f.t_hi; ++t) {
-        const int c0 = (t - f.t_lo) * NP;
-        if (page_base < 0 || c0 + NP > page_base + 32) {
-          page_base = c0;
-          const int r0 = (f.t_lo * NP + c0 + lane) * 16;
+      int page = 0, k = 0;  // lane: the page of piece `piece` of the ring's tile k + lane / NP
+      for (int t = f.t_lo + ring; t < f.t_hi; t += WK, ++n, ++k) {
+        if (k % AHEAD == 0) {
+          const int r0 = (t + WK * (lane / NP)) * C::KT + 16 * piece;
           page = r0 < f.keys ? __ldca(table + (r0 >> pa.page_shift)) : 0;
         }
-        const int ring = (t - f.t_lo) % WK;
-        uint32_t n = 0;
-#pragma unroll
-        for (int r = 0; r < WK; ++r) n = r == ring ? use[r] : n;
-        const int st = ring * C::S + (int)(n % C::S);
-        if (!mbar_wait<kPoll>(&empty[st], ((n / C::S) & 1u) ^ 1u, abort)) ok = false;
-        if (!__all_sync(0xffffffffu, ok)) {
-          ok = false;
-          break;
-        }
+        const int pg = __shfl_sync(0xffffffffu, page, (k % AHEAD) * NP + piece);
         const int npieces = min(NP, (f.keys - t * C::KT + 15) / 16);
-        // lanes 0..NP-1: K pieces, NP..2NP-1: V pieces
-        const int piece = lane % NP;
-        const int pg = __shfl_sync(0xffffffffu, page, c0 - page_base + piece);
         const bool mine = lane < 2 * NP && piece < npieces;
         const bool wrong = mine && (unsigned)pg >= (unsigned)pa.num_pages;
         const unsigned any_bad = __ballot_sync(0xffffffffu, wrong);
+        const int st = ring * C::S + (int)(n % C::S);
+        if (!__all_sync(0xffffffffu, mbar_wait<kPoll>(&empty[st], ((n / C::S) & 1u) ^ 1u, abort))) {
+          ok = false;
+          break;
+        }
         if (lane == 0) {
           bad[st] = any_bad != 0u;
           if (any_bad) record_status(d_status, KVS_ERR_PAGE);
@@ -532,8 +520,6 @@ __global__ void __launch_bounds__((WK * WR + 1) * 32, 1)
           unsigned char *dst = smem + st * C::STAGE + (lane >= NP ? C::TILE : 0) + piece * C::GB;
           tma_rows(dst, lane >= NP ? &vmap : &kmap, row, &full[st], policy);
         }
-#pragma unroll
-        for (int r = 0; r < WK; ++r) use[r] += r == ring;
       }
       if (!ok) break;
       if (!next_unit(pa, u, f, ln)) break;
@@ -541,13 +527,8 @@ __global__ void __launch_bounds__((WK * WR + 1) * 32, 1)
     if (lane == 0) {
       if (!ok) give_up(abort, d_status, epoch);
       // every copy lands before the block exits
-      for (int r = 0; r < WK; ++r) {
-        uint32_t n = 0;
-#pragma unroll
-        for (int k = 0; k < WK; ++k) n = k == r ? use[k] : n;
-        for (uint32_t j = n > (uint32_t)C::S ? n - C::S : 0u; j < n; ++j)
-          mbar_wait_drain(&full[r * C::S + j % C::S], (j / C::S) & 1u);
-      }
+      for (uint32_t j = n > (uint32_t)C::S ? n - C::S : 0u; j < n; ++j)
+        mbar_wait_drain(&full[ring * C::S + j % C::S], (j / C::S) & 1u);
     }
     return;
   }
@@ -703,7 +684,9 @@ __global__ void __launch_bounds__((WK * WR + 1) * 32, 1)
         if (!consumers_barrier()) return;  // (also: the merge buffers may be written again)
       }
       if (!whole) {
-        const int b1 = column_at(f.k0, pl.R, pl.P);  // the block of the unit's tile 0
+        // the blocks of the unit's first and last tile; every block between has some
+        const int b1 = column_at(f.k0, pl.R, pl.P);
+        const int b2 = column_at(f.k0 + (long long)(f.nt - 1) * C::KT, pl.R, pl.P);
         if (threadIdx.x == 0) {
           const unsigned add = (unsigned)(f.t_hi - f.t_lo);
           const unsigned before = tagged_add(counters + b1, add, tag, d_status, epoch);
@@ -716,26 +699,9 @@ __global__ void __launch_bounds__((WK * WR + 1) * 32, 1)
           __threadfence();
           for (int e = threadIdx.x; e < rows * (D / 4); e += C::NW * 32) {
             const int r = e / (D / 4), d = (e - r * (D / 4)) * 4;
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-            float ls = 0.f, mx = neg_inf_f();
-            for (int c = b1; c < (int)pl.P; ++c) {
-              const int lo = tiles_before(column_start(pl.R, pl.P, c), f.k0, f.nt, C::KT);
-              const int hi = tiles_before(column_start(pl.R, pl.P, c + 1), f.k0, f.nt, C::KT);
-              if (lo >= f.nt) break;
-              if (lo >= hi) continue;
-              const float *ps = slots + (2 * (size_t)c + (lo == 0 ? 1 : 0)) * paged_slot_floats(C::RT, D);
-              const float2 ml = __ldcg(reinterpret_cast<const float2 *>(ps) + r);
-              const float4 v = __ldcg(reinterpret_cast<const float4 *>(ps + 2 * C::RT + (size_t)r * D + d));
-              const float mn = fmaxf(mx, ml.x);
-              const float mz = mn == neg_inf_f() ? 0.f : mn;
-              const float wa = ex2f(mx - mz), wb = ex2f(ml.x - mz);
-              acc.x = acc.x * wa + v.x * wb;
-              acc.y = acc.y * wa + v.y * wb;
-              acc.z = acc.z * wa + v.z * wb;
-              acc.w = acc.w * wa + v.w * wb;
-              ls = ls * wa + ml.y * wb;
-              mx = mn;
-            }
+            float4 acc;
+            float ls;
+            merge_pieces(slots, paged_slot_floats(C::RT, D), 2 * C::RT + r * D + d, r, b1, b2, acc, ls);
             const float inv = 1.f / ls;
             const int tok = r / G;
             store4<T>(orow + (long long)tok * out_stride + (r - tok * G) * D + d,

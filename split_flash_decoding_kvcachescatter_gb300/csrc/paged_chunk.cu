@@ -130,6 +130,52 @@ __device__ __forceinline__ void tma_q(void *dst, const CUtensorMap *map, int hea
       : "memory");
 }
 
+// merge_pieces for NR rows at once (rows r0 + k * step < rows), pieces two at
+// a time: 2 NR loads in flight a thread.  Accumulators of row r at float
+// at + r D + d of a slot.
+template <int NR>
+__device__ __forceinline__ void merge_rows(const float *slots, size_t stride, int at, int D, int d,
+                                           int r0, int step, int rows, int b1, int b2,
+                                           float4 (&acc)[NR], float (&l)[NR]) {
+  float m[NR];
+#pragma unroll
+  for (int k = 0; k < NR; ++k) {
+    acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    l[k] = 0.f;
+    m[k] = neg_inf_f();
+  }
+  for (int c = b1; c <= b2; c += 2) {
+    float2 ml[NR][2];
+    float4 v[NR][2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const float *ps = slots + (2 * (size_t)min(c + j, b2) + (c + j == b1 ? 1 : 0)) * stride;
+#pragma unroll
+      for (int k = 0; k < NR; ++k) {
+        const int r = min(r0 + k * step, rows - 1);
+        ml[k][j] = __ldcg(reinterpret_cast<const float2 *>(ps) + r);
+        v[k][j] = __ldcg(reinterpret_cast<const float4 *>(ps + at + (size_t)r * D + d));
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      if (c + j > b2) break;
+#pragma unroll
+      for (int k = 0; k < NR; ++k) {
+        const float mn = fmaxf(m[k], ml[k][j].x);
+        const float mz = mn == neg_inf_f() ? 0.f : mn;
+        const float wa = ex2(m[k] - mz), wb = ex2(ml[k][j].x - mz);
+        acc[k].x = acc[k].x * wa + v[k][j].x * wb;
+        acc[k].y = acc[k].y * wa + v[k][j].y * wb;
+        acc[k].z = acc[k].z * wa + v[k][j].z * wb;
+        acc[k].w = acc[k].w * wa + v[k][j].w * wb;
+        l[k] = l[k] * wa + ml[k][j].y * wb;
+        m[k] = mn;
+      }
+    }
+  }
+}
+
 // The two tiles of a unit: tokens, key tiles that each attends, and those of
 // this block's column.
 struct CTile {
@@ -603,7 +649,9 @@ __global__ void __launch_bounds__(kCThreads, 1)
               failed = true;
               break;
             }
-            const int b1 = column_at(f.k0, pl.R, pl.P);  // the block of the unit's tile 0
+            // the blocks of tile x's first and last key tile
+            const int b1 = column_at(f.k0, pl.R, pl.P);
+            const int b2 = column_at(f.k0 + (long long)(tl.nt - 1) * kCN, pl.R, pl.P);
             if (t == 0) {
               const unsigned add = (unsigned)(tl.hi - tl.lo);
               unsigned long long *ctr = counters + 2 * b1 + x;
@@ -618,33 +666,26 @@ __global__ void __launch_bounds__(kCThreads, 1)
             }
             if (s_last[x]) {
               __threadfence();
-              for (int e = t; e < rows * (D / 4); e += kCM) {
-                const int r = e / (D / 4), d = (e - r * (D / 4)) * 4;
-                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-                float ls = 0.f, mx = neg_inf_f();
-                for (int c = b1; c < (int)pl.P; ++c) {
-                  const int lo = tiles_before(column_start(pl.R, pl.P, c), f.k0, tl.nt, kCN);
-                  const int hi = tiles_before(column_start(pl.R, pl.P, c + 1), f.k0, tl.nt, kCN);
-                  if (lo >= tl.nt) break;
-                  if (lo >= hi) continue;
-                  const float *ps = slot_of(c, lo);
-                  const float2 ml = __ldcg(reinterpret_cast<const float2 *>(ps) + r);
-                  const float4 v = __ldcg(reinterpret_cast<const float4 *>(ps + 2 * kCM + (size_t)r * D + d));
-                  const float mn = fmaxf(mx, ml.x);
-                  const float mz = mn == neg_inf_f() ? 0.f : mn;
-                  const float wa = ex2(mx - mz), wb = ex2(ml.x - mz);
-                  acc.x = acc.x * wa + v.x * wb;
-                  acc.y = acc.y * wa + v.y * wb;
-                  acc.z = acc.z * wa + v.z * wb;
-                  acc.w = acc.w * wa + v.w * wb;
-                  ls = ls * wa + ml.y * wb;
-                  mx = mn;
+              // four rows a thread in flight (most units have two or three pieces)
+              constexpr int kRowsAhead = 4, kStep = kCM / (D / 4);  // rows a pass
+              const int d = (t % (D / 4)) * 4;
+              const float *base = slots + x * paged_slot_floats(kCM, D);
+              for (int r0 = t / (D / 4); r0 < rows; r0 += kRowsAhead * kStep) {
+                float4 acc[kRowsAhead];
+                float ls[kRowsAhead];
+                merge_rows<kRowsAhead>(base, 2 * paged_slot_floats(kCM, D), 2 * kCM, D, d, r0, kStep,
+                                       rows, b1, b2, acc, ls);
+#pragma unroll
+                for (int k = 0; k < kRowsAhead; ++k) {
+                  const int r = r0 + k * kStep;
+                  if (r >= rows) break;
+                  const float inv = 1.f / ls[k];
+                  const int tk = r / G;
+                  T *p = out + (row0 + tk) * out_stride + (long long)(u.g * G + (r - tk * G)) * D + d;
+                  *reinterpret_cast<uint2 *>(p) =
+                      make_uint2(pack_pair<T>(acc[k].x * inv, acc[k].y * inv),
+                                 pack_pair<T>(acc[k].z * inv, acc[k].w * inv));
                 }
-                const float inv = 1.f / ls;
-                const int tk = r / G;
-                T *p = out + (row0 + tk) * out_stride + (long long)(u.g * G + (r - tk * G)) * D + d;
-                *reinterpret_cast<uint2 *>(p) = make_uint2(pack_pair<T>(acc.x * inv, acc.y * inv),
-                                                           pack_pair<T>(acc.z * inv, acc.w * inv));
               }
             }
           }

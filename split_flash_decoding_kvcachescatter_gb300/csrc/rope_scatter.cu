@@ -2,11 +2,11 @@
 // keys, and the new K and V rows written into a paged cache, in one launch.
 //
 // Mathematics: pair j of a head at position P turns by t = P w_j.  t matters
-// modulo a full turn only, so the kernel keeps w_j / 2 pi as a 64-bit binary
-// fraction of a turn (one double product a thread and pair) and multiplies
-// it by P in wrapping 64-bit integers: the reduction is exact, where a
-// float32 product P w_j would be off by 2^-24 P w_j radians (0.008 at
-// position 131072).  The top 32 bits of the fraction go to sincospi.
+// modulo a full turn only, so the kernel makes w_j / 2 pi a 64-bit binary
+// fraction of a turn (in integers) and multiplies it by P in wrapping 64-bit
+// integers: the reduction is exact, where a float32 product P w_j would be
+// off by 2^-24 P w_j radians (0.008 at position 131072).  The top 32 bits of
+// the fraction go to sincospi.
 //
 // Bound: bytes (each row of q, k, v read once and written once).  A block
 // takes one token, or a slice of its heads when tokens are few: it puts the
@@ -40,15 +40,85 @@ __device__ __forceinline__ int warp_find_seq(const PagedArgs &b, int row, int la
   return __reduce_add_sync(0xffffffffu, n);
 }
 
+// Turns a position, in units of 2^-64 turns: |w| / 2 pi modulo 1.  w = f 2^e
+// with a 24-bit integer f and e < 0 (|w| < 2^24), and 1 / 2 pi to 128 bits,
+// so the integer product f / 2 pi is exact to 2^-64 before the shift by -e.
+__device__ __forceinline__ unsigned long long turns_of(float w) {
+  constexpr unsigned long long kHi = 0x28BE60DB9391054Aull, kLo = 0x7F09D5F47D4D3770ull;
+  const unsigned u = __float_as_uint(w);
+  const unsigned ex = (u >> 23) & 255u;
+  const unsigned long long f = (u & 0x7fffffu) | (ex ? 0x800000u : 0u);
+  const int e = 150 - (int)(ex ? ex : 1u);  // w = f 2^-e
+  // f (hi + lo 2^-64), a number of 64 + 24 bits
+  const unsigned long long low = f * kHi, carry = __umul64hi(f, kLo);
+  const unsigned long long sum = low + carry;
+  const unsigned long long high = __umul64hi(f, kHi) + (sum < low ? 1ull : 0ull);
+  unsigned long long t;
+  if (e >= 128)
+    t = 0ull;
+  else if (e >= 64)
+    t = high >> (e - 64);
+  else if (e > 0)
+    t = (sum >> e) | (high << (64 - e));
+  else
+    t = sum << -e;  // (beyond the documented range: whole turns drop out)
+  return (u >> 31) ? 0ull - t : t;
+}
+
 // grid (num_rows, slices).  VE: elements of a vector; IL: interleaved pairs.
+// A thread's first vectors are loaded before anything is known of the row's
+// sequence, so that the look-ups (offsets, position, page) run in the shadow
+// of the copy.
 template <typename T, int VE, bool IL>
 __global__ void __launch_bounds__(kRopeThreads)
     rope_scatter_kernel(RopeArgs a, PagedArgs b, int *d_status) {
   __shared__ float2 cs[64];
-  grid_dependency_wait();
-  allow_dependent_launch();
   const int tid = threadIdx.x;
   const int row = blockIdx.x;
+  const int half = a.rot / 2;
+  // vectors of a rotated head: pair vectors first, then those copied
+  const int npair = IL ? a.rot / VE : half / VE;
+  const int per_head = npair + (a.D - a.rot) / VE;
+  const int nrot = (a.H + a.Hkv) * per_head;
+  const int total = nrot + a.Hkv * (a.D / VE);
+  const T *q = static_cast<const T *>(a.q) + (long long)row * a.q_stride;
+  const T *k = static_cast<const T *>(a.k) + (long long)row * a.k_stride;
+  const T *v = static_cast<const T *>(a.v) + (long long)row * a.v_stride;
+  const int step = kRopeThreads * gridDim.y;
+  Vec<T, VE> x[kRopeItems], y[kRopeItems];
+  // item it: vector w of head h (q's heads, k's, then v's with every vector copied)
+  auto where = [&](int it, int &h, int &w, int &first) {  // first: its element in the head
+    if (it < nrot) {
+      h = it / per_head;
+      w = it - h * per_head;
+      first = w < npair ? w * VE : a.rot + (w - npair) * VE;
+    } else {
+      const int e = (it - nrot) * VE;
+      h = e / a.D;
+      first = e - h * a.D;
+      h += a.H + a.Hkv;
+      w = npair;
+    }
+  };
+  auto load = [&](int base) {
+#pragma unroll
+    for (int u = 0; u < kRopeItems; ++u) {
+      const int it = base + u * step;
+      if (it >= total) break;
+      int h, w, first;
+      where(it, h, w, first);
+      const T *src = (h < a.H               ? q + h * a.D
+                      : h < a.H + a.Hkv     ? k + (h - a.H) * a.D
+                                            : v + (h - a.H - a.Hkv) * a.D) +
+                     first;
+      x[u] = vec_load<T, VE>(src);
+      if (!IL && w < npair) y[u] = vec_load<T, VE>(src + half);
+    }
+  };
+  int base = blockIdx.y * kRopeThreads + tid;
+  grid_dependency_wait();
+  load(base);
+  allow_dependent_launch();
   if (blockIdx.y == 0)  // the status of every sequence, spread over the blocks
     for (int i = row * kRopeThreads + tid; i < b.M; i += gridDim.x * kRopeThreads) {
       const int err = paged_seq(b, i).err;
@@ -68,83 +138,43 @@ __global__ void __launch_bounds__(kRopeThreads)
       page = -1;
     }
   }
-  for (int j = tid; j < a.rot / 2; j += kRopeThreads) {
-    // turns per position, modulo 1, in units of 2^-64
-    double f = (double)a.inv_freq[j] * 0.15915494309189533577;  // 1 / 2 pi
-    f -= floor(f);
-    const unsigned long long turn = __double2ull_rn(f * 18446744073709551616.0) *
-                                    (unsigned long long)(unsigned)pos;
-    // signed 32-bit fraction of a half turn's angle: t / pi in [-1, 1)
-    const float x = (float)(int)(unsigned)(turn >> 32) * 4.656612873077393e-10f;  // 2^-31
+  if (tid < half) {  // (half <= 64 < kRopeThreads)
+    const unsigned long long turn = turns_of(a.inv_freq[tid]) * (unsigned long long)(unsigned)pos;
+    // the angle over pi, in [-1, 1): the fraction's top 32 bits, signed, times 2^-31
+    const float t = (float)(int)(unsigned)(turn >> 32) * 4.656612873077393e-10f;
     float sn, c;
-    sincospif(x, &sn, &c);
-    cs[j] = make_float2(c * a.scale, sn * a.scale);
+    sincospif(t, &sn, &c);
+    cs[tid] = make_float2(c * a.scale, sn * a.scale);
   }
   __syncthreads();
-  const int half = a.rot / 2;
-  // vectors of a rotated head: pair vectors first, then those copied
-  const int npair = IL ? a.rot / VE : half / VE;
-  const int per_head = npair + (a.D - a.rot) / VE;
-  const int nrot = (a.H + a.Hkv) * per_head;
-  const int total = nrot + a.Hkv * (a.D / VE);
-  const int slot = pos & ((1 << b.page_shift) - 1);
-  const T *q = static_cast<const T *>(a.q) + (long long)row * a.q_stride;
-  const T *k = static_cast<const T *>(a.k) + (long long)row * a.k_stride;
-  const T *v = static_cast<const T *>(a.v) + (long long)row * a.v_stride;
   T *qo = static_cast<T *>(a.q_out) + (long long)row * a.q_out_stride;
-  const size_t head_rows = (size_t)1 << b.page_shift;
-  // row of kv head g in the page
-  const size_t page_row = (size_t)(page < 0 ? 0 : page) * a.Hkv * head_rows + slot;
-  T *kp = static_cast<T *>(a.k_pages) + page_row * a.D;
-  T *vp = static_cast<T *>(a.v_pages) + page_row * a.D;
-  const int step = kRopeThreads * gridDim.y;
-  for (int base = blockIdx.y * kRopeThreads + tid; base < total; base += kRopeItems * step) {
-    Vec<T, VE> x[kRopeItems], y[kRopeItems];
-    T *dst[kRopeItems];
-    int j0[kRopeItems];  // first pair (rotated) or -1 (copied), -2: nothing
+  // kv head g's row in the page: elements g * head_step further
+  const size_t head_step = (size_t)a.D << b.page_shift;
+  const size_t page_at = (size_t)(page < 0 ? 0 : page) * a.Hkv * head_step +
+                         (size_t)(pos & ((1 << b.page_shift) - 1)) * a.D;
+  T *kp = static_cast<T *>(a.k_pages) + page_at;
+  T *vp = static_cast<T *>(a.v_pages) + page_at;
+  for (;;) {
 #pragma unroll
     for (int u = 0; u < kRopeItems; ++u) {
       const int it = base + u * step;
-      j0[u] = -2;
-      if (it >= total) continue;
-      const T *src;
-      if (it < nrot) {
-        const int h = it / per_head;
-        const int w = it - h * per_head;
-        const bool is_q = h < a.H;
-        src = is_q ? q + h * a.D : k + (h - a.H) * a.D;
-        dst[u] = is_q ? qo + h * a.D : page < 0 ? nullptr : kp + (size_t)(h - a.H) * head_rows * a.D;
-        if (w < npair) {
-          j0[u] = IL ? w * (VE / 2) : w * VE;
-          src += w * VE;
-          if (dst[u]) dst[u] += w * VE;
-          if (!IL) y[u] = vec_load<T, VE>(src + half);
-        } else {
-          j0[u] = -1;
-          src += a.rot + (w - npair) * VE;
-          if (dst[u]) dst[u] += a.rot + (w - npair) * VE;
-        }
-      } else {
-        const int e = (it - nrot) * VE;
-        const int g = e / a.D;
-        src = v + e;
-        dst[u] = page < 0 ? nullptr : vp + (size_t)g * head_rows * a.D + (e - g * a.D);
-        j0[u] = -1;
-      }
-      x[u] = vec_load<T, VE>(src);
-    }
-#pragma unroll
-    for (int u = 0; u < kRopeItems; ++u) {
-      if (j0[u] == -2 || dst[u] == nullptr) continue;
+      if (it >= total) break;
+      int h, w, first;
+      where(it, h, w, first);
+      if (page < 0 && h >= a.H) continue;  // nowhere to write
+      T *dst = (h < a.H             ? qo + h * a.D
+                : h < a.H + a.Hkv   ? kp + (h - a.H) * head_step
+                                    : vp + (h - a.H - a.Hkv) * head_step) +
+               first;
       if (bad_pos) {  // (page is -1, so this is q_out)
         const T nan = from_f32<T>(__int_as_float(0x7fc00000));
 #pragma unroll
         for (int e = 0; e < VE; ++e) x[u].e[e] = y[u].e[e] = nan;
-      } else if (j0[u] >= 0) {
+      } else if (w < npair) {
         if (IL) {
 #pragma unroll
           for (int e = 0; e + 1 < VE; e += 2) {
-            const float2 t = cs[j0[u] + e / 2];
+            const float2 t = cs[w * (VE / 2) + e / 2];
             const float p = to_f32(x[u].e[e]), r = to_f32(x[u].e[e + 1]);
             x[u].e[e] = from_f32<T>(p * t.x - r * t.y);
             x[u].e[e + 1] = from_f32<T>(r * t.x + p * t.y);
@@ -152,16 +182,19 @@ __global__ void __launch_bounds__(kRopeThreads)
         } else {
 #pragma unroll
           for (int e = 0; e < VE; ++e) {
-            const float2 t = cs[j0[u] + e];
+            const float2 t = cs[w * VE + e];
             const float p = to_f32(x[u].e[e]), r = to_f32(y[u].e[e]);
             x[u].e[e] = from_f32<T>(p * t.x - r * t.y);
             y[u].e[e] = from_f32<T>(r * t.x + p * t.y);
           }
         }
       }
-      vec_store<T, VE>(dst[u], x[u]);
-      if (!IL && j0[u] >= 0) vec_store<T, VE>(dst[u] + half, y[u]);
+      vec_store<T, VE>(dst, x[u]);
+      if (!IL && w < npair) vec_store<T, VE>(dst + half, y[u]);
     }
+    base += kRopeItems * step;
+    if (base >= total) break;
+    load(base);
   }
 }
 
