@@ -588,8 +588,8 @@ typedef struct kvs_paged_batch {
  *   scale           factor of the rotated part (1 without length scaling)
  * A token with a bad position or page has no page row written; its q_out
  * row is NaN (bad position) or still the rotated q (bad page).
- * Errors: NULL, DIMS, UNSUPPORTED, ALIGN, LAUNCH on the host; ROWS,
- * POSITION, PAGE via d_status.
+ * Errors: NULL, DIMS, UNSUPPORTED (also H / Hkv > 8 or H > 4096), ALIGN,
+ * LAUNCH on the host; ROWS, POSITION, PAGE via d_status.
  */
 int kvs_rope_scatter_paged(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
                            const void *v, int64_t v_stride, void *q_out, int64_t q_out_stride,
@@ -652,8 +652,8 @@ int kvs_rope_frequencies(int rot_dim, double base, int kind, double factor, doub
  *              epoch rule for captured graphs after a KVS_ERR_TIMEOUT)
  * The rows of a sequence with a bad position are NaN; where a sequence needs
  * a bad page, the rows that attend it are NaN and its other rows may be.
- * Errors: NULL, DIMS, UNSUPPORTED (also H / Hkv > 8), ALIGN, WORKSPACE,
- * LAUNCH on the host; ROWS, POSITION, PAGE, TIMEOUT via d_status.
+ * Errors: NULL, DIMS, UNSUPPORTED (also H / Hkv > 8 or H > 4096), ALIGN,
+ * WORKSPACE, LAUNCH on the host; ROWS, POSITION, PAGE, TIMEOUT via d_status.
  */
 size_t kvs_paged_attention_workspace_bytes(int num_heads, int num_kv_heads, int head_dim,
                                            int max_new);

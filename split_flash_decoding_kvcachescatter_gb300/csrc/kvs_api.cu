@@ -435,7 +435,8 @@ static int check_paged(const kvs_paged_cache *cache, const kvs_paged_batch *batc
     return KVS_ERR_DIMS;
   if (cache->dtype != KVS_F32 && cache->dtype != KVS_F16 && cache->dtype != KVS_BF16)
     return KVS_ERR_UNSUPPORTED;
-  if (!head_dim_supported(cache->head_dim) || num_heads / Hkv > 8) return KVS_ERR_UNSUPPORTED;
+  if (!head_dim_supported(cache->head_dim) || num_heads / Hkv > 8 || num_heads > 4096)
+    return KVS_ERR_UNSUPPORTED;
   if (cache->page_size < 16 || (cache->page_size & (cache->page_size - 1)) != 0)
     return KVS_ERR_UNSUPPORTED;
   // rows of the pages and of one sequence are counted in 32 bits

@@ -6,14 +6,14 @@
 // the counts of a row are needed before its first logit is final.  One
 // thread-block cluster takes a row; block r owns an equal slice of the
 // vocabulary and keeps one 32-bit word a token in shared memory (how often
-// generated, whether seen, whether biased).  The blocks share the row's
-// history: each reads its part of the list once and adds every token to the
-// word in its owner's shared memory (distributed shared memory atomics, the
-// equal tokens of a warp combined first, since histories repeat a few tokens
-// often).  After one cluster barrier each block streams its slice with
-// 16-byte loads and stores, and the (value, index) maxima meet as in the
-// batched argmax.  Integer atomics only: the result does not depend on their
-// order.
+// generated, whether seen, whether biased).  Every block reads the whole
+// history (it comes from L2) and counts the tokens of its own slice with
+// shared-memory atomics; the slice's logits are on their way meanwhile, in
+// 16-byte loads.  (Sharing the list out, each entry sent once to its owner's
+// shared memory, measured 24.1 us against 14 us for 32 rows of 152,064 with
+// 4,096 entries: the frequent tokens' updates queue at one block.)  The
+// (value, index) maxima meet in block 0's shared memory.  Integer atomics
+// only: the result does not depend on their order.
 //
 // Arithmetic is one IEEE operation at a time (no fused multiply-add), so a
 // logit is the same whichever variant or alignment handles it.
@@ -42,15 +42,12 @@ struct LogitArgs {
   int *d_status;
 };
 
-__device__ __forceinline__ void red_add_cluster(uint32_t addr, unsigned v) {
-  asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;" ::"r"(addr), "r"(v)
-               : "memory");
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
-__device__ __forceinline__ void red_or_cluster(uint32_t addr, unsigned v) {
-  asm volatile("red.relaxed.cluster.shared::cluster.or.b32 [%0], %1;" ::"r"(addr), "r"(v)
-               : "memory");
+__device__ __forceinline__ void st_cluster_s32(uint32_t addr, int v) {
+  asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
-
 // [lo, hi) of row m in a ragged list, or an empty range when the offsets are
 // bad (`report`: this thread records that).
 __device__ __forceinline__ int2 list_range(const int32_t *offsets, int m, int len, bool report,
@@ -69,19 +66,13 @@ struct RowRules {
   int2 bias;
 };
 
-// One logit: the rules in their order.  `w` is the token's word.
-__device__ __forceinline__ float apply_rules(float x, unsigned w, int id, const RowRules &rr,
-                                             const kvs_logit_rules &r) {
-  if (w != 0u) {
-    const unsigned c = w & kCount;
-    if ((w & kSeen) || c) x = x > 0.f ? __fdiv_rn(x, rr.rep) : __fmul_rn(x, rr.rep);
-    if (c) {
-      x = __fsub_rn(x, __fmul_rn(rr.freq, (float)c));
-      x = __fsub_rn(x, rr.pres);
-    }
-    if (w & kBiased)  // few: walk the list, so that equal ids add up in its order
-      for (int e = rr.bias.x; e < rr.bias.y; ++e)
-        if (__ldca(r.bias_ids + e) == id) x = __fadd_rn(x, __ldca(r.bias_values + e));
+// One logit under the penalties.  `w` is the token's word.
+__device__ __forceinline__ float penalised(float x, unsigned w, const RowRules &rr) {
+  const unsigned c = w & kCount;
+  if ((w & kSeen) || c) x = x > 0.f ? __fdiv_rn(x, rr.rep) : __fmul_rn(x, rr.rep);
+  if (c) {
+    x = __fsub_rn(x, __fmul_rn(rr.freq, (float)c));
+    x = __fsub_rn(x, rr.pres);
   }
   return x;
 }
@@ -90,7 +81,7 @@ __device__ __forceinline__ float apply_rules(float x, unsigned w, int id, const 
 __device__ __forceinline__ unsigned mask_bits(const uint32_t *mask, int id, int V) {
   const int w = id >> 5;
   const unsigned lo = __ldca(mask + w);
-  const unsigned hi = (w + 1) * 32 < V ? __ldca(mask + w + 1) : 0u;
+  const unsigned hi = (id & 31) && (w + 1) * 32 < V ? __ldca(mask + w + 1) : 0u;
   return __funnelshift_r(lo, hi, id & 31);
 }
 
@@ -115,14 +106,20 @@ __device__ __forceinline__ Best warp_best(Best b) {
   return b;
 }
 
-// grid (CS, rows), clusters of (CS, 1, 1); rows past gridDim.y loop.
+// grid (CS, rows), clusters of (CS, 1, 1); rows past gridDim.y loop.  A
+// thread's first kAhead vectors are loaded before the history is counted, so
+// that the row streams in behind the counting.
 template <typename T>
-__global__ void __launch_bounds__(kLogitThreads) logits_kernel(LogitArgs a) {
+__global__ void __launch_bounds__(kLogitThreads, 2) logits_kernel(LogitArgs a) {
   constexpr int VE = 16 / sizeof(T);
-  extern __shared__ unsigned words[];  // [slice]
+  constexpr int kAhead = 3;
+  constexpr int kStep = VE * kLogitThreads;
+  constexpr unsigned kAll = (1u << VE) - 1u;
+  extern __shared__ __align__(16) unsigned words[];  // [slice + 4]
   __shared__ Best s_warp[kLogitThreads / 32];
-  __shared__ float s_v;
-  __shared__ int s_i;
+  __shared__ float s_v[2][16];  // of the cluster's blocks, in block 0; by row parity
+  __shared__ int s_i[2][16];
+  __shared__ int s_twice;  // m + 1: the bias list of row m has an id of this slice twice
   const int t = threadIdx.x;
   const int lane = t & 31;
   const int cs = (int)gridDim.x;
@@ -130,9 +127,24 @@ __global__ void __launch_bounds__(kLogitThreads) logits_kernel(LogitArgs a) {
   const int V = a.V;
   const int lo = min(V, rank * a.slice), hi = min(V, lo + a.slice);
   const bool counts = a.r.history != nullptr || a.r.bias_ids != nullptr;
+  if (t == 0) s_twice = 0;
   grid_dependency_wait();
   allow_dependent_launch();
-  for (int m = blockIdx.y; m < a.M; m += gridDim.y) {  // same trip count in a cluster
+  int parity = 0;
+  for (int m = blockIdx.y; m < a.M; m += gridDim.y, parity ^= 1) {  // same trip count in a cluster
+    const T *x = static_cast<const T *>(a.logits) + (long long)m * a.logits_stride;
+    T *y = a.out ? static_cast<T *>(a.out) + (long long)m * a.out_stride : nullptr;
+    // [lo, va) and [vb, hi) one by one, [va, vb) in aligned 16-byte vectors
+    // where logits and out are aligned alike
+    const int mis = (int)((reinterpret_cast<uintptr_t>(x + lo) & 15u) / sizeof(T));
+    const bool alike = !y || ((reinterpret_cast<uintptr_t>(y + lo) & 15u) / sizeof(T)) == (unsigned)mis;
+    const int va = alike ? min(hi, lo + (mis ? VE - mis : 0)) : hi;
+    const int vb = va + (hi - va) / VE * VE;
+    // token id's word: words[id - lo + pad], so that a vector's words are
+    // 16-byte aligned (slices are whole multiples of 16 bytes: the same pad
+    // in every block)
+    const int pad = mis ? mis & 3 : 0;
+    unsigned *const wl = words + pad - lo;
     const bool report = rank == 0 && t == 0;
     RowRules rr;
     rr.rep = a.r.repetition ? __ldca(a.r.repetition + m) : 1.f;
@@ -148,74 +160,160 @@ __global__ void __launch_bounds__(kLogitThreads) logits_kernel(LogitArgs a) {
         rr.mask = a.r.mask + (size_t)k * ((V + 31) / 32);
       }
     }
+    Vec<T, VE> v[kAhead];
+    unsigned bits[kAhead];  // the vectors' mask bits
+    auto load = [&](int j, int id0) {
+      if (id0 < vb) v[j] = vec_load<T, VE>(x + id0);
+    };
+    auto load_bits = [&](int j, int id0) {
+      if (rr.mask && id0 < vb)  // (aligned vectors lie in one word)
+        bits[j] = mis == 0 ? __ldca(rr.mask + (id0 >> 5)) >> (id0 & 31) : mask_bits(rr.mask, id0, V);
+    };
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) load(j, va + VE * t + j * kStep);
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) load_bits(j, va + VE * t + j * kStep);
     if (counts) {
-      for (int j = t; j < hi - lo; j += kLogitThreads) words[j] = 0u;
-      cluster_sync_all();  // every block's words are zero
-      const uint32_t base = smem_addr(words);
+      constexpr int kBatch = 4;  // history entries of a thread in flight
+      int2 h = make_int2(0, 0);
+      int prompt = 0;
       if (a.r.history) {
-        const int2 h = list_range(a.r.history_offsets, m, a.r.history_len, report, a.d_status);
-        const int n = h.y - h.x;
-        const int prompt = a.r.prompt_lens ? __ldca(a.r.prompt_lens + m) : 0;
-        for (int e0 = rank * kLogitThreads + (t & ~31); e0 < n; e0 += cs * kLogitThreads) {
-          const int e = e0 + lane;
-          const int id = e < n ? __ldca(a.r.history + h.x + e) : -1;
-          const bool made = e >= prompt;
-          const bool ok = id >= 0 && id < V;
-          // equal (token, kind) of the warp become one update by their first lane
-          const unsigned peers = __match_any_sync(0xffffffffu, ok ? (id << 1) | (int)made : -1);
-          if (ok && lane == __ffs(peers) - 1) {
-            const int owner = id / a.slice;
-            uint32_t at;
-            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
-                         : "=r"(at)
-                         : "r"(base + 4u * (uint32_t)(id - owner * a.slice)), "r"(owner));
-            if (made)
-              red_add_cluster(at, (unsigned)__popc(peers));
+        h = list_range(a.r.history_offsets, m, a.r.history_len, report, a.d_status);
+        if (a.r.prompt_lens) prompt = __ldca(a.r.prompt_lens + m);
+      }
+      const int n = h.y - h.x;
+      int id[kBatch];
+      auto fetch = [&](int e0) {
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+          const int e = e0 + j * kLogitThreads;
+          id[j] = e < n ? __ldca(a.r.history + h.x + e) : -1;
+        }
+      };
+      fetch(t);
+      for (int j = 4 * t; j < a.slice + 4; j += 4 * kLogitThreads)
+        *reinterpret_cast<uint4 *>(words + j) = make_uint4(0u, 0u, 0u, 0u);
+      __syncthreads();  // the words are zero
+      for (int e0 = t; e0 < n; e0 += kBatch * kLogitThreads) {
+        if (e0 != t) fetch(e0);
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+          if (id[j] >= lo && id[j] < hi) {
+            if (e0 + j * kLogitThreads >= prompt)
+              atomicAdd(&wl[id[j]], 1u);
             else
-              red_or_cluster(at, kSeen);
+              atomicOr(&wl[id[j]], kSeen);
           }
         }
       }
       if (a.r.bias_ids) {
         rr.bias = list_range(a.r.bias_offsets, m, a.r.bias_len, report, a.d_status);
         for (int e = rr.bias.x + t; e < rr.bias.y; e += kLogitThreads) {
-          const int id = __ldca(a.r.bias_ids + e);  // every block marks its own slice
-          if (id >= lo && id < hi) atomicOr(&words[id - lo], kBiased);
+          const int bid = __ldca(a.r.bias_ids + e);
+          if (bid >= lo && bid < hi && (atomicOr(&wl[bid], kBiased) & kBiased)) s_twice = m + 1;
         }
       }
-      cluster_sync_all();  // every update has landed
+      __syncthreads();  // every update has landed
     }
-    const T *x = static_cast<const T *>(a.logits) + (long long)m * a.logits_stride;
-    T *y = a.out ? static_cast<T *>(a.out) + (long long)m * a.out_stride : nullptr;
     Best b{neg_inf_f(), 0x7fffffff};
-    auto one = [&](int id) {
-      float f = to_f32(x[id]);
-      if (counts) f = apply_rules(f, words[id - lo], id, rr, a.r);
+    auto one = [&](int id, unsigned w, float bias_free) {  // bias_free: the penalised logit
+      float f = bias_free;
+      if (w & kBiased) {
+        // the list's values on this id, in its order
+        for (int e = rr.bias.x; e < rr.bias.y; ++e)
+          if (__ldca(a.r.bias_ids + e) == id) f = __fadd_rn(f, __ldca(a.r.bias_values + e));
+      }
       if (rr.mask && !((__ldca(rr.mask + (id >> 5)) >> (id & 31)) & 1u)) f = neg_inf_f();
       const T o = from_f32<T>(f);
       if (y) y[id] = o;
       take(b, to_f32(o), id);
     };
-    // [lo, va) and [vb, hi) one by one, [va, vb) in aligned 16-byte vectors
-    // where logits and out are aligned alike
-    const int mis = (int)((reinterpret_cast<uintptr_t>(x + lo) & 15u) / sizeof(T));
-    const bool alike = !y || ((reinterpret_cast<uintptr_t>(y + lo) & 15u) / sizeof(T)) == (unsigned)mis;
-    const int va = alike ? min(hi, lo + (mis ? VE - mis : 0)) : hi;
-    const int vb = va + (hi - va) / VE * VE;
-    for (int id = lo + t; id < va; id += kLogitThreads) one(id);
-    for (int id = vb + t; id < hi; id += kLogitThreads) one(id);
-    for (int id0 = va + VE * t; id0 < vb; id0 += VE * kLogitThreads) {
-      Vec<T, VE> v = vec_load<T, VE>(x + id0);
-      const unsigned bits = rr.mask ? mask_bits(rr.mask, id0, V) : ~0u;
+    auto scalar = [&](int id) {
+      const unsigned w = counts ? wl[id] : 0u;
+      if (!(w & kBiased)) one(id, w, penalised(to_f32(x[id]), w, rr));
+    };
+    // The biased tokens, a thread an entry of the list: nothing else touches
+    // them, so this may run beside the rest.  With no id twice in the slice
+    // (the usual list) an entry is its token's only one; else the first entry
+    // of an id adds up the list.
+    for (int e = rr.bias.x + t; e < rr.bias.y; e += kLogitThreads) {
+      const int id = __ldca(a.r.bias_ids + e);
+      if (id < lo || id >= hi) continue;
+      bool first = true;
+      if (s_twice == m + 1)
+        for (int k = rr.bias.x; k < e && first; ++k) first = __ldca(a.r.bias_ids + k) != id;
+      if (!first) continue;
+      const float f = penalised(to_f32(x[id]), wl[id], rr);
+      if (s_twice == m + 1)
+        one(id, kBiased, f);
+      else
+        one(id, 0u, __fadd_rn(f, __ldca(a.r.bias_values + e)));
+    }
+    for (int id = lo + t; id < va; id += kLogitThreads) scalar(id);
+    for (int id = vb + t; id < hi; id += kLogitThreads) scalar(id);
+    for (int i0 = va + VE * t; i0 < vb; i0 += kAhead * kStep) {
 #pragma unroll
-      for (int e = 0; e < VE; ++e) {
-        float f = to_f32(v.e[e]);
-        if (counts) f = apply_rules(f, words[id0 - lo + e], id0 + e, rr, a.r);
-        if (!((bits >> e) & 1u)) f = neg_inf_f();
-        v.e[e] = from_f32<T>(f);
-        take(b, to_f32(v.e[e]), id0 + e);
+      for (int j = 0; j < kAhead; ++j) {
+        const int id0 = i0 + j * kStep;
+        if (id0 >= vb) break;
+        Vec<T, VE> u = v[j];
+        const unsigned mb = bits[j];
+        load(j, id0 + kAhead * kStep);  // the slot's next vector
+        load_bits(j, id0 + kAhead * kStep);
+        unsigned biased = 0u;  // elements that the loop above has
+        if (counts) {
+          uint4 w[VE / 4];
+          unsigned any = 0u;
+#pragma unroll
+          for (int k = 0; k < VE / 4; ++k) {
+            w[k] = *reinterpret_cast<const uint4 *>(wl + id0 + 4 * k);
+            any |= w[k].x | w[k].y | w[k].z | w[k].w;
+          }
+          if (any != 0u) {  // few vectors hold a token with a word
+#pragma unroll
+            for (int e = 0; e < VE; ++e) {
+              const uint4 q = w[e / 4];
+              const unsigned word = e % 4 == 0 ? q.x : e % 4 == 1 ? q.y : e % 4 == 2 ? q.z : q.w;
+              u.e[e] = from_f32<T>(penalised(to_f32(u.e[e]), word, rr));
+              if (word & kBiased) biased |= 1u << e;
+            }
+          }
+        }
+        if (rr.mask && (mb & kAll) != kAll) {
+#pragma unroll
+          for (int e = 0; e < VE; ++e)
+            if (!((mb >> e) & 1u)) u.e[e] = from_f32<T>(neg_inf_f());
+        }
+        if (biased) {
+#pragma unroll
+          for (int e = 0; e < VE; ++e)
+            if (!((biased >> e) & 1u)) {
+              if (y) y[id0 + e] = u.e[e];
+              take(b, to_f32(u.e[e]), id0 + e);
+            }
+          continue;
+        }
+        if (y) vec_store<T, VE>(y + id0, u);
+        // the vector's maximum (fmaxf passes over NaN) and the first element
+        // that holds it; a thread's vectors come in ascending order, so a
+        // later one wins only if it is larger (or if the biased tokens, which
+        // came before, hold the same value at a larger index)
+        float mx = to_f32(u.e[VE - 1]);
+        int at = VE - 1;
+#pragma unroll
+        for (int e = VE - 2; e >= 0; --e) {
+          const float f = to_f32(u.e[e]);
+          at = f >= mx || mx != mx ? e : at;
+          mx = fmaxf(mx, f);
+        }
+        const bool better = mx > b.v || (mx == b.v && id0 + at < b.i);
+        b.i = better ? id0 + at : b.i;
+        b.v = better ? mx : b.v;
       }
-      if (y) vec_store<T, VE>(y + id0, v);
+    }
+    if (!a.ids) {
+      __syncthreads();  // the words may be cleared for the next row
+      continue;
     }
     b = warp_best(b);
     if (lane == 0) s_warp[t >> 5] = b;
@@ -224,21 +322,20 @@ __global__ void __launch_bounds__(kLogitThreads) logits_kernel(LogitArgs a) {
       Best c = (t < kLogitThreads / 32) ? s_warp[t] : Best{neg_inf_f(), 0x7fffffff};
       c = warp_best(c);
       if (t == 0) {
-        s_v = c.v;
-        s_i = c.i;
+        st_cluster_f32(dsmem_addr(&s_v[parity][rank], 0), c.v);
+        st_cluster_s32(dsmem_addr(&s_i[parity][rank], 0), c.i);
       }
     }
-    cluster_sync_all();  // every block's maximum is in its shared memory
-    if (rank == 0 && t < 32 && a.ids) {
+    cluster_sync_all();  // every block's maximum is in block 0
+    if (rank == 0 && t < 32) {
       Best c{neg_inf_f(), 0x7fffffff};
       if (t < cs) {
-        c.v = ld_dsmem_f32(dsmem_addr(&s_v, t));
-        c.i = ld_dsmem_s32(dsmem_addr(&s_i, t));
+        c.v = s_v[parity][t];
+        c.i = s_i[parity][t];
       }
       c = warp_best(c);
       if (t == 0) a.ids[m] = c.v == neg_inf_f() ? 0 : c.i;
     }
-    cluster_sync_all();  // block 0 has read them: they, and the words, may be overwritten
   }
 }
 
@@ -315,7 +412,7 @@ int launch_logits_impl(LogitArgs a, cudaStream_t stream) {
   const long long row_bytes = (long long)a.V * sizeof(T);
   auto slice_of = [&](int k) { return ((a.V + (1 << k) - 1) / (1 << k) + 31) / 32 * 32; };
   const bool counts = a.r.history != nullptr || a.r.bias_ids != nullptr;
-  auto words_of = [&](int k) { return counts ? (long long)slice_of(k) * 4 : 0ll; };
+  auto words_of = [&](int k) { return counts ? (long long)(slice_of(k) + 4) * 4 : 0ll; };
   int k = li->top;
   while (k > 0 && (a.M > li->active[k] || (row_bytes >> k) < (8 << 10))) --k;
   while (k < li->top && words_of(k) > li->smem) ++k;

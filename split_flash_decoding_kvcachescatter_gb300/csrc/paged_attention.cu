@@ -53,7 +53,7 @@ struct PagedGeo {
   static constexpr bool F32 = std::is_same<T, float>::value;
   static constexpr int NW = WK * WR;         // consumer warps
   static constexpr int RT = 16 * WR;         // rows of a unit
-  static constexpr int KT = F32 ? 16 : 32;   // keys of a tile
+  static constexpr int KT = F32 && D == 128 ? 16 : 32;  // keys of a tile
   static constexpr int GB = 16 * D * (int)sizeof(T);  // bytes of a 16-row copy
   static constexpr int BLK = 2048;           // one of its column blocks
   static constexpr int TILE = KT / 16 * GB;  // K (or V) of a stage
@@ -161,15 +161,23 @@ __device__ __forceinline__ int key_of_col(int n) {
 template <typename T, int D>
 struct WarpRows {
   static constexpr bool F32 = std::is_same<T, float>::value;
-  static constexpr int KT = F32 ? 16 : 32;
-  // float32: q stays in L1 (its fragments would take 64 of the 255 registers)
-  static constexpr int NQ = F32 ? 1 : D / 4;
+  static constexpr int KT = F32 && D == 128 ? 16 : 32;
+  // float32 with D = 128: q stays in L1 (its fragments would take 64 of the
+  // 255 registers)
+  static constexpr bool QL1 = F32 && D == 128;
+  static constexpr int NQ = QL1 ? 1 : F32 ? D / 2 : D / 4;
 
   uint32_t qf[NQ];
-  const T *qrow[2];  // float32: this lane's two rows of q, nullptr where there is none
+  const T *qrow[2];  // QL1: this lane's two rows of q, nullptr where there is none
   float o[D / 8][4];
   float m[2], l[2];
   int lane;
+
+  // Four columns (from 16 c + 4 q) of this lane's row half hh (float32).
+  __device__ __forceinline__ float4 q_piece(int hh, int c) const {
+    return qrow[hh] ? __ldca(reinterpret_cast<const float4 *>(qrow[hh] + 16 * c))
+                    : make_float4(0.f, 0.f, 0.f, 0.f);
+  }
 
   // Rows 16 w .. of the unit: row x is token x / G of the tile, head x % G.
   __device__ __forceinline__ void start(const T *q, long long q_stride, int w, int rows, int G,
@@ -190,6 +198,16 @@ struct WarpRows {
                      (long long)(g * G + (live ? x - tok * G : 0)) * D;
       if constexpr (F32) {
         qrow[hh] = live ? src + 4 * (lane & 3) : nullptr;
+        if constexpr (!QL1) {  // registers [column group of 16][row half][4]
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c) {
+            const float4 v = q_piece(hh, c);
+            qf[(c * 2 + hh) * 4 + 0] = __float_as_uint(v.x);
+            qf[(c * 2 + hh) * 4 + 1] = __float_as_uint(v.y);
+            qf[(c * 2 + hh) * 4 + 2] = __float_as_uint(v.z);
+            qf[(c * 2 + hh) * 4 + 3] = __float_as_uint(v.w);
+          }
+        }
       } else {
         // registers [k step of 16][a0 a1 a2 a3]: a0, a1 rows, a2, a3 k + 8
 #pragma unroll
@@ -225,8 +243,14 @@ struct WarpRows {
         uint32_t ah[2][4], al[2][4];      // two k steps of 8: a0: row, even; a1: row + 8; a2, a3: odd
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
-          const float4 v = qrow[hh] ? __ldca(reinterpret_cast<const float4 *>(qrow[hh] + 16 * c))
-                                    : make_float4(0.f, 0.f, 0.f, 0.f);
+          float4 v;
+          if constexpr (QL1) {
+            v = q_piece(hh, c);
+          } else {
+            const uint32_t *r = &qf[(c * 2 + hh) * 4];
+            v = make_float4(__uint_as_float(r[0]), __uint_as_float(r[1]), __uint_as_float(r[2]),
+                            __uint_as_float(r[3]));
+          }
           split_tf32(v.x, ah[0][hh], al[0][hh]);
           split_tf32(v.y, ah[0][2 + hh], al[0][2 + hh]);
           split_tf32(v.z, ah[1][hh], al[1][hh]);
@@ -238,7 +262,8 @@ struct WarpRows {
           // sum, so a long chain of additions would lose its last bits)
           const int row = 8 * j + key_of_col<true>(lane >> 2);
           const int pc = ((lane & 3) + 4 * (c & 1)) ^ (row & 7);
-          const float4 kv = lds_f4(sk + (c >> 1) * 2048 + row * 128 + pc * 16);
+          const float4 kv =
+              lds_f4(sk + (j >> 1) * kGroup + (c >> 1) * 2048 + (row & 15) * 128 + pc * 16);
           uint32_t bh[4], bl[4];
           split_tf32(kv.x, bh[0], bl[0]);
           split_tf32(kv.y, bh[1], bl[1]);
@@ -337,8 +362,8 @@ struct WarpRows {
         for (int j = 0; j < NT; ++j) {
           const int r0 = 8 * j + key_of_col<true>(2 * (lane & 3));
           const int r1 = 8 * j + key_of_col<true>(2 * (lane & 3) + 1);
-          const float4 v0 = lds_f4(sv + b * 2048 + r0 * 128 + (n ^ (r0 & 7)) * 16);
-          const float4 v1 = lds_f4(sv + b * 2048 + r1 * 128 + (n ^ (r1 & 7)) * 16);
+          const float4 v0 = lds_f4(sv + (j >> 1) * kGroup + b * 2048 + (r0 & 15) * 128 + (n ^ (r0 & 7)) * 16);
+          const float4 v1 = lds_f4(sv + (j >> 1) * kGroup + b * 2048 + (r1 & 15) * 128 + (n ^ (r1 & 7)) * 16);
           const float e0[4] = {v0.x, v0.y, v0.z, v0.w}, e1[4] = {v1.x, v1.y, v1.z, v1.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {

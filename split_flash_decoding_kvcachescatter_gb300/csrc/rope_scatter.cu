@@ -32,13 +32,32 @@ struct RopeArgs {
   float scale;
 };
 
-// Index of the sequence whose rows hold `row`, by one warp (every lane gets
-// it): the number of sequences that end at or before it.
-__device__ __forceinline__ int warp_find_seq(const PagedArgs &b, int row, int lane) {
+// The sequence whose rows hold `row`, by one warp (every lane gets index and
+// sequence): its index is the number of sequences that end at or before the
+// row, M behind the last one.
+__device__ __forceinline__ int warp_find_seq(const PagedArgs &b, int row, int lane, PagedSeq &s) {
+  if (b.M <= 32) {  // offsets and positions in one round trip
+    PagedSeq mine{0, 0, 0, KVS_OK};
+    if (lane < b.M) mine = paged_seq(b, lane);
+    const bool before = lane < b.M && __ldca(b.row_offsets + lane + 1) <= row;
+    const int i = __popc(__ballot_sync(0xffffffffu, before));
+    const int src = i & 31;
+    s.p = __shfl_sync(0xffffffffu, mine.p, src);
+    s.n = __shfl_sync(0xffffffffu, mine.n, src);
+    s.row0 = __shfl_sync(0xffffffffu, mine.row0, src);
+    s.err = __shfl_sync(0xffffffffu, mine.err, src);
+    return i;
+  }
   int n = 0;
   for (int i = lane; i < b.M; i += 32) n += __ldca(b.row_offsets + i + 1) <= row;
-  return __reduce_add_sync(0xffffffffu, n);
+  n = __reduce_add_sync(0xffffffffu, n);
+  if (n < b.M) s = paged_seq(b, n);
+  return n;
 }
+
+// Where pair j's (cos, sin) sits in shared memory: one gap for eight pairs,
+// so that the eight lanes of a head that read pairs 8 apart hit 16 banks.
+__device__ __forceinline__ constexpr int cs_at(int j) { return j + (j >> 3); }
 
 // Turns a position, in units of 2^-64 turns: |w| / 2 pi modulo 1.  w = f 2^e
 // with a 24-bit integer f and e < 0 (|w| < 2^24), and 1 / 2 pi to 128 bits,
@@ -70,15 +89,16 @@ __device__ __forceinline__ unsigned long long turns_of(float w) {
 // sequence, so that the look-ups (offsets, position, page) run in the shadow
 // of the copy.
 template <typename T, int VE, bool IL>
-__global__ void __launch_bounds__(kRopeThreads)
+__global__ void __launch_bounds__(kRopeThreads, 10)
     rope_scatter_kernel(RopeArgs a, PagedArgs b, int *d_status) {
-  __shared__ float2 cs[64];
+  __shared__ float2 cs[cs_at(64)];
   const int tid = threadIdx.x;
   const int row = blockIdx.x;
   const int half = a.rot / 2;
   // vectors of a rotated head: pair vectors first, then those copied
   const int npair = IL ? a.rot / VE : half / VE;
   const int per_head = npair + (a.D - a.rot) / VE;
+  const float inv_per_head = 1.f / (float)per_head;
   const int nrot = (a.H + a.Hkv) * per_head;
   const int total = nrot + a.Hkv * (a.D / VE);
   const T *q = static_cast<const T *>(a.q) + (long long)row * a.q_stride;
@@ -89,7 +109,7 @@ __global__ void __launch_bounds__(kRopeThreads)
   // item it: vector w of head h (q's heads, k's, then v's with every vector copied)
   auto where = [&](int it, int &h, int &w, int &first) {  // first: its element in the head
     if (it < nrot) {
-      h = it / per_head;
+      h = (int)(((float)it + 0.5f) * inv_per_head);  // it / per_head (it < 2^20)
       w = it - h * per_head;
       first = w < npair ? w * VE : a.rot + (w - npair) * VE;
     } else {
@@ -124,9 +144,9 @@ __global__ void __launch_bounds__(kRopeThreads)
       const int err = paged_seq(b, i).err;
       if (err != KVS_OK) record_status(d_status, err);
     }
-  const int i = warp_find_seq(b, row, tid & 31);
+  PagedSeq s{0, 0, 0, KVS_OK};
+  const int i = warp_find_seq(b, row, tid & 31, s);
   if (i >= b.M) return;  // a row behind the last sequence
-  const PagedSeq s = paged_seq(b, i);
   if (s.err == KVS_ERR_ROWS || row < s.row0 || row >= s.row0 + s.n) return;
   const bool bad_pos = s.err != KVS_OK;
   const int pos = s.p + (row - s.row0);
@@ -144,7 +164,7 @@ __global__ void __launch_bounds__(kRopeThreads)
     const float t = (float)(int)(unsigned)(turn >> 32) * 4.656612873077393e-10f;
     float sn, c;
     sincospif(t, &sn, &c);
-    cs[tid] = make_float2(c * a.scale, sn * a.scale);
+    cs[cs_at(tid)] = make_float2(c * a.scale, sn * a.scale);
   }
   __syncthreads();
   T *qo = static_cast<T *>(a.q_out) + (long long)row * a.q_out_stride;
@@ -174,7 +194,7 @@ __global__ void __launch_bounds__(kRopeThreads)
         if (IL) {
 #pragma unroll
           for (int e = 0; e + 1 < VE; e += 2) {
-            const float2 t = cs[w * (VE / 2) + e / 2];
+            const float2 t = cs[cs_at(w * (VE / 2) + e / 2)];
             const float p = to_f32(x[u].e[e]), r = to_f32(x[u].e[e + 1]);
             x[u].e[e] = from_f32<T>(p * t.x - r * t.y);
             x[u].e[e + 1] = from_f32<T>(r * t.x + p * t.y);
@@ -182,7 +202,7 @@ __global__ void __launch_bounds__(kRopeThreads)
         } else {
 #pragma unroll
           for (int e = 0; e < VE; ++e) {
-            const float2 t = cs[w * VE + e];
+            const float2 t = cs[cs_at(w * VE + e)];
             const float p = to_f32(x[u].e[e]), r = to_f32(y[u].e[e]);
             x[u].e[e] = from_f32<T>(p * t.x - r * t.y);
             y[u].e[e] = from_f32<T>(r * t.x + p * t.y);
