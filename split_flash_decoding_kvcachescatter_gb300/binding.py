@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 import torch
@@ -82,6 +83,8 @@ class KvsError(RuntimeError):
 def lib() -> ctypes.CDLL:
     """The loaded library (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -634,6 +637,7 @@ class PagedCache:
                                          self.page_size, self.num_kv_heads, self.head_dim,
                                          _DTYPES[k_pages.dtype])
         self._addr = ctypes.addressof(self._struct)
+        self._call = lib().kvs_paged_attention, lib().kvs_rope_scatter_paged
 
 
 class PagedBatch:
@@ -661,34 +665,30 @@ class PagedBatch:
         self._addr = ctypes.addressof(self._struct)
 
 
-def _call_device(t: torch.Tensor, where: str) -> int:
-    """The current device, which the call's tensors (t is one) must be on."""
-    dev = t.get_device()
-    if dev != torch.cuda.current_device():
+# The paged-cache and logit calls are a few microseconds of GPU work in a
+# decode step, so their checks are written to cost little: handles are
+# checked once, tensors by as few attribute reads as say it.
+_get_device = torch._C._cuda_getDevice
+_get_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _call_device(dev: int, where: str) -> None:
+    """The call's tensors (on device dev) must be on the current device."""
+    if dev < 0 or dev != _get_device():
         raise ValueError(f"{where}: the tensors are on device {dev}, which is not the current one")
-    return dev
 
 
-def _call_stream(stream, dev: int) -> int:
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev)
-    return _stream(stream)
-
-
-def _rows(t: torch.Tensor, name: str, rows: int, heads: int, D: int, dtype, dev: int):
-    """Pointer and row stride of a [rows, heads, D] tensor whose rows are contiguous."""
-    if t.dtype != dtype or t.get_device() != dev or t.shape != (rows, heads, D):
-        raise TypeError(f"{name}: need a {dtype} tensor [{rows}, {heads}, {D}] on device {dev}, got "
+def _rows(t: torch.Tensor, name: str, shape, dtype, dev: int):
+    """Pointer and row stride of a tensor [rows, heads, D] whose rows are contiguous."""
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != shape:
+        raise TypeError(f"{name}: need a {dtype} tensor {list(shape)} on device {dev}, got "
                         f"{tuple(t.shape)} {t.dtype} {t.device}")
+    if t.is_contiguous():
+        return t.data_ptr(), shape[1] * shape[2]
     s0, s1, s2 = t.stride()
-    if s2 != 1 or (s1 != D and heads > 1):
+    if s2 != 1 or (s1 != shape[2] and shape[1] > 1):
         raise TypeError(f"{name}: the [heads, D] rows must be contiguous, got strides {t.stride()}")
-    return t.data_ptr(), s0 if rows > 1 else heads * D
-
-
-def _same_device(cache, batch, dev, where):
-    if cache.device_index != dev or batch.device_index != dev:
-        raise ValueError(f"{where}: cache, batch and tensors on different devices")
+    return t.data_ptr(), s0
 
 
 def kvs_rope_frequencies(rot_dim, base=10000.0, kind=KVS_ROPE_PLAIN, factor=1.0, original_len=0.0,
@@ -710,21 +710,23 @@ def kvs_rope_scatter_paged(q, k, v, q_out, cache, batch, inv_freq, interleaved=F
     to q_out (q itself is fine), rotated k and plain v into the pages of a PagedCache.  Rows may
     be strided (column blocks of one matrix).  The head's first 2 * inv_freq.numel() elements
     turn, the rest is copied."""
-    dev = _call_device(q, "kvs_rope_scatter_paged")
-    _same_device(cache, batch, dev, "kvs_rope_scatter_paged")
-    N, D, Hkv, dt = batch.num_rows, cache.head_dim, cache.num_kv_heads, cache.dtype
+    dev, dt, N, D = cache.device_index, cache.dtype, batch.num_rows, cache.head_dim
+    _call_device(dev, "kvs_rope_scatter_paged")
+    if batch.device_index != dev:
+        raise ValueError("kvs_rope_scatter_paged: cache and batch on different devices")
     H = q.shape[1] if q.dim() == 3 else -1
-    if inv_freq.dtype != torch.float32 or inv_freq.get_device() != dev or inv_freq.dim() != 1 or \
-            not inv_freq.is_contiguous():
+    if inv_freq.dtype is not torch.float32 or inv_freq.get_device() != dev or \
+            inv_freq.dim() != 1 or not inv_freq.is_contiguous():
         raise TypeError("inv_freq: need a contiguous float32 vector on the tensors' device")
-    qp, qs = _rows(q, "q", N, H, D, dt, dev)
-    kp, ks = _rows(k, "k", N, Hkv, D, dt, dev)
-    vp, vs = _rows(v, "v", N, Hkv, D, dt, dev)
-    op, os_ = _rows(q_out, "q_out", N, H, D, dt, dev)
-    rc = lib().kvs_rope_scatter_paged(qp, qs, kp, ks, vp, vs, op, os_, cache._addr, batch._addr,
-                                      inv_freq.data_ptr(), H, 2 * inv_freq.numel(),
-                                      1 if interleaved else 0, scale, _status_ptr(d_status),
-                                      _call_stream(stream, dev))
+    of_q, of_kv = (N, H, D), (N, cache.num_kv_heads, D)
+    qp, qs = _rows(q, "q", of_q, dt, dev)
+    kp, ks = _rows(k, "k", of_kv, dt, dev)
+    vp, vs = _rows(v, "v", of_kv, dt, dev)
+    op, os_ = _rows(q_out, "q_out", of_q, dt, dev)
+    rc = cache._call[1](qp, qs, kp, ks, vp, vs, op, os_, cache._addr, batch._addr,
+                        inv_freq.data_ptr(), H, 2 * inv_freq.numel(), 1 if interleaved else 0,
+                        scale, 0 if d_status is None else _status_ptr(d_status),
+                        _get_stream(dev) if stream is None else _stream(stream))
     if rc != KVS_OK:
         raise KvsError(rc, "kvs_rope_scatter_paged")
     return q_out
@@ -742,31 +744,39 @@ def paged_attention_workspace(cache, batch, num_heads, device=None):
 def kvs_paged_attention(q, cache, batch, out, workspace=None, d_status=None, stream=None):
     """out [num_rows, H, D] = attention of every new token of a PagedBatch over its sequence's
     pages, rows 0 .. its own position."""
-    dev = _call_device(q, "kvs_paged_attention")
-    _same_device(cache, batch, dev, "kvs_paged_attention")
+    dev, dt = cache.device_index, cache.dtype
+    _call_device(dev, "kvs_paged_attention")
+    if batch.device_index != dev:
+        raise ValueError("kvs_paged_attention: cache and batch on different devices")
     if workspace is None:
         raise ValueError("kvs_paged_attention: pass a workspace (see "
                          "binding.paged_attention_workspace)")
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        raise TypeError("kvs_paged_attention: the workspace must be a contiguous tensor on the "
+                        "tensors' device")
     H = q.shape[1] if q.dim() == 3 else -1
-    qp, qs = _rows(q, "q", batch.num_rows, H, cache.head_dim, cache.dtype, dev)
-    op, os_ = _rows(out, "out", batch.num_rows, H, cache.head_dim, cache.dtype, dev)
-    rc = lib().kvs_paged_attention(qp, qs, cache._addr, batch._addr, op, os_, H,
-                                   workspace.data_ptr(), workspace.nbytes,
-                                   _status_ptr(d_status), _call_stream(stream, dev))
+    shape = (batch.num_rows, H, cache.head_dim)
+    qp, qs = _rows(q, "q", shape, dt, dev)
+    op, os_ = _rows(out, "out", shape, dt, dev)
+    rc = cache._call[0](qp, qs, cache._addr, batch._addr, op, os_, H, workspace.data_ptr(),
+                        workspace.nbytes, 0 if d_status is None else _status_ptr(d_status),
+                        _get_stream(dev) if stream is None else _stream(stream))
     if rc != KVS_OK:
         raise KvsError(rc, "kvs_paged_attention")
     return out
 
 
 def _vector(t, name, dtype, n, dev):
-    """Pointer of a contiguous vector of n entries (n None: any), 0 for None."""
-    if t is None:
-        return 0
-    if t.dtype != dtype or t.get_device() != dev or t.dim() != 1 or not t.is_contiguous() or \
+    """Pointer of a contiguous vector of n entries (n None: any)."""
+    if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous() or \
             (n is not None and t.numel() != n):
         raise TypeError(f"{name}: need a contiguous {dtype} vector{'' if n is None else f' of {n}'} "
                         f"on the logits' device, got {tuple(t.shape)} {t.dtype} {t.device}")
     return t.data_ptr()
+
+
+# kvs_logit_rules: eleven pointers, three 32-bit counts, padding
+_pack_rules = struct.Struct("@11Q3i4x").pack
 
 
 def kvs_process_logits(logits, out=None, token_ids=None, history=None, history_offsets=None,
@@ -777,52 +787,62 @@ def kvs_process_logits(logits, out=None, token_ids=None, history=None, history_o
     be strided) into out (logits itself is fine; None: only the tokens), and the greedy token of
     the result into token_ids (int32 [M], made when None).  Returns token_ids."""
     dt = _DTYPES.get(logits.dtype)
-    if dt is None or not logits.is_cuda or logits.dim() != 2 or \
-            (logits.shape[1] > 1 and logits.stride(1) != 1):
-        raise TypeError("logits: need a CUDA matrix [M, V] of float32, float16 or bfloat16 with "
-                        "contiguous rows")
-    dev = _call_device(logits, "kvs_process_logits")
-    M, V = logits.shape
-    ls = logits.stride(0) if M > 1 else V
-    op, os_ = 0, 0
+    if dt is None or not logits.is_cuda or logits.dim() != 2:
+        raise TypeError("logits: need a CUDA matrix [M, V] of float32, float16 or bfloat16")
+    dev = logits.get_device()
+    _call_device(dev, "kvs_process_logits")
+    shape = logits.shape
+    M, V = shape
+    ls = V if logits.is_contiguous() else _row_stride(logits, "logits")
+    op = os_ = 0
     if out is not None:
-        if out.dtype != logits.dtype or out.shape != logits.shape or out.get_device() != dev or \
-                (V > 1 and out.stride(1) != 1):
+        if out.dtype is not logits.dtype or out.shape != shape or out.get_device() != dev:
             raise TypeError("out: need a matrix like logits")
-        op, os_ = out.data_ptr(), out.stride(0) if M > 1 else V
+        op, os_ = out.data_ptr(), V if out.is_contiguous() else _row_stride(out, "out")
     if token_ids is None:
         token_ids = torch.empty(M, dtype=torch.int32, device=logits.device)
-    if (history is None) != (history_offsets is None):
-        raise ValueError("kvs_process_logits: history and history_offsets come together")
-    if len({bias_ids is None, bias_values is None, bias_offsets is None}) > 1:
-        raise ValueError("kvs_process_logits: bias_ids, bias_values and bias_offsets come together")
-    nh = nb = nm = 0
     i32, f32 = torch.int32, torch.float32
-    if history is not None:
-        nh = history.numel()
-    if bias_ids is not None:
-        nb = bias_ids.numel()
-    mp = 0
+    h = ho = pl = rp = pr = fr = bi = bv = bo = mp = mr = nh = nb = nm = 0
+    if history is not None and history_offsets is not None:
+        h, nh = _vector(history, "history", i32, None, dev), history.numel()
+        ho = _vector(history_offsets, "history_offsets", i32, M + 1, dev)
+    elif history is not None or history_offsets is not None:
+        raise ValueError("kvs_process_logits: history and history_offsets come together")
+    if prompt_lens is not None:
+        pl = _vector(prompt_lens, "prompt_lens", i32, M, dev)
+    if repetition is not None:
+        rp = _vector(repetition, "repetition", f32, M, dev)
+    if presence is not None:
+        pr = _vector(presence, "presence", f32, M, dev)
+    if frequency is not None:
+        fr = _vector(frequency, "frequency", f32, M, dev)
+    if bias_ids is not None and bias_values is not None and bias_offsets is not None:
+        bi, nb = _vector(bias_ids, "bias_ids", i32, None, dev), bias_ids.numel()
+        bv = _vector(bias_values, "bias_values", f32, nb, dev)
+        bo = _vector(bias_offsets, "bias_offsets", i32, M + 1, dev)
+    elif not (bias_ids is None and bias_values is None and bias_offsets is None):
+        raise ValueError("kvs_process_logits: bias_ids, bias_values and bias_offsets come together")
     if mask is not None:
-        if mask.dtype != i32 or mask.get_device() != dev or mask.dim() != 2 or \
+        if mask.dtype is not i32 or mask.get_device() != dev or mask.dim() != 2 or \
                 mask.shape[1] != (V + 31) // 32 or not mask.is_contiguous():
             raise TypeError("mask: need a contiguous int32 matrix [masks, ceil(V / 32)] on the "
                             "logits' device")
         mp, nm = mask.data_ptr(), mask.shape[0]
-    rules = _LogitRulesStruct(
-        _vector(history, "history", i32, None, dev),
-        _vector(history_offsets, "history_offsets", i32, M + 1, dev),
-        _vector(prompt_lens, "prompt_lens", i32, M, dev),
-        _vector(repetition, "repetition", f32, M, dev),
-        _vector(presence, "presence", f32, M, dev),
-        _vector(frequency, "frequency", f32, M, dev),
-        _vector(bias_ids, "bias_ids", i32, None, dev),
-        _vector(bias_values, "bias_values", f32, nb, dev),
-        _vector(bias_offsets, "bias_offsets", i32, M + 1, dev), mp,
-        _vector(mask_rows, "mask_rows", i32, M, dev), nh, nb, nm)
-    rc = lib().kvs_process_logits(logits.data_ptr(), ls, op, os_, dt, M, V,
-                                  ctypes.addressof(rules), _vector(token_ids, "token_ids", i32, M, dev),
-                                  _status_ptr(d_status), _call_stream(stream, dev))
+    if mask_rows is not None:
+        mr = _vector(mask_rows, "mask_rows", i32, M, dev)
+    rules = _pack_rules(h, ho, pl, rp, pr, fr, bi, bv, bo, mp, mr, nh, nb, nm)
+    rc = lib().kvs_process_logits(logits.data_ptr(), ls, op, os_, dt, M, V, rules,
+                                  _vector(token_ids, "token_ids", i32, M, dev),
+                                  0 if d_status is None else _status_ptr(d_status),
+                                  _get_stream(dev) if stream is None else _stream(stream))
     if rc != KVS_OK:
         raise KvsError(rc, "kvs_process_logits")
     return token_ids
+
+
+def _row_stride(t: torch.Tensor, name: str) -> int:
+    """Row stride of a matrix whose rows are contiguous."""
+    s0, s1 = t.stride()
+    if s1 != 1 and t.shape[1] > 1:
+        raise TypeError(f"{name}: the rows must be contiguous, got strides {t.stride()}")
+    return s0 if t.shape[0] > 1 else t.shape[1]
