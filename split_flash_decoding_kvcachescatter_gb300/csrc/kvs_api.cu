@@ -614,6 +614,7 @@ int kvs_set_wait_limit_ns(uint64_t ns, uint64_t *previous) {
   if (rc == KVS_OK) rc = kvs::set_wait_limit_cluster(ns);
   if (rc == KVS_OK) rc = kvs::set_wait_limit_prefill(ns);
   if (rc == KVS_OK) rc = kvs::set_wait_limit_paged(ns);
+  if (rc == KVS_OK) rc = kvs::set_wait_limit_decode(ns);
   if (rc == KVS_OK) rc = kvs::set_wait_limit_chunk(ns);
   if (rc != KVS_OK) return rc;
   if (previous) *previous = g_limit[dev].load();

@@ -176,6 +176,12 @@ int launch_paged_attention(const void *q, long long q_stride, const kvs_paged_ca
                            const PagedArgs &b, void *out, long long out_stride, int H,
                            void *workspace, int *d_status, cudaStream_t stream);
 
+// The variant for decode steps (max_new * G <= 16).
+size_t paged_decode_workspace_bytes(int D);
+int launch_paged_decode(const void *q, long long q_stride, const kvs_paged_cache &cache,
+                        const PagedArgs &b, void *out, long long out_stride, int H,
+                        void *workspace, int *d_status, cudaStream_t stream);
+
 // The tensor-core variant for chunks (float16 and bfloat16 pages).
 size_t paged_chunk_workspace_bytes(int D);
 int launch_paged_chunk(const void *q, long long q_stride, const kvs_paged_cache &cache,
@@ -209,6 +215,7 @@ int set_wait_limit_step(uint64_t ns);
 int set_wait_limit_cluster(uint64_t ns);
 int set_wait_limit_prefill(uint64_t ns);
 int set_wait_limit_paged(uint64_t ns);
+int set_wait_limit_decode(uint64_t ns);
 int set_wait_limit_chunk(uint64_t ns);
 
 }  // namespace kvs

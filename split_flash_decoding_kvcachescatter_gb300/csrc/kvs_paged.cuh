@@ -117,34 +117,53 @@ struct Unit {
   long long base;
 };
 
-struct PagedPlan {
-  long long R;   // cost rows in all
-  long long P;   // columns in use
-  Unit first;    // the unit that holds this block's first cost row
+// a / b for a >= 0, b > 0: a 32-bit division when both fit (the 64-bit one
+// is a long instruction sequence, on the path to a block's first copy).
+__device__ __forceinline__ long long div_nn(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return (long long)((unsigned)a / (unsigned)b);
+  return a / b;
+}
+
+// How a line of R cost rows is cut: [0, S) into NS equal ranges, the rest
+// into ND equal ones; ranges are numbered through.
+struct Cuts {
+  long long R, S;
+  int NS, ND;
+  __device__ long long start(int r) const {
+    return r <= NS ? div_nn(S * r, NS) : S + div_nn((R - S) * (r - NS), ND);
+  }
+  // The range that holds cost row x: the last one that starts at or before it.
+  __device__ int at(long long x) const {
+    if (x < S || ND == 0) {
+      const long long c = div_nn(x * NS + NS - 1, S);
+      return (int)(c < NS - 1 ? c : NS - 1);
+    }
+    const long long c = div_nn((x - S) * ND + ND - 1, R - S);
+    return NS + (int)(c < ND - 1 ? c : ND - 1);
+  }
 };
 
-__device__ __forceinline__ long long column_start(long long R, long long P, long long b) {
-  return R * b / P;
-}
-// Column holding cost row x: the largest b with R * b / P <= x.
-__device__ __forceinline__ int column_at(long long x, long long R, long long P) {
-  const long long c = (x * P + P - 1) / R;
-  return (int)(c < P - 1 ? c : P - 1);
-}
-
-// Warp-cooperative; every lane returns the plan.
-static __device__ PagedPlan warp_plan(const PagedArgs &a, const Line &ln, int blocks, int b, int lane) {
-  PagedPlan pl{0, 1, {a.M, 0, 0, 0}};
+// The cost rows of the whole line (warp-cooperative; every lane returns it).
+static __device__ long long warp_line_total(const PagedArgs &a, const Line &ln, int lane) {
   long long sum = 0;
   for (int i = lane; i < a.M; i += 32) sum += SeqCost(paged_seq(a, i), ln).head_total();
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  pl.R = sum * ln.Hkv;
-  if (pl.R == 0) return pl;
-  // short lines use fewer columns, so that one holds work worth a block
-  pl.P = max(1ll, min((long long)blocks, pl.R / ln.min_column));
-  if (b >= pl.P) return pl;
-  const long long x0 = column_start(pl.R, pl.P, b);
+  return sum * ln.Hkv;
+}
+
+// The line in at most `blocks` equal ranges, fewer when short, so that one
+// holds work worth a block.
+__device__ __forceinline__ Cuts equal_cuts(long long R, const Line &ln, int blocks) {
+  Cuts c{R, R, 1, 0};
+  if (R > 0) c.NS = (int)max(1ll, min((long long)blocks, div_nn(R, ln.min_column)));
+  return c;
+}
+
+// The unit that holds cost row x of the line, x < R (warp-cooperative; every
+// lane returns it).
+static __device__ Unit warp_unit_at(const PagedArgs &a, const Line &ln, long long x, int lane) {
+  Unit u{a.M, 0, 0, 0};
   long long base = 0;
   for (int i0 = 0; i0 < a.M; i0 += 32) {
     const int i = i0 + lane;
@@ -156,14 +175,14 @@ static __device__ PagedPlan warp_plan(const PagedArgs &a, const Line &ln, int bl
       const long long v = __shfl_up_sync(0xffffffffu, inc, o);
       if (lane >= o) inc += v;
     }
-    const bool hit = mine > 0 && x0 >= base + inc - mine && x0 < base + inc;
+    const bool hit = mine > 0 && x >= base + inc - mine && x < base + inc;
     const unsigned ballot = __ballot_sync(0xffffffffu, hit);
     if (ballot) {
       const int src = __ffs(ballot) - 1;
       const long long sb = __shfl_sync(0xffffffffu, base + inc - mine, src);
-      pl.first.i = i0 + src;
-      const SeqCost c(paged_seq(a, pl.first.i), ln);
-      const long long off = x0 - sb;
+      u.i = i0 + src;
+      const SeqCost c(paged_seq(a, u.i), ln);
+      const long long off = x - sb;
       int lo = 0, hi = c.Rn - 1;  // the last row tile that starts at or before off
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
@@ -172,14 +191,14 @@ static __device__ PagedPlan warp_plan(const PagedArgs &a, const Line &ln, int bl
       }
       const long long tile_base = c.before(lo) * ln.Hkv;
       const long long span = c.keys(lo) + ln.fix;
-      pl.first.rt = lo;
-      pl.first.g = (int)((off - tile_base) / span);
-      pl.first.base = sb + tile_base + pl.first.g * span;
-      return pl;
+      u.rt = lo;
+      u.g = (int)div_nn(off - tile_base, span);
+      u.base = sb + tile_base + u.g * span;
+      return u;
     }
     base += __shfl_sync(0xffffffffu, inc, 31);
   }
-  return pl;
+  return u;
 }
 
 // Everything a warp needs to know about a unit.
@@ -228,12 +247,12 @@ __device__ __forceinline__ bool next_unit(const PagedArgs &a, Unit &u, const Uni
 }
 
 // Four accumulator columns of one row, merged over a unit's pieces in column
-// order: block b1's piece began the unit (its slot 2 b1 + 1), those of blocks
+// order: range b1's piece began the unit (its slot 2 b1 + 1), those of ranges
 // b1 + 1 .. b2 continue it (slots 2 b).  A slot of `stride` floats has the
 // row's (m, l) at float2 `r` and its accumulators at float `at`.  Pieces are
 // taken eight at a time, all loads of a batch before the first is used, so a
 // batch costs one L2 round trip.
-static __device__ __noinline__ void merge_pieces(const float *slots, size_t stride, int at,
+static __device__ __forceinline__ void merge_pieces(const float *slots, size_t stride, int at,
                                                     int r, int b1, int b2, float4 &acc, float &l) {
   constexpr int kBatch = 8;
   acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -270,6 +289,53 @@ static __device__ __noinline__ void merge_pieces(const float *slots, size_t stri
       }
     }
     m = mn;
+  }
+}
+
+// merge_pieces for NR rows at once (rows r0 + k * step < rows), PB pieces at a
+// time: NR * PB accumulator loads in flight a thread.  Accumulators of row r
+// are at float at + r D + d of a slot.
+template <int NR, int PB>
+__device__ __forceinline__ void merge_rows(const float *slots, size_t stride, int at, int D, int d,
+                                           int r0, int step, int rows, int b1, int b2,
+                                           float4 (&acc)[NR], float (&l)[NR]) {
+  float m[NR];
+#pragma unroll
+  for (int k = 0; k < NR; ++k) {
+    acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    l[k] = 0.f;
+    m[k] = neg_inf_f();
+  }
+  for (int c = b1; c <= b2; c += PB) {
+    float2 ml[NR][PB];
+    float4 v[NR][PB];
+#pragma unroll
+    for (int j = 0; j < PB; ++j) {
+      // (past the last piece: its loads again, not used)
+      const float *ps = slots + (2 * (size_t)min(c + j, b2) + (min(c + j, b2) == b1 ? 1 : 0)) * stride;
+#pragma unroll
+      for (int k = 0; k < NR; ++k) {
+        const int r = min(r0 + k * step, rows - 1);
+        ml[k][j] = __ldcg(reinterpret_cast<const float2 *>(ps) + r);
+        v[k][j] = __ldcg(reinterpret_cast<const float4 *>(ps + at + (size_t)r * D + d));
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < PB; ++j) {
+      if (c + j > b2) break;
+#pragma unroll
+      for (int k = 0; k < NR; ++k) {
+        const float mn = fmaxf(m[k], ml[k][j].x);
+        const float mz = mn == neg_inf_f() ? 0.f : mn;
+        const float wa = exp2f(m[k] - mz), wb = exp2f(ml[k][j].x - mz);
+        acc[k].x = acc[k].x * wa + v[k][j].x * wb;
+        acc[k].y = acc[k].y * wa + v[k][j].y * wb;
+        acc[k].z = acc[k].z * wa + v[k][j].z * wb;
+        acc[k].w = acc[k].w * wa + v[k][j].w * wb;
+        l[k] = l[k] * wa + ml[k][j].y * wb;  // (a NaN sum stays one also under a zero weight)
+        m[k] = mn;
+      }
+    }
   }
 }
 

@@ -130,52 +130,6 @@ __device__ __forceinline__ void tma_q(void *dst, const CUtensorMap *map, int hea
       : "memory");
 }
 
-// merge_pieces for NR rows at once (rows r0 + k * step < rows), pieces two at
-// a time: 2 NR loads in flight a thread.  Accumulators of row r at float
-// at + r D + d of a slot.
-template <int NR>
-__device__ __forceinline__ void merge_rows(const float *slots, size_t stride, int at, int D, int d,
-                                           int r0, int step, int rows, int b1, int b2,
-                                           float4 (&acc)[NR], float (&l)[NR]) {
-  float m[NR];
-#pragma unroll
-  for (int k = 0; k < NR; ++k) {
-    acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-    l[k] = 0.f;
-    m[k] = neg_inf_f();
-  }
-  for (int c = b1; c <= b2; c += 2) {
-    float2 ml[NR][2];
-    float4 v[NR][2];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const float *ps = slots + (2 * (size_t)min(c + j, b2) + (c + j == b1 ? 1 : 0)) * stride;
-#pragma unroll
-      for (int k = 0; k < NR; ++k) {
-        const int r = min(r0 + k * step, rows - 1);
-        ml[k][j] = __ldcg(reinterpret_cast<const float2 *>(ps) + r);
-        v[k][j] = __ldcg(reinterpret_cast<const float4 *>(ps + at + (size_t)r * D + d));
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      if (c + j > b2) break;
-#pragma unroll
-      for (int k = 0; k < NR; ++k) {
-        const float mn = fmaxf(m[k], ml[k][j].x);
-        const float mz = mn == neg_inf_f() ? 0.f : mn;
-        const float wa = ex2(m[k] - mz), wb = ex2(ml[k][j].x - mz);
-        acc[k].x = acc[k].x * wa + v[k][j].x * wb;
-        acc[k].y = acc[k].y * wa + v[k][j].y * wb;
-        acc[k].z = acc[k].z * wa + v[k][j].z * wb;
-        acc[k].w = acc[k].w * wa + v[k][j].w * wb;
-        l[k] = l[k] * wa + ml[k][j].y * wb;
-        m[k] = mn;
-      }
-    }
-  }
-}
-
 // The two tiles of a unit: tokens, key tiles that each attends, and those of
 // this block's column.
 struct CTile {
@@ -253,11 +207,12 @@ __global__ void __launch_bounds__(kCThreads, 1)
   tc_fence_after();
   allow_dependent_launch();
   const uint32_t tmem = *tmem_slot;
-  const PagedPlan pl = warp_plan(pa, ln, gridDim.x, b, lane);
-  const bool work = pl.R > 0 && b < pl.P;
-  const long long x0 = work ? column_start(pl.R, pl.P, b) : 0;
-  const long long x1 = work ? column_start(pl.R, pl.P, b + 1) : 0;
-  Unit u = pl.first;
+  const Cuts cut = equal_cuts(warp_line_total(pa, ln, lane), ln, gridDim.x);
+  const bool work = cut.R > 0 && b < cut.NS;
+  const long long x0 = work ? cut.start(b) : 0;
+  const long long x1 = work ? cut.start(b + 1) : 0;
+  Unit u{pa.M, 0, 0, 0};
+  if (work) u = warp_unit_at(pa, ln, x0, lane);
   bool more = work;
   auto tile_of = [&](const UnitInfo &f, int x) {
     CTile t;
@@ -650,8 +605,8 @@ __global__ void __launch_bounds__(kCThreads, 1)
               break;
             }
             // the blocks of tile x's first and last key tile
-            const int b1 = column_at(f.k0, pl.R, pl.P);
-            const int b2 = column_at(f.k0 + (long long)(tl.nt - 1) * kCN, pl.R, pl.P);
+            const int b1 = cut.at(f.k0);
+            const int b2 = cut.at(f.k0 + (long long)(tl.nt - 1) * kCN);
             if (t == 0) {
               const unsigned add = (unsigned)(tl.hi - tl.lo);
               unsigned long long *ctr = counters + 2 * b1 + x;
@@ -673,7 +628,7 @@ __global__ void __launch_bounds__(kCThreads, 1)
               for (int r0 = t / (D / 4); r0 < rows; r0 += kRowsAhead * kStep) {
                 float4 acc[kRowsAhead];
                 float ls[kRowsAhead];
-                merge_rows<kRowsAhead>(base, 2 * paged_slot_floats(kCM, D), 2 * kCM, D, d, r0, kStep,
+                merge_rows<kRowsAhead, 2>(base, 2 * paged_slot_floats(kCM, D), 2 * kCM, D, d, r0, kStep,
                                        rows, b1, b2, acc, ls);
 #pragma unroll
                 for (int k = 0; k < kRowsAhead; ++k) {

@@ -1,0 +1,400 @@
+// paged_decode.cu -- attention of single tokens (and of the few tokens whose
+// rows with all G query heads are 16 at most) over a paged KV cache.
+//
+// Bound: HBM, which has to deliver every live K and V row once.  Mathematics,
+// units and ranges as in paged_attention.cu, one equal range a block.
+//
+// Block: 4 consumer warps of the same 16 rows (the keys are split over the
+// warps, each with a ring of stages: K and V of one tile) and 4 producer
+// warps, one a ring (tensor-map copies of 16 rows, each looked up in the page
+// table).  Producers run ahead over the ends of units, so the copies go on
+// while the consumers join a unit's four states in shared memory and write
+// the output or a partial.
+//
+// Products run on mma.sync (16 rows: an M = 128 tcgen05 tile would be seven
+// eighths padding): m16n8k16 for the 16-bit types, float32 as three TF32
+// products.  A 32-key tile of a decode step costs a warp about 900 cycles for
+// 16 KB where HBM delivers 23 bytes a cycle an SM, so four warps keep ahead.
+//
+// Measured (GB300, copy peak 6.79 TB/s): 8 x 32768 keys, H 32 / 8, D 128,
+// float16 (1.07 GB) 167 us, 95 % of the peak; 32 sequences of up to 8192 keys
+// in bfloat16 (586 MB) 108 us, 80 %.  Tried: one producer warp for all four
+// rings 190 us (it needs about 1000 cycles a tile), two producers of two
+// rings 234 us (rings wait for each other); a warp of its own for the joining
+// 171 and 107 us; with it the last fifth of the line in short ranges handed
+// out by a counter, 180 and 114 us (blocks then finish within 10 % of each
+// other, not 26 %, but a long unit's 24 pieces are slow to join).
+
+#include <algorithm>
+#include <cmath>
+#include <mutex>
+#include <type_traits>
+
+#include "kvs_paged.cuh"
+#include "kvs_rows_mma.cuh"
+#include "kvs_tags.cuh"
+#include "kvs_tma.cuh"
+
+namespace kvs {
+
+namespace {
+
+constexpr int kDW = 4;     // rings: consumer and producer warps
+constexpr int kDRows = 16; // rows of a unit
+constexpr int kDThreads = 2 * kDW * 32;
+constexpr int kDFix = 64;  // cost rows that stand for a unit's fixed price
+constexpr int kDMaxDevices = 64;
+
+template <typename T, int D_>
+struct DGeo {
+  static constexpr int D = D_;
+  static constexpr bool F32 = std::is_same<T, float>::value;
+  static constexpr int KT = WarpRows<T, D>::KT;        // keys of a tile
+  static constexpr int GB = 16 * D * (int)sizeof(T);   // bytes of a 16-row copy
+  static constexpr int BLK = 2048;                     // one of its column blocks
+  static constexpr int TILE = KT / 16 * GB;            // K (or V) of a stage
+  static constexpr int STAGE = 2 * TILE;
+  static constexpr int STATE = kDW * 16 * (D + 4) * 4;  // the consumers' accumulators
+  static constexpr int BUDGET = 227 * 1024 - 2048 - STATE;
+  static constexpr int S0 = BUDGET / (kDW * STAGE);
+  static constexpr int S = S0 > 8 ? 8 : S0;            // stages of a ring
+  static constexpr int OFF_STATE = kDW * S * STAGE;
+  static constexpr int OFF_ML = OFF_STATE + STATE;     // float2 [kDW][16]
+  static constexpr int OFF_BAR = OFF_ML + kDW * 16 * 8;
+  static constexpr int OFF_BAD = OFF_BAR + (2 * kDW * S + 1) * 8;  // int [kDW][S]
+  static constexpr int OFF_MISC = OFF_BAD + kDW * S * 4;           // abort, last
+  static constexpr int SMEM = OFF_MISC + 8;
+  static_assert(S >= 2, "two stages at least");
+  static_assert(SMEM <= 227 * 1024, "one block per SM must fit");
+};
+
+// ---- the kernel ---------------------------------------------------------------
+template <typename T, int D, bool kPoll>
+__global__ void __launch_bounds__(kDThreads, 1)
+    paged_decode_kernel(const T *__restrict__ q, long long q_stride, T *__restrict__ out,
+                        long long out_stride, PagedArgs pa,
+                        const __grid_constant__ CUtensorMap kmap,
+                        const __grid_constant__ CUtensorMap vmap, int G, int Hkv, float sl2,
+                        int min_column, unsigned char *ws, unsigned host_tag, int *d_status) {
+  using C = DGeo<T, D>;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);  // [kDW][S]
+  uint64_t *empty = full + kDW * C::S;
+  uint64_t *cbar = empty + kDW * C::S;  // all consumer warps
+  int *bad = reinterpret_cast<int *>(smem + C::OFF_BAD);
+  volatile int *abort = reinterpret_cast<volatile int *>(smem + C::OFF_MISC);
+  volatile int *s_last = abort + 1;
+  unsigned *epoch = reinterpret_cast<unsigned *>(ws);
+  unsigned long long *counters = reinterpret_cast<unsigned long long *>(ws + 256);
+  float *slots = reinterpret_cast<float *>(ws + 256 + (size_t)kPagedMaxBlocks * 8);
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int b = blockIdx.x;
+  const Line ln{Hkv, kDRows / G, kDFix, C::KT, min_column};
+  if (threadIdx.x == 0) {
+    prefetch_map(&kmap);
+    prefetch_map(&vmap);
+    for (int s = 0; s < kDW * C::S; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(cbar, kDW);
+    *abort = 0;
+    *s_last = 0;
+    fence_mbar_init();
+  }
+  grid_dependency_wait();
+  // bad sequences: status, and NaN rows where the rows are known
+  for (int i = b; i < pa.M; i += gridDim.x) {
+    const PagedSeq s = paged_seq(pa, i);
+    if (s.err != KVS_OK) {
+      if (threadIdx.x == 0) record_status(d_status, s.err);
+      const T nan = from_f32<T>(__int_as_float(0x7fc00000));
+      for (int r = 0; r < s.n; ++r)
+        for (int e = threadIdx.x; e < Hkv * G * D; e += kDThreads)
+          out[(long long)(s.row0 + r) * out_stride + e] = nan;
+    }
+  }
+  const unsigned tag = launch_tag(host_tag, __ldcg(epoch));
+  __syncthreads();
+  allow_dependent_launch();
+  const Cuts cut = equal_cuts(warp_line_total(pa, ln, lane), ln, gridDim.x);
+  if (cut.R == 0 || b >= cut.NS) return;
+  const long long x0 = cut.start(b), x1 = cut.start(b + 1);
+  Unit u = warp_unit_at(pa, ln, x0, lane);
+
+  if (warp >= kDW) {
+    // ======================= producer of a ring ==============================
+    const uint64_t policy = policy_evict_first();  // a row is read once
+    const int ring = warp - kDW;
+    uint32_t n = 0;  // tiles put in the ring
+    bool ok = true;
+    constexpr int NP = C::KT / 16;  // 16-row pieces of a tile
+    constexpr int AHEAD = 32 / NP;  // tiles whose pages one look-up finds
+    const int piece = lane % NP;    // lanes 0..NP-1: K pieces, NP..2NP-1: V pieces
+    do {
+      const UnitInfo f = unit_info(pa, u, ln, x0, x1);
+      const int32_t *table = pa.page_table + (size_t)u.i * pa.max_pages;
+      int page = 0, k = 0;  // lane: the page of piece `piece` of the ring's tile k + lane / NP
+      for (int t = f.t_lo + ring; t < f.t_hi; t += kDW, ++n, ++k) {
+        if (k % AHEAD == 0) {
+          const long long r0 = (long long)(t + kDW * (lane / NP)) * C::KT + 16 * piece;
+          page = r0 < f.keys ? __ldca(table + (r0 >> pa.page_shift)) : 0;
+        }
+        const int pg = __shfl_sync(0xffffffffu, page, (k % AHEAD) * NP + piece);
+        const int npieces = min(NP, (f.keys - t * C::KT + 15) / 16);
+        const bool mine = lane < 2 * NP && piece < npieces;
+        const bool wrong = mine && (unsigned)pg >= (unsigned)pa.num_pages;
+        const unsigned any_bad = __ballot_sync(0xffffffffu, wrong);
+        const int st = ring * C::S + (int)(n % C::S);
+        if (!__all_sync(0xffffffffu, mbar_wait<kPoll>(&empty[st], ((n / C::S) & 1u) ^ 1u, abort))) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) {
+          bad[st] = any_bad != 0u;
+          if (any_bad) record_status(d_status, KVS_ERR_PAGE);
+          mbar_arrive_expect_tx(&full[st], 2u * (uint32_t)npieces * C::GB);
+        }
+        __syncwarp();
+        if (mine) {
+          const int r0 = t * C::KT + 16 * piece;
+          const int row = ((wrong ? 0 : pg) * Hkv + u.g) * (1 << pa.page_shift) +
+                          (r0 & ((1 << pa.page_shift) - 1));
+          unsigned char *dst = smem + st * C::STAGE + (lane >= NP ? C::TILE : 0) + piece * C::GB;
+          tma_rows(dst, lane >= NP ? &vmap : &kmap, row, &full[st], policy);
+        }
+      }
+      if (!ok) break;
+      if (!next_unit(pa, u, f, ln)) break;
+    } while (u.base < x1);
+    if (lane == 0) {
+      if (!ok) give_up(abort, d_status, epoch);
+      // every copy lands before the block exits
+      for (uint32_t j = n > (uint32_t)C::S ? n - C::S : 0u; j < n; ++j)
+        mbar_wait_drain(&full[ring * C::S + j % C::S], (j / C::S) & 1u);
+    }
+    return;
+  }
+
+  // ========================= consumers ======================================
+  uint32_t n = 0, cphase = 0;
+  auto consumers_barrier = [&]() -> bool {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(cbar);
+    bool got = mbar_wait<kPoll>(cbar, cphase, abort);
+    got = __all_sync(0xffffffffu, got);
+    if (!got) {
+      if (lane == 0) give_up(abort, d_status, epoch);
+      return false;
+    }
+    cphase ^= 1u;
+    return true;
+  };
+  const float nan = __int_as_float(0x7fc00000);
+  WarpRows<T, D> w;
+  do {
+    const UnitInfo f = unit_info(pa, u, ln, x0, x1);
+    if (f.t_lo < f.t_hi) {
+      const int rows = f.ntok * G;
+      w.start(q, q_stride, 0, rows, G, f, u.g);
+      // keys that this lane's two rows attend
+      int reach[2];
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh)
+        reach[hh] = f.s.p + f.tok0 + min(lane / 4 + 8 * hh, rows - 1) / G + 1;
+      bool poison = false;
+      for (int t = f.t_lo + warp; t < f.t_hi; t += kDW, ++n) {
+        const int st = warp * C::S + (int)(n % C::S);
+        if (!__all_sync(0xffffffffu, mbar_wait<kPoll>(&full[st], (n / C::S) & 1u, abort))) {
+          if (lane == 0) give_up(abort, d_status, epoch);
+          return;
+        }
+        poison |= bad[st] != 0;
+        unsigned char *sk = smem + st * C::STAGE;
+        const int left = f.keys - t * C::KT;  // keys of the tile that exist
+        if (left < C::KT) {
+          // rows past the last key hold anything: V's become zero (their
+          // weights are zero, but 0 x NaN is not)
+          for (int e = lane; e < (C::KT - left) * (D * (int)sizeof(T) / 16); e += 32) {
+            const int row = left + e % (C::KT - left), pc = e / (C::KT - left);
+            *reinterpret_cast<uint4 *>(sk + C::TILE + (row >> 4) * C::GB + (pc >> 3) * C::BLK +
+                                       (row & 15) * 128 + (pc & 7) * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_shared();
+          __syncwarp();
+        }
+        const int lim[2] = {reach[0] - t * C::KT, reach[1] - t * C::KT};
+        w.tile(smem_addr(sk), smem_addr(sk + C::TILE), sl2, lim);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[st]);
+      }
+      w.finish();
+      if (poison) w.l[0] = w.l[1] = nan;
+      const bool whole = f.t_hi - f.t_lo == f.nt;
+      const size_t slot = 2 * (size_t)b + (f.t_lo == 0 ? 1 : 0);
+      float *sl = slots + slot * paged_slot_floats(kDRows, D);
+      float *sacc = sl + 2 * kDRows;
+      T *orow = out + (long long)(f.s.row0 + f.tok0) * out_stride + (long long)u.g * G * D;
+      // the key groups' states merge in shared memory
+      float *macc = reinterpret_cast<float *>(smem + C::OFF_STATE);  // [kDW][16][D + 4]
+      float2 *mml = reinterpret_cast<float2 *>(smem + C::OFF_ML);    // [kDW][16]
+      float *mine = macc + warp * 16 * (D + 4);
+      w.each([&](int hh, int d, const float(&v)[4]) {
+        float *p = mine + (lane / 4 + 8 * hh) * (D + 4) + d;
+        if constexpr (C::F32)
+          *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+        else
+          *reinterpret_cast<float2 *>(p) = make_float2(v[0], v[1]);
+      });
+      if ((lane & 3) == 0) {
+        mml[warp * 16 + lane / 4] = make_float2(w.m[0], w.l[0]);
+        mml[warp * 16 + lane / 4 + 8] = make_float2(w.m[1], w.l[1]);
+      }
+      if (!consumers_barrier()) return;
+      for (int e = threadIdx.x; e < rows * (D / 4); e += kDW * 32) {
+        const int r = e / (D / 4), d = (e - r * (D / 4)) * 4;
+        float mx = neg_inf_f();
+#pragma unroll
+        for (int k = 0; k < kDW; ++k) mx = fmaxf(mx, mml[k * 16 + r].x);
+        const float mz = mx == neg_inf_f() ? 0.f : mx;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        float ls = 0.f;
+#pragma unroll
+        for (int k = 0; k < kDW; ++k) {
+          const float2 ml = mml[k * 16 + r];
+          const float wgt = ex2f(ml.x - mz);
+          const float4 v = *reinterpret_cast<const float4 *>(macc + (k * 16 + r) * (D + 4) + d);
+          acc.x = fmaf(wgt, v.x, acc.x);
+          acc.y = fmaf(wgt, v.y, acc.y);
+          acc.z = fmaf(wgt, v.z, acc.z);
+          acc.w = fmaf(wgt, v.w, acc.w);
+          // (a NaN sum stays one also under a zero weight)
+          ls = fmaf(wgt, ml.y, ls);
+        }
+        if (whole) {
+          const float inv = 1.f / ls;
+          const int tok = r / G;
+          store4<T>(orow + (long long)tok * out_stride + (r - tok * G) * D + d,
+                    make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+        } else {
+          __stcg(reinterpret_cast<float4 *>(sacc + (size_t)r * D + d), acc);
+          if (d == 0) __stcg(reinterpret_cast<float2 *>(sl) + r, make_float2(mx, ls));
+        }
+      }
+      if (!whole) __threadfence();  // the partial is visible GPU-wide before it counts
+      if (!consumers_barrier()) return;  // (also: the states may be written again)
+      if (!whole) {
+        // the blocks of the unit's first and last tile; every block between has some
+        const int b1 = cut.at(f.k0);
+        const int b2 = cut.at(f.k0 + (long long)(f.nt - 1) * C::KT);
+        if (threadIdx.x == 0) {
+          const unsigned add = (unsigned)(f.t_hi - f.t_lo);
+          const unsigned before = tagged_add(counters + b1, add, tag, d_status, epoch);
+          const bool last = before != 0xffffffffu && before + add == (unsigned)f.nt;
+          if (last) counters[b1] = 0ull;  // a replayed graph uses the same tag again
+          *s_last = last;
+        }
+        if (!consumers_barrier()) return;
+        if (*s_last) {
+          __threadfence();
+          for (int e = threadIdx.x; e < rows * (D / 4); e += kDW * 32) {
+            const int r = e / (D / 4), d = (e - r * (D / 4)) * 4;
+            float4 acc;
+            float ls;
+            merge_pieces(slots, paged_slot_floats(kDRows, D), 2 * kDRows + r * D + d, r, b1, b2, acc, ls);
+            const float inv = 1.f / ls;
+            const int tok = r / G;
+            store4<T>(orow + (long long)tok * out_stride + (r - tok * G) * D + d,
+                      make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+          }
+        }
+      }
+    }
+    if (!next_unit(pa, u, f, ln)) break;
+  } while (u.base < x1);
+}
+
+template <typename T, int D>
+int launch_decode(const void *q, long long q_stride, const kvs_paged_cache &cache,
+                  const PagedArgs &pa, void *out, long long out_stride, int H, void *workspace,
+                  int *d_status, cudaStream_t stream) {
+  using C = DGeo<T, D>;
+  static bool configured[kDMaxDevices] = {false};
+  static std::mutex mu;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDMaxDevices)
+    return KVS_ERR_LAUNCH;
+  {
+    std::lock_guard<std::mutex> lk(mu);
+    if (!configured[dev]) {
+      for (auto kern : {paged_decode_kernel<T, D, false>,
+                        paged_decode_kernel<T, D, true>}) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) !=
+            cudaSuccess) {
+          cudaGetLastError();
+          return KVS_ERR_LAUNCH;
+        }
+      }
+      configured[dev] = true;
+    }
+  }
+  const int sms = device_sm_count();
+  if (sms <= 0) return KVS_ERR_LAUNCH;
+  CUtensorMap kmap, vmap;
+  const uint64_t rows = (uint64_t)cache.num_pages * cache.num_kv_heads * cache.page_size;
+  int rc = make_row_map(&kmap, cache.k_pages, rows, D, cache.dtype, 16,
+                        D * (int)sizeof(T) / 128);
+  if (rc == KVS_OK) rc = make_row_map(&vmap, cache.v_pages, rows, D, cache.dtype, 16,
+                        D * (int)sizeof(T) / 128);
+  if (rc != KVS_OK) return rc;
+  const int Hkv = cache.num_kv_heads;
+  const int grid = sms < kPagedMaxBlocks ? sms : kPagedMaxBlocks;
+  const float sl2 = (float)(1.4426950408889634074 / std::sqrt((double)D));
+  // the shortest range worth a block: small_model's step (f32, 4 x 1500 keys,
+  // 2 kv heads) took 16.2 us at 48 cost rows, 15.4 at 96, 16.5 at 192, 18.9
+  // at 384
+  const int min_column = 3 * 32;
+  const cudaError_t e = launch_pdl(
+      poll_waits() ? paged_decode_kernel<T, D, true>
+                   : paged_decode_kernel<T, D, false>,
+      dim3(grid), dim3(kDThreads), C::SMEM, stream, static_cast<const T *>(q), q_stride,
+      static_cast<T *>(out), out_stride, pa, kmap, vmap, H / Hkv, Hkv, sl2, min_column,
+      static_cast<unsigned char *>(workspace), fresh_tag(), d_status);
+  return e == cudaSuccess ? KVS_OK : KVS_ERR_LAUNCH;
+}
+
+}  // namespace
+
+int set_wait_limit_decode(uint64_t ns) {
+  if (set_unit_wait_limit(ns) != cudaSuccess) {
+    cudaGetLastError();
+    return KVS_ERR_LAUNCH;
+  }
+  return KVS_OK;
+}
+
+// Workspace: 256 bytes (epoch), a counter per block, then per block two
+// partial slots (0: a unit begun in an earlier range, 1: one begun here and
+// not finished).
+size_t paged_decode_workspace_bytes(int D) {
+  return 256 + (size_t)kPagedMaxBlocks * 8 +
+         2 * (size_t)kPagedMaxBlocks * paged_slot_floats(kDRows, D) * 4;
+}
+
+int launch_paged_decode(const void *q, long long q_stride, const kvs_paged_cache &cache,
+                        const PagedArgs &pa, void *out, long long out_stride, int H,
+                        void *workspace, int *d_status, cudaStream_t stream) {
+#define KVS_DECODE(T)                                                                           \
+  return cache.head_dim == 64                                                                   \
+             ? launch_decode<T, 64>(q, q_stride, cache, pa, out, out_stride, H, workspace,      \
+                                    d_status, stream)                                           \
+             : launch_decode<T, 128>(q, q_stride, cache, pa, out, out_stride, H, workspace,     \
+                                     d_status, stream)
+  if (cache.dtype == KVS_F32) KVS_DECODE(float);
+  if (cache.dtype == KVS_F16) KVS_DECODE(__half);
+  KVS_DECODE(__nv_bfloat16);
+#undef KVS_DECODE
+}
+
+}  // namespace kvs

@@ -57,6 +57,19 @@ def test_long_chunk_over_long_context(dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("n,p", [([1, 1, 1], [20011, 15000, 5003]), ([1], [40000]),
+                                 ([1] * 40, [900 + 7 * i for i in range(40)]),
+                                 ([2, 0, 1], [31000, 5, 12345])])
+def test_decode_over_every_block(dtype, n, p):
+    """Enough keys to give every block of the decode kernel a long range."""
+    b = Paged(n, p, 16, 8, 64, dtype, 64, seed=sum(n) + len(p))
+    first = b.attend()
+    b.check(first)
+    for _ in range(5):
+        assert torch.equal(b.attend(), first)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 def test_large_scores(dtype):
     """Scores of some hundreds: the running maximum moves often and far."""
     b = Paged([1, 90], [600, 500], 8, 2, 128, dtype, 32, seed=4)
@@ -166,7 +179,8 @@ def test_same_bits_every_time(dtype):
 
 
 @pytest.mark.parametrize("n,p,q", [([1, 1, 1], [100, 900, 40], [2000, 3, 777]),
-                                   ([50, 1, 100], [100, 900, 40], [50, 1200, 0])])
+                                   ([50, 1, 100], [100, 900, 40], [50, 1200, 0]),
+                                   ([1, 1, 1], [50000, 9000, 31000], [20, 70000, 20000])])
 def test_graph_follows_positions(n, p, q):
     """A captured call replays on other positions, with a batch's tables rewritten in place."""
     big = [max(a, c) for a, c in zip(p, q)]
