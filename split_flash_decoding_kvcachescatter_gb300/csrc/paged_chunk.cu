@@ -8,22 +8,29 @@
 // K and V tile of 128 keys: per key tile a block reads 64 KB (D = 128) for
 // four products of 128 x 128 x 128, 2048 tensor-core cycles.
 //
-// Block (12 warps, one block an SM):
+// Block (11 warps, one block an SM):
 //   warps 0-3, 4-7  softmax of tile A and of tile B: thread t owns row t,
 //                   which is TMEM lane t
-//   warp 8          issues the products: S_x = Q_x K^T (operands in shared
-//                   memory, K-major), O_x += P_x V (P from TMEM, V as the
-//                   copies leave it: head elements contiguous, which is the
-//                   MN-major operand, so nothing is transposed)
-//   warp 9          copies: Q by tensor maps over (head element, head of the
+//   warp 8          issues S_x = Q_x K^T (operands in shared memory, K-major)
+//   warp 9          issues O_x += P_x V (P from TMEM; V as the copies leave
+//                   it: head elements contiguous, which is the MN-major
+//                   operand, so nothing is transposed)
+//   warp 10         copies: Q by tensor maps over (head element, head of the
 //                   group, row), K and V page by page, two stages each
-//   warps 10-11     none (they make the register split whole)
-// TMEM columns: S_A [0, 128), S_B [128, 256), O_A and O_B behind, P_x in 16
-// bits over the first half of S_x.
+// TMEM columns: S [0, 128), used by both tiles in turn; P_A [128, 192) and
+// P_B [192, 256) in 16 bits; O_A, O_B behind.
 //
-// The issuing thread runs on events: it polls tile A and tile B in turn and
-// issues whatever is ready (P V once the softmax has written P, the next S
-// once P V has read it), so one tile's products fill the other's softmax.
+// The softmax takes its whole row of S into registers at once and frees S
+// for the other tile's product, which then runs under the exponentials; P
+// has columns of its own, so a product S never waits for a product P V.
+//
+// What it took (4096 tokens over 8192, H 32 / 8, D 128, bfloat16; the four
+// products of a pair of tiles take 2150 cycles): one warp whose lane 0 issued
+// everything 403 us -- beside eight busy softmax warps each product took 143
+// cycles to issue instead of 67; issued by an elected lane of a converged
+// warp 365 us -- now its polling of six barriers, 140 cycles a look, set the
+// pace; with two issuing warps that wait in a fixed order XXX us.  P laid over
+// S with a first half of P V issued early: 477 us (more barriers to poll).
 //
 // The softmax keeps a reference maximum that moves only when a row's maximum
 // grows by more than 2^8, so P and O are rarely rescaled; the weights are
@@ -44,8 +51,8 @@ namespace {
 
 constexpr int kCM = 128;                 // rows of a tile (MMA M)
 constexpr int kCN = 128;                 // keys of a tile
-constexpr int kCMmaWarp = 8, kCCopyWarp = 9;
-constexpr int kCThreads = 12 * 32;
+constexpr int kCMmaWarp = 8, kCPvWarp = 9, kCCopyWarp = 10;
+constexpr int kCThreads = 11 * 32;
 constexpr int kCFix = 128;               // fixed price of a unit, in cost rows
 constexpr float kCRescale = 8.f;
 constexpr uint32_t kCTmemCols = 512;
@@ -62,8 +69,8 @@ struct CGeo {
   static constexpr int OFF_V = OFF_K + KS * TILE;
   static constexpr int OFF_BAR = OFF_V + VS * TILE;
   // q, qfree, kfull[KS], kfree[KS], vfull[VS], vfree[VS], vpart, sfull[2],
-  // pfull[2], pvdone[2], odone[2], wg[2], final
-  static constexpr int NBAR = 2 + 2 * KS + 2 * VS + 1 + 10 + 1;
+  // sread, pfull[2], pvdone[2], wg[2], final[2]
+  static constexpr int NBAR = 2 + 2 * KS + 2 * VS + 1 + 2 + 1 + 6 + 2;
   static constexpr int OFF_TMEM = OFF_BAR + NBAR * 8;
   static constexpr int OFF_MISC = OFF_TMEM + 8;   // abort, last[2], bad[4], pad
   static constexpr int NEED = OFF_MISC + 32;
@@ -98,19 +105,6 @@ __device__ __forceinline__ uint32_t pack_pair(float a, float b) {
   }
 }
 
-// x * f for two packed values, f a power of two (exact above the subnormals).
-template <typename T>
-__device__ __forceinline__ uint32_t scale_pair(uint32_t x, float f) {
-  if constexpr (std::is_same<T, __half>::value) {
-    const __half2 v = __hmul2(*reinterpret_cast<const __half2 *>(&x), __float2half2_rn(f));
-    return *reinterpret_cast<const uint32_t *>(&v);
-  } else {
-    const __nv_bfloat162 v =
-        __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&x), __float2bfloat162_rn(f));
-    return *reinterpret_cast<const uint32_t *>(&v);
-  }
-}
-
 // Box of 64 elements x R rows of one column block (coordinates element, row,
 // block) and the Q box (element, head, row, block).
 __device__ __forceinline__ void tma_block(void *dst, const CUtensorMap *map, int row, int blk,
@@ -129,6 +123,10 @@ __device__ __forceinline__ void tma_q(void *dst, const CUtensorMap *map, int hea
       "l"(map), "r"(0), "r"(head), "r"(row), "r"(blk), "r"(smem_addr(bar))
       : "memory");
 }
+
+// Upper half of every descriptor here (desc_sw128 with a stride byte offset of
+// 1024) and one tile further on in the lower half's 16-byte pieces.
+constexpr uint32_t kDescHi = 1024u >> 4 | 1u << 14 | 2u << 29;
 
 // The two tiles of a unit: tokens, key tiles that each attends, and those of
 // this block's column.
@@ -154,12 +152,12 @@ __global__ void __launch_bounds__(kCThreads, 1)
   uint64_t *vfull = kfree + KS;      // [VS]
   uint64_t *vfree = vfull + VS;      // [VS] the P V products of a stage done (commit)
   uint64_t *vpart = vfree + VS;      // a V tile that ends past the last key landed
-  uint64_t *sfull = vpart + 1;       // [2] S_x ready (commit)
-  uint64_t *pfull = sfull + 2;       // [2] P_x written, O_x rescaled (128 arrivals)
+  uint64_t *sfull = vpart + 1;       // [2] S of tile x ready (commit)
+  uint64_t *sread = sfull + 2;       // S is in registers (128 arrivals of the tile's threads)
+  uint64_t *pfull = sread + 1;       // [2] P_x written, O_x rescaled (128 arrivals)
   uint64_t *pvdone = pfull + 2;      // [2] P V_x done (commit)
-  uint64_t *odone = pvdone + 2;      // [2] the unit's last P V_x done (commit)
-  uint64_t *wgbar = odone + 2;       // [2] the warps of a warpgroup
-  uint64_t *final = wgbar + 2;       // every product of the block done (commit)
+  uint64_t *wgbar = pvdone + 2;      // [2] the warps of a warpgroup
+  uint64_t *final = wgbar + 2;       // [2] every product S, every P V of the block done (commit)
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_TMEM);
   volatile int *abort = reinterpret_cast<volatile int *>(smem + C::OFF_MISC);
   volatile int *s_last = abort + 1;  // [2]
@@ -171,6 +169,7 @@ __global__ void __launch_bounds__(kCThreads, 1)
   const int lane = threadIdx.x & 31;
   const int b = blockIdx.x;
   const int TT = kCM / G;  // tokens of a tile
+  constexpr uint32_t kTileStep = C::TILE >> 4;  // one tile further on, in a descriptor
   const Line ln{Hkv, 2 * TT, kCFix, kCN, kCN + kCFix};
 
   if (threadIdx.x == 0) {
@@ -182,6 +181,7 @@ __global__ void __launch_bounds__(kCThreads, 1)
       mbar_init(&pfull[x], kCM);
       mbar_init(&wgbar[x], 4);
     }
+    mbar_init(sread, kCM);
     *abort = 0;
     fence_mbar_init();
   }
@@ -318,143 +318,113 @@ __global__ void __launch_bounds__(kCThreads, 1)
     }
     __syncwarp();
   } else if (warp == kCMmaWarp) {
-    // ======================= tensor-core work ================================
-    if (lane == 0) {
-      const uint64_t dq = desc_sw128(smem + C::OFF_Q, 16, 1024);
-      const uint64_t dk = desc_sw128(smem + C::OFF_K, 16, 1024);
-      const uint64_t dv = desc_sw128(smem + C::OFF_V, C::BLK, 1024);
-      constexpr uint64_t kTileStep = C::TILE >> 4;
-      constexpr uint32_t kIdS = idesc16<T>(kCM, kCN, false);
-      constexpr uint32_t kIdO = idesc16<T>(kCM, D, true);
-      int gt = 0;                 // K (and V) tiles of the earlier units
-      int sdone[2] = {0, 0};      // S_x products of the earlier units (pfull, pvdone phases)
-      int nq = 0;
-      bool ok = true;
-      uint32_t out_commits = 0;   // a bit per x: a commit on pvdone[x] not yet waited for
-      const uint64_t limit = kPoll ? (uint64_t)g_wait_limit_ns : kWaitLimitNs;
-      while (more && ok) {
-        const UnitInfo f = unit_info(pa, u, ln, x0, x1);
-        if (f.t_lo < f.t_hi) {
-          const CTile ta = tile_of(f, 0), tb = tile_of(f, 1);
-          const int n_x[2] = {ta.hi - ta.lo, tb.hi - tb.lo};  // products of each tile
-          const int n_all = f.t_hi - f.t_lo;                  // K and V tiles of the unit
-          // (a tile attends the first n_x of them; key tiles that only B attends come last)
-          int s_next[2] = {0, 0}, pv_next[2] = {0, 0};
-          int k_done = 0, v_done = 0;  // stages released
-          int k_in = 0, v_in = 0;      // stages known to have landed
-          bool have_q = false;
-          uint64_t t0 = global_timer_ns();
-          uint32_t idle = 0;
-          while (k_done < n_all || v_done < n_all) {
-            bool did = false;
-            if (!have_q) {
-              have_q = mbar_test_wait(bar_q, (uint32_t)nq & 1u);
-              if (have_q) tc_fence_after();
-            }
+    // ======================= products S ======================================
+    // The whole warp runs the loop, converged; an elected lane issues.  Order:
+    // S_A(0), S_B(0), S_A(1), ... into the same columns, each once the one
+    // before has been read.
+    const uint32_t lq = (uint32_t)desc_sw128(smem + C::OFF_Q, 16, 1024);
+    const uint32_t lk = lq + ((C::OFF_K - C::OFF_Q) >> 4);
+    const uint32_t tm = warp_uniform(tmem);
+    constexpr uint32_t kIdS = idesc16<T>(kCM, kCN, false);
+    int gt = 0;       // K tiles of the earlier units
+    uint32_t ns = 0;  // S products issued
+    int nq = 0;
+    bool ok = true;
+    auto wait = [&](uint64_t *bar, uint32_t phase) {
+      return ok = __all_sync(0xffffffffu, mbar_wait<kPoll>(bar, phase & 1u, abort)) != 0;
+    };
+    while (more && ok) {
+      const UnitInfo f = unit_info(pa, u, ln, x0, x1);
+      if (f.t_lo < f.t_hi) {
+        const CTile ta = tile_of(f, 0), tb = tile_of(f, 1);
+        const int n_x[2] = {ta.hi - ta.lo, tb.hi - tb.lo};  // products of each tile
+        const int n_all = f.t_hi - f.t_lo;                  // K tiles of the unit
+        if (!wait(bar_q, nq)) break;
+        for (int i = 0; i < n_all && ok; ++i, ++gt) {
+          if (!wait(&kfull[gt % KS], gt / KS)) break;
+          const uint32_t bk = warp_uniform(lk + (uint32_t)(gt % KS) * kTileStep);
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              // P V_x(j): P_x(j) is written and V(j) has landed
-              const int j = pv_next[x];
-              if (j < s_next[x] && mbar_test_wait(&pfull[x], (uint32_t)(sdone[x] + j) & 1u)) {
-                bool in = j < v_in;
-                if (!in) {
-                  const int gv = gt + j;
-                  in = mbar_test_wait(&vfull[gv % VS], (uint32_t)(gv / VS) & 1u);
-                  if (in) v_in = j + 1;
-                }
-                if (in) {
-                  tc_fence_after();
-                  const uint64_t bv = dv + (uint64_t)((gt + j) % VS) * kTileStep;
-                  const uint32_t d = tmem + 2 * kCN + x * D, a = tmem + x * kCN;
+          for (int x = 0; x < 2; ++x) {
+            if (i >= n_x[x]) continue;
+            if (ns > 0 && !wait(sread, ns - 1u)) break;
+            tc_fence_after();
 #pragma unroll
-                  for (int ks = 0; ks < kCN / 16; ++ks)
-                    mma_f16_ts(d, a + ks * 8, bv + 128 * ks, kIdO, (j > 0 || ks > 0) ? 1u : 0u);
-                  if (j + 1 == n_x[x]) mma_commit(&odone[x]);
-                  mma_commit(&pvdone[x]);
-                  out_commits |= 1u << x;
-                  pv_next[x] = j + 1;
-                  did = true;
-                }
-              }
-              // S_x(i): P V_x(i - 1) is done with P_x, and K(i) has landed
-              const int i = s_next[x];
-              if (have_q && i < n_x[x] && i == pv_next[x]) {
-                if (out_commits >> x & 1u) {
-                  if (mbar_test_wait(&pvdone[x], (uint32_t)(sdone[x] + i - 1) & 1u))
-                    out_commits &= ~(1u << x);
-                }
-                if (!(out_commits >> x & 1u)) {
-                  bool in = i < k_in;
-                  if (!in) {
-                    const int gk = gt + i;
-                    in = mbar_test_wait(&kfull[gk % KS], (uint32_t)(gk / KS) & 1u);
-                    if (in) k_in = i + 1;
-                  }
-                  if (in) {
-                    tc_fence_after();
-                    const uint64_t a = dq + (x ? kTileStep : 0);
-                    const uint64_t bk = dk + (uint64_t)((gt + i) % KS) * kTileStep;
-                    const uint32_t d = tmem + x * kCN;
-#pragma unroll
-                    for (int ks = 0; ks < D / 16; ++ks) {
-                      const uint64_t at = (uint64_t)(ks >> 2) * (C::BLK >> 4) + (ks & 3) * 2;
-                      mma_f16(d, a + at, bk + at, kIdS, ks > 0 ? 1u : 0u);
-                    }
-                    mma_commit(&sfull[x]);
-                    s_next[x] = i + 1;
-                    did = true;
-                  }
-                }
-              }
+            for (int ks = 0; ks < D / 16; ++ks) {
+              const uint32_t at = (uint32_t)(ks >> 2) * (C::BLK >> 4) + (ks & 3) * 2;
+              mma_f16_warp(tm, lq + (x ? kTileStep : 0u) + at, bk + at, kDescHi, kIdS, ks > 0 ? 1u : 0u);
             }
-            if (did) {
-              // stages whose last product is issued: their commit frees them
-              while (k_done < n_all && (s_next[0] > k_done || k_done >= n_x[0]) &&
-                     (s_next[1] > k_done || k_done >= n_x[1])) {
-                mma_commit(&kfree[(gt + k_done) % KS]);
-                if (++k_done == n_all) mma_commit(qfree);
-              }
-              while (v_done < n_all && (pv_next[0] > v_done || v_done >= n_x[0]) &&
-                     (pv_next[1] > v_done || v_done >= n_x[1])) {
-                mma_commit(&vfree[(gt + v_done) % VS]);
-                ++v_done;
-              }
-              idle = 0;
-            } else {
-              // nothing was ready: bounded polling
-              if (idle == 0) t0 = global_timer_ns();
-              if ((++idle & (kPoll ? 0u : 255u)) == 0) {
-                if (*abort || global_timer_ns() - t0 > limit) {
-                  ok = false;
-                  break;
-                }
-              }
-            }
+            mma_commit_warp(&sfull[x]);
+            ++ns;
           }
           if (!ok) break;
-          gt += n_all;
-          sdone[0] += n_x[0];
-          sdone[1] += n_x[1];
-          ++nq;
+          mma_commit_warp(&kfree[gt % KS]);
+          if (i + 1 == n_all) mma_commit_warp(qfree);
         }
-        advance(f);
+        if (!ok) break;
+        ++nq;
       }
-      if (!ok) give_up(abort, d_status, epoch);
-      // every product issued finishes before the block frees the tensor memory
-      mma_commit(final);
-      mbar_wait_drain(final, 0u);
+      advance(f);
     }
+    if (!ok && lane == 0) give_up(abort, d_status, epoch);
+    // every product issued finishes before the block frees the tensor memory
+    mma_commit_warp(&final[0]);
+    mbar_wait_drain(&final[0], 0u);
+    __syncwarp();
+  } else if (warp == kCPvWarp) {
+    // ======================= products P V ====================================
+    const uint32_t lv = (uint32_t)desc_sw128(smem + C::OFF_V, C::BLK, 1024);
+    const uint32_t tm = warp_uniform(tmem);
+    constexpr uint32_t kIdO = idesc16<T>(kCM, D, true);
+    int gt = 0;             // V tiles of the earlier units
+    int pdone[2] = {0, 0};  // P V_x products of the earlier units
+    bool ok = true;
+    auto wait = [&](uint64_t *bar, uint32_t phase) {
+      return ok = __all_sync(0xffffffffu, mbar_wait<kPoll>(bar, phase & 1u, abort)) != 0;
+    };
+    while (more && ok) {
+      const UnitInfo f = unit_info(pa, u, ln, x0, x1);
+      if (f.t_lo < f.t_hi) {
+        const CTile ta = tile_of(f, 0), tb = tile_of(f, 1);
+        const int n_x[2] = {ta.hi - ta.lo, tb.hi - tb.lo};
+        const int n_all = f.t_hi - f.t_lo;
+        for (int j = 0; j < n_all && ok; ++j, ++gt) {
+          if (!wait(&vfull[gt % VS], gt / VS)) break;
+          const uint32_t bv = warp_uniform(lv + (uint32_t)(gt % VS) * kTileStep);
+          const uint32_t acc = warp_uniform(j > 0 ? 1u : 0u);  // O_x (+)= P_x V
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            if (j >= n_x[x]) continue;
+            if (!wait(&pfull[x], pdone[x] + j)) break;
+            tc_fence_after();
+#pragma unroll
+            for (int ks = 0; ks < kCN / 16; ++ks)
+              mma_f16_ts_warp(tm + 2 * kCN + x * D, tm + kCN + x * (kCN / 2) + ks * 8, bv + 128 * ks,
+                              kDescHi, kIdO, ks > 0 ? 1u : acc);
+            mma_commit_warp(&pvdone[x]);
+          }
+          if (!ok) break;
+          mma_commit_warp(&vfree[gt % VS]);
+        }
+        if (!ok) break;
+        pdone[0] += n_x[0];
+        pdone[1] += n_x[1];
+      }
+      advance(f);
+    }
+    if (!ok && lane == 0) give_up(abort, d_status, epoch);
+    mma_commit_warp(&final[1]);
+    mbar_wait_drain(&final[1], 0u);
     __syncwarp();
   } else if (warp < 8) {
     // ======================= softmax of tile x ===============================
     const int x = warp >> 2;
     const int t = threadIdx.x & 127;
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t tm_s = tmem + lane_base + x * kCN;
+    const uint32_t tm_s = tmem + lane_base;
+    const uint32_t tm_p = tmem + lane_base + kCN + x * (kCN / 2);
     const uint32_t tm_o = tmem + lane_base + 2 * kCN + x * D;
     const float nan = __int_as_float(0x7fc00000);
     int sb = 0;  // S_x products of the earlier units
-    int ob = 0;  // earlier units with products of tile x
     int nq = 0;  // earlier units
     uint32_t wphase = 0;
     bool failed = false;
@@ -482,70 +452,68 @@ __global__ void __launch_bounds__(kCThreads, 1)
             break;
           }
           tc_fence_after();
+          float r[kCN];
+          tmem_ld64(tm_s, *reinterpret_cast<float(*)[64]>(&r[0]));
+          tmem_ld64(tm_s + 64, *reinterpret_cast<float(*)[64]>(&r[64]));
+          tmem_wait_ld();
+          tc_fence_before();
+          mbar_arrive(sread);  // the other tile's product may have the columns
           const int key0 = n * kCN;
-          const bool masked = key0 + kCN - 1 > first_last;
-          float m_ref = m;
-          float lt = 0.f;
+          if (key0 + kCN - 1 > first_last) {
+            const int lim = last - key0;  // keys 0..lim of the tile are attended
+#pragma unroll
+            for (int v = 0; v < kCN; ++v) r[v] = v <= lim ? r[v] : neg_inf_f();
+          }
+          float mx[4] = {r[0], r[1], r[2], r[3]};  // four chains (max is exact in any order)
+#pragma unroll
+          for (int v = 4; v < kCN; v += 4) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], r[v + k]);
+          }
+          const float cm = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
+          // the reference maximum moves only when the row's grows by more
+          // than 2^kCRescale: below that P stays in range and nothing needs
+          // rescaling
+          const float m_ref = cm > m + kCRescale ? cm : m;
+          // (rows that do not exist hold anything: they never ask for a rescale)
+          const float alpha = (m == neg_inf_f() || !live) ? 1.f : ex2(m - m_ref);
+          // P_x and O_x are free once the product before has read and written them
+          if (n > tl.lo) {
+            if (!__all_sync(0xffffffffu, mbar_wait<kPoll>(&pvdone[x], ph ^ 1u, abort))) {
+              failed = true;
+              break;
+            }
+            tc_fence_after();
+            if (__any_sync(0xffffffffu, alpha != 1.f)) {
 #pragma unroll 1
-          for (int ch = 0; ch < 2; ++ch) {
-            float r[64];
-            tmem_ld64(tm_s + ch * 64, r);
-            tmem_wait_ld();
-            if (masked) {
-              const int lim = last - (key0 + ch * 64);  // keys 0..lim of the chunk are attended
+              for (int c = 0; c < D / 16; ++c) {
+                float o[16];
+                uint32_t w[16];
+                tmem_ld16(tm_o + c * 16, o);
+                tmem_wait_ld();
 #pragma unroll
-              for (int v = 0; v < 64; ++v) r[v] = v <= lim ? r[v] : neg_inf_f();
+                for (int v = 0; v < 16; ++v) w[v] = __float_as_uint(o[v] * alpha);
+                tmem_st16u(tm_o + c * 16, w);
+              }
             }
-            float mx[32];
+          }
+          const float mb = (m_ref == neg_inf_f()) ? 0.f : m_ref;
+          float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          const float2 sl2x2 = make_float2(sl2, sl2), nmb2 = make_float2(-mb, -mb);
 #pragma unroll
-            for (int v = 0; v < 32; ++v) mx[v] = fmaxf(r[v], r[v + 32]);
+          for (int ch = 0; ch < 4; ++ch) {
+            uint32_t w[16];
 #pragma unroll
-            for (int w = 16; w >= 1; w >>= 1) {
-#pragma unroll
-              for (int v = 0; v < w; ++v) mx[v] = fmaxf(mx[v], mx[v + w]);
-            }
-            const float cm = mx[0] * sl2;
-            const float m_prev = m_ref;
-            if (cm > m_ref + kCRescale) m_ref = cm;
-            if (ch > 0 && __any_sync(0xffffffffu, m_ref != m_prev)) {  // rare
-              const float fac = (m_ref != m_prev) ? ex2(m_prev - m_ref) : 1.f;
-              lt *= fac;
-              uint32_t w0[32];
-              tmem_wait_st();  // chunk 0's P has landed
-              tmem_ld32u(tm_s, w0);
-              tmem_wait_ld();
-#pragma unroll
-              for (int v = 0; v < 32; ++v) w0[v] = scale_pair<T>(w0[v], fac);
-              tmem_st32u(tm_s, w0);
-            }
-            const float mb = (m_ref == neg_inf_f()) ? 0.f : m_ref;
-            uint32_t w[32];
-            float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-            const float2 sl2x2 = make_float2(sl2, sl2), nmb2 = make_float2(-mb, -mb);
-#pragma unroll
-            for (int v = 0; v < 32; ++v) {
-              const float2 x2 = __ffma2_rn(make_float2(r[2 * v], r[2 * v + 1]), sl2x2, nmb2);
+            for (int v = 0; v < 16; ++v) {
+              const float2 x2 = __ffma2_rn(make_float2(r[32 * ch + 2 * v], r[32 * ch + 2 * v + 1]),
+                                           sl2x2, nmb2);
               const float p0 = ex2(x2.x), p1 = ex2(x2.y);
               ls[v & 1] = __fadd2_rn(ls[v & 1], make_float2(p0, p1));
               w[v] = pack_pair<T>(p0, p1);
             }
-            lt += (ls[0].x + ls[1].x) + (ls[0].y + ls[1].y);
-            tmem_st32u(tm_s + ch * 32, w);
+            tmem_st16u(tm_p + ch * 16, w);
           }
-          // (rows that do not exist hold anything: they never ask for a rescale)
-          const float alpha = (m == neg_inf_f() || !live) ? 1.f : ex2(m - m_ref);
-          if (n > tl.lo && __any_sync(0xffffffffu, alpha != 1.f)) {
-#pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-              float r[32];
-              tmem_ld32(tm_o + c * 32, r);
-              tmem_wait_ld();
-#pragma unroll
-              for (int v = 0; v < 32; ++v) r[v] *= alpha;
-              tmem_st32(tm_o + c * 32, r);
-            }
-          }
-          l = l * alpha + lt;
+          l = l * alpha + ((ls[0].x + ls[1].x) + (ls[0].y + ls[1].y));
           m = m_ref;
           tmem_wait_st();
           tc_fence_before();
@@ -554,11 +522,11 @@ __global__ void __launch_bounds__(kCThreads, 1)
         if (failed) break;
         sb += tl.hi - tl.lo;
         if (tl.lo < tl.hi) {
-          if (!__all_sync(0xffffffffu, mbar_wait<kPoll>(&odone[x], (uint32_t)ob & 1u, abort))) {
+          // the tile's last product is done: O_x is final
+          if (!__all_sync(0xffffffffu, mbar_wait<kPoll>(&pvdone[x], (uint32_t)(sb - 1) & 1u, abort))) {
             failed = true;
             break;
           }
-          ++ob;
           tc_fence_after();
           if (s_bad[nq & 3]) l = nan;
           const bool whole = tl.hi - tl.lo == tl.nt;
