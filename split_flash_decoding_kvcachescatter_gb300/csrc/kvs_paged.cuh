@@ -292,51 +292,4 @@ static __device__ __forceinline__ void merge_pieces(const float *slots, size_t s
   }
 }
 
-// merge_pieces for NR rows at once (rows r0 + k * step < rows), PB pieces at a
-// time: NR * PB accumulator loads in flight a thread.  Accumulators of row r
-// are at float at + r D + d of a slot.
-template <int NR, int PB>
-__device__ __forceinline__ void merge_rows(const float *slots, size_t stride, int at, int D, int d,
-                                           int r0, int step, int rows, int b1, int b2,
-                                           float4 (&acc)[NR], float (&l)[NR]) {
-  float m[NR];
-#pragma unroll
-  for (int k = 0; k < NR; ++k) {
-    acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-    l[k] = 0.f;
-    m[k] = neg_inf_f();
-  }
-  for (int c = b1; c <= b2; c += PB) {
-    float2 ml[NR][PB];
-    float4 v[NR][PB];
-#pragma unroll
-    for (int j = 0; j < PB; ++j) {
-      // (past the last piece: its loads again, not used)
-      const float *ps = slots + (2 * (size_t)min(c + j, b2) + (min(c + j, b2) == b1 ? 1 : 0)) * stride;
-#pragma unroll
-      for (int k = 0; k < NR; ++k) {
-        const int r = min(r0 + k * step, rows - 1);
-        ml[k][j] = __ldcg(reinterpret_cast<const float2 *>(ps) + r);
-        v[k][j] = __ldcg(reinterpret_cast<const float4 *>(ps + at + (size_t)r * D + d));
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < PB; ++j) {
-      if (c + j > b2) break;
-#pragma unroll
-      for (int k = 0; k < NR; ++k) {
-        const float mn = fmaxf(m[k], ml[k][j].x);
-        const float mz = mn == neg_inf_f() ? 0.f : mn;
-        const float wa = exp2f(m[k] - mz), wb = exp2f(ml[k][j].x - mz);
-        acc[k].x = acc[k].x * wa + v[k][j].x * wb;
-        acc[k].y = acc[k].y * wa + v[k][j].y * wb;
-        acc[k].z = acc[k].z * wa + v[k][j].z * wb;
-        acc[k].w = acc[k].w * wa + v[k][j].w * wb;
-        l[k] = l[k] * wa + ml[k][j].y * wb;  // (a NaN sum stays one also under a zero weight)
-        m[k] = mn;
-      }
-    }
-  }
-}
-
 }  // namespace kvs

@@ -128,6 +128,29 @@ __device__ __forceinline__ void tma_q(void *dst, const CUtensorMap *map, int hea
 // 1024) and one tile further on in the lower half's 16-byte pieces.
 constexpr uint32_t kDescHi = 1024u >> 4 | 1u << 14 | 2u << 29;
 
+__device__ __forceinline__ unsigned long long ld_acquire_u64(const unsigned long long *p) {
+  unsigned long long v;
+  asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
+  return v;
+}
+
+// The pieces of a unit's tile: those of ranges b1 .. b2, the first in its
+// slot 1, the others in their slots 0; a piece has each row's (m, l), then
+// its accumulators.  A row's pieces always join in this way, whichever block
+// does it: the largest m first, then weighted sums in range order.
+struct Pieces {
+  const float *slots;  // of this tile
+  size_t stride;       // floats between a block's slots
+  int b1, b2;
+  __device__ const float *at(int c) const {
+    return slots + (2 * (size_t)c + (c == b1 ? 1 : 0)) * stride;
+  }
+};
+// Weight of a piece with maximum m beside the overall maximum mx.
+__device__ __forceinline__ float piece_weight(float m, float mx) {
+  return ex2(m - (mx == neg_inf_f() ? 0.f : mx));
+}
+
 // The two tiles of a unit: tokens, key tiles that each attends, and those of
 // this block's column.
 struct CTile {
@@ -550,38 +573,16 @@ __global__ void __launch_bounds__(kCThreads, 1)
               }
             }
           } else {
-            auto slot_of = [&](int c, int lo) {
-              return slots + ((2 * (size_t)c + (lo == 0 ? 1 : 0)) * 2 + x) * paged_slot_floats(kCM, D);
-            };
-            float *sl = slot_of(b, tl.lo);
-#pragma unroll 1
-            for (int ch = 0; ch < D / 32; ++ch) {
-              float o[32];
-              tmem_ld32(tm_o + ch * 32, o);
-              tmem_wait_ld();
-              if (live) {
-                float4 *o4 = reinterpret_cast<float4 *>(sl + 2 * kCM + (size_t)t * D + ch * 32);
-#pragma unroll
-                for (int v = 0; v < 8; ++v)
-                  __stcg(o4 + v, make_float4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]));
-              }
-            }
-            if (live) __stcg(reinterpret_cast<float2 *>(sl) + t, make_float2(m, l));
-            __threadfence();  // the partial is visible GPU-wide before it counts
-            if (!wg_barrier()) {
-              failed = true;
-              break;
-            }
-            // the blocks of tile x's first and last key tile
-            const int b1 = cut.at(f.k0);
-            const int b2 = cut.at(f.k0 + (long long)(tl.nt - 1) * kCN);
+            // the blocks of tile x's first and last key tile, and their partials
+            const Pieces pc{slots + x * paged_slot_floats(kCM, D), 2 * paged_slot_floats(kCM, D),
+                            cut.at(f.k0), cut.at(f.k0 + (long long)(tl.nt - 1) * kCN)};
+            unsigned long long *ctr = counters + 2 * pc.b1 + x;
+            const unsigned add = (unsigned)(tl.hi - tl.lo);
+            // Usually the other pieces were finished long ago: then this block
+            // joins them with the accumulator it still holds in TMEM.
             if (t == 0) {
-              const unsigned add = (unsigned)(tl.hi - tl.lo);
-              unsigned long long *ctr = counters + 2 * b1 + x;
-              const unsigned before = tagged_add(ctr, add, tag, d_status, epoch);
-              const bool fin = before != 0xffffffffu && before + add == (unsigned)tl.nt;
-              if (fin) *ctr = 0ull;  // a replayed graph uses the same tag again
-              s_last[x] = fin;
+              const unsigned long long v = ld_acquire_u64(ctr);
+              s_last[x] = (unsigned)(v >> 32) == tag && (unsigned)v + add == (unsigned)tl.nt;
             }
             if (!wg_barrier()) {
               failed = true;
@@ -589,25 +590,112 @@ __global__ void __launch_bounds__(kCThreads, 1)
             }
             if (s_last[x]) {
               __threadfence();
-              // four rows a thread in flight (most units have two or three pieces)
-              constexpr int kRowsAhead = 4, kStep = kCM / (D / 4);  // rows a pass
-              const int d = (t % (D / 4)) * 4;
-              const float *base = slots + x * paged_slot_floats(kCM, D);
-              for (int r0 = t / (D / 4); r0 < rows; r0 += kRowsAhead * kStep) {
-                float4 acc[kRowsAhead];
-                float ls[kRowsAhead];
-                merge_rows<kRowsAhead, 2>(base, 2 * paged_slot_floats(kCM, D), 2 * kCM, D, d, r0, kStep,
-                                       rows, b1, b2, acc, ls);
+              if (t == 0) *ctr = 0ull;  // (no other block will look; a replayed graph uses the tag again)
+              float mx = m;
+              for (int c = pc.b1; c <= pc.b2; ++c)
+                if (c != b) mx = fmaxf(mx, __ldcg(reinterpret_cast<const float2 *>(pc.at(c)) + t).x);
+              float ls = 0.f;
+              for (int c = pc.b1; c <= pc.b2; ++c) {
+                const float2 ml = c == b ? make_float2(m, l)
+                                         : __ldcg(reinterpret_cast<const float2 *>(pc.at(c)) + t);
+                ls = fmaf(piece_weight(ml.x, mx), ml.y, ls);
+              }
+              const float inv = 1.f / ls;
+              T *orow = out + (row0 + tok) * out_stride + (long long)(u.g * G + (t - tok * G)) * D;
+#pragma unroll 1
+              for (int ch = 0; ch < D / 32; ++ch) {
+                float o[32], acc[32];
+                tmem_ld32(tm_o + ch * 32, o);
+                tmem_wait_ld();
 #pragma unroll
-                for (int k = 0; k < kRowsAhead; ++k) {
-                  const int r = r0 + k * kStep;
-                  if (r >= rows) break;
-                  const float inv = 1.f / ls[k];
+                for (int v = 0; v < 32; ++v) acc[v] = 0.f;
+                for (int c = pc.b1; c <= pc.b2; ++c) {
+                  if (c == b) {
+                    const float w = piece_weight(m, mx);
+#pragma unroll
+                    for (int v = 0; v < 32; ++v) acc[v] = fmaf(w, o[v], acc[v]);
+                  } else {
+                    const float *ps = pc.at(c);
+                    const float w = piece_weight(__ldcg(reinterpret_cast<const float2 *>(ps) + t).x, mx);
+                    const float4 *p4 = reinterpret_cast<const float4 *>(ps + 2 * kCM + (size_t)t * D + ch * 32);
+                    float4 q[8];
+#pragma unroll
+                    for (int v = 0; v < 8; ++v) q[v] = __ldcg(p4 + v);
+#pragma unroll
+                    for (int v = 0; v < 8; ++v) {
+                      acc[4 * v] = fmaf(w, q[v].x, acc[4 * v]);
+                      acc[4 * v + 1] = fmaf(w, q[v].y, acc[4 * v + 1]);
+                      acc[4 * v + 2] = fmaf(w, q[v].z, acc[4 * v + 2]);
+                      acc[4 * v + 3] = fmaf(w, q[v].w, acc[4 * v + 3]);
+                    }
+                  }
+                }
+                if (live) {
+                  uint4 *o4 = reinterpret_cast<uint4 *>(orow + ch * 32);
+#pragma unroll
+                  for (int v = 0; v < 4; ++v)
+                    o4[v] = make_uint4(pack_pair<T>(acc[8 * v] * inv, acc[8 * v + 1] * inv),
+                                       pack_pair<T>(acc[8 * v + 2] * inv, acc[8 * v + 3] * inv),
+                                       pack_pair<T>(acc[8 * v + 4] * inv, acc[8 * v + 5] * inv),
+                                       pack_pair<T>(acc[8 * v + 6] * inv, acc[8 * v + 7] * inv));
+                }
+              }
+            } else {
+              float *sl = const_cast<float *>(pc.at(b));
+#pragma unroll 1
+              for (int ch = 0; ch < D / 32; ++ch) {
+                float o[32];
+                tmem_ld32(tm_o + ch * 32, o);
+                tmem_wait_ld();
+                if (live) {
+                  float4 *o4 = reinterpret_cast<float4 *>(sl + 2 * kCM + (size_t)t * D + ch * 32);
+#pragma unroll
+                  for (int v = 0; v < 8; ++v)
+                    __stcg(o4 + v, make_float4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]));
+                }
+              }
+              if (live) __stcg(reinterpret_cast<float2 *>(sl) + t, make_float2(m, l));
+              __threadfence();  // the partial is visible GPU-wide before it counts
+              if (!wg_barrier()) {
+                failed = true;
+                break;
+              }
+              if (t == 0) {
+                const unsigned before = tagged_add(ctr, add, tag, d_status, epoch);
+                const bool fin = before != 0xffffffffu && before + add == (unsigned)tl.nt;
+                if (fin) *ctr = 0ull;
+                s_last[x] = fin;
+              }
+              if (!wg_barrier()) {
+                failed = true;
+                break;
+              }
+              if (s_last[x]) {
+                // (the others finished in the meantime: all pieces from memory)
+                __threadfence();
+                for (int e = t; e < rows * (D / 4); e += kCM) {
+                  const int r = e / (D / 4), d = (e - r * (D / 4)) * 4;
+                  float mx = neg_inf_f();
+                  for (int c = pc.b1; c <= pc.b2; ++c)
+                    mx = fmaxf(mx, __ldcg(reinterpret_cast<const float2 *>(pc.at(c)) + r).x);
+                  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+                  float ls = 0.f;
+                  for (int c = pc.b1; c <= pc.b2; ++c) {
+                    const float *ps = pc.at(c);
+                    const float2 ml = __ldcg(reinterpret_cast<const float2 *>(ps) + r);
+                    const float4 v = __ldcg(reinterpret_cast<const float4 *>(ps + 2 * kCM + (size_t)r * D + d));
+                    const float w = piece_weight(ml.x, mx);
+                    ls = fmaf(w, ml.y, ls);
+                    acc.x = fmaf(w, v.x, acc.x);
+                    acc.y = fmaf(w, v.y, acc.y);
+                    acc.z = fmaf(w, v.z, acc.z);
+                    acc.w = fmaf(w, v.w, acc.w);
+                  }
+                  const float inv = 1.f / ls;
                   const int tk = r / G;
                   T *p = out + (row0 + tk) * out_stride + (long long)(u.g * G + (r - tk * G)) * D + d;
-                  *reinterpret_cast<uint2 *>(p) =
-                      make_uint2(pack_pair<T>(acc[k].x * inv, acc[k].y * inv),
-                                 pack_pair<T>(acc[k].z * inv, acc[k].w * inv));
+                  *reinterpret_cast<uint2 *>(p) = make_uint2(pack_pair<T>(acc.x * inv, acc.y * inv),
+                                                             pack_pair<T>(acc.z * inv, acc.w * inv));
                 }
               }
             }
