@@ -128,6 +128,18 @@ __device__ __forceinline__ void tma_q(void *dst, const CUtensorMap *map, int hea
 // 1024) and one tile further on in the lower half's 16-byte pieces.
 constexpr uint32_t kDescHi = 1024u >> 4 | 1u << 14 | 2u << 29;
 
+// 32 columns of a row times inv, rounded to the type.
+template <typename T>
+__device__ __forceinline__ void store_row32(T *p, const float (&o)[32], float inv) {
+  uint4 *o4 = reinterpret_cast<uint4 *>(p);
+#pragma unroll
+  for (int v = 0; v < 4; ++v)
+    o4[v] = make_uint4(pack_pair<T>(o[8 * v] * inv, o[8 * v + 1] * inv),
+                       pack_pair<T>(o[8 * v + 2] * inv, o[8 * v + 3] * inv),
+                       pack_pair<T>(o[8 * v + 4] * inv, o[8 * v + 5] * inv),
+                       pack_pair<T>(o[8 * v + 6] * inv, o[8 * v + 7] * inv));
+}
+
 __device__ __forceinline__ unsigned long long ld_acquire_u64(const unsigned long long *p) {
   unsigned long long v;
   asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
@@ -136,14 +148,20 @@ __device__ __forceinline__ unsigned long long ld_acquire_u64(const unsigned long
 
 // The pieces of a unit's tile: those of ranges b1 .. b2, the first in its
 // slot 1, the others in their slots 0; a piece has each row's (m, l), then
-// its accumulators.  A row's pieces always join in this way, whichever block
+// its accumulators, four columns of all 128 rows after the other (thread t
+// writes and reads row t, so a warp moves 512 contiguous bytes).  A row's pieces always join in this way, whichever block
 // does it: the largest m first, then weighted sums in range order.
 struct Pieces {
   const float *slots;  // of this tile
   size_t stride;       // floats between a block's slots
   int b1, b2;
-  __device__ const float *at(int c) const {
-    return slots + (2 * (size_t)c + (c == b1 ? 1 : 0)) * stride;
+  __device__ float2 *ml(int c, int row) const {
+    float *p = const_cast<float *>(slots) + (2 * (size_t)c + (c == b1 ? 1 : 0)) * stride;
+    return reinterpret_cast<float2 *>(p) + row;
+  }
+  __device__ float4 *acc(int c, int row, int d) const {  // columns d .. d + 3
+    float *p = const_cast<float *>(slots) + (2 * (size_t)c + (c == b1 ? 1 : 0)) * stride;
+    return reinterpret_cast<float4 *>(p + 2 * kCM) + (d / 4) * kCM + row;
   }
 };
 // Weight of a piece with maximum m beside the overall maximum mx.
@@ -176,8 +194,8 @@ __global__ void __launch_bounds__(kCThreads, 1)
   uint64_t *vfree = vfull + VS;      // [VS] the P V products of a stage done (commit)
   uint64_t *vpart = vfree + VS;      // a V tile that ends past the last key landed
   uint64_t *sfull = vpart + 1;       // [2] S of tile x ready (commit)
-  uint64_t *sread = sfull + 2;       // S is in registers (128 arrivals of the tile's threads)
-  uint64_t *pfull = sread + 1;       // [2] P_x written, O_x rescaled (128 arrivals)
+  uint64_t *sread = sfull + 2;       // S is in registers (an arrival of each of the tile's warps)
+  uint64_t *pfull = sread + 1;       // [2] P_x written, O_x rescaled (an arrival a warp)
   uint64_t *pvdone = pfull + 2;      // [2] P V_x done (commit)
   uint64_t *wgbar = pvdone + 2;      // [2] the warps of a warpgroup
   uint64_t *final = wgbar + 2;       // [2] every product S, every P V of the block done (commit)
@@ -201,10 +219,10 @@ __global__ void __launch_bounds__(kCThreads, 1)
     prefetch_map(&vmap);
     for (int j = 0; j < C::NBAR; ++j) mbar_init(&bars[j], 1);
     for (int x = 0; x < 2; ++x) {
-      mbar_init(&pfull[x], kCM);
+      mbar_init(&pfull[x], 4);  // (an arrival a warp: 128 of them took some 200 cycles)
       mbar_init(&wgbar[x], 4);
     }
-    mbar_init(sread, kCM);
+    mbar_init(sread, 4);
     *abort = 0;
     fence_mbar_init();
   }
@@ -480,7 +498,8 @@ __global__ void __launch_bounds__(kCThreads, 1)
           tmem_ld64(tm_s + 64, *reinterpret_cast<float(*)[64]>(&r[64]));
           tmem_wait_ld();
           tc_fence_before();
-          mbar_arrive(sread);  // the other tile's product may have the columns
+          __syncwarp();
+          if (lane == 0) mbar_arrive(sread);  // the other tile's product may have the columns
           const int key0 = n * kCN;
           if (key0 + kCN - 1 > first_last) {
             const int lim = last - key0;  // keys 0..lim of the tile are attended
@@ -540,7 +559,8 @@ __global__ void __launch_bounds__(kCThreads, 1)
           m = m_ref;
           tmem_wait_st();
           tc_fence_before();
-          mbar_arrive(&pfull[x]);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&pfull[x]);
         }
         if (failed) break;
         sb += tl.hi - tl.lo;
@@ -554,23 +574,15 @@ __global__ void __launch_bounds__(kCThreads, 1)
           if (s_bad[nq & 3]) l = nan;
           const bool whole = tl.hi - tl.lo == tl.nt;
           const long long row0 = f.s.row0 + tl.tok0;
+          T *orow = out + (row0 + tok) * out_stride + (long long)(u.g * G + (t - tok * G)) * D;
           if (whole) {
             const float inv = 1.f / l;
-            T *orow = out + (row0 + tok) * out_stride + (long long)(u.g * G + (t - tok * G)) * D;
 #pragma unroll 1
             for (int ch = 0; ch < D / 32; ++ch) {
               float o[32];
               tmem_ld32(tm_o + ch * 32, o);
               tmem_wait_ld();
-              if (live) {
-                uint4 *o4 = reinterpret_cast<uint4 *>(orow + ch * 32);
-#pragma unroll
-                for (int v = 0; v < 4; ++v)
-                  o4[v] = make_uint4(pack_pair<T>(o[8 * v] * inv, o[8 * v + 1] * inv),
-                                     pack_pair<T>(o[8 * v + 2] * inv, o[8 * v + 3] * inv),
-                                     pack_pair<T>(o[8 * v + 4] * inv, o[8 * v + 5] * inv),
-                                     pack_pair<T>(o[8 * v + 6] * inv, o[8 * v + 7] * inv));
-              }
+              if (live) store_row32<T>(orow + ch * 32, o, inv);
             }
           } else {
             // the blocks of tile x's first and last key tile, and their partials
@@ -591,17 +603,42 @@ __global__ void __launch_bounds__(kCThreads, 1)
             if (s_last[x]) {
               __threadfence();
               if (t == 0) *ctr = 0ull;  // (no other block will look; a replayed graph uses the tag again)
+              if (pc.b2 == pc.b1 + 1) {  // two pieces, the usual unit: all loads first
+                const int oc = b == pc.b1 ? pc.b2 : pc.b1;
+                const float2 om = __ldcg(pc.ml(oc, t));
+#pragma unroll 1
+                for (int ch = 0; ch < D / 64; ++ch) {
+                  float4 q[16];
+#pragma unroll
+                  for (int v = 0; v < 16; ++v) q[v] = __ldcg(pc.acc(oc, t, ch * 64 + 4 * v));
+                  const float mx = fmaxf(m, om.x);
+                  const float wo = piece_weight(om.x, mx), ww = piece_weight(m, mx);
+                  const float ls = b == pc.b1 ? fmaf(wo, om.y, ww * l) : fmaf(ww, l, wo * om.y);
+                  const float inv = 1.f / ls;
+#pragma unroll
+                  for (int hc = 0; hc < 2; ++hc) {
+                    float o[32];
+                    tmem_ld32(tm_o + ch * 64 + hc * 32, o);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int v = 0; v < 32; ++v) {
+                      const float4 qq = q[8 * hc + v / 4];
+                      const float other = v % 4 == 0 ? qq.x : v % 4 == 1 ? qq.y : v % 4 == 2 ? qq.z : qq.w;
+                      o[v] = b == pc.b1 ? fmaf(wo, other, ww * o[v]) : fmaf(ww, o[v], wo * other);
+                    }
+                    if (live) store_row32<T>(orow + ch * 64 + hc * 32, o, inv);
+                  }
+                }
+              } else {
               float mx = m;
               for (int c = pc.b1; c <= pc.b2; ++c)
-                if (c != b) mx = fmaxf(mx, __ldcg(reinterpret_cast<const float2 *>(pc.at(c)) + t).x);
+                if (c != b) mx = fmaxf(mx, __ldcg(pc.ml(c, t)).x);
               float ls = 0.f;
               for (int c = pc.b1; c <= pc.b2; ++c) {
-                const float2 ml = c == b ? make_float2(m, l)
-                                         : __ldcg(reinterpret_cast<const float2 *>(pc.at(c)) + t);
+                const float2 ml = c == b ? make_float2(m, l) : __ldcg(pc.ml(c, t));
                 ls = fmaf(piece_weight(ml.x, mx), ml.y, ls);
               }
               const float inv = 1.f / ls;
-              T *orow = out + (row0 + tok) * out_stride + (long long)(u.g * G + (t - tok * G)) * D;
 #pragma unroll 1
               for (int ch = 0; ch < D / 32; ++ch) {
                 float o[32], acc[32];
@@ -615,12 +652,10 @@ __global__ void __launch_bounds__(kCThreads, 1)
 #pragma unroll
                     for (int v = 0; v < 32; ++v) acc[v] = fmaf(w, o[v], acc[v]);
                   } else {
-                    const float *ps = pc.at(c);
-                    const float w = piece_weight(__ldcg(reinterpret_cast<const float2 *>(ps) + t).x, mx);
-                    const float4 *p4 = reinterpret_cast<const float4 *>(ps + 2 * kCM + (size_t)t * D + ch * 32);
                     float4 q[8];
 #pragma unroll
-                    for (int v = 0; v < 8; ++v) q[v] = __ldcg(p4 + v);
+                    for (int v = 0; v < 8; ++v) q[v] = __ldcg(pc.acc(c, t, ch * 32 + 4 * v));
+                    const float w = piece_weight(__ldcg(pc.ml(c, t)).x, mx);
 #pragma unroll
                     for (int v = 0; v < 8; ++v) {
                       acc[4 * v] = fmaf(w, q[v].x, acc[4 * v]);
@@ -630,31 +665,21 @@ __global__ void __launch_bounds__(kCThreads, 1)
                     }
                   }
                 }
-                if (live) {
-                  uint4 *o4 = reinterpret_cast<uint4 *>(orow + ch * 32);
-#pragma unroll
-                  for (int v = 0; v < 4; ++v)
-                    o4[v] = make_uint4(pack_pair<T>(acc[8 * v] * inv, acc[8 * v + 1] * inv),
-                                       pack_pair<T>(acc[8 * v + 2] * inv, acc[8 * v + 3] * inv),
-                                       pack_pair<T>(acc[8 * v + 4] * inv, acc[8 * v + 5] * inv),
-                                       pack_pair<T>(acc[8 * v + 6] * inv, acc[8 * v + 7] * inv));
-                }
+                if (live) store_row32<T>(orow + ch * 32, acc, inv);
+              }
               }
             } else {
-              float *sl = const_cast<float *>(pc.at(b));
 #pragma unroll 1
               for (int ch = 0; ch < D / 32; ++ch) {
                 float o[32];
                 tmem_ld32(tm_o + ch * 32, o);
                 tmem_wait_ld();
-                if (live) {
-                  float4 *o4 = reinterpret_cast<float4 *>(sl + 2 * kCM + (size_t)t * D + ch * 32);
 #pragma unroll
-                  for (int v = 0; v < 8; ++v)
-                    __stcg(o4 + v, make_float4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]));
-                }
+                for (int v = 0; v < 8; ++v)
+                  __stcg(pc.acc(b, t, ch * 32 + 4 * v),
+                         make_float4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]));
               }
-              if (live) __stcg(reinterpret_cast<float2 *>(sl) + t, make_float2(m, l));
+              __stcg(pc.ml(b, t), make_float2(m, l));
               __threadfence();  // the partial is visible GPU-wide before it counts
               if (!wg_barrier()) {
                 failed = true;
@@ -673,29 +698,30 @@ __global__ void __launch_bounds__(kCThreads, 1)
               if (s_last[x]) {
                 // (the others finished in the meantime: all pieces from memory)
                 __threadfence();
-                for (int e = t; e < rows * (D / 4); e += kCM) {
-                  const int r = e / (D / 4), d = (e - r * (D / 4)) * 4;
-                  float mx = neg_inf_f();
-                  for (int c = pc.b1; c <= pc.b2; ++c)
-                    mx = fmaxf(mx, __ldcg(reinterpret_cast<const float2 *>(pc.at(c)) + r).x);
-                  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-                  float ls = 0.f;
+                float mx = neg_inf_f(), ls = 0.f;
+                for (int c = pc.b1; c <= pc.b2; ++c) mx = fmaxf(mx, __ldcg(pc.ml(c, t)).x);
+                for (int c = pc.b1; c <= pc.b2; ++c) {
+                  const float2 ml = __ldcg(pc.ml(c, t));
+                  ls = fmaf(piece_weight(ml.x, mx), ml.y, ls);
+                }
+                const float inv = 1.f / ls;
+#pragma unroll 1
+                for (int ch = 0; ch < D / 32; ++ch) {
+                  float acc[32];
+#pragma unroll
+                  for (int v = 0; v < 32; ++v) acc[v] = 0.f;
                   for (int c = pc.b1; c <= pc.b2; ++c) {
-                    const float *ps = pc.at(c);
-                    const float2 ml = __ldcg(reinterpret_cast<const float2 *>(ps) + r);
-                    const float4 v = __ldcg(reinterpret_cast<const float4 *>(ps + 2 * kCM + (size_t)r * D + d));
-                    const float w = piece_weight(ml.x, mx);
-                    ls = fmaf(w, ml.y, ls);
-                    acc.x = fmaf(w, v.x, acc.x);
-                    acc.y = fmaf(w, v.y, acc.y);
-                    acc.z = fmaf(w, v.z, acc.z);
-                    acc.w = fmaf(w, v.w, acc.w);
+                    const float w = piece_weight(__ldcg(pc.ml(c, t)).x, mx);
+#pragma unroll
+                    for (int v = 0; v < 8; ++v) {
+                      const float4 q = __ldcg(pc.acc(c, t, ch * 32 + 4 * v));
+                      acc[4 * v] = fmaf(w, q.x, acc[4 * v]);
+                      acc[4 * v + 1] = fmaf(w, q.y, acc[4 * v + 1]);
+                      acc[4 * v + 2] = fmaf(w, q.z, acc[4 * v + 2]);
+                      acc[4 * v + 3] = fmaf(w, q.w, acc[4 * v + 3]);
+                    }
                   }
-                  const float inv = 1.f / ls;
-                  const int tk = r / G;
-                  T *p = out + (row0 + tk) * out_stride + (long long)(u.g * G + (r - tk * G)) * D + d;
-                  *reinterpret_cast<uint2 *>(p) = make_uint2(pack_pair<T>(acc.x * inv, acc.y * inv),
-                                                             pack_pair<T>(acc.z * inv, acc.w * inv));
+                  if (live) store_row32<T>(orow + ch * 32, acc, inv);
                 }
               }
             }
