@@ -53,6 +53,12 @@ __device__ __forceinline__ unsigned launch_tag(unsigned host_tag, unsigned epoch
   return t != 0u ? t : 0x5BD1E995u;
 }
 
+__device__ __forceinline__ unsigned long long ld_acquire_u64(const unsigned long long *p) {
+  unsigned long long v;
+  asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
+  return v;
+}
+
 // A block gives up the call: stop every role of the block, report it, and
 // move the workspace epoch on (see launch_tag).
 __device__ __forceinline__ void give_up(volatile int *abort, int *d_status, unsigned *epoch) {

@@ -66,16 +66,68 @@ struct RGeo {
 
 // Workspace: 256 bytes (epoch), a counter per block, then per block two
 // partial slots (0: a unit begun in an earlier range, 1: one begun here and
-// not finished), each kRRows float2 (m, l) and kRRows x D floats.
+// not finished) as the threads hold them: a float4 (m, l, m, l) of every
+// thread's two rows, then the threads' accumulators, a float4 of all threads
+// after the other.
+__host__ __device__ constexpr size_t rows_slot_floats(int D) {
+  return (size_t)kRWarps * 32 * 4 * (1 + D / 8);
+}
 inline size_t rows_workspace_bytes(int D) {
   return 256 + (size_t)kPagedMaxBlocks * 8 +
-         2 * (size_t)kPagedMaxBlocks * paged_slot_floats(kRRows, D) * 4;
+         2 * (size_t)kPagedMaxBlocks * rows_slot_floats(D) * 4;
 }
 
-__device__ __noinline__ void merge_pieces_out_of_line(const float *slots, size_t stride, int at,
-                                                      int r, int b1, int b2, float4 &acc,
-                                                      float &l) {
-  merge_pieces(slots, stride, at, r, b1, b2, acc, l);
+// A thread's rows joined over a unit's pieces (ranges b1 .. b2, the first in
+// its slot 1, the others in their slots 0): the largest m first, then weighted
+// sums in range order, whichever block joins.  Piece `own` is in registers
+// (w), the others come from the workspace; own = -1: all of them.  Leaves
+// the joined accumulators in w.o and the row sums in w.l.
+template <int D>
+__device__ __forceinline__ void join_pieces(WarpRows<float, D> &w, const float *slots, int b1,
+                                            int b2, int own) {
+  constexpr int kThreads = kRWarps * 32;
+  auto slot = [&](int c) {
+    return reinterpret_cast<const float4 *>(slots + (2 * (size_t)c + (c == b1 ? 1 : 0)) *
+                                                        rows_slot_floats(D)) + threadIdx.x;
+  };
+  const float4 mine = make_float4(w.m[0], w.l[0], w.m[1], w.l[1]);
+  float mx[2] = {neg_inf_f(), neg_inf_f()};
+  for (int c = b1; c <= b2; ++c) {
+    const float4 ml = c == own ? mine : __ldcg(slot(c));
+    mx[0] = fmaxf(mx[0], ml.x);
+    mx[1] = fmaxf(mx[1], ml.z);
+  }
+  const float mz[2] = {mx[0] == neg_inf_f() ? 0.f : mx[0], mx[1] == neg_inf_f() ? 0.f : mx[1]};
+  float acc[D / 8][4];
+#pragma unroll
+  for (int j = 0; j < D / 8; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
+  float ls[2] = {0.f, 0.f};
+  for (int c = b1; c <= b2; ++c) {
+    float4 v[D / 8];
+    const float4 ml = c == own ? mine : __ldcg(slot(c));
+#pragma unroll
+    for (int j = 0; j < D / 8; ++j)
+      v[j] = c == own ? make_float4(w.o[j][0], w.o[j][1], w.o[j][2], w.o[j][3])
+                      : __ldcg(slot(c) + (j + 1) * kThreads);
+    const float wt[2] = {ex2f(ml.x - mz[0]), ex2f(ml.z - mz[1])};
+    ls[0] = fmaf(wt[0], ml.y, ls[0]);  // (a NaN sum stays one also under a zero weight)
+    ls[1] = fmaf(wt[1], ml.w, ls[1]);
+#pragma unroll
+    for (int j = 0; j < D / 8; ++j) {
+      acc[j][0] = fmaf(wt[0], v[j].x, acc[j][0]);
+      acc[j][1] = fmaf(wt[0], v[j].y, acc[j][1]);
+      acc[j][2] = fmaf(wt[1], v[j].z, acc[j][2]);
+      acc[j][3] = fmaf(wt[1], v[j].w, acc[j][3]);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < D / 8; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) w.o[j][e] = acc[j][e];
+  w.l[0] = ls[0];
+  w.l[1] = ls[1];
 }
 
 template <int D, bool kPoll>
@@ -243,60 +295,59 @@ __global__ void __launch_bounds__(kRThreads, 1)
       }
       w.finish();
       if (poison) w.l[0] = w.l[1] = __int_as_float(0x7fc00000);
-      const bool whole = f.t_hi - f.t_lo == f.nt;
-      float *sl = slots + (2 * (size_t)b + (f.t_lo == 0 ? 1 : 0)) * paged_slot_floats(kRRows, D);
-      float *sacc = sl + 2 * kRRows;
       float *orow = out + (long long)(f.s.row0 + f.tok0) * out_stride + (long long)u.g * G * D;
-      if (any_rows) {
+      bool write = f.t_hi - f.t_lo == f.nt;  // the whole unit is here, or joined here
+      if (!write) {
+        // the ranges of the unit's first and last tile; every range between has some
+        const int b1 = cut.at(f.k0);
+        const int b2 = cut.at(f.k0 + (long long)(f.nt - 1) * C::KT);
+        unsigned long long *ctr = counters + b1;
+        const unsigned add = (unsigned)(f.t_hi - f.t_lo);
+        // usually the other pieces were finished long ago: then this block
+        // joins them with the accumulators it still holds
+        if (threadIdx.x == 0) {
+          const unsigned long long v = ld_acquire_u64(ctr);
+          *s_last = (unsigned)(v >> 32) == tag && (unsigned)v + add == (unsigned)f.nt;
+        }
+        if (!consumers_barrier()) return;
+        write = *s_last != 0;
+        if (write) {
+          __threadfence();
+          if (threadIdx.x == 0) *ctr = 0ull;  // (a replayed graph uses the tag again)
+          join_pieces<D>(w, slots, b1, b2, b);
+        } else {
+          float4 *sl = reinterpret_cast<float4 *>(slots + (2 * (size_t)b + (f.t_lo == 0 ? 1 : 0)) *
+                                                              rows_slot_floats(D)) + threadIdx.x;
+          __stcg(sl, make_float4(w.m[0], w.l[0], w.m[1], w.l[1]));
+#pragma unroll
+          for (int j = 0; j < D / 8; ++j)
+            __stcg(sl + (j + 1) * kRWarps * 32, make_float4(w.o[j][0], w.o[j][1], w.o[j][2], w.o[j][3]));
+          __threadfence();  // the partial is visible GPU-wide before it counts
+          if (!consumers_barrier()) return;
+          if (threadIdx.x == 0) {
+            const unsigned before = tagged_add(ctr, add, tag, d_status, epoch);
+            const bool last = before != 0xffffffffu && before + add == (unsigned)f.nt;
+            if (last) *ctr = 0ull;
+            *s_last = last;
+          }
+          if (!consumers_barrier()) return;
+          write = *s_last != 0;
+          if (write) {
+            __threadfence();
+            join_pieces<D>(w, slots, b1, b2, -1);
+          }
+        }
+        if (!consumers_barrier()) return;  // (s_last has been read)
+      }
+      if (write && any_rows) {
         const float inv[2] = {1.f / w.l[0], 1.f / w.l[1]};
         w.each([&](int hh, int d, const float(&v)[4]) {
           const int r = 16 * warp + lane / 4 + 8 * hh;
           if (r >= rows) return;
-          if (whole) {
-            const int tok = r / G;
-            *reinterpret_cast<float4 *>(orow + (long long)tok * out_stride + (r - tok * G) * D + d) =
-                make_float4(v[0] * inv[hh], v[1] * inv[hh], v[2] * inv[hh], v[3] * inv[hh]);
-          } else {
-            __stcg(reinterpret_cast<float4 *>(sacc + (size_t)r * D + d),
-                   make_float4(v[0], v[1], v[2], v[3]));
-          }
+          const int tok = r / G;
+          *reinterpret_cast<float4 *>(orow + (long long)tok * out_stride + (r - tok * G) * D + d) =
+              make_float4(v[0] * inv[hh], v[1] * inv[hh], v[2] * inv[hh], v[3] * inv[hh]);
         });
-        if (!whole && (lane & 3) == 0) {
-#pragma unroll
-          for (int hh = 0; hh < 2; ++hh) {
-            const int r = 16 * warp + lane / 4 + 8 * hh;
-            if (r < rows) __stcg(reinterpret_cast<float2 *>(sl) + r, make_float2(w.m[hh], w.l[hh]));
-          }
-        }
-      }
-      if (!whole) {
-        __threadfence();  // the partial is visible GPU-wide before it counts
-        if (!consumers_barrier()) return;
-        // the ranges of the unit's first and last tile; every range between has some
-        const int b1 = cut.at(f.k0);
-        const int b2 = cut.at(f.k0 + (long long)(f.nt - 1) * C::KT);
-        if (threadIdx.x == 0) {
-          const unsigned add = (unsigned)(f.t_hi - f.t_lo);
-          const unsigned before = tagged_add(counters + b1, add, tag, d_status, epoch);
-          const bool last = before != 0xffffffffu && before + add == (unsigned)f.nt;
-          if (last) counters[b1] = 0ull;  // a replayed graph uses the same tag again
-          *s_last = last;
-        }
-        if (!consumers_barrier()) return;
-        if (*s_last) {
-          __threadfence();
-          for (int e = threadIdx.x; e < rows * (D / 4); e += kRWarps * 32) {
-            const int r = e / (D / 4), d = (e - r * (D / 4)) * 4;
-            float4 acc;
-            float ls;
-            merge_pieces_out_of_line(slots, paged_slot_floats(kRRows, D), 2 * kRRows + r * D + d, r,
-                                     b1, b2, acc, ls);
-            const float inv = 1.f / ls;
-            const int tok = r / G;
-            *reinterpret_cast<float4 *>(orow + (long long)tok * out_stride + (r - tok * G) * D + d) =
-                make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-          }
-        }
       }
     }
     if (!next_unit(pa, u, f, ln)) break;

@@ -29,7 +29,8 @@
 // everything 403 us -- beside eight busy softmax warps each product took 143
 // cycles to issue instead of 67; issued by an elected lane of a converged
 // warp 365 us -- now its polling of six barriers, 140 cycles a look, set the
-// pace; with two issuing warps that wait in a fixed order XXX us.  P laid over
+// pace; with two issuing warps that wait in a fixed order 312 us;
+// then 286 us by what blocks do at the ends of units (below).  P laid over
 // S with a first half of P V issued early: 477 us (more barriers to poll).
 //
 // The softmax keeps a reference maximum that moves only when a row's maximum
@@ -138,12 +139,6 @@ __device__ __forceinline__ void store_row32(T *p, const float (&o)[32], float in
                        pack_pair<T>(o[8 * v + 2] * inv, o[8 * v + 3] * inv),
                        pack_pair<T>(o[8 * v + 4] * inv, o[8 * v + 5] * inv),
                        pack_pair<T>(o[8 * v + 6] * inv, o[8 * v + 7] * inv));
-}
-
-__device__ __forceinline__ unsigned long long ld_acquire_u64(const unsigned long long *p) {
-  unsigned long long v;
-  asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
-  return v;
 }
 
 // The pieces of a unit's tile: those of ranges b1 .. b2, the first in its
