@@ -678,17 +678,16 @@ def _call_device(dev: int, where: str) -> None:
         raise ValueError(f"{where}: the tensors are on device {dev}, which is not the current one")
 
 
-def _rows(t: torch.Tensor, name: str, shape, dtype, dev: int):
-    """Pointer and row stride of a tensor [rows, heads, D] whose rows are contiguous."""
-    if t.dtype is not dtype or t.get_device() != dev or t.shape != shape:
-        raise TypeError(f"{name}: need a {dtype} tensor {list(shape)} on device {dev}, got "
-                        f"{tuple(t.shape)} {t.dtype} {t.device}")
-    if t.is_contiguous():
-        return t.data_ptr(), shape[1] * shape[2]
-    s0, s1, s2 = t.stride()
-    if s2 != 1 or (s1 != shape[2] and shape[1] > 1):
-        raise TypeError(f"{name}: the [heads, D] rows must be contiguous, got strides {t.stride()}")
-    return t.data_ptr(), s0
+def _bad_rows(where: str, dtype, dev: int, **tensors) -> None:
+    """Raises for the first (tensor, shape) that is not [rows, heads, D] as the call needs it."""
+    for name, (t, shape) in tensors.items():
+        if t.dtype is not dtype or t.get_device() != dev or t.shape != shape:
+            raise TypeError(f"{where}: {name}: need a {dtype} tensor {list(shape)} on device {dev}, "
+                            f"got {tuple(t.shape)} {t.dtype} {t.device}")
+        s = t.stride()
+        if s[2] != 1 or (s[1] != shape[2] and shape[1] > 1):
+            raise TypeError(f"{where}: {name}: the [heads, D] rows must be contiguous, got strides {s}")
+    raise AssertionError(where)
 
 
 def kvs_rope_frequencies(rot_dim, base=10000.0, kind=KVS_ROPE_PLAIN, factor=1.0, original_len=0.0,
@@ -710,22 +709,34 @@ def kvs_rope_scatter_paged(q, k, v, q_out, cache, batch, inv_freq, interleaved=F
     to q_out (q itself is fine), rotated k and plain v into the pages of a PagedCache.  Rows may
     be strided (column blocks of one matrix).  The head's first 2 * inv_freq.numel() elements
     turn, the rest is copied."""
-    dev, dt, N, D = cache.device_index, cache.dtype, batch.num_rows, cache.head_dim
-    _call_device(dev, "kvs_rope_scatter_paged")
-    if batch.device_index != dev:
-        raise ValueError("kvs_rope_scatter_paged: cache and batch on different devices")
+    dev, dt, N, D, Hkv = (cache.device_index, cache.dtype, batch.num_rows, cache.head_dim,
+                          cache.num_kv_heads)
+    if dev != _get_device() or batch.device_index != dev:
+        raise ValueError("kvs_rope_scatter_paged: cache and batch must be on the current device")
     H = q.shape[1] if q.dim() == 3 else -1
     if inv_freq.dtype is not torch.float32 or inv_freq.get_device() != dev or \
             inv_freq.dim() != 1 or not inv_freq.is_contiguous():
         raise TypeError("inv_freq: need a contiguous float32 vector on the tensors' device")
-    of_q, of_kv = (N, H, D), (N, cache.num_kv_heads, D)
-    qp, qs = _rows(q, "q", of_q, dt, dev)
-    kp, ks = _rows(k, "k", of_kv, dt, dev)
-    vp, vs = _rows(v, "v", of_kv, dt, dev)
-    op, os_ = _rows(q_out, "q_out", of_q, dt, dev)
-    rc = cache._call[1](qp, qs, kp, ks, vp, vs, op, os_, cache._addr, batch._addr,
-                        inv_freq.data_ptr(), H, 2 * inv_freq.numel(), 1 if interleaved else 0,
-                        scale, 0 if d_status is None else _status_ptr(d_status),
+    of_q, of_kv = (N, H, D), (N, Hkv, D)
+    if not (q.dtype is k.dtype is v.dtype is q_out.dtype is dt and
+            q.get_device() == k.get_device() == v.get_device() == q_out.get_device() == dev and
+            q.shape == of_q == q_out.shape and k.shape == of_kv == v.shape):
+        _bad_rows("kvs_rope_scatter_paged", dt, dev, q=(q, of_q), k=(k, of_kv), v=(v, of_kv),
+                  q_out=(q_out, of_q))
+    qs, ks, vs, os_ = q.stride(), k.stride(), v.stride(), q_out.stride()
+    if not (qs[2] == ks[2] == vs[2] == os_[2] == 1 and (qs[1] == os_[1] == D or H == 1) and
+            (ks[1] == vs[1] == D or Hkv == 1)):
+        _bad_rows("kvs_rope_scatter_paged", dt, dev, q=(q, of_q), k=(k, of_kv), v=(v, of_kv),
+                  q_out=(q_out, of_q))
+    if N > 1:
+        qs, ks, vs, os_ = qs[0], ks[0], vs[0], os_[0]
+    else:  # (the stride of a single row says nothing)
+        qs = os_ = H * D
+        ks = vs = Hkv * D
+    rc = cache._call[1](q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, q_out.data_ptr(), os_,
+                        cache._addr, batch._addr, inv_freq.data_ptr(), H, 2 * inv_freq.numel(),
+                        1 if interleaved else 0, scale,
+                        0 if d_status is None else _status_ptr(d_status),
                         _get_stream(dev) if stream is None else _stream(stream))
     if rc != KVS_OK:
         raise KvsError(rc, "kvs_rope_scatter_paged")
@@ -744,10 +755,9 @@ def paged_attention_workspace(cache, batch, num_heads, device=None):
 def kvs_paged_attention(q, cache, batch, out, workspace=None, d_status=None, stream=None):
     """out [num_rows, H, D] = attention of every new token of a PagedBatch over its sequence's
     pages, rows 0 .. its own position."""
-    dev, dt = cache.device_index, cache.dtype
-    _call_device(dev, "kvs_paged_attention")
-    if batch.device_index != dev:
-        raise ValueError("kvs_paged_attention: cache and batch on different devices")
+    dev, dt, N, D = cache.device_index, cache.dtype, batch.num_rows, cache.head_dim
+    if dev != _get_device() or batch.device_index != dev:
+        raise ValueError("kvs_paged_attention: cache and batch must be on the current device")
     if workspace is None:
         raise ValueError("kvs_paged_attention: pass a workspace (see "
                          "binding.paged_attention_workspace)")
@@ -755,11 +765,20 @@ def kvs_paged_attention(q, cache, batch, out, workspace=None, d_status=None, str
         raise TypeError("kvs_paged_attention: the workspace must be a contiguous tensor on the "
                         "tensors' device")
     H = q.shape[1] if q.dim() == 3 else -1
-    shape = (batch.num_rows, H, cache.head_dim)
-    qp, qs = _rows(q, "q", shape, dt, dev)
-    op, os_ = _rows(out, "out", shape, dt, dev)
-    rc = cache._call[0](qp, qs, cache._addr, batch._addr, op, os_, H, workspace.data_ptr(),
-                        workspace.nbytes, 0 if d_status is None else _status_ptr(d_status),
+    shape = (N, H, D)
+    if not (q.dtype is out.dtype is dt and q.get_device() == out.get_device() == dev and
+            q.shape == shape == out.shape):
+        _bad_rows("kvs_paged_attention", dt, dev, q=(q, shape), out=(out, shape))
+    qs, os_ = q.stride(), out.stride()
+    if not (qs[2] == os_[2] == 1 and (qs[1] == os_[1] == D or H == 1)):
+        _bad_rows("kvs_paged_attention", dt, dev, q=(q, shape), out=(out, shape))
+    if N > 1:
+        qs, os_ = qs[0], os_[0]
+    else:  # (the stride of a single row says nothing)
+        qs = os_ = H * D
+    rc = cache._call[0](q.data_ptr(), qs, cache._addr, batch._addr, out.data_ptr(), os_, H,
+                        workspace.data_ptr(), workspace.nbytes,
+                        0 if d_status is None else _status_ptr(d_status),
                         _get_stream(dev) if stream is None else _stream(stream))
     if rc != KVS_OK:
         raise KvsError(rc, "kvs_paged_attention")
