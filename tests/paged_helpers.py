@@ -37,9 +37,11 @@ def within(got, ref, bound, where=""):
 class Paged:
     """A batch of sequences (n new tokens from position p each) over pages in
     shuffled order.  Pages' rows that hold no live key are NaN, and so are the
-    pages that no sequence uses; the table's unused entries are out of range."""
+    pages that no sequence uses; the table's unused entries (columns of them behind
+    the longest sequence) are out of range."""
 
-    def __init__(self, n, p, H, Hkv, D, dtype, page, seed=0, spare=3, tail_rows=0):
+    def __init__(self, n, p, H, Hkv, D, dtype, page, seed=0, spare=3, tail_rows=0,
+                 columns=2):
         g = torch.Generator(device=DEV)
         g.manual_seed(seed)
         rng = np.random.default_rng(seed)
@@ -49,7 +51,7 @@ class Paged:
         need = [-(-(a + b) // page) if a else 0 for a, b in zip(n, p)]
         total = sum(need) + spare
         order = rng.permutation(total)
-        self.table_host = np.full((M, max(need + [1]) + 2), -1, np.int32)
+        self.table_host = np.full((M, max(need + [1]) + columns), -1, np.int32)
         at = 0
         for i in range(M):
             self.table_host[i, :need[i]] = order[at:at + need[i]]

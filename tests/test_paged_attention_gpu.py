@@ -69,6 +69,83 @@ def test_decode_over_every_block(dtype, n, p):
         assert torch.equal(b.attend(), first)
 
 
+# A decode step chooses its kernel by the page table's width: a table with room for 2^19 keys a
+# sequence takes the one for long caches, also when the live keys are few.
+WIDE = 2 ** 19
+
+
+@pytest.mark.parametrize("batch", [b for b in BATCHES if max(BATCHES[b][0]) <= 2])
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("H,Hkv,D,page", [(4, 2, 64, 16), (14, 2, 64, 64), (40, 8, 128, 32),
+                                          (8, 1, 128, 128), (3, 3, 64, 32), (6, 2, 128, 256)])
+def test_decode_with_room_for_long_sequences(batch, dtype, H, Hkv, D, page):
+    n, p = BATCHES[batch]
+    b = Paged(n, p, H, Hkv, D, dtype, page, seed=len(batch) * 1000 + H * 10 + page,
+              columns=WIDE // page)
+    b.check(b.attend(), f"{batch} {dtype} {H}/{Hkv} {D} {page}")
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("H,Hkv,D,most", [(16, 8, 64, 250), (16, 8, 64, 1100), (32, 8, 128, 120),
+                                          (8, 8, 128, 400), (14, 2, 64, 700)])
+def test_decode_of_many_sequences(dtype, H, Hkv, D, most):
+    """More (sequence, kv head) pairs than blocks run at once; some sequences are empty."""
+    n = [0 if i % 11 == 5 else 2 if i % 7 == 3 else 1 for i in range(83)]
+    p = [(i * 37) % (most - 2) for i in range(83)]
+    b = Paged(n, p, H, Hkv, D, dtype, 16, seed=most + D)
+    first = b.attend()
+    b.check(first)
+    for _ in range(3):
+        assert torch.equal(b.attend(), first)
+
+
+@pytest.mark.parametrize("columns", [2, WIDE // 32])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_decode_bad_input_and_short_waits(dtype, columns):
+    """Bad pages and positions poison their sequence alone, and waits that run out are told."""
+    n, p = [1, 2, 1] * 9, [5000, 3000, 2000, 300, 200, 100, 0, 1, 40] * 3
+    for what in ("page", "position"):
+        b = Paged(n, p, 8, 2, 64, dtype, 32, seed=19, columns=columns)
+        (b.page_table[4] if what == "page" else b.positions[4:5])[:1] = 2 ** 31 - 1
+        out = b.attend()
+        assert int(b.status.item()) == (B.KVS_ERR_PAGE if what == "page" else B.KVS_ERR_POSITION)
+        ref, bound = b.reference()
+        a, e = int(b.offsets_host[4]), int(b.offsets_host[5])
+        assert out[a:e].isnan().all()
+        keep = [r for r in range(sum(n)) if not a <= r < e]
+        within(out[keep], ref[keep], bound[keep], what)
+    b = Paged(n, p, 8, 2, 64, dtype, 32, seed=20, columns=columns)
+    prev = B.kvs_set_wait_limit_ns(0)
+    try:
+        b.attend()
+        torch.cuda.synchronize()
+        assert int(b.status.item()) == B.KVS_ERR_TIMEOUT
+    finally:
+        B.kvs_set_wait_limit_ns(prev)
+    b.status.zero_()
+    b.check(b.attend())
+
+
+def test_wide_decode_graph_and_two_streams():
+    """The kernel for long caches: replays of a capture, and two streams at once."""
+    a = Paged([1] * 8, [4000 + 3 * i for i in range(8)], 32, 8, 128, "f16", 64, seed=21,
+              columns=WIDE // 64)
+    b = Paged([1, 2, 1], [9000, 10, 700], 16, 4, 64, "f32", 32, seed=22, columns=WIDE // 32)
+    torch.cuda.synchronize()
+    s, t = torch.cuda.Stream(), torch.cuda.Stream()
+    oa, ob = torch.empty_like(a.q), torch.empty_like(b.q)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        a.attend(out=oa)
+    for _ in range(5):
+        with torch.cuda.stream(s):
+            graph.replay()
+        b.attend(out=ob, stream=t)
+    torch.cuda.synchronize()
+    a.check(oa)
+    b.check(ob)
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 def test_large_scores(dtype):
     """Scores of some hundreds: the running maximum moves often and far."""
