@@ -15,8 +15,9 @@
 //   warp 9          issues O_x += P_x V (P from TMEM; V as the copies leave
 //                   it: head elements contiguous, which is the MN-major
 //                   operand, so nothing is transposed)
-//   warp 10         copies: Q by tensor maps over (head element, head of the
-//                   group, row), K and V page by page, two stages each
+//   warp 10         walks the units and describes each to the others; copies:
+//                   Q by tensor maps over (head element, head of the group,
+//                   row), K and V page by page, two stages each
 // TMEM columns: S [0, 128), used by both tiles in turn; P_A [128, 192) and
 // P_B [192, 256) in 16 bits; O_A, O_B behind.
 //
@@ -54,10 +55,26 @@ constexpr int kCM = 128;                 // rows of a tile (MMA M)
 constexpr int kCN = 128;                 // keys of a tile
 constexpr int kCMmaWarp = 8, kCPvWarp = 9, kCCopyWarp = 10;
 constexpr int kCThreads = 11 * 32;
-constexpr int kCFix = 128;               // fixed price of a unit, in cost rows
+// A unit's fixed price and the shortest range worth a block, in cost rows (keys
+// of a unit): prompts of 2048 tokens, H 32 / 8, took 61 us at a price of 128
+// (and a unit's start and end 1.5 us dearer than now), 49 at 128, 44.7 at 384,
+// 45.7 at 512; 512 tokens 26.6 us at a shortest range of 256, 23.0 at 768;
+// 20 tokens 31 us at 1024, 11 at 768 or less.
+constexpr int kCFix = 384;
+constexpr int kCMinRange = 768;
 constexpr float kCRescale = 8.f;
 constexpr uint32_t kCTmemCols = 512;
 constexpr int kCMaxDevices = 64;
+
+// What the copy warp tells the others of a unit of this block.
+struct CUnit {
+  int p, row0, tok0, ntok;  // position, first row of the sequence; tokens of the unit
+  int t_lo, t_hi;           // key tiles of this block; t_lo == t_hi: no further unit
+  int g;                    // kv head
+  int bad;                  // a page of it is bad
+  int b1, b2[2], pad;       // blocks of its first key tile and of the last ones of tiles A and B
+};
+constexpr int kCUnits = 4;  // the copy warp is at most so many units ahead
 
 template <int D>
 struct CGeo {
@@ -68,13 +85,15 @@ struct CGeo {
   static constexpr int OFF_Q = 0;                 // Q_A, Q_B
   static constexpr int OFF_K = 2 * TILE;
   static constexpr int OFF_V = OFF_K + KS * TILE;
-  static constexpr int OFF_BAR = OFF_V + VS * TILE;
+  static constexpr int OFF_STAGE = OFF_V + VS * TILE;  // 4 KB a softmax warp: rows on their way out
+  static constexpr int OFF_BAR = OFF_STAGE + 8 * 4096;
   // q, qfree, kfull[KS], kfree[KS], vfull[VS], vfree[VS], vpart, sfull[2],
-  // sread, pfull[2], pvdone[2], wg[2], final[2]
-  static constexpr int NBAR = 2 + 2 * KS + 2 * VS + 1 + 2 + 1 + 6 + 2;
+  // sread, pfull[2], pvdone[2], wg[2], final[2], ufull[kCUnits], ufree[kCUnits]
+  static constexpr int NBAR = 2 + 2 * KS + 2 * VS + 1 + 2 + 1 + 6 + 2 + 2 * kCUnits;
   static constexpr int OFF_TMEM = OFF_BAR + NBAR * 8;
-  static constexpr int OFF_MISC = OFF_TMEM + 8;   // abort, last[2], bad[4], pad
-  static constexpr int NEED = OFF_MISC + 32;
+  static constexpr int OFF_MISC = OFF_TMEM + 8;   // abort, last[2], pad
+  static constexpr int OFF_UNIT = OFF_MISC + 16;  // CUnit [kCUnits]
+  static constexpr int NEED = OFF_UNIT + kCUnits * (int)sizeof(CUnit);
   // all 512 TMEM columns are this block's: more than half of the SM's shared
   // memory keeps a second block away
   static constexpr int SMEM = NEED > 116 * 1024 ? NEED : 116 * 1024;
@@ -129,16 +148,35 @@ __device__ __forceinline__ void tma_q(void *dst, const CUtensorMap *map, int hea
 // 1024) and one tile further on in the lower half's 16-byte pieces.
 constexpr uint32_t kDescHi = 1024u >> 4 | 1u << 14 | 2u << 29;
 
-// 32 columns of a row times inv, rounded to the type.
+// 64 columns of a warp's 32 rows on their way out: a thread puts its own row's
+// into shared memory (16-byte pieces swizzled by the row, so that no access
+// conflicts), then eight threads a row write them.  Straight from the thread
+// that owns the row each store would touch 32 rows (2060 cycles for a tile of
+// 128 x 128, against 700).
 template <typename T>
-__device__ __forceinline__ void store_row32(T *p, const float (&o)[32], float inv) {
-  uint4 *o4 = reinterpret_cast<uint4 *>(p);
+__device__ __forceinline__ void put_row32(unsigned char *stg, int lane, int half,
+                                          const float (&o)[32], float inv) {
 #pragma unroll
   for (int v = 0; v < 4; ++v)
-    o4[v] = make_uint4(pack_pair<T>(o[8 * v] * inv, o[8 * v + 1] * inv),
-                       pack_pair<T>(o[8 * v + 2] * inv, o[8 * v + 3] * inv),
-                       pack_pair<T>(o[8 * v + 4] * inv, o[8 * v + 5] * inv),
-                       pack_pair<T>(o[8 * v + 6] * inv, o[8 * v + 7] * inv));
+    *reinterpret_cast<uint4 *>(stg + lane * 128 + (((4 * half + v) ^ (lane & 7)) * 16)) =
+        make_uint4(pack_pair<T>(o[8 * v] * inv, o[8 * v + 1] * inv),
+                   pack_pair<T>(o[8 * v + 2] * inv, o[8 * v + 3] * inv),
+                   pack_pair<T>(o[8 * v + 4] * inv, o[8 * v + 5] * inv),
+                   pack_pair<T>(o[8 * v + 6] * inv, o[8 * v + 7] * inv));
+}
+// at: where this lane's row starts in out, negative for a row that does not exist
+template <typename T>
+__device__ __forceinline__ void write_rows64(const unsigned char *stg, int lane, T *out,
+                                             long long at, int col) {
+  __syncwarp();
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int r = 4 * k + lane / 8;
+    const long long to = __shfl_sync(0xffffffffu, at, r);
+    const uint4 v = *reinterpret_cast<const uint4 *>(stg + r * 128 + (((lane ^ r) & 7) * 16));
+    if (to >= 0) *reinterpret_cast<uint4 *>(out + to + col + (lane & 7) * 8) = v;
+  }
+  __syncwarp();
 }
 
 // The pieces of a unit's tile: those of ranges b1 .. b2, the first in its
@@ -194,10 +232,12 @@ __global__ void __launch_bounds__(kCThreads, 1)
   uint64_t *pvdone = pfull + 2;      // [2] P V_x done (commit)
   uint64_t *wgbar = pvdone + 2;      // [2] the warps of a warpgroup
   uint64_t *final = wgbar + 2;       // [2] every product S, every P V of the block done (commit)
+  uint64_t *ufull = final + 2;       // [kCUnits] a unit is described
+  uint64_t *ufree = ufull + kCUnits; // [kCUnits] the ten other warps are done with it
+  CUnit *units = reinterpret_cast<CUnit *>(smem + C::OFF_UNIT);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_TMEM);
   volatile int *abort = reinterpret_cast<volatile int *>(smem + C::OFF_MISC);
   volatile int *s_last = abort + 1;  // [2]
-  volatile int *s_bad = abort + 3;   // [4] a bad page in the unit of round rd, at rd % 4
   unsigned *epoch = reinterpret_cast<unsigned *>(ws);
   unsigned long long *counters = reinterpret_cast<unsigned long long *>(ws + 256);
   float *slots = reinterpret_cast<float *>(ws + 256 + (size_t)kPagedMaxBlocks * 16);
@@ -206,7 +246,7 @@ __global__ void __launch_bounds__(kCThreads, 1)
   const int b = blockIdx.x;
   const int TT = kCM / G;  // tokens of a tile
   constexpr uint32_t kTileStep = C::TILE >> 4;  // one tile further on, in a descriptor
-  const Line ln{Hkv, 2 * TT, kCFix, kCN, kCN + kCFix};
+  const Line ln{Hkv, 2 * TT, kCFix, kCN, kCMinRange};
 
   if (threadIdx.x == 0) {
     prefetch_map(&qmap);
@@ -218,6 +258,7 @@ __global__ void __launch_bounds__(kCThreads, 1)
       mbar_init(&wgbar[x], 4);
     }
     mbar_init(sread, 4);
+    for (int j = 0; j < kCUnits; ++j) mbar_init(&ufree[j], 10);
     *abort = 0;
     fence_mbar_init();
   }
@@ -226,47 +267,54 @@ __global__ void __launch_bounds__(kCThreads, 1)
     tmem_relinquish();
   }
   grid_dependency_wait();
-  // bad sequences: status, and NaN rows where the rows are known
-  for (int i = b; i < pa.M; i += gridDim.x) {
-    const PagedSeq s = paged_seq(pa, i);
-    if (s.err != KVS_OK) {
-      if (threadIdx.x == 0) record_status(d_status, s.err);
-      const T nan = from_f32<T>(__int_as_float(0x7fc00000));
-      for (int r = 0; r < s.n; ++r)
-        for (int e = threadIdx.x; e < Hkv * G * D; e += kCThreads)
-          out[(long long)(s.row0 + r) * out_stride + e] = nan;
-    }
-  }
-  const unsigned tag = launch_tag(host_tag, __ldcg(epoch));
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   allow_dependent_launch();
   const uint32_t tmem = *tmem_slot;
-  const Cuts cut = equal_cuts(warp_line_total(pa, ln, lane), ln, gridDim.x);
-  const bool work = cut.R > 0 && b < cut.NS;
-  const long long x0 = work ? cut.start(b) : 0;
-  const long long x1 = work ? cut.start(b + 1) : 0;
-  Unit u{pa.M, 0, 0, 0};
-  if (work) u = warp_unit_at(pa, ln, x0, lane);
-  bool more = work;
-  auto tile_of = [&](const UnitInfo &f, int x) {
+  auto tile_of = [&](const CUnit &f, int x) {
     CTile t;
     t.tok0 = f.tok0 + x * TT;
     t.ntok = min(TT, f.ntok - x * TT);
-    t.nt = t.ntok > 0 ? (f.s.p + t.tok0 + t.ntok + kCN - 1) / kCN : 0;
+    t.nt = t.ntok > 0 ? (f.p + t.tok0 + t.ntok + kCN - 1) / kCN : 0;
     t.lo = min(f.t_lo, t.nt);
     t.hi = min(f.t_hi, t.nt);
     return t;
   };
-  // the next unit of the column with work in it; false at its end
-  auto advance = [&](const UnitInfo &f) { more = next_unit(pa, u, f, ln) && u.base < x1; };
+  // The block's n-th unit, once it is described; false when a wait ran out.
+  auto unit = [&](int n, CUnit &f) -> bool {
+    if (!__all_sync(0xffffffffu, mbar_wait<kPoll>(&ufull[n % kCUnits], (uint32_t)(n / kCUnits) & 1u, abort)))
+      return false;
+    f = units[n % kCUnits];
+    return true;
+  };
+  auto unit_done = [&](int n) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&ufree[n % kCUnits]);
+  };
 
   if (warp == kCCopyWarp) {
     // ======================= copies ==========================================
     int nk = 0, nv = 0;  // K and V tiles issued
     int nq = 0, npart = 0;
     bool ok = true, part_failed = false;
+    const Cuts cut = equal_cuts(warp_line_total(pa, ln, lane), ln, gridDim.x);
+    bool more = cut.R > 0 && b < cut.NS;
+    const long long x0 = more ? cut.start(b) : 0, x1 = more ? cut.start(b + 1) : 0;
+    Unit u{pa.M, 0, 0, 0};
+    if (more) u = warp_unit_at(pa, ln, x0, lane);
+    // Describes a unit, once the one before in the same place is done with.
+    auto describe = [&](int n, const CUnit &f) {
+      if (n >= kCUnits &&
+          !__all_sync(0xffffffffu, mbar_wait<kPoll>(&ufree[n % kCUnits], (uint32_t)(n / kCUnits - 1) & 1u, abort)))
+        return false;
+      if (lane == 0) {
+        units[n % kCUnits] = f;
+        mbar_arrive(&ufull[n % kCUnits]);
+      }
+      __syncwarp();
+      return true;
+    };
     const int R = 1 << box_shift;          // rows of a copy
     const int pieces = kCN >> box_shift;   // copies of a tile's column block
     const uint32_t piece_bytes = (uint32_t)R * 128;
@@ -275,10 +323,18 @@ __global__ void __launch_bounds__(kCThreads, 1)
       if (f.t_lo < f.t_hi) {
         const int32_t *table = pa.page_table + (size_t)u.i * pa.max_pages;
         const int L = f.s.p + f.s.n;
+        CUnit d{f.s.p, f.s.row0, f.tok0, f.ntok, f.t_lo, f.t_hi, u.g, 0, b, {b, b}, 0};
+        if (f.t_hi - f.t_lo < f.nt) {
+          d.b1 = cut.at(f.k0);
+          for (int x = 0; x < 2; ++x) {
+            const int nt = tile_of(d, x).nt;
+            d.b2[x] = nt > 0 ? cut.at(f.k0 + (long long)(nt - 1) * kCN) : d.b1;
+          }
+        }
+        if (!(ok = describe(nq, d))) break;
         if (nq > 0 && !(ok = __all_sync(0xffffffffu, mbar_wait<kPoll>(qfree, (uint32_t)(nq - 1) & 1u, abort))))
           break;
         if (lane == 0) {
-          s_bad[nq & 3] = 0;
           const int tiles = f.ntok > TT ? 2 : 1;
           mbar_arrive_expect_tx(bar_q, (uint32_t)(tiles * C::NB * TT * G * 128));
           for (int x = 0; x < tiles; ++x)
@@ -298,7 +354,7 @@ __global__ void __launch_bounds__(kCThreads, 1)
           int page = mine ? __ldca(table + (key >> pa.page_shift)) : 0;
           if ((unsigned)page >= (unsigned)pa.num_pages) {
             record_status(d_status, KVS_ERR_PAGE);
-            s_bad[(nq - 1) & 3] = 1;
+            *const_cast<volatile int *>(&units[(nq - 1) % kCUnits].bad) = 1;
             page = 0;
           }
           const int row = ((page * Hkv + u.g) << pa.page_shift) + (key & ((1 << pa.page_shift) - 1));
@@ -339,8 +395,9 @@ __global__ void __launch_bounds__(kCThreads, 1)
           }
         }
       }
-      if (ok) advance(f);
+      more = ok && next_unit(pa, u, f, ln) && u.base < x1;
     }
+    if (ok) ok = describe(nq, CUnit{});
     if (lane == 0) {
       if (!ok) give_up(abort, d_status, epoch);
       // every copy issued lands before the block can exit
@@ -364,42 +421,39 @@ __global__ void __launch_bounds__(kCThreads, 1)
     constexpr uint32_t kIdS = idesc16<T>(kCM, kCN, false);
     int gt = 0;       // K tiles of the earlier units
     uint32_t ns = 0;  // S products issued
-    int nq = 0;
     bool ok = true;
     auto wait = [&](uint64_t *bar, uint32_t phase) {
       return ok = __all_sync(0xffffffffu, mbar_wait<kPoll>(bar, phase & 1u, abort)) != 0;
     };
-    while (more && ok) {
-      const UnitInfo f = unit_info(pa, u, ln, x0, x1);
-      if (f.t_lo < f.t_hi) {
-        const CTile ta = tile_of(f, 0), tb = tile_of(f, 1);
-        const int n_x[2] = {ta.hi - ta.lo, tb.hi - tb.lo};  // products of each tile
-        const int n_all = f.t_hi - f.t_lo;                  // K tiles of the unit
-        if (!wait(bar_q, nq)) break;
-        for (int i = 0; i < n_all && ok; ++i, ++gt) {
-          if (!wait(&kfull[gt % KS], gt / KS)) break;
-          const uint32_t bk = warp_uniform(lk + (uint32_t)(gt % KS) * kTileStep);
+    for (int nq = 0; ok; ++nq) {
+      CUnit f;
+      if (!(ok = unit(nq, f)) || f.t_lo == f.t_hi) break;
+      const CTile ta = tile_of(f, 0), tb = tile_of(f, 1);
+      const int n_x[2] = {ta.hi - ta.lo, tb.hi - tb.lo};  // products of each tile
+      const int n_all = f.t_hi - f.t_lo;                  // K tiles of the unit
+      if (!wait(bar_q, nq)) break;
+      for (int i = 0; i < n_all && ok; ++i, ++gt) {
+        if (!wait(&kfull[gt % KS], gt / KS)) break;
+        const uint32_t bk = warp_uniform(lk + (uint32_t)(gt % KS) * kTileStep);
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            if (i >= n_x[x]) continue;
-            if (ns > 0 && !wait(sread, ns - 1u)) break;
-            tc_fence_after();
+        for (int x = 0; x < 2; ++x) {
+          if (i >= n_x[x]) continue;
+          if (ns > 0 && !wait(sread, ns - 1u)) break;
+          tc_fence_after();
 #pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks) {
-              const uint32_t at = (uint32_t)(ks >> 2) * (C::BLK >> 4) + (ks & 3) * 2;
-              mma_f16_warp(tm, lq + (x ? kTileStep : 0u) + at, bk + at, kDescHi, kIdS, ks > 0 ? 1u : 0u);
-            }
-            mma_commit_warp(&sfull[x]);
-            ++ns;
+          for (int ks = 0; ks < D / 16; ++ks) {
+            const uint32_t at = (uint32_t)(ks >> 2) * (C::BLK >> 4) + (ks & 3) * 2;
+            mma_f16_warp(tm, lq + (x ? kTileStep : 0u) + at, bk + at, kDescHi, kIdS, ks > 0 ? 1u : 0u);
           }
-          if (!ok) break;
-          mma_commit_warp(&kfree[gt % KS]);
-          if (i + 1 == n_all) mma_commit_warp(qfree);
+          mma_commit_warp(&sfull[x]);
+          ++ns;
         }
         if (!ok) break;
-        ++nq;
+        mma_commit_warp(&kfree[gt % KS]);
+        if (i + 1 == n_all) mma_commit_warp(qfree);
       }
-      advance(f);
+      if (!ok) break;
+      unit_done(nq);
     }
     if (!ok && lane == 0) give_up(abort, d_status, epoch);
     // every product issued finishes before the block frees the tensor memory
@@ -417,35 +471,34 @@ __global__ void __launch_bounds__(kCThreads, 1)
     auto wait = [&](uint64_t *bar, uint32_t phase) {
       return ok = __all_sync(0xffffffffu, mbar_wait<kPoll>(bar, phase & 1u, abort)) != 0;
     };
-    while (more && ok) {
-      const UnitInfo f = unit_info(pa, u, ln, x0, x1);
-      if (f.t_lo < f.t_hi) {
-        const CTile ta = tile_of(f, 0), tb = tile_of(f, 1);
-        const int n_x[2] = {ta.hi - ta.lo, tb.hi - tb.lo};
-        const int n_all = f.t_hi - f.t_lo;
-        for (int j = 0; j < n_all && ok; ++j, ++gt) {
-          if (!wait(&vfull[gt % VS], gt / VS)) break;
-          const uint32_t bv = warp_uniform(lv + (uint32_t)(gt % VS) * kTileStep);
-          const uint32_t acc = warp_uniform(j > 0 ? 1u : 0u);  // O_x (+)= P_x V
+    for (int nq = 0; ok; ++nq) {
+      CUnit f;
+      if (!(ok = unit(nq, f)) || f.t_lo == f.t_hi) break;
+      const CTile ta = tile_of(f, 0), tb = tile_of(f, 1);
+      const int n_x[2] = {ta.hi - ta.lo, tb.hi - tb.lo};
+      const int n_all = f.t_hi - f.t_lo;
+      for (int j = 0; j < n_all && ok; ++j, ++gt) {
+        if (!wait(&vfull[gt % VS], gt / VS)) break;
+        const uint32_t bv = warp_uniform(lv + (uint32_t)(gt % VS) * kTileStep);
+        const uint32_t acc = warp_uniform(j > 0 ? 1u : 0u);  // O_x (+)= P_x V
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            if (j >= n_x[x]) continue;
-            if (!wait(&pfull[x], pdone[x] + j)) break;
-            tc_fence_after();
+        for (int x = 0; x < 2; ++x) {
+          if (j >= n_x[x]) continue;
+          if (!wait(&pfull[x], pdone[x] + j)) break;
+          tc_fence_after();
 #pragma unroll
-            for (int ks = 0; ks < kCN / 16; ++ks)
-              mma_f16_ts_warp(tm + 2 * kCN + x * D, tm + kCN + x * (kCN / 2) + ks * 8, bv + 128 * ks,
-                              kDescHi, kIdO, ks > 0 ? 1u : acc);
-            mma_commit_warp(&pvdone[x]);
-          }
-          if (!ok) break;
-          mma_commit_warp(&vfree[gt % VS]);
+          for (int ks = 0; ks < kCN / 16; ++ks)
+            mma_f16_ts_warp(tm + 2 * kCN + x * D, tm + kCN + x * (kCN / 2) + ks * 8, bv + 128 * ks,
+                            kDescHi, kIdO, ks > 0 ? 1u : acc);
+          mma_commit_warp(&pvdone[x]);
         }
         if (!ok) break;
-        pdone[0] += n_x[0];
-        pdone[1] += n_x[1];
+        mma_commit_warp(&vfree[gt % VS]);
       }
-      advance(f);
+      if (!ok) break;
+      pdone[0] += n_x[0];
+      pdone[1] += n_x[1];
+      unit_done(nq);
     }
     if (!ok && lane == 0) give_up(abort, d_status, epoch);
     mma_commit_warp(&final[1]);
@@ -460,8 +513,8 @@ __global__ void __launch_bounds__(kCThreads, 1)
     const uint32_t tm_p = tmem + lane_base + kCN + x * (kCN / 2);
     const uint32_t tm_o = tmem + lane_base + 2 * kCN + x * D;
     const float nan = __int_as_float(0x7fc00000);
+    unsigned char *stg = smem + C::OFF_STAGE + warp * 4096;
     int sb = 0;  // S_x products of the earlier units
-    int nq = 0;  // earlier units
     uint32_t wphase = 0;
     bool failed = false;
     auto wg_barrier = [&]() -> bool {  // the warpgroup's four warps, bounded
@@ -471,260 +524,279 @@ __global__ void __launch_bounds__(kCThreads, 1)
       wphase ^= 1u;
       return got;
     };
-    while (more && !failed) {
-      const UnitInfo f = unit_info(pa, u, ln, x0, x1);
-      if (f.t_lo < f.t_hi) {
-        const CTile tl = tile_of(f, x);
-        const int rows = tl.ntok * G;
-        const bool live = t < rows;
-        const int tok = live ? t / G : tl.ntok - 1;
-        const int last = f.s.p + tl.tok0 + tok;  // the row's last key
-        const int first_last = f.s.p + tl.tok0;  // the tile's first row's
-        float m = neg_inf_f(), l = 0.f;
-        for (int n = tl.lo; n < tl.hi; ++n) {
-          const uint32_t ph = (uint32_t)(sb + n - tl.lo) & 1u;
-          if (!__all_sync(0xffffffffu, mbar_wait<kPoll>(&sfull[x], ph, abort))) {
-            failed = true;
-            break;
-          }
-          tc_fence_after();
-          float r[kCN];
-          tmem_ld64(tm_s, *reinterpret_cast<float(*)[64]>(&r[0]));
-          tmem_ld64(tm_s + 64, *reinterpret_cast<float(*)[64]>(&r[64]));
-          tmem_wait_ld();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(sread);  // the other tile's product may have the columns
-          const int key0 = n * kCN;
-          if (key0 + kCN - 1 > first_last) {
-            const int lim = last - key0;  // keys 0..lim of the tile are attended
-#pragma unroll
-            for (int v = 0; v < kCN; ++v) r[v] = v <= lim ? r[v] : neg_inf_f();
-          }
-          float mx[4] = {r[0], r[1], r[2], r[3]};  // four chains (max is exact in any order)
-#pragma unroll
-          for (int v = 4; v < kCN; v += 4) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], r[v + k]);
-          }
-          const float cm = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
-          // the reference maximum moves only when the row's grows by more
-          // than 2^kCRescale: below that P stays in range and nothing needs
-          // rescaling
-          const float m_ref = cm > m + kCRescale ? cm : m;
-          // (rows that do not exist hold anything: they never ask for a rescale)
-          const float alpha = (m == neg_inf_f() || !live) ? 1.f : ex2(m - m_ref);
-          // P_x and O_x are free once the product before has read and written them
-          if (n > tl.lo) {
-            if (!__all_sync(0xffffffffu, mbar_wait<kPoll>(&pvdone[x], ph ^ 1u, abort))) {
-              failed = true;
-              break;
-            }
-            tc_fence_after();
-            if (__any_sync(0xffffffffu, alpha != 1.f)) {
-#pragma unroll 1
-              for (int c = 0; c < D / 16; ++c) {
-                float o[16];
-                uint32_t w[16];
-                tmem_ld16(tm_o + c * 16, o);
-                tmem_wait_ld();
-#pragma unroll
-                for (int v = 0; v < 16; ++v) w[v] = __float_as_uint(o[v] * alpha);
-                tmem_st16u(tm_o + c * 16, w);
-              }
-            }
-          }
-          const float mb = (m_ref == neg_inf_f()) ? 0.f : m_ref;
-          float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-          const float2 sl2x2 = make_float2(sl2, sl2), nmb2 = make_float2(-mb, -mb);
-#pragma unroll
-          for (int ch = 0; ch < 4; ++ch) {
-            uint32_t w[16];
-#pragma unroll
-            for (int v = 0; v < 16; ++v) {
-              const float2 x2 = __ffma2_rn(make_float2(r[32 * ch + 2 * v], r[32 * ch + 2 * v + 1]),
-                                           sl2x2, nmb2);
-              const float p0 = ex2(x2.x), p1 = ex2(x2.y);
-              ls[v & 1] = __fadd2_rn(ls[v & 1], make_float2(p0, p1));
-              w[v] = pack_pair<T>(p0, p1);
-            }
-            tmem_st16u(tm_p + ch * 16, w);
-          }
-          l = l * alpha + ((ls[0].x + ls[1].x) + (ls[0].y + ls[1].y));
-          m = m_ref;
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&pfull[x]);
+    // bad sequences: status, and NaN rows where the rows are known
+    for (int i = b; i < pa.M; i += gridDim.x) {
+      const PagedSeq q = paged_seq(pa, i);
+      if (q.err != KVS_OK) {
+        if (threadIdx.x == 0) record_status(d_status, q.err);
+        for (int r = 0; r < q.n; ++r)
+          for (int e = threadIdx.x; e < Hkv * G * D; e += 256)
+            out[(long long)(q.row0 + r) * out_stride + e] = from_f32<T>(nan);
+      }
+    }
+    const unsigned tag = launch_tag(host_tag, __ldcg(epoch));
+    for (int nq = 0; !failed; ++nq) {
+      CUnit f;
+      if (!unit(nq, f)) failed = true;
+      if (failed || f.t_lo == f.t_hi) break;
+      const CTile tl = tile_of(f, x);
+      const int rows = tl.ntok * G;
+      const bool live = t < rows;
+      const int tok = live ? t / G : tl.ntok - 1;
+      const int last = f.p + tl.tok0 + tok;  // the row's last key
+      const int first_last = f.p + tl.tok0;  // the tile's first row's
+      float m = neg_inf_f(), l = 0.f;
+      for (int n = tl.lo; n < tl.hi; ++n) {
+        const uint32_t ph = (uint32_t)(sb + n - tl.lo) & 1u;
+        if (!__all_sync(0xffffffffu, mbar_wait<kPoll>(&sfull[x], ph, abort))) {
+          failed = true;
+          break;
         }
-        if (failed) break;
-        sb += tl.hi - tl.lo;
-        if (tl.lo < tl.hi) {
-          // the tile's last product is done: O_x is final
-          if (!__all_sync(0xffffffffu, mbar_wait<kPoll>(&pvdone[x], (uint32_t)(sb - 1) & 1u, abort))) {
+        tc_fence_after();
+        float r[kCN];
+        tmem_ld64(tm_s, *reinterpret_cast<float(*)[64]>(&r[0]));
+        tmem_ld64(tm_s + 64, *reinterpret_cast<float(*)[64]>(&r[64]));
+        tmem_wait_ld();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sread);  // the other tile's product may have the columns
+        const int key0 = n * kCN;
+        if (key0 + kCN - 1 > first_last) {
+          const int lim = last - key0;  // keys 0..lim of the tile are attended
+#pragma unroll
+          for (int v = 0; v < kCN; ++v) r[v] = v <= lim ? r[v] : neg_inf_f();
+        }
+        float mx[4] = {r[0], r[1], r[2], r[3]};  // four chains (max is exact in any order)
+#pragma unroll
+        for (int v = 4; v < kCN; v += 4) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], r[v + k]);
+        }
+        const float cm = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
+        // the reference maximum moves only when the row's grows by more
+        // than 2^kCRescale: below that P stays in range and nothing needs
+        // rescaling
+        const float m_ref = cm > m + kCRescale ? cm : m;
+        // (rows that do not exist hold anything: they never ask for a rescale)
+        const float alpha = (m == neg_inf_f() || !live) ? 1.f : ex2(m - m_ref);
+        // P_x and O_x are free once the product before has read and written them
+        if (n > tl.lo) {
+          if (!__all_sync(0xffffffffu, mbar_wait<kPoll>(&pvdone[x], ph ^ 1u, abort))) {
             failed = true;
             break;
           }
           tc_fence_after();
-          if (s_bad[nq & 3]) l = nan;
-          const bool whole = tl.hi - tl.lo == tl.nt;
-          const long long row0 = f.s.row0 + tl.tok0;
-          T *orow = out + (row0 + tok) * out_stride + (long long)(u.g * G + (t - tok * G)) * D;
-          if (whole) {
-            const float inv = 1.f / l;
+          if (__any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll 1
+            for (int c = 0; c < D / 16; ++c) {
+              float o[16];
+              uint32_t w[16];
+              tmem_ld16(tm_o + c * 16, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int v = 0; v < 16; ++v) w[v] = __float_as_uint(o[v] * alpha);
+              tmem_st16u(tm_o + c * 16, w);
+            }
+          }
+        }
+        const float mb = (m_ref == neg_inf_f()) ? 0.f : m_ref;
+        float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        const float2 sl2x2 = make_float2(sl2, sl2), nmb2 = make_float2(-mb, -mb);
+#pragma unroll
+        for (int ch = 0; ch < 4; ++ch) {
+          uint32_t w[16];
+#pragma unroll
+          for (int v = 0; v < 16; ++v) {
+            const float2 x2 = __ffma2_rn(make_float2(r[32 * ch + 2 * v], r[32 * ch + 2 * v + 1]),
+                                         sl2x2, nmb2);
+            const float p0 = ex2(x2.x), p1 = ex2(x2.y);
+            ls[v & 1] = __fadd2_rn(ls[v & 1], make_float2(p0, p1));
+            w[v] = pack_pair<T>(p0, p1);
+          }
+          tmem_st16u(tm_p + ch * 16, w);
+        }
+        l = l * alpha + ((ls[0].x + ls[1].x) + (ls[0].y + ls[1].y));
+        m = m_ref;
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&pfull[x]);
+      }
+      if (failed) break;
+      sb += tl.hi - tl.lo;
+      if (tl.lo < tl.hi) {
+        // the tile's last product is done: O_x is final
+        if (!__all_sync(0xffffffffu, mbar_wait<kPoll>(&pvdone[x], (uint32_t)(sb - 1) & 1u, abort))) {
+          failed = true;
+          break;
+        }
+        tc_fence_after();
+        // (read again: in registers they would crowd out the row)
+        const volatile CUnit *ud = &units[nq % kCUnits];
+        if (ud->bad) l = nan;
+        const bool whole = tl.hi - tl.lo == tl.nt;
+        const long long row0 = ud->row0 + tl.tok0;
+        const long long at =
+            live ? (row0 + tok) * out_stride + (long long)(ud->g * G + (t - tok * G)) * D : -1;
+        if (whole) {
+          const float inv = 1.f / l;
+#pragma unroll 1
+          for (int ch = 0; ch < D / 64; ++ch) {
+            float o[2][32];
+            tmem_ld32(tm_o + ch * 64, o[0]);
+            tmem_ld32(tm_o + ch * 64 + 32, o[1]);
+            tmem_wait_ld();
+            put_row32<T>(stg, lane, 0, o[0], inv);
+            put_row32<T>(stg, lane, 1, o[1], inv);
+            write_rows64(stg, lane, out, at, ch * 64);
+          }
+        } else {
+          // the blocks of tile x's first and last key tile, and their partials
+          const Pieces pc{slots + x * paged_slot_floats(kCM, D), 2 * paged_slot_floats(kCM, D),
+                          ud->b1, ud->b2[x]};
+          unsigned long long *ctr = counters + 2 * pc.b1 + x;
+          const unsigned add = (unsigned)(tl.hi - tl.lo);
+          // Usually the other pieces were finished long ago: then this block
+          // joins them with the accumulator it still holds in TMEM.
+          if (t == 0) {
+            const unsigned long long v = ld_acquire_u64(ctr);
+            s_last[x] = (unsigned)(v >> 32) == tag && (unsigned)v + add == (unsigned)tl.nt;
+          }
+          if (!wg_barrier()) {
+            failed = true;
+            break;
+          }
+          if (s_last[x]) {
+            __threadfence();
+            if (t == 0) *ctr = 0ull;  // (no other block will look; a replayed graph uses the tag again)
+            if (pc.b2 == pc.b1 + 1) {  // two pieces, the usual unit: all loads first
+              const int oc = b == pc.b1 ? pc.b2 : pc.b1;
+              const float2 om = __ldcg(pc.ml(oc, t));
+#pragma unroll 1
+              for (int ch = 0; ch < D / 64; ++ch) {
+                float4 q[16];
+#pragma unroll
+                for (int v = 0; v < 16; ++v) q[v] = __ldcg(pc.acc(oc, t, ch * 64 + 4 * v));
+                const float mx = fmaxf(m, om.x);
+                const float wo = piece_weight(om.x, mx), ww = piece_weight(m, mx);
+                const float ls = b == pc.b1 ? fmaf(wo, om.y, ww * l) : fmaf(ww, l, wo * om.y);
+                const float inv = 1.f / ls;
+#pragma unroll
+                for (int hc = 0; hc < 2; ++hc) {
+                  float o[32];
+                  tmem_ld32(tm_o + ch * 64 + hc * 32, o);
+                  tmem_wait_ld();
+#pragma unroll
+                  for (int v = 0; v < 32; ++v) {
+                    const float4 qq = q[8 * hc + v / 4];
+                    const float other = v % 4 == 0 ? qq.x : v % 4 == 1 ? qq.y : v % 4 == 2 ? qq.z : qq.w;
+                    o[v] = b == pc.b1 ? fmaf(wo, other, ww * o[v]) : fmaf(ww, o[v], wo * other);
+                  }
+                  put_row32<T>(stg, lane, hc, o, inv);
+                }
+                write_rows64(stg, lane, out, at, ch * 64);
+              }
+            } else {
+            float mx = m;
+            for (int c = pc.b1; c <= pc.b2; ++c)
+              if (c != b) mx = fmaxf(mx, __ldcg(pc.ml(c, t)).x);
+            float ls = 0.f;
+            for (int c = pc.b1; c <= pc.b2; ++c) {
+              const float2 ml = c == b ? make_float2(m, l) : __ldcg(pc.ml(c, t));
+              ls = fmaf(piece_weight(ml.x, mx), ml.y, ls);
+            }
+            const float inv = 1.f / ls;
+#pragma unroll 1
+            for (int ch = 0; ch < D / 32; ++ch) {
+              float o[32], acc[32];
+              tmem_ld32(tm_o + ch * 32, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int v = 0; v < 32; ++v) acc[v] = 0.f;
+              for (int c = pc.b1; c <= pc.b2; ++c) {
+                if (c == b) {
+                  const float w = piece_weight(m, mx);
+#pragma unroll
+                  for (int v = 0; v < 32; ++v) acc[v] = fmaf(w, o[v], acc[v]);
+                } else {
+                  float4 q[8];
+#pragma unroll
+                  for (int v = 0; v < 8; ++v) q[v] = __ldcg(pc.acc(c, t, ch * 32 + 4 * v));
+                  const float w = piece_weight(__ldcg(pc.ml(c, t)).x, mx);
+#pragma unroll
+                  for (int v = 0; v < 8; ++v) {
+                    acc[4 * v] = fmaf(w, q[v].x, acc[4 * v]);
+                    acc[4 * v + 1] = fmaf(w, q[v].y, acc[4 * v + 1]);
+                    acc[4 * v + 2] = fmaf(w, q[v].z, acc[4 * v + 2]);
+                    acc[4 * v + 3] = fmaf(w, q[v].w, acc[4 * v + 3]);
+                  }
+                }
+              }
+              put_row32<T>(stg, lane, ch & 1, acc, inv);
+              if (ch & 1) write_rows64(stg, lane, out, at, (ch - 1) * 32);
+            }
+            }
+          } else {
 #pragma unroll 1
             for (int ch = 0; ch < D / 32; ++ch) {
               float o[32];
               tmem_ld32(tm_o + ch * 32, o);
               tmem_wait_ld();
-              if (live) store_row32<T>(orow + ch * 32, o, inv);
+#pragma unroll
+              for (int v = 0; v < 8; ++v)
+                __stcg(pc.acc(b, t, ch * 32 + 4 * v),
+                       make_float4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]));
             }
-          } else {
-            // the blocks of tile x's first and last key tile, and their partials
-            const Pieces pc{slots + x * paged_slot_floats(kCM, D), 2 * paged_slot_floats(kCM, D),
-                            cut.at(f.k0), cut.at(f.k0 + (long long)(tl.nt - 1) * kCN)};
-            unsigned long long *ctr = counters + 2 * pc.b1 + x;
-            const unsigned add = (unsigned)(tl.hi - tl.lo);
-            // Usually the other pieces were finished long ago: then this block
-            // joins them with the accumulator it still holds in TMEM.
+            __stcg(pc.ml(b, t), make_float2(m, l));
+            __threadfence();  // the partial is visible GPU-wide before it counts
+            if (!wg_barrier()) {
+              failed = true;
+              break;
+            }
             if (t == 0) {
-              const unsigned long long v = ld_acquire_u64(ctr);
-              s_last[x] = (unsigned)(v >> 32) == tag && (unsigned)v + add == (unsigned)tl.nt;
+              const unsigned before = tagged_add(ctr, add, tag, d_status, epoch);
+              const bool fin = before != 0xffffffffu && before + add == (unsigned)tl.nt;
+              if (fin) *ctr = 0ull;
+              s_last[x] = fin;
             }
             if (!wg_barrier()) {
               failed = true;
               break;
             }
             if (s_last[x]) {
+              // (the others finished in the meantime: all pieces from memory)
               __threadfence();
-              if (t == 0) *ctr = 0ull;  // (no other block will look; a replayed graph uses the tag again)
-              if (pc.b2 == pc.b1 + 1) {  // two pieces, the usual unit: all loads first
-                const int oc = b == pc.b1 ? pc.b2 : pc.b1;
-                const float2 om = __ldcg(pc.ml(oc, t));
-#pragma unroll 1
-                for (int ch = 0; ch < D / 64; ++ch) {
-                  float4 q[16];
-#pragma unroll
-                  for (int v = 0; v < 16; ++v) q[v] = __ldcg(pc.acc(oc, t, ch * 64 + 4 * v));
-                  const float mx = fmaxf(m, om.x);
-                  const float wo = piece_weight(om.x, mx), ww = piece_weight(m, mx);
-                  const float ls = b == pc.b1 ? fmaf(wo, om.y, ww * l) : fmaf(ww, l, wo * om.y);
-                  const float inv = 1.f / ls;
-#pragma unroll
-                  for (int hc = 0; hc < 2; ++hc) {
-                    float o[32];
-                    tmem_ld32(tm_o + ch * 64 + hc * 32, o);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int v = 0; v < 32; ++v) {
-                      const float4 qq = q[8 * hc + v / 4];
-                      const float other = v % 4 == 0 ? qq.x : v % 4 == 1 ? qq.y : v % 4 == 2 ? qq.z : qq.w;
-                      o[v] = b == pc.b1 ? fmaf(wo, other, ww * o[v]) : fmaf(ww, o[v], wo * other);
-                    }
-                    if (live) store_row32<T>(orow + ch * 64 + hc * 32, o, inv);
-                  }
-                }
-              } else {
-              float mx = m;
-              for (int c = pc.b1; c <= pc.b2; ++c)
-                if (c != b) mx = fmaxf(mx, __ldcg(pc.ml(c, t)).x);
-              float ls = 0.f;
+              float mx = neg_inf_f(), ls = 0.f;
+              for (int c = pc.b1; c <= pc.b2; ++c) mx = fmaxf(mx, __ldcg(pc.ml(c, t)).x);
               for (int c = pc.b1; c <= pc.b2; ++c) {
-                const float2 ml = c == b ? make_float2(m, l) : __ldcg(pc.ml(c, t));
+                const float2 ml = __ldcg(pc.ml(c, t));
                 ls = fmaf(piece_weight(ml.x, mx), ml.y, ls);
               }
               const float inv = 1.f / ls;
 #pragma unroll 1
               for (int ch = 0; ch < D / 32; ++ch) {
-                float o[32], acc[32];
-                tmem_ld32(tm_o + ch * 32, o);
-                tmem_wait_ld();
+                float acc[32];
 #pragma unroll
                 for (int v = 0; v < 32; ++v) acc[v] = 0.f;
                 for (int c = pc.b1; c <= pc.b2; ++c) {
-                  if (c == b) {
-                    const float w = piece_weight(m, mx);
+                  const float w = piece_weight(__ldcg(pc.ml(c, t)).x, mx);
 #pragma unroll
-                    for (int v = 0; v < 32; ++v) acc[v] = fmaf(w, o[v], acc[v]);
-                  } else {
-                    float4 q[8];
-#pragma unroll
-                    for (int v = 0; v < 8; ++v) q[v] = __ldcg(pc.acc(c, t, ch * 32 + 4 * v));
-                    const float w = piece_weight(__ldcg(pc.ml(c, t)).x, mx);
-#pragma unroll
-                    for (int v = 0; v < 8; ++v) {
-                      acc[4 * v] = fmaf(w, q[v].x, acc[4 * v]);
-                      acc[4 * v + 1] = fmaf(w, q[v].y, acc[4 * v + 1]);
-                      acc[4 * v + 2] = fmaf(w, q[v].z, acc[4 * v + 2]);
-                      acc[4 * v + 3] = fmaf(w, q[v].w, acc[4 * v + 3]);
-                    }
+                  for (int v = 0; v < 8; ++v) {
+                    const float4 q = __ldcg(pc.acc(c, t, ch * 32 + 4 * v));
+                    acc[4 * v] = fmaf(w, q.x, acc[4 * v]);
+                    acc[4 * v + 1] = fmaf(w, q.y, acc[4 * v + 1]);
+                    acc[4 * v + 2] = fmaf(w, q.z, acc[4 * v + 2]);
+                    acc[4 * v + 3] = fmaf(w, q.w, acc[4 * v + 3]);
                   }
                 }
-                if (live) store_row32<T>(orow + ch * 32, acc, inv);
-              }
-              }
-            } else {
-#pragma unroll 1
-              for (int ch = 0; ch < D / 32; ++ch) {
-                float o[32];
-                tmem_ld32(tm_o + ch * 32, o);
-                tmem_wait_ld();
-#pragma unroll
-                for (int v = 0; v < 8; ++v)
-                  __stcg(pc.acc(b, t, ch * 32 + 4 * v),
-                         make_float4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]));
-              }
-              __stcg(pc.ml(b, t), make_float2(m, l));
-              __threadfence();  // the partial is visible GPU-wide before it counts
-              if (!wg_barrier()) {
-                failed = true;
-                break;
-              }
-              if (t == 0) {
-                const unsigned before = tagged_add(ctr, add, tag, d_status, epoch);
-                const bool fin = before != 0xffffffffu && before + add == (unsigned)tl.nt;
-                if (fin) *ctr = 0ull;
-                s_last[x] = fin;
-              }
-              if (!wg_barrier()) {
-                failed = true;
-                break;
-              }
-              if (s_last[x]) {
-                // (the others finished in the meantime: all pieces from memory)
-                __threadfence();
-                float mx = neg_inf_f(), ls = 0.f;
-                for (int c = pc.b1; c <= pc.b2; ++c) mx = fmaxf(mx, __ldcg(pc.ml(c, t)).x);
-                for (int c = pc.b1; c <= pc.b2; ++c) {
-                  const float2 ml = __ldcg(pc.ml(c, t));
-                  ls = fmaf(piece_weight(ml.x, mx), ml.y, ls);
-                }
-                const float inv = 1.f / ls;
-#pragma unroll 1
-                for (int ch = 0; ch < D / 32; ++ch) {
-                  float acc[32];
-#pragma unroll
-                  for (int v = 0; v < 32; ++v) acc[v] = 0.f;
-                  for (int c = pc.b1; c <= pc.b2; ++c) {
-                    const float w = piece_weight(__ldcg(pc.ml(c, t)).x, mx);
-#pragma unroll
-                    for (int v = 0; v < 8; ++v) {
-                      const float4 q = __ldcg(pc.acc(c, t, ch * 32 + 4 * v));
-                      acc[4 * v] = fmaf(w, q.x, acc[4 * v]);
-                      acc[4 * v + 1] = fmaf(w, q.y, acc[4 * v + 1]);
-                      acc[4 * v + 2] = fmaf(w, q.z, acc[4 * v + 2]);
-                      acc[4 * v + 3] = fmaf(w, q.w, acc[4 * v + 3]);
-                    }
-                  }
-                  if (live) store_row32<T>(orow + ch * 32, acc, inv);
-                }
+                put_row32<T>(stg, lane, ch & 1, acc, inv);
+              if (ch & 1) write_rows64(stg, lane, out, at, (ch - 1) * 32);
               }
             }
           }
         }
-        ++nq;
       }
-      if (!failed) advance(f);
+      unit_done(nq);
     }
     if (failed && lane == 0) give_up(abort, d_status, epoch);
   }
