@@ -31,8 +31,15 @@
 // cycles to issue instead of 67; issued by an elected lane of a converged
 // warp 365 us -- now its polling of six barriers, 140 cycles a look, set the
 // pace; with two issuing warps that wait in a fixed order 312 us;
-// then 286 us by what blocks do at the ends of units (below).  P laid over
-// S with a first half of P V issued early: 477 us (more barriers to poll).
+// 281 us by what blocks do at the ends of units (below); 259 us with P V
+// held back until the tile's next S is in the pipe -- the two products of one
+// pipe took turns before, which doubled the time until S was there, and S is
+// what the softmax waits for.  Slower: P laid over S with a first half of P V
+// issued early 477 us, S and P V by one warp in the order in which they get
+// ready 313 us (it stalls in the pipe while the other could be looked at),
+// issuing warps that spin 304 us (they take the softmax's issue slots), a warp
+// of its own for V 270 to 296 us (but 16-key pages then 169 us instead of 200
+// at 3200 tokens over 3200: their copies of 2 KB take long to issue).
 //
 // The softmax keeps a reference maximum that moves only when a row's maximum
 // grows by more than 2^8, so P and O are rarely rescaled; the weights are
@@ -72,7 +79,8 @@ struct CUnit {
   int t_lo, t_hi;           // key tiles of this block; t_lo == t_hi: no further unit
   int g;                    // kv head
   int bad;                  // a page of it is bad
-  int b1, b2[2], pad;       // blocks of its first key tile and of the last ones of tiles A and B
+  int seq, L;               // the sequence and its keys
+  int b1, b2[2];            // blocks of its first key tile and of the last ones of tiles A and B
 };
 constexpr int kCUnits = 4;  // the copy warp is at most so many units ahead
 
@@ -87,9 +95,9 @@ struct CGeo {
   static constexpr int OFF_V = OFF_K + KS * TILE;
   static constexpr int OFF_STAGE = OFF_V + VS * TILE;  // 4 KB a softmax warp: rows on their way out
   static constexpr int OFF_BAR = OFF_STAGE + 8 * 4096;
-  // q, qfree, kfull[KS], kfree[KS], vfull[VS], vfree[VS], vpart, sfull[2],
-  // sread, pfull[2], pvdone[2], wg[2], final[2], ufull[kCUnits], ufree[kCUnits]
-  static constexpr int NBAR = 2 + 2 * KS + 2 * VS + 1 + 2 + 1 + 6 + 2 + 2 * kCUnits;
+  // q, qfree, kfull[KS], kfree[KS], vfull[VS], vfree[VS], sfull[2],
+  // sread, pfull[2], pvdone[2], wg[2], final[2], ufull[kCUnits], ufree[kCUnits], sgone[4]
+  static constexpr int NBAR = 2 + 2 * KS + 2 * VS + 2 + 1 + 6 + 2 + 2 * kCUnits + 4;
   static constexpr int OFF_TMEM = OFF_BAR + NBAR * 8;
   static constexpr int OFF_MISC = OFF_TMEM + 8;   // abort, last[2], pad
   static constexpr int OFF_UNIT = OFF_MISC + 16;  // CUnit [kCUnits]
@@ -225,8 +233,7 @@ __global__ void __launch_bounds__(kCThreads, 1)
   uint64_t *kfree = kfull + KS;      // [KS] the S products of a stage done (commit)
   uint64_t *vfull = kfree + KS;      // [VS]
   uint64_t *vfree = vfull + VS;      // [VS] the P V products of a stage done (commit)
-  uint64_t *vpart = vfree + VS;      // a V tile that ends past the last key landed
-  uint64_t *sfull = vpart + 1;       // [2] S of tile x ready (commit)
+  uint64_t *sfull = vfree + VS;      // [2] S of tile x ready (commit)
   uint64_t *sread = sfull + 2;       // S is in registers (an arrival of each of the tile's warps)
   uint64_t *pfull = sread + 1;       // [2] P_x written, O_x rescaled (an arrival a warp)
   uint64_t *pvdone = pfull + 2;      // [2] P V_x done (commit)
@@ -234,6 +241,7 @@ __global__ void __launch_bounds__(kCThreads, 1)
   uint64_t *final = wgbar + 2;       // [2] every product S, every P V of the block done (commit)
   uint64_t *ufull = final + 2;       // [kCUnits] a unit is described
   uint64_t *ufree = ufull + kCUnits; // [kCUnits] the ten other warps are done with it
+  uint64_t *sgone = ufree + kCUnits;  // [4] S product k of the block issued, at k % 4
   CUnit *units = reinterpret_cast<CUnit *>(smem + C::OFF_UNIT);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_TMEM);
   volatile int *abort = reinterpret_cast<volatile int *>(smem + C::OFF_MISC);
@@ -293,11 +301,33 @@ __global__ void __launch_bounds__(kCThreads, 1)
     if (lane == 0) mbar_arrive(&ufree[n % kCUnits]);
   };
 
+  const int R = 1 << box_shift;          // rows of a copy
+  const int pieces = kCN >> box_shift;   // copies of a tile's column block
+  const int piece = lane & (pieces - 1), blk = lane / pieces;  // a copying lane's part of a tile
+  // The row of the cache where this lane's part of key tile n starts; live:
+  // parts that hold keys; mine: this lane has one.
+  struct Part {
+    int row, live;
+    bool mine, bad;
+  };
+  auto part_of = [&](int seq, int L, int g, int n) {
+    Part c;
+    const int key = n * kCN + piece * R;
+    c.live = min(pieces, (L - n * kCN + R - 1) / R);
+    c.mine = blk < C::NB && piece < c.live;
+    int page = c.mine ? __ldca(pa.page_table + (size_t)seq * pa.max_pages + (key >> pa.page_shift)) : 0;
+    c.bad = (unsigned)page >= (unsigned)pa.num_pages;
+    if (c.bad) page = 0;
+    c.row = ((page * Hkv + g) << pa.page_shift) + (key & ((1 << pa.page_shift) - 1));
+    return c;
+  };
+  const uint32_t part_bytes = (uint32_t)(C::NB * R) * 128;  // of all column blocks
+  const int part_at = blk * C::BLK + piece * R * 128;
+
   if (warp == kCCopyWarp) {
-    // ======================= copies ==========================================
-    int nk = 0, nv = 0;  // K and V tiles issued
-    int nq = 0, npart = 0;
-    bool ok = true, part_failed = false;
+    // ======================= units and copies ================================
+    int nk = 0, nv = 0, nq = 0;  // K and V tiles issued, units described
+    bool ok = true;
     const Cuts cut = equal_cuts(warp_line_total(pa, ln, lane), ln, gridDim.x);
     bool more = cut.R > 0 && b < cut.NS;
     const long long x0 = more ? cut.start(b) : 0, x1 = more ? cut.start(b + 1) : 0;
@@ -315,15 +345,10 @@ __global__ void __launch_bounds__(kCThreads, 1)
       __syncwarp();
       return true;
     };
-    const int R = 1 << box_shift;          // rows of a copy
-    const int pieces = kCN >> box_shift;   // copies of a tile's column block
-    const uint32_t piece_bytes = (uint32_t)R * 128;
     while (more && ok) {
       const UnitInfo f = unit_info(pa, u, ln, x0, x1);
       if (f.t_lo < f.t_hi) {
-        const int32_t *table = pa.page_table + (size_t)u.i * pa.max_pages;
-        const int L = f.s.p + f.s.n;
-        CUnit d{f.s.p, f.s.row0, f.tok0, f.ntok, f.t_lo, f.t_hi, u.g, 0, b, {b, b}, 0};
+        CUnit d{f.s.p, f.s.row0, f.tok0, f.ntok, f.t_lo, f.t_hi, u.g, 0, u.i, f.s.p + f.s.n, b, {b, b}};
         if (f.t_hi - f.t_lo < f.nt) {
           d.b1 = cut.at(f.k0);
           for (int x = 0; x < 2; ++x) {
@@ -338,61 +363,39 @@ __global__ void __launch_bounds__(kCThreads, 1)
           const int tiles = f.ntok > TT ? 2 : 1;
           mbar_arrive_expect_tx(bar_q, (uint32_t)(tiles * C::NB * TT * G * 128));
           for (int x = 0; x < tiles; ++x)
-            for (int blk = 0; blk < C::NB; ++blk)
-              tma_q(smem + C::OFF_Q + x * C::TILE + blk * C::BLK, &qmap, u.g * G,
-                    f.s.row0 + f.tok0 + x * TT, blk, bar_q);
+            for (int cb = 0; cb < C::NB; ++cb)
+              tma_q(smem + C::OFF_Q + x * C::TILE + cb * C::BLK, &qmap, u.g * G,
+                    f.s.row0 + f.tok0 + x * TT, cb, bar_q);
         }
         ++nq;
         __syncwarp();
-        for (int n = f.t_lo; n < f.t_hi; ++n) {
-          // lane: column block lane / pieces, piece lane % pieces of the tile
-          const int piece = lane & (pieces - 1);
-          const int blk = lane / pieces;
-          const int key = n * kCN + piece * R;
-          const int live_pieces = min(pieces, (L - n * kCN + R - 1) / R);
-          const bool mine = blk < C::NB && piece < live_pieces;
-          int page = mine ? __ldca(table + (key >> pa.page_shift)) : 0;
-          if ((unsigned)page >= (unsigned)pa.num_pages) {
-            record_status(d_status, KVS_ERR_PAGE);
-            *const_cast<volatile int *>(&units[(nq - 1) % kCUnits].bad) = 1;
-            page = 0;
-          }
-          const int row = ((page * Hkv + u.g) << pa.page_shift) + (key & ((1 << pa.page_shift) - 1));
-          const uint32_t bytes = (uint32_t)(C::NB * live_pieces) * piece_bytes;
-          unsigned char *part = smem + blk * C::BLK + piece * R * 128;
-          const int ks = nk % KS, vs = nv % VS;
-          if (nk >= KS && !(ok = __all_sync(0xffffffffu, mbar_wait<kPoll>(&kfree[ks], (uint32_t)((nk - KS) / KS) & 1u, abort))))
-            break;
-          if (lane == 0) mbar_arrive_expect_tx(&kfull[ks], bytes);
-          __syncwarp();
-          if (mine) tma_block(part + C::OFF_K + ks * C::TILE, &kmap, row, blk, &kfull[ks]);
-          ++nk;
-          if (nv >= VS && !(ok = __all_sync(0xffffffffu, mbar_wait<kPoll>(&vfree[vs], (uint32_t)((nv - VS) / VS) & 1u, abort))))
-            break;
-          // a V tile that ends past the last key: its other rows hold anything
-          // (their weights are zero, but 0 x NaN is not), so they are zeroed
-          // before the products may read it
-          const int left = L - n * kCN;
-          uint64_t *bar = left < kCN ? vpart : &vfull[vs];
-          if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
-          __syncwarp();
-          if (mine) tma_block(part + C::OFF_V + vs * C::TILE, &vmap, row, blk, bar);
-          ++nv;
-          if (left < kCN) {
-            ++npart;
-            if (!(ok = __all_sync(0xffffffffu, mbar_wait<kPoll>(vpart, (uint32_t)(npart - 1) & 1u, abort)))) {
-              part_failed = true;
+        // in the order in which their places get free: K one tile ahead of V
+        Part cv, ck = part_of(u.i, d.L, u.g, f.t_lo);
+        for (int n = f.t_lo; n <= f.t_hi && ok; ++n) {
+          if (n < f.t_hi) {
+            if (ck.bad) {
+              record_status(d_status, KVS_ERR_PAGE);
+              *const_cast<volatile int *>(&units[(nq - 1) % kCUnits].bad) = 1;
+            }
+            const int ks = nk % KS;
+            if (nk >= KS && !(ok = __all_sync(0xffffffffu, mbar_wait<kPoll>(&kfree[ks], (uint32_t)((nk - KS) / KS) & 1u, abort))))
               break;
-            }
-            unsigned char *v = smem + C::OFF_V + vs * C::TILE;
-            for (int e = lane; e < (kCN - left) * 8 * C::NB; e += 32) {
-              const int r = left + (e >> 3) / C::NB, bb = (e >> 3) % C::NB;
-              *reinterpret_cast<uint4 *>(v + bb * C::BLK + r * 128 + (e & 7) * 16) = make_uint4(0, 0, 0, 0);
-            }
-            fence_proxy_async_shared();
+            if (lane == 0) mbar_arrive_expect_tx(&kfull[ks], ck.live * part_bytes);
             __syncwarp();
-            if (lane == 0) mbar_arrive(&vfull[vs]);
+            if (ck.mine) tma_block(smem + C::OFF_K + ks * C::TILE + part_at, &kmap, ck.row, blk, &kfull[ks]);
+            ++nk;
           }
+          if (n > f.t_lo) {
+            const int vs = nv % VS;
+            if (nv >= VS && !(ok = __all_sync(0xffffffffu, mbar_wait<kPoll>(&vfree[vs], (uint32_t)((nv - VS) / VS) & 1u, abort))))
+              break;
+            if (lane == 0) mbar_arrive_expect_tx(&vfull[vs], cv.live * part_bytes);
+            __syncwarp();
+            if (cv.mine) tma_block(smem + C::OFF_V + vs * C::TILE + part_at, &vmap, cv.row, blk, &vfull[vs]);
+            ++nv;
+          }
+          cv = ck;
+          if (n + 1 < f.t_hi) ck = part_of(u.i, d.L, u.g, n + 1);
         }
       }
       more = ok && next_unit(pa, u, f, ln) && u.base < x1;
@@ -404,9 +407,7 @@ __global__ void __launch_bounds__(kCThreads, 1)
       if (nq > 0) mbar_wait_drain(bar_q, (uint32_t)(nq - 1) & 1u);
       for (int j = (nk > KS ? nk - KS : 0); j < nk; ++j)
         mbar_wait_drain(&kfull[j % KS], (uint32_t)(j / KS) & 1u);
-      // a V tile counted on vpart completes vfull only once its tail is zeroed
-      if (npart > 0) mbar_wait_drain(vpart, (uint32_t)(npart - 1) & 1u);
-      for (int j = (nv > VS ? nv - VS : 0); j < nv - (part_failed ? 1 : 0); ++j)
+      for (int j = (nv > VS ? nv - VS : 0); j < nv; ++j)
         mbar_wait_drain(&vfull[j % VS], (uint32_t)(j / VS) & 1u);
     }
     __syncwarp();
@@ -446,6 +447,7 @@ __global__ void __launch_bounds__(kCThreads, 1)
             mma_f16_warp(tm, lq + (x ? kTileStep : 0u) + at, bk + at, kDescHi, kIdS, ks > 0 ? 1u : 0u);
           }
           mma_commit_warp(&sfull[x]);
+          if (lane == 0) mbar_arrive(&sgone[ns & 3]);
           ++ns;
         }
         if (!ok) break;
@@ -466,6 +468,7 @@ __global__ void __launch_bounds__(kCThreads, 1)
     const uint32_t tm = warp_uniform(tmem);
     constexpr uint32_t kIdO = idesc16<T>(kCM, D, true);
     int gt = 0;             // V tiles of the earlier units
+    uint32_t s0 = 0;        // S products of the key tiles before
     int pdone[2] = {0, 0};  // P V_x products of the earlier units
     bool ok = true;
     auto wait = [&](uint64_t *bar, uint32_t phase) {
@@ -479,11 +482,30 @@ __global__ void __launch_bounds__(kCThreads, 1)
       const int n_all = f.t_hi - f.t_lo;
       for (int j = 0; j < n_all && ok; ++j, ++gt) {
         if (!wait(&vfull[gt % VS], gt / VS)) break;
+        const int left = f.L - (f.t_lo + j) * kCN;
+        if (left < kCN) {
+          // rows past the last key hold anything (their weights are zero, but
+          // 0 x NaN is not)
+          unsigned char *v = smem + C::OFF_V + (gt % VS) * C::TILE;
+          for (int e = lane; e < (kCN - left) * 8 * C::NB; e += 32) {
+            const int r = left + (e >> 3) / C::NB, bb = (e >> 3) % C::NB;
+            *reinterpret_cast<uint4 *>(v + bb * C::BLK + r * 128 + (e & 7) * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_shared();
+          __syncwarp();
+        }
         const uint32_t bv = warp_uniform(lv + (uint32_t)(gt % VS) * kTileStep);
         const uint32_t acc = warp_uniform(j > 0 ? 1u : 0u);  // O_x (+)= P_x V
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           if (j >= n_x[x]) continue;
+          // O_x += P_x V goes behind the tile's next S.  (sgone is at most two
+          // products past the one waited for: the softmax needs this P V
+          // before it can read the S after that.)
+          if (j + 1 < n_x[x]) {
+            const uint32_t k = s0 + (j < n_x[0]) + (j < n_x[1]) + (x && j + 1 < n_x[0] ? 1 : 0);
+            if (!wait(&sgone[k & 3], k >> 2)) break;
+          }
           if (!wait(&pfull[x], pdone[x] + j)) break;
           tc_fence_after();
 #pragma unroll
@@ -494,6 +516,7 @@ __global__ void __launch_bounds__(kCThreads, 1)
         }
         if (!ok) break;
         mma_commit_warp(&vfree[gt % VS]);
+        s0 += (j < n_x[0]) + (j < n_x[1]);
       }
       if (!ok) break;
       pdone[0] += n_x[0];
