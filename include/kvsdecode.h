@@ -541,8 +541,8 @@ typedef struct kvs_paged_cache {
  * row_offsets[i] + t of q, k, v and out belongs to its token t.  Row j of
  * its cache is row j % page_size of page page_table[i][j / page_size].
  * Rows of q, k, v and out outside every [row_offsets[i], row_offsets[i + 1])
- * are neither read nor written.  Table entries past the last page that a
- * sequence's rows reach are not read.
+ * are not written, and what they hold is not used.  Table entries past the
+ * last page that a sequence's rows reach are not read.
  *
  * Checked on the device, per sequence, with the first error in d_status:
  *   KVS_ERR_ROWS      row_offsets[i] <= row_offsets[i + 1] does not hold, or

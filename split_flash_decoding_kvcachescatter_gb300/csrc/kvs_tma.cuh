@@ -32,14 +32,31 @@ static inline TensorMapEncode tensor_map_encoder() {
   return fn;
 }
 
+// Calls the encoder.  It needs the device's context current in the calling
+// thread, which a thread has only once it has made a runtime call that binds
+// it; the encoder itself does not.
+template <typename... Args>
+static inline int encode_map(Args... args) {
+  const TensorMapEncode enc = tensor_map_encoder();
+  if (!enc) return KVS_ERR_LAUNCH;
+  CUresult r = enc(args...);
+  if (r == CUDA_ERROR_INVALID_CONTEXT || r == CUDA_ERROR_NOT_INITIALIZED) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaSetDevice(dev) != cudaSuccess) {
+      cudaGetLastError();
+      return KVS_ERR_LAUNCH;
+    }
+    r = enc(args...);
+  }
+  return r == CUDA_SUCCESS ? KVS_OK : KVS_ERR_LAUNCH;
+}
+
 // Map over `rows` rows of D elements (contiguous), cut into column blocks of
 // 128 bytes: a copy of box_rows rows and `blocks` column blocks fills
 // [blocks][box_rows][128 bytes] of shared memory, 16-byte pieces swizzled by
 // the row (piece c of row r at c ^ (r % 8)).  Coordinates (0, row, block).
 static inline int make_row_map(CUtensorMap *map, const void *base, uint64_t rows, int D, int dtype,
                                int box_rows, int blocks) {
-  const TensorMapEncode enc = tensor_map_encoder();
-  if (!enc) return KVS_ERR_LAUNCH;
   const int size = dtype == KVS_F32 ? 4 : 2;
   const cuuint64_t dims[3] = {(cuuint64_t)(128 / size), rows, (cuuint64_t)(D * size / 128)};
   const cuuint64_t strides[2] = {(cuuint64_t)D * size, 128};
@@ -48,10 +65,9 @@ static inline int make_row_map(CUtensorMap *map, const void *base, uint64_t rows
   const CUtensorMapDataType type = dtype == KVS_F32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                                    : dtype == KVS_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                                       : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  const CUresult r = enc(map, type, 3, const_cast<void *>(base), dims, strides, box, es,
-                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? KVS_OK : KVS_ERR_LAUNCH;
+  return encode_map(map, type, 3, const_cast<void *>(base), dims, strides, box, es,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 // Map over rows of [heads][D] 16-bit elements, row_stride elements apart: a
@@ -60,19 +76,15 @@ static inline int make_row_map(CUtensorMap *map, const void *base, uint64_t rows
 // Coordinates (0, head, row, block).
 static inline int make_q_map(CUtensorMap *map, const void *base, uint64_t rows, int64_t row_stride,
                              int heads, int D, int dtype, int box_rows, int box_heads) {
-  const TensorMapEncode enc = tensor_map_encoder();
-  if (!enc) return KVS_ERR_LAUNCH;
   const cuuint64_t dims[4] = {64, (cuuint64_t)heads, rows, (cuuint64_t)(D / 64)};
   const cuuint64_t strides[3] = {(cuuint64_t)D * 2, (cuuint64_t)row_stride * 2, 128};
   const cuuint32_t box[4] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_rows, 1};
   const cuuint32_t es[4] = {1, 1, 1, 1};
-  const CUresult r = enc(map,
-                         dtype == KVS_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
-                                          : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                         4, const_cast<void *>(base), dims, strides, box, es,
-                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? KVS_OK : KVS_ERR_LAUNCH;
+  const CUtensorMapDataType type =
+      dtype == KVS_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  return encode_map(map, type, 4, const_cast<void *>(base), dims, strides, box, es,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 // The box at row `row` into dst (1024-byte aligned), counted on `bar`.

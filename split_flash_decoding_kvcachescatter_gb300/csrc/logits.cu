@@ -10,10 +10,15 @@
 // history (it comes from L2) and counts the tokens of its own slice with
 // shared-memory atomics; the slice's logits are on their way meanwhile, in
 // 16-byte loads.  (Sharing the list out, each entry sent once to its owner's
-// shared memory, measured 24.1 us against 14 us for 32 rows of 152,064 with
+// shared memory, took 24.4 us where this takes 15.9 for 32 rows of 152,064 with
 // 4,096 entries: the frequent tokens' updates queue at one block.)  The
 // (value, index) maxima meet in block 0's shared memory.  Integer atomics
 // only: the result does not depend on their order.
+//
+// Measured: 32 float32 rows of 152,064 tokens, 4,096 history entries, half of
+// them masked: 15.9 us (39.6 MB, 2.5 TB/s; 5.8 us at the copy peak); one row
+// 5.9 us; 67 bfloat16 rows of 32,001: 9.7 us.  The chain of launch, counting,
+// row and maxima is what takes the time, not the bytes.
 //
 // Arithmetic is one IEEE operation at a time (no fused multiply-add), so a
 // logit is the same whichever variant or alignment handles it.

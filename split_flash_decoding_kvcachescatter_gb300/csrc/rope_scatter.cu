@@ -11,8 +11,15 @@
 // Bound: bytes (each row of q, k, v read once and written once).  A block
 // takes one token, or a slice of its heads when tokens are few: it puts the
 // token's rot_dim / 2 (cos, sin) pairs in shared memory once for all heads,
-// then each thread moves up to kItems pair vectors (two 16-byte loads each
-// with the half layout), all loads issued before the first is used.
+// then each thread moves up to kRopeItems pair vectors at a time (two 16-byte
+// loads each with the half layout), all loads issued before the first is used.
+//
+// Measured: 8192 tokens, H 32 / 8, D 128, bfloat16 (201 MB read and written)
+// 36.9 us, 5.4 TB/s, 80 % of the measured copy peak; a decode step of 32
+// tokens 2.7 us; 1531 tokens, H 14 / 2, D 64, float32, 16 elements rotated in
+// pairs 5.4 us.  Threads x vectors for the first: 128 x 3 36.9, 192 x 2 36.5
+// (but the decode step 2.9), 96 x 4 37.8, 64 x 6 41, 384 x 1 48 us; looking the
+// sequence up before the first load 56 us.
 
 #include "kvs_paged.cuh"
 
