@@ -587,7 +587,8 @@ typedef struct kvs_paged_batch {
  *   rot_dim         even, 0 .. head_dim
  *   scale           factor of the rotated part (1 without length scaling)
  * A token with a bad position or page has no page row written; its q_out
- * row is NaN (bad position) or still the rotated q (bad page).
+ * row is NaN (bad position) or still the rotated q (bad page).  Where offsets
+ * of some sequence are bad, rows of others may be left out too.
  * Errors: NULL, DIMS, UNSUPPORTED (also H / Hkv > 8 or H > 4096), ALIGN,
  * LAUNCH on the host; ROWS, POSITION, PAGE via d_status.
  */
