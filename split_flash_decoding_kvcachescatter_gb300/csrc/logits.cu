@@ -25,6 +25,7 @@
 
 #include <mutex>
 
+#include "kvs_cluster.cuh"
 #include "kvs_paged.cuh"
 
 namespace kvs {
@@ -47,12 +48,6 @@ struct LogitArgs {
   int *d_status;
 };
 
-__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
-}
-__device__ __forceinline__ void st_cluster_s32(uint32_t addr, int v) {
-  asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
-}
 // [lo, hi) of row m in a ragged list, or an empty range when the offsets are
 // bad (`report`: this thread records that).
 __device__ __forceinline__ int2 list_range(const int32_t *offsets, int m, int len, bool report,
@@ -133,6 +128,7 @@ __global__ void __launch_bounds__(kLogitThreads, 2) logits_kernel(LogitArgs a) {
   const int lo = min(V, rank * a.slice), hi = min(V, lo + a.slice);
   const bool counts = a.r.history != nullptr || a.r.bias_ids != nullptr;
   if (t == 0) s_twice = 0;
+  if (a.ids) cluster_arrive_relaxed();  // waited for before the first remote store
   grid_dependency_wait();
   allow_dependent_launch();
   int parity = 0;
@@ -323,12 +319,13 @@ __global__ void __launch_bounds__(kLogitThreads, 2) logits_kernel(LogitArgs a) {
     b = warp_best(b);
     if (lane == 0) s_warp[t >> 5] = b;
     __syncthreads();
+    if (m == (int)blockIdx.y) cluster_wait();  // block 0 runs: its shared memory may be written
     if (t < 32) {
       Best c = (t < kLogitThreads / 32) ? s_warp[t] : Best{neg_inf_f(), 0x7fffffff};
       c = warp_best(c);
       if (t == 0) {
-        st_cluster_f32(dsmem_addr(&s_v[parity][rank], 0), c.v);
-        st_cluster_s32(dsmem_addr(&s_i[parity][rank], 0), c.i);
+        st_dsmem_f32(dsmem_addr(&s_v[parity][rank], 0), c.v);
+        st_dsmem_s32(dsmem_addr(&s_i[parity][rank], 0), c.i);
       }
     }
     cluster_sync_all();  // every block's maximum is in block 0
