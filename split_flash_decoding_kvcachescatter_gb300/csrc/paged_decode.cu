@@ -20,7 +20,7 @@
 //
 // Measured (GB300, copy peak 6.79 TB/s): 8 x 32768 keys, H 32 / 8, D 128,
 // float16 (1.07 GB) 164 us, 96 % of the peak; 32 sequences of up to 8192 keys
-// in bfloat16 (586 MB) 106 us, 81 %.  Tried: one producer warp for all four
+// in bfloat16 (586 MB) 93 us, 93 %.  Tried: one producer warp for all four
 // rings 190 us (it needs about 1000 cycles a tile), two producers of two
 // rings 234 us (rings wait for each other); a warp of its own for the joining
 // 171 and 107 us; with it the last fifth of the line in short ranges handed
@@ -44,7 +44,12 @@ namespace {
 constexpr int kDW = 4;     // rings: consumer and producer warps
 constexpr int kDRows = 16; // rows of a unit
 constexpr int kDThreads = 2 * kDW * 32;
-constexpr int kDFix = 64;  // cost rows that stand for a unit's fixed price
+// A unit's fixed price (its start, the joining of its four states, its output)
+// in bytes of K and V: 32 sequences of up to 8192 keys, H 32 / 8, D 128,
+// bfloat16, took 104 us at 32 KB, 98 at 96, 94 at 128, 92.7 at 192, 93.0 at
+// 256; 32 of up to 4500 62, 55, 48.6, 45.6 and 44.7 us (float32: 134, 123,
+// 121, 123, 125).
+constexpr int kDFixBytes = 192 << 10;
 constexpr int kDMaxDevices = 64;
 // Rules for clusters: the K and V bytes of a block, and those of a unit that
 // halves the block, all counted as if every page of a table were in use.
@@ -233,7 +238,7 @@ __global__ void __launch_bounds__(kDThreads, 1)
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int b = blockIdx.x;
-  const Line ln{Hkv, kDRows / G, kDFix, C::KT, min_column};
+  const Line ln{Hkv, kDRows / G, kDFixBytes / (2 * D * (int)sizeof(T)), C::KT, min_column};
   if (threadIdx.x == 0) {
     prefetch_map(&kmap);
     prefetch_map(&vmap);
@@ -386,11 +391,13 @@ __global__ void __launch_bounds__(kDThreads, 1)
 //
 // Measured against the equal ranges (us; H 32 / 8, D 128, float16, 16-key
 // pages, replayed, so that up to 100 MB come from L2):
-//   sequences x keys       1 x 256   1 x 4096   8 x 1024   32 x 2048   1 x 32768   8 x 32768
-//   full cache a block      128 KB      1 MB     256 KB        1 MB        8 MB       32 MB
-//   clusters                 5.2        7.6        7.8        46.5        27.2       159.7
-//   equal ranges             9.3       14.0       14.7        48.6        31.7       163.9
-// A block reads about 45 MB/ms, so 1 MB bounds what a call can lose by one
+//   sequences x keys       1 x 256   1 x 4096   4 x 1024   32 x 2048   1 x 32768   8 x 32768
+//   full cache a block       16 KB     256 KB     128 KB        1 MB        2 MB        8 MB
+//   clusters                  5.2        7.7        6.5        46.5        26.8       158.7
+//   equal ranges              9.9       13.2       11.1        49.2        32.8       163.5
+//   lengths of 1/8 to all     9.5       13.4       11.0        31.5        25.3       125.9
+//   the same, clusters        5.4        7.2        6.5        31.8        21.2       123.2
+// A block reads about 45 KB/us, so 1 MB bounds what a call can lose by one
 // long sequence among short ones at 20 us; past it the equal ranges run.
 //
 // With W = 2 rings a block, two blocks an SM: one starts and joins while the
