@@ -776,7 +776,10 @@ def kvs_paged_attention(q, cache, batch, out, workspace=None, d_status=None, str
         qs, os_ = qs[0], os_[0]
     else:  # (the stride of a single row says nothing)
         qs = os_ = H * D
-    rc = cache._call[0](q.data_ptr(), qs, cache._addr, batch._addr, out.data_ptr(), os_, H,
+    qp, op = q.data_ptr(), out.data_ptr()
+    if qp == op and N > 0:
+        raise ValueError("kvs_paged_attention: out must not overlap q")
+    rc = cache._call[0](qp, qs, cache._addr, batch._addr, op, os_, H,
                         workspace.data_ptr(), workspace.nbytes,
                         0 if d_status is None else _status_ptr(d_status),
                         _get_stream(dev) if stream is None else _stream(stream))

@@ -504,7 +504,7 @@ int kvs_rope_frequencies(int rot_dim, double base, int kind, double factor, doub
   if (rot_dim < 2 || rot_dim % 2 != 0 || kind < KVS_ROPE_PLAIN || kind > KVS_ROPE_BANDS ||
       !(base > 0.0) || (kind != KVS_ROPE_PLAIN && !(factor >= 1.0)) ||
       (ramp && (!(original_len > 0.0) || !(slow > 0.0) || !(fast > slow))) ||
-      (kind == KVS_ROPE_NTK && rot_dim < 4))
+      (kind == KVS_ROPE_NTK && rot_dim < 4) || (kind == KVS_ROPE_YARN && !(base > 1.0)))
     return KVS_ERR_DIMS;
   if (!inv_freq) return KVS_ERR_NULL;
   const double two_pi = 6.28318530717958647693;

@@ -169,5 +169,12 @@ def test_frequency_refusals(L, kw):
     assert table(L, **kw)[0] == B.KVS_ERR_DIMS
 
 
+@pytest.mark.parametrize("base", [1.0, 0.5])
+def test_yarn_needs_pairs_of_different_speed(L, base):
+    """With base <= 1 no pair is slower than the first, and the ramp over the pairs means nothing."""
+    assert table(L, 64, base, 3, 2.0, 100.0)[0] == B.KVS_ERR_DIMS
+    assert table(L, 64, base, 4, 2.0, 100.0)[0] == 0
+
+
 def test_frequency_null(L):
     assert L.kvs_rope_frequencies(64, 1e4, 0, 1.0, 0.0, 1.0, 2.0, None, None) == B.KVS_ERR_NULL

@@ -173,6 +173,12 @@ def test_without_a_status_word():
     assert out[0].isnan().all() and not out[1:].isnan().any()
 
 
+def test_attention_over_its_own_queries_is_refused():
+    b = Paged([1, 20], [30, 0], 8, 2, 64, "f16", 16, seed=12)
+    with pytest.raises(ValueError):
+        b.attend(out=b.q)
+
+
 @pytest.mark.parametrize("V", [9, 40])
 def test_more_logit_rows_than_a_grid_holds(V):
     M = 66001
