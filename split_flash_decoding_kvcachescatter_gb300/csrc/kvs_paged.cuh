@@ -124,22 +124,15 @@ __device__ __forceinline__ long long div_nn(long long a, long long b) {
   return a / b;
 }
 
-// How a line of R cost rows is cut: [0, S) into NS equal ranges, the rest
-// into ND equal ones; ranges are numbered through.
+// A line of R cost rows cut into NS equal ranges.
 struct Cuts {
-  long long R, S;
-  int NS, ND;
-  __device__ long long start(int r) const {
-    return r <= NS ? div_nn(S * r, NS) : S + div_nn((R - S) * (r - NS), ND);
-  }
+  long long R;
+  int NS;
+  __device__ long long start(int r) const { return div_nn(R * r, NS); }
   // The range that holds cost row x: the last one that starts at or before it.
   __device__ int at(long long x) const {
-    if (x < S || ND == 0) {
-      const long long c = div_nn(x * NS + NS - 1, S);
-      return (int)(c < NS - 1 ? c : NS - 1);
-    }
-    const long long c = div_nn((x - S) * ND + ND - 1, R - S);
-    return NS + (int)(c < ND - 1 ? c : ND - 1);
+    const long long c = div_nn(x * NS + NS - 1, R);
+    return (int)(c < NS - 1 ? c : NS - 1);
   }
 };
 
@@ -155,7 +148,7 @@ static __device__ long long warp_line_total(const PagedArgs &a, const Line &ln, 
 // The line in at most `blocks` equal ranges, fewer when short, so that one
 // holds work worth a block.
 __device__ __forceinline__ Cuts equal_cuts(long long R, const Line &ln, int blocks) {
-  Cuts c{R, R, 1, 0};
+  Cuts c{R, 1};
   if (R > 0) c.NS = (int)max(1ll, min((long long)blocks, div_nn(R, ln.min_column)));
   return c;
 }
