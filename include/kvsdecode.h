@@ -642,7 +642,8 @@ int kvs_rope_frequencies(int rot_dim, double base, int kind, double factor, doub
  * Every live K and V row must be finite; cache rows past a sequence's last
  * new token are never used, whatever they hold.  Products of 16-bit types
  * accumulate in float32, the softmax runs in float32 with its weights
- * rounded to the type before the product with v; float32 inputs keep float32
+ * rounded to the type before the product with v (float16 weights below 2^-30
+ * of the row's largest count as zero there); float32 inputs keep float32
  * accuracy throughout.
  *
  *   q, out     rows [num_rows] of [H][D], the strides in elements between

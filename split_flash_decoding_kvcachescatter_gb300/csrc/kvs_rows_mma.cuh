@@ -90,6 +90,12 @@ __device__ __forceinline__ int key_of_col(int n) {
 }
 
 // One warp's 16 rows: query fragments, running state, one tile at a time.
+// The state's m is the reference of its weights 2^(s - m): the running maximum
+// less kLift, so that float16 weights reach 2^10 and lose what is below 2^-35 of
+// the largest one (with a lift of 0 they lost what is below 2^-25: 131,072 keys
+// of 2^-26 each are 2^-9 of the sum).  All of a row's sums carry the factor, so
+// nothing else knows of it.  (2^6 of room are left for m's own rounding, which
+// is 2^5 where scores reach 2^26.)
 // Fragment coordinates: row r = lane / 4 (+ 8), q = lane % 4.
 template <typename T, int D>
 struct WarpRows {
@@ -98,6 +104,7 @@ struct WarpRows {
   // float32 with D = 128: q stays in L1 (its fragments would take 64 of the
   // 255 registers)
   static constexpr bool QL1 = F32 && D == 128;
+  static constexpr float kLift = std::is_same<T, __half>::value ? 10.f : 0.f;
   static constexpr int NQ = QL1 ? 1 : F32 ? D / 2 : D / 4;
 
   uint32_t qf[NQ];
@@ -247,7 +254,7 @@ struct WarpRows {
       for (int j = 0; j < NT; ++j) x = fmaxf(x, fmaxf(s[j][2 * hh], s[j][2 * hh + 1]));
       x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
       x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-      const float mn = fmaxf(m[hh], x * sl2);
+      const float mn = fmaxf(m[hh], x * sl2 - kLift);
       mb[hh] = mn == neg_inf_f() ? 0.f : mn;  // (no key so far: every weight is 2^-inf = 0)
       alpha[hh] = ex2f(m[hh] - mb[hh]);
       moved |= mn != m[hh];

@@ -44,6 +44,11 @@
 // The softmax keeps a reference maximum that moves only when a row's maximum
 // grows by more than 2^8, so P and O are rarely rescaled; the weights are
 // rounded to the type for the product, their sum is taken in float32 before.
+// (A second 16-bit part of P would need 128 more TMEM columns and half a
+// product more.)  In float16 the reference is 2^5 below the maximum, so that P
+// reaches 2^13 and loses what is below 2^-30 of the largest weight; with no such
+// lift 131,072 keys of 2^-26 each, 2^-9 of the sum, were lost.  (2^3 of room are
+// left for the reference's own rounding, 2^2 where scores reach 2^25.)
 
 #include <cmath>
 #include <mutex>
@@ -70,6 +75,8 @@ constexpr int kCThreads = 11 * 32;
 constexpr int kCFix = 384;
 constexpr int kCMinRange = 768;
 constexpr float kCRescale = 8.f;
+template <typename T>
+constexpr float kCLift = std::is_same<T, __half>::value ? 5.f : 0.f;
 constexpr uint32_t kCTmemCols = 512;
 constexpr int kCMaxDevices = 64;
 
@@ -595,7 +602,7 @@ __global__ void __launch_bounds__(kCThreads, 1)
 #pragma unroll
           for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], r[v + k]);
         }
-        const float cm = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
+        const float cm = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2 - kCLift<T>;
         // the reference maximum moves only when the row's grows by more
         // than 2^kCRescale: below that P stays in range and nothing needs
         // rescaling
