@@ -558,8 +558,13 @@ typedef struct kvs_paged_batch {
   int32_t num_seqs;           /* M >= 0 */
   int32_t num_rows;           /* rows of q, k, v and out, >= 0 */
   int32_t max_new;            /* the largest n_i that may occur, >= 1 */
-  int32_t max_pages;          /* >= 1; max_pages * page_size < 2^31 */
+  int32_t max_pages;          /* >= 1; max_pages * page_size < 2^31
+                                 (kvs_paged_attention: KVS_PAGED_MAX_KEYS at most) */
 } kvs_paged_batch;
+
+/* Rows of one sequence's pages, max_pages * page_size, that kvs_paged_attention
+ * takes at most; more is KVS_ERR_DIMS. */
+#define KVS_PAGED_MAX_KEYS (0x7fffffff - 4095)
 
 /*
  * kvs_rope_scatter_paged -- what precedes the attention of a step: rotary

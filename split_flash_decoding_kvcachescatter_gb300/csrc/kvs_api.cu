@@ -549,6 +549,9 @@ int kvs_paged_attention(const void *q, int64_t q_stride, const kvs_paged_cache *
                         kvs_stream_t stream) {
   int rc = check_paged(cache, batch, num_heads);
   if (rc != KVS_OK) return rc;
+  // The kernels count a sequence's keys and what they look ahead (a tile, a
+  // unit's fixed price, 32 tiles of pages: all under 2048 keys) in 32 bits.
+  if ((int64_t)batch->max_pages * cache->page_size > KVS_PAGED_MAX_KEYS) return KVS_ERR_DIMS;
   if (batch->num_seqs == 0 || batch->num_rows == 0) return KVS_OK;
   const int D = cache->head_dim;
   rc = check_paged_pointers(cache, batch);

@@ -63,6 +63,19 @@ def test_cache_and_batch_validation(L, ckw, bkw, code):
     assert rope(L, cache(**ckw), batch(**bkw)) == code
 
 
+@pytest.mark.parametrize("page", [16, 256, 4096, 1 << 20])
+def test_attention_keeps_clear_of_32_bit_key_counts(L, page):
+    """Lengths near 2^31 are reachable (a table may name one page many times), and the kernels look
+    ahead of a key: the table's reach stays 4,096 below.  The scatter has no such need."""
+    most = (2 ** 31 - 4096) // page
+    for M in (0, 2):
+        above = batch(M=M, rows=0, max_pages=most + 1)
+        if (most + 1) * page < 2 ** 31:
+            assert attend(L, cache(pages=1, page=page), above) == B.KVS_ERR_DIMS
+            assert rope(L, cache(pages=1, page=page), above) == B.KVS_OK
+        assert attend(L, cache(pages=1, page=page), batch(M=M, rows=0, max_pages=most)) == B.KVS_OK
+
+
 def test_null_structs(L):
     assert attend(L, None, batch()) == B.KVS_ERR_NULL
     assert attend(L, cache(), None) == B.KVS_ERR_NULL
