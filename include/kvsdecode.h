@@ -703,8 +703,8 @@ typedef struct kvs_logit_rules {
   const uint32_t *mask;           /* device [mask_count][ceil(vocab / 32)], bit j % 32 of word
                                      j / 32 set: j allowed; or NULL: no masks */
   const int32_t *mask_rows;       /* device [M]: row m's mask, negative: none; or NULL: mask m */
-  int32_t history_len;            /* entries of history, >= 0 */
-  int32_t bias_len;               /* entries of bias_ids and bias_values, >= 0 */
+  int32_t history_len;            /* entries of history, 0 .. 2^29 */
+  int32_t bias_len;               /* entries of bias_ids and bias_values, 0 .. 2^29 */
   int32_t mask_count;             /* rows of mask (>= M where mask_rows is NULL) */
 } kvs_logit_rules;
 

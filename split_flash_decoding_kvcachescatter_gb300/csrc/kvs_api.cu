@@ -583,6 +583,7 @@ int kvs_process_logits(const void *logits, int64_t logits_stride, void *out, int
   if (r.history && !r.history_offsets) return KVS_ERR_NULL;
   if (r.bias_ids && (!r.bias_values || !r.bias_offsets)) return KVS_ERR_NULL;
   if (r.history_len < 0 || r.history_len > (1 << 29) || r.bias_len < 0 ||
+      r.bias_len > (1 << 29) ||
       (r.mask && r.mask_count < (r.mask_rows ? 1 : M)))
     return KVS_ERR_DIMS;
   for (const void *p : {(const void *)r.history, (const void *)r.history_offsets,

@@ -126,6 +126,8 @@ def logits(L, x=A16, xs=1000, o=A16, os_=1000, dtype=B.KVS_F32, M=2, V=1000, ids
     (dict(ids=A16 + 2), B.KVS_ERR_ALIGN), (dict(history=A16), B.KVS_ERR_NULL),
     (dict(history=A16, history_offsets=A16, history_len=-1), B.KVS_ERR_DIMS),
     (dict(history=A16, history_offsets=A16, history_len=(1 << 29) + 1), B.KVS_ERR_DIMS),
+    (dict(bias_ids=A16, bias_values=A16, bias_offsets=A16, bias_len=-1), B.KVS_ERR_DIMS),
+    (dict(bias_ids=A16, bias_values=A16, bias_offsets=A16, bias_len=(1 << 29) + 1), B.KVS_ERR_DIMS),
     (dict(bias_ids=A16, bias_offsets=A16), B.KVS_ERR_NULL), (dict(bias_ids=A16, bias_values=A16), B.KVS_ERR_NULL),
     (dict(mask=A16, mask_count=1), B.KVS_ERR_DIMS), (dict(mask=A16, mask_rows=A16, mask_count=0), B.KVS_ERR_DIMS),
     (dict(repetition=A16 + 2), B.KVS_ERR_ALIGN), (dict(M=0, x=None, o=None, ids=None), B.KVS_OK),
