@@ -234,3 +234,51 @@ def test_refusals_of_the_binding():
     assert e.value.status == B.KVS_ERR_DIMS
     with pytest.raises(TypeError):
         B.kvs_process_logits(x, repetition=torch.ones(3, device=DEV))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("V,names", [(900, 40), (5000, 1), (40001, 6000), (152064, 152064)])
+def test_bias_lists_with_repeated_ids(dtype, V, names):
+    """Thousands of entries, most ids many times: the values add up in list order."""
+    M = 3
+    r = Rules(M, V, history=400, bias=0, seed=V)
+    g = np.random.default_rng(names)
+    r.b_ids = [g.integers(-1, names, n).astype(np.int32) for n in (4001, 33, 0)]
+    r.b_val = [g.uniform(-5, 5, len(i)).astype(np.float32) for i in r.b_ids]
+    for i in r.b_ids[:2]:
+        i[-1] = i[0] = min(V - 1, 5)  # one at least
+    x = logits(M, V, dtype, 20)
+    out = torch.empty_like(x)
+    ids = B.kvs_process_logits(x, out, **r.kwargs())
+    want = torch.from_numpy(r.apply(x.float().cpu().numpy(), np.float32)).to(x.dtype)
+    assert torch.equal(out.cpu(), want)
+    assert np.array_equal(ids.cpu().numpy(), oracle.argmax_rows(np.ascontiguousarray(want.float().numpy())))
+    only = B.kvs_process_logits(x, None, **r.kwargs())
+    B.kvs_process_logits(x, x, **r.kwargs())
+    assert torch.equal(only, ids) and torch.equal(x, out)
+
+
+def test_repeated_ids_cost_what_a_list_costs():
+    """One id twice in a list of 20,000: no more than a few passes over it."""
+    M, V, n = 4, 152064, 20000
+    x = logits(M, V, "f32", 21)
+    out, took = torch.empty_like(x), []
+    for repeat in (False, True):
+        r = Rules(M, V, history=10, bias=0, mask=False, seed=22)
+        r.b_ids = [np.random.default_rng(m).permutation(V)[:n].astype(np.int32) for m in range(M)]
+        r.b_val = [np.ones(n, np.float32)] * M
+        if repeat:
+            for i in r.b_ids:
+                i[n // 2] = i[7]
+        kw = r.kwargs()
+        ts = []
+        for _ in range(4):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            a.record()
+            ids = B.kvs_process_logits(x, out, **kw)
+            b.record()
+            torch.cuda.synchronize()
+            ts.append(a.elapsed_time(b))
+        check(x, out, ids, r)
+        took.append(min(ts))
+    assert took[1] < 10 * took[0] + 0.5, took
