@@ -77,8 +77,10 @@ typedef enum kvs_status {
   KVS_ERR_MEMORY = 10,     /* the device could not provide memory the library
                               itself holds (kvs_flash_decode_static) */
   KVS_ERR_PAGE = 11,       /* device: a page number outside [0, num_pages) */
-  KVS_ERR_ROWS = 12        /* device: row offsets that decrease, leave
+  KVS_ERR_ROWS = 12,       /* device: row offsets that decrease, leave
                               [0, num_rows], or span more than max_new rows */
+  KVS_ERR_OVERLAP = 13     /* rows of an output overlap rows of an input that
+                              the call does not take in place */
 } kvs_status;
 
 /* Element types of the paged-cache and logit entry points. */
@@ -595,7 +597,7 @@ typedef struct kvs_paged_batch {
  * row is NaN (bad position) or still the rotated q (bad page).  Where offsets
  * of some sequence are bad, rows of others may be left out too.
  * Errors: NULL, DIMS, UNSUPPORTED (also H / Hkv > 8 or H > 4096), ALIGN,
- * LAUNCH on the host; ROWS, POSITION, PAGE via d_status.
+ * OVERLAP, LAUNCH on the host; ROWS, POSITION, PAGE via d_status.
  */
 int kvs_rope_scatter_paged(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
                            const void *v, int64_t v_stride, void *q_out, int64_t q_out_stride,
@@ -661,7 +663,7 @@ int kvs_rope_frequencies(int rot_dim, double base, int kind, double factor, doub
  * The rows of a sequence with a bad position are NaN; where a sequence needs
  * a bad page, the rows that attend it are NaN and its other rows may be.
  * Errors: NULL, DIMS, UNSUPPORTED (also H / Hkv > 8 or H > 4096), ALIGN,
- * WORKSPACE, LAUNCH on the host; ROWS, POSITION, PAGE, TIMEOUT via d_status.
+ * OVERLAP, WORKSPACE, LAUNCH on the host; ROWS, POSITION, PAGE, TIMEOUT via d_status.
  */
 size_t kvs_paged_attention_workspace_bytes(int num_heads, int num_kv_heads, int head_dim,
                                            int max_new);
@@ -719,8 +721,9 @@ typedef struct kvs_logit_rules {
  * An offset pair that decreases or leaves [0, *_len] is KVS_ERR_ROWS via
  * d_status, a mask row at or past mask_count KVS_ERR_PAGE; that list or mask
  * counts as empty (no history, no biases, no mask).
- * Errors: DIMS (M < 0, vocab_size < 1, a stride or length too small), NULL,
- * ALIGN, UNSUPPORTED (dtype; a vocabulary of more than 2^19 tokens), LAUNCH.
+ * Errors: DIMS (M < 0, vocab_size < 1, a stride too small, a length out of
+ * range), NULL, ALIGN, UNSUPPORTED (dtype; a vocabulary of more than 2^19
+ * tokens), OVERLAP, LAUNCH.
  * M = 0 enqueues nothing.
  */
 int kvs_process_logits(const void *logits, int64_t logits_stride, void *out, int64_t out_stride,

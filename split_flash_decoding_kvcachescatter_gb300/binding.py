@@ -32,6 +32,7 @@ KVS_ERR_SLOT = 9
 KVS_ERR_MEMORY = 10
 KVS_ERR_PAGE = 11
 KVS_ERR_ROWS = 12
+KVS_ERR_OVERLAP = 13
 
 # kvs_dtype values
 KVS_F32, KVS_F16, KVS_BF16 = 0, 1, 2

@@ -103,6 +103,7 @@ const char *kvs_strerror(int status) {
     case KVS_ERR_MEMORY: return "the device could not provide the library's own buffer";
     case KVS_ERR_PAGE: return "a page or mask number is out of range";
     case KVS_ERR_ROWS: return "row offsets decrease or leave their list";
+    case KVS_ERR_OVERLAP: return "an output overlaps an input";
     default: return "unknown kvs status";
   }
 }
@@ -466,6 +467,38 @@ static int check_rows(const void *p, int64_t stride, int64_t row, int dtype) {
   return KVS_OK;
 }
 
+// `n` rows of `len` bytes, `stride` bytes apart (stride >= len).
+struct RowSpan {
+  uintptr_t at;
+  int64_t stride, len;
+};
+static RowSpan row_span(const void *p, int64_t stride, int64_t row, int dtype) {
+  const int64_t size = dtype == KVS_F32 ? 4 : 2;
+  return RowSpan{reinterpret_cast<uintptr_t>(p), stride * size, row * size};
+}
+
+// Whether some row of a shares a byte with some row of b, n rows each.  Blocks
+// of columns of one matrix do not, although their spans lie in each other.
+static bool rows_overlap(const RowSpan &a, const RowSpan &b, int64_t n) {
+  const int64_t d = (int64_t)(b.at - a.at);  // row j of b starts d + j b.stride behind a
+  if (d >= (n - 1) * a.stride + a.len || -d >= (n - 1) * b.stride + b.len) return false;
+  auto div_up = [](int64_t x, int64_t y) { return x > 0 ? (x + y - 1) / y : -(-x / y); };
+  if (a.stride == b.stride || n == 1) {
+    // rows i and i + k: apart unless -b.len < d + k stride < a.len
+    const int64_t k = std::max(div_up(1 - b.len - d, a.stride), 1 - n);
+    return k < n && d + k * a.stride < a.len;
+  }
+  for (int64_t i = 0; i < n; ++i) {
+    const int64_t j = std::max<int64_t>(div_up(i * a.stride + 1 - b.len - d, b.stride), 0);
+    if (j < n && d + j * b.stride < i * a.stride + a.len) return true;
+  }
+  return false;
+}
+// The same rows: an operator that may work in place does.
+static bool same_rows(const RowSpan &a, const RowSpan &b, int64_t n) {
+  return a.at == b.at && (a.stride == b.stride || n == 1);
+}
+
 static kvs::PagedArgs paged_args(const kvs_paged_cache *cache, const kvs_paged_batch *batch) {
   int shift = 0;
   while ((1 << shift) < cache->page_size) ++shift;
@@ -492,6 +525,13 @@ int kvs_rope_scatter_paged(const void *q, int64_t q_stride, const void *k, int64
   if (rc != KVS_OK) return rc;
   if (rot_dim > 0 && !inv_freq) return KVS_ERR_NULL;
   if (!aligned(inv_freq, 4)) return KVS_ERR_ALIGN;
+  const int64_t n = batch->num_rows;
+  const RowSpan to = row_span(q_out, q_out_stride, (int64_t)num_heads * D, dtype);
+  const RowSpan from = row_span(q, q_stride, (int64_t)num_heads * D, dtype);
+  if ((!same_rows(from, to, n) && rows_overlap(from, to, n)) ||
+      rows_overlap(row_span(k, k_stride, (int64_t)Hkv * D, dtype), to, n) ||
+      rows_overlap(row_span(v, v_stride, (int64_t)Hkv * D, dtype), to, n))
+    return KVS_ERR_OVERLAP;
   return kvs::launch_rope_scatter(q, q_stride, k, k_stride, v, v_stride, q_out, q_out_stride,
                                   cache->k_pages, cache->v_pages, paged_args(cache, batch),
                                   inv_freq, num_heads, Hkv, D, dtype, rot_dim, interleaved ? 1 : 0,
@@ -563,6 +603,10 @@ int kvs_paged_attention(const void *q, int64_t q_stride, const kvs_paged_cache *
   if (workspace_bytes < kvs::paged_attention_workspace_bytes(num_heads, cache->num_kv_heads, D,
                                                              batch->max_new))
     return KVS_ERR_WORKSPACE;
+  if (rows_overlap(row_span(q, q_stride, (int64_t)num_heads * D, cache->dtype),
+                   row_span(out, out_stride, (int64_t)num_heads * D, cache->dtype),
+                   batch->num_rows))
+    return KVS_ERR_OVERLAP;
   return kvs::launch_paged_attention(q, q_stride, *cache, paged_args(cache, batch), out,
                                      out_stride, num_heads, workspace, d_status,
                                      reinterpret_cast<cudaStream_t>(stream));
@@ -593,6 +637,11 @@ int kvs_process_logits(const void *logits, int64_t logits_stride, void *out, int
                         (const void *)r.bias_offsets, (const void *)r.mask,
                         (const void *)r.mask_rows})
     if (!aligned(p, 4)) return KVS_ERR_ALIGN;
+  if (out) {
+    const RowSpan from = row_span(logits, logits_stride, vocab_size, dtype);
+    const RowSpan to = row_span(out, out_stride, vocab_size, dtype);
+    if (!same_rows(from, to, M) && rows_overlap(from, to, M)) return KVS_ERR_OVERLAP;
+  }
   return kvs::launch_logits(logits, logits_stride, out, out_stride, dtype, M, vocab_size, r,
                             token_ids, d_status, reinterpret_cast<cudaStream_t>(stream));
 }

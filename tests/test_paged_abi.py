@@ -4,6 +4,7 @@ import ctypes
 
 import numpy as np
 import pytest
+import torch
 
 from split_flash_decoding_kvcachescatter_gb300 import binding as B
 from split_flash_decoding_kvcachescatter_gb300 import build as kbuild
@@ -134,6 +135,61 @@ def logits(L, x=A16, xs=1000, o=A16, os_=1000, dtype=B.KVS_F32, M=2, V=1000, ids
 ])
 def test_process_logits_validation(L, kw, code):
     assert logits(L, **kw) == code
+
+
+# ---- outputs that overlap inputs ----------------------------------------------------------------
+# (The overlap check is the last one.  A call that passes it has no device to run on here; where
+# there is one, nothing may be launched at these addresses.)
+no_gpu = pytest.mark.skipif(torch.cuda.is_available(), reason="would launch at made-up addresses")
+
+
+def shares_a_byte(a, sa, la, b, sb, lb, n):
+    at = set()
+    for i in range(n):
+        at.update(range(a + i * sa, a + i * sa + la))
+    return any(not at.isdisjoint(range(b + j * sb, b + j * sb + lb)) for j in range(n))
+
+
+@no_gpu
+def test_attention_out_over_queries(L):
+    rng = np.random.default_rng(0)
+    seen = set()
+    for _ in range(400):
+        n = int(rng.integers(1, 7))
+        qs, os_ = (int(x) for x in 256 + 4 * rng.integers(0, 80, 2))
+        if rng.random() < 0.5:
+            os_ = qs
+        out = A16 + 16 * int(rng.integers(-900, 900))
+        want = shares_a_byte(A16, qs * 4, 1024, out, os_ * 4, 1024, n)
+        seen.add((want, qs == os_))
+        got = attend(L, cache(), batch(rows=n), qs=qs, out=out, os_=os_)
+        assert got == (B.KVS_ERR_OVERLAP if want else B.KVS_ERR_LAUNCH), (n, qs, os_, out - A16)
+    assert len(seen) == 4
+
+
+@no_gpu
+@pytest.mark.parametrize("kw,overlap", [
+    (dict(o=A16), False), (dict(o=A16, os_=272), True), (dict(o=A16, os_=272, rows=1), False),
+    (dict(o=A16 + 16), True), (dict(o=A16 + 1024, qs=512, os_=512), False), (dict(o=A16 + 1008, qs=512, os_=512), True),
+    (dict(o=A16 + 5 * 1024), False), (dict(o=A16 + 5 * 1024 - 16), True),
+    (dict(k=A16 + 8192, o=A16 + 8192 - 1024, rows=1), False), (dict(k=A16 + 8192, o=A16 + 8192 - 1008, rows=1), True),
+    (dict(v=A16 + 8192, o=A16 + 8192 + 512, rows=1), False), (dict(v=A16 + 8192, o=A16 + 8192 + 496, rows=1), True),
+])
+def test_rope_queries_out(L, kw, overlap):
+    far = dict(k=A16 + (1 << 16), v=A16 + (1 << 17))
+    rows = kw.pop("rows", 5)
+    assert rope(L, cache(), batch(rows=rows), **{**far, **kw}) == \
+        (B.KVS_ERR_OVERLAP if overlap else B.KVS_ERR_LAUNCH)
+
+
+@no_gpu
+@pytest.mark.parametrize("kw,overlap", [
+    (dict(), False), (dict(os_=1001), True), (dict(os_=1001, M=1), False), (dict(o=A16 + 4), True),
+    (dict(o=A16 + 4000, xs=2000, os_=2000), False), (dict(o=A16 + 3996, xs=2000, os_=2000), True),
+    (dict(o=A16 + 8000), False), (dict(o=A16 + 7996), True), (dict(o=A16 - 8000), False), (dict(o=None), False),
+])
+def test_logits_out(L, kw, overlap):
+    assert logits(L, **kw) == (B.KVS_ERR_OVERLAP if overlap else B.KVS_ERR_LAUNCH)
 
 
 # ---- frequency tables -------------------------------------------------------------------------

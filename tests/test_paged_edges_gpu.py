@@ -187,3 +187,20 @@ def test_more_logit_rows_than_a_grid_holds(V):
     out = torch.empty_like(x)
     ids = B.kvs_process_logits(x, out, **r.kwargs())
     check_logits(x, out, ids, r)
+
+
+def test_partial_overlaps_are_refused_and_column_blocks_are_not():
+    b = make_case([1, 20], [30, 0], 8, 2, 64, "f16", 16, seed=12)
+    wide = torch.zeros(b.rows, 2 * 512, dtype=b.dtype, device=DEV)
+    heads = lambda t: t.unflatten(1, (8, 64))
+    q, out, across = (heads(wide[:, a:a + 512]) for a in (0, 512, 256))
+    q.copy_(b.q)
+    b.check(b.attend(q=q, out=out))
+    inv, _ = B.kvs_rope_frequencies(64)
+    for call in (lambda: b.attend(q=q, out=across),
+                 lambda: B.kvs_rope_scatter_paged(q, b.new_k, b.new_v, across, b.cache, b.batch, inv),
+                 lambda: B.kvs_process_logits(wide[:, :512], wide[:, 500:1012])):
+        with pytest.raises(B.KvsError) as e:
+            call()
+        assert e.value.status == B.KVS_ERR_OVERLAP
+    assert torch.equal(q, b.q)
