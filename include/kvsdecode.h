@@ -622,8 +622,8 @@ int kvs_rope_scatter_paged(const void *q, int64_t q_stride, const void *k, int64
  *   inv_freq  out  float[rot_dim / 2], host
  *   scale     out  float, host (nullable)
  *   base > 0; factor >= 1 (not read by PLAIN); original_len > 0 and
- *   0 < slow < fast (read by YARN and BANDS only); NTK: rot_dim >= 4; YARN:
- *   base > 1
+ *   0 < slow < fast (read by YARN and BANDS only); all of them finite; NTK:
+ *   rot_dim >= 4; YARN: base > 1; no w_j above 1e6
  * Errors: DIMS (rot_dim < 2 or odd, an unknown kind, a value out of range),
  * NULL.
  */

@@ -544,7 +544,9 @@ int kvs_rope_frequencies(int rot_dim, double base, int kind, double factor, doub
   if (rot_dim < 2 || rot_dim % 2 != 0 || kind < KVS_ROPE_PLAIN || kind > KVS_ROPE_BANDS ||
       !(base > 0.0) || (kind != KVS_ROPE_PLAIN && !(factor >= 1.0)) ||
       (ramp && (!(original_len > 0.0) || !(slow > 0.0) || !(fast > slow))) ||
-      (kind == KVS_ROPE_NTK && rot_dim < 4) || (kind == KVS_ROPE_YARN && !(base > 1.0)))
+      (kind == KVS_ROPE_NTK && rot_dim < 4) || (kind == KVS_ROPE_YARN && !(base > 1.0)) ||
+      !std::isfinite(base) || (kind != KVS_ROPE_PLAIN && !std::isfinite(factor)) ||
+      (ramp && (!std::isfinite(original_len) || !std::isfinite(fast))))
     return KVS_ERR_DIMS;
   if (!inv_freq) return KVS_ERR_NULL;
   const double two_pi = 6.28318530717958647693;
@@ -561,6 +563,9 @@ int kvs_rope_frequencies(int rot_dim, double base, int kind, double factor, doub
     last = std::min(rot_dim - 1.0, std::ceil(pair_of(slow)));
     if (last <= first) last = first + 0.001;
   }
+  // (the largest entry is the first, or with a base below 1 the last)
+  const double fastest = std::max(1.0, std::pow(base, 2.0 / rot_dim - 1.0));
+  if (!(fastest <= 1e6)) return KVS_ERR_DIMS;
   for (int j = 0; j < rot_dim / 2; ++j) {
     double w = std::pow(base, -2.0 * j / rot_dim);
     double keep = 1.0;  // share of w kept, the rest is w / factor

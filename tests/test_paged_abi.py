@@ -240,6 +240,16 @@ def test_frequency_refusals(L, kw):
     assert table(L, **kw)[0] == B.KVS_ERR_DIMS
 
 
+@pytest.mark.parametrize("kw", [
+    dict(base=np.inf), dict(kind=1, factor=np.inf), dict(kind=2, factor=np.inf), dict(kind=3, factor=np.inf, length=100.0),
+    dict(kind=3, factor=2.0, length=np.inf), dict(kind=4, factor=2.0, length=np.inf),
+    dict(kind=4, factor=2.0, length=100.0, fast=np.inf), dict(base=1e-7), dict(base=1e-300), dict(base=np.inf, kind=3, factor=2.0, length=100.0)])
+def test_tables_that_the_rotation_does_not_take(L, kw):
+    """Finite entries up to 1e6 are what kvs_rope_scatter_paged asks for."""
+    assert table(L, 64, **kw)[0] == B.KVS_ERR_DIMS
+    assert table(L, 64, base=1e-6)[0] == 0 and table(L, 64, base=1e-6)[1].max() <= 1e6
+
+
 @pytest.mark.parametrize("base", [1.0, 0.5])
 def test_yarn_needs_pairs_of_different_speed(L, base):
     """With base <= 1 no pair is slower than the first, and the ramp over the pairs means nothing."""
