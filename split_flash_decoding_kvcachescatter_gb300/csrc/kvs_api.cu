@@ -558,7 +558,9 @@ int kvs_rope_frequencies(int rot_dim, double base, int kind, double factor, doub
     return rot_dim * std::log(original_len / (turns * two_pi)) / (2.0 * std::log(base));
   };
   double first = 0.0, last = 0.0;
+  bool none = false;  // not even pair 0 turns `slow` times
   if (kind == KVS_ROPE_YARN) {
+    none = pair_of(slow) < 0.0;
     first = std::max(0.0, std::floor(pair_of(fast)));
     last = std::min(rot_dim - 1.0, std::ceil(pair_of(slow)));
     if (last <= first) last = first + 0.001;
@@ -570,7 +572,8 @@ int kvs_rope_frequencies(int rot_dim, double base, int kind, double factor, doub
     double w = std::pow(base, -2.0 * j / rot_dim);
     double keep = 1.0;  // share of w kept, the rest is w / factor
     if (kind == KVS_ROPE_LINEAR) keep = 0.0;
-    if (kind == KVS_ROPE_YARN) keep = 1.0 - std::min(1.0, std::max(0.0, (j - first) / (last - first)));
+    if (kind == KVS_ROPE_YARN)
+      keep = none ? 0.0 : 1.0 - std::min(1.0, std::max(0.0, (j - first) / (last - first)));
     if (kind == KVS_ROPE_BANDS)
       keep = std::min(1.0, std::max(0.0, (original_len * w / two_pi - slow) / (fast - slow)));
     if (kind == KVS_ROPE_LINEAR || ramp) w = keep * w + (1.0 - keep) * w / factor;

@@ -250,6 +250,14 @@ def test_tables_that_the_rotation_does_not_take(L, kw):
     assert table(L, 64, base=1e-6)[0] == 0 and table(L, 64, base=1e-6)[1].max() <= 1e6
 
 
+@pytest.mark.parametrize("length,slow", [(3.0, 1.0), (6.0, 1.0), (100.0, 20.0), (0.01, 1.0)])
+def test_yarn_where_no_pair_turns_the_slow_number_of_times(L, length, slow):
+    """Pair 0 turns length / 2 pi times: below `slow` it is compressed like the others."""
+    rc, got, _ = table(L, 64, 10000.0, 3, 4.0, length, slow, 32.0)
+    want = 10000.0 ** (-2.0 * np.arange(32) / 64) / 4
+    assert rc == 0 and np.abs(got / want - 1).max() <= 2.0 ** -23
+
+
 @pytest.mark.parametrize("base", [1.0, 0.5])
 def test_yarn_needs_pairs_of_different_speed(L, base):
     """With base <= 1 no pair is slower than the first, and the ramp over the pairs means nothing."""
