@@ -267,13 +267,13 @@ __global__ void __launch_bounds__(kCThreads, 1)
     prefetch_map(&qmap);
     prefetch_map(&kmap);
     prefetch_map(&vmap);
-    for (int j = 0; j < C::NBAR; ++j) mbar_init(&bars[j], 1);
-    for (int x = 0; x < 2; ++x) {
-      mbar_init(&pfull[x], 4);  // (an arrival a warp: 128 of them took some 200 cycles)
-      mbar_init(&wgbar[x], 4);
+    for (int j = 0; j < C::NBAR; ++j) {  // each once
+      uint64_t *bar = bars + j;
+      const bool of_warpgroup = bar == sread || bar == pfull || bar == pfull + 1 || bar == wgbar ||
+                                bar == wgbar + 1;
+      // (an arrival a warp: one a thread took some 200 cycles)
+      mbar_init(bar, of_warpgroup ? 4 : bar >= ufree && bar < ufree + kCUnits ? 10 : 1);
     }
-    mbar_init(sread, 4);
-    for (int j = 0; j < kCUnits; ++j) mbar_init(&ufree[j], 10);
     *abort = 0;
     fence_mbar_init();
   }
