@@ -80,6 +80,18 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   }
 }
 
+// (a, b) = hi + lo in 16 bits each: hi is rounded, lo what it leaves, rounded.
+template <typename T>
+__device__ __forceinline__ void split2(float a, float b, uint32_t &hi, uint32_t &lo) {
+  hi = pack2<T>(a, b);
+  if constexpr (std::is_same<T, __half>::value) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+    lo = pack2<T>(a - f.x, b - f.y);
+  } else {
+    lo = pack2<T>(a - __uint_as_float(hi << 16), b - __uint_as_float(hi & 0xffff0000u));
+  }
+}
+
 // Key (of 8) that column n of a score fragment stands for.  16-bit types:
 // n.  float32: 0 5 2 7 4 1 6 3, which makes the shared-memory reads of both
 // K (8 rows by n, 4 pieces) and V (rows of columns 2q, and of 2q + 1)
@@ -163,7 +175,9 @@ struct WarpRows {
   }
 
   // One tile at (K at sk, V at sv).  lim[hh]: keys of the tile that row half
-  // hh attends (>= KT: all of them).
+  // hh attends (>= KT: all of them).  kFew (16-bit types): the unit has 8 rows
+  // at most, and those behind them carry the second parts of their weights.
+  template <bool kFew = false>
   __device__ __forceinline__ void tile(uint32_t sk, uint32_t sv, float sl2, const int (&lim)[2]) {
     constexpr int NT = KT / 8;
     [[maybe_unused]] constexpr int kGroup = 16 * D * (int)sizeof(T);  // bytes of 16 keys
@@ -261,17 +275,19 @@ struct WarpRows {
       m[hh] = mn;
     }
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) s[j][e] = ex2f(fmaf(s[j][e], sl2, -mb[e >> 1]));
-#pragma unroll
     for (int hh = 0; hh < 2; ++hh) {
+      if (kFew && hh == 1) break;
       float t = 0.f;
 #pragma unroll
-      for (int j = 0; j < NT; ++j) t += s[j][2 * hh] + s[j][2 * hh + 1];
+      for (int j = 0; j < NT; ++j) {
+        s[j][2 * hh] = ex2f(fmaf(s[j][2 * hh], sl2, -mb[hh]));
+        s[j][2 * hh + 1] = ex2f(fmaf(s[j][2 * hh + 1], sl2, -mb[hh]));
+        t += s[j][2 * hh] + s[j][2 * hh + 1];
+      }
       l[hh] = l[hh] * alpha[hh] + t;  // this lane's columns; summed over the lanes at the end
     }
     if (!F32 && __any_sync(0xffffffffu, moved)) {
+      if (kFew) alpha[1] = alpha[0];
 #pragma unroll
       for (int j = 0; j < D / 8; ++j)
 #pragma unroll
@@ -321,18 +337,34 @@ struct WarpRows {
           for (int k = 0; k < 4; ++k) o[b * 4 + e][k] = fmaf(o[b * 4 + e][k], alpha[k >> 1], t[e][k]);
       }
     } else {
+      // Each weight in two 16-bit parts, so that what one rounding would lose
+      // (a third of the outputs then differed in their last bit) stays.  Units of
+      // 8 rows at most, which is every single token: row r's second part stands
+      // where row r + 8 would, and costs no product; finish() adds the two sums.
+      // More rows: a second product (it took 2 to 6 % of a step's time; the form
+      // for few rows takes none).
       const int row = (lane & 7) + (((lane >> 3) & 1) << 3);
 #pragma unroll
       for (int gg = 0; gg < KT / 16; ++gg) {
-        const uint32_t a[4] = {pack2<T>(s[2 * gg][0], s[2 * gg][1]),
-                               pack2<T>(s[2 * gg][2], s[2 * gg][3]),
-                               pack2<T>(s[2 * gg + 1][0], s[2 * gg + 1][1]),
-                               pack2<T>(s[2 * gg + 1][2], s[2 * gg + 1][3])};
+        uint32_t a[4], al[4];
+        if constexpr (kFew) {
+          split2<T>(s[2 * gg][0], s[2 * gg][1], a[0], a[1]);
+          split2<T>(s[2 * gg + 1][0], s[2 * gg + 1][1], a[2], a[3]);
+        } else {
+          split2<T>(s[2 * gg][0], s[2 * gg][1], a[0], al[0]);
+          split2<T>(s[2 * gg][2], s[2 * gg][3], a[1], al[1]);
+          split2<T>(s[2 * gg + 1][0], s[2 * gg + 1][1], a[2], al[2]);
+          split2<T>(s[2 * gg + 1][2], s[2 * gg + 1][3], a[3], al[3]);
+        }
 #pragma unroll
         for (int c = 0; c < D / 8; c += 2) {
           const int pc = ((c + (lane >> 4)) & 7) ^ (row & 7);
           uint32_t b[4];
           ldsm4t(sv + gg * kGroup + (c >> 3) * 2048 + row * 128 + pc * 16, b);
+          if constexpr (!kFew) {
+            mma16<T>(o[c], al, b[0], b[1]);
+            mma16<T>(o[c + 1], al, b[2], b[3]);
+          }
           mma16<T>(o[c], a, b[0], b[1]);
           mma16<T>(o[c + 1], a, b[2], b[3]);
         }
@@ -340,7 +372,15 @@ struct WarpRows {
     }
   }
 
+  template <bool kFew = false>
   __device__ __forceinline__ void finish() {  // row sums over the four lanes of a row
+    if constexpr (kFew) {
+#pragma unroll
+      for (int j = 0; j < D / 8; ++j) {
+        o[j][0] += o[j][2];
+        o[j][1] += o[j][3];
+      }
+    }
 #pragma unroll
     for (int hh = 0; hh < 2; ++hh) {
       l[hh] += __shfl_xor_sync(0xffffffffu, l[hh], 1);

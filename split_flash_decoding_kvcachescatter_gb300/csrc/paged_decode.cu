@@ -145,8 +145,8 @@ __device__ __forceinline__ void drain_ring(const Rings &rg, int ring, uint32_t n
 
 // The ring's tiles of [t_lo, t_hi) against the warp's rows; n as in
 // fill_ring.  False when a wait ran out; poison: a bad page was among them.
-template <typename T, int D, int W, bool kPoll>
-__device__ __forceinline__ bool consume_ring(WarpRows<T, D> &w, const Rings &rg, int ring, int t_lo,
+template <typename T, int D, int W, bool kPoll, bool kFew>
+__device__ __forceinline__ bool consume_tiles(WarpRows<T, D> &w, const Rings &rg, int ring, int t_lo,
                                              int t_hi, int keys, const int (&reach)[2], float sl2,
                                              uint32_t &n, bool &poison) {
   using C = DGeo<T, D, W>;
@@ -170,11 +170,28 @@ __device__ __forceinline__ bool consume_ring(WarpRows<T, D> &w, const Rings &rg,
       __syncwarp();
     }
     const int lim[2] = {reach[0] - t * C::KT, reach[1] - t * C::KT};
-    w.tile(smem_addr(sk), smem_addr(sk + C::TILE), sl2, lim);
+    w.template tile<kFew>(smem_addr(sk), smem_addr(sk + C::TILE), sl2, lim);
     __syncwarp();
     if (lane == 0) mbar_arrive(&rg.empty[st]);
   }
   return true;
+}
+
+// The same for a unit of `rows` rows, with the row sums finished.
+template <typename T, int D, int W, bool kPoll>
+__device__ __forceinline__ bool consume_ring(WarpRows<T, D> &w, const Rings &rg, int ring, int rows,
+                                             int t_lo, int t_hi, int keys, const int (&reach)[2],
+                                             float sl2, uint32_t &n, bool &poison) {
+  bool ok;
+  if (!std::is_same<T, float>::value && rows <= 8) {
+    constexpr bool kFew = !std::is_same<T, float>::value;
+    ok = consume_tiles<T, D, W, kPoll, kFew>(w, rg, ring, t_lo, t_hi, keys, reach, sl2, n, poison);
+    w.template finish<kFew>();
+  } else {
+    ok = consume_tiles<T, D, W, kPoll, false>(w, rg, ring, t_lo, t_hi, keys, reach, sl2, n, poison);
+    w.finish();
+  }
+  return ok;
 }
 
 // A warp's state into shared memory: [16][D + 4] accumulators, [16] (m, l).
@@ -318,11 +335,11 @@ __global__ void __launch_bounds__(kDThreads, 1)
       for (int hh = 0; hh < 2; ++hh)
         reach[hh] = f.s.p + f.tok0 + min(lane / 4 + 8 * hh, rows - 1) / G + 1;
       bool poison = false;
-      if (!consume_ring<T, D, kDW, kPoll>(w, rg, warp, f.t_lo, f.t_hi, f.keys, reach, sl2, n, poison)) {
+      if (!consume_ring<T, D, kDW, kPoll>(w, rg, warp, rows, f.t_lo, f.t_hi, f.keys, reach, sl2, n,
+                                         poison)) {
         if (lane == 0) give_up(abort, d_status, epoch);
         return;
       }
-      w.finish();
       if (poison) w.l[0] = w.l[1] = nan;
       const bool whole = f.t_hi - f.t_lo == f.nt;
       const size_t slot = 2 * (size_t)b + (f.t_lo == 0 ? 1 : 0);
@@ -474,8 +491,7 @@ __global__ void __launch_bounds__(2 * W * 32, 4 / W)
 #pragma unroll
     for (int hh = 0; hh < 2; ++hh) reach[hh] = s.p + min(lane / 4 + 8 * hh, rows - 1) / G + 1;
     bool poison = false;
-    ok = consume_ring<T, D, W, kPoll>(w, rg, warp, t_lo, t_hi, keys, reach, sl2, n, poison);
-    w.finish();
+    ok = consume_ring<T, D, W, kPoll>(w, rg, warp, rows, t_lo, t_hi, keys, reach, sl2, n, poison);
     if (poison) w.l[0] = w.l[1] = __int_as_float(0x7fc00000);
     put_state<T, D>(w, macc + warp * 16 * (D + 4), mml + warp * 16);
     __syncwarp();

@@ -46,10 +46,10 @@ def norm_limit(o, spread, size, L, dtype, weights):
     # partial sum, `size` at most), the sum of the small products and its addition; float32's
     # three TF32 products leave 2^-21 of a product; the exponent's rounding, and ex2's 2^-22.
     ds = size * ((D / 8 + 3) * 2.0 ** -23 + (2.0 ** -21 if f32 else 0)) + 2.0 ** -22
-    # Weights times v: in 16 bits L / 16 truncated additions to one accumulator; in float32
-    # twelve a tile, then one rounded addition a tile (roundings of either sign: the root of
+    # Weights times v: in 16 bits L / 16 truncated additions to one accumulator, twice as many
+    # for weights in two parts; in float32 twelve a tile, then one rounded addition a tile (roundings of either sign: the root of
     # their number), and the product's 2^-21.  The sum of the weights: rounded additions.
-    dv = (12 * 2.0 ** -23 + 2.0 ** -21 + math.sqrt(L / 16) * 2.0 ** -24 if f32 else L / 16 * 2.0 ** -23)
+    dv = (12 * 2.0 ** -23 + 2.0 ** -21 + math.sqrt(L / 16) * 2.0 ** -24 if f32 else L / 8 * 2.0 ** -23)
     dv += math.sqrt(L) * 2.0 ** -24 + 8 * 2.0 ** -24
     # An error e_j of weight j moves o by w_j e_j (v_j - o).  Errors of different weights are
     # independent of each other and of v: the squares add up, mean square a third of the

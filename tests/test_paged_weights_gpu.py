@@ -65,3 +65,16 @@ def test_one_key_far_above_the_others(n, p, columns, dtype):
         assert int(b.status.item()) == 0
         rel = torch.finfo(b.dtype).eps + 2.0 ** -20
         assert ((out.double() + 0.75).abs() <= 0.75 * rel).all(), (size, float(out.min()), float(out.max()))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("p,columns", [(900, 2), (5000, 2), (5000, 2 ** 13)])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_decode_steps_hold_their_weights_in_more_than_16_bits(p, columns, dtype, D):
+    """The output is the definition's, rounded once, but where float32's errors carry it over the
+    middle of two numbers: they are under 2^-16 of it, a hundredth of such numbers' distance in
+    float16.  With weights rounded to 16 bits a quarter of the elements differ."""
+    b = Paged([1] * 4, [p, p - 77, p // 2, 300], 16, 4, D, dtype, 64, seed=D, columns=columns)
+    out = b.attend()
+    want, _ = b.reference()
+    assert float((out == want.to(b.dtype)).double().mean()) > 0.95
