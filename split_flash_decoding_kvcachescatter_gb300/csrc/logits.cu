@@ -391,9 +391,11 @@ __global__ void __launch_bounds__(kLogitThreads, 2) logits_kernel(LogitArgs a) {
 }
 
 struct LogitInfo {
-  int active[5] = {0};  // resident clusters of 1, 2, 4, 8, 16 blocks with no words
+  // resident clusters of 1, 2, 4, 8, 16 blocks, with one block an SM and with two
+  int active[2][5] = {{0}, {0}};
   int top = 0;          // index of the largest cluster size
   int smem = 0;         // bytes of words a block may have
+  int two = 0;          // ... of which an SM holds two
   bool configured = false;
 };
 
@@ -404,13 +406,16 @@ const LogitInfo *logit_info(int dev) {
   std::lock_guard<std::mutex> lk(mu);
   if (!info[dev].configured) {
     LogitInfo rec;
-    int optin = 0;
+    int optin = 0, of_sm = 0;
     if (cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) !=
-        cudaSuccess) {
+            cudaSuccess ||
+        cudaDeviceGetAttribute(&of_sm, cudaDevAttrMaxSharedMemoryPerMultiprocessor, dev) !=
+            cudaSuccess) {
       cudaGetLastError();
       return nullptr;
     }
     rec.smem = optin - 1024;
+    rec.two = of_sm / 2 - 2048;  // (1 KB reserved a block, and its static arrays)
     if (cudaFuncSetAttribute(logits_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              rec.smem) != cudaSuccess) {
       cudaGetLastError();
@@ -426,7 +431,6 @@ const LogitInfo *logit_info(int dev) {
       cudaLaunchConfig_t cfg = {};
       cfg.gridDim = dim3(1u << k, 1, 1);
       cfg.blockDim = dim3(kLogitThreads, 1, 1);
-      cfg.dynamicSmemBytes = 32 << 10;
       cudaLaunchAttribute attr[1];
       attr[0].id = cudaLaunchAttributeClusterDimension;
       attr[0].val.clusterDim.x = 1u << k;
@@ -434,16 +438,19 @@ const LogitInfo *logit_info(int dev) {
       attr[0].val.clusterDim.z = 1;
       cfg.attrs = attr;
       cfg.numAttrs = 1;
-      int n = 0;
-      if (cudaOccupancyMaxActiveClusters(&n, logits_kernel<T>, &cfg) != cudaSuccess) {
-        cudaGetLastError();
-        n = 0;
+      for (int of = 0; of < 2; ++of) {
+        cfg.dynamicSmemBytes = of ? rec.two : rec.smem;
+        int n = 0;
+        if (cudaOccupancyMaxActiveClusters(&n, logits_kernel<T>, &cfg) != cudaSuccess) {
+          cudaGetLastError();
+          n = 0;
+        }
+        rec.active[of][k] = n;
       }
-      if (n <= 0) break;
-      rec.active[k] = n;
+      if (rec.active[0][k] <= 0) break;
       rec.top = k;
     }
-    if (rec.active[0] < 1) return nullptr;
+    if (rec.active[0][0] < 1) return nullptr;
     rec.configured = true;
     info[dev] = rec;
   }
@@ -457,17 +464,30 @@ int launch_logits_impl(LogitArgs a, cudaStream_t stream) {
     return KVS_ERR_LAUNCH;
   const LogitInfo *li = logit_info<T>(dev);
   if (!li) return KVS_ERR_LAUNCH;
-  // The largest cluster whose clusters for all M rows are resident at once
-  // (one wave) with slices of 8 KB or more; then larger ones until a slice's
-  // words fit a block's shared memory.
   const long long row_bytes = (long long)a.V * sizeof(T);
   auto slice_of = [&](int k) { return ((a.V + (1 << k) - 1) / (1 << k) + 31) / 32 * 32; };
   const bool counts = a.r.history != nullptr || a.r.bias_ids != nullptr;
   auto words_of = [&](int k) { return counts ? (long long)(slice_of(k) + 4) * 4 : 0ll; };
+  // The largest cluster whose clusters for all M rows are resident at once (one
+  // wave; words past `two` leave an SM one block) with slices of 8 KB or more.
+  // Where none is: the smallest whose words let an SM hold two blocks, or else
+  // the smallest whose words fit.  With history and
+  // biases, us at clusters of 1, 2, 4, 8, 16 (-: does not fit), * chosen:
+  //   48 rows of 152,064, float32     -     -    31.0  24.4*  33.6
+  //   300 rows of 152,064, float32    -     -     138  108*   177
+  //   128 rows of 128,256, bfloat16   -     -    60.2  47.8*  80.8
+  //   67 rows of 32,001, bfloat16   16.7  12.1   10.9* 16.5   34.2
+  //   300 rows of 32,001, bfloat16  36.7  30.1*  46.1  71.3   160
+  //   304 rows of 50,000, float32   43.2  34.8*  50.0  70.6   138
+  //   15 rows of 262,144, bfloat16    -     -      -   16.5*  21.1
+  auto resident = [&](int k) { return words_of(k) > li->smem ? 0 : li->active[words_of(k) <= li->two][k]; };
   int k = li->top;
-  while (k > 0 && (a.M > li->active[k] || (row_bytes >> k) < (8 << 10))) --k;
-  while (k < li->top && words_of(k) > li->smem) ++k;
-  if (words_of(k) > li->smem) return KVS_ERR_UNSUPPORTED;
+  while (k >= 0 && (a.M > resident(k) || (row_bytes >> k) < (8 << 10))) --k;
+  for (const int most : {li->two, li->smem})
+    if (k < 0)
+      for (int c = li->top; c >= 0; --c)
+        if (words_of(c) <= most) k = c;
+  if (k < 0) return KVS_ERR_UNSUPPORTED;
   a.slice = slice_of(k);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(1u << k, (unsigned)(a.M < 65535 ? a.M : 65535), 1);

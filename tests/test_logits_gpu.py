@@ -282,3 +282,14 @@ def test_repeated_ids_cost_what_a_list_costs():
         check(x, out, ids, r)
         took.append(min(ts))
     assert took[1] < 10 * took[0] + 0.5, took
+
+
+@pytest.mark.parametrize("M,V,dtype", [(36, 152064, "f32"), (37, 152064, "bf16"), (75, 32001, "bf16"), (300, 32001, "f16"),
+                                       (153, 50000, "f32"), (15, 262144, "bf16"), (3, 2 ** 19, "f32")])
+def test_batches_around_the_cluster_rule(M, V, dtype):
+    """One row more than are resident at once, words that leave an SM one block, the largest vocabulary."""
+    r = Rules(M, V, history=200, bias=4, seed=M)
+    x = logits(M, V, dtype, M)
+    out = torch.empty_like(x)
+    ids = B.kvs_process_logits(x, out, **r.kwargs())
+    check(x, out, ids, r)
