@@ -145,9 +145,10 @@ __global__ void __launch_bounds__(kRopeThreads, 10)
   grid_dependency_wait();
   load(base);
   allow_dependent_launch();
-  if (blockIdx.y == 0)  // the status of every sequence, spread over the blocks
-    for (int i = row * kRopeThreads + tid; i < b.M; i += gridDim.x * kRopeThreads) {
-      const int err = paged_seq(b, i).err;
+  if (blockIdx.y == 0)  // the status of every sequence, spread over the blocks (past 2^31 threads)
+    for (long long i = (long long)row * kRopeThreads + tid; i < b.M;
+         i += (long long)gridDim.x * kRopeThreads) {
+      const int err = paged_seq(b, (int)i).err;
       if (err != KVS_OK) record_status(d_status, err);
     }
   PagedSeq s{0, 0, 0, KVS_OK};

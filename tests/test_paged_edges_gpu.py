@@ -9,10 +9,10 @@ import numpy as np
 import pytest
 import torch
 
-from paged_helpers import DEV, DTYPES, Paged, within
+from paged_helpers import DEV, DTYPES, Paged, half_step, least_step, within
 from split_flash_decoding_kvcachescatter_gb300 import binding as B
 from test_logits_gpu import Rules, check as check_logits, logits
-from test_rope_gpu import check as check_rope, make_case
+from test_rope_gpu import check as check_rope, make_case, rotate64
 
 pytestmark = pytest.mark.gpu
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -204,3 +204,34 @@ def test_partial_overlaps_are_refused_and_column_blocks_are_not():
             call()
         assert e.value.status == B.KVS_ERR_OVERLAP
     assert torch.equal(q, b.q)
+
+
+def test_more_rotated_rows_than_32_bit_thread_numbers():
+    """2^24 rows are 2^31 threads of the rotary kernel: every sequence's rows are found and written."""
+    N, D, page = 2 ** 24 + 300, 64, 2 ** 15
+    n = [N - 257, 0, 256, 1]
+    p = [0, 5, 3, 2 ** 20]
+    g = torch.Generator(device=DEV)
+    g.manual_seed(1)
+    qkv = torch.empty(N, 3 * D, dtype=torch.bfloat16, device=DEV).normal_(generator=g)
+    q, k, v = (qkv[:, j * D:(j + 1) * D].unflatten(1, (1, D)) for j in range(3))
+    pages = -(-n[0] // page)
+    kp = torch.zeros(pages + 2, 1, page, D, dtype=torch.bfloat16, device=DEV)
+    cache = B.PagedCache(kp, torch.zeros_like(kp))
+    table = torch.zeros(4, pages, dtype=torch.int32, device=DEV)
+    table[0] = torch.arange(pages, dtype=torch.int32, device=DEV)
+    table[2], table[3] = pages, pages + 1
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=DEV)
+    batch = B.PagedBatch(i32(p), i32(np.concatenate([[0], np.cumsum(n)])), table, N, max(n))
+    status = i32([0])
+    inv, _ = B.kvs_rope_frequencies(D)
+    out = torch.zeros(N, 1, D, dtype=torch.bfloat16, device=DEV)
+    B.kvs_rope_scatter_paged(q, k, v, out, cache, batch, inv, d_status=status)
+    assert int(status.item()) == 0
+    assert torch.equal(cache.v_pages[:pages].view(-1, D)[:n[0]], v[:n[0], 0])
+    assert torch.equal(cache.v_pages[pages, 0, 3:259], v[n[0]:N - 1, 0])
+    assert torch.equal(cache.v_pages[pages + 1, 0, 2 ** 20 % page], v[N - 1, 0])
+    rows = torch.tensor([0, 1, 2 ** 23, 2 ** 24 - 1, 2 ** 24, n[0] - 1, n[0], N - 2, N - 1], device=DEV)
+    pos = torch.tensor([0, 1, 2 ** 23, 2 ** 24 - 1, 2 ** 24, n[0] - 1, 3, 258, 2 ** 20], device=DEV)
+    ref, size = rotate64(q[rows], pos, inv, False, 1.0)
+    within(out[rows], ref, size * 2.0 ** -21 + half_step(out.dtype) * ref.abs() * 1.01 + least_step(out.dtype))
