@@ -557,7 +557,7 @@ typedef struct kvs_paged_batch {
   const int32_t *positions;   /* device [M] */
   const int32_t *row_offsets; /* device [M + 1] */
   const int32_t *page_table;  /* device [M][max_pages] */
-  int32_t num_seqs;           /* M >= 0 */
+  int32_t num_seqs;           /* M, 0 .. 2^20 */
   int32_t num_rows;           /* rows of q, k, v and out, >= 0 */
   int32_t max_new;            /* the largest n_i that may occur, >= 1 */
   int32_t max_pages;          /* >= 1; max_pages * page_size < 2^31
@@ -596,8 +596,8 @@ typedef struct kvs_paged_batch {
  * A token with a bad position or page has no page row written; its q_out
  * row is NaN (bad position) or still the rotated q (bad page).  Where offsets
  * of some sequence are bad, rows of others may be left out too.
- * Errors: NULL, DIMS, UNSUPPORTED (also H / Hkv > 8 or H > 4096), ALIGN,
- * OVERLAP, LAUNCH on the host; ROWS, POSITION, PAGE via d_status.
+ * Errors: NULL, DIMS, UNSUPPORTED (also H / Hkv > 8, H > 4096 or M > 2^20),
+ * ALIGN, OVERLAP, LAUNCH on the host; ROWS, POSITION, PAGE via d_status.
  */
 int kvs_rope_scatter_paged(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
                            const void *v, int64_t v_stride, void *q_out, int64_t q_out_stride,
@@ -663,8 +663,8 @@ int kvs_rope_frequencies(int rot_dim, double base, int kind, double factor, doub
  *              epoch rule for captured graphs after a KVS_ERR_TIMEOUT)
  * The rows of a sequence with a bad position are NaN; where a sequence needs
  * a bad page, the rows that attend it are NaN and its other rows may be.
- * Errors: NULL, DIMS, UNSUPPORTED (also H / Hkv > 8 or H > 4096), ALIGN,
- * OVERLAP, WORKSPACE, LAUNCH on the host; ROWS, POSITION, PAGE, TIMEOUT via d_status.
+ * Errors: NULL, DIMS, UNSUPPORTED (also H / Hkv > 8, H > 4096 or M > 2^20),
+ * ALIGN, OVERLAP, WORKSPACE, LAUNCH on the host; ROWS, POSITION, PAGE, TIMEOUT via d_status.
  */
 size_t kvs_paged_attention_workspace_bytes(int num_heads, int num_kv_heads, int head_dim,
                                            int max_new);
@@ -724,7 +724,7 @@ typedef struct kvs_logit_rules {
  * counts as empty (no history, no biases, no mask).
  * Errors: DIMS (M < 0, vocab_size < 1, a stride too small, a length out of
  * range), NULL, ALIGN, UNSUPPORTED (dtype; a vocabulary of more than 2^19
- * tokens), OVERLAP, LAUNCH.
+ * tokens; more than 2^30 rows), OVERLAP, LAUNCH.
  * M = 0 enqueues nothing.
  */
 int kvs_process_logits(const void *logits, int64_t logits_stride, void *out, int64_t out_stride,

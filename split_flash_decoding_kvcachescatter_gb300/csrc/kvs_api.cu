@@ -440,6 +440,9 @@ static int check_paged(const kvs_paged_cache *cache, const kvs_paged_batch *batc
     return KVS_ERR_UNSUPPORTED;
   if (cache->page_size < 16 || (cache->page_size & (cache->page_size - 1)) != 0)
     return KVS_ERR_UNSUPPORTED;
+  // (a block walks the sequences one after the other, empty ones too: 2^20 of them in about half a
+  // second, within its waits' bound)
+  if (batch->num_seqs > (1 << 20)) return KVS_ERR_UNSUPPORTED;
   // rows of the pages and of one sequence are counted in 32 bits
   if ((int64_t)cache->num_pages * Hkv > 0x7fffffffll / cache->page_size ||
       (int64_t)batch->max_pages > 0x7fffffffll / cache->page_size)
@@ -626,6 +629,7 @@ int kvs_process_logits(const void *logits, int64_t logits_stride, void *out, int
   if (M < 0 || vocab_size < 1) return KVS_ERR_DIMS;
   if (dtype != KVS_F32 && dtype != KVS_F16 && dtype != KVS_BF16) return KVS_ERR_UNSUPPORTED;
   if (vocab_size > (1 << 19)) return KVS_ERR_UNSUPPORTED;
+  if (M > (1 << 30)) return KVS_ERR_UNSUPPORTED;  // (the kernel steps past M by a grid's rows)
   if (M == 0) return KVS_OK;
   if (!logits || !rules || (!out && !token_ids)) return KVS_ERR_NULL;
   if (logits_stride < vocab_size || (out && out_stride < vocab_size)) return KVS_ERR_DIMS;

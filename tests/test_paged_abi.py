@@ -41,6 +41,8 @@ SHAPES = [
     ({}, dict(table=None), B.KVS_ERR_NULL),
     (dict(k=A16 + 8), {}, B.KVS_ERR_ALIGN), ({}, dict(table=A16 + 2), B.KVS_ERR_ALIGN),
     ({}, dict(M=0), B.KVS_OK), ({}, dict(rows=0), B.KVS_OK),
+    ({}, dict(M=(1 << 20) + 1, rows=0), B.KVS_ERR_UNSUPPORTED), ({}, dict(M=2 ** 31 - 1, rows=0), B.KVS_ERR_UNSUPPORTED),
+    ({}, dict(M=1 << 20, rows=0), B.KVS_OK),
 ]
 
 
@@ -120,6 +122,7 @@ def logits(L, x=A16, xs=1000, o=A16, os_=1000, dtype=B.KVS_F32, M=2, V=1000, ids
 
 
 @pytest.mark.parametrize("kw,code", [
+    (dict(M=(1 << 30) + 1, x=None), B.KVS_ERR_UNSUPPORTED), (dict(M=1 << 30, x=None), B.KVS_ERR_NULL),
     (dict(M=-1), B.KVS_ERR_DIMS), (dict(V=0), B.KVS_ERR_DIMS), (dict(V=(1 << 19) + 1), B.KVS_ERR_UNSUPPORTED),
     (dict(dtype=7), B.KVS_ERR_UNSUPPORTED), (dict(x=None), B.KVS_ERR_NULL), (dict(rules=False), B.KVS_ERR_NULL),
     (dict(o=None, ids=None), B.KVS_ERR_NULL), (dict(xs=999), B.KVS_ERR_DIMS), (dict(os_=999), B.KVS_ERR_DIMS),

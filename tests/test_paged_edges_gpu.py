@@ -235,3 +235,18 @@ def test_more_rotated_rows_than_32_bit_thread_numbers():
     pos = torch.tensor([0, 1, 2 ** 23, 2 ** 24 - 1, 2 ** 24, n[0] - 1, 3, 258, 2 ** 20], device=DEV)
     ref, size = rotate64(q[rows], pos, inv, False, 1.0)
     within(out[rows], ref, size * 2.0 ** -21 + half_step(out.dtype) * ref.abs() * 1.01 + least_step(out.dtype))
+
+
+@pytest.mark.parametrize("dtype,n", [("f16", 1), ("f32", 1), ("f16", 40), ("f32", 40)])
+def test_most_sequences_of_a_batch_are_empty(dtype, n):
+    """The largest number of sequences, all but the first and the last without a token."""
+    M = 2 ** 20
+    b = Paged([n, 1], [700, 90], 8, 2, 64, dtype, 16, seed=13)
+    wide = torch.zeros(M, b.page_table.shape[1], dtype=torch.int32, device=DEV)
+    wide[0], wide[-1] = b.page_table[0], b.page_table[1]
+    positions = torch.zeros(M, dtype=torch.int32, device=DEV)
+    positions[0], positions[-1] = 700, 90
+    offsets = torch.full((M + 1,), n, dtype=torch.int32, device=DEV)
+    offsets[0], offsets[-1] = 0, n + 1
+    b.batch = B.PagedBatch(positions, offsets, wide, b.rows, n)
+    b.check(b.attend())
