@@ -646,13 +646,14 @@ int kvs_rope_frequencies(int rot_dim, double base, int kind, double factor, doub
  *     out[row][h][:] = softmax_j( q[row][h] . k_j[g] / sqrt(D) ) applied to
  *     v_j[g], j = 0 .. p_i + t.
  * One call serves prompts, chunks of prompts and decode steps together.
- * Every live K and V row must be finite; cache rows past a sequence's last
- * new token are never used, whatever they hold.  Products of 16-bit types
- * accumulate in float32 and the softmax runs in float32.  Where max_new * G
- * is 16 at most (decode steps), the weights go into the product with v in two
- * 16-bit parts; in longer chunks they are rounded to the type for it (float16
- * weights below 2^-30 of the row's largest count as zero there).  float32
- * inputs keep float32 accuracy throughout.
+ * Every live K and V row must be finite, and float32 q, K and V below 3.4e38
+ * (from 2^128 (1 - 2^-12) on, their TF32 parts overflow); cache rows past a
+ * sequence's last new token are never used, whatever they hold.  Products of
+ * 16-bit types accumulate in float32 and the softmax runs in float32.  Where
+ * max_new * G is 16 at most (decode steps), the weights go into the product
+ * with v in two 16-bit parts; in longer chunks they are rounded to the type
+ * for it (float16 weights below 2^-30 of the row's largest count as zero
+ * there).  float32 inputs keep float32 accuracy throughout.
  *
  *   q, out     rows [num_rows] of [H][D], the strides in elements between
  *              rows, 16-byte aligned pointers and row strides; out must not

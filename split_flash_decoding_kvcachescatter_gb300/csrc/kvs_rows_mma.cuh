@@ -59,8 +59,8 @@ __device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], 
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// x = hi + lo: hi is x rounded to TF32's 11 significant bits, lo the rest,
-// under 2^-12 of x, of which TF32 keeps 11 bits: 2^-23 of x is lost.  (hi
+// x = hi + lo: hi is x rounded to TF32's 11 significant bits, lo the rest, 2^-11
+// of x at most; of its 12 bits TF32 keeps 11, so 2^-23 of x is lost.  (hi
 // truncated, one addition less a value, loses 2^-21, always toward zero:
 // attention over 600 keys was then off by 1.1e-6, now by 6e-7.  Rounding takes
 // the last 2^-12 below the largest float to infinity.)

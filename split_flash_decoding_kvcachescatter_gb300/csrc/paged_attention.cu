@@ -20,7 +20,8 @@
 // Kernels: rows that a unit's 16 can hold (max_new G <= 16: a decode step)
 // paged_decode.cu; more rows in 16 bits paged_chunk.cu (tcgen05); more rows
 // in float32 the one here, on mma.sync: float32 as three TF32 products of a
-// high and a low part (hi hi + hi lo + lo hi), off by 2^-21.7 of it at most.
+// high and a low part (hi hi + hi lo + lo hi), off by 2^-21 of it at most (lo lo 2^-22,
+// a lost bit of each lo 2^-23).
 //
 // Block: one producer warp and 7 consumer warps of 16 rows (eight warps, so
 // that a thread may have 255 registers), which share a ring of stages (K and
