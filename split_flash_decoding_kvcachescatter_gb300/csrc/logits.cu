@@ -16,8 +16,8 @@
 // only: the result does not depend on their order.
 //
 // Measured: 32 float32 rows of 152,064 tokens, 4,096 history entries, half of
-// them masked: 15.9 us (39.6 MB, 2.5 TB/s; 5.8 us at the copy peak); one row
-// 5.9 us; 67 bfloat16 rows of 32,001: 9.7 us.  The chain of launch, counting,
+// them masked: 16.0 us (39.6 MB, 2.5 TB/s; 5.8 us at the copy peak); one row
+// 6.3 us; 67 bfloat16 rows of 32,001: 9.8 us.  The chain of launch, counting,
 // row and maxima is what takes the time, not the bytes.
 //
 // Arithmetic is one IEEE operation at a time (no fused multiply-add), so a

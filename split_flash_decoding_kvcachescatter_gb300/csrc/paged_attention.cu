@@ -29,11 +29,13 @@
 // of 16 rows, each looked up in the page table).
 //
 // Measured: 1001 new tokens of three sequences over up to 2048, H 14 / 2, D 64:
-// 79 us (101 with the pieces of split units joined from memory by one group of
-// threads).  Three TF32 products at the 303 TFLOP/s that mma.sync reaches here
-// would take 42 us; splitting the operands and the softmax take the rest.  A
-// dearer unit in the split is slower (128 cost rows 84 us, 256 92 us), and so
-// are 11 warps of fewer registers.
+// 57 to 74 us by the positions (65 us at 3.7 GFLOP, whose three TF32 products
+// would take 36 us at the 303 TFLOP/s that mma.sync reaches here; splitting the
+// operands and the softmax take the rest).  At positions where it took 82 us:
+// 101 with the pieces of split units joined from memory by one group of threads;
+// dearer units in the split 84 us (128 cost rows) and 92 (256); 11 warps of fewer
+// registers 84.  1001 tokens over up to 1900, H 40 / 8, D 128: 483 us
+// (22.6 GFLOP; 223 us).
 
 #include <algorithm>
 #include <cmath>

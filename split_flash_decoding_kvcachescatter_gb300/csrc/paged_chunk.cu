@@ -39,7 +39,8 @@
 // ready 313 us (it stalls in the pipe while the other could be looked at),
 // issuing warps that spin 304 us (they take the softmax's issue slots), a warp
 // of its own for V 270 to 296 us (but 16-key pages then 169 us instead of 200
-// at 3200 tokens over 3200: their copies of 2 KB take long to issue).
+// at 3200 tokens over 3200: their copies of 2 KB take long to issue).  Now 251 to
+// 289 us by the box, at 168 registers a thread, of which 104 to 112 bytes spill.
 //
 // The softmax keeps a reference maximum that moves only when a row's maximum
 // grows by more than 2^8, so P and O are rarely rescaled; the weights are

@@ -17,7 +17,8 @@
 // Measured: 8192 tokens, H 32 / 8, D 128, bfloat16 (201 MB read and written)
 // 36.9 us, 5.4 TB/s, 80 % of the measured copy peak; a decode step of 32
 // tokens 2.7 us; 1531 tokens, H 14 / 2, D 64, float32, 16 elements rotated in
-// pairs 5.4 us.  Threads x vectors, for the first: 128 x 3 36.9, 192 x 2 36.5,
+// pairs 5.4 us.  (Ten blocks an SM leave 48 registers a thread: the half layout
+// at its widest spills 68 bytes, in float32 100.)  Threads x vectors, for the first: 128 x 3 36.9, 192 x 2 36.5,
 // 96 x 4 37.8, 64 x 6 41, 384 x 1 48 us.
 
 #include "kvs_paged.cuh"
