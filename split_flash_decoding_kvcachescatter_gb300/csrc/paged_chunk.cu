@@ -40,13 +40,14 @@
 // issuing warps that spin 304 us (they take the softmax's issue slots), a warp
 // of its own for V 270 to 296 us (but 16-key pages then 169 us instead of 200
 // at 3200 tokens over 3200: their copies of 2 KB take long to issue).  Now 251 to
-// 289 us by the box, at 168 registers a thread, of which 104 to 112 bytes spill.
+// 289 us by the clocks that the power limit leaves, at 168 registers a thread;
+// 104 to 112 bytes a thread spill.
 //
 // The softmax keeps a reference maximum that moves only when a row's maximum
 // grows by more than 2^8, so P and O are rarely rescaled; the weights are
 // rounded to the type for the product, their sum is taken in float32 before.
-// (A second 16-bit part of P would need 128 more TMEM columns and half a
-// product more.)  In float16 the reference is 2^5 below the maximum, so that P
+// (A second 16-bit part of P would need 128 more TMEM columns and twice the
+// products P V.)  In float16 the reference is 2^5 below the maximum, so that P
 // reaches 2^13 and loses what is below 2^-30 of the largest weight; with no such
 // lift 131,072 keys of 2^-26 each, 2^-9 of the sum, were lost.  (2^3 of room are
 // left for the reference's own rounding, 2^2 where scores reach 2^25.)

@@ -21,12 +21,13 @@
 // Measured (GB300, copy peak 6.79 TB/s): 8 x 32768 keys, H 32 / 8, D 128,
 // float16 (1.07 GB) 162 us, 97 % of the peak; 32 sequences of up to 8192 keys
 // in bfloat16 (586 MB) 93 us, 93 %; 8 x 32768 in float32 (2.15 GB; 16-key tiles,
-// q split again for each) 403 us, 79 %.  (float32, D 64: 76 bytes spill.)  Tried: one producer warp for all four
-// rings 190 us (it needs about 1000 cycles a tile), two producers of two
-// rings 234 us (rings wait for each other); a warp of its own for the joining
-// 171 and 107 us; with it the last fifth of the line in short ranges handed
-// out by a counter, 180 and 114 us (blocks then finish within 10 % of each
-// other, not 26 %, but a long unit's 24 pieces are slow to join).
+// q split again for each) 403 us, 79 %.  (float32, D 64: 76 bytes a thread
+// spill.)  Tried: one producer warp for all four rings 190 us (it needs about
+// 1000 cycles a tile), two producers of two rings 234 us (rings wait for each
+// other); a warp of its own for the joining 171 and 107 us; with it the last
+// fifth of the line in short ranges handed out by a counter, 180 and 114 us
+// (blocks then finish within 10 % of each other, not 26 %, but a long unit's 24
+// pieces are slow to join).
 
 #include <algorithm>
 #include <cmath>
