@@ -676,6 +676,78 @@ int kvs_paged_attention(const void *q, int64_t q_stride, const kvs_paged_cache *
                         kvs_stream_t stream);
 
 /*
+ * A paged KV cache in 8 bits: half the bytes of a 16-bit one to hold and to
+ * read.  An element is its block's scale times an e4m3 number (sign, 4
+ * exponent bits, 3 mantissa bits; 448 at most, steps of 2^-9 below 2^-6); a
+ * block is KVS_SCALE_BLOCK positions of one kv head in a page.
+ * kvs_rope_scatter_paged_q8 writes powers of two as scales.
+ */
+#define KVS_SCALE_BLOCK 16
+
+typedef struct kvs_paged_cache_q8 {
+  void *k_pages, *v_pages;   /* device, 16-byte aligned: e4m3 [num_pages][Hkv][page_size][D] */
+  float *k_scales, *v_scales; /* device: [num_pages][Hkv][page_size / 16], >= 0 and finite */
+  int32_t num_pages;         /* as kvs_paged_cache's */
+  int32_t page_size;
+  int32_t num_kv_heads;
+  int32_t head_dim;
+} kvs_paged_cache_q8;
+
+/*
+ * kvs_rope_scatter_paged_q8 -- kvs_rope_scatter_paged into an 8-bit cache:
+ * the rotation and q_out are the same; rotated k (in float32, not rounded to
+ * the type) and v are rounded to the cache's numbers.  For every block (16
+ * positions of a kv head) that gets rows, k and v apart, with a = the largest
+ * |element| of the new rows:
+ *     s = the least power of two with a <= 448 s, 2^-60 at least
+ *     a new row is the first of its block: scale = s
+ *     older rows are in it:                scale = max(s, old scale), and where
+ *         that has grown, numbers of the older rows (those before the
+ *         sequence's first new position) become e4m3(number * old scale / scale)
+ *     new numbers = e4m3(element / scale)
+ * with e4m3() to nearest, ties to even.  A block's scale so does not depend on
+ * whether its rows came in one call or in many, and its numbers only below
+ * 2^-6.  Numbers and scales of no other rows and blocks are written.  A page
+ * that gets rows, or whose last block holds the rows before them, must not be
+ * shared by another sequence.  A NaN stays one and does not count for the
+ * scale; infinities become the largest number.
+ *
+ *   q, k, v, q_out, inv_freq, rot_dim, scale  as for kvs_rope_scatter_paged
+ *   dtype  kvs_dtype of q, k, v and q_out
+ * Errors: as kvs_rope_scatter_paged.
+ */
+int kvs_rope_scatter_paged_q8(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                              const void *v, int64_t v_stride, void *q_out, int64_t q_out_stride,
+                              int dtype, const kvs_paged_cache_q8 *cache,
+                              const kvs_paged_batch *batch, const float *inv_freq, int num_heads,
+                              int rot_dim, int interleaved, float scale, int *d_status,
+                              kvs_stream_t stream);
+
+/*
+ * kvs_paged_attention_q8 -- kvs_paged_attention over an 8-bit cache: K and V
+ * rows are the values that the cache's numbers and scales stand for (scales of
+ * V below 2^-60 count as 2^-60).  The numbers are exact in the products
+ * (float16 operands, float32 sums); a row of q is brought to 2^15 by a power of
+ * two first, and elements below 2^-28 of its largest one may lose bits there
+ * (float32 rows go in as two parts of 22 bits together).  Weights: decode
+ * steps and float32 as two float16 parts; chunks in 16 bits rounded to float16,
+ * and those below 2^-30 of a row's largest may count as zero in the product
+ * with v.  Live rows and scales must be finite.
+ *
+ *   q, out     rows as for kvs_paged_attention, of kvs_dtype `dtype`
+ *   workspace  device scratch of >= kvs_paged_attention_q8_workspace_bytes
+ *              bytes, 256-byte aligned; the rules of kvs_paged_attention
+ * Errors: as kvs_paged_attention.
+ */
+size_t kvs_paged_attention_q8_workspace_bytes(int num_heads, int num_kv_heads, int head_dim,
+                                              int max_new);
+
+int kvs_paged_attention_q8(const void *q, int64_t q_stride, int dtype,
+                           const kvs_paged_cache_q8 *cache, const kvs_paged_batch *batch,
+                           void *out, int64_t out_stride, int num_heads, void *workspace,
+                           size_t workspace_bytes, int *d_status, kvs_stream_t stream);
+
+/*
  * kvs_process_logits -- what happens between the model's logits and the
  * choice of a token: penalties for repeated tokens, biases and a grammar
  * mask, and the greedy token of the result, in ONE launch.  For row m and
@@ -731,6 +803,50 @@ typedef struct kvs_logit_rules {
 int kvs_process_logits(const void *logits, int64_t logits_stride, void *out, int64_t out_stride,
                        int dtype, int M, int vocab_size, const kvs_logit_rules *rules,
                        int32_t *token_ids, int *d_status, kvs_stream_t stream);
+
+/*
+ * kvs_sample_logits -- a token drawn from each of M rows of logits, with given
+ * random numbers, in ONE launch.  For row m, with its tokens in order of falling
+ * logit (of equal ones the lower id first) and x the largest logit:
+ *     T = temperature[m]:  weights w_j = e^((logits[m][j] - x) / T); T below
+ *                          2^-126 (0, negative, NaN): the first token alone
+ *     k = top_k[m]:        only the first k are kept; k <= 0: all
+ *     p = top_p[m]:        of those, the shortest run from the front whose weight
+ *                          is at least p times theirs, one token at the least;
+ *                          p >= 1 or NaN: all
+ *     l = min_p[m]:        of those, the ones with w_j >= l (l above 1 counts as 1)
+ *     u = uniforms[m]:     the least id at which the sum of the kept weights, in
+ *                          the order of ids, is above u times their whole sum (u
+ *                          below 0 or NaN counts as 0, u from 1 up draws the last)
+ * token_probs[m] is that token's weight over the sum of the kept ones, probs[m][j]
+ * the same for every id (0 for those not kept).  NaN and -inf are never drawn; a row
+ * without anything above -inf gives token 0 and probabilities 0; where a logit is
+ * +inf, those tokens share the row.  Weights below 2^-45 of the largest count as 0;
+ * others are computed to 2^-40 of themselves and summed exactly, so the result does
+ * not depend on the order of anything.
+ */
+typedef struct kvs_sample_rules {
+  const float *temperature; /* device [M], or NULL: 1 */
+  const int32_t *top_k;     /* device [M], or NULL: all */
+  const float *top_p;       /* device [M], or NULL: 1 */
+  const float *min_p;       /* device [M], or NULL: 0 */
+} kvs_sample_rules;
+
+/*
+ *   logits       in   as for kvs_process_logits
+ *   uniforms     in   [M] float32, device, each from [0, 1)
+ *   rules        in   HOST struct of device pointers, or NULL: none
+ *   token_ids    out  [M] int32, device, or NULL
+ *   token_probs  out  [M] float32, device, or NULL
+ *   probs        out  [M] rows of vocab_size float32, probs_stride apart, or NULL;
+ *                     must not overlap logits
+ * Errors: DIMS (M < 0, vocab_size < 1, a stride too small), NULL (logits, uniforms,
+ * or all three outputs), ALIGN, UNSUPPORTED (dtype; a vocabulary of more than 2^19
+ * tokens; more than 2^30 rows), OVERLAP, LAUNCH.  M = 0 enqueues nothing.
+ */
+int kvs_sample_logits(const void *logits, int64_t logits_stride, int dtype, int M, int vocab_size,
+                      const float *uniforms, const kvs_sample_rules *rules, int32_t *token_ids,
+                      float *token_probs, float *probs, int64_t probs_stride, kvs_stream_t stream);
 
 /*
  * Kernel schedule of kvs_flash_decode, kvs_decode_step (and so of the

@@ -11,4 +11,6 @@ from .binding import (EXPORTS, kvs_argmax, kvs_prefill_attention, KVS_SCHEDULE_A
                       kvs_prepare, kvs_schedule_for, prefill_workspace, kvs_set_schedule, kvs_step_graph_create, lib, strerror,
                       workspace, PagedBatch, PagedCache, kvs_paged_attention, kvs_process_logits,
                       kvs_rope_frequencies, kvs_rope_scatter_paged, paged_attention_workspace,
+                      PagedCacheQ8, kvs_paged_attention_q8, kvs_rope_scatter_paged_q8,
+                      kvs_sample_logits, paged_attention_q8_workspace,
                       KVS_ROPE_BANDS, KVS_ROPE_LINEAR, KVS_ROPE_NTK, KVS_ROPE_PLAIN, KVS_ROPE_YARN)

@@ -51,7 +51,11 @@ EXPORTS = ("kvs_kv_scatter", "kvs_choose_chunk_size", "kvs_flash_decode_workspac
            "kvs_set_wait_limit_ns", "kvs_step_io_layout", "kvs_decode_step_host_io",
            "kvs_step_graph_io_layout", "kvs_step_graph_create_host_io", "kvs_rope_scatter_paged",
            "kvs_rope_frequencies", "kvs_paged_attention_workspace_bytes", "kvs_paged_attention",
-           "kvs_process_logits")
+           "kvs_process_logits", "kvs_rope_scatter_paged_q8",
+           "kvs_paged_attention_q8_workspace_bytes", "kvs_paged_attention_q8", "kvs_sample_logits")
+
+# Positions of a kv head that share a scale in an 8-bit paged cache.
+KVS_SCALE_BLOCK = 16
 
 # Default bound on each pipeline wait of the kernels (kvs_set_wait_limit_ns).
 KVS_WAIT_LIMIT_DEFAULT_NS = 2_000_000_000
@@ -161,6 +165,15 @@ def lib() -> ctypes.CDLL:
             L.kvs_paged_attention.argtypes = [_P, _L, _P, _P, _P, _L, _I, _P, _SZ, _P, _P]
             L.kvs_process_logits.restype = _I
             L.kvs_process_logits.argtypes = [_P, _L, _P, _L, _I, _I, _I, _P, _P, _P, _P]
+            L.kvs_rope_scatter_paged_q8.restype = _I
+            L.kvs_rope_scatter_paged_q8.argtypes = [_P, _L, _P, _L, _P, _L, _P, _L, _I, _P, _P, _P,
+                                                    _I, _I, _I, _F, _P, _P]
+            L.kvs_paged_attention_q8_workspace_bytes.restype = _SZ
+            L.kvs_paged_attention_q8_workspace_bytes.argtypes = [_I, _I, _I, _I]
+            L.kvs_paged_attention_q8.restype = _I
+            L.kvs_paged_attention_q8.argtypes = [_P, _L, _I, _P, _P, _P, _L, _I, _P, _SZ, _P, _P]
+            L.kvs_sample_logits.restype = _I
+            L.kvs_sample_logits.argtypes = [_P, _L, _I, _I, _I, _P, _P, _P, _P, _P, _L, _P]
             L.kvs_strerror.restype = ctypes.c_char_p
             L.kvs_strerror.argtypes = [_I]
             _lib = L
@@ -605,6 +618,11 @@ class _PagedCacheStruct(ctypes.Structure):
                 ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32)]
 
 
+class _PagedCacheQ8Struct(ctypes.Structure):
+    _fields_ = [(n, _P) for n in ("k_pages", "v_pages", "k_scales", "v_scales")] + \
+               [(n, ctypes.c_int32) for n in ("num_pages", "page_size", "num_kv_heads", "head_dim")]
+
+
 class _PagedBatchStruct(ctypes.Structure):
     _fields_ = [("positions", _P), ("row_offsets", _P), ("page_table", _P),
                 ("num_seqs", ctypes.c_int32), ("num_rows", ctypes.c_int32),
@@ -639,6 +657,36 @@ class PagedCache:
                                          _DTYPES[k_pages.dtype])
         self._addr = ctypes.addressof(self._struct)
         self._call = lib().kvs_paged_attention, lib().kvs_rope_scatter_paged
+
+
+class PagedCacheQ8:
+    """A paged KV cache in 8 bits, checked once: k_pages and v_pages [num_pages, Hkv, page_size, D]
+    (float8_e4m3fn), k_scales and v_scales [num_pages, Hkv, page_size / 16] (float32); contiguous,
+    CUDA.  An element is its block's scale times the stored number."""
+
+    def __init__(self, k_pages, v_pages, k_scales, v_scales):
+        for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
+            if not (t.is_cuda and t.dtype is torch.float8_e4m3fn and t.dim() == 4 and
+                    t.is_contiguous()):
+                raise TypeError(f"{name}: need a contiguous CUDA tensor [num_pages, Hkv, page_size, "
+                                f"D] of float8_e4m3fn, got {tuple(t.shape)} {t.dtype} {t.device}")
+        if k_pages.shape != v_pages.shape or k_pages.device != v_pages.device:
+            raise ValueError("PagedCacheQ8: k_pages and v_pages differ in shape or device")
+        shape = (*k_pages.shape[:2], k_pages.shape[2] // KVS_SCALE_BLOCK)
+        for name, t in (("k_scales", k_scales), ("v_scales", v_scales)):
+            if not (t.dtype is torch.float32 and t.shape == shape and t.is_contiguous() and
+                    t.device == k_pages.device):
+                raise TypeError(f"{name}: need a contiguous float32 tensor {list(shape)} on "
+                                f"{k_pages.device}, got {tuple(t.shape)} {t.dtype} {t.device}")
+        self.k_pages, self.v_pages = k_pages, v_pages
+        self.k_scales, self.v_scales = k_scales, v_scales
+        self.device_index = k_pages.get_device()
+        self.num_pages, self.num_kv_heads, self.page_size, self.head_dim = k_pages.shape
+        self._struct = _PagedCacheQ8Struct(k_pages.data_ptr(), v_pages.data_ptr(),
+                                           k_scales.data_ptr(), v_scales.data_ptr(), self.num_pages,
+                                           self.page_size, self.num_kv_heads, self.head_dim)
+        self._addr = ctypes.addressof(self._struct)
+        self._call = lib().kvs_paged_attention_q8, lib().kvs_rope_scatter_paged_q8
 
 
 class PagedBatch:
@@ -789,6 +837,92 @@ def kvs_paged_attention(q, cache, batch, out, workspace=None, d_status=None, str
     return out
 
 
+def _q8_rows(where, q, cache, batch):
+    """(dtype, kvs_dtype, device, heads) of a call's q over a PagedCacheQ8."""
+    dev = cache.device_index
+    if dev != _get_device() or batch.device_index != dev:
+        raise ValueError(f"{where}: cache and batch must be on the current device")
+    dt = q.dtype
+    kd = _DTYPES.get(dt)
+    if kd is None:
+        raise TypeError(f"{where}: q: need float32, float16 or bfloat16, got {dt}")
+    return dt, kd, dev, q.shape[1] if q.dim() == 3 else -1
+
+
+def kvs_rope_scatter_paged_q8(q, k, v, q_out, cache, batch, inv_freq, interleaved=False, scale=1.0,
+                              d_status=None, stream=None):
+    """kvs_rope_scatter_paged into a PagedCacheQ8: rotated q to q_out, rotated k and plain v rounded
+    to 8 bits into the pages, with a power of two as the scale of each 16 positions of a kv head.
+    q, k, v and q_out have one type (float32, float16 or bfloat16)."""
+    where = "kvs_rope_scatter_paged_q8"
+    dt, kd, dev, H = _q8_rows(where, q, cache, batch)
+    N, D, Hkv = batch.num_rows, cache.head_dim, cache.num_kv_heads
+    if inv_freq.dtype is not torch.float32 or inv_freq.get_device() != dev or \
+            inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+        raise TypeError("inv_freq: need a contiguous float32 vector on the tensors' device")
+    of_q, of_kv = (N, H, D), (N, Hkv, D)
+    qs, ks, vs, os_ = q.stride(), k.stride(), v.stride(), q_out.stride()
+    if not (k.dtype is v.dtype is q_out.dtype is dt and
+            q.get_device() == k.get_device() == v.get_device() == q_out.get_device() == dev and
+            q.shape == of_q == q_out.shape and k.shape == of_kv == v.shape and
+            qs[2] == ks[2] == vs[2] == os_[2] == 1 and (qs[1] == os_[1] == D or H == 1) and
+            (ks[1] == vs[1] == D or Hkv == 1)):
+        _bad_rows(where, dt, dev, q=(q, of_q), k=(k, of_kv), v=(v, of_kv), q_out=(q_out, of_q))
+    if N > 1:
+        qs, ks, vs, os_ = qs[0], ks[0], vs[0], os_[0]
+    else:  # (the stride of a single row says nothing)
+        qs = os_ = H * D
+        ks = vs = Hkv * D
+    rc = cache._call[1](q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, q_out.data_ptr(), os_,
+                        kd, cache._addr, batch._addr, inv_freq.data_ptr(), H, 2 * inv_freq.numel(),
+                        1 if interleaved else 0, scale,
+                        0 if d_status is None else _status_ptr(d_status),
+                        _get_stream(dev) if stream is None else _stream(stream))
+    if rc != KVS_OK:
+        raise KvsError(rc, where)
+    return q_out
+
+
+def paged_attention_q8_workspace(cache, batch, num_heads, device=None):
+    """A device byte buffer large enough for kvs_paged_attention_q8 (allocated by torch)."""
+    n = int(lib().kvs_paged_attention_q8_workspace_bytes(num_heads, cache.num_kv_heads,
+                                                         cache.head_dim, batch.max_new))
+    if n == 0:
+        raise KvsError(KVS_ERR_DIMS, "kvs_paged_attention_q8_workspace_bytes")
+    return torch.empty(n, dtype=torch.uint8, device=device or cache.k_pages.device)
+
+
+def kvs_paged_attention_q8(q, cache, batch, out, workspace=None, d_status=None, stream=None):
+    """kvs_paged_attention over a PagedCacheQ8; q and out have one type (float32, float16 or
+    bfloat16)."""
+    where = "kvs_paged_attention_q8"
+    dt, kd, dev, H = _q8_rows(where, q, cache, batch)
+    N, D = batch.num_rows, cache.head_dim
+    if workspace is None:
+        raise ValueError(f"{where}: pass a workspace (see binding.paged_attention_q8_workspace)")
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        raise TypeError(f"{where}: the workspace must be a contiguous tensor on the tensors' device")
+    shape = (N, H, D)
+    qs, os_ = q.stride(), out.stride()
+    if not (out.dtype is dt and q.get_device() == out.get_device() == dev and
+            q.shape == shape == out.shape and qs[2] == os_[2] == 1 and
+            (qs[1] == os_[1] == D or H == 1)):
+        _bad_rows(where, dt, dev, q=(q, shape), out=(out, shape))
+    if N > 1:
+        qs, os_ = qs[0], os_[0]
+    else:  # (the stride of a single row says nothing)
+        qs = os_ = H * D
+    qp, op = q.data_ptr(), out.data_ptr()
+    if qp == op and N > 0:
+        raise ValueError(f"{where}: out must not overlap q")
+    rc = cache._call[0](qp, qs, kd, cache._addr, batch._addr, op, os_, H, workspace.data_ptr(),
+                        workspace.nbytes, 0 if d_status is None else _status_ptr(d_status),
+                        _get_stream(dev) if stream is None else _stream(stream))
+    if rc != KVS_OK:
+        raise KvsError(rc, where)
+    return out
+
+
 def _vector(t, name, dtype, n, dev):
     """Pointer of a contiguous vector of n entries (n None: any)."""
     if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous() or \
@@ -860,6 +994,47 @@ def kvs_process_logits(logits, out=None, token_ids=None, history=None, history_o
                                   _get_stream(dev) if stream is None else _stream(stream))
     if rc != KVS_OK:
         raise KvsError(rc, "kvs_process_logits")
+    return token_ids
+
+
+# kvs_sample_rules: four pointers
+_pack_sample = struct.Struct("@4Q").pack
+
+
+def kvs_sample_logits(logits, uniforms, token_ids=None, temperature=None, top_k=None, top_p=None,
+                      min_p=None, token_probs=None, probs=None, stream=None):
+    """A token drawn from each row of logits [M, V] (float32, float16 or bfloat16; rows may be
+    strided) with the random numbers uniforms (float32 [M], from [0, 1)) into token_ids (int32 [M],
+    made when None), under temperature, top_k (int32), top_p and min_p ([M] each, or None).
+    token_probs (float32 [M]) gets the tokens' probabilities, probs (float32 [M, V]) those of all
+    ids.  Returns token_ids."""
+    dt = _DTYPES.get(logits.dtype)
+    if dt is None or not logits.is_cuda or logits.dim() != 2:
+        raise TypeError("logits: need a CUDA matrix [M, V] of float32, float16 or bfloat16")
+    dev = logits.get_device()
+    _call_device(dev, "kvs_sample_logits")
+    M, V = logits.shape
+    ls = V if logits.is_contiguous() else _row_stride(logits, "logits")
+    f32, i32 = torch.float32, torch.int32
+    pp = ps = 0
+    if probs is not None:
+        if probs.dtype is not f32 or probs.shape != logits.shape or probs.get_device() != dev:
+            raise TypeError("probs: need a float32 matrix [M, V] on the logits' device")
+        pp, ps = probs.data_ptr(), V if probs.is_contiguous() else _row_stride(probs, "probs")
+    if token_ids is None:
+        token_ids = torch.empty(M, dtype=i32, device=logits.device)
+    rules = _pack_sample(
+        0 if temperature is None else _vector(temperature, "temperature", f32, M, dev),
+        0 if top_k is None else _vector(top_k, "top_k", i32, M, dev),
+        0 if top_p is None else _vector(top_p, "top_p", f32, M, dev),
+        0 if min_p is None else _vector(min_p, "min_p", f32, M, dev))
+    rc = lib().kvs_sample_logits(
+        logits.data_ptr(), ls, dt, M, V, _vector(uniforms, "uniforms", f32, M, dev), rules,
+        _vector(token_ids, "token_ids", i32, M, dev),
+        0 if token_probs is None else _vector(token_probs, "token_probs", f32, M, dev), pp, ps,
+        _get_stream(dev) if stream is None else _stream(stream))
+    if rc != KVS_OK:
+        raise KvsError(rc, "kvs_sample_logits")
     return token_ids
 
 

@@ -510,17 +510,26 @@ static kvs::PagedArgs paged_args(const kvs_paged_cache *cache, const kvs_paged_b
                         batch->max_pages, shift,              cache->num_pages};
 }
 
-int kvs_rope_scatter_paged(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
-                           const void *v, int64_t v_stride, void *q_out, int64_t q_out_stride,
-                           const kvs_paged_cache *cache, const kvs_paged_batch *batch,
-                           const float *inv_freq, int num_heads, int rot_dim, int interleaved,
-                           float scale, int *d_status, kvs_stream_t stream) {
-  int rc = check_paged(cache, batch, num_heads);
-  if (rc != KVS_OK) return rc;
+// The checks of a paged cache for one in 8 bits under rows of `dtype`.
+static kvs_paged_cache as_paged(const kvs_paged_cache_q8 *c, int dtype) {
+  return kvs_paged_cache{c->k_pages,      c->v_pages,  c->num_pages, c->page_size,
+                         c->num_kv_heads, c->head_dim, dtype};
+}
+static int check_scales(const kvs_paged_cache_q8 *c) {
+  if (!c->k_scales || !c->v_scales) return KVS_ERR_NULL;
+  return aligned(c->k_scales, 4) && aligned(c->v_scales, 4) ? KVS_OK : KVS_ERR_ALIGN;
+}
+
+// What a rotary scatter's rows and table need; done: there is nothing to do.
+static int check_rope(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                      const void *v, int64_t v_stride, const void *q_out, int64_t q_out_stride,
+                      const kvs_paged_cache *cache, const kvs_paged_batch *batch,
+                      const float *inv_freq, int num_heads, int rot_dim, bool &done) {
   const int D = cache->head_dim, Hkv = cache->num_kv_heads, dtype = cache->dtype;
   if (rot_dim < 0 || rot_dim > D || rot_dim % 2 != 0) return KVS_ERR_DIMS;
-  if (batch->num_seqs == 0 || batch->num_rows == 0) return KVS_OK;
-  rc = check_paged_pointers(cache, batch);
+  done = batch->num_seqs == 0 || batch->num_rows == 0;
+  if (done) return KVS_OK;
+  int rc = check_paged_pointers(cache, batch);
   if (rc == KVS_OK) rc = check_rows(q, q_stride, (int64_t)num_heads * D, dtype);
   if (rc == KVS_OK) rc = check_rows(k, k_stride, (int64_t)Hkv * D, dtype);
   if (rc == KVS_OK) rc = check_rows(v, v_stride, (int64_t)Hkv * D, dtype);
@@ -535,10 +544,47 @@ int kvs_rope_scatter_paged(const void *q, int64_t q_stride, const void *k, int64
       rows_overlap(row_span(k, k_stride, (int64_t)Hkv * D, dtype), to, n) ||
       rows_overlap(row_span(v, v_stride, (int64_t)Hkv * D, dtype), to, n))
     return KVS_ERR_OVERLAP;
+  return KVS_OK;
+}
+
+int kvs_rope_scatter_paged(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                           const void *v, int64_t v_stride, void *q_out, int64_t q_out_stride,
+                           const kvs_paged_cache *cache, const kvs_paged_batch *batch,
+                           const float *inv_freq, int num_heads, int rot_dim, int interleaved,
+                           float scale, int *d_status, kvs_stream_t stream) {
+  int rc = check_paged(cache, batch, num_heads);
+  if (rc != KVS_OK) return rc;
+  bool done = false;
+  rc = check_rope(q, q_stride, k, k_stride, v, v_stride, q_out, q_out_stride, cache, batch, inv_freq,
+                  num_heads, rot_dim, done);
+  if (rc != KVS_OK || done) return rc;
   return kvs::launch_rope_scatter(q, q_stride, k, k_stride, v, v_stride, q_out, q_out_stride,
                                   cache->k_pages, cache->v_pages, paged_args(cache, batch),
-                                  inv_freq, num_heads, Hkv, D, dtype, rot_dim, interleaved ? 1 : 0,
-                                  scale, d_status, reinterpret_cast<cudaStream_t>(stream));
+                                  inv_freq, num_heads, cache->num_kv_heads, cache->head_dim,
+                                  cache->dtype, rot_dim, interleaved ? 1 : 0, scale, d_status,
+                                  reinterpret_cast<cudaStream_t>(stream));
+}
+
+int kvs_rope_scatter_paged_q8(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                              const void *v, int64_t v_stride, void *q_out, int64_t q_out_stride,
+                              int dtype, const kvs_paged_cache_q8 *cache,
+                              const kvs_paged_batch *batch, const float *inv_freq, int num_heads,
+                              int rot_dim, int interleaved, float scale, int *d_status,
+                              kvs_stream_t stream) {
+  if (!cache) return KVS_ERR_NULL;
+  const kvs_paged_cache plain = as_paged(cache, dtype);
+  int rc = check_paged(&plain, batch, num_heads);
+  if (rc != KVS_OK) return rc;
+  bool done = false;
+  rc = check_rope(q, q_stride, k, k_stride, v, v_stride, q_out, q_out_stride, &plain, batch, inv_freq,
+                  num_heads, rot_dim, done);
+  if (rc != KVS_OK || done) return rc;
+  rc = check_scales(cache);
+  if (rc != KVS_OK) return rc;
+  return kvs::launch_rope_scatter_q8(q, q_stride, k, k_stride, v, v_stride, q_out, q_out_stride,
+                                     *cache, dtype, paged_args(&plain, batch), inv_freq, num_heads,
+                                     rot_dim, interleaved ? 1 : 0, scale, d_status,
+                                     reinterpret_cast<cudaStream_t>(stream));
 }
 
 int kvs_rope_frequencies(int rot_dim, double base, int kind, double factor, double original_len,
@@ -594,33 +640,69 @@ size_t kvs_paged_attention_workspace_bytes(int num_heads, int num_kv_heads, int 
   return kvs::paged_attention_workspace_bytes(num_heads, num_kv_heads, head_dim, max_new);
 }
 
-int kvs_paged_attention(const void *q, int64_t q_stride, const kvs_paged_cache *cache,
-                        const kvs_paged_batch *batch, void *out, int64_t out_stride,
-                        int num_heads, void *workspace, size_t workspace_bytes, int *d_status,
-                        kvs_stream_t stream) {
+// What attention's rows and workspace need; done: there is nothing to do.
+static int check_attention(const void *q, int64_t q_stride, const kvs_paged_cache *cache,
+                           const kvs_paged_batch *batch, const void *out, int64_t out_stride,
+                           int num_heads, const void *workspace, size_t workspace_bytes,
+                           size_t (*need)(int, int, int, int), bool &done) {
   int rc = check_paged(cache, batch, num_heads);
   if (rc != KVS_OK) return rc;
   // The kernels count a sequence's keys and what they look ahead (a tile, a
   // unit's fixed price, 32 tiles of pages: all under 2048 keys) in 32 bits.
   if ((int64_t)batch->max_pages * cache->page_size > KVS_PAGED_MAX_KEYS) return KVS_ERR_DIMS;
-  if (batch->num_seqs == 0 || batch->num_rows == 0) return KVS_OK;
-  const int D = cache->head_dim;
+  done = batch->num_seqs == 0 || batch->num_rows == 0;
+  if (done) return KVS_OK;
+  const int64_t row = (int64_t)num_heads * cache->head_dim;
   rc = check_paged_pointers(cache, batch);
-  if (rc == KVS_OK) rc = check_rows(q, q_stride, (int64_t)num_heads * D, cache->dtype);
-  if (rc == KVS_OK) rc = check_rows(out, out_stride, (int64_t)num_heads * D, cache->dtype);
+  if (rc == KVS_OK) rc = check_rows(q, q_stride, row, cache->dtype);
+  if (rc == KVS_OK) rc = check_rows(out, out_stride, row, cache->dtype);
   if (rc != KVS_OK) return rc;
   if (!workspace) return KVS_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return KVS_ERR_ALIGN;
-  if (workspace_bytes < kvs::paged_attention_workspace_bytes(num_heads, cache->num_kv_heads, D,
-                                                             batch->max_new))
+  if (workspace_bytes < need(num_heads, cache->num_kv_heads, cache->head_dim, batch->max_new))
     return KVS_ERR_WORKSPACE;
-  if (rows_overlap(row_span(q, q_stride, (int64_t)num_heads * D, cache->dtype),
-                   row_span(out, out_stride, (int64_t)num_heads * D, cache->dtype),
-                   batch->num_rows))
+  if (rows_overlap(row_span(q, q_stride, row, cache->dtype),
+                   row_span(out, out_stride, row, cache->dtype), batch->num_rows))
     return KVS_ERR_OVERLAP;
+  return KVS_OK;
+}
+
+int kvs_paged_attention(const void *q, int64_t q_stride, const kvs_paged_cache *cache,
+                        const kvs_paged_batch *batch, void *out, int64_t out_stride,
+                        int num_heads, void *workspace, size_t workspace_bytes, int *d_status,
+                        kvs_stream_t stream) {
+  bool done = false;
+  const int rc = check_attention(q, q_stride, cache, batch, out, out_stride, num_heads, workspace,
+                                 workspace_bytes, kvs::paged_attention_workspace_bytes, done);
+  if (rc != KVS_OK || done) return rc;
   return kvs::launch_paged_attention(q, q_stride, *cache, paged_args(cache, batch), out,
                                      out_stride, num_heads, workspace, d_status,
                                      reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t kvs_paged_attention_q8_workspace_bytes(int num_heads, int num_kv_heads, int head_dim,
+                                              int max_new) {
+  if (num_heads < 1 || num_kv_heads < 1 || num_heads % num_kv_heads != 0 || max_new < 1 ||
+      !head_dim_supported(head_dim) || num_heads / num_kv_heads > 8)
+    return 0;
+  return kvs::paged_attention_q8_workspace_bytes(num_heads, num_kv_heads, head_dim, max_new);
+}
+
+int kvs_paged_attention_q8(const void *q, int64_t q_stride, int dtype,
+                           const kvs_paged_cache_q8 *cache, const kvs_paged_batch *batch,
+                           void *out, int64_t out_stride, int num_heads, void *workspace,
+                           size_t workspace_bytes, int *d_status, kvs_stream_t stream) {
+  if (!cache) return KVS_ERR_NULL;
+  const kvs_paged_cache plain = as_paged(cache, dtype);
+  bool done = false;
+  int rc = check_attention(q, q_stride, &plain, batch, out, out_stride, num_heads, workspace,
+                           workspace_bytes, kvs::paged_attention_q8_workspace_bytes, done);
+  if (rc != KVS_OK || done) return rc;
+  rc = check_scales(cache);
+  if (rc != KVS_OK) return rc;
+  return kvs::launch_paged_attention_q8(q, q_stride, *cache, dtype, paged_args(&plain, batch), out,
+                                        out_stride, num_heads, workspace, d_status,
+                                        reinterpret_cast<cudaStream_t>(stream));
 }
 
 int kvs_process_logits(const void *logits, int64_t logits_stride, void *out, int64_t out_stride,
@@ -658,6 +740,30 @@ int kvs_process_logits(const void *logits, int64_t logits_stride, void *out, int
                             token_ids, d_status, reinterpret_cast<cudaStream_t>(stream));
 }
 
+int kvs_sample_logits(const void *logits, int64_t logits_stride, int dtype, int M, int vocab_size,
+                      const float *uniforms, const kvs_sample_rules *rules, int32_t *token_ids,
+                      float *token_probs, float *probs, int64_t probs_stride, kvs_stream_t stream) {
+  if (M < 0 || vocab_size < 1) return KVS_ERR_DIMS;
+  if (dtype != KVS_F32 && dtype != KVS_F16 && dtype != KVS_BF16) return KVS_ERR_UNSUPPORTED;
+  if (vocab_size > (1 << 19)) return KVS_ERR_UNSUPPORTED;
+  if (M > (1 << 30)) return KVS_ERR_UNSUPPORTED;  // (the kernel steps past M by a grid's rows)
+  if (M == 0) return KVS_OK;
+  if (!logits || !uniforms || (!token_ids && !token_probs && !probs)) return KVS_ERR_NULL;
+  if (logits_stride < vocab_size || (probs && probs_stride < vocab_size)) return KVS_ERR_DIMS;
+  const kvs_sample_rules none{nullptr, nullptr, nullptr, nullptr};
+  const kvs_sample_rules &r = rules ? *rules : none;
+  if (!aligned(logits, dtype == KVS_F32 ? 4 : 2)) return KVS_ERR_ALIGN;
+  for (const void *p : {(const void *)uniforms, (const void *)token_ids, (const void *)token_probs,
+                        (const void *)probs, (const void *)r.temperature, (const void *)r.top_k,
+                        (const void *)r.top_p, (const void *)r.min_p})
+    if (!aligned(p, 4)) return KVS_ERR_ALIGN;
+  if (probs && rows_overlap(row_span(logits, logits_stride, vocab_size, dtype),
+                            row_span(probs, probs_stride, vocab_size, KVS_F32), M))
+    return KVS_ERR_OVERLAP;
+  return kvs::launch_sample(logits, logits_stride, dtype, M, vocab_size, uniforms, r, token_ids,
+                            token_probs, probs, probs_stride, reinterpret_cast<cudaStream_t>(stream));
+}
+
 int kvs_set_schedule(int schedule) {
   if (schedule != KVS_SCHEDULE_AUTO && schedule != KVS_SCHEDULE_PERSISTENT &&
       schedule != KVS_SCHEDULE_CLUSTER)
@@ -681,6 +787,7 @@ int kvs_set_wait_limit_ns(uint64_t ns, uint64_t *previous) {
   if (rc == KVS_OK) rc = kvs::set_wait_limit_paged(ns);
   if (rc == KVS_OK) rc = kvs::set_wait_limit_decode(ns);
   if (rc == KVS_OK) rc = kvs::set_wait_limit_chunk(ns);
+  if (rc == KVS_OK) rc = kvs::set_wait_limit_decode_q8(ns);
   if (rc != KVS_OK) return rc;
   if (previous) *previous = g_limit[dev].load();
   g_limit[dev].store(ns);

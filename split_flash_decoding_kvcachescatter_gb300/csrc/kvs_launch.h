@@ -188,6 +188,22 @@ int launch_paged_chunk(const void *q, long long q_stride, const kvs_paged_cache 
                        const PagedArgs &b, void *out, long long out_stride, int H,
                        void *workspace, int *d_status, cudaStream_t stream);
 
+// The same two over a cache in 8 bits; q, k, v and out of `dtype`.
+int launch_rope_scatter_q8(const void *q, long long q_stride, const void *k, long long k_stride,
+                           const void *v, long long v_stride, void *q_out, long long q_out_stride,
+                           const kvs_paged_cache_q8 &cache, int dtype, const PagedArgs &b,
+                           const float *inv_freq, int H, int rot, int interleaved, float scale,
+                           int *d_status, cudaStream_t stream);
+size_t paged_attention_q8_workspace_bytes(int H, int Hkv, int D, int max_new);
+int launch_paged_attention_q8(const void *q, long long q_stride, const kvs_paged_cache_q8 &cache,
+                              int dtype, const PagedArgs &b, void *out, long long out_stride, int H,
+                              void *workspace, int *d_status, cudaStream_t stream);
+
+// A token drawn from each of M logit rows, one launch.
+int launch_sample(const void *logits, long long logits_stride, int dtype, int M, int V,
+                  const float *uniforms, const kvs_sample_rules &rules, int32_t *ids,
+                  float *token_probs, float *probs, long long probs_stride, cudaStream_t stream);
+
 // Sets the step kernel's attributes for (H / Hkv, D) on the current device
 // (done on first use anyway; a stream capture calls it beforehand).
 int prepare_step_kernel(int H, int Hkv, int D);
@@ -217,5 +233,6 @@ int set_wait_limit_prefill(uint64_t ns);
 int set_wait_limit_paged(uint64_t ns);
 int set_wait_limit_decode(uint64_t ns);
 int set_wait_limit_chunk(uint64_t ns);
+int set_wait_limit_decode_q8(uint64_t ns);
 
 }  // namespace kvs

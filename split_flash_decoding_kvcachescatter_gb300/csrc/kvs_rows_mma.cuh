@@ -117,6 +117,7 @@ struct WarpRows {
   // 255 registers)
   static constexpr bool QL1 = F32 && D == 128;
   static constexpr float kLift = std::is_same<T, __half>::value ? 10.f : 0.f;
+  static constexpr int kEach = F32 ? 4 : 2;  // columns of a piece of each()
   static constexpr int NQ = QL1 ? 1 : F32 ? D / 2 : D / 4;
 
   uint32_t qf[NQ];

@@ -70,6 +70,18 @@ static inline int make_row_map(CUtensorMap *map, const void *base, uint64_t rows
                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
+// Map over `lines` lines of 128 bytes: a copy of box_lines of them, 16-byte pieces
+// swizzled likewise.  Coordinates (0, line, 0).
+static inline int make_line_map(CUtensorMap *map, const void *base, uint64_t lines, int box_lines) {
+  const cuuint64_t dims[3] = {128, lines, 1};
+  const cuuint64_t strides[2] = {128, 128};
+  const cuuint32_t box[3] = {128, (cuuint32_t)box_lines, 1};
+  const cuuint32_t es[3] = {1, 1, 1};
+  return encode_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), dims, strides,
+                    box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+}
+
 // Map over rows of [heads][D] 16-bit elements, row_stride elements apart: a
 // copy takes box_heads heads of box_rows rows, one column block of 64
 // elements, as [box_rows][box_heads][128 bytes], swizzled likewise.

@@ -1,0 +1,81 @@
+// paged_decode_q8.cu -- attention over a paged KV cache in 8 bits for single
+// tokens (the kernels: kvs_decode.cuh, the products: kvs_rows_q8.cuh).
+
+#include "kvs_decode.cuh"
+#include "kvs_rows_q8.cuh"
+
+namespace kvs {
+
+namespace {
+
+// Pages in 8 bits under q and out of Type (kvs_decode.cuh).
+template <typename Type, int D_>
+struct PagesQ8 {
+  using T = Type;
+  using Rows = RowsQ8<T, D_>;
+  static constexpr int D = D_, kElem = 1;
+  static constexpr bool kScaled = true;
+  static constexpr bool kFewForm = true;
+  struct Extra {
+    const float *k_scales, *v_scales;
+  };
+  static constexpr int kFixBytes = 96 << 10;
+  static constexpr long long kBlockBytes = 512 << 10;
+  static constexpr long long kShortBytes = 128 << 10;
+  // the line of 128 bytes that row `row` of the pages begins in
+  static __device__ __forceinline__ int map_row(int row) { return D == 128 ? row : row >> 1; }
+  // Rows `left` and up of a tile become zero (by one warp).
+  static __device__ __forceinline__ void clear_rows(unsigned char *tile, int left) {
+    constexpr int KT = Rows::KT, PC = D / 16;  // 16-byte pieces of a row
+    for (int e = threadIdx.x & 31; e < (KT - left) * PC; e += 32) {
+      const int row = left + e / PC, line = D == 128 ? row : row >> 1;
+      const int pc = ((D == 128 ? 0 : (row & 1) * 4) + e % PC) ^ (line & 7);
+      *reinterpret_cast<uint4 *>(tile + line * 128 + pc * 16) = make_uint4(0, 0, 0, 0);
+    }
+  }
+};
+
+template <typename T, int D>
+int launch_q8(const void *q, long long q_stride, const kvs_paged_cache_q8 &cache,
+              const PagedArgs &pa, void *out, long long out_stride, int H, void *workspace,
+              int *d_status, cudaStream_t stream) {
+  CUtensorMap kmap, vmap;
+  const uint64_t rows = (uint64_t)cache.num_pages * cache.num_kv_heads * cache.page_size;
+  int rc = make_line_map(&kmap, cache.k_pages, rows * D / 128, 16 * D / 128);
+  if (rc == KVS_OK) rc = make_line_map(&vmap, cache.v_pages, rows * D / 128, 16 * D / 128);
+  if (rc != KVS_OK) return rc;
+  return launch_decode<PagesQ8<T, D>>(q, q_stride, kmap, vmap, {cache.k_scales, cache.v_scales},
+                                      cache.num_kv_heads, pa, out, out_stride, H, workspace,
+                                      d_status, stream);
+}
+
+}  // namespace
+
+int set_wait_limit_decode_q8(uint64_t ns) {
+  if (set_unit_wait_limit(ns) != cudaSuccess) {
+    cudaGetLastError();
+    return KVS_ERR_LAUNCH;
+  }
+  return KVS_OK;
+}
+
+size_t paged_attention_q8_workspace_bytes(int, int, int D, int) {
+  return paged_decode_workspace_bytes(D);
+}
+
+int launch_paged_attention_q8(const void *q, long long q_stride, const kvs_paged_cache_q8 &cache,
+                           int dtype, const PagedArgs &pa, void *out, long long out_stride, int H,
+                           void *workspace, int *d_status, cudaStream_t stream) {
+#define KVS_DECODE(T)                                                                           \
+  return cache.head_dim == 64                                                                   \
+             ? launch_q8<T, 64>(q, q_stride, cache, pa, out, out_stride, H, workspace,          \
+                                d_status, stream)                                               \
+             : launch_q8<T, 128>(q, q_stride, cache, pa, out, out_stride, H, workspace,         \
+                                 d_status, stream)
+  if (dtype == KVS_F32) KVS_DECODE(float);
+  if (dtype == KVS_F16) KVS_DECODE(__half);
+  KVS_DECODE(__nv_bfloat16);
+#undef KVS_DECODE
+}
+
+}  // namespace kvs
