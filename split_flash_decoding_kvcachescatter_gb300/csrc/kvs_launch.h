@@ -199,6 +199,12 @@ int launch_paged_attention_q8(const void *q, long long q_stride, const kvs_paged
                               int dtype, const PagedArgs &b, void *out, long long out_stride, int H,
                               void *workspace, int *d_status, cudaStream_t stream);
 
+// Its tensor-core variant for chunks (q in float16 or bfloat16; the workspace of
+// launch_paged_chunk).
+int launch_paged_chunk_q8(const void *q, long long q_stride, const kvs_paged_cache_q8 &cache,
+                          int dtype, const PagedArgs &b, void *out, long long out_stride, int H,
+                          void *workspace, int *d_status, cudaStream_t stream);
+
 // A token drawn from each of M logit rows, one launch.
 int launch_sample(const void *logits, long long logits_stride, int dtype, int M, int V,
                   const float *uniforms, const kvs_sample_rules &rules, int32_t *ids,
@@ -234,5 +240,6 @@ int set_wait_limit_paged(uint64_t ns);
 int set_wait_limit_decode(uint64_t ns);
 int set_wait_limit_chunk(uint64_t ns);
 int set_wait_limit_decode_q8(uint64_t ns);
+int set_wait_limit_chunk_q8(uint64_t ns);
 
 }  // namespace kvs

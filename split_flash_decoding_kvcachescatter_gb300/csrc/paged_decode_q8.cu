@@ -59,13 +59,18 @@ int set_wait_limit_decode_q8(uint64_t ns) {
   return KVS_OK;
 }
 
-size_t paged_attention_q8_workspace_bytes(int, int, int D, int) {
-  return paged_decode_workspace_bytes(D);
+size_t paged_attention_q8_workspace_bytes(int H, int Hkv, int D, int max_new) {
+  // (float32 chunks take the decode kernel too)
+  const size_t rows = paged_decode_workspace_bytes(D);
+  return (long long)max_new * (H / Hkv) <= kDRows ? rows : std::max(rows, paged_chunk_workspace_bytes(D));
 }
 
 int launch_paged_attention_q8(const void *q, long long q_stride, const kvs_paged_cache_q8 &cache,
-                           int dtype, const PagedArgs &pa, void *out, long long out_stride, int H,
-                           void *workspace, int *d_status, cudaStream_t stream) {
+                              int dtype, const PagedArgs &pa, void *out, long long out_stride, int H,
+                              void *workspace, int *d_status, cudaStream_t stream) {
+  if ((long long)pa.max_new * (H / cache.num_kv_heads) > kDRows && dtype != KVS_F32)
+    return launch_paged_chunk_q8(q, q_stride, cache, dtype, pa, out, out_stride, H, workspace,
+                                 d_status, stream);
 #define KVS_DECODE(T)                                                                           \
   return cache.head_dim == 64                                                                   \
              ? launch_q8<T, 64>(q, q_stride, cache, pa, out, out_stride, H, workspace,          \
