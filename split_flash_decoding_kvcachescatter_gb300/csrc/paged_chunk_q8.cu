@@ -3,22 +3,25 @@
 // bfloat16.
 //
 // Mathematics and split: as paged_chunk.cu; scales as kvs_rows_q8.cuh: stored
-// numbers are exact in float16, so both products run in float16, K's scales go into
-// the exponent, and a row's reference is the maximum of score + log2(V's scale), so
-// that the weights of the stored V numbers are 2^13 at most however the scales
-// differ; a block's share of the row sum is its weights' sum over V's scale.
+// numbers are exact in float16, so both products run in float16.  A tile of 128 keys
+// has one scale for K and one for V, the largest of its blocks'; where a block's is
+// smaller its numbers are multiplied by the quotient on their way to float16, which
+// for powers of two rounds only what is 2^-33 of the tile's largest or less.  The
+// tile's scale of K goes into the exponent, and a row's reference is the maximum of
+// score + log2(V's scale), so that the weights of V's numbers are 2^13 at most however
+// the scales differ; a tile's share of the row sum is its weights' sum over V's scale.
 // bfloat16 rows of q are brought to 2^15 by a power of two (exact down to 2^-28 of
 // the row's largest element).  Weights are rounded to float16 for the product: they
 // keep 11 bits for bfloat16 too.
 //
 // Block (16 warps, one block an SM):
-//   warps 0-3, 4-7  softmax of tile A and of tile B (168 registers a thread)
+//   warps 0-3, 4-7  softmax of tile A and of tile B
 //   warp 8, 9       issue S_x = Q_x K^T and O_x += P_x V, as in paged_chunk.cu
 //   warp 10         walks the units, describes each to the others, copies Q
-//   warps 12-15     read K and V from the pages, 16 bytes a thread at a time a tile
-//                   ahead, and write them as float16 in the layout that the tensor
-//                   cores read (K one tile ahead of V); the blocks' scales; bfloat16
-//                   queries to float16 in place
+//   warp 11         copies K and V, half a tile (64 keys) at a time, into a ring, and
+//                   makes the scales of each tile
+//   warps 12-15     write the halves as float16 in the layout that the tensor cores
+//                   read (K one tile ahead of V); bfloat16 queries to float16 in place
 // TMEM as in paged_chunk.cu.
 
 #include <cmath>
@@ -33,15 +36,22 @@ namespace kvs {
 
 namespace {
 
-constexpr int kCqMmaWarp = 8, kCqPvWarp = 9, kCqUnitWarp = 10, kCqReadWarp = 12;
+constexpr int kCqMmaWarp = 8, kCqPvWarp = 9, kCqUnitWarp = 10, kCqCopyWarp = 11, kCqTurnWarp = 12;
 constexpr int kCqThreads = 16 * 32;
 // registers a thread: 128 each at launch; the shares' sum is the launch's
-constexpr int kCqRegsSoftmax = 168, kCqRegsIssue = 72, kCqRegsRead = 104;
-static_assert(2 * kCqRegsSoftmax + kCqRegsIssue + kCqRegsRead <= 4 * 128, "what the launch has");
+constexpr int kCqRegsSoftmax = 184, kCqRegsIssue = 72, kCqRegsTurn = 72;
+static_assert(2 * kCqRegsSoftmax + kCqRegsIssue + kCqRegsTurn <= 4 * 128, "what the launch has");
 // as paged_chunk.cu's
 constexpr int kCqFix = 384;
 constexpr int kCqMinRange = 768;
 constexpr float kCqLift = 5.f;
+
+// The scales of a key tile: its blocks' over the tile's, twice in float16, and the
+// tile's: K's times log2(e) / sqrt(D), log2 of V's and 1 / V's.
+struct CqScales {
+  uint32_t k[8], v[8];
+  float score, lg, inv, pad;
+};
 
 template <int D>
 struct CqGeo {
@@ -49,17 +59,23 @@ struct CqGeo {
   static constexpr int BLK = 128 * 128;           // bytes of a block of 128 rows
   static constexpr int TILE = NB * BLK;           // one tile of Q, K or V in float16
   static constexpr int KS = 2, VS = 2;            // stages
-  static constexpr int SR = 4;                    // tiles whose scales are kept
+  static constexpr int HK = kCN / 2;              // keys of a half, as they come from the pages
+  static constexpr int HALF = HK * D;             // its bytes
+  static constexpr int RH = D == 128 ? 3 : 6;     // halves in the ring
+  static constexpr int SR = 8;                    // tiles whose scales are kept
   static constexpr int OFF_Q = 0;                 // Q_A, Q_B
   static constexpr int OFF_K = 2 * TILE;
   static constexpr int OFF_V = OFF_K + KS * TILE;
-  static constexpr int OFF_STAGE = OFF_V + VS * TILE;  // 4 KB a softmax warp: rows on their way out
-  static constexpr int OFF_QFAC = OFF_STAGE + 8 * 4096;  // float [2][2][128]: factors of the rows, by unit parity
-  static constexpr int OFF_SCALE = OFF_QFAC + 2 * 2 * 128 * 4;  // float [SR][3][8]
-  static constexpr int OFF_BAR = OFF_SCALE + SR * 3 * 8 * 4;
+  static constexpr int OFF_STAGE = OFF_V + VS * TILE;  // 1 KB a softmax warp: rows on their way out
+  static constexpr int OFF_RAW = OFF_STAGE + 8 * 1024;
+  // exponents of the rows' factors (biased), by unit parity: uint8 [2][2][128]
+  static constexpr int OFF_QFAC = OFF_RAW + RH * HALF;
+  static constexpr int OFF_SCALE = OFF_QFAC + 2 * 2 * 128;  // CqScales [SR]
+  static constexpr int OFF_BAR = OFF_SCALE + SR * (int)sizeof(CqScales);
   // q, qraw, qfree, kfull[KS], kfree[KS], vfull[VS], vfree[VS], sfull[2], sread,
-  // pfull[2], pvdone[2], wg[2], final[2], ufull[kCUnits], ufree[kCUnits], sgone[4], sbar[SR]
-  static constexpr int NBAR = 3 + 2 * KS + 2 * VS + 2 + 1 + 6 + 2 + 2 * kCUnits + 4 + SR;
+  // pfull[2], pvdone[2], wg[2], final[2], ufull[kCUnits], ufree[kCUnits], sgone[4], sbar[SR],
+  // rfull[RH], rfree[RH], qf[2]
+  static constexpr int NBAR = 3 + 2 * KS + 2 * VS + 2 + 1 + 6 + 2 + 2 * kCUnits + 4 + SR + 2 * RH + 2;
   static constexpr int OFF_TMEM = OFF_BAR + NBAR * 8;
   static constexpr int OFF_MISC = OFF_TMEM + 8;   // abort, last[2], pad
   static constexpr int OFF_UNIT = OFF_MISC + 16;  // CUnit [kCUnits]
@@ -83,12 +99,17 @@ struct CqCache {
   const float *k_scales, *v_scales;
 };
 
-// 16 e4m3 numbers as float16, 16-byte pieces 2c and 2c + 1 of a row at `row` of a
+// 16 e4m3 numbers times `by` (float16 twice) as float16, 16-byte pieces 2c and 2c + 1 of a row at `row` of a
 // tile (128 bytes a row and column block, swizzled by the row).
 template <int D>
-__device__ __forceinline__ void put_piece(unsigned char *tile, int row, int c, uint4 x) {
-  const uint4 lo = make_uint4(from_e4m3x2(x.x), from_e4m3x2(x.x >> 16), from_e4m3x2(x.y), from_e4m3x2(x.y >> 16));
-  const uint4 hi = make_uint4(from_e4m3x2(x.z), from_e4m3x2(x.z >> 16), from_e4m3x2(x.w), from_e4m3x2(x.w >> 16));
+__device__ __forceinline__ void put_piece(unsigned char *tile, int row, int c, uint4 x, uint32_t by) {
+  auto turn = [&](uint32_t w) {
+    const uint32_t f = from_e4m3x2(w);
+    const __half2 r = __hmul2(*reinterpret_cast<const __half2 *>(&f), *reinterpret_cast<const __half2 *>(&by));
+    return *reinterpret_cast<const uint32_t *>(&r);
+  };
+  const uint4 lo = make_uint4(turn(x.x), turn(x.x >> 16), turn(x.y), turn(x.y >> 16));
+  const uint4 hi = make_uint4(turn(x.z), turn(x.z >> 16), turn(x.w), turn(x.w >> 16));
   unsigned char *at = tile + (c >> 2) * (128 * 128) + row * 128;
   const int p = (2 * c) & 7;
   // (the lanes of the second column block write their upper half first: no bank conflicts)
@@ -110,7 +131,7 @@ __global__ void __launch_bounds__(kCqThreads, 1)
   uint64_t *bar_q = bars;            // Q of the unit is there in float16
   uint64_t *bar_qraw = bar_q + 1;    // Q of the unit landed
   uint64_t *qfree = bar_qraw + 1;    // the unit's S products done (commit)
-  uint64_t *kfull = qfree + 1;       // [KS] an arrival a reading warp
+  uint64_t *kfull = qfree + 1;       // [KS] an arrival a turning warp
   uint64_t *kfree = kfull + KS;      // [KS] the S products of a stage done (commit)
   uint64_t *vfull = kfree + KS;      // [VS]
   uint64_t *vfree = vfull + VS;      // [VS] the P V products of a stage done (commit)
@@ -121,15 +142,18 @@ __global__ void __launch_bounds__(kCqThreads, 1)
   uint64_t *wgbar = pvdone + 2;      // [2] the warps of a warpgroup
   uint64_t *final = wgbar + 2;       // [2] every product S, every P V of the block done (commit)
   uint64_t *ufull = final + 2;       // [kCUnits] a unit is described
-  uint64_t *ufree = ufull + kCUnits; // [kCUnits] the 14 other warps are done with it
+  uint64_t *ufree = ufull + kCUnits; // [kCUnits] the 15 other warps are done with it
   uint64_t *sgone = ufree + kCUnits; // [4] S product k of the block issued, at k % 4
-  uint64_t *sbar = sgone + 4;        // [SR] scales of key tile k (and factors of its unit's rows), at k % SR
+  uint64_t *sbar = sgone + 4;        // [SR] scales of key tile k, at k % SR
+  uint64_t *rfull = sbar + SR;       // [RH] a half has landed
+  uint64_t *rfree = rfull + C::RH;   // [RH] and has been read (an arrival a turning warp)
+  uint64_t *qf = rfree + C::RH;      // [2] factors of unit n's rows, at n % 2 (an arrival a turning warp)
   CUnit *units = reinterpret_cast<CUnit *>(smem + C::OFF_UNIT);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_TMEM);
   volatile int *abort = reinterpret_cast<volatile int *>(smem + C::OFF_MISC);
   volatile int *s_last = abort + 1;  // [2]
-  float *qfac = reinterpret_cast<float *>(smem + C::OFF_QFAC);
-  float *scales = reinterpret_cast<float *>(smem + C::OFF_SCALE);
+  unsigned char *qfac = smem + C::OFF_QFAC;
+  CqScales *scales = reinterpret_cast<CqScales *>(smem + C::OFF_SCALE);
   unsigned *epoch = reinterpret_cast<unsigned *>(ws);
   unsigned long long *counters = reinterpret_cast<unsigned long long *>(ws + 256);
   float *slots = reinterpret_cast<float *>(ws + 256 + (size_t)kPagedMaxBlocks * 16);
@@ -144,12 +168,12 @@ __global__ void __launch_bounds__(kCqThreads, 1)
     prefetch_map(&qmap);
     for (int j = 0; j < C::NBAR; ++j) {  // each once
       uint64_t *bar = bars + j;
-      // an arrival a warp of the softmax's four or the four that read
+      // an arrival a warp of the softmax's four or the four that turn
       const bool of_four = bar == sread || bar == pfull || bar == pfull + 1 || bar == wgbar ||
                            bar == wgbar + 1 || (kTurnQ && bar == bar_q) ||
                            (bar >= kfull && bar < kfull + KS) || (bar >= vfull && bar < vfull + VS) ||
-                           bar >= sbar;
-      mbar_init(bar, of_four ? 4 : bar >= ufree && bar < ufree + kCUnits ? 14 : 1);
+                           bar >= rfree;
+      mbar_init(bar, of_four ? 4 : bar >= ufree && bar < ufree + kCUnits ? 15 : 1);
     }
     *abort = 0;
     fence_mbar_init();
@@ -194,7 +218,7 @@ __global__ void __launch_bounds__(kCqThreads, 1)
     const uint32_t tm_s = tmem + lane_base;
     const uint32_t tm_p = tmem + lane_base + kCN + x * (kCN / 2);
     const uint32_t tm_o = tmem + lane_base + 2 * kCN + x * D;
-    unsigned char *stg = smem + C::OFF_STAGE + warp * 4096;
+    unsigned char *stg = smem + C::OFF_STAGE + warp * 1024;
     int sb = 0;   // S_x products of the earlier units
     int kt0 = 0;  // key tiles of the earlier units
     uint32_t wphase = 0;
@@ -237,8 +261,15 @@ __global__ void __launch_bounds__(kCqThreads, 1)
           break;
         }
         tc_fence_after();
-        if (kTurnQ && n == tl.lo) fac = qfac[(nq & 1) * 256 + x * 128 + t];
-        const float *sc = scales + (kt % SR) * 24;  // K's times sl2, log2 of V's, 1 / V's
+        if (kTurnQ && n == tl.lo) {
+          if (!__all_sync(0xffffffffu, mbar_wait<kPoll>(&qf[nq & 1], (uint32_t)(nq >> 1) & 1u, abort))) {
+            failed = true;
+            break;
+          }
+          fac = __uint_as_float((unsigned)qfac[(nq & 1) * 256 + x * 128 + t] << 23);
+        }
+        const CqScales &sc = scales[kt % SR];
+        const float f = fac * sc.score, lg = sc.lg, inv = sc.inv;  // (f > 0)
         float r[kCN];
         tmem_ld64(tm_s, *reinterpret_cast<float(*)[64]>(&r[0]));
         tmem_ld64(tm_s + 64, *reinterpret_cast<float(*)[64]>(&r[64]));
@@ -252,20 +283,13 @@ __global__ void __launch_bounds__(kCqThreads, 1)
 #pragma unroll
           for (int v = 0; v < kCN; ++v) r[v] = v <= lim ? r[v] : neg_inf_f();
         }
-        // (a factor of 0 would make NaN of -inf; what is below 10^-30 is nothing in an exponent)
-        auto factor = [&](int g) { return fmaxf(fac * sc[g], 1e-30f); };
-        float cm = neg_inf_f();
+        float mx[4] = {r[0], r[1], r[2], r[3]};  // four chains (max is exact in any order)
 #pragma unroll
-        for (int g = 0; g < 8; ++g) {
-          float m0 = fmaxf(r[16 * g], r[16 * g + 2]), m1 = fmaxf(r[16 * g + 1], r[16 * g + 3]);
+        for (int v = 4; v < kCN; v += 4) {
 #pragma unroll
-          for (int v = 4; v < 16; v += 2) {
-            m0 = fmaxf(m0, r[16 * g + v]);
-            m1 = fmaxf(m1, r[16 * g + v + 1]);
-          }
-          cm = fmaxf(cm, fmaf(fmaxf(m0, m1), factor(g), sc[8 + g]));
+          for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], r[v + k]);
         }
-        cm -= kCqLift;
+        const float cm = fmaf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), f, lg - kCqLift);
         // the reference moves only when the row's grows by more than 2^kCRescale
         // (rows that do not exist hold anything: they never ask for a rescale)
         const float m_ref = cm > m + kCRescale ? cm : m;
@@ -291,28 +315,21 @@ __global__ void __launch_bounds__(kCqThreads, 1)
           }
         }
         const float mb = (m_ref == neg_inf_f()) ? 0.f : m_ref;
-        float ls = 0.f;
+        float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        const float2 f2 = make_float2(f, f), up2 = make_float2(lg - mb, lg - mb);
 #pragma unroll
         for (int ch = 0; ch < 4; ++ch) {
           uint32_t w[16];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int g = 2 * ch + h;
-            const float fg = factor(g), up = sc[8 + g] - mb;
-            const float2 f2 = make_float2(fg, fg), up2 = make_float2(up, up);
-            float2 gs = make_float2(0.f, 0.f);
-#pragma unroll
-            for (int v = 0; v < 8; ++v) {
-              const float2 x2 = __ffma2_rn(make_float2(r[16 * g + 2 * v], r[16 * g + 2 * v + 1]), f2, up2);
-              const float p0 = ex2(x2.x), p1 = ex2(x2.y);
-              gs = __fadd2_rn(gs, make_float2(p0, p1));
-              w[8 * h + v] = pack_pair<__half>(p0, p1);
-            }
-            ls = fmaf(gs.x + gs.y, sc[16 + g], ls);
+          for (int v = 0; v < 16; ++v) {
+            const float2 x2 = __ffma2_rn(make_float2(r[32 * ch + 2 * v], r[32 * ch + 2 * v + 1]), f2, up2);
+            const float p0 = ex2(x2.x), p1 = ex2(x2.y);
+            ls[v & 1] = __fadd2_rn(ls[v & 1], make_float2(p0, p1));
+            w[v] = pack_pair<__half>(p0, p1);
           }
           tmem_st16u(tm_p + ch * 16, w);
         }
-        l = l * alpha + ls;
+        l = fmaf((ls[0].x + ls[1].x) + (ls[0].y + ls[1].y), inv, l * alpha);
         m = m_ref;
         tmem_wait_st();
         tc_fence_before();
@@ -330,7 +347,7 @@ __global__ void __launch_bounds__(kCqThreads, 1)
         }
         tc_fence_after();
         // (the unit is read again there: in registers it would crowd out the row)
-        if (!finish_tile<T, D>(out, out_stride, &units[nq % kCUnits], tl, x, t, lane, live, tok, G, b,
+        if (!finish_tile<T, D, false>(out, out_stride, &units[nq % kCUnits], tl, x, t, lane, live, tok, G, b,
                                tm_o, m, l, stg, slots, counters, tag, epoch, d_status, s_last,
                                wg_barrier)) {
           failed = true;
@@ -340,7 +357,7 @@ __global__ void __launch_bounds__(kCqThreads, 1)
       unit_done(nq);
     }
     if (failed && lane == 0) give_up(abort, d_status, epoch);
-  } else if (warp < kCqReadWarp) {
+  } else if (warp < kCqTurnWarp) {
     fewer_registers<kCqRegsIssue>();
     if (warp == kCqUnitWarp) {
       // ======================= units, Q =======================================
@@ -396,6 +413,114 @@ __global__ void __launch_bounds__(kCqThreads, 1)
         if (!ok) give_up(abort, d_status, epoch);
         // every copy issued lands before the block can exit
         if (nq > 0) mbar_wait_drain(qbar, (uint32_t)(nq - 1) & 1u);
+      }
+      __syncwarp();
+    } else if (warp == kCqCopyWarp) {
+      // ======================= halves of K and V, scales =======================
+      // A key tile: this lane's group of 16 rows is number lane % 8 of it; lanes 0 to 7
+      // have K's scales, 8 to 15 V's.
+      struct Tile {
+        int page, row, left;  // page of the group; its first row in the pages; keys from the tile's first on
+        int nq, g, key;       // unit, kv head, first key of the group
+        bool first;           // of its unit
+        float scale;
+      };
+      int uq = -1, n = 0;
+      CUnit f{};
+      bool ok = true;
+      // The next key tile of the block, its pages asked for; false after the last one.
+      auto next = [&](Tile &a) -> bool {
+        a.first = uq < 0 || n + 1 >= f.t_hi;
+        if (a.first) {
+          if (uq >= 0) unit_done(uq);
+          if (!(ok = unit(++uq, f)) || f.t_lo == f.t_hi) return false;
+          n = f.t_lo;
+        } else {
+          ++n;
+        }
+        a.nq = uq;
+        a.g = f.g;
+        a.left = f.L - n * kCN;
+        a.key = n * kCN + 16 * (lane & 7);
+        a.page = a.key < f.L ? __ldca(pa.page_table + (size_t)f.seq * pa.max_pages + (a.key >> pa.page_shift)) : 0;
+        return true;
+      };
+      // Its rows, once the pages are known; the scales asked for.
+      auto resolve = [&](Tile &a) {
+        if ((unsigned)a.page >= (unsigned)pa.num_pages) {
+          record_status(d_status, KVS_ERR_PAGE);
+          *const_cast<volatile int *>(&units[a.nq % kCUnits].bad) = 1;
+          a.page = 0;
+        }
+        a.row = ((a.page * Hkv + a.g) << pa.page_shift) + (a.key & ((1 << pa.page_shift) - 1));
+        a.scale = 0.f;
+        if (lane < 16 && 16 * (lane & 7) < a.left)
+          a.scale = __ldcg((lane < 8 ? cache.k_scales : cache.v_scales) + (a.row >> 4));
+      };
+      const int run = min(1 << pa.page_shift, C::HK);  // keys of a copy
+      int nr = 0, nk = 0;  // halves copied, tiles whose scales are there
+      auto wait = [&](uint64_t *bar, uint32_t phase) {
+        return ok = __all_sync(0xffffffffu, mbar_wait<kPoll>(bar, phase & 1u, abort)) != 0;
+      };
+      auto copy = [&](const Tile &a, const unsigned char *pages) {
+        for (int h = 0; h < 2; ++h) {
+          const int st = nr % C::RH;
+          if (nr >= C::RH && !wait(&rfree[st], (uint32_t)((nr - C::RH) / C::RH))) return;
+          const int live = min(C::HK, max(0, (a.left - h * C::HK + 15) & ~15));
+          if (lane == 0) mbar_arrive_expect_tx(&rfull[st], (uint32_t)(live * D));
+          const int at = (lane * run) & (C::HK - 1);  // first key of this lane's copy
+          const int row = __shfl_sync(0xffffffffu, a.row, h * 4 + at / 16);
+          if (lane * run < live)
+            bulk_g2s(smem + C::OFF_RAW + st * C::HALF + at * D, pages + (size_t)row * D,
+                     (uint32_t)(min(run, live - at) * D), &rfull[st]);
+          __syncwarp();
+          ++nr;
+        }
+      };
+      Tile p{}, a{}, c{};  // the tile before (V still to be copied), this one, the next one
+      bool have = next(a), behind = false;
+      if (have) resolve(a);
+      bool more = have && next(c);
+      while (have && ok) {
+        if (a.first && behind) {  // (in the order in which the halves are used)
+          copy(p, cache.v_pages);
+          if (!ok) break;
+          behind = false;
+        }
+        // the tile's scales: the largest of its blocks' and what each is of that
+        float most = a.scale;
+#pragma unroll
+        for (int o = 4; o >= 1; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+        most = fmaxf(most, 8.673617379884035e-19f);  // 2^-60
+        CqScales &sc = scales[nk % SR];
+        if (lane < 16) {
+          const __half2 by = __float2half2_rn(a.scale / most);
+          (lane < 8 ? sc.k : sc.v)[lane & 7] = *reinterpret_cast<const uint32_t *>(&by);
+          if (lane == 0) sc.score = most * sl2;
+          if (lane == 8) value_scale(most, sc.lg, sc.inv);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sbar[nk % SR]);
+        ++nk;
+        copy(a, cache.k_pages);
+        if (!ok) break;
+        if (more) resolve(c);
+        if (behind) {
+          copy(p, cache.v_pages);
+          if (!ok) break;
+        }
+        behind = true;
+        p = a;
+        a = c;
+        have = more;
+        more = have && next(c);
+      }
+      if (ok && behind) copy(p, cache.v_pages);
+      if (lane == 0) {
+        if (!ok) give_up(abort, d_status, epoch);
+        // every copy issued lands before the block can exit
+        for (int j = (nr > C::RH ? nr - C::RH : 0); j < nr; ++j)
+          mbar_wait_drain(&rfull[j % C::RH], (uint32_t)(j / C::RH) & 1u);
       }
       __syncwarp();
     } else if (warp == kCqMmaWarp) {
@@ -500,155 +625,105 @@ __global__ void __launch_bounds__(kCqThreads, 1)
       __syncwarp();
     }
   } else {
-    // ======================= K and V from the pages ============================
-    fewer_registers<kCqRegsRead>();
-    constexpr int PC = D / 16;        // 16-byte pieces of a row
-    constexpr int NV = 128 * PC / 128;  // of a tile, a thread
+    // ======================= K and V to float16 ================================
+    fewer_registers<kCqRegsTurn>();
+    constexpr int PC = D / 16;               // 16-byte pieces of a row
+    constexpr int NV = C::HALF / 16 / 128;   // of a half, a thread
     const int t = threadIdx.x & 127;
-    // piece i of this thread: row (i 128 + t) / PC of the tile, piece t % PC of it
-    const int pc = t % PC;
-    // A key tile: this lane's group of 16 rows is number lane % 8.
-    struct Tile {
-      int page, row, left;  // page of the group; its first row in the pages; keys from the tile's first on
-      int nq, g, key;       // unit, kv head, first key of the group
-      int tiles;            // row tiles of the unit; 0: not the unit's first key tile
-      float ks, vs;         // the group's scales (warp kCqReadWarp)
-    };
-    int uq = -1, n = 0;
-    CUnit f{};
     bool ok = true;
-    // The next key tile of the block, its pages asked for; false after the last one.
-    auto next = [&](Tile &a) -> bool {
-      a.tiles = 0;
-      if (uq < 0 || n + 1 >= f.t_hi) {
-        if (uq >= 0) unit_done(uq);
-        if (!(ok = unit(++uq, f)) || f.t_lo == f.t_hi) return false;
-        n = f.t_lo;
-        a.tiles = f.ntok > TT ? 2 : 1;
-      } else {
-        ++n;
-      }
-      a.nq = uq;
-      a.g = f.g;
-      a.left = f.L - n * kCN;
-      a.key = n * kCN + 16 * (lane & 7);
-      a.page = a.key < f.L ? __ldca(pa.page_table + (size_t)f.seq * pa.max_pages + (a.key >> pa.page_shift)) : 0;
-      return true;
+    auto wait = [&](uint64_t *bar, uint32_t phase) {
+      return ok = __all_sync(0xffffffffu, mbar_wait<kPoll>(bar, phase & 1u, abort)) != 0;
     };
-    // Its rows, once the pages are known; the scales asked for.
-    auto resolve = [&](Tile &a) {
-      if ((unsigned)a.page >= (unsigned)pa.num_pages) {
-        record_status(d_status, KVS_ERR_PAGE);
-        *const_cast<volatile int *>(&units[a.nq % kCUnits].bad) = 1;
-        a.page = 0;
-      }
-      a.row = ((a.page * Hkv + a.g) << pa.page_shift) + (a.key & ((1 << pa.page_shift) - 1));
-      a.ks = a.vs = 1.f;
-      if (warp == kCqReadWarp && lane < 8 && 16 * lane < a.left) {
-        a.ks = __ldcg(cache.k_scales + (a.row >> 4));
-        a.vs = __ldcg(cache.v_scales + (a.row >> 4));
-      }
-    };
-    auto load = [&](const Tile &a, const unsigned char *pages, uint4 (&v)[NV]) {
+    int nr = 0, nk = 0, nv = 0;  // halves read, K and V tiles written
+    // The ring's next two halves, with `left` keys from the tile's first on, as a tile.
+    auto turn = [&](unsigned char *tile, const uint32_t *by, int left, uint64_t *full) {
+#pragma unroll 1
+      for (int h = 0; h < 2; ++h) {
+        const int st = nr % C::RH;
+        if (!wait(&rfull[st], (uint32_t)(nr / C::RH))) return;
+        uint4 v[NV];
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int r = (i * 128 + t) / PC;  // row of the tile
-        const int row = __shfl_sync(0xffffffffu, a.row, r >> 4) + (r & 15);
-        v[i] = r < a.left ? __ldcg(reinterpret_cast<const uint4 *>(pages + (size_t)row * D + pc * 16))
-                          : make_uint4(0, 0, 0, 0);
-      }
-    };
-    auto put = [&](unsigned char *tile, const uint4 (&v)[NV], uint64_t *full) {
+        for (int i = 0; i < NV; ++i)
+          v[i] = *reinterpret_cast<const uint4 *>(smem + C::OFF_RAW + st * C::HALF + (i * 128 + t) * 16);
 #pragma unroll
-      for (int i = 0; i < NV; ++i) put_piece<D>(tile, (i * 128 + t) / PC, pc, v[i]);
+        for (int i = 0; i < NV; ++i) {
+          const int row = h * C::HK + (i * 128 + t) / PC;
+          // (rows behind the last key hold anything)
+          put_piece<D>(tile, row, t % PC, row < left ? v[i] : make_uint4(0, 0, 0, 0), by[row >> 4]);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&rfree[st]);
+        ++nr;
+      }
       fence_proxy_async_shared();
       __syncwarp();
       if (lane == 0) mbar_arrive(full);
     };
-    auto wait = [&](uint64_t *bar, uint32_t phase) {
-      return ok = __all_sync(0xffffffffu, mbar_wait<kPoll>(bar, phase & 1u, abort)) != 0;
-    };
-    uint4 kv[NV], vv[NV];
-    int nk = 0, nv = 0;  // K and V tiles written
-    auto put_v = [&]() {
+    int v_left = 0;  // of the tile whose V is to be written next
+    auto turn_v = [&]() {
       const int st = nv % VS;
       if (nv >= VS && !wait(&vfree[st], (uint32_t)((nv - VS) / VS))) return;
-      put(smem + C::OFF_V + st * C::TILE, vv, &vfull[st]);
+      turn(smem + C::OFF_V + st * C::TILE, scales[nv % SR].v, v_left, &vfull[st]);
       ++nv;
     };
-    Tile a{}, c{};
-    bool have = next(a), behind = false;  // behind: V of the tile before is still to be written
-    if (have) {
-      resolve(a);
-      load(a, cache.k_pages, kv);
-      load(a, cache.v_pages, vv);
-    }
-    bool more = have && next(c);
-    while (have && ok) {
-      if (a.tiles && behind) {  // (before anything of the next unit is waited for)
-        put_v();
-        if (!ok) break;
-        load(a, cache.v_pages, vv);
-        behind = false;
-      }
-      if (kTurnQ && a.tiles) {
-        // rows of q to float16 in place: a thread a row
-        if (!wait(bar_qraw, (uint32_t)a.nq)) break;
-        for (int x = 0; x < a.tiles; ++x) {
-          unsigned char *row = smem + C::OFF_Q + x * C::TILE + t * 128;
-          auto piece = [&](int j) {
-            return reinterpret_cast<uint4 *>(row + (j >> 3) * C::BLK + (((j & 7) ^ (t & 7)) * 16));
-          };
-          uint32_t most = 0;  // |elements| as integers: bfloat16 orders them
+    for (int nq = 0; ok; ++nq) {
+      CUnit f;
+      if (!(ok = unit(nq, f)) || f.t_lo == f.t_hi) break;
+      for (int n = f.t_lo; n < f.t_hi && ok; ++n) {
+        if (n == f.t_lo) {
+          if (nk > nv) turn_v();  // (before anything of this unit is waited for)
+          if (!ok) break;
+          if constexpr (kTurnQ) {
+            // rows of q to float16 in place: a thread a row
+            if (!wait(bar_qraw, (uint32_t)nq)) break;
+            for (int x = 0; x < (f.ntok > TT ? 2 : 1); ++x) {
+              unsigned char *row = smem + C::OFF_Q + x * C::TILE + t * 128;
+              auto piece = [&](int j) {
+                return reinterpret_cast<uint4 *>(row + (j >> 3) * C::BLK + (((j & 7) ^ (t & 7)) * 16));
+              };
+              uint32_t most = 0;  // |elements| as integers: bfloat16 orders them
 #pragma unroll 4
-          for (int j = 0; j < D / 8; ++j) {
-            const uint4 w = *piece(j);
-            most = __vmaxu2(__vmaxu2(most, __vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu)),
-                            __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu));
-          }
-          const int ex = max((int)(max(most & 0xffffu, most >> 16) >> 7) - 127, -100);  // largest < 2^(ex + 1)
-          const float up = __uint_as_float((unsigned)(14 - ex + 127) << 23);
+              for (int j = 0; j < D / 8; ++j) {
+                const uint4 w = *piece(j);
+                most = __vmaxu2(__vmaxu2(most, __vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu)),
+                                __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu));
+              }
+              // largest < 2^(ex + 1)
+              const int ex = max((int)(max(most & 0xffffu, most >> 16) >> 7) - 127, -60);
+              const float up = __uint_as_float((unsigned)(14 - ex + 127) << 23);
 #pragma unroll 4
-          for (int j = 0; j < D / 8; ++j) {
-            uint4 w = *piece(j);
-            auto turn = [&](uint32_t e) {
-              return pack_pair<__half>(__uint_as_float(e << 16) * up, __uint_as_float(e & 0xffff0000u) * up);
-            };
-            w = make_uint4(turn(w.x), turn(w.y), turn(w.z), turn(w.w));
-            *piece(j) = w;
+              for (int j = 0; j < D / 8; ++j) {
+                const uint4 w = *piece(j);
+                auto half2_of = [&](uint32_t e) {
+                  return pack_pair<__half>(__uint_as_float(e << 16) * up, __uint_as_float(e & 0xffff0000u) * up);
+                };
+                *piece(j) = make_uint4(half2_of(w.x), half2_of(w.y), half2_of(w.z), half2_of(w.w));
+              }
+              qfac[(nq & 1) * 256 + x * 128 + t] = (unsigned char)(ex - 14 + 127);
+            }
+            fence_proxy_async_shared();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(bar_q);
+              mbar_arrive(&qf[nq & 1]);
+            }
           }
-          qfac[(a.nq & 1) * 256 + x * 128 + t] = __uint_as_float((unsigned)(ex - 14 + 127) << 23);
         }
-        fence_proxy_async_shared();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar_q);
-      }
-      if (more) resolve(c);
-      const int st = nk % KS;
-      if (nk >= KS && !wait(&kfree[st], (uint32_t)((nk - KS) / KS))) break;
-      if (warp == kCqReadWarp && lane < 8) {
-        float lg, inv;
-        value_scale(a.vs, lg, inv);
-        float *sc = scales + (nk % SR) * 24 + lane;
-        sc[0] = a.ks * sl2;
-        sc[8] = lg;
-        sc[16] = inv;
-      }
-      put(smem + C::OFF_K + st * C::TILE, kv, &kfull[st]);  // (ends in a warp barrier)
-      if (lane == 0) mbar_arrive(&sbar[nk % SR]);
-      ++nk;
-      if (more) load(c, cache.k_pages, kv);
-      if (behind) {
-        put_v();
+        const int st = nk % KS;
+        if (nk >= KS && !wait(&kfree[st], (uint32_t)((nk - KS) / KS))) break;
+        if (!wait(&sbar[nk % SR], (uint32_t)(nk / SR))) break;
+        turn(smem + C::OFF_K + st * C::TILE, scales[nk % SR].k, f.L - n * kCN, &kfull[st]);
         if (!ok) break;
-        load(a, cache.v_pages, vv);
+        if (nk > nv) {
+          turn_v();
+          if (!ok) break;
+        }
+        ++nk;
+        v_left = f.L - n * kCN;
       }
-      behind = true;
-      a = c;
-      have = more;
-      more = have && next(c);
+      if (ok) unit_done(nq);
     }
-    if (ok && behind) put_v();
+    if (ok && nk > nv) turn_v();
     if (!ok && lane == 0) give_up(abort, d_status, epoch);
     __syncwarp();
   }

@@ -42,7 +42,7 @@ class PagedQ8:
         g.manual_seed(seed)
         rng = np.random.default_rng(seed)
         self.n, self.p, self.H, self.Hkv, self.D, self.page = n, p, H, Hkv, D, page
-        self.dtype = DTYPES[dtype]
+        self.dtype, self.powers = DTYPES[dtype], powers
         M = len(n)
         need = [-(-(a + b) // page) if a else 0 for a, b in zip(n, p)]
         total = sum(need) + spare
@@ -123,13 +123,17 @@ class PagedQ8:
             # step; three factors of 2^-24
             ds = size * ((2.0 ** -22 if f32 else 0) + self.D * 2.0 ** -39 + 3 * self.D / 8 * 2.0 ** -23
                          + 2.0 ** -22)
+            # chunks in 16 bits: numbers times their block's scale over the tile's, which for powers
+            # of two rounds what is 2^-33 of the largest or less, else twice to float16 (2^-12 each)
+            if not two:
+                ds += size * (2.0 ** -26 if self.powers else 2.0 ** -11)
             # exponents x + (log2 scale - m): sums of numbers of at most 1.5 size + lg, each
             # rounded to 2^-24 of itself; ex2 2^-22
             ds += 2 * (1.5 * size + lg) * 2.0 ** -24
             rel = 2 * ds + 2.0 ** -21
             # weights: a rounding to float16 (2^-12), or two parts (2^-22); the sums over L / 16
             # steps and that of the weights
-            rel = rel + (2.0 ** -22 if two else 2.0 ** -12) + (L / 16 * 2 + L / 8 + 64) * 2.0 ** -23
+            rel = rel + (2.0 ** -22 if two else 2.0 ** -12 if self.powers else 3 * 2.0 ** -12) + (L / 16 * 2 + L / 8 + 64) * 2.0 ** -23
             # weights that float16 no longer holds: 2^-25 beside 2^10 (2^5 in chunks)
             lost = L * vmax * 2.0 ** (-35 if two else -30)
             out[a:a + n] = o
