@@ -14,14 +14,14 @@
 // the row's largest element).  Weights are rounded to float16 for the product: they
 // keep 11 bits for bfloat16 too.
 //
-// Block (16 warps, one block an SM):
+// Block (20 warps, one block an SM):
 //   warps 0-3, 4-7  softmax of tile A and of tile B
 //   warp 8, 9       issue S_x = Q_x K^T and O_x += P_x V, as in paged_chunk.cu
 //   warp 10         walks the units, describes each to the others, copies Q
-//   warp 11         copies K and V, half a tile (64 keys) at a time, into a ring, and
-//                   makes the scales of each tile
-//   warps 12-15     write the halves as float16 in the layout that the tensor cores
-//                   read (K one tile ahead of V); bfloat16 queries to float16 in place
+//   warps 12-15, 16-19  K and V: each thread copies the pieces that it will turn, 32
+//                   keys at a time and three of those ahead, and writes them as float16
+//                   in the layout that the tensor cores read; the tiles' scales; the
+//                   latter warps also turn bfloat16 queries, in place
 // TMEM as in paged_chunk.cu.
 
 #include <cmath>
@@ -36,20 +36,19 @@ namespace kvs {
 
 namespace {
 
-constexpr int kCqMmaWarp = 8, kCqPvWarp = 9, kCqUnitWarp = 10, kCqCopyWarp = 11, kCqTurnWarp = 12;
-constexpr int kCqThreads = 16 * 32;
-// registers a thread: 128 each at launch; the shares' sum is the launch's
-constexpr int kCqRegsSoftmax = 184, kCqRegsIssue = 72, kCqRegsTurn = 72;
-static_assert(2 * kCqRegsSoftmax + kCqRegsIssue + kCqRegsTurn <= 4 * 128, "what the launch has");
+constexpr int kCqMmaWarp = 8, kCqPvWarp = 9, kCqUnitWarp = 10, kCqTurnWarp = 12;
+constexpr int kCqThreads = 20 * 32;
+// registers a thread: at launch, and by warpgroup; the shares' sum is the launch's
+constexpr int kCqRegs = 96;
+constexpr int kCqRegsSoftmax = 168, kCqRegsIssue = 48, kCqRegsTurn = 48;
+static_assert(2 * kCqRegsSoftmax + kCqRegsIssue + 2 * kCqRegsTurn == 5 * kCqRegs, "what the launch has");
 // as paged_chunk.cu's
 constexpr int kCqFix = 384;
 constexpr int kCqMinRange = 768;
 constexpr float kCqLift = 5.f;
 
-// The scales of a key tile: its blocks' over the tile's, twice in float16, and the
-// tile's: K's times log2(e) / sqrt(D), log2 of V's and 1 / V's.
+// The scales of a key tile: K's times log2(e) / sqrt(D), log2 of V's and 1 / V's.
 struct CqScales {
-  uint32_t k[8], v[8];
   float score, lg, inv, pad;
 };
 
@@ -58,10 +57,10 @@ struct CqGeo {
   static constexpr int NB = D / 64;               // 128-byte column blocks of a row
   static constexpr int BLK = 128 * 128;           // bytes of a block of 128 rows
   static constexpr int TILE = NB * BLK;           // one tile of Q, K or V in float16
-  static constexpr int KS = 2, VS = 2;            // stages
-  static constexpr int HK = kCN / 2;              // keys of a half, as they come from the pages
-  static constexpr int HALF = HK * D;             // its bytes
-  static constexpr int RH = D == 128 ? 3 : 6;     // halves in the ring
+  static constexpr int KS = 2, VS = 2;            // stages (the turning warps count on two)
+  static constexpr int QK = kCN / 4;              // keys of a quarter, as they come from the pages
+  static constexpr int QUARTER = QK * D;          // its bytes
+  static constexpr int RQ = 3;                    // quarters in a ring
   static constexpr int SR = 8;                    // tiles whose scales are kept
   static constexpr int OFF_Q = 0;                 // Q_A, Q_B
   static constexpr int OFF_K = 2 * TILE;
@@ -69,13 +68,13 @@ struct CqGeo {
   static constexpr int OFF_STAGE = OFF_V + VS * TILE;  // 1 KB a softmax warp: rows on their way out
   static constexpr int OFF_RAW = OFF_STAGE + 8 * 1024;
   // exponents of the rows' factors (biased), by unit parity: uint8 [2][2][128]
-  static constexpr int OFF_QFAC = OFF_RAW + RH * HALF;
+  static constexpr int OFF_QFAC = OFF_RAW + 2 * RQ * QUARTER;
   static constexpr int OFF_SCALE = OFF_QFAC + 2 * 2 * 128;  // CqScales [SR]
   static constexpr int OFF_BAR = OFF_SCALE + SR * (int)sizeof(CqScales);
   // q, qraw, qfree, kfull[KS], kfree[KS], vfull[VS], vfree[VS], sfull[2], sread,
   // pfull[2], pvdone[2], wg[2], final[2], ufull[kCUnits], ufree[kCUnits], sgone[4], sbar[SR],
-  // rfull[RH], rfree[RH], qf[2]
-  static constexpr int NBAR = 3 + 2 * KS + 2 * VS + 2 + 1 + 6 + 2 + 2 * kCUnits + 4 + SR + 2 * RH + 2;
+  // qf[2]
+  static constexpr int NBAR = 3 + 2 * KS + 2 * VS + 2 + 1 + 6 + 2 + 2 * kCUnits + 4 + SR + 2;
   static constexpr int OFF_TMEM = OFF_BAR + NBAR * 8;
   static constexpr int OFF_MISC = OFF_TMEM + 8;   // abort, last[2], pad
   static constexpr int OFF_UNIT = OFF_MISC + 16;  // CUnit [kCUnits]
@@ -99,23 +98,11 @@ struct CqCache {
   const float *k_scales, *v_scales;
 };
 
-// 16 e4m3 numbers times `by` (float16 twice) as float16, 16-byte pieces 2c and 2c + 1 of a row at `row` of a
-// tile (128 bytes a row and column block, swizzled by the row).
-template <int D>
-__device__ __forceinline__ void put_piece(unsigned char *tile, int row, int c, uint4 x, uint32_t by) {
-  auto turn = [&](uint32_t w) {
-    const uint32_t f = from_e4m3x2(w);
-    const __half2 r = __hmul2(*reinterpret_cast<const __half2 *>(&f), *reinterpret_cast<const __half2 *>(&by));
-    return *reinterpret_cast<const uint32_t *>(&r);
-  };
-  const uint4 lo = make_uint4(turn(x.x), turn(x.x >> 16), turn(x.y), turn(x.y >> 16));
-  const uint4 hi = make_uint4(turn(x.z), turn(x.z >> 16), turn(x.w), turn(x.w >> 16));
-  unsigned char *at = tile + (c >> 2) * (128 * 128) + row * 128;
-  const int p = (2 * c) & 7;
-  // (the lanes of the second column block write their upper half first: no bank conflicts)
-  const bool swap = D == 128 && (c & 4);
-  *reinterpret_cast<uint4 *>(at + (((p + (swap ? 1 : 0)) ^ (row & 7)) * 16)) = swap ? hi : lo;
-  *reinterpret_cast<uint4 *>(at + (((p + (swap ? 0 : 1)) ^ (row & 7)) * 16)) = swap ? lo : hi;
+// Two e4m3 numbers times `by` (float16 twice) as float16.
+__device__ __forceinline__ uint32_t turned(uint32_t w, uint32_t by) {
+  const uint32_t f = from_e4m3x2(w);
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2 *>(&f), *reinterpret_cast<const __half2 *>(&by));
+  return *reinterpret_cast<const uint32_t *>(&r);
 }
 
 template <typename T, int D, bool kPoll>
@@ -142,12 +129,10 @@ __global__ void __launch_bounds__(kCqThreads, 1)
   uint64_t *wgbar = pvdone + 2;      // [2] the warps of a warpgroup
   uint64_t *final = wgbar + 2;       // [2] every product S, every P V of the block done (commit)
   uint64_t *ufull = final + 2;       // [kCUnits] a unit is described
-  uint64_t *ufree = ufull + kCUnits; // [kCUnits] the 15 other warps are done with it
+  uint64_t *ufree = ufull + kCUnits; // [kCUnits] the 18 other warps are done with it
   uint64_t *sgone = ufree + kCUnits; // [4] S product k of the block issued, at k % 4
-  uint64_t *sbar = sgone + 4;        // [SR] scales of key tile k, at k % SR
-  uint64_t *rfull = sbar + SR;       // [RH] a half has landed
-  uint64_t *rfree = rfull + C::RH;   // [RH] and has been read (an arrival a turning warp)
-  uint64_t *qf = rfree + C::RH;      // [2] factors of unit n's rows, at n % 2 (an arrival a turning warp)
+  uint64_t *sbar = sgone + 4;        // [SR] scales of key tile k, at k % SR (K's and V's)
+  uint64_t *qf = sbar + SR;          // [2] factors of unit n's rows, at n % 2 (an arrival a turning warp)
   CUnit *units = reinterpret_cast<CUnit *>(smem + C::OFF_UNIT);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_TMEM);
   volatile int *abort = reinterpret_cast<volatile int *>(smem + C::OFF_MISC);
@@ -172,8 +157,9 @@ __global__ void __launch_bounds__(kCqThreads, 1)
       const bool of_four = bar == sread || bar == pfull || bar == pfull + 1 || bar == wgbar ||
                            bar == wgbar + 1 || (kTurnQ && bar == bar_q) ||
                            (bar >= kfull && bar < kfull + KS) || (bar >= vfull && bar < vfull + VS) ||
-                           bar >= rfree;
-      mbar_init(bar, of_four ? 4 : bar >= ufree && bar < ufree + kCUnits ? 15 : 1);
+                           bar >= qf;
+      const bool of_k_and_v = bar >= sbar && bar < sbar + SR;
+      mbar_init(bar, of_four ? 4 : of_k_and_v ? 2 : bar >= ufree && bar < ufree + kCUnits ? 18 : 1);
     }
     *abort = 0;
     fence_mbar_init();
@@ -415,114 +401,6 @@ __global__ void __launch_bounds__(kCqThreads, 1)
         if (nq > 0) mbar_wait_drain(qbar, (uint32_t)(nq - 1) & 1u);
       }
       __syncwarp();
-    } else if (warp == kCqCopyWarp) {
-      // ======================= halves of K and V, scales =======================
-      // A key tile: this lane's group of 16 rows is number lane % 8 of it; lanes 0 to 7
-      // have K's scales, 8 to 15 V's.
-      struct Tile {
-        int page, row, left;  // page of the group; its first row in the pages; keys from the tile's first on
-        int nq, g, key;       // unit, kv head, first key of the group
-        bool first;           // of its unit
-        float scale;
-      };
-      int uq = -1, n = 0;
-      CUnit f{};
-      bool ok = true;
-      // The next key tile of the block, its pages asked for; false after the last one.
-      auto next = [&](Tile &a) -> bool {
-        a.first = uq < 0 || n + 1 >= f.t_hi;
-        if (a.first) {
-          if (uq >= 0) unit_done(uq);
-          if (!(ok = unit(++uq, f)) || f.t_lo == f.t_hi) return false;
-          n = f.t_lo;
-        } else {
-          ++n;
-        }
-        a.nq = uq;
-        a.g = f.g;
-        a.left = f.L - n * kCN;
-        a.key = n * kCN + 16 * (lane & 7);
-        a.page = a.key < f.L ? __ldca(pa.page_table + (size_t)f.seq * pa.max_pages + (a.key >> pa.page_shift)) : 0;
-        return true;
-      };
-      // Its rows, once the pages are known; the scales asked for.
-      auto resolve = [&](Tile &a) {
-        if ((unsigned)a.page >= (unsigned)pa.num_pages) {
-          record_status(d_status, KVS_ERR_PAGE);
-          *const_cast<volatile int *>(&units[a.nq % kCUnits].bad) = 1;
-          a.page = 0;
-        }
-        a.row = ((a.page * Hkv + a.g) << pa.page_shift) + (a.key & ((1 << pa.page_shift) - 1));
-        a.scale = 0.f;
-        if (lane < 16 && 16 * (lane & 7) < a.left)
-          a.scale = __ldcg((lane < 8 ? cache.k_scales : cache.v_scales) + (a.row >> 4));
-      };
-      const int run = min(1 << pa.page_shift, C::HK);  // keys of a copy
-      int nr = 0, nk = 0;  // halves copied, tiles whose scales are there
-      auto wait = [&](uint64_t *bar, uint32_t phase) {
-        return ok = __all_sync(0xffffffffu, mbar_wait<kPoll>(bar, phase & 1u, abort)) != 0;
-      };
-      auto copy = [&](const Tile &a, const unsigned char *pages) {
-        for (int h = 0; h < 2; ++h) {
-          const int st = nr % C::RH;
-          if (nr >= C::RH && !wait(&rfree[st], (uint32_t)((nr - C::RH) / C::RH))) return;
-          const int live = min(C::HK, max(0, (a.left - h * C::HK + 15) & ~15));
-          if (lane == 0) mbar_arrive_expect_tx(&rfull[st], (uint32_t)(live * D));
-          const int at = (lane * run) & (C::HK - 1);  // first key of this lane's copy
-          const int row = __shfl_sync(0xffffffffu, a.row, h * 4 + at / 16);
-          if (lane * run < live)
-            bulk_g2s(smem + C::OFF_RAW + st * C::HALF + at * D, pages + (size_t)row * D,
-                     (uint32_t)(min(run, live - at) * D), &rfull[st]);
-          __syncwarp();
-          ++nr;
-        }
-      };
-      Tile p{}, a{}, c{};  // the tile before (V still to be copied), this one, the next one
-      bool have = next(a), behind = false;
-      if (have) resolve(a);
-      bool more = have && next(c);
-      while (have && ok) {
-        if (a.first && behind) {  // (in the order in which the halves are used)
-          copy(p, cache.v_pages);
-          if (!ok) break;
-          behind = false;
-        }
-        // the tile's scales: the largest of its blocks' and what each is of that
-        float most = a.scale;
-#pragma unroll
-        for (int o = 4; o >= 1; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-        most = fmaxf(most, 8.673617379884035e-19f);  // 2^-60
-        CqScales &sc = scales[nk % SR];
-        if (lane < 16) {
-          const __half2 by = __float2half2_rn(a.scale / most);
-          (lane < 8 ? sc.k : sc.v)[lane & 7] = *reinterpret_cast<const uint32_t *>(&by);
-          if (lane == 0) sc.score = most * sl2;
-          if (lane == 8) value_scale(most, sc.lg, sc.inv);
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sbar[nk % SR]);
-        ++nk;
-        copy(a, cache.k_pages);
-        if (!ok) break;
-        if (more) resolve(c);
-        if (behind) {
-          copy(p, cache.v_pages);
-          if (!ok) break;
-        }
-        behind = true;
-        p = a;
-        a = c;
-        have = more;
-        more = have && next(c);
-      }
-      if (ok && behind) copy(p, cache.v_pages);
-      if (lane == 0) {
-        if (!ok) give_up(abort, d_status, epoch);
-        // every copy issued lands before the block can exit
-        for (int j = (nr > C::RH ? nr - C::RH : 0); j < nr; ++j)
-          mbar_wait_drain(&rfull[j % C::RH], (uint32_t)(j / C::RH) & 1u);
-      }
-      __syncwarp();
     } else if (warp == kCqMmaWarp) {
       // ======================= products S ======================================
       // (order and waits: paged_chunk.cu)
@@ -627,103 +505,182 @@ __global__ void __launch_bounds__(kCqThreads, 1)
   } else {
     // ======================= K and V to float16 ================================
     fewer_registers<kCqRegsTurn>();
-    constexpr int PC = D / 16;               // 16-byte pieces of a row
-    constexpr int NV = C::HALF / 16 / 128;   // of a half, a thread
+    constexpr int NV = C::QUARTER / 16 / 128;  // 16-byte pieces of a quarter, a thread
+    static_assert(NV == D / 64, "pieces of a row pair, or of a row");
     const int t = threadIdx.x & 127;
+    const bool is_v = warp >= kCqTurnWarp + 4;
+    uint64_t *full = is_v ? vfull : kfull, *free = is_v ? vfree : kfree;
+    const unsigned char *pages = is_v ? cache.v_pages : cache.k_pages;
+    const float *page_scales = is_v ? cache.v_scales : cache.k_scales;
+    // This thread's pieces of a quarter.  D = 64: piece t % 4 of row t / 4.  D = 128: of
+    // rows r and r ^ 1, r = 2 (t / 8) + s with s = t / 4 % 2, pieces t % 4 + 4 s: eight
+    // lanes then read 128 bytes that share no bank, and write to different pieces.  All
+    // rows of a warp lie in group `half` of the quarter's two groups of 16.
+    const int sub = D == 128 ? (t >> 2) & 1 : 0, half = t >> 6;
+    const int row0 = D == 128 ? 2 * (t >> 3) + sub : t >> 2, c = (t & 3) + 4 * sub;
+    const int to0 = sub * C::BLK + row0 * 128 + (((2 * c) ^ row0) & 7) * 16;  // the lower half's place
+    unsigned char *raw = smem + C::OFF_RAW + (is_v ? C::RQ * C::QUARTER : 0) + row0 * D + c * 16;
+    constexpr int kPair = D;  // (row r ^ 1: this far on, or back)
+    const int pair = row0 & 1 ? -kPair : kPair;
     bool ok = true;
     auto wait = [&](uint64_t *bar, uint32_t phase) {
       return ok = __all_sync(0xffffffffu, mbar_wait<kPoll>(bar, phase & 1u, abort)) != 0;
     };
-    int nr = 0, nk = 0, nv = 0;  // halves read, K and V tiles written
-    // The ring's next two halves, with `left` keys from the tile's first on, as a tile.
-    auto turn = [&](unsigned char *tile, const uint32_t *by, int left, uint64_t *full) {
+    // A key tile: this lane's group of 16 rows is number lane % 8 of it.
+    struct Tile {
+      int row;    // first row of the group in the pages (before resolve(): its page)
+      int left;   // keys from the tile's first on
+      int unit;   // number of the unit, negative: ~number, the unit's first tile
+      float scale;
+    };
+    int uq = -1, n = 0;
+    CUnit f{};
+    // The next key tile of the block, its pages asked for; false after the last one.
+    auto next = [&](Tile &a) -> bool {
+      const bool first = uq < 0 || n + 1 >= f.t_hi;
+      if (first) {
+        if (uq >= 0) unit_done(uq);
+        if (!(ok = unit(++uq, f)) || f.t_lo == f.t_hi) return false;
+        n = f.t_lo;
+      } else {
+        ++n;
+      }
+      a.unit = first ? ~uq : uq;
+      a.left = f.L - n * kCN;
+      const int key = n * kCN + 16 * (lane & 7);
+      a.row = key < f.L ? __ldca(pa.page_table + (size_t)f.seq * pa.max_pages + (key >> pa.page_shift)) : 0;
+      return true;
+    };
+    // Its rows, once the pages are known (next() has not gone on); the scales asked for.
+    auto resolve = [&](Tile &a) {
+      const int key = n * kCN + 16 * (lane & 7);
+      if ((unsigned)a.row >= (unsigned)pa.num_pages) {
+        record_status(d_status, KVS_ERR_PAGE);
+        *const_cast<volatile int *>(&units[uq % kCUnits].bad) = 1;
+        a.row = 0;
+      }
+      a.row = ((a.row * Hkv + f.g) << pa.page_shift) + (key & ((1 << pa.page_shift) - 1));
+      a.scale = 16 * (lane & 7) < a.left ? __ldcg(page_scales + (a.row >> 4)) : 0.f;
+    };
+    // Quarter q of tile a into place s of the ring, rows behind the last key as zeros.
+    auto copy = [&](const Tile &a, int q, int s) {
+      const int row = __shfl_sync(0xffffffffu, a.row, 2 * q + half) + (row0 & 15);
+      const unsigned char *from = pages + (size_t)row * D + c * 16;
+      unsigned char *to = raw + s * C::QUARTER;
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        const int live = q * C::QK + (row0 ^ k) < a.left ? 16 : 0;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(to + k * pair)),
+                     "l"(from + k * pair), "r"(live)
+                     : "memory");
+      }
+    };
+    auto commit = [&]() { asm volatile("cp.async.commit_group;" ::: "memory"); };
+    Tile a{}, b2{};
+    bool have = next(a);
+    if (have) resolve(a);
+    for (int q = 0; q < 3; ++q) {
+      if (have) copy(a, q, q);
+      commit();
+    }
+    bool more = have && next(b2);
+    int done = 0, s = 0;  // tiles written; place of the next quarter in the ring
+    while (have && ok) {
+      // the tile's scale, the largest of its blocks', and what each is of that
+      float most = a.scale;
+#pragma unroll
+      for (int o = 4; o >= 1; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+      most = fmaxf(most, 8.673617379884035e-19f);  // 2^-60
+      float lg, inv;
+      value_scale(most, lg, inv);
+      const __half2 by_h = __float2half2_rn(a.scale * inv);
+      const uint32_t by = *reinterpret_cast<const uint32_t *>(&by_h);
+      if ((warp & 3) == 0 && lane == 0) {
+        CqScales &sc = scales[done % SR];
+        if (is_v) {
+          sc.lg = lg;
+          sc.inv = inv;
+        } else {
+          sc.score = most * sl2;
+        }
+        mbar_arrive(&sbar[done % SR]);
+      }
+      if (more) resolve(b2);
+      if (kTurnQ && is_v && a.unit < 0) {
+        // rows of q to float16 in place: a thread a row
+        const int nq = ~a.unit;
+        if (!wait(bar_qraw, (uint32_t)nq)) break;
+        const int tiles = units[nq % kCUnits].ntok > TT ? 2 : 1;
 #pragma unroll 1
-      for (int h = 0; h < 2; ++h) {
-        const int st = nr % C::RH;
-        if (!wait(&rfull[st], (uint32_t)(nr / C::RH))) return;
+        for (int x = 0; x < tiles; ++x) {
+          unsigned char *row = smem + C::OFF_Q + x * C::TILE + t * 128;
+          auto piece = [&](int j) {
+            return reinterpret_cast<uint4 *>(row + (j >> 3) * C::BLK + (((j & 7) ^ (t & 7)) * 16));
+          };
+          uint32_t top = 0;  // |elements| as integers: bfloat16 orders them
+#pragma unroll 2
+          for (int j = 0; j < D / 8; ++j) {
+            const uint4 w = *piece(j);
+            top = __vmaxu2(__vmaxu2(top, __vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu)),
+                           __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu));
+          }
+          // largest < 2^(ex + 1)
+          const int ex = max((int)(max(top & 0xffffu, top >> 16) >> 7) - 127, -60);
+          const float up = __uint_as_float((unsigned)(14 - ex + 127) << 23);
+#pragma unroll 2
+          for (int j = 0; j < D / 8; ++j) {
+            const uint4 w = *piece(j);
+            auto half2_of = [&](uint32_t e) {
+              return pack_pair<__half>(__uint_as_float(e << 16) * up, __uint_as_float(e & 0xffff0000u) * up);
+            };
+            *piece(j) = make_uint4(half2_of(w.x), half2_of(w.y), half2_of(w.z), half2_of(w.w));
+          }
+          qfac[(nq & 1) * 256 + x * 128 + t] = (unsigned char)(ex - 14 + 127);
+        }
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bar_q);
+          mbar_arrive(&qf[nq & 1]);
+        }
+      }
+      const int st = done & 1;
+      if (done >= 2 && !wait(&free[st], (uint32_t)(done / 2 - 1))) break;
+      unsigned char *tile = smem + (is_v ? C::OFF_V : C::OFF_K) + st * C::TILE + to0;
+#pragma unroll 1
+      for (int q = 0; q < 4; ++q) {
+        asm volatile("cp.async.wait_group 2;" ::: "memory");  // this thread's pieces of the quarter
         uint4 v[NV];
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-          v[i] = *reinterpret_cast<const uint4 *>(smem + C::OFF_RAW + st * C::HALF + (i * 128 + t) * 16);
+        for (int k = 0; k < NV; ++k) v[k] = *reinterpret_cast<const uint4 *>(raw + s * C::QUARTER + k * pair);
+        const uint32_t m2 = __shfl_sync(0xffffffffu, by, 2 * q + half);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-          const int row = h * C::HK + (i * 128 + t) / PC;
-          // (rows behind the last key hold anything)
-          put_piece<D>(tile, row, t % PC, row < left ? v[i] : make_uint4(0, 0, 0, 0), by[row >> 4]);
+        for (int k = 0; k < NV; ++k) {
+          // (row r ^ 1: the other half's place, a row on or back)
+          unsigned char *at = tile + q * C::QK * 128 + (k ? (row0 & 1 ? -128 : 128) : 0);
+          const int x = reinterpret_cast<uintptr_t>(at) & 16 ? -16 : 16;
+          *reinterpret_cast<uint4 *>(k ? at + x : at) =
+              make_uint4(turned(v[k].x, m2), turned(v[k].x >> 16, m2), turned(v[k].y, m2), turned(v[k].y >> 16, m2));
+          *reinterpret_cast<uint4 *>(k ? at : at + x) =
+              make_uint4(turned(v[k].z, m2), turned(v[k].z >> 16, m2), turned(v[k].w, m2), turned(v[k].w >> 16, m2));
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&rfree[st]);
-        ++nr;
+        // the quarter three further on takes its place
+        if (q == 0)
+          copy(a, 3, s);
+        else if (more)
+          copy(b2, q - 1, s);
+        commit();
+        s = s == 2 ? 0 : s + 1;
       }
       fence_proxy_async_shared();
       __syncwarp();
-      if (lane == 0) mbar_arrive(full);
-    };
-    int v_left = 0;  // of the tile whose V is to be written next
-    auto turn_v = [&]() {
-      const int st = nv % VS;
-      if (nv >= VS && !wait(&vfree[st], (uint32_t)((nv - VS) / VS))) return;
-      turn(smem + C::OFF_V + st * C::TILE, scales[nv % SR].v, v_left, &vfull[st]);
-      ++nv;
-    };
-    for (int nq = 0; ok; ++nq) {
-      CUnit f;
-      if (!(ok = unit(nq, f)) || f.t_lo == f.t_hi) break;
-      for (int n = f.t_lo; n < f.t_hi && ok; ++n) {
-        if (n == f.t_lo) {
-          if (nk > nv) turn_v();  // (before anything of this unit is waited for)
-          if (!ok) break;
-          if constexpr (kTurnQ) {
-            // rows of q to float16 in place: a thread a row
-            if (!wait(bar_qraw, (uint32_t)nq)) break;
-            for (int x = 0; x < (f.ntok > TT ? 2 : 1); ++x) {
-              unsigned char *row = smem + C::OFF_Q + x * C::TILE + t * 128;
-              auto piece = [&](int j) {
-                return reinterpret_cast<uint4 *>(row + (j >> 3) * C::BLK + (((j & 7) ^ (t & 7)) * 16));
-              };
-              uint32_t most = 0;  // |elements| as integers: bfloat16 orders them
-#pragma unroll 4
-              for (int j = 0; j < D / 8; ++j) {
-                const uint4 w = *piece(j);
-                most = __vmaxu2(__vmaxu2(most, __vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu)),
-                                __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu));
-              }
-              // largest < 2^(ex + 1)
-              const int ex = max((int)(max(most & 0xffffu, most >> 16) >> 7) - 127, -60);
-              const float up = __uint_as_float((unsigned)(14 - ex + 127) << 23);
-#pragma unroll 4
-              for (int j = 0; j < D / 8; ++j) {
-                const uint4 w = *piece(j);
-                auto half2_of = [&](uint32_t e) {
-                  return pack_pair<__half>(__uint_as_float(e << 16) * up, __uint_as_float(e & 0xffff0000u) * up);
-                };
-                *piece(j) = make_uint4(half2_of(w.x), half2_of(w.y), half2_of(w.z), half2_of(w.w));
-              }
-              qfac[(nq & 1) * 256 + x * 128 + t] = (unsigned char)(ex - 14 + 127);
-            }
-            fence_proxy_async_shared();
-            __syncwarp();
-            if (lane == 0) {
-              mbar_arrive(bar_q);
-              mbar_arrive(&qf[nq & 1]);
-            }
-          }
-        }
-        const int st = nk % KS;
-        if (nk >= KS && !wait(&kfree[st], (uint32_t)((nk - KS) / KS))) break;
-        if (!wait(&sbar[nk % SR], (uint32_t)(nk / SR))) break;
-        turn(smem + C::OFF_K + st * C::TILE, scales[nk % SR].k, f.L - n * kCN, &kfull[st]);
-        if (!ok) break;
-        if (nk > nv) {
-          turn_v();
-          if (!ok) break;
-        }
-        ++nk;
-        v_left = f.L - n * kCN;
-      }
-      if (ok) unit_done(nq);
+      if (lane == 0) mbar_arrive(&full[st]);
+      ++done;
+      a = b2;
+      have = more;
+      more = have && next(b2);
     }
-    if (ok && nk > nv) turn_v();
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
     if (!ok && lane == 0) give_up(abort, d_status, epoch);
     __syncwarp();
   }
@@ -745,6 +702,12 @@ int launch_chunk(const void *q, long long q_stride, const kvs_paged_cache_q8 &ca
     std::lock_guard<std::mutex> lk(mu);
     if (!configured[dev]) {
       for (auto kern : {paged_chunk_q8_kernel<T, D, false>, paged_chunk_q8_kernel<T, D, true>}) {
+        // (with fewer at launch the warpgroups' shares would never come together)
+        cudaFuncAttributes fa;
+        if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess || fa.numRegs != kCqRegs) {
+          cudaGetLastError();
+          return KVS_ERR_LAUNCH;
+        }
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) !=
             cudaSuccess) {
           cudaGetLastError();
