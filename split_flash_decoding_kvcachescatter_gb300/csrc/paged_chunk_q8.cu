@@ -17,7 +17,7 @@
 // Block (20 warps, one block an SM):
 //   warps 0-3, 4-7  softmax of tile A and of tile B
 //   warp 8, 9       issue S_x = Q_x K^T and O_x += P_x V, as in paged_chunk.cu
-//   warp 10         walks the units, describes each to the others, copies Q
+//   warp 10, 11     walks the units and describes each to the others; copies Q
 //   warps 12-15, 16-19  K and V: each thread copies the pieces that it will turn, 32
 //                   keys at a time and three of those ahead, and writes them as float16
 //                   in the layout that the tensor cores read; the tiles' scales; the
@@ -36,7 +36,7 @@ namespace kvs {
 
 namespace {
 
-constexpr int kCqMmaWarp = 8, kCqPvWarp = 9, kCqUnitWarp = 10, kCqTurnWarp = 12;
+constexpr int kCqMmaWarp = 8, kCqPvWarp = 9, kCqUnitWarp = 10, kCqQueryWarp = 11, kCqTurnWarp = 12;
 constexpr int kCqThreads = 20 * 32;
 // registers a thread: at launch, and by warpgroup; the shares' sum is the launch's
 constexpr int kCqRegs = 96;
@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(kCqThreads, 1)
   uint64_t *wgbar = pvdone + 2;      // [2] the warps of a warpgroup
   uint64_t *final = wgbar + 2;       // [2] every product S, every P V of the block done (commit)
   uint64_t *ufull = final + 2;       // [kCUnits] a unit is described
-  uint64_t *ufree = ufull + kCUnits; // [kCUnits] the 18 other warps are done with it
+  uint64_t *ufree = ufull + kCUnits; // [kCUnits] the 19 other warps are done with it
   uint64_t *sgone = ufree + kCUnits; // [4] S product k of the block issued, at k % 4
   uint64_t *sbar = sgone + 4;        // [SR] scales of key tile k, at k % SR (K's and V's)
   uint64_t *qf = sbar + SR;          // [2] factors of unit n's rows, at n % 2 (an arrival a turning warp)
@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(kCqThreads, 1)
                            (bar >= kfull && bar < kfull + KS) || (bar >= vfull && bar < vfull + VS) ||
                            bar >= qf;
       const bool of_k_and_v = bar >= sbar && bar < sbar + SR;
-      mbar_init(bar, of_four ? 4 : of_k_and_v ? 2 : bar >= ufree && bar < ufree + kCUnits ? 18 : 1);
+      mbar_init(bar, of_four ? 4 : of_k_and_v ? 2 : bar >= ufree && bar < ufree + kCUnits ? 19 : 1);
     }
     *abort = 0;
     fence_mbar_init();
@@ -346,7 +346,7 @@ __global__ void __launch_bounds__(kCqThreads, 1)
   } else if (warp < kCqTurnWarp) {
     fewer_registers<kCqRegsIssue>();
     if (warp == kCqUnitWarp) {
-      // ======================= units, Q =======================================
+      // ======================= units ===========================================
       int nq = 0;  // units described
       bool ok = true;
       const Cuts cut = equal_cuts(warp_line_total(pa, ln, lane), ln, gridDim.x);
@@ -354,7 +354,9 @@ __global__ void __launch_bounds__(kCqThreads, 1)
       const long long x0 = more ? cut.start(b) : 0, x1 = more ? cut.start(b + 1) : 0;
       Unit u{pa.M, 0, 0, 0};
       if (more) u = warp_unit_at(pa, ln, x0, lane);
-      // Describes a unit, once the one before in the same place is done with.
+      // Describes a unit, once the one before in the same place is done with.  (Nothing
+      // else is waited for: the warps that turn K and V look two tiles ahead, which may
+      // be two units.)
       auto describe = [&](int n, const CUnit &f) {
         if (n >= kCUnits &&
             !__all_sync(0xffffffffu, mbar_wait<kPoll>(&ufree[n % kCUnits], (uint32_t)(n / kCUnits - 1) & 1u, abort)))
@@ -366,7 +368,6 @@ __global__ void __launch_bounds__(kCqThreads, 1)
         __syncwarp();
         return true;
       };
-      uint64_t *qbar = kTurnQ ? bar_qraw : bar_q;
       while (more && ok) {
         const UnitInfo f = unit_info(pa, u, ln, x0, x1);
         if (f.t_lo < f.t_hi) {
@@ -378,23 +379,33 @@ __global__ void __launch_bounds__(kCqThreads, 1)
               d.b2[x] = nt > 0 ? cut.at(f.k0 + (long long)(nt - 1) * kCN) : d.b1;
             }
           }
-          if (!(ok = describe(nq, d))) break;
-          if (nq > 0 && !(ok = __all_sync(0xffffffffu, mbar_wait<kPoll>(qfree, (uint32_t)(nq - 1) & 1u, abort))))
-            break;
-          if (lane == 0) {
-            const int tiles = f.ntok > TT ? 2 : 1;
-            mbar_arrive_expect_tx(qbar, (uint32_t)(tiles * C::NB * TT * G * 128));
-            for (int x = 0; x < tiles; ++x)
-              for (int cb = 0; cb < C::NB; ++cb)
-                tma_q(smem + C::OFF_Q + x * C::TILE + cb * C::BLK, &qmap, u.g * G,
-                      f.s.row0 + f.tok0 + x * TT, cb, qbar);
-          }
-          ++nq;
-          __syncwarp();
+          if (!(ok = describe(nq++, d))) break;
         }
         more = next_unit(pa, u, f, ln) && u.base < x1;
       }
       if (ok) ok = describe(nq, CUnit{});
+      if (!ok && lane == 0) give_up(abort, d_status, epoch);
+      __syncwarp();
+    } else if (warp == kCqQueryWarp) {
+      // ======================= Q ===============================================
+      uint64_t *qbar = kTurnQ ? bar_qraw : bar_q;
+      int nq = 0;  // units whose rows are copied
+      bool ok = true;
+      for (;; ++nq) {
+        CUnit f;
+        if (!(ok = unit(nq, f)) || f.t_lo == f.t_hi) break;
+        if (nq > 0 && !(ok = __all_sync(0xffffffffu, mbar_wait<kPoll>(qfree, (uint32_t)(nq - 1) & 1u, abort))))
+          break;
+        if (lane == 0) {
+          const int tiles = f.ntok > TT ? 2 : 1;
+          mbar_arrive_expect_tx(qbar, (uint32_t)(tiles * C::NB * TT * G * 128));
+          for (int x = 0; x < tiles; ++x)
+            for (int cb = 0; cb < C::NB; ++cb)
+              tma_q(smem + C::OFF_Q + x * C::TILE + cb * C::BLK, &qmap, f.g * G,
+                    f.row0 + f.tok0 + x * TT, cb, qbar);
+        }
+        unit_done(nq);
+      }
       if (lane == 0) {
         if (!ok) give_up(abort, d_status, epoch);
         // every copy issued lands before the block can exit
@@ -533,18 +544,24 @@ __global__ void __launch_bounds__(kCqThreads, 1)
       int unit;   // number of the unit, negative: ~number, the unit's first tile
       float scale;
     };
-    int uq = -1, n = 0;
-    CUnit f{};
+    // The cursor: tile n of unit uq, which ends at tile t_hi (the rest is read where it is
+    // needed: these threads have few registers).
+    int uq = -1, n = 0, t_hi = 0;
     // The next key tile of the block, its pages asked for; false after the last one.
     auto next = [&](Tile &a) -> bool {
-      const bool first = uq < 0 || n + 1 >= f.t_hi;
+      const bool first = uq < 0 || n + 1 >= t_hi;
       if (first) {
         if (uq >= 0) unit_done(uq);
-        if (!(ok = unit(++uq, f)) || f.t_lo == f.t_hi) return false;
-        n = f.t_lo;
+        ++uq;
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait<kPoll>(&ufull[uq % kCUnits], (uint32_t)(uq / kCUnits) & 1u, abort))))
+          return false;
+        n = units[uq % kCUnits].t_lo;
+        t_hi = units[uq % kCUnits].t_hi;
+        if (n == t_hi) return false;
       } else {
         ++n;
       }
+      const CUnit &f = units[uq % kCUnits];
       a.unit = first ? ~uq : uq;
       a.left = f.L - n * kCN;
       const int key = n * kCN + 16 * (lane & 7);
@@ -559,7 +576,7 @@ __global__ void __launch_bounds__(kCqThreads, 1)
         *const_cast<volatile int *>(&units[uq % kCUnits].bad) = 1;
         a.row = 0;
       }
-      a.row = ((a.row * Hkv + f.g) << pa.page_shift) + (key & ((1 << pa.page_shift) - 1));
+      a.row = ((a.row * Hkv + units[uq % kCUnits].g) << pa.page_shift) + (key & ((1 << pa.page_shift) - 1));
       a.scale = 16 * (lane & 7) < a.left ? __ldcg(page_scales + (a.row >> 4)) : 0.f;
     };
     // Quarter q of tile a into place s of the ring, rows behind the last key as zeros.
@@ -567,16 +584,23 @@ __global__ void __launch_bounds__(kCqThreads, 1)
       const int row = __shfl_sync(0xffffffffu, a.row, 2 * q + half) + (row0 & 15);
       const unsigned char *from = pages + (size_t)row * D + c * 16;
       unsigned char *to = raw + s * C::QUARTER;
+      if (a.left >= kCN) {
 #pragma unroll
-      for (int k = 0; k < NV; ++k) {
-        const int live = q * C::QK + (row0 ^ k) < a.left ? 16 : 0;
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(to + k * pair)),
-                     "l"(from + k * pair), "r"(live)
-                     : "memory");
+        for (int k = 0; k < NV; ++k)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(to + k * pair)), "l"(from + k * pair)
+                       : "memory");
+      } else {
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+          const int live = q * C::QK + (row0 ^ k) < a.left ? 16 : 0;
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(to + k * pair)),
+                       "l"(from + k * pair), "r"(live)
+                       : "memory");
+        }
       }
     };
     auto commit = [&]() { asm volatile("cp.async.commit_group;" ::: "memory"); };
-    Tile a{}, b2{};
+    Tile a{}, b2{}, b3{};  // a tile under way, the next one (resolved a tile ahead) and the one after (asked for)
     bool have = next(a);
     if (have) resolve(a);
     for (int q = 0; q < 3; ++q) {
@@ -591,21 +615,21 @@ __global__ void __launch_bounds__(kCqThreads, 1)
 #pragma unroll
       for (int o = 4; o >= 1; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
       most = fmaxf(most, 8.673617379884035e-19f);  // 2^-60
-      float lg, inv;
-      value_scale(most, lg, inv);
+      float inv = __uint_as_float((254u << 23) - __float_as_uint(most));
+      if (__float_as_uint(most) & 0x7fffffu) inv = 1.f / most;  // (no power of two)
       const __half2 by_h = __float2half2_rn(a.scale * inv);
       const uint32_t by = *reinterpret_cast<const uint32_t *>(&by_h);
       if ((warp & 3) == 0 && lane == 0) {
         CqScales &sc = scales[done % SR];
-        if (is_v) {
-          sc.lg = lg;
-          sc.inv = inv;
-        } else {
+        if (is_v)
+          value_scale(most, sc.lg, sc.inv);
+        else
           sc.score = most * sl2;
-        }
         mbar_arrive(&sbar[done % SR]);
       }
       if (more) resolve(b2);
+      const bool third = more && next(b3);
+      if (!ok) break;
       if (kTurnQ && is_v && a.unit < 0) {
         // rows of q to float16 in place: a thread a row
         const int nq = ~a.unit;
@@ -653,6 +677,12 @@ __global__ void __launch_bounds__(kCqThreads, 1)
         uint4 v[NV];
 #pragma unroll
         for (int k = 0; k < NV; ++k) v[k] = *reinterpret_cast<const uint4 *>(raw + s * C::QUARTER + k * pair);
+        // the quarter three further on takes its place
+        if (q == 0)
+          copy(a, 3, s);
+        else if (more)
+          copy(b2, q - 1, s);
+        commit();
         const uint32_t m2 = __shfl_sync(0xffffffffu, by, 2 * q + half);
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
@@ -664,12 +694,6 @@ __global__ void __launch_bounds__(kCqThreads, 1)
           *reinterpret_cast<uint4 *>(k ? at : at + x) =
               make_uint4(turned(v[k].z, m2), turned(v[k].z >> 16, m2), turned(v[k].w, m2), turned(v[k].w >> 16, m2));
         }
-        // the quarter three further on takes its place
-        if (q == 0)
-          copy(a, 3, s);
-        else if (more)
-          copy(b2, q - 1, s);
-        commit();
         s = s == 2 ? 0 : s + 1;
       }
       fence_proxy_async_shared();
@@ -677,8 +701,9 @@ __global__ void __launch_bounds__(kCqThreads, 1)
       if (lane == 0) mbar_arrive(&full[st]);
       ++done;
       a = b2;
+      b2 = b3;
       have = more;
-      more = have && next(b2);
+      more = third;
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     if (!ok && lane == 0) give_up(abort, d_status, epoch);
