@@ -23,6 +23,7 @@
 // Bound: bytes (a row is read once).
 
 #include <mutex>
+#include <type_traits>
 
 #include "kvs_cluster.cuh"
 #include "kvs_exp2_table.cuh"
@@ -33,7 +34,7 @@ namespace kvs {
 namespace {
 
 constexpr int kSThreads = 512;
-constexpr int kSBins = 2048;
+constexpr int kSBins = 2048;  // of a digit of 11 bits
 constexpr int kSMaxDevices = 64;
 typedef unsigned long long u64;
 
@@ -49,18 +50,42 @@ struct SampleArgs {
   float *token_probs;
 };
 
-// An integer that orders logits: larger for larger ones, equal for equal ones; 0 for
-// NaN and -inf, which are never chosen.
-__device__ __forceinline__ unsigned key_of(float x) {
-  const unsigned u = __float_as_uint(x + 0.f);  // (-0 equals 0)
-  if (!(x > neg_inf_f())) return 0u;
-  return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
-}
-__device__ __forceinline__ float logit_of(unsigned key) {
-  return __uint_as_float(key ^ ((key >> 31) ? 0x80000000u : 0xffffffffu));
-}
+// An integer of the type's size that orders its numbers: larger for larger ones, equal
+// for equal ones; 0 for NaN and -inf, which are never chosen.
+template <typename T>
+struct Keys {  // the 16-bit types
+  using Key = uint16_t;
+  static constexpr int kPasses = 2;
+  static constexpr bool kHalf = std::is_same<T, __half>::value;
+  static __host__ __device__ constexpr int shift(int pass) { return pass == 0 ? 5 : 0; }
+  static __device__ __forceinline__ Key of(T x) {
+    const unsigned u = *reinterpret_cast<const uint16_t *>(&x), inf = kHalf ? 0x7c00u : 0x7f80u;
+    if ((u & 0x7fffu) > inf || u == (inf | 0x8000u)) return 0;
+    if ((u & 0x7fffu) == 0u) return 0x8000;  // (-0 equals 0)
+    return (Key)(u ^ ((u & 0x8000u) ? 0xffffu : 0x8000u));
+  }
+  static __device__ __forceinline__ float logit(unsigned key) {
+    const uint16_t u = (uint16_t)(key ^ ((key & 0x8000u) ? 0x8000u : 0xffffu));
+    return to_f32(*reinterpret_cast<const T *>(&u));
+  }
+};
+template <>
+struct Keys<float> {
+  using Key = uint32_t;
+  static constexpr int kPasses = 3;
+  static __host__ __device__ constexpr int shift(int pass) { return pass == 0 ? 21 : pass == 1 ? 10 : 0; }
+  static __device__ __forceinline__ Key of(float x) {
+    const unsigned u = __float_as_uint(x + 0.f);  // (-0 equals 0)
+    if (!(x > neg_inf_f())) return 0u;
+    return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
+  }
+  static __device__ __forceinline__ float logit(unsigned key) {
+    return __uint_as_float(key ^ ((key >> 31) ? 0x80000000u : 0xffffffffu));
+  }
+};
 
 // Weights of a row: largest logit and log2(e) / T in two parts.
+template <typename T>
 struct Weigher {
   float top, ch, cl;
   const u64 *table;  // 2^(i / 256) 2^44
@@ -71,7 +96,7 @@ struct Weigher {
   // are below 2^-17, so float arithmetic is off by 2^-41 there.
   __device__ __forceinline__ u64 operator()(unsigned key) const {
     if (key == 0u) return 0ull;
-    const float x = logit_of(key);
+    const float x = Keys<T>::logit(key);
     if (!(top < __uint_as_float(0x7f800000u))) return x == top ? 1ull << 44 : 0ull;
     const float d = fmaxf(__fsub_rn(x, top), -3.4e38f);
     const float b = __fsub_rn(d, x);
@@ -122,149 +147,145 @@ __device__ __forceinline__ u64 share_of(float f, u64 x, bool &left) {
   return (lo >> s) | (hi << (64 - s));
 }
 
-struct SampleShared {
-  unsigned count[kSBins];   // of this block's tokens
-  unsigned tcount[kSBins];  // of the row's
-  u64 mass[kSBins];
-  u64 tmass[kSBins];
+struct alignas(16) SampleShared {  // (the keys lie behind it)
+  unsigned low[kSBins], high[kSBins];  // this block's amounts (tokens or weight), a digit a bin
+  u64 amount[kSBins];                  // the row's
   u64 table[256];
-  unsigned top[16];         // of the cluster's blocks
+  unsigned top[16];  // of the cluster's blocks
   unsigned ties[16];
   u64 above[16];
-  u64 wmass[32];
+  u64 wsum[32];
   unsigned wcount[32];
-  int bin;
-  unsigned before_count;
-  u64 before_mass;
-  int cut;
+  int bin, cut;
+  u64 before, inside;
 };
+static_assert(sizeof(SampleShared) % 16 == 0 && kSBins % 4 == 0, "vectors of keys and of bins");
 
-// The bin, from the top, in which a running number passes `need`, over the row's
-// counts (kCount) or weights; leaves it in s.bin with what lies above it (s.bin = -1:
-// all of them do not reach it).  By the whole block.
-template <bool kCount>
-__device__ __forceinline__ void find_bin(SampleShared &s, u64 need) {
-  constexpr int kPer = kSBins / kSThreads;
-  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-  unsigned c[kPer], csum = 0u;
-  u64 m[kPer], msum = 0ull;
-  // thread t takes bins from the top: kSBins - 1 - (kPer t + j)
+// The row's amounts from the cluster's blocks': (bin, block) pairs, four a thread, the
+// pairs of a bin side by side: four loads in flight, sums over the threads of a bin,
+// and each pair's thread stores the bin's sum to the pair's block.
+__device__ __forceinline__ void sum_bins(SampleShared &s, int rank, int cs) {
+  const int log = __ffs(cs) - 1, per = kSBins >> log;
+  u64 v[4];
 #pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    c[j] = s.tcount[kSBins - 1 - (kPer * t + j)];
-    m[j] = s.tmass[kSBins - 1 - (kPer * t + j)];
-    csum += c[j];
-    msum += m[j];
+  for (int u = 0; u < 4; ++u) {
+    const int pair = 4 * (int)threadIdx.x + u, bin = rank * per + (pair >> log), r = pair & (cs - 1);
+    v[u] = (u64)(unsigned)ld_dsmem_s32(dsmem_addr(&s.high[bin], r)) << 32;
+    v[u] += (unsigned)ld_dsmem_s32(dsmem_addr(&s.low[bin], r));
   }
-  unsigned ci = csum;
-  u64 mi = msum;
+  if (cs >= 4) {
+    u64 t = v[0] + v[1] + v[2] + v[3];
+    for (int o = cs / 8; o >= 1; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+    v[0] = v[1] = v[2] = v[3] = t;
+  } else if (cs == 2) {
+    v[0] = v[1] = v[0] + v[1];
+    v[2] = v[3] = v[2] + v[3];
+  }
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const int pair = 4 * (int)threadIdx.x + u, bin = rank * per + (pair >> log), r = pair & (cs - 1);
+    st_dsmem_u64(dsmem_addr(&s.amount[bin], r), v[u]);
+  }
+}
+
+// The bin, from the top, in which the running amount reaches need(all of it); leaves it
+// in s.bin with what lies above it and in it (s.bin = -1: all of them do not reach it),
+// and returns the whole amount.  By the whole block.
+template <typename Need>
+__device__ __forceinline__ u64 find_bin(SampleShared &s, Need need) {
+  constexpr int kPer = kSBins / kSThreads;
+  static_assert(kPer == 4, "two 16-byte loads");
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  // thread t takes bins from the top: kSBins - 1 - (4 t + j)
+  const ulonglong2 hi = *reinterpret_cast<const ulonglong2 *>(&s.amount[kSBins - 2 - 4 * t]);
+  const ulonglong2 lo = *reinterpret_cast<const ulonglong2 *>(&s.amount[kSBins - 4 - 4 * t]);
+  const u64 m[4] = {hi.y, hi.x, lo.y, lo.x};
+  const u64 mine = m[0] + m[1] + m[2] + m[3];
+  u64 inc = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const unsigned cv = __shfl_up_sync(0xffffffffu, ci, o);
-    const u64 mv = __shfl_up_sync(0xffffffffu, mi, o);
-    if (lane >= o) {
-      ci += cv;
-      mi += mv;
-    }
+    const u64 v = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += v;
   }
-  if (lane == 31) {
-    s.wcount[warp] = ci;
-    s.wmass[warp] = mi;
-  }
+  if (lane == 31) s.wsum[warp] = inc;
   if (t == 0) s.bin = -1;
   __syncthreads();
-  unsigned cb = ci - csum;
-  u64 mb = mi - msum;
-  for (int w = 0; w < warp; ++w) {
-    cb += s.wcount[w];
-    mb += s.wmass[w];
+  u64 before = inc - mine, all = 0ull;
+#pragma unroll
+  for (int w = 0; w < kSThreads / 32; ++w) {
+    const u64 x = s.wsum[w];
+    if (w < warp) before += x;
+    all += x;
   }
+  const u64 n = need(all);
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
-    const u64 lo = kCount ? (u64)cb : mb, hi = lo + (kCount ? (u64)c[j] : m[j]);
-    if (lo < need && need <= hi) {  // (one bin at most)
+    if (before < n && n <= before + m[j]) {  // (one bin at most)
       s.bin = kSBins - 1 - (kPer * t + j);
-      s.before_count = cb;
-      s.before_mass = mb;
+      s.before = before;
+      s.inside = m[j];
     }
-    cb += c[j];
-    mb += m[j];
+    before += m[j];
   }
   __syncthreads();
+  return all;
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kSThreads) sample_kernel(SampleArgs a) {
-  constexpr int VE = 16 / sizeof(T);
+__global__ void __launch_bounds__(kSThreads, 2) sample_kernel(SampleArgs a) {
+  using Key = typename Keys<T>::Key;
+  constexpr int VE = 16 / sizeof(T);  // logits, and keys, of a vector
   extern __shared__ __align__(16) unsigned char raw[];
   SampleShared &s = *reinterpret_cast<SampleShared *>(raw);
-  unsigned *keys = reinterpret_cast<unsigned *>(raw + sizeof(SampleShared));
+  Key *keys = reinterpret_cast<Key *>(raw + sizeof(SampleShared));  // [slice], 0 behind the last id
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const int cs = (int)gridDim.x, rank = (int)cluster_rank();
   const int lo = min(a.V, rank * a.slice), hi = min(a.V, lo + a.slice), n = hi - lo;
+  const int vecs = a.slice / VE;  // (slices are multiples of 32)
   if (t < 256) s.table[t] = kExp2Table[t];
   grid_dependency_wait();
   allow_dependent_launch();
-  // a histogram of digit `shift` of the keys whose bits from `from` up are `prefix`
-  auto histogram = [&](const Weigher &weigh, int shift, int from, unsigned prefix, bool with_mass) {
-    for (int j = t; j < kSBins; j += kSThreads) {
-      s.count[j] = 0u;
-      s.mass[j] = 0ull;
+  auto clear = [&]() {
+    for (int j = 4 * t; j < kSBins; j += 4 * kSThreads) {
+      *reinterpret_cast<uint4 *>(&s.low[j]) = make_uint4(0u, 0u, 0u, 0u);
+      *reinterpret_cast<uint4 *>(&s.high[j]) = make_uint4(0u, 0u, 0u, 0u);
     }
-    __syncthreads();
-    for (int j = t; j < n; j += kSThreads) {
-      const unsigned k = keys[j];
-      if (k == 0u || (from < 32 && (k >> from) != prefix)) continue;
-      const unsigned bin = (k >> shift) & (kSBins - 1);
-      atomicAdd(&s.count[bin], 1u);
-      if (with_mass) atomicAdd(&s.mass[bin], weigh(k));
-    }
-    cluster_sync_all();  // every block's histogram is there
-    const int per = kSBins / cs;
-    for (int j = t; j < per; j += kSThreads) {
-      const int bin = rank * per + j;
-      unsigned c = 0u;
-      u64 m = 0ull;
-      for (int r = 0; r < cs; ++r) {
-        c += (unsigned)ld_dsmem_s32(dsmem_addr(&s.count[bin], r));
-        m += ld_dsmem_u64(dsmem_addr(&s.mass[bin], r));
-      }
-      for (int r = 0; r < cs; ++r) {
-        st_dsmem_s32(dsmem_addr(&s.tcount[bin], r), (int)c);
-        st_dsmem_u64(dsmem_addr(&s.tmass[bin], r), m);
-      }
-    }
-    cluster_sync_all();  // the row's histogram is in every block
   };
-  constexpr int kShift[3] = {21, 10, 0};
+  clear();
   for (int m = blockIdx.y; m < a.M; m += gridDim.y) {  // same trip count in a cluster
     const T *x = static_cast<const T *>(a.logits) + (long long)m * a.logits_stride + lo;
     const float temp = a.r.temperature ? __ldca(a.r.temperature + m) : 1.f;
     const bool greedy = !(temp >= 1.1754943508222875e-38f);
-    int k = a.r.top_k ? __ldca(a.r.top_k + m) : 0;
-    if (greedy) k = 1;
+    const int k = greedy ? 1 : a.r.top_k ? __ldca(a.r.top_k + m) : 0;
     const float p = !greedy && a.r.top_p ? __ldca(a.r.top_p + m) : 1.f;
     const float least = !greedy && a.r.min_p ? __ldca(a.r.min_p + m) : 0.f;
     const float u = __ldca(a.uniforms + m);
     // ---- the slice's logits ----
     unsigned most = 0u;
-    const int mis = (int)((reinterpret_cast<uintptr_t>(x) & 15u) / sizeof(T));
-    const int va = min(n, mis ? VE - mis : 0), vb = va + (n - va) / VE * VE;
-    auto put = [&](int j, float f) {
-      const unsigned key = key_of(f);
-      keys[j] = key;
-      most = max(most, key);
-    };
-    for (int j = t; j < va; j += kSThreads) put(j, to_f32(x[j]));
-    for (int j = vb + t; j < n; j += kSThreads) put(j, to_f32(x[j]));
-    for (int j = va + VE * t; j < vb; j += VE * kSThreads) {
-      const Vec<T, VE> v = vec_load<T, VE>(x + j);
+    if ((reinterpret_cast<uintptr_t>(x) & 15u) == 0u) {
+      for (int j = t; j < vecs; j += kSThreads) {
+        Vec<Key, VE> kv;
+        if (j * VE + VE <= n) {
+          const Vec<T, VE> v = vec_load<T, VE>(x + j * VE);
 #pragma unroll
-      for (int e = 0; e < VE; ++e) put(j + e, to_f32(v.e[e]));
+          for (int e = 0; e < VE; ++e) kv.e[e] = Keys<T>::of(v.e[e]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < VE; ++e) kv.e[e] = j * VE + e < n ? Keys<T>::of(x[j * VE + e]) : (Key)0;
+        }
+#pragma unroll
+        for (int e = 0; e < VE; ++e) most = max(most, (unsigned)kv.e[e]);
+        *reinterpret_cast<Vec<Key, VE> *>(keys + j * VE) = kv;
+      }
+    } else {
+      for (int j = t; j < a.slice; j += kSThreads) {
+        const Key key = j < n ? Keys<T>::of(x[j]) : (Key)0;
+        keys[j] = key;
+        most = max(most, (unsigned)key);
+      }
     }
     most = __reduce_max_sync(0xffffffffu, most);
     if (lane == 0) s.wcount[warp] = most;
-    __syncthreads();
     cluster_sync_all();  // every block runs, and is done with the row before
     if (t < cs) {
       unsigned w = 0u;
@@ -281,64 +302,94 @@ __global__ void __launch_bounds__(kSThreads) sample_kernel(SampleArgs a) {
       }
       if (a.probs)
         for (int j = t; j < n; j += kSThreads) a.probs[(long long)m * a.probs_stride + lo + j] = 0.f;
+      __syncthreads();  // the keys may be replaced
       continue;
     }
-    Weigher weigh{logit_of(top), 0.f, 0.f, s.table};
+    Weigher<T> weigh{Keys<T>::logit(top), 0.f, 0.f, s.table};
     {
       const double c = 1.4426950408889634074 / (double)(greedy ? 1.f : temp);
       weigh.ch = (float)c;
       weigh.cl = (float)(c - (double)weigh.ch);
     }
     // ---- the last logit that is kept, and how many tokens that equal it ----
+    // A pass over one digit of the keys from `least_key` up whose higher digits are
+    // `prefix`: amounts by bin, summed over the cluster.
+    auto pass_over = [&](bool weights, int pass, unsigned prefix, unsigned least_key) {
+      const int shift = Keys<T>::shift(pass), above = pass == 0 ? 31 : Keys<T>::shift(pass - 1);
+      auto bin_of = [&](unsigned key) {  // negative: not of this pass
+        if (key < least_key || (pass > 0 && (key >> above) != prefix)) return -1;
+        return (int)((key >> shift) & ((pass == 0 ? kSBins : 1u << (above - shift)) - 1u));
+      };
+      if (weights) {  // (key by key: the code of a weight is long)
+#pragma unroll 2
+        for (int j = t; j < a.slice; j += kSThreads) {
+          const unsigned key = keys[j];
+          const int bin = bin_of(key);
+          if (bin < 0) continue;
+          const u64 w = weigh(key);
+          const unsigned wl = (unsigned)w, old = atomicAdd(&s.low[bin], wl);
+          const unsigned carry = (unsigned)(w >> 32) + (old + wl < old ? 1u : 0u);
+          if (carry) atomicAdd(&s.high[bin], carry);
+        }
+      } else {
+        for (int j = t; j < vecs; j += kSThreads) {
+          const Vec<Key, VE> v = *reinterpret_cast<const Vec<Key, VE> *>(keys + j * VE);
+#pragma unroll
+          for (int e = 0; e < VE; ++e) {
+            const int bin = bin_of(v.e[e]);
+            if (bin >= 0) atomicAdd(&s.low[bin], 1u);
+          }
+        }
+      }
+      cluster_sync_all();  // every block's amounts are there
+      sum_bins(s, rank, cs);
+      cluster_sync_all();  // the row's are in every block
+      clear();
+    };
     unsigned thr = 0u, kept = 0u;  // (nothing equals key 0)
     const bool by_k = k > 0 && k < a.V, by_p = p < 1.f;
-    u64 sum = 0ull;  // weight of what top-k keeps
+    u64 cut_off = 0ull;  // weight of the tokens that equal thr and are not kept
     if (by_k && k == 1) {
       thr = top;
       kept = 1u;
-      sum = 1ull << 44;
     } else if (by_k) {
-      unsigned prefix = 0u;
-      u64 need = (u64)k;
-      int from = 32;
-      for (int pass = 0; pass < 3; ++pass) {
-        histogram(weigh, kShift[pass], from, prefix, by_p);
-        find_bin<true>(s, need);
-        if (s.bin < 0) break;  // fewer tokens than k
-        need -= s.before_count;
-        sum += s.before_mass;
-        from = kShift[pass];
-        prefix = pass == 0 ? (unsigned)s.bin : prefix << (kShift[pass - 1] - kShift[pass]) | (unsigned)s.bin;
+      unsigned prefix = 0u, need = (unsigned)k;
+      bool reached = true;
+      u64 ties = 0ull;
+      for (int pass = 0; pass < Keys<T>::kPasses && reached; ++pass) {
+        pass_over(false, pass, prefix, 1u);
+        find_bin(s, [&](u64) { return (u64)need; });
+        reached = s.bin >= 0;  // (else fewer tokens than k)
+        if (reached) {
+          need -= (unsigned)s.before;
+          ties = s.inside;
+          prefix = pass == 0 ? (unsigned)s.bin
+                             : prefix << (Keys<T>::shift(pass - 1) - Keys<T>::shift(pass)) | (unsigned)s.bin;
+        }
         __syncthreads();
       }
-      if (from == 0) {
+      if (reached) {
         thr = prefix;
-        kept = (unsigned)need;
-        sum += need * weigh(thr);
+        kept = need;
+        cut_off = (ties - need) * weigh(thr);
       }
     }
     if (by_p && !(by_k && k == 1)) {
       unsigned prefix = 0u;
-      int from = 32;
       u64 need = 0ull;
-      for (int pass = 0; pass < 3; ++pass) {
-        histogram(weigh, kShift[pass], from, prefix, true);
-        if (pass == 0) {
-          if (thr == 0u) {  // all of the row
-            sum = 0ull;
-            for (int j = lane; j < kSBins; j += 32) sum += s.tmass[j];
-#pragma unroll
-            for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      for (int pass = 0; pass < Keys<T>::kPasses; ++pass) {
+        pass_over(true, pass, prefix, max(thr, 1u));
+        find_bin(s, [&](u64 all) {
+          if (pass == 0) {  // p times the weight of what top-k keeps, rounded up; one token at the least
+            bool left = false;
+            need = p > 0.f ? share_of(p, all - cut_off, left) : 0ull;
+            need = max(need + (left ? 1ull : 0ull), 1ull);
           }
-          bool left;
-          need = p > 0.f ? share_of(p, sum, left) : 0ull;
-          if (p > 0.f && left) ++need;
-          if (need == 0ull) need = 1ull;
-        }
-        find_bin<false>(s, need);
-        need -= s.before_mass;
-        from = kShift[pass];
-        prefix = pass == 0 ? (unsigned)s.bin : prefix << (kShift[pass - 1] - kShift[pass]) | (unsigned)s.bin;
+          return need;
+        });
+        need -= s.before;
+        prefix = pass == 0 ? (unsigned)s.bin
+                           : prefix << (Keys<T>::shift(pass - 1) - Keys<T>::shift(pass)) | (unsigned)s.bin;
         __syncthreads();
       }
       thr = prefix;
@@ -358,6 +409,7 @@ __global__ void __launch_bounds__(kSThreads) sample_kernel(SampleArgs a) {
     const int j0 = min(n, t * run), j1 = min(n, j0 + run);
     u64 above = 0ull;
     unsigned ties = 0u;
+#pragma unroll 2
     for (int j = j0; j < j1; ++j) {
       const unsigned key = keys[j];
       if (key > thr) {
@@ -379,7 +431,7 @@ __global__ void __launch_bounds__(kSThreads) sample_kernel(SampleArgs a) {
       }
     }
     if (lane == 31) {
-      s.wmass[warp] = ai;
+      s.wsum[warp] = ai;
       s.wcount[warp] = ci;
     }
     __syncthreads();
@@ -387,10 +439,10 @@ __global__ void __launch_bounds__(kSThreads) sample_kernel(SampleArgs a) {
     unsigned cb = ci - ties, ctot = 0u;
     for (int w = 0; w < kSThreads / 32; ++w) {
       if (w < warp) {
-        ab += s.wmass[w];
+        ab += s.wsum[w];
         cb += s.wcount[w];
       }
-      atot += s.wmass[w];
+      atot += s.wsum[w];
       ctot += s.wcount[w];
     }
     if (t < cs) {
@@ -445,8 +497,7 @@ __global__ void __launch_bounds__(kSThreads) sample_kernel(SampleArgs a) {
       const int cut = s.cut >= 0 ? s.cut : seen_first + ctot <= kept ? n : -1;
       const float inv = (float)(1.0 / (double)total);
       float *to = a.probs + (long long)m * a.probs_stride + lo;
-      for (int j = t; j < n; j += kSThreads) {
-        const unsigned key = keys[j];
+      auto prob = [&](int j, unsigned key) {
         u64 w = 0ull;
         if (key > thr) {
           w = weigh(key);
@@ -454,7 +505,22 @@ __global__ void __launch_bounds__(kSThreads) sample_kernel(SampleArgs a) {
         } else if (key == thr && key && j <= cut) {
           w = kept ? thr_w : 0ull;
         }
-        to[j] = __ull2float_rn(w) * inv;
+        return __ull2float_rn(w) * inv;
+      };
+      if ((reinterpret_cast<uintptr_t>(to) & 15u) == 0u) {
+        for (int j = 4 * t; j < n; j += 4 * kSThreads) {
+          const Vec<Key, 4> v = *reinterpret_cast<const Vec<Key, 4> *>(keys + j);
+          Vec<float, 4> o;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o.e[e] = prob(j + e, v.e[e]);
+          if (j + 4 <= n) {
+            vec_store<float, 4>(to + j, o);
+          } else {
+            for (int e = 0; j + e < n; ++e) to[j + e] = o.e[e];
+          }
+        }
+      } else {
+        for (int j = t; j < n; j += kSThreads) to[j] = prob(j, keys[j]);
       }
     }
     __syncthreads();  // the keys may be replaced
@@ -532,7 +598,9 @@ int launch_sample_impl(SampleArgs a, cudaStream_t stream) {
   const SampleInfo *si = sample_info<T>(dev);
   if (!si) return KVS_ERR_LAUNCH;
   auto slice_of = [&](int k) { return ((a.V + (1 << k) - 1) / (1 << k) + 31) / 32 * 32; };
-  auto bytes_of = [&](int k) { return (long long)sizeof(SampleShared) + 4ll * slice_of(k); };
+  auto bytes_of = [&](int k) {
+    return (long long)sizeof(SampleShared) + (long long)sizeof(typename Keys<T>::Key) * slice_of(k);
+  };
   // The largest cluster whose clusters for all M rows are resident at once, with
   // slices of 2048 ids or more; where none is, the smallest whose slices fit.
   auto resident = [&](int k) { return bytes_of(k) > si->smem ? 0 : si->active[bytes_of(k) <= si->two][k]; };
