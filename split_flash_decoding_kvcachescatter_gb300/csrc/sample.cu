@@ -16,9 +16,13 @@
 // within about 2^-40 of a border between two tokens.
 //
 // A thread-block cluster takes a row; block r owns an equal slice of the ids and keeps
-// their logits in shared memory.  Histograms of a digit are gathered with
-// shared-memory atomics, summed over the cluster a share of the bins a block, and
-// scanned by every block.
+// their logits in shared memory.  One histogram over the distance from the largest
+// logit, 64 bins a unit of (x - max) / T, says in which bin the last kept token lies
+// (amounts by shared-memory atomics, summed over the cluster a share of the bins a
+// block, scanned by every block); the bin's tokens, or all down to it where they are at
+// most 1024, go to block 0, which sorts them.  Few tokens are then finished there, and
+// the row's 150,000 have been looked at twice.  Where the bin holds more (rows of nearly
+// equal logits) or lies 32 units down, the logit is found digit by digit of its bits.
 //
 // Bound: bytes (a row is read once).
 
@@ -34,7 +38,8 @@ namespace kvs {
 namespace {
 
 constexpr int kSThreads = 512;
-constexpr int kSBins = 2048;  // of a digit of 11 bits
+constexpr int kSBins = 2048;  // of a digit of 11 bits, and of 32 units of distance
+constexpr int kSMost = 1024;  // tokens that block 0 sorts
 constexpr int kSMaxDevices = 64;
 typedef unsigned long long u64;
 
@@ -148,18 +153,34 @@ __device__ __forceinline__ u64 share_of(float f, u64 x, bool &left) {
 }
 
 struct alignas(16) SampleShared {  // (the keys lie behind it)
-  unsigned low[kSBins], high[kSBins];  // this block's amounts (tokens or weight), a digit a bin
-  u64 amount[kSBins];                  // the row's
+  // this block's amounts (tokens or weight), by bin; or the tokens it sends to block 0
+  union {
+    struct {
+      unsigned low[kSBins], high[kSBins];
+    };
+    u64 out[kSMost];
+  };
+  // the row's; or in block 0 the tokens to sort (key, then ~id), and their weights
+  union {
+    u64 amount[kSBins];
+    struct {
+      u64 item[kSMost], weight[kSMost];
+    };
+  };
   u64 table[256];
-  unsigned top[16];  // of the cluster's blocks
+  unsigned top[2][16];  // of the cluster's blocks, by row parity
   unsigned ties[16];
   u64 above[16];
   u64 wsum[32];
   unsigned wcount[32];
   int bin, cut;
   u64 before, inside;
+  unsigned sent, total[2];       // tokens in out; in block 0: in item, by gather parity
+  unsigned found_key, found_kept;  // the last kept logit, and how many tokens that equal it
+  u64 found_cut, pad;            // weight of those that equal it and are not kept
 };
 static_assert(sizeof(SampleShared) % 16 == 0 && kSBins % 4 == 0, "vectors of keys and of bins");
+static_assert(kSMost <= 2 * kSThreads && kSMost * 16 <= kSBins * 8, "two tokens a thread, where the amounts were");
 
 // The row's amounts from the cluster's blocks': (bin, block) pairs, four a thread, the
 // pairs of a bin side by side: four loads in flight, sums over the threads of a bin,
@@ -231,6 +252,57 @@ __device__ __forceinline__ u64 find_bin(SampleShared &s, Need need) {
   return all;
 }
 
+// The first `n` of x (a power of two, at most kSMost) in falling order; by the block.
+__device__ __forceinline__ void sort_falling(u64 *x, int n) {
+  const int t = threadIdx.x;
+  for (int size = 2; size <= n; size <<= 1) {
+    for (int step = size >> 1; step >= 1; step >>= 1) {
+      if (2 * t < n) {
+        const int i = 2 * t - (t & (step - 1)), j = i + step;
+        const u64 p = x[i], q = x[j];
+        if ((p < q) == ((i & size) == 0)) {
+          x[i] = q;
+          x[j] = p;
+        }
+      }
+      __syncthreads();
+    }
+  }
+}
+
+// Sums of x[0 .. i] in place, i < n <= kSMost; by the block.
+__device__ __forceinline__ void running_sums(SampleShared &s, u64 *x, int n) {
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  u64 p = 2 * t < n ? x[2 * t] : 0ull, q = 2 * t + 1 < n ? x[2 * t + 1] : 0ull;
+  u64 inc = p + q;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const u64 v = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += v;
+  }
+  if (lane == 31) s.wsum[warp] = inc;
+  __syncthreads();
+  u64 before = inc - p - q;
+  for (int w = 0; w < warp; ++w) before += s.wsum[w];
+  if (2 * t < n) x[2 * t] = before + p;
+  if (2 * t + 1 < n) x[2 * t + 1] = before + p + q;
+  __syncthreads();
+}
+
+// How many of x[0 .. n), which do not fall, are below `need`; by every thread.
+__device__ __forceinline__ int first_reaching(const u64 *x, int n, u64 need) {
+  int lo = 0, hi = n;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (x[mid] < need)
+      lo = mid + 1;
+    else
+      hi = mid;
+  }
+  return lo;
+}
+__device__ __forceinline__ int power_of_two(int n) { return n <= 1 ? 1 : 1 << (32 - __clz(n - 1)); }
+
 template <typename T>
 __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(SampleArgs a) {
   using Key = typename Keys<T>::Key;
@@ -242,9 +314,12 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(SampleArgs a) {
   const int cs = (int)gridDim.x, rank = (int)cluster_rank();
   const int lo = min(a.V, rank * a.slice), hi = min(a.V, lo + a.slice), n = hi - lo;
   const int vecs = a.slice / VE;  // (slices are multiples of 32)
+  cluster_arrive_relaxed();  // waited for before the first remote store
   if (t < 256) s.table[t] = kExp2Table[t];
+  if (t < 2) s.total[t] = 0u;
   grid_dependency_wait();
   allow_dependent_launch();
+  int parity = 0, gathers = 0;
   auto clear = [&]() {
     for (int j = 4 * t; j < kSBins; j += 4 * kSThreads) {
       *reinterpret_cast<uint4 *>(&s.low[j]) = make_uint4(0u, 0u, 0u, 0u);
@@ -252,7 +327,7 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(SampleArgs a) {
     }
   };
   clear();
-  for (int m = blockIdx.y; m < a.M; m += gridDim.y) {  // same trip count in a cluster
+  for (int m = blockIdx.y; m < a.M; m += gridDim.y, parity ^= 1) {  // same trip count in a cluster
     const T *x = static_cast<const T *>(a.logits) + (long long)m * a.logits_stride + lo;
     const float temp = a.r.temperature ? __ldca(a.r.temperature + m) : 1.f;
     const bool greedy = !(temp >= 1.1754943508222875e-38f);
@@ -286,15 +361,16 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(SampleArgs a) {
     }
     most = __reduce_max_sync(0xffffffffu, most);
     if (lane == 0) s.wcount[warp] = most;
-    cluster_sync_all();  // every block runs, and is done with the row before
+    __syncthreads();
+    if (m == (int)blockIdx.y) cluster_wait();  // every block runs
     if (t < cs) {
       unsigned w = 0u;
       for (int j = 0; j < kSThreads / 32; ++j) w = max(w, s.wcount[j]);
-      st_dsmem_s32(dsmem_addr(&s.top[rank], t), (int)w);
+      st_dsmem_s32(dsmem_addr(&s.top[parity][rank], t), (int)w);
     }
     cluster_sync_all();
     unsigned top = 0u;
-    for (int r = 0; r < cs; ++r) top = max(top, s.top[r]);
+    for (int r = 0; r < cs; ++r) top = max(top, s.top[parity][r]);
     if (top == 0u) {  // nothing above -inf
       if (rank == 0 && t == 0) {
         if (a.ids) a.ids[m] = 0;
@@ -311,13 +387,27 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(SampleArgs a) {
       weigh.ch = (float)c;
       weigh.cl = (float)(c - (double)weigh.ch);
     }
+    // ---- min-p: a weight that is kept at the least ----
+    const u64 floor_w = least > 0.f ? (least >= 1.f ? 1ull << 44 : [&] {
+      bool left;
+      const u64 w = share_of(least, 1ull << 44, left);
+      return w + (left ? 1ull : 0ull);
+    }()) : 0ull;
     // ---- the last logit that is kept, and how many tokens that equal it ----
-    // A pass over one digit of the keys from `least_key` up whose higher digits are
-    // `prefix`: amounts by bin, summed over the cluster.
+    // The bin of a key by its distance from the top, the largest bin nearest; the least bin
+    // holds all from 32 units down.  (Rounding keeps the order, so bins fall as keys do.)
+    const float x_top = Keys<T>::logit(top);
+    const float per_unit = fminf(64.f / (greedy ? 1.f : temp), 1e30f);
+    auto near_bin = [&](unsigned key) {
+      return kSBins - 1 - (int)fminf((x_top - Keys<T>::logit(key)) * per_unit, (float)(kSBins - 1));
+    };
+    // Amounts by bin, summed over the cluster, of the keys from `least_key` up: by distance
+    // (pass < 0), or by digit `pass` of those whose higher digits are `prefix`.
     auto pass_over = [&](bool weights, int pass, unsigned prefix, unsigned least_key) {
-      const int shift = Keys<T>::shift(pass), above = pass == 0 ? 31 : Keys<T>::shift(pass - 1);
+      const int shift = pass < 0 ? 0 : Keys<T>::shift(pass), above = pass <= 0 ? 31 : Keys<T>::shift(pass - 1);
       auto bin_of = [&](unsigned key) {  // negative: not of this pass
         if (key < least_key || (pass > 0 && (key >> above) != prefix)) return -1;
+        if (pass < 0) return near_bin(key);
         return (int)((key >> shift) & ((pass == 0 ? kSBins : 1u << (above - shift)) - 1u));
       };
       if (weights) {  // (key by key: the code of a weight is long)
@@ -347,12 +437,165 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(SampleArgs a) {
       clear();
     };
     unsigned thr = 0u, kept = 0u;  // (nothing equals key 0)
+    u64 cut_off = 0ull;            // weight of the tokens that equal thr and are not kept
     const bool by_k = k > 0 && k < a.V, by_p = p < 1.f;
-    u64 cut_off = 0ull;  // weight of the tokens that equal thr and are not kept
+    const bool near = x_top < __uint_as_float(0x7f800000u);  // (from +inf there is no distance)
+    // p times the weight of what top-k keeps, rounded up; one token at the least
+    auto p_need = [&](u64 all) {
+      bool left = false;
+      const u64 w = p > 0.f ? share_of(p, all, left) : 0ull;
+      return max(w + (left ? 1ull : 0ull), 1ull);
+    };
+    // Sends to block 0 the keys from `least_key` up in bin `bin` of the distances, and
+    // above it where `whole`.  All blocks call it, after find_bin().
+    auto gather = [&](int bin, bool whole, unsigned least_key) {
+      cluster_arrive_release();  // this block is done with the row's amounts
+      if (t == 0) s.sent = 0u;
+      __syncthreads();
+      for (int j = t; j < vecs; j += kSThreads) {
+        const Vec<Key, VE> v = *reinterpret_cast<const Vec<Key, VE> *>(keys + j * VE);
+#pragma unroll
+        for (int e = 0; e < VE; ++e) {
+          const unsigned key = v.e[e];
+          if (key < least_key) continue;
+          const int at = near_bin(key);
+          if (at == bin || (whole && at > bin)) {
+            const unsigned i = atomicAdd(&s.sent, 1u);
+            if (i < (unsigned)kSMost) s.out[i] = (u64)key << 32 | (unsigned)~(lo + j * VE + e);
+          }
+        }
+      }
+      __syncthreads();
+      cluster_wait_acquire();  // and so is block 0
+      const unsigned sent = s.sent;
+      if (t == 0 && sent) s.cut = (int)atom_dsmem_add(dsmem_addr(&s.total[gathers & 1], 0), sent);
+      __syncthreads();
+      const unsigned at = (unsigned)s.cut;
+      for (unsigned j = t; j < min(sent, (unsigned)kSMost); j += kSThreads)
+        if (at + j < (unsigned)kSMost) st_dsmem_u64(dsmem_addr(&s.item[at + j], 0), s.out[j]);
+      cluster_sync_all();  // block 0 has them
+      clear();             // (the amounts' place)
+      ++gathers;
+      if (t == 0) s.total[gathers & 1] = 0u;  // of the gather after this one
+    };
+    // Block 0: its n tokens in falling order, and the sums of their weights.
+    auto sort_items = [&](int n, bool weights) {
+      const int n2 = power_of_two(n);
+      for (int i = n + t; i < n2; i += kSThreads) s.item[i] = 0ull;
+      __syncthreads();
+      sort_falling(s.item, n2);
+      if (weights) {
+        for (int i = t; i < n; i += kSThreads) s.weight[i] = weigh((unsigned)(s.item[i] >> 32));
+        __syncthreads();
+        running_sums(s, s.weight, n);
+      }
+    };
+    // Of the sorted tokens [0, n), how many of the first `upto` equal the last of those.
+    auto ties_upto = [&](int upto, int n) {
+      const unsigned key = (unsigned)(s.item[upto - 1] >> 32);
+      int c = 0;
+      for (int i = t; i < n; i += kSThreads) c += i < upto && (unsigned)(s.item[i] >> 32) == key;
+      const int c2 = __reduce_add_sync(0xffffffffu, c);
+      if (t == 0) s.sent = 0u;
+      __syncthreads();
+      if (lane == 0 && c2) atomicAdd(&s.sent, (unsigned)c2);
+      __syncthreads();
+      const unsigned r = s.sent;
+      __syncthreads();
+      return r;
+    };
+    // Block 0 tells all (it alone gives the values); by all blocks.
+    auto tell = [&](unsigned key, unsigned count, u64 cut) {
+      if (rank == 0 && t < cs) {
+        st_dsmem_s32(dsmem_addr(&s.found_key, t), (int)key);
+        st_dsmem_s32(dsmem_addr(&s.found_kept, t), (int)count);
+        st_dsmem_u64(dsmem_addr(&s.found_cut, t), cut);
+      }
+      cluster_sync_all();
+      thr = s.found_key;
+      kept = s.found_kept;
+      cut_off = s.found_cut;
+    };
+    bool k_open = by_k, p_open = by_p;
     if (by_k && k == 1) {
       thr = top;
       kept = 1u;
-    } else if (by_k) {
+      k_open = p_open = false;
+    }
+    if (k_open && near) {
+      pass_over(false, -1, 0u, 1u);
+      find_bin(s, [&](u64) { return (u64)k; });
+      const int bin = s.bin;
+      const u64 before = s.before, inside = s.inside;
+      if (bin < 0) {  // fewer tokens than k
+        k_open = false;
+      } else if (bin > 0 && inside <= (u64)kSMost) {
+        k_open = false;
+        const bool whole = before + inside <= (u64)kSMost;
+        const int n = (int)(whole ? before + inside : inside);
+        gather(bin, whole, 1u);
+        unsigned key = 0u, count = 0u;
+        u64 cut = 0ull;
+        if (whole && !a.probs) {
+          if (rank == 0) {  // the rest of the row is block 0's
+            sort_items(n, true);
+            int c = k;
+            if (by_p) c = min(c, first_reaching(s.weight, c, p_need(s.weight[c - 1])) + 1);
+            int have = 0;
+            for (int i = t; i < c; i += kSThreads)
+              have += s.weight[i] - (i ? s.weight[i - 1] : 0ull) >= floor_w;
+            have = __reduce_add_sync(0xffffffffu, have);
+            if (t == 0) s.sent = 0u;
+            __syncthreads();
+            if (lane == 0 && have) atomicAdd(&s.sent, (unsigned)have);
+            __syncthreads();
+            c = (int)s.sent;
+            const u64 total = s.weight[c - 1];
+            // the kept ones in the order of ids, with the sums of their weights
+            const int c2 = power_of_two(c);
+            for (int i = t; i < c2; i += kSThreads)
+              s.out[i] = i < c ? (s.item[i] << 32 | (unsigned)i) : 0ull;
+            __syncthreads();
+            sort_falling(s.out, c2);
+            for (int i = t; i < c; i += kSThreads) {
+              const int r = (int)(unsigned)s.out[i];
+              s.item[i] = s.weight[r] - (r ? s.weight[r - 1] : 0ull);
+            }
+            __syncthreads();
+            running_sums(s, s.item, c);
+            bool left;
+            u64 mark = !(u > 0.f) ? 0ull : u < 1.f ? share_of(u, total, left) : total - 1ull;
+            if (mark >= total) mark = total - 1ull;
+            const int i = first_reaching(s.item, c, mark + 1ull);
+            if (t == 0) {
+              const u64 w = s.item[i] - (i ? s.item[i - 1] : 0ull);
+              if (a.ids) a.ids[m] = (int)~(unsigned)(s.out[i] >> 32);
+              if (a.token_probs) a.token_probs[m] = (float)((double)w / (double)total);
+            }
+            __syncthreads();
+            clear();
+          }
+          __syncthreads();  // the keys may be replaced
+          continue;
+        }
+        if (rank == 0) {
+          sort_items(n, whole);
+          int c = whole ? k : (int)((u64)k - before);
+          if (whole && by_p) c = min(c, first_reaching(s.weight, c, p_need(s.weight[c - 1])) + 1);
+          key = (unsigned)(s.item[c - 1] >> 32);
+          count = ties_upto(c, n);
+          if (!whole) {
+            // all that equal the key lie in the bin: those behind the c-th are not kept
+            int e = c;
+            while (e < n && (unsigned)(s.item[e] >> 32) == key) ++e;
+            cut = (u64)(e - c) * weigh(key);
+          }
+        }
+        tell(key, count, cut);
+        if (whole) p_open = false;
+      }
+    }
+    if (k_open) {  // digit by digit
       unsigned prefix = 0u, need = (unsigned)k;
       bool reached = true;
       u64 ties = 0ull;
@@ -366,7 +609,6 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(SampleArgs a) {
           prefix = pass == 0 ? (unsigned)s.bin
                              : prefix << (Keys<T>::shift(pass - 1) - Keys<T>::shift(pass)) | (unsigned)s.bin;
         }
-        __syncthreads();
       }
       if (reached) {
         thr = prefix;
@@ -374,34 +616,46 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(SampleArgs a) {
         cut_off = (ties - need) * weigh(thr);
       }
     }
-    if (by_p && !(by_k && k == 1)) {
+    if (p_open && near) {
+      pass_over(true, -1, 0u, max(thr, 1u));
+      u64 need = 0ull;
+      find_bin(s, [&](u64 all) { return need = p_need(all - cut_off); });
+      const int bin = s.bin;
+      const u64 before = s.before;
+      if (bin > 0) {
+        gather(bin, false, max(thr, 1u));
+        const unsigned n = (unsigned)ld_dsmem_s32(dsmem_addr(&s.total[(gathers - 1) & 1], 0));
+        if (n <= (unsigned)kSMost) {
+          p_open = false;
+          unsigned key = 0u, count = 0u;
+          if (rank == 0) {
+            sort_items((int)n, true);
+            const int c = first_reaching(s.weight, (int)n, need - before) + 1;
+            key = (unsigned)(s.item[c - 1] >> 32);
+            count = ties_upto(c, (int)n);
+          }
+          tell(key, count, 0ull);
+        }
+      }
+    }
+    if (p_open) {
       unsigned prefix = 0u;
       u64 need = 0ull;
+      const unsigned least_key = max(thr, 1u);
       for (int pass = 0; pass < Keys<T>::kPasses; ++pass) {
-        pass_over(true, pass, prefix, max(thr, 1u));
+        pass_over(true, pass, prefix, least_key);
         find_bin(s, [&](u64 all) {
-          if (pass == 0) {  // p times the weight of what top-k keeps, rounded up; one token at the least
-            bool left = false;
-            need = p > 0.f ? share_of(p, all - cut_off, left) : 0ull;
-            need = max(need + (left ? 1ull : 0ull), 1ull);
-          }
+          if (pass == 0) need = p_need(all - cut_off);
           return need;
         });
         need -= s.before;
         prefix = pass == 0 ? (unsigned)s.bin
                            : prefix << (Keys<T>::shift(pass - 1) - Keys<T>::shift(pass)) | (unsigned)s.bin;
-        __syncthreads();
       }
       thr = prefix;
       const u64 w = weigh(thr);
       kept = (unsigned)((need + w - 1ull) / w);
     }
-    // ---- min-p: a weight that is kept at the least ----
-    const u64 floor_w = least > 0.f ? (least >= 1.f ? 1ull << 44 : [&] {
-      bool left;
-      const u64 w = share_of(least, 1ull << 44, left);
-      return w + (left ? 1ull : 0ull);
-    }()) : 0ull;
     const u64 thr_w = thr ? weigh(thr) : 0ull;
     if (thr_w < floor_w) kept = 0u;
     // ---- this block's share: a run of ids a thread ----
