@@ -822,7 +822,7 @@ int kvs_process_logits(const void *logits, int64_t logits_stride, void *out, int
  * the same for every id (0 for those not kept).  NaN and -inf are never drawn; a row
  * without anything above -inf gives token 0 and probabilities 0; where a logit is
  * +inf, those tokens share the row.  Weights below 2^-45 of the largest count as 0;
- * others are computed to 2^-40 of themselves and summed exactly, so the result does
+ * others are computed to 2^-37 of themselves and summed exactly, so the result does
  * not depend on the order of anything.
  */
 typedef struct kvs_sample_rules {

@@ -11,9 +11,9 @@
 // first id at which the running sum of kept weights, in the order of ids, exceeds u
 // times their sum.
 //
-// Weights are integers, w 2^44 rounded, computed to 2^-41 of themselves (below), so
+// Weights are integers, w 2^44 rounded, computed to 2^-37 of themselves (below), so
 // sums are exact whatever their order, and a token is drawn wrongly only where u falls
-// within about 2^-40 of a border between two tokens.
+// within about 2^-37 of a border between two tokens.
 //
 // A thread-block cluster takes a row; block r owns an equal slice of the ids and keeps
 // their logits in shared memory.  One histogram over the distance from the largest
@@ -95,10 +95,10 @@ struct Weigher {
   float top, ch, cl;
   const u64 *table;  // 2^(i / 256) 2^44
 
-  // e^((x - top) / T) 2^44.  y = (x - top) log2(e) / T as a sum of two floats
-  // (off by 2^-46 of it); y = n + i / 256 + r with |r| <= 2^-9; 2^r - 1 = e^(r ln 2) - 1
-  // by its series, whose first term is kept in two floats; all but the leading parts
-  // are below 2^-17, so float arithmetic is off by 2^-41 there.
+  // e^((x - top) / T) 2^44.  y = (x - top) log2(e) / T as a sum of two floats (off by
+  // 2^-46 of it); y = n + i / 256 + r with |r| <= 2^-9; z = 2^r - 1 = e^(r ln 2) - 1 by its
+  // series: the first term in two floats, the others, below 2^-19, in one; then 2^(i / 256)
+  // (1 + z) in integers, z in units of 2^-40.  Off by 2^-37 of itself at most.
   __device__ __forceinline__ u64 operator()(unsigned key) const {
     if (key == 0u) return 0ull;
     const float x = Keys<T>::logit(key);
@@ -109,27 +109,18 @@ struct Weigher {
     const float p = __fmul_rn(d, ch);
     if (!(p > -46.f)) return 0ull;
     const float e = __fadd_rn(__fmaf_rn(d, ch, -p), __fmaf_rn(d, cl, __fmul_rn(dl, ch)));
-    const float t = rintf(__fmul_rn(p, 256.f));
-    const float rr = __fmaf_rn(t, -1.f / 256.f, p);  // exact
+    const int t = __float2int_rn(__fmul_rn(p, 256.f));
+    const float rr = __fmaf_rn((float)t, -1.f / 256.f, p);  // exact
     constexpr float kLn2 = 0.693147182464599609375f, kLn2Low = -1.904654323148236e-09f;
     const float zh = __fmul_rn(rr, kLn2);
     const float zl = __fadd_rn(__fmaf_rn(rr, kLn2, -zh), __fmaf_rn(rr, kLn2Low, __fmul_rn(e, kLn2)));
-    const float sq = __fmul_rn(zh, zh);
-    const float poly = __fmul_rn(sq, __fmaf_rn(zh, __fmaf_rn(zh, 1.f / 24.f, 1.f / 6.f), 0.5f));
-    const float rest = __fadd_rn(poly, __fmaf_rn(zh, zl, zl));  // e^z - 1 = zh + rest
-    const int ti = (int)t;
-    const u64 tab = table[ti & 255];
-    const float th = (float)(unsigned)(tab >> 21) * 1.1920928955078125e-07f;  // 2^(i / 256), 24 bits
-    const float tl = (float)((int)(tab & 0x1fffffu)) * 5.684341886080802e-14f;  // and what is left
-    const float hi = __fmul_rn(th, zh);
-    const float lo = __fadd_rn(__fmaf_rn(th, zh, -hi), __fmaf_rn(tl, zh, __fmul_rn(th, rest)));
-    // hi + lo in units of 2^-44, in two steps
-    const float h1 = rintf(__fmul_rn(hi, 2147483648.f));
-    const float left = __fadd_rn(__fmaf_rn(h1, -4.656612873077393e-10f, hi), lo);
-    const long long w = (long long)tab + (long long)(int)h1 * 8192 +
-                        (long long)(int)rintf(__fmul_rn(left, 17592186044416.f));
-    const int n = -(ti >> 8);  // 0 .. 46
-    return n == 0 ? (u64)w : ((u64)w + (1ull << (n - 1))) >> n;
+    const float rest = __fmaf_rn(__fmul_rn(zh, zh), __fmaf_rn(zh, 1.f / 6.f, 0.5f), __fmaf_rn(zh, zl, zl));
+    const int z = __float2int_rn(__fmul_rn(zh, 1099511627776.f)) + __float2int_rn(__fmul_rn(rest, 1099511627776.f));
+    const u64 tab = table[t & 255];
+    // tab z 2^-40, from tab's upper 32 bits
+    const u64 w = tab + (u64)(((long long)(int)(unsigned)(tab >> 14) * (long long)z) >> 26);
+    const int n = -(t >> 8);  // 0 .. 46
+    return (w + ((1ull << n) >> 1)) >> n;
   }
 };
 
@@ -177,7 +168,8 @@ struct alignas(16) SampleShared {  // (the keys lie behind it)
   u64 before, inside;
   unsigned sent, total[2];       // tokens in out; in block 0: in item, by gather parity
   unsigned found_key, found_kept;  // the last kept logit, and how many tokens that equal it
-  u64 found_cut, pad;            // weight of those that equal it and are not kept
+  u64 found_cut;                 // weight of those that equal it and are not kept
+  float rate[2];                 // log2(e) / T in two parts
 };
 static_assert(sizeof(SampleShared) % 16 == 0 && kSBins % 4 == 0, "vectors of keys and of bins");
 static_assert(kSMost <= 2 * kSThreads && kSMost * 16 <= kSBins * 8, "two tokens a thread, where the amounts were");
@@ -253,6 +245,7 @@ __device__ __forceinline__ u64 find_bin(SampleShared &s, Need need) {
 }
 
 // The first `n` of x (a power of two, at most kSMost) in falling order; by the block.
+// (Steps of 32 and less stay within the 64 places of a warp's threads.)
 __device__ __forceinline__ void sort_falling(u64 *x, int n) {
   const int t = threadIdx.x;
   for (int size = 2; size <= n; size <<= 1) {
@@ -265,9 +258,14 @@ __device__ __forceinline__ void sort_falling(u64 *x, int n) {
           x[j] = p;
         }
       }
-      __syncthreads();
+      // the next step, of this size or of the next one
+      if ((step > 1 ? step >> 1 : size) >= 64 || step >= 64)
+        __syncthreads();
+      else
+        __syncwarp();
     }
   }
+  __syncthreads();
 }
 
 // Sums of x[0 .. i] in place, i < n <= kSMost; by the block.
@@ -335,6 +333,11 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(SampleArgs a) {
     const float p = !greedy && a.r.top_p ? __ldca(a.r.top_p + m) : 1.f;
     const float least = !greedy && a.r.min_p ? __ldca(a.r.min_p + m) : 0.f;
     const float u = __ldca(a.uniforms + m);
+    if (t == kSThreads - 1) {  // (one thread: all of them would take 4 us for it)
+      const double c = 1.4426950408889634074 / (double)(greedy ? 1.f : temp);
+      s.rate[0] = (float)c;
+      s.rate[1] = (float)(c - (double)(float)c);
+    }
     // ---- the slice's logits ----
     unsigned most = 0u;
     if ((reinterpret_cast<uintptr_t>(x) & 15u) == 0u) {
@@ -359,6 +362,7 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(SampleArgs a) {
         most = max(most, (unsigned)key);
       }
     }
+    const unsigned own_most = most;
     most = __reduce_max_sync(0xffffffffu, most);
     if (lane == 0) s.wcount[warp] = most;
     __syncthreads();
@@ -381,12 +385,7 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(SampleArgs a) {
       __syncthreads();  // the keys may be replaced
       continue;
     }
-    Weigher<T> weigh{Keys<T>::logit(top), 0.f, 0.f, s.table};
-    {
-      const double c = 1.4426950408889634074 / (double)(greedy ? 1.f : temp);
-      weigh.ch = (float)c;
-      weigh.cl = (float)(c - (double)weigh.ch);
-    }
+    const Weigher<T> weigh{Keys<T>::logit(top), s.rate[0], s.rate[1], s.table};
     // ---- min-p: a weight that is kept at the least ----
     const u64 floor_w = least > 0.f ? (least >= 1.f ? 1ull << 44 : [&] {
       bool left;
@@ -400,6 +399,21 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(SampleArgs a) {
     const float per_unit = fminf(64.f / (greedy ? 1.f : temp), 1e30f);
     auto near_bin = [&](unsigned key) {
       return kSBins - 1 - (int)fminf((x_top - Keys<T>::logit(key)) * per_unit, (float)(kSBins - 1));
+    };
+    // The least key of a bin or a higher one (1 or more); by a warp, 32 looks at a time.
+    auto first_key = [&](int bin) {
+      unsigned low = 1u, high = top;  // of [low, high], high's bin is the largest
+      while (low < high) {
+        const unsigned step = (high - low) / 32u + 1u;
+        const unsigned at = min(high, low + step * (unsigned)lane + (step - 1u));  // the end of a part
+        const unsigned hit = __ballot_sync(0xffffffffu, near_bin(at) >= bin);      // (lane 31's at the least)
+        const int part = __ffs(hit) - 1;
+        const unsigned end = min(high, low + step * (unsigned)part + (step - 1u));
+        low += step * (unsigned)part;
+        high = end;
+        if (step == 1u) break;
+      }
+      return high;
     };
     // Amounts by bin, summed over the cluster, of the keys from `least_key` up: by distance
     // (pass < 0), or by digit `pass` of those whose higher digits are `prefix`.
@@ -452,14 +466,14 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(SampleArgs a) {
       cluster_arrive_release();  // this block is done with the row's amounts
       if (t == 0) s.sent = 0u;
       __syncthreads();
+      const unsigned from = max(least_key, first_key(bin));
+      const unsigned upto = whole || bin == kSBins - 1 ? top : first_key(bin + 1) - 1u;
       for (int j = t; j < vecs; j += kSThreads) {
         const Vec<Key, VE> v = *reinterpret_cast<const Vec<Key, VE> *>(keys + j * VE);
 #pragma unroll
         for (int e = 0; e < VE; ++e) {
           const unsigned key = v.e[e];
-          if (key < least_key) continue;
-          const int at = near_bin(key);
-          if (at == bin || (whole && at > bin)) {
+          if (key >= from && key <= upto) {
             const unsigned i = atomicAdd(&s.sent, 1u);
             if (i < (unsigned)kSMost) s.out[i] = (u64)key << 32 | (unsigned)~(lo + j * VE + e);
           }
@@ -490,15 +504,14 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(SampleArgs a) {
         running_sums(s, s.weight, n);
       }
     };
-    // Of the sorted tokens [0, n), how many of the first `upto` equal the last of those.
-    auto ties_upto = [&](int upto, int n) {
-      const unsigned key = (unsigned)(s.item[upto - 1] >> 32);
+    // How many of the sorted tokens [from, to) have this key; by block 0.
+    auto equal_in = [&](int from, int to, unsigned key) {
       int c = 0;
-      for (int i = t; i < n; i += kSThreads) c += i < upto && (unsigned)(s.item[i] >> 32) == key;
-      const int c2 = __reduce_add_sync(0xffffffffu, c);
+      for (int i = from + t; i < to; i += kSThreads) c += (unsigned)(s.item[i] >> 32) == key;
+      c = __reduce_add_sync(0xffffffffu, c);
       if (t == 0) s.sent = 0u;
       __syncthreads();
-      if (lane == 0 && c2) atomicAdd(&s.sent, (unsigned)c2);
+      if (lane == 0 && c) atomicAdd(&s.sent, (unsigned)c);
       __syncthreads();
       const unsigned r = s.sent;
       __syncthreads();
@@ -523,7 +536,32 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(SampleArgs a) {
       k_open = p_open = false;
     }
     if (k_open && near) {
-      pass_over(false, -1, 0u, 1u);
+      // Where this block alone has k maxima of groups of its tokens, the k-th of those is at
+      // most the row's k-th logit: what lies in lower bins than it need not be counted.
+      // (Each count is a shared-memory atomic on a place of its own, some 17 cycles a warp.)
+      const bool by_thread = 2 * k <= kSThreads;  // groups: a thread's tokens, or a vector's
+      unsigned least_key = 1u;
+      if (by_thread || 4 * k <= vecs) {
+        if (by_thread) {
+          if (own_most) atomicAdd(&s.low[near_bin(own_most)], 1u);
+        } else {
+          for (int j = t; j < vecs; j += kSThreads) {
+            const Vec<Key, VE> v = *reinterpret_cast<const Vec<Key, VE> *>(keys + j * VE);
+            unsigned w = v.e[0];
+#pragma unroll
+            for (int e = 1; e < VE; ++e) w = max(w, (unsigned)v.e[e]);
+            if (w) atomicAdd(&s.low[near_bin(w)], 1u);
+          }
+        }
+        __syncthreads();
+        for (int j = t; j < kSBins; j += kSThreads) s.amount[j] = s.low[j];
+        __syncthreads();
+        clear();
+        find_bin(s, [&](u64) { return (u64)k; });
+        if (s.bin > 0) least_key = first_key(s.bin);
+        __syncthreads();
+      }
+      pass_over(false, -1, 0u, least_key);
       find_bin(s, [&](u64) { return (u64)k; });
       const int bin = s.bin;
       const u64 before = s.before, inside = s.inside;
@@ -583,13 +621,9 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(SampleArgs a) {
           int c = whole ? k : (int)((u64)k - before);
           if (whole && by_p) c = min(c, first_reaching(s.weight, c, p_need(s.weight[c - 1])) + 1);
           key = (unsigned)(s.item[c - 1] >> 32);
-          count = ties_upto(c, n);
-          if (!whole) {
-            // all that equal the key lie in the bin: those behind the c-th are not kept
-            int e = c;
-            while (e < n && (unsigned)(s.item[e] >> 32) == key) ++e;
-            cut = (u64)(e - c) * weigh(key);
-          }
+          count = equal_in(0, c, key);
+          // (all that equal the key lie in the bin)
+          if (!whole) cut = equal_in(c, n, key) * weigh(key);
         }
         tell(key, count, cut);
         if (whole) p_open = false;
@@ -632,7 +666,7 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(SampleArgs a) {
             sort_items((int)n, true);
             const int c = first_reaching(s.weight, (int)n, need - before) + 1;
             key = (unsigned)(s.item[c - 1] >> 32);
-            count = ties_upto(c, (int)n);
+            count = equal_in(0, c, key);
           }
           tell(key, count, 0ull);
         }
@@ -749,7 +783,7 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(SampleArgs a) {
       // ties up to position `cut` of the slice are kept; all of them where the last kept
       // one lies in a later block
       const int cut = s.cut >= 0 ? s.cut : seen_first + ctot <= kept ? n : -1;
-      const float inv = (float)(1.0 / (double)total);
+      const float inv = 1.f / __ull2float_rn(total);
       float *to = a.probs + (long long)m * a.probs_stride + lo;
       auto prob = [&](int j, unsigned key) {
         u64 w = 0ull;
