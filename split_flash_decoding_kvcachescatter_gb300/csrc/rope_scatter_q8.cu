@@ -9,13 +9,17 @@
 // its older numbers are then divided by the growth and rounded again (exact down
 // to 2^-6, the end of e4m3's normal range).
 //
-// A thread block takes the 16-position blocks whose first new row lies in its
-// rows of the batch, and a slice of the heads: it makes the (cos, sin) of the
-// block's tokens in shared memory once, then a warp takes a head at a time: one
-// pass over the new rows for the largest element, one that rounds and writes them
-// (the rows come from L2 then).
-//
-// Bound: bytes (each row of q, k, v read once, q and the 8-bit rows written once).
+// Bound: bytes (each row of q, k, v read once, q and the 8-bit rows written once).  Two
+// kernels.  The usual one, for heads of whole 16-byte vectors that turn whole or in
+// interleaved pairs, has two kinds of thread blocks in one launch.  K or V: the 16-position
+// blocks whose first new row lies in the thread block's rows of the batch, two warps a kv
+// head, eight rows each, which hold the turned rows in registers between the look for the
+// largest element and the rounding.  q: a token or two.  Both issue their loads before
+// the look-ups (sequence, page, old scale) that decide where the results go.
+// The other kernel, for any head: a warp a head of a 16-position block at a time, the rows
+// of K and V read twice.
+
+#include <type_traits>
 
 #include "kvs_fp8.cuh"
 #include "kvs_paged.cuh"
@@ -51,6 +55,18 @@ __device__ __forceinline__ void store_e4m3(uint8_t *p, const float (&f)[VE], flo
     *reinterpret_cast<unsigned short *>(p) = (unsigned short)to_e4m3x2(f[0] * inv, f[1] * inv);
   } else {
     *p = (uint8_t)to_e4m3x2(f[0] * inv, 0.f);
+  }
+}
+
+// Older numbers of a block, `words` words of four, under a scale that has grown: times
+// `ratio`, rounded again.  By threads `first`, first + step, ...
+__device__ __forceinline__ void requantise(unsigned *w, int words, int first, int step, float ratio) {
+  for (int e = first; e < words; e += step) {
+    const unsigned x = __ldcg(w + e);
+    const uint32_t u0 = from_e4m3x2(x), u1 = from_e4m3x2(x >> 16);
+    const float2 f0 = __half22float2(*reinterpret_cast<const __half2 *>(&u0));
+    const float2 f1 = __half22float2(*reinterpret_cast<const __half2 *>(&u1));
+    w[e] = to_e4m3x4(f0.x * ratio, f0.y * ratio, f1.x * ratio, f1.y * ratio);
   }
 }
 
@@ -204,17 +220,7 @@ __global__ void __launch_bounds__(kRqThreads)
       if (in > 0 && old >= scale) {
         scale = old;
       } else {
-        if (in > 0) {  // older rows under a scale that has grown
-          const float ratio = old / scale;
-          unsigned *w = reinterpret_cast<unsigned *>(block);
-          for (int e = lane; e < in * a.D / 4; e += 32) {
-            const unsigned x = __ldcg(w + e);
-            const uint32_t u0 = from_e4m3x2(x), u1 = from_e4m3x2(x >> 16);
-            const float2 f0 = __half22float2(*reinterpret_cast<const __half2 *>(&u0));
-            const float2 f1 = __half22float2(*reinterpret_cast<const __half2 *>(&u1));
-            w[e] = to_e4m3x4(f0.x * ratio, f0.y * ratio, f1.x * ratio, f1.y * ratio);
-          }
-        }
+        if (in > 0) requantise(reinterpret_cast<unsigned *>(block), in * a.D / 4, lane, 32, old / scale);
         if (lane == 0) *scale_at = scale;
       }
       const float inv = 1.f / scale;
@@ -229,6 +235,297 @@ __global__ void __launch_bounds__(kRqThreads)
   }
 }
 
+// ---- whole vectors ---------------------------------------------------------------
+constexpr int kWThreads = 256;
+constexpr int kWHeads = kWThreads / 64;  // kv heads of a thread block: two warps each
+constexpr int kWRows = kScaleBlock / 2;  // rows of a warp
+constexpr int kWTokens = 2;              // rows of q a thread block has at most
+
+struct WholeArgs {
+  RopeQ8Args r;
+  int kv_parts, kv_blocks;  // parts of the kv heads (K's, then V's), thread blocks for K and V
+  int q_tokens, q_parts;    // rows of q a thread block, and parts of a row
+};
+
+// (cos, sin) of a frequency's turns at a position, times scale.
+__device__ __forceinline__ float2 angle_of(unsigned long long turns, int pos, float scale) {
+  const unsigned long long turn = turns * (unsigned long long)(unsigned)pos;
+  // the angle over pi, in [-1, 1): the fraction's top 32 bits, signed, times 2^-31
+  const float t = (float)(int)(unsigned)(turn >> 32) * 4.656612873077393e-10f;
+  float sn, c;
+  sincospif(t, &sn, &c);
+  return make_float2(c * scale, sn * scale);
+}
+
+// A token's (cos, sin) in shared memory: those of vector w of a head in float4s, one a row
+// of the table, so that the lanes of a head read 16 bytes side by side.
+template <int VE, bool IL, int D>
+struct Angles {
+  static constexpr int kOf = IL ? VE / 2 : VE;        // pairs of a vector
+  static constexpr int kVectors = D / 2 / kOf;        // vectors that turn, at most
+  static __device__ __forceinline__ int at(int j) {   // of pair j
+    const int w = j / kOf, e = j % kOf;
+    return ((e >> 1) * kVectors + w) * 4 + (e & 1) * 2;
+  }
+  // turns vector x (IL), or the pair (x, y)
+  static __device__ __forceinline__ void turn(const float *table, int w, float (&x)[VE], float (&y)[VE]) {
+#pragma unroll
+    for (int c = 0; c < kOf / 2; ++c) {
+      const float4 t = *reinterpret_cast<const float4 *>(table + (c * kVectors + w) * 4);
+      if constexpr (IL) {
+        const float p0 = x[4 * c], r0 = x[4 * c + 1], p1 = x[4 * c + 2], r1 = x[4 * c + 3];
+        x[4 * c] = p0 * t.x - r0 * t.y;
+        x[4 * c + 1] = r0 * t.x + p0 * t.y;
+        x[4 * c + 2] = p1 * t.z - r1 * t.w;
+        x[4 * c + 3] = r1 * t.z + p1 * t.w;
+      } else {
+        const float p0 = x[2 * c], r0 = y[2 * c], p1 = x[2 * c + 1], r1 = y[2 * c + 1];
+        x[2 * c] = p0 * t.x - r0 * t.y;
+        y[2 * c] = r0 * t.x + p0 * t.y;
+        x[2 * c + 1] = p1 * t.z - r1 * t.w;
+        y[2 * c + 1] = r1 * t.z + p1 * t.w;
+      }
+    }
+  }
+};
+
+template <typename T, int VE>
+__device__ __forceinline__ void to_floats(const Vec<T, VE> &v, float (&f)[VE]) {
+#pragma unroll
+  for (int e = 0; e < VE; ++e) f[e] = to_f32(v.e[e]);
+}
+
+// IL: interleaved pairs, of which rot / 2 turn; else the half layout, turned whole.
+template <typename T, bool IL, int D>
+__global__ void __launch_bounds__(kWThreads, sizeof(T) == 4 ? 3 : 4)
+    rope_q8_whole_kernel(WholeArgs wa, PagedArgs b, int *d_status) {
+  constexpr int VE = 16 / sizeof(T);
+  using A = Angles<VE, IL, D>;
+  constexpr int PV = IL ? D / VE : D / 2 / VE;   // units of a row: vectors, or pairs of them
+  constexpr int U = kWRows * PV / 32;            // of a lane, eight rows a warp
+  constexpr int UV = kWRows * D / VE / 32;       // vectors of V, the same
+  static_assert(U >= 1 && 32 % PV == 0, "a lane's units lie in rows 32 / PV apart");
+  const RopeQ8Args &a = wa.r;
+  __shared__ __align__(16) float cs[kScaleBlock][D];
+  __shared__ float s_most[kWThreads / 32];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int half = a.rot / 2, nturn = IL ? a.rot / VE : PV;  // pairs that turn, units that do
+  grid_dependency_wait();
+  if ((int)blockIdx.x >= wa.kv_blocks) {
+    // ======================= q =================================================
+    const int block = (int)blockIdx.x - wa.kv_blocks, part = block % wa.q_parts;
+    const int row0 = block / wa.q_parts * wa.q_tokens, ntok = min(wa.q_tokens, b.num_rows - row0);
+    const int of_token = a.H * PV, step = kWThreads * wa.q_parts;
+    Vec<T, VE> x[kWTokens], y[kWTokens];
+    auto load = [&](int it) {
+#pragma unroll
+      for (int t = 0; t < kWTokens; ++t) {
+        if (t >= ntok || it >= of_token) break;
+        const T *src = static_cast<const T *>(a.q) + (long long)(row0 + t) * a.q_stride + (it / PV) * D + (it % PV) * VE;
+        x[t] = vec_load<T, VE>(src);
+        if constexpr (!IL) y[t] = vec_load<T, VE>(src + D / 2);
+      }
+    };
+    int it = part * kWThreads + tid;
+    load(it);
+    const unsigned long long turns = tid % (D / 2) < half ? turns_of(a.inv_freq[tid % (D / 2)]) : 0ull;
+    allow_dependent_launch();
+    if (part == 0)  // the status of every sequence, spread over the blocks
+      for (long long i = (long long)(block / wa.q_parts) * kWThreads + tid; i < b.M;
+           i += (long long)((b.num_rows + wa.q_tokens - 1) / wa.q_tokens) * kWThreads) {
+        const int err = paged_seq(b, (int)i).err;
+        if (err != KVS_OK) record_status(d_status, err);
+      }
+    int state[kWTokens];  // 0: nothing to write, 1: rotated, 2: NaN
+    PagedSeq s{0, 0, 0, KVS_OK};
+    int i = -1;
+#pragma unroll
+    for (int t = 0; t < kWTokens; ++t) {
+      state[t] = 0;
+      const int row = row0 + t;
+      if (t >= ntok) break;
+      if (i < 0 || row >= s.row0 + s.n) i = warp_find_seq(b, row, lane, s);
+      if (i >= b.M || s.err == KVS_ERR_ROWS || row < s.row0 || row >= s.row0 + s.n) {
+        i = -1;
+        continue;
+      }
+      state[t] = s.err != KVS_OK ? 2 : 1;
+      if (tid / (D / 2) == t && tid % (D / 2) < half)
+        *reinterpret_cast<float2 *>(&cs[t][A::at(tid % (D / 2))]) = angle_of(turns, s.p + row - s.row0, a.scale);
+    }
+    __syncthreads();
+    for (; it < of_token; load(it)) {
+      const int w = it % PV, at = (it / PV) * D + w * VE;
+#pragma unroll
+      for (int t = 0; t < kWTokens; ++t) {
+        if (t >= ntok || state[t] == 0) continue;
+        T *to = static_cast<T *>(a.q_out) + (long long)(row0 + t) * a.q_out_stride + at;
+        if (state[t] == 2 || w < nturn) {
+          float fx[VE], fy[VE];
+          to_floats<T, VE>(x[t], fx);
+          if constexpr (!IL) to_floats<T, VE>(y[t], fy);
+          A::turn(cs[t], w, fx, fy);
+#pragma unroll
+          for (int e = 0; e < VE; ++e) {
+            x[t].e[e] = from_f32<T>(state[t] == 2 ? __int_as_float(0x7fc00000) : fx[e]);
+            if constexpr (!IL) y[t].e[e] = from_f32<T>(state[t] == 2 ? __int_as_float(0x7fc00000) : fy[e]);
+          }
+        }
+        vec_store<T, VE>(to, x[t]);
+        if constexpr (!IL) vec_store<T, VE>(to + D / 2, y[t]);
+      }
+      it += step;
+    }
+    return;
+  }
+  // ========================= K or V =============================================
+  const int part = (int)blockIdx.x % wa.kv_parts, first_row = (int)blockIdx.x / wa.kv_parts * a.group;
+  const int end_row = min(first_row + a.group, b.num_rows);
+  const bool is_k = part < wa.kv_parts / 2;
+  const int g = (is_k ? part : part - wa.kv_parts / 2) * kWHeads + (warp >> 1);  // this warp's kv head
+  const int first_tok = (warp & 1) * kWRows;                                     // and rows of a block
+  const bool works = g < a.Hkv;
+  const long long stride = is_k ? a.k_stride : a.v_stride;
+  const T *rows = static_cast<const T *>(is_k ? a.k : a.v) + (works ? g * D : 0) + first_tok * stride;
+  // this lane's units: K's are unit lane % PV of rows lane / PV + 32 / PV u, V's vector lane %
+  // (D / VE) of rows lane / (D / VE) + ... (a pair of vectors half a head apart is two of f)
+  constexpr int kOfRow = D / VE;
+  const int kw = lane % PV, kt = lane / PV, vw = lane % kOfRow, vt = lane / kOfRow;
+  float f[UV][VE];
+  auto load = [&](const T *src, int n) {  // n rows of this warp's at most
+    if (is_k) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int tok = kt + 32 / PV * u;
+        if (tok >= n) continue;
+        const T *at = src + tok * stride + kw * VE;
+        to_floats<T, VE>(vec_load<T, VE>(at), f[u]);
+        if constexpr (!IL) to_floats<T, VE>(vec_load<T, VE>(at + D / 2), f[U + u]);
+      }
+    } else {
+#pragma unroll
+      for (int u = 0; u < UV; ++u) {
+        const int tok = vt + 32 / kOfRow * u;
+        if (tok < n) to_floats<T, VE>(vec_load<T, VE>(src + tok * stride + vw * VE), f[u]);
+      }
+    }
+  };
+  if (works && a.group == 1) load(rows + (long long)first_row * stride, 1 - first_tok);  // (usually all of it)
+  constexpr int kServe = kWThreads / (D / 2);  // tokens whose angles are made at a time
+  const int jf = tid % (D / 2), tf = tid / (D / 2);
+  const unsigned long long turns = is_k && jf < half ? turns_of(a.inv_freq[jf]) : 0ull;
+  allow_dependent_launch();
+  PagedSeq s{0, 0, 0, KVS_OK};
+  int i = -1;
+  for (int row = first_row; row < end_row;) {  // (the same for every thread)
+    if (i < 0 || row >= s.row0 + s.n) {
+      i = warp_find_seq(b, row, lane, s);
+      if (i >= b.M) return;  // rows behind the last sequence
+    }
+    if (s.err != KVS_OK || row < s.row0 || row >= s.row0 + s.n) {
+      i = -1;
+      ++row;
+      continue;
+    }
+    const int t0 = row - s.row0;
+    const int pos = s.p + t0, in = pos & (kScaleBlock - 1);
+    if (t0 > 0 && in != 0) {  // an earlier row begins this block
+      row += min(kScaleBlock - in, s.n - t0);
+      continue;
+    }
+    const int ntok = min(kScaleBlock - in, s.n - t0), mine = ntok - first_tok;
+    const int page = __ldca(b.page_table + (size_t)i * b.max_pages + (pos >> b.page_shift));
+    if (works && (a.group != 1 || ntok > 1)) load(rows + (long long)row * stride, mine);
+    const bool bad_page = (unsigned)page >= (unsigned)b.num_pages;
+    if (bad_page && tid == 0 && part == 0) record_status(d_status, KVS_ERR_PAGE);
+    const int slot = pos & ((1 << b.page_shift) - 1);
+    const size_t head = (size_t)(bad_page ? 0 : page) * a.Hkv + g;
+    float *scale_at = (is_k ? a.k_scales : a.v_scales) + (head << (b.page_shift - 4)) + (slot >> 4);
+    const float old = in > 0 && works && !bad_page ? __ldcg(scale_at) : 0.f;
+    __syncthreads();  // the tables of the block before have been read
+    if (is_k && jf < half)
+      for (int t = tf; t < ntok; t += kServe)
+        *reinterpret_cast<float2 *>(&cs[t][A::at(jf)]) = angle_of(turns, pos + t, a.scale);
+    if (is_k) __syncthreads();
+    row += ntok;
+    float most = 0.f;
+    if (works && is_k) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int tok = kt + 32 / PV * u;
+        if (tok >= mine) continue;
+        if (kw < nturn) A::turn(cs[first_tok + tok], kw, f[u], f[IL ? u : U + u]);
+#pragma unroll
+        for (int e = 0; e < VE; ++e) {
+          most = fmaxf(most, fabsf(f[u][e]));
+          if constexpr (!IL) most = fmaxf(most, fabsf(f[U + u][e]));
+        }
+      }
+    } else if (works) {
+#pragma unroll
+      for (int u = 0; u < UV; ++u)
+        if (vt + 32 / kOfRow * u < mine)
+#pragma unroll
+          for (int e = 0; e < VE; ++e) most = fmaxf(most, fabsf(f[u][e]));
+    }
+    // (sizes are ordered as integers; a NaN was passed over)
+    const unsigned top = __reduce_max_sync(0xffffffffu, __float_as_uint(most));
+    if (lane == 0) s_most[warp] = __uint_as_float(top);
+    __syncthreads();
+    if (!works || bad_page) continue;
+    uint8_t *block = (is_k ? a.k_pages : a.v_pages) + ((head << b.page_shift) + (slot - in)) * D;
+    float scale = scale_for(fmaxf(s_most[warp & ~1], s_most[warp | 1]));
+    if (in > 0 && old >= scale) {
+      scale = old;
+    } else {
+      if (in > 0) requantise(reinterpret_cast<unsigned *>(block), in * D / 4, lane + 32 * (warp & 1), 64, old / scale);
+      if (lane == 0 && first_tok == 0) *scale_at = scale;
+    }
+    const float inv = 1.f / scale;
+    uint8_t *to = block + (in + first_tok) * D;
+    if (is_k) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int tok = kt + 32 / PV * u;
+        if (tok >= mine) continue;
+        store_e4m3<VE>(to + tok * D + kw * VE, f[u], inv);
+        if constexpr (!IL) store_e4m3<VE>(to + tok * D + kw * VE + D / 2, f[U + u], inv);
+      }
+    } else {
+#pragma unroll
+      for (int u = 0; u < UV; ++u) {
+        const int tok = vt + 32 / kOfRow * u;
+        if (tok < mine) store_e4m3<VE>(to + tok * D + vw * VE, f[u], inv);
+      }
+    }
+  }
+}
+
+template <typename T, bool IL, int D>
+int launch_whole(const RopeQ8Args &r, const PagedArgs &b, int *d_status, cudaStream_t stream) {
+  const int sms = device_sm_count();
+  if (sms <= 0) return KVS_ERR_LAUNCH;
+  WholeArgs a{r, 0, 0, 0, 0};
+  // Few rows: a thread block a row (those that do not begin a block of 16 leave at
+  // once); else 16 rows, which begin one block of a prompt.
+  const bool few = b.num_rows <= 4 * sms;
+  a.r.group = few ? 1 : kScaleBlock;
+  a.kv_parts = 2 * ((r.Hkv + kWHeads - 1) / kWHeads);
+  const long long kv = (long long)((b.num_rows + a.r.group - 1) / a.r.group) * a.kv_parts;
+  a.q_tokens = few ? 1 : kWTokens;
+  const long long groups = (b.num_rows + a.q_tokens - 1) / a.q_tokens;
+  // a row of q is split until every SM has a block or a thread one unit left
+  const int units = r.H * (IL ? D : D / 2) / (16 / (int)sizeof(T));
+  const long long most = (units + kWThreads - 1) / kWThreads, want = (2 * sms + groups - 1) / groups;
+  a.q_parts = (int)(want < 1 ? 1 : want < most ? want : most);
+  if (kv + groups * a.q_parts > 0x7fffffffll) return KVS_ERR_UNSUPPORTED;
+  a.kv_blocks = (int)kv;
+  const cudaError_t e = launch_pdl(rope_q8_whole_kernel<T, IL, D>, dim3((unsigned)(kv + groups * a.q_parts)),
+                                   dim3(kWThreads), 0, stream, a, b, d_status);
+  return e == cudaSuccess ? KVS_OK : KVS_ERR_LAUNCH;
+}
+
+// ---- any head ----------------------------------------------------------------------
 template <typename T, int VE, bool IL>
 int launch_rope(RopeQ8Args a, const PagedArgs &b, int *d_status, cudaStream_t stream) {
   const int sms = device_sm_count();
@@ -252,9 +549,13 @@ int dispatch_rope(const RopeQ8Args &a, const PagedArgs &b, int interleaved, int 
                   cudaStream_t stream) {
   constexpr int kMost = 16 / sizeof(T);
   const int n = interleaved ? a.rot : a.rot / 2;
-  if (n % kMost == 0)
-    return interleaved ? launch_rope<T, kMost, true>(a, b, d_status, stream)
-                       : launch_rope<T, kMost, false>(a, b, d_status, stream);
+  if (interleaved && n % kMost == 0)
+    return a.D == 64 ? launch_whole<T, true, 64>(a, b, d_status, stream)
+                     : launch_whole<T, true, 128>(a, b, d_status, stream);
+  if (a.rot == a.D)
+    return a.D == 64 ? launch_whole<T, false, 64>(a, b, d_status, stream)
+                     : launch_whole<T, false, 128>(a, b, d_status, stream);
+  if (n % kMost == 0) return launch_rope<T, kMost, false>(a, b, d_status, stream);
   if (kMost == 8 && n % 4 == 0)
     return interleaved ? launch_rope<T, 4, true>(a, b, d_status, stream)
                        : launch_rope<T, 4, false>(a, b, d_status, stream);
