@@ -30,9 +30,10 @@ namespace kvs {
 
 namespace {
 
-constexpr int kDW = 4;     // rings: consumer and producer warps
 constexpr int kDRows = 16; // rows of a unit
-constexpr int kDThreads = 2 * kDW * 32;
+// Registers a thread of a block with 8 consumer and 4 producer warps: at launch, and shares.
+constexpr int kLaunchRegs = 168, kConsumerRegs = 208, kProducerRegs = 88;
+static_assert(2 * kConsumerRegs + kProducerRegs == 3 * kLaunchRegs, "what the launch has");
 constexpr int kDMaxDevices = 64;
 
 // Four bytes global -> shared, asynchronously ...
@@ -47,7 +48,9 @@ __device__ __forceinline__ void arrive_when_copied(uint64_t *bar) {
 // What a kernel of this file needs to know of the pages is its policy P: the type
 // T of q and out, the head size D, the bytes kElem of an element of the pages, the
 // warp's rows (WarpRows or a class like it), whether 16 keys share a scale
-// (kScaled), and what a launch passes beside the tensor maps (Extra).
+// (kScaled), the rings of a block where ranges are equal (kRings: as many consumer
+// warps), whether units have 8 rows at most (kOnlyFew), and what a launch passes beside the
+// tensor maps (Extra).
 template <class P, int W_>
 struct DGeo {
   static constexpr int W = W_;                         // rings: consumer and producer warps
@@ -57,20 +60,22 @@ struct DGeo {
   static constexpr int TILE = KT / 16 * GB;            // K (or V) of a stage
   static constexpr int STAGE = 2 * TILE;
   static constexpr int SCALES = P::kScaled ? 2 * KT / 16 * 4 : 0;  // bytes of a stage's scales
-  static constexpr int THREADS = 2 * W * 32;
-  static constexpr int STATE = W * 16 * (D + 4) * 4;  // the consumers' accumulators
-  static constexpr int BUDGET = (W == 4 ? 227 : 113) * 1024 - 2048 - STATE;
+  static constexpr int PW = W > 4 ? W / 2 : W;        // producer warps
+  static constexpr int THREADS = (W + PW) * 32;
+  static constexpr int ROWS = P::kOnlyFew ? 8 : 16;   // of a unit
+  static constexpr int STATE = W * ROWS * (D + 4) * 4;  // the consumers' accumulators
+  static constexpr int BUDGET = (W >= 4 ? 227 : 113) * 1024 - 2048 - STATE;
   static constexpr int S0 = BUDGET / (W * (STAGE + SCALES));
   static constexpr int S = S0 > 8 ? 8 : S0;            // stages of a ring
   static constexpr int OFF_STATE = W * S * STAGE;
-  static constexpr int OFF_ML = OFF_STATE + STATE;     // float2 [W][16]
-  static constexpr int OFF_SCALE = OFF_ML + W * 16 * 8;  // float [W][S][2][KT / 16]
+  static constexpr int OFF_ML = OFF_STATE + STATE;     // float2 [W][ROWS]
+  static constexpr int OFF_SCALE = OFF_ML + W * ROWS * 8;  // float [W][S][2][KT / 16]
   static constexpr int OFF_BAR = OFF_SCALE + W * S * SCALES;
   static constexpr int OFF_BAD = OFF_BAR + (2 * W * S + 1) * 8;  // int [W][S]
   static constexpr int OFF_MISC = OFF_BAD + W * S * 4;           // abort, last
   static constexpr int SMEM = OFF_MISC + 8;
   static_assert(S >= 2, "two stages at least");
-  static_assert(SMEM <= (W == 4 ? 227 : 113) * 1024, "one block per SM must fit");
+  static_assert(SMEM <= (W >= 4 ? 227 : 113) * 1024, "one block per SM must fit");
   // arrivals that fill a stage: the one that expects the copies, and with scales
   // each lane's, made when its part of them has landed
   static constexpr int FULL = P::kScaled ? 33 : 1;
@@ -84,24 +89,26 @@ struct Rings {
   unsigned char *smem;
 };
 
-// Fills a ring with its tiles of [t_lo, t_hi) (tile t goes to ring (t - t_lo) %
-// W); by one warp.  n: tiles put in the ring so far.
+// Fills the rings of producer `part` with their tiles of [t_lo, t_hi) (tile t goes to
+// ring (t - t_lo) % W; a producer has ring `part`, or that and ring part + PW in turn); by
+// one warp.  n: tiles put in each of them so far.
 template <class P, int W, bool kPoll>
-__device__ __forceinline__ bool fill_ring(const Rings &rg, const PagedArgs &pa,
+__device__ __forceinline__ bool fill_rings(const Rings &rg, const PagedArgs &pa,
                                           const typename P::Extra &extra,
-                                          const CUtensorMap *kmap, const CUtensorMap *vmap, int ring,
+                                          const CUtensorMap *kmap, const CUtensorMap *vmap, int part,
                                           int i, int g, int Hkv, int t_lo, int t_hi, int keys,
-                                          uint32_t &n, uint64_t policy, int *d_status) {
+                                          uint32_t (&n)[2], uint64_t policy, int *d_status) {
   using C = DGeo<P, W>;
   constexpr int NP = C::KT / 16;  // 16-row pieces of a tile
   constexpr int AHEAD = 32 / NP;  // tiles whose pages one look-up finds
   const int lane = threadIdx.x & 31;
   const int piece = lane % NP;    // lanes 0..NP-1: K pieces, NP..2NP-1: V pieces
   const int32_t *table = pa.page_table + (size_t)i * pa.max_pages;
-  int page = 0, k = 0;  // lane: the page of piece `piece` of the ring's tile k + lane / NP
-  for (int t = t_lo + ring; t < t_hi; t += W, ++n, ++k) {
+  constexpr int PW = C::PW;
+  int page = 0, k = 0;  // lane: the page of piece `piece` of the producer's tile k + lane / NP
+  for (int t = t_lo + part; t < t_hi; t += PW, ++k) {
     if (k % AHEAD == 0) {
-      const long long r0 = (long long)(t + W * (lane / NP)) * C::KT + 16 * piece;
+      const long long r0 = (long long)(t + PW * (lane / NP)) * C::KT + 16 * piece;
       page = r0 < keys ? __ldca(table + (r0 >> pa.page_shift)) : 0;
     }
     const int pg = __shfl_sync(0xffffffffu, page, (k % AHEAD) * NP + piece);
@@ -109,10 +116,15 @@ __device__ __forceinline__ bool fill_ring(const Rings &rg, const PagedArgs &pa,
     const bool mine = lane < 2 * NP && piece < npieces;
     const bool wrong = mine && (unsigned)pg >= (unsigned)pa.num_pages;
     const unsigned any_bad = __ballot_sync(0xffffffffu, wrong);
-    const int st = ring * C::S + (int)(n % C::S);
+    const int second = PW < W ? k & 1 : 0;
+    const uint32_t nr = second ? n[1]++ : n[0]++;
+    const int st = (part + second * PW) * C::S + (int)(nr % C::S);
     if (!__all_sync(0xffffffffu,
-                    mbar_wait<kPoll>(&rg.empty[st], ((n / C::S) & 1u) ^ 1u, rg.abort)))
+                    mbar_wait<kPoll>(&rg.empty[st], ((nr / C::S) & 1u) ^ 1u, rg.abort))) {
+      if (second) --n[1];
+      else --n[0];
       return false;
+    }
     [[maybe_unused]] float *scales = reinterpret_cast<float *>(rg.smem + C::OFF_SCALE + st * C::SCALES);
     if constexpr (P::kScaled) {  // (groups behind the last key: any scale that is a number)
       if (lane < 2 * NP && !mine) scales[lane] = 1.f;
@@ -187,11 +199,11 @@ __device__ __forceinline__ bool consume_ring(typename P::Rows &w, const Rings &r
                                              int t_lo, int t_hi, int keys, const int (&reach)[2],
                                              float sl2, uint32_t &n, bool &poison) {
   bool ok;
-  if (P::kFewForm && rows <= 8) {
+  if (P::kFewForm && (P::kOnlyFew || rows <= 8)) {
     constexpr bool kFew = P::kFewForm;
     ok = consume_tiles<P, W, kPoll, kFew>(w, rg, ring, t_lo, t_hi, keys, reach, sl2, n, poison);
     w.template finish<kFew>();
-  } else {
+  } else if constexpr (!P::kOnlyFew) {
     ok = consume_tiles<P, W, kPoll, false>(w, rg, ring, t_lo, t_hi, keys, reach, sl2, n, poison);
     w.finish();
   }
@@ -204,6 +216,7 @@ __device__ __forceinline__ void put_state(const typename P::Rows &w, float *acc,
   constexpr int D = P::D;
   const int lane = threadIdx.x & 31;
   w.each([&](int hh, int d, const float(&v)[4]) {
+    if (P::kOnlyFew && hh == 1) return;
     float *p = acc + (lane / 4 + 8 * hh) * (D + 4) + d;
     if constexpr (P::Rows::kEach == 4)
       *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
@@ -212,25 +225,25 @@ __device__ __forceinline__ void put_state(const typename P::Rows &w, float *acc,
   });
   if ((lane & 3) == 0) {
     ml[lane / 4] = make_float2(w.m[0], w.l[0]);
-    ml[lane / 4 + 8] = make_float2(w.m[1], w.l[1]);
+    if (!P::kOnlyFew) ml[lane / 4 + 8] = make_float2(w.m[1], w.l[1]);
   }
 }
 
 // Columns d .. d + 3 of row r joined over the W warps' states.
-template <int D, int W>
+template <int D, int W, int ROWS>
 __device__ __forceinline__ void join_states(const float *acc0, const float2 *ml0, int r, int d,
                                             float4 &acc, float &mx, float &ls) {
   mx = neg_inf_f();
 #pragma unroll
-  for (int k = 0; k < W; ++k) mx = fmaxf(mx, ml0[k * 16 + r].x);
+  for (int k = 0; k < W; ++k) mx = fmaxf(mx, ml0[k * ROWS + r].x);
   const float mz = mx == neg_inf_f() ? 0.f : mx;
   acc = make_float4(0.f, 0.f, 0.f, 0.f);
   ls = 0.f;
 #pragma unroll
   for (int k = 0; k < W; ++k) {
-    const float2 ml = ml0[k * 16 + r];
+    const float2 ml = ml0[k * ROWS + r];
     const float wgt = ex2f(ml.x - mz);
-    const float4 v = *reinterpret_cast<const float4 *>(acc0 + (k * 16 + r) * (D + 4) + d);
+    const float4 v = *reinterpret_cast<const float4 *>(acc0 + (k * ROWS + r) * (D + 4) + d);
     acc.x = fmaf(wgt, v.x, acc.x);
     acc.y = fmaf(wgt, v.y, acc.y);
     acc.z = fmaf(wgt, v.z, acc.z);
@@ -240,7 +253,7 @@ __device__ __forceinline__ void join_states(const float *acc0, const float2 *ml0
 }
 
 template <class P, bool kPoll>
-__global__ void __launch_bounds__(kDThreads, 1)
+__global__ void __launch_bounds__((DGeo<P, P::kRings>::THREADS), 1)
     paged_decode_kernel(const typename P::T *__restrict__ q, long long q_stride,
                         typename P::T *__restrict__ out,
                         long long out_stride, PagedArgs pa,
@@ -250,11 +263,12 @@ __global__ void __launch_bounds__(kDThreads, 1)
                         typename P::Extra extra, int *d_status) {
   using T = typename P::T;
   constexpr int D = P::D;
-  using C = DGeo<P, kDW>;
+  constexpr int W = P::kRings;
+  using C = DGeo<P, W>;
   extern __shared__ __align__(1024) unsigned char smem[];
-  uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);  // [kDW][S]
-  uint64_t *empty = full + kDW * C::S;
-  uint64_t *cbar = empty + kDW * C::S;  // all consumer warps
+  uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);  // [W][S]
+  uint64_t *empty = full + W * C::S;
+  uint64_t *cbar = empty + W * C::S;  // all consumer warps
   volatile int *abort = reinterpret_cast<volatile int *>(smem + C::OFF_MISC);
   volatile int *s_last = abort + 1;
   const Rings rg{full, empty, reinterpret_cast<int *>(smem + C::OFF_BAD), abort, smem};
@@ -268,11 +282,11 @@ __global__ void __launch_bounds__(kDThreads, 1)
   if (threadIdx.x == 0) {
     prefetch_map(&kmap);
     prefetch_map(&vmap);
-    for (int s = 0; s < kDW * C::S; ++s) {
+    for (int s = 0; s < W * C::S; ++s) {
       mbar_init(&full[s], C::FULL);
       mbar_init(&empty[s], 1);
     }
-    mbar_init(cbar, kDW);
+    mbar_init(cbar, W);
     *abort = 0;
     *s_last = 0;
     fence_mbar_init();
@@ -285,7 +299,7 @@ __global__ void __launch_bounds__(kDThreads, 1)
       if (threadIdx.x == 0) record_status(d_status, s.err);
       const T nan = from_f32<T>(__int_as_float(0x7fc00000));
       for (int r = 0; r < s.n; ++r)
-        for (int e = threadIdx.x; e < Hkv * G * D; e += kDThreads)
+        for (int e = threadIdx.x; e < Hkv * G * D; e += C::THREADS)
           out[(long long)(s.row0 + r) * out_stride + e] = nan;
     }
   }
@@ -297,25 +311,31 @@ __global__ void __launch_bounds__(kDThreads, 1)
   const long long x0 = cut.start(b), x1 = cut.start(b + 1);
   Unit u = warp_unit_at(pa, ln, x0, lane);
 
-  if (warp >= kDW) {
-    // ======================= producer of a ring ==============================
+  // With more consumers than producers, warpgroups of both: the producers' registers go to
+  // the consumers (the shares' sum is the launch's, kLaunchRegs for each of three).
+  constexpr bool kShares = C::PW < W;
+  if (warp >= W) {
+    // ======================= producer ========================================
+    if constexpr (kShares) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
     const uint64_t policy = policy_evict_first();  // a row is read once
-    const int ring = warp - kDW;
-    uint32_t n = 0;
+    const int part = warp - W;
+    uint32_t n[2] = {0, 0};
     bool ok = true;
     do {
       const UnitInfo f = unit_info(pa, u, ln, x0, x1);
-      ok = fill_ring<P, kDW, kPoll>(rg, pa, extra, &kmap, &vmap, ring, u.i, u.g, Hkv, f.t_lo, f.t_hi, f.keys,
-                                  n, policy, d_status);
+      ok = fill_rings<P, W, kPoll>(rg, pa, extra, &kmap, &vmap, part, u.i, u.g, Hkv, f.t_lo, f.t_hi,
+                                   f.keys, n, policy, d_status);
       if (!ok) break;
       if (!next_unit(pa, u, f, ln)) break;
     } while (u.base < x1);
     if (lane == 0) {
       if (!ok) give_up(abort, d_status, epoch);
-      drain_ring<P, kDW>(rg, ring, n);
+      drain_ring<P, W>(rg, part, n[0]);
+      if (kShares) drain_ring<P, W>(rg, part + C::PW, n[1]);
     }
     return;
   }
+  if constexpr (kShares) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kConsumerRegs));
 
   // ========================= consumers ======================================
   uint32_t n = 0, cphase = 0;
@@ -344,7 +364,7 @@ __global__ void __launch_bounds__(kDThreads, 1)
       for (int hh = 0; hh < 2; ++hh)
         reach[hh] = f.s.p + f.tok0 + min(lane / 4 + 8 * hh, rows - 1) / G + 1;
       bool poison = false;
-      if (!consume_ring<P, kDW, kPoll>(w, rg, warp, rows, f.t_lo, f.t_hi, f.keys, reach, sl2, n,
+      if (!consume_ring<P, W, kPoll>(w, rg, warp, rows, f.t_lo, f.t_hi, f.keys, reach, sl2, n,
                                          poison)) {
         if (lane == 0) give_up(abort, d_status, epoch);
         return;
@@ -356,15 +376,15 @@ __global__ void __launch_bounds__(kDThreads, 1)
       float *sacc = sl + 2 * kDRows;
       T *orow = out + (long long)(f.s.row0 + f.tok0) * out_stride + (long long)u.g * G * D;
       // the key groups' states merge in shared memory
-      float *macc = reinterpret_cast<float *>(smem + C::OFF_STATE);  // [kDW][16][D + 4]
-      float2 *mml = reinterpret_cast<float2 *>(smem + C::OFF_ML);    // [kDW][16]
-      put_state<P>(w, macc + warp * 16 * (D + 4), mml + warp * 16);
+      float *macc = reinterpret_cast<float *>(smem + C::OFF_STATE);  // [W][ROWS][D + 4]
+      float2 *mml = reinterpret_cast<float2 *>(smem + C::OFF_ML);    // [W][ROWS]
+      put_state<P>(w, macc + warp * C::ROWS * (D + 4), mml + warp * C::ROWS);
       if (!consumers_barrier()) return;
-      for (int e = threadIdx.x; e < rows * (D / 4); e += kDW * 32) {
+      for (int e = threadIdx.x; e < rows * (D / 4); e += W * 32) {
         const int r = e / (D / 4), d = (e - r * (D / 4)) * 4;
         float4 acc;
         float mx, ls;
-        join_states<D, kDW>(macc, mml, r, d, acc, mx, ls);
+        join_states<D, W, C::ROWS>(macc, mml, r, d, acc, mx, ls);
         if (whole) {
           const float inv = 1.f / ls;
           const int tok = r / G;
@@ -391,7 +411,7 @@ __global__ void __launch_bounds__(kDThreads, 1)
         if (!consumers_barrier()) return;
         if (*s_last) {
           __threadfence();
-          for (int e = threadIdx.x; e < rows * (D / 4); e += kDW * 32) {
+          for (int e = threadIdx.x; e < rows * (D / 4); e += W * 32) {
             const int r = e / (D / 4), d = (e - r * (D / 4)) * 4;
             float4 acc;
             float ls;
@@ -447,8 +467,8 @@ __global__ void __launch_bounds__(2 * W * 32, 4 / W)
   uint64_t *cbar = empty + W * C::S;  // all consumer warps
   volatile int *abort = reinterpret_cast<volatile int *>(smem + C::OFF_MISC);
   const Rings rg{full, empty, reinterpret_cast<int *>(smem + C::OFF_BAD), abort, smem};
-  float *macc = reinterpret_cast<float *>(smem + C::OFF_STATE);  // [W][16][D + 4]
-  float2 *mml = reinterpret_cast<float2 *>(smem + C::OFF_ML);    // [W][16]
+  float *macc = reinterpret_cast<float *>(smem + C::OFF_STATE);  // [W][ROWS][D + 4]
+  float2 *mml = reinterpret_cast<float2 *>(smem + C::OFF_ML);    // [W][ROWS]
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int cs = (int)gridDim.x, rank = (int)cluster_rank();
@@ -484,14 +504,15 @@ __global__ void __launch_bounds__(2 * W * 32, 4 / W)
   bool ok = true;
   uint32_t n = 0;
   if (warp >= W) {
-    ok = fill_ring<P, W, kPoll>(rg, pa, extra, &kmap, &vmap, warp - W, i, g, Hkv, t_lo, t_hi, keys, n,
-                                policy_evict_first(), d_status);
+    uint32_t nf[2] = {0, 0};
+    ok = fill_rings<P, W, kPoll>(rg, pa, extra, &kmap, &vmap, warp - W, i, g, Hkv, t_lo, t_hi, keys,
+                                 nf, policy_evict_first(), d_status);
     if (lane == 0) {
       if (!ok) {
         *abort = 1;
         record_status(d_status, KVS_ERR_TIMEOUT);
       }
-      drain_ring<P, W>(rg, warp - W, n);
+      drain_ring<P, W>(rg, warp - W, nf[0]);
     }
   } else {
     typename P::Rows w;
@@ -505,7 +526,7 @@ __global__ void __launch_bounds__(2 * W * 32, 4 / W)
     bool poison = false;
     ok = consume_ring<P, W, kPoll>(w, rg, warp, rows, t_lo, t_hi, keys, reach, sl2, n, poison);
     if (poison) w.l[0] = w.l[1] = __int_as_float(0x7fc00000);
-    put_state<P>(w, macc + warp * 16 * (D + 4), mml + warp * 16);
+    put_state<P>(w, macc + warp * C::ROWS * (D + 4), mml + warp * C::ROWS);
     __syncwarp();
     if (lane == 0) mbar_arrive(cbar);
     ok = __all_sync(0xffffffffu, mbar_wait<kPoll>(cbar, 0u, abort)) && ok;
@@ -519,7 +540,7 @@ __global__ void __launch_bounds__(2 * W * 32, 4 / W)
       const int r = e / (D / 4), d = (e - r * (D / 4)) * 4;
       float4 acc;
       float mx, ls;
-      join_states<D, W>(macc, mml, r, d, acc, mx, ls);
+      join_states<D, W, C::ROWS>(macc, mml, r, d, acc, mx, ls);
       *reinterpret_cast<float4 *>(macc + r * (D + 4) + d) = acc;
       if (d == 0) *reinterpret_cast<float2 *>(smem + r * 8) = make_float2(mx, ls);
     }
@@ -656,7 +677,7 @@ int launch_decode(const void *q, long long q_stride, const CUtensorMap &kmap,
                   int *d_status, cudaStream_t stream) {
   using T = typename P::T;
   constexpr int D = P::D;
-  using C = DGeo<P, kDW>;
+  using C = DGeo<P, P::kRings>;
   static bool configured[kDMaxDevices] = {false};
   static std::mutex mu;
   int dev = 0;
@@ -667,6 +688,12 @@ int launch_decode(const void *q, long long q_stride, const CUtensorMap &kmap,
     if (!configured[dev]) {
       for (auto kern : {paged_decode_kernel<P, false>,
                         paged_decode_kernel<P, true>}) {
+        // (with fewer registers at launch the warpgroups' shares would never come together)
+        cudaFuncAttributes fa;
+        if (C::PW < C::W && (cudaFuncGetAttributes(&fa, kern) != cudaSuccess || fa.numRegs != kLaunchRegs)) {
+          cudaGetLastError();
+          return KVS_ERR_LAUNCH;
+        }
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) !=
             cudaSuccess) {
           cudaGetLastError();
@@ -688,10 +715,10 @@ int launch_decode(const void *q, long long q_stride, const CUtensorMap &kmap,
   // lengths differ.
   const long long units = (long long)pa.M * Hkv;
   const long long unit_bytes = ((long long)pa.max_pages << pa.page_shift) * D * 2 * P::kElem;
-  const ClusterInfo *ci = cluster_info<P, kDW>(dev);
+  const ClusterInfo *ci = cluster_info<P, 4>(dev);
   if (!ci) return KVS_ERR_LAUNCH;
   int k = 4;  // clusters of 2^k blocks: all resident at once, no block without a tile
-  while (k > 0 && (units > ci->active[k - 1] || unit_bytes < (long long)C::STAGE << k)) --k;
+  while (k > 0 && (units > ci->active[k - 1] || unit_bytes < (long long)DGeo<P, 4>::STAGE << k)) --k;
   // (a unit of the clusters has all of a sequence's rows)
   const bool one_tile = (long long)pa.max_new * (H / Hkv) <= kDRows;
   if (one_tile && units <= 65535 && unit_bytes <= P::kBlockBytes << k) {
@@ -700,13 +727,13 @@ int launch_decode(const void *q, long long q_stride, const CUtensorMap &kmap,
       return launch_clusters<P, 2>(1, q, q_stride, pa, out, out_stride, H / Hkv, Hkv, sl2, kmap,
                                       vmap, extra, d_status, stream);
     }
-    return launch_clusters<P, kDW>(1u << k, q, q_stride, pa, out, out_stride, H / Hkv, Hkv, sl2,
+    return launch_clusters<P, 4>(1u << k, q, q_stride, pa, out, out_stride, H / Hkv, Hkv, sl2,
                                       kmap, vmap, extra, d_status, stream);
   }
   const cudaError_t e = launch_pdl(
       poll_waits() ? paged_decode_kernel<P, true>
                    : paged_decode_kernel<P, false>,
-      dim3(grid), dim3(kDThreads), C::SMEM, stream, static_cast<const T *>(q), q_stride,
+      dim3(grid), dim3(C::THREADS), C::SMEM, stream, static_cast<const T *>(q), q_stride,
       static_cast<T *>(out), out_stride, pa, kmap, vmap, H / Hkv, Hkv, sl2, min_column,
       static_cast<unsigned char *>(workspace), fresh_tag(), extra, d_status);
   return e == cudaSuccess ? KVS_OK : KVS_ERR_LAUNCH;

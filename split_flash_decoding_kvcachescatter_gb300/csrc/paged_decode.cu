@@ -29,7 +29,8 @@ struct PlainPages {
   using T = Type;
   using Rows = WarpRows<T, D_>;
   static constexpr int D = D_, kElem = sizeof(T);
-  static constexpr bool kScaled = false;
+  static constexpr int kRings = 4;
+  static constexpr bool kScaled = false, kOnlyFew = false;
   static constexpr bool kFewForm = !std::is_same<T, float>::value;  // units of 8 rows have a form
   struct Extra {};
   // A unit's fixed price (its start, the joining of its four states, its output)

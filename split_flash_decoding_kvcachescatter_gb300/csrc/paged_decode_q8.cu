@@ -8,13 +8,15 @@ namespace kvs {
 
 namespace {
 
-// Pages in 8 bits under q and out of Type (kvs_decode.cuh).
-template <typename Type, int D_>
+// Pages in 8 bits under q and out of Type (kvs_decode.cuh); kFew: units of 8 rows at most,
+// for which 16-bit rows leave registers for eight consumer warps a block.
+template <typename Type, int D_, bool kFew>
 struct PagesQ8 {
   using T = Type;
   using Rows = RowsQ8<T, D_>;
   static constexpr int D = D_, kElem = 1;
-  static constexpr bool kScaled = true;
+  static constexpr int kRings = kFew && sizeof(T) == 2 ? 8 : 4;
+  static constexpr bool kScaled = true, kOnlyFew = kFew;
   static constexpr bool kFewForm = true;
   struct Extra {
     const float *k_scales, *v_scales;
@@ -44,9 +46,13 @@ int launch_q8(const void *q, long long q_stride, const kvs_paged_cache_q8 &cache
   int rc = make_line_map(&kmap, cache.k_pages, rows * D / 128, 16 * D / 128);
   if (rc == KVS_OK) rc = make_line_map(&vmap, cache.v_pages, rows * D / 128, 16 * D / 128);
   if (rc != KVS_OK) return rc;
-  return launch_decode<PagesQ8<T, D>>(q, q_stride, kmap, vmap, {cache.k_scales, cache.v_scales},
-                                      cache.num_kv_heads, pa, out, out_stride, H, workspace,
-                                      d_status, stream);
+  if ((long long)pa.max_new * (H / cache.num_kv_heads) <= 8)
+    return launch_decode<PagesQ8<T, D, true>>(q, q_stride, kmap, vmap, {cache.k_scales, cache.v_scales},
+                                              cache.num_kv_heads, pa, out, out_stride, H, workspace,
+                                              d_status, stream);
+  return launch_decode<PagesQ8<T, D, false>>(q, q_stride, kmap, vmap, {cache.k_scales, cache.v_scales},
+                                             cache.num_kv_heads, pa, out, out_stride, H, workspace,
+                                             d_status, stream);
 }
 
 }  // namespace
