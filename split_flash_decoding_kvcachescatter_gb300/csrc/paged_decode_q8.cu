@@ -21,7 +21,9 @@ struct PagesQ8 {
   struct Extra {
     const float *k_scales, *v_scales;
   };
-  static constexpr int kFixBytes = 96 << 10;
+  // as PlainPages'; 32 sequences of up to 8192 keys in bfloat16 took 66.3 us at 96 KB, 58.3 at 192,
+  // 60.6 at 384, 65.6 at 768
+  static constexpr int kFixBytes = 192 << 10;
   static constexpr long long kBlockBytes = 512 << 10;
   static constexpr long long kShortBytes = 128 << 10;
   // the line of 128 bytes that row `row` of the pages begins in
