@@ -112,34 +112,22 @@ __device__ __forceinline__ void write_rows64(const unsigned char *stg, int lane,
   __syncwarp();
 }
 
-// The way out in steps of 32 columns; kWide: 4 KB of shared memory a warp, as above,
-// else 1 KB (16 columns at a time, 32 bytes a row).
-template <typename T, bool kWide>
+// The way out in steps of 32 columns: through 4 KB of shared memory a warp, as above
+// (kStaged), or, where that is taken, by each thread into its own row.
+template <typename T, bool kStaged>
 __device__ __forceinline__ void put_columns(unsigned char *stg, int lane, T *out, long long at,
                                             int c32, const float (&o)[32], float inv) {
-  if constexpr (kWide) {
+  if constexpr (kStaged) {
     put_row32<T>(stg, lane, c32 & 1, o, inv);
     if (c32 & 1) write_rows64(stg, lane, out, at, (c32 - 1) * 32);
-  } else {
+  } else if (at >= 0) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-#pragma unroll
-      for (int v = 0; v < 2; ++v)  // (pieces swapped in every other four rows: no access conflicts)
-        *reinterpret_cast<uint4 *>(stg + lane * 32 + ((v ^ (lane >> 2)) & 1) * 16) =
-            make_uint4(pack_pair<T>(o[16 * h + 8 * v] * inv, o[16 * h + 8 * v + 1] * inv),
-                       pack_pair<T>(o[16 * h + 8 * v + 2] * inv, o[16 * h + 8 * v + 3] * inv),
-                       pack_pair<T>(o[16 * h + 8 * v + 4] * inv, o[16 * h + 8 * v + 5] * inv),
-                       pack_pair<T>(o[16 * h + 8 * v + 6] * inv, o[16 * h + 8 * v + 7] * inv));
-      __syncwarp();
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int r = 16 * k + lane / 2;
-        const long long to = __shfl_sync(0xffffffffu, at, r);
-        const uint4 v = *reinterpret_cast<const uint4 *>(stg + r * 32 + ((lane ^ (r >> 2)) & 1) * 16);
-        if (to >= 0) *reinterpret_cast<uint4 *>(out + to + c32 * 32 + h * 16 + (lane & 1) * 8) = v;
-      }
-      __syncwarp();
-    }
+    for (int v = 0; v < 4; ++v)
+      *reinterpret_cast<uint4 *>(out + at + c32 * 32 + 8 * v) =
+          make_uint4(pack_pair<T>(o[8 * v] * inv, o[8 * v + 1] * inv),
+                     pack_pair<T>(o[8 * v + 2] * inv, o[8 * v + 3] * inv),
+                     pack_pair<T>(o[8 * v + 4] * inv, o[8 * v + 5] * inv),
+                     pack_pair<T>(o[8 * v + 6] * inv, o[8 * v + 7] * inv));
   }
 }
 
@@ -177,7 +165,7 @@ struct CTile {
 // joined with theirs by the block that completes it.  By the tile's four warps
 // (thread t has row t: live, token tok of the tile, running maximum m and sum l,
 // accumulators at tm_o); false when a wait ran out.
-template <typename T, int D, bool kWide, class Barrier>
+template <typename T, int D, bool kStaged, class Barrier>
 __device__ __forceinline__ bool finish_tile(T *out, long long out_stride, const volatile CUnit *ud,
                                             const CTile &tl, int x, int t, int lane, bool live,
                                             int tok, int G, int b, uint32_t tm_o, float m, float l,
@@ -199,8 +187,8 @@ __device__ __forceinline__ bool finish_tile(T *out, long long out_stride, const 
       tmem_ld32(tm_o + ch * 64, o[0]);
       tmem_ld32(tm_o + ch * 64 + 32, o[1]);
       tmem_wait_ld();
-      put_columns<T, kWide>(stg, lane, out, at, 2 * ch, o[0], inv);
-      put_columns<T, kWide>(stg, lane, out, at, 2 * ch + 1, o[1], inv);
+      put_columns<T, kStaged>(stg, lane, out, at, 2 * ch, o[0], inv);
+      put_columns<T, kStaged>(stg, lane, out, at, 2 * ch + 1, o[1], inv);
     }
   } else {
     // the blocks of tile x's first and last key tile, and their partials
@@ -241,7 +229,7 @@ __device__ __forceinline__ bool finish_tile(T *out, long long out_stride, const 
               const float other = v % 4 == 0 ? qq.x : v % 4 == 1 ? qq.y : v % 4 == 2 ? qq.z : qq.w;
               o[v] = b == pc.b1 ? fmaf(wo, other, ww * o[v]) : fmaf(ww, o[v], wo * other);
             }
-            put_columns<T, kWide>(stg, lane, out, at, 2 * ch + hc, o, inv);
+            put_columns<T, kStaged>(stg, lane, out, at, 2 * ch + hc, o, inv);
           }
         }
       } else {
@@ -280,7 +268,7 @@ __device__ __forceinline__ bool finish_tile(T *out, long long out_stride, const 
             }
           }
         }
-        put_columns<T, kWide>(stg, lane, out, at, ch, acc, inv);
+        put_columns<T, kStaged>(stg, lane, out, at, ch, acc, inv);
       }
       }
     } else {
@@ -330,7 +318,7 @@ __device__ __forceinline__ bool finish_tile(T *out, long long out_stride, const 
               acc[4 * v + 3] = fmaf(w, q.w, acc[4 * v + 3]);
             }
           }
-          put_columns<T, kWide>(stg, lane, out, at, ch, acc, inv);
+          put_columns<T, kStaged>(stg, lane, out, at, ch, acc, inv);
         }
       }
     }

@@ -19,10 +19,20 @@
 //   warp 8, 9       issue S_x = Q_x K^T and O_x += P_x V, as in paged_chunk.cu
 //   warp 10, 11     walks the units and describes each to the others; copies Q
 //   warps 12-15, 16-19  K and V: each thread copies the pieces that it will turn, 32
-//                   keys at a time and three of those ahead, and writes them as float16
+//                   keys at a time and a tile ahead, and writes them as float16
 //                   in the layout that the tensor cores read; the tiles' scales; the
 //                   latter warps also turn bfloat16 queries, in place
 // TMEM as in paged_chunk.cu.
+//
+// What bounds it: the turning.  A pair of tiles moves about 320 KB through shared
+// memory (pages in and out, float16 in, and what the products read), the pages come
+// from L2 with as many bytes on their way as the rings hold, and eight warps convert.
+// 8192 rows of 32 query heads on 8 kv heads of 128 behind 8192 keys: 340 us, where
+// paged_chunk.cu takes about 255 for pages in 16 bits.
+// Measured at that shape: rings of a whole tile and rows that leave without a staging
+// area 340 us, 8 KB of staging and three quarters 402; two quarters a step 487; a
+// warp that copies for the turning ones 566 to 646; pages read straight into
+// registers 701; mma.sync units as the decode steps' 2966.
 
 #include <cmath>
 #include <mutex>
@@ -60,13 +70,12 @@ struct CqGeo {
   static constexpr int KS = 2, VS = 2;            // stages (the turning warps count on two)
   static constexpr int QK = kCN / 4;              // keys of a quarter, as they come from the pages
   static constexpr int QUARTER = QK * D;          // its bytes
-  static constexpr int RQ = 3;                    // quarters in a ring
+  static constexpr int RQ = 4;                    // quarters in a ring: a tile
   static constexpr int SR = 8;                    // tiles whose scales are kept
   static constexpr int OFF_Q = 0;                 // Q_A, Q_B
   static constexpr int OFF_K = 2 * TILE;
   static constexpr int OFF_V = OFF_K + KS * TILE;
-  static constexpr int OFF_STAGE = OFF_V + VS * TILE;  // 1 KB a softmax warp: rows on their way out
-  static constexpr int OFF_RAW = OFF_STAGE + 8 * 1024;
+  static constexpr int OFF_RAW = OFF_V + VS * TILE;
   // exponents of the rows' factors (biased), by unit parity: uint8 [2][2][128]
   static constexpr int OFF_QFAC = OFF_RAW + 2 * RQ * QUARTER;
   static constexpr int OFF_SCALE = OFF_QFAC + 2 * 2 * 128;  // CqScales [SR]
@@ -204,7 +213,6 @@ __global__ void __launch_bounds__(kCqThreads, 1)
     const uint32_t tm_s = tmem + lane_base;
     const uint32_t tm_p = tmem + lane_base + kCN + x * (kCN / 2);
     const uint32_t tm_o = tmem + lane_base + 2 * kCN + x * D;
-    unsigned char *stg = smem + C::OFF_STAGE + warp * 1024;
     int sb = 0;   // S_x products of the earlier units
     int kt0 = 0;  // key tiles of the earlier units
     uint32_t wphase = 0;
@@ -334,7 +342,7 @@ __global__ void __launch_bounds__(kCqThreads, 1)
         tc_fence_after();
         // (the unit is read again there: in registers it would crowd out the row)
         if (!finish_tile<T, D, false>(out, out_stride, &units[nq % kCUnits], tl, x, t, lane, live, tok, G, b,
-                               tm_o, m, l, stg, slots, counters, tag, epoch, d_status, s_last,
+                               tm_o, m, l, nullptr, slots, counters, tag, epoch, d_status, s_last,
                                wg_barrier)) {
           failed = true;
           break;
@@ -579,11 +587,11 @@ __global__ void __launch_bounds__(kCqThreads, 1)
       a.row = ((a.row * Hkv + units[uq % kCUnits].g) << pa.page_shift) + (key & ((1 << pa.page_shift) - 1));
       a.scale = 16 * (lane & 7) < a.left ? __ldcg(page_scales + (a.row >> 4)) : 0.f;
     };
-    // Quarter q of tile a into place s of the ring, rows behind the last key as zeros.
-    auto copy = [&](const Tile &a, int q, int s) {
+    // Quarter q of tile a into the ring, rows behind the last key as zeros.
+    auto copy = [&](const Tile &a, int q) {
       const int row = __shfl_sync(0xffffffffu, a.row, 2 * q + half) + (row0 & 15);
       const unsigned char *from = pages + (size_t)row * D + c * 16;
-      unsigned char *to = raw + s * C::QUARTER;
+      unsigned char *to = raw + q * C::QUARTER;
       if (a.left >= kCN) {
 #pragma unroll
         for (int k = 0; k < NV; ++k)
@@ -603,12 +611,12 @@ __global__ void __launch_bounds__(kCqThreads, 1)
     Tile a{}, b2{}, b3{};  // a tile under way, the next one (resolved a tile ahead) and the one after (asked for)
     bool have = next(a);
     if (have) resolve(a);
-    for (int q = 0; q < 3; ++q) {
-      if (have) copy(a, q, q);
+    for (int q = 0; q < 4; ++q) {
+      if (have) copy(a, q);
       commit();
     }
     bool more = have && next(b2);
-    int done = 0, s = 0;  // tiles written; place of the next quarter in the ring
+    int done = 0;  // tiles written
     while (have && ok) {
       // the tile's scale, the largest of its blocks', and what each is of that
       float most = a.scale;
@@ -673,15 +681,11 @@ __global__ void __launch_bounds__(kCqThreads, 1)
       unsigned char *tile = smem + (is_v ? C::OFF_V : C::OFF_K) + st * C::TILE + to0;
 #pragma unroll 1
       for (int q = 0; q < 4; ++q) {
-        asm volatile("cp.async.wait_group 2;" ::: "memory");  // this thread's pieces of the quarter
+        asm volatile("cp.async.wait_group 3;" ::: "memory");  // this thread's pieces of the quarter
         uint4 v[NV];
 #pragma unroll
-        for (int k = 0; k < NV; ++k) v[k] = *reinterpret_cast<const uint4 *>(raw + s * C::QUARTER + k * pair);
-        // the quarter three further on takes its place
-        if (q == 0)
-          copy(a, 3, s);
-        else if (more)
-          copy(b2, q - 1, s);
+        for (int k = 0; k < NV; ++k) v[k] = *reinterpret_cast<const uint4 *>(raw + q * C::QUARTER + k * pair);
+        if (more) copy(b2, q);  // the next tile's takes its place
         commit();
         const uint32_t m2 = __shfl_sync(0xffffffffu, by, 2 * q + half);
 #pragma unroll
@@ -694,7 +698,6 @@ __global__ void __launch_bounds__(kCqThreads, 1)
           *reinterpret_cast<uint4 *>(k ? at : at + x) =
               make_uint4(turned(v[k].z, m2), turned(v[k].z >> 16, m2), turned(v[k].w, m2), turned(v[k].w >> 16, m2));
         }
-        s = s == 2 ? 0 : s + 1;
       }
       fence_proxy_async_shared();
       __syncwarp();
