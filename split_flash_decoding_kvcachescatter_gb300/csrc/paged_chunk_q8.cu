@@ -27,10 +27,10 @@
 // What bounds it: the turning.  A pair of tiles moves about 320 KB through shared
 // memory (pages in and out, float16 in, and what the products read), the pages come
 // from L2 with as many bytes on their way as the rings hold, and eight warps convert.
-// 8192 rows of 32 query heads on 8 kv heads of 128 behind 8192 keys: 340 us, where
+// 8192 rows of 32 query heads on 8 kv heads of 128 behind 8192 keys: 343 us, where
 // paged_chunk.cu takes about 255 for pages in 16 bits.
 // Measured at that shape: rings of a whole tile and rows that leave without a staging
-// area 340 us, 8 KB of staging and three quarters 402; two quarters a step 487; a
+// area 343 us, 8 KB of staging and three quarters 402; two quarters a step 487; a
 // warp that copies for the turning ones 566 to 646; pages read straight into
 // registers 701; mma.sync units as the decode steps' 2966.
 
@@ -588,9 +588,11 @@ __global__ void __launch_bounds__(kCqThreads, 1)
       a.scale = 16 * (lane & 7) < a.left ? __ldcg(page_scales + (a.row >> 4)) : 0.f;
     };
     // Quarter q of tile a into the ring, rows behind the last key as zeros.
-    auto copy = [&](const Tile &a, int q) {
+    auto source = [&](const Tile &a, int q) {
       const int row = __shfl_sync(0xffffffffu, a.row, 2 * q + half) + (row0 & 15);
-      const unsigned char *from = pages + (size_t)row * D + c * 16;
+      return pages + (size_t)row * D + c * 16;
+    };
+    auto copy = [&](const Tile &a, int q, const unsigned char *from) {
       unsigned char *to = raw + q * C::QUARTER;
       if (a.left >= kCN) {
 #pragma unroll
@@ -612,7 +614,7 @@ __global__ void __launch_bounds__(kCqThreads, 1)
     bool have = next(a);
     if (have) resolve(a);
     for (int q = 0; q < 4; ++q) {
-      if (have) copy(a, q);
+      if (have) copy(a, q, source(a, q));
       commit();
     }
     bool more = have && next(b2);
@@ -685,8 +687,7 @@ __global__ void __launch_bounds__(kCqThreads, 1)
         uint4 v[NV];
 #pragma unroll
         for (int k = 0; k < NV; ++k) v[k] = *reinterpret_cast<const uint4 *>(raw + q * C::QUARTER + k * pair);
-        if (more) copy(b2, q);  // the next tile's takes its place
-        commit();
+        const unsigned char *from = source(b2, q);
         const uint32_t m2 = __shfl_sync(0xffffffffu, by, 2 * q + half);
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
@@ -698,6 +699,9 @@ __global__ void __launch_bounds__(kCqThreads, 1)
           *reinterpret_cast<uint4 *>(k ? at : at + x) =
               make_uint4(turned(v[k].z, m2), turned(v[k].z >> 16, m2), turned(v[k].w, m2), turned(v[k].w >> 16, m2));
         }
+        // the next tile's takes its place (here: what was read has arrived in registers)
+        if (more) copy(b2, q, from);
+        commit();
       }
       fence_proxy_async_shared();
       __syncwarp();
