@@ -18,6 +18,10 @@
 // the look-ups (sequence, page, old scale) that decide where the results go.
 // The other kernel, for any head: a warp a head of a 16-position block at a time, the rows
 // of K and V read twice.
+// Measured (32 query heads on 8 kv heads of 128, bfloat16): 8192 rows of prompts 41 us, 66% of
+// what a copy of the same bytes takes; by the other kernel 82; 16 rows a warp 64, eight of them
+// with q's angles made by every warp 72 to 78.  A decode step of 32 tokens: 3.2 us, a launch
+// and four dependent reads.
 
 #include <type_traits>
 
@@ -511,9 +515,9 @@ int launch_whole(const RopeQ8Args &r, const PagedArgs &b, int *d_status, cudaStr
   const bool few = b.num_rows <= 4 * sms;
   a.r.group = few ? 1 : kScaleBlock;
   a.kv_parts = 2 * ((r.Hkv + kWHeads - 1) / kWHeads);
-  const long long kv = (long long)((b.num_rows + a.r.group - 1) / a.r.group) * a.kv_parts;
+  const long long kv = ((long long)b.num_rows + a.r.group - 1) / a.r.group * a.kv_parts;
   a.q_tokens = few ? 1 : kWTokens;
-  const long long groups = (b.num_rows + a.q_tokens - 1) / a.q_tokens;
+  const long long groups = ((long long)b.num_rows + a.q_tokens - 1) / a.q_tokens;
   // a row of q is split until every SM has a block or a thread one unit left
   const int units = r.H * (IL ? D : D / 2) / (16 / (int)sizeof(T));
   const long long most = (units + kWThreads - 1) / kWThreads, want = (2 * sms + groups - 1) / groups;
@@ -533,7 +537,7 @@ int launch_rope(RopeQ8Args a, const PagedArgs &b, int *d_status, cudaStream_t st
   // Few rows: a thread block a row (those that do not begin a block of 16 leave at
   // once); else 16 rows, which begin one block of a prompt.
   a.group = b.num_rows <= 4 * sms ? 1 : kScaleBlock;
-  const int groups = (b.num_rows + a.group - 1) / a.group;
+  const int groups = (int)(((long long)b.num_rows + a.group - 1) / a.group);
   const int most = (a.H + 2 * a.Hkv + kRqThreads / 32 - 1) / (kRqThreads / 32);
   const int want = (8 * sms + groups - 1) / groups;
   const int slices = want < 1 ? 1 : want < most ? want : most;
@@ -549,7 +553,7 @@ int dispatch_rope(const RopeQ8Args &a, const PagedArgs &b, int interleaved, int 
                   cudaStream_t stream) {
   constexpr int kMost = 16 / sizeof(T);
   const int n = interleaved ? a.rot : a.rot / 2;
-  if (interleaved && n % kMost == 0)
+  if ((interleaved || a.rot == 0) && n % kMost == 0)  // (nothing that turns is either layout)
     return a.D == 64 ? launch_whole<T, true, 64>(a, b, d_status, stream)
                      : launch_whole<T, true, 128>(a, b, d_status, stream);
   if (a.rot == a.D)

@@ -222,4 +222,3 @@ def test_binding_refuses_wrong_tensors():
         B.PagedCacheQ8(b.k_pages, b.v_pages, b.k_scales[:, :, :0], b.v_scales)
     with pytest.raises(ValueError):
         B.PagedCacheQ8(b.k_pages, b.v_pages[:1], b.k_scales, b.v_scales)
-    assert b.k_pages.dtype == E4M3 and b.k_scales.shape[2] * BLOCK == 16 and not math.isnan(0.0)

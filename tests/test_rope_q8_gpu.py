@@ -129,7 +129,7 @@ class Append:
                         e = e4m3(want_n[at, :, older] * ratio)
                         want_n[at, :, older] = torch.where(ratio < 1, e, want_n[at, :, older])
                     want_s[at, :, j] = s
-                    y = (rows / s[:, None]).transpose(0, 1) if False else rows.transpose(0, 1) / s[:, None, None]
+                    y = rows.transpose(0, 1) / s[:, None, None]
                     want_n[at, :, lo:lo + b - a] = y
                     step = torch.exp2(torch.floor(torch.log2(y.abs().clamp_min(2.0 ** -6))) - 3)
                     d = off.transpose(0, 1) / s[:, None, None]
