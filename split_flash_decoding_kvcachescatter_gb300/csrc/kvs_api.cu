@@ -789,6 +789,7 @@ int kvs_set_wait_limit_ns(uint64_t ns, uint64_t *previous) {
   if (rc == KVS_OK) rc = kvs::set_wait_limit_chunk(ns);
   if (rc == KVS_OK) rc = kvs::set_wait_limit_decode_q8(ns);
   if (rc == KVS_OK) rc = kvs::set_wait_limit_chunk_q8(ns);
+  if (rc == KVS_OK) rc = kvs::set_wait_limit_rows_q8(ns);
   if (rc != KVS_OK) return rc;
   if (previous) *previous = g_limit[dev].load();
   g_limit[dev].store(ns);

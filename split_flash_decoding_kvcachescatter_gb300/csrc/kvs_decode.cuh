@@ -36,15 +36,6 @@ constexpr int kLaunchRegs = 168, kConsumerRegs = 208, kProducerRegs = 88;
 static_assert(2 * kConsumerRegs + kProducerRegs == 3 * kLaunchRegs, "what the launch has");
 constexpr int kDMaxDevices = 64;
 
-// Four bytes global -> shared, asynchronously ...
-__device__ __forceinline__ void copy_async4(void *dst, const void *src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
-}
-// ... and an arrival on `bar` once this thread's copies so far have landed.
-__device__ __forceinline__ void arrive_when_copied(uint64_t *bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
-}
-
 // What a kernel of this file needs to know of the pages is its policy P: the type
 // T of q and out, the head size D, the bytes kElem of an element of the pages, the
 // warp's rows (WarpRows or a class like it), whether 16 keys share a scale

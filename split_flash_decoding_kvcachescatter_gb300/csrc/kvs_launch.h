@@ -204,6 +204,11 @@ int launch_paged_attention_q8(const void *q, long long q_stride, const kvs_paged
 int launch_paged_chunk_q8(const void *q, long long q_stride, const kvs_paged_cache_q8 &cache,
                           int dtype, const PagedArgs &b, void *out, long long out_stride, int H,
                           void *workspace, int *d_status, cudaStream_t stream);
+// Chunks in float32 over the same pages, and their workspace.
+size_t paged_rows_workspace_bytes(int D);
+int launch_paged_rows_q8(const void *q, long long q_stride, const kvs_paged_cache_q8 &cache,
+                         const PagedArgs &pa, void *out, long long out_stride, int H,
+                         void *workspace, int *d_status, cudaStream_t stream);
 
 // A token drawn from each of M logit rows, one launch.
 int launch_sample(const void *logits, long long logits_stride, int dtype, int M, int V,
@@ -241,5 +246,6 @@ int set_wait_limit_decode(uint64_t ns);
 int set_wait_limit_chunk(uint64_t ns);
 int set_wait_limit_decode_q8(uint64_t ns);
 int set_wait_limit_chunk_q8(uint64_t ns);
+int set_wait_limit_rows_q8(uint64_t ns);
 
 }  // namespace kvs

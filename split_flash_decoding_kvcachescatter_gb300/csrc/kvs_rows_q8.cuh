@@ -48,13 +48,35 @@ __device__ __forceinline__ void value_scale(float sv, float &lg, float &inv) {
   inv = mant == 1.f ? __uint_as_float((254u << 23) - u) : 1.f / sv;
 }
 
+// The scales of a cache.
+struct ScalesQ8 {
+  const float *k_scales, *v_scales;
+};
+
+// Pages, and tiles of KT rows, as lines of 128 bytes.
+template <int D, int KT>
+struct LinesQ8 {
+  // the line of 128 bytes that row `row` of the pages begins in
+  static __device__ __forceinline__ int map_row(int row) { return D == 128 ? row : row >> 1; }
+  // Rows `left` and up of a tile become zero (by one warp).
+  static __device__ __forceinline__ void clear_rows(unsigned char *tile, int left) {
+    constexpr int PC = D / 16;  // 16-byte pieces of a row
+    for (int e = threadIdx.x & 31; e < (KT - left) * PC; e += 32) {
+      const int row = left + e / PC, line = D == 128 ? row : row >> 1;
+      const int pc = ((D == 128 ? 0 : (row & 1) * 4) + e % PC) ^ (line & 7);
+      *reinterpret_cast<uint4 *>(tile + line * 128 + pc * 16) = make_uint4(0, 0, 0, 0);
+    }
+  }
+};
+
 // The tile in shared memory: rows of D bytes in lines of 128, 16-byte pieces
 // swizzled by the line (piece c of line r at c ^ (r % 8)).
 // Which elements a lane reads is free as long as both operands agree on it, and
 // chosen so that it reads 16 bytes at a time without bank conflicts: of a key, lane
 // (n, q) takes the D / 4 elements from D / 4 q (k step s: four of them, from 4 s), of
 // a value those from D / 8 n (column n of product c: element D / 8 n + c).
-template <typename T, int D>
+// kFewForm: units of 8 rows at most have a form of their own (tile<true>).
+template <typename T, int D, bool kFewForm = true>
 struct RowsQ8 {
   static constexpr bool F32 = std::is_same<T, float>::value;
   static constexpr int KT = D == 128 ? 32 : 64;
@@ -79,7 +101,7 @@ struct RowsQ8 {
     for (int j = 0; j < D / 8; ++j)
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
-    const bool few = rows <= 8;
+    const bool few = kFewForm && rows <= 8;
 #pragma unroll
     for (int hh = 0; hh < 2; ++hh) {
       m[hh] = neg_inf_f();

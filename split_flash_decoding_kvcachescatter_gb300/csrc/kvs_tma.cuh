@@ -109,6 +109,15 @@ __device__ __forceinline__ void tma_rows(void *dst, const CUtensorMap *map, int 
       : "memory");
 }
 
+// Four bytes global -> shared, asynchronously ...
+__device__ __forceinline__ void copy_async4(void *dst, const void *src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+}
+// ... and an arrival on `bar` once this thread's copies so far have landed.
+__device__ __forceinline__ void arrive_when_copied(uint64_t *bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+
 __device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }

@@ -27,7 +27,7 @@
 // What bounds it: the turning.  A pair of tiles moves about 320 KB through shared
 // memory (pages in and out, float16 in, and what the products read), the pages come
 // from L2 with as many bytes on their way as the rings hold, and eight warps convert.
-// 8192 rows of 32 query heads on 8 kv heads of 128 behind 8192 keys: 343 us, where
+// 4096 rows of 32 query heads on 8 kv heads of 128 behind 4096 keys: 343 us, where
 // paged_chunk.cu takes about 255 for pages in 16 bits.
 // Measured at that shape: rings of a whole tile and rows that leave without a staging
 // area 343 us, 8 KB of staging and three quarters 402; two quarters a step 487; a

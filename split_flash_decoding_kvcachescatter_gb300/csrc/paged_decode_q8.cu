@@ -1,5 +1,7 @@
-// paged_decode_q8.cu -- attention over a paged KV cache in 8 bits for single
-// tokens (the kernels: kvs_decode.cuh, the products: kvs_rows_q8.cuh).
+// paged_decode_q8.cu -- attention over a paged KV cache in 8 bits: the choice of
+// kernel, and single tokens (the kernels: kvs_decode.cuh, the products:
+// kvs_rows_q8.cuh).  Chunks in 16 bits: paged_chunk_q8.cu, long ones in float32:
+// paged_rows_q8.cu.
 
 #include "kvs_decode.cuh"
 #include "kvs_rows_q8.cuh"
@@ -11,32 +13,19 @@ namespace {
 // Pages in 8 bits under q and out of Type (kvs_decode.cuh); kFew: units of 8 rows at most,
 // for which 16-bit rows leave registers for eight consumer warps a block.
 template <typename Type, int D_, bool kFew>
-struct PagesQ8 {
+struct PagesQ8 : LinesQ8<D_, RowsQ8<Type, D_>::KT> {
   using T = Type;
   using Rows = RowsQ8<T, D_>;
   static constexpr int D = D_, kElem = 1;
   static constexpr int kRings = kFew && sizeof(T) == 2 ? 8 : 4;
   static constexpr bool kScaled = true, kOnlyFew = kFew;
   static constexpr bool kFewForm = true;
-  struct Extra {
-    const float *k_scales, *v_scales;
-  };
+  using Extra = ScalesQ8;
   // as PlainPages'; 32 sequences of up to 8192 keys in bfloat16 took 66.3 us at 96 KB, 58.3 at 192,
   // 60.6 at 384, 65.6 at 768
   static constexpr int kFixBytes = 192 << 10;
   static constexpr long long kBlockBytes = 512 << 10;
   static constexpr long long kShortBytes = 128 << 10;
-  // the line of 128 bytes that row `row` of the pages begins in
-  static __device__ __forceinline__ int map_row(int row) { return D == 128 ? row : row >> 1; }
-  // Rows `left` and up of a tile become zero (by one warp).
-  static __device__ __forceinline__ void clear_rows(unsigned char *tile, int left) {
-    constexpr int KT = Rows::KT, PC = D / 16;  // 16-byte pieces of a row
-    for (int e = threadIdx.x & 31; e < (KT - left) * PC; e += 32) {
-      const int row = left + e / PC, line = D == 128 ? row : row >> 1;
-      const int pc = ((D == 128 ? 0 : (row & 1) * 4) + e % PC) ^ (line & 7);
-      *reinterpret_cast<uint4 *>(tile + line * 128 + pc * 16) = make_uint4(0, 0, 0, 0);
-    }
-  }
 };
 
 template <typename T, int D>
@@ -68,17 +57,30 @@ int set_wait_limit_decode_q8(uint64_t ns) {
 }
 
 size_t paged_attention_q8_workspace_bytes(int H, int Hkv, int D, int max_new) {
-  // (float32 chunks take the decode kernel too)
-  const size_t rows = paged_decode_workspace_bytes(D);
-  return (long long)max_new * (H / Hkv) <= kDRows ? rows : std::max(rows, paged_chunk_workspace_bytes(D));
+  const size_t few = paged_decode_workspace_bytes(D);
+  return (long long)max_new * (H / Hkv) <= kDRows
+             ? few
+             : std::max({few, paged_chunk_workspace_bytes(D), paged_rows_workspace_bytes(D)});
 }
 
 int launch_paged_attention_q8(const void *q, long long q_stride, const kvs_paged_cache_q8 &cache,
                               int dtype, const PagedArgs &pa, void *out, long long out_stride, int H,
                               void *workspace, int *d_status, cudaStream_t stream) {
-  if ((long long)pa.max_new * (H / cache.num_kv_heads) > kDRows && dtype != KVS_F32)
-    return launch_paged_chunk_q8(q, q_stride, cache, dtype, pa, out, out_stride, H, workspace,
-                                 d_status, stream);
+  const int G = H / cache.num_kv_heads;
+  if ((long long)pa.max_new * G > kDRows) {
+    if (dtype != KVS_F32)
+      return launch_paged_chunk_q8(q, q_stride, cache, dtype, pa, out, out_stride, H, workspace,
+                                   d_status, stream);
+    // Units of 112 rows share their keys where there are rows for them; below that more of the
+    // SM's warps have work in units of 16.  us by units of 112 and of 16, H 14 / 2, D 64 and
+    // H 40 / 8, D 128: 4 sequences of up to 3000 keys with 40, 100, 250, 700 new tokens 23.5, 25.8,
+    // 30.7, 46.3 (15.4, 22.3, 39.2, 73.6) and 35, 48, 92, 243 (36, 66, 161, 439); 16 of up to
+    // 2500 with 100, 250 23.4, 27.3 (21.2, 32.6) and 86, 89 (77, 120); one of 12,000 with 40
+    // 29.8 (19.5) and 65 (94).
+    if ((long long)pa.num_rows * H >= 1500 && (long long)pa.num_rows * G >= 32ll * pa.M)
+      return launch_paged_rows_q8(q, q_stride, cache, pa, out, out_stride, H, workspace, d_status,
+                                  stream);
+  }
 #define KVS_DECODE(T)                                                                           \
   return cache.head_dim == 64                                                                   \
              ? launch_q8<T, 64>(q, q_stride, cache, pa, out, out_stride, H, workspace,          \
