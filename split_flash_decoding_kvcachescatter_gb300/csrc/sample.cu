@@ -244,13 +244,33 @@ __device__ __forceinline__ u64 find_bin(SampleShared &s, Need need) {
   return all;
 }
 
-// The first `n` of x (a power of two, at most kSMost) in falling order; by the block.
-// (Steps of 32 and less stay within the 64 places of a warp's threads.)
+__device__ __forceinline__ int power_of_two(int n) { return n <= 1 ? 1 : 1 << (32 - __clz(n - 1)); }
+
+// The first n of x (all different, above 0; n <= kSMost) in falling order; by the block.  What
+// lies behind them up to a power of two may be overwritten.
 __device__ __forceinline__ void sort_falling(u64 *x, int n) {
   const int t = threadIdx.x;
-  for (int size = 2; size <= n; size <<= 1) {
+  const int n2 = power_of_two(n);
+  if (n2 <= 256) {
+    // An item's place is the number of larger ones, counted by kSThreads / n2 threads side by
+    // side (32 at most): for 50 items some 200 cycles where the network below takes 1300.
+    const int parts = min(kSThreads / n2, 32), i = t / parts, part = t & (parts - 1);
+    const u64 mine = i < n ? x[i] : 0ull;
+    int place = 0;
+    if (i < n)
+      for (int j = part; j < n; j += parts) place += x[j] > mine;
+    for (int o = parts >> 1; o >= 1; o >>= 1) place += __shfl_xor_sync(0xffffffffu, place, o);
+    __syncthreads();
+    if (i < n && part == 0) x[place] = mine;
+    __syncthreads();
+    return;
+  }
+  for (int i = n + t; i < n2; i += kSThreads) x[i] = 0ull;
+  __syncthreads();
+  // (Steps of 32 and less stay within the 64 places of a warp's threads.)
+  for (int size = 2; size <= n2; size <<= 1) {
     for (int step = size >> 1; step >= 1; step >>= 1) {
-      if (2 * t < n) {
+      if (2 * t < n2) {
         const int i = 2 * t - (t & (step - 1)), j = i + step;
         const u64 p = x[i], q = x[j];
         if ((p < q) == ((i & size) == 0)) {
@@ -299,7 +319,6 @@ __device__ __forceinline__ int first_reaching(const u64 *x, int n, u64 need) {
   }
   return lo;
 }
-__device__ __forceinline__ int power_of_two(int n) { return n <= 1 ? 1 : 1 << (32 - __clz(n - 1)); }
 
 template <typename T>
 __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(SampleArgs a) {
@@ -494,10 +513,8 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(SampleArgs a) {
     };
     // Block 0: its n tokens in falling order, and the sums of their weights.
     auto sort_items = [&](int n, bool weights) {
-      const int n2 = power_of_two(n);
-      for (int i = n + t; i < n2; i += kSThreads) s.item[i] = 0ull;
       __syncthreads();
-      sort_falling(s.item, n2);
+      sort_falling(s.item, n);
       if (weights) {
         for (int i = t; i < n; i += kSThreads) s.weight[i] = weigh((unsigned)(s.item[i] >> 32));
         __syncthreads();
@@ -590,11 +607,9 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(SampleArgs a) {
             c = (int)s.sent;
             const u64 total = s.weight[c - 1];
             // the kept ones in the order of ids, with the sums of their weights
-            const int c2 = power_of_two(c);
-            for (int i = t; i < c2; i += kSThreads)
-              s.out[i] = i < c ? (s.item[i] << 32 | (unsigned)i) : 0ull;
+            for (int i = t; i < c; i += kSThreads) s.out[i] = s.item[i] << 32 | (unsigned)i;
             __syncthreads();
-            sort_falling(s.out, c2);
+            sort_falling(s.out, c);
             for (int i = t; i < c; i += kSThreads) {
               const int r = (int)(unsigned)s.out[i];
               s.item[i] = s.weight[r] - (r ? s.weight[r - 1] : 0ull);

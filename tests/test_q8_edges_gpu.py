@@ -424,3 +424,29 @@ def test_no_call_allocates():
     torch.cuda.synchronize()
     assert torch.cuda.memory_stats()["allocation.all.allocated"] == held
     b.check(outs[0])
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("spread", [0.01, 4.0])
+def test_sampling_from_the_largest_vocabulary(dtype, spread):
+    """2^19 tokens, of nearly equal logits and of few that count, under each rule alone."""
+    M, V = 3, 2 ** 19
+    g = torch.Generator(device=DEV)
+    g.manual_seed(7)
+    x = (torch.empty(M, V, device=DEV).normal_(generator=g) * spread).to(DTYPES[dtype])
+    u = torch.tensor([0.1, 0.5, 0.999], device=DEV)
+    w = torch.softmax(x.double(), 1)
+    order = torch.sort(x.double(), dim=1, descending=True, stable=True)[1]
+    full = lambda v, t=torch.float32: torch.full((M,), v, dtype=t, device=DEV)
+    for rules, count in ((dict(), V), (dict(top_k=full(700, torch.int32)), 700), (dict(top_p=full(0.5)), None)):
+        ranked = w.gather(1, order)
+        sums = ranked.cumsum(1)
+        keep = torch.arange(V, device=DEV) < count if count else (sums - ranked) < 0.5 * sums[:, -1:]
+        kept = torch.zeros_like(w).scatter_(1, order, ranked * keep)
+        c = kept.cumsum(1) / kept.sum(1, keepdim=True)
+        got = B.kvs_sample_logits(x, u, **rules).long()[:, None]
+        low = c.gather(1, got) - kept.gather(1, got) / kept.sum(1, keepdim=True)
+        # weights to 2^-37 of themselves; sums of 2^19 numbers of 64 bits here
+        slack = 2.0 ** -30
+        assert (low <= u[:, None].double() + slack).all() and (c.gather(1, got) >= u[:, None].double() - slack).all()
+        assert (kept.gather(1, got) > 0).all()
