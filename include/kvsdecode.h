@@ -680,13 +680,14 @@ int kvs_paged_attention(const void *q, int64_t q_stride, const kvs_paged_cache *
  * read.  An element is its block's scale times an e4m3 number (sign, 4
  * exponent bits, 3 mantissa bits; 448 at most, steps of 2^-9 below 2^-6); a
  * block is KVS_SCALE_BLOCK positions of one kv head in a page.
- * kvs_rope_scatter_paged_q8 writes powers of two as scales.
+ * kvs_rope_scatter_paged_q8 writes powers of two as scales; a program that
+ * fills pages itself may use any from 0 to 2^100.
  */
 #define KVS_SCALE_BLOCK 16
 
 typedef struct kvs_paged_cache_q8 {
   void *k_pages, *v_pages;   /* device, 16-byte aligned: e4m3 [num_pages][Hkv][page_size][D] */
-  float *k_scales, *v_scales; /* device: [num_pages][Hkv][page_size / 16], >= 0 and finite */
+  float *k_scales, *v_scales; /* device: [num_pages][Hkv][page_size / 16] */
   int32_t num_pages;         /* as kvs_paged_cache's */
   int32_t page_size;
   int32_t num_kv_heads;
@@ -705,7 +706,8 @@ typedef struct kvs_paged_cache_q8 {
  *         that has grown, numbers of the older rows (those before the
  *         sequence's first new position) become e4m3(number * old scale / scale)
  *     new numbers = e4m3(element / scale)
- * with e4m3() to nearest, ties to even.  A block's scale so does not depend on
+ * with e4m3() to nearest, ties to even (an old scale that is no power of two
+ * divides by way of its reciprocal, rounded to float32).  A block's scale so does not depend on
  * whether its rows came in one call or in many, and its numbers only below
  * 2^-6.  Numbers and scales of no other rows and blocks are written.  A page
  * that gets rows, or whose last block holds the rows before them, must not be
@@ -732,7 +734,10 @@ int kvs_rope_scatter_paged_q8(const void *q, int64_t q_stride, const void *k, in
  * (float32 rows go in as two parts of 22 bits together).  Weights: decode
  * steps and float32 as two float16 parts; chunks in 16 bits rounded to float16,
  * and those below 2^-30 of a row's largest may count as zero in the product
- * with v.  Live rows and scales must be finite.
+ * with v.  In chunks of 16-bit rows, too, bfloat16 elements of q below 2^-88 may
+ * lose bits, and where scales are no powers of two a number goes into the
+ * products times its scale over the largest of its 128 keys, rounded to float16.
+ * Live rows and scales must be finite.
  *
  *   q, out     rows as for kvs_paged_attention, of kvs_dtype `dtype`
  *   workspace  device scratch of >= kvs_paged_attention_q8_workspace_bytes
@@ -840,6 +845,7 @@ typedef struct kvs_sample_rules {
  *   token_probs  out  [M] float32, device, or NULL
  *   probs        out  [M] rows of vocab_size float32, probs_stride apart, or NULL;
  *                     must not overlap logits
+ * (the outputs must not overlap the rules either; token_probs may be uniforms)
  * Errors: DIMS (M < 0, vocab_size < 1, a stride too small), NULL (logits, uniforms,
  * or all three outputs), ALIGN, UNSUPPORTED (dtype; a vocabulary of more than 2^19
  * tokens; more than 2^30 rows), OVERLAP, LAUNCH.  M = 0 enqueues nothing.

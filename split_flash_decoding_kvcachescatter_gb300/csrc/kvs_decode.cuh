@@ -13,7 +13,9 @@
 // warps, one a ring (tensor-map copies of 16 rows, each looked up in the page
 // table).  Producers run ahead over the ends of units, so the copies go on
 // while the consumers join a unit's four states in shared memory and write
-// the output or a partial.
+// the output or a partial.  Where a byte of the pages brings more products (8
+// bits under few rows) 8 consumer warps, whose rings 4 producers fill two each
+// and give registers to.
 #pragma once
 
 #include <algorithm>
