@@ -845,7 +845,7 @@ typedef struct kvs_sample_rules {
  *   token_probs  out  [M] float32, device, or NULL
  *   probs        out  [M] rows of vocab_size float32, probs_stride apart, or NULL;
  *                     must not overlap logits
- * (the outputs must not overlap the rules either; token_probs may be uniforms)
+ * No output may overlap another one or the inputs.
  * Errors: DIMS (M < 0, vocab_size < 1, a stride too small), NULL (logits, uniforms,
  * or all three outputs), ALIGN, UNSUPPORTED (dtype; a vocabulary of more than 2^19
  * tokens; more than 2^30 rows), OVERLAP, LAUNCH.  M = 0 enqueues nothing.
