@@ -23,14 +23,16 @@
 // most 1024, go to block 0, which sorts them.  Few tokens are then finished there, and
 // the row's 150,000 have been looked at twice.  Where the bin holds more (rows of nearly
 // equal logits) or lies 32 units down, the logit is found digit by digit of its bits.
+// For a small k each block bounds the row's k-th logit by the k-th of its threads' maxima;
+// what reaches the largest of these bounds goes to block 0 without the row's histogram.
 //
 // Bound: bytes (a row is read once); what it takes is a chain of short phases (a cluster
 // barrier each 0.6 us) and, without a top-k, the instructions of a weight for every token.
-// Measured: one row of 152,064 in float32 18 us, 32 rows 56, 67 of 32,001 in bfloat16 36, 24 of
+// Measured: one row of 152,064 in float32 17 us, 32 rows 57, 67 of 32,001 in bfloat16 36, 24 of
 // 152,064 in float16 with all probabilities 55.  By digits of the bits alone, 64-bit atomics
 // for the weights 73 (one row) and 229 (32), pairs of 32-bit ones 39 and 77; the histogram over
 // the distance 19 and 65; weights in fewer steps, one thread for 1 / T and bounds that spare
-// the counting 18 and 58.
+// the counting 18 and 58.  (Small k by the row's histogram: one row 18.)
 
 #include <mutex>
 #include <type_traits>
@@ -166,6 +168,7 @@ struct alignas(16) SampleShared {  // (the keys lie behind it)
   };
   u64 table[256];
   unsigned top[2][16];  // of the cluster's blocks, by row parity
+  int bound[16];
   unsigned ties[16];
   u64 above[16];
   u64 wsum[32];
@@ -209,16 +212,22 @@ __device__ __forceinline__ void sum_bins(SampleShared &s, int rank, int cs) {
 
 // The bin, from the top, in which the running amount reaches need(all of it); leaves it
 // in s.bin with what lies above it and in it (s.bin = -1: all of them do not reach it),
-// and returns the whole amount.  By the whole block.
-template <typename Need>
+// and returns the whole amount.  By the whole block.  kOwn: of this block's counts.
+template <bool kOwn = false, typename Need>
 __device__ __forceinline__ u64 find_bin(SampleShared &s, Need need) {
   constexpr int kPer = kSBins / kSThreads;
   static_assert(kPer == 4, "two 16-byte loads");
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   // thread t takes bins from the top: kSBins - 1 - (4 t + j)
-  const ulonglong2 hi = *reinterpret_cast<const ulonglong2 *>(&s.amount[kSBins - 2 - 4 * t]);
-  const ulonglong2 lo = *reinterpret_cast<const ulonglong2 *>(&s.amount[kSBins - 4 - 4 * t]);
-  const u64 m[4] = {hi.y, hi.x, lo.y, lo.x};
+  u64 m[4];
+  if constexpr (kOwn) {
+    const uint4 c = *reinterpret_cast<const uint4 *>(&s.low[kSBins - 4 - 4 * t]);
+    m[0] = c.w, m[1] = c.z, m[2] = c.y, m[3] = c.x;
+  } else {
+    const ulonglong2 hi = *reinterpret_cast<const ulonglong2 *>(&s.amount[kSBins - 2 - 4 * t]);
+    const ulonglong2 lo = *reinterpret_cast<const ulonglong2 *>(&s.amount[kSBins - 4 - 4 * t]);
+    m[0] = hi.y, m[1] = hi.x, m[2] = lo.y, m[3] = lo.x;
+  }
   const u64 mine = m[0] + m[1] + m[2] + m[3];
   u64 inc = mine;
 #pragma unroll
@@ -486,9 +495,10 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(SampleArgs a) {
       return max(w + (left ? 1ull : 0ull), 1ull);
     };
     // Sends to block 0 the keys from `least_key` up in bin `bin` of the distances, and
-    // above it where `whole`.  All blocks call it, after find_bin().
-    auto gather = [&](int bin, bool whole, unsigned least_key) {
-      cluster_arrive_release();  // this block is done with the row's amounts
+    // above it where `whole`.  All blocks call it, after find_bin() (settled: and after a
+    // barrier of the cluster).
+    auto gather = [&](int bin, bool whole, unsigned least_key, bool settled) {
+      if (!settled) cluster_arrive_release();  // this block is done with the row's amounts
       if (t == 0) s.sent = 0u;
       __syncthreads();
       const unsigned from = max(least_key, first_key(bin));
@@ -505,7 +515,7 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(SampleArgs a) {
         }
       }
       __syncthreads();
-      cluster_wait_acquire();  // and so is block 0
+      if (!settled) cluster_wait_acquire();  // and so is block 0
       const unsigned sent = s.sent;
       if (t == 0 && sent) s.cut = (int)atom_dsmem_add(dsmem_addr(&s.total[gathers & 1], 0), sent);
       __syncthreads();
@@ -563,7 +573,7 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(SampleArgs a) {
       // most the row's k-th logit: what lies in lower bins than it need not be counted.
       // (Each count is a shared-memory atomic on a place of its own, some 17 cycles a warp.)
       const bool by_thread = 2 * k <= kSThreads;  // groups: a thread's tokens, or a vector's
-      unsigned least_key = 1u;
+      int bound = 0;
       if (by_thread || 4 * k <= vecs) {
         if (by_thread) {
           if (own_most) atomicAdd(&s.low[near_bin(own_most)], 1u);
@@ -577,24 +587,60 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(SampleArgs a) {
           }
         }
         __syncthreads();
-        for (int j = t; j < kSBins; j += kSThreads) s.amount[j] = s.low[j];
+        find_bin<true>(s, [&](u64) { return (u64)k; });
+        bound = max(s.bin, 0);
         __syncthreads();
         clear();
-        find_bin(s, [&](u64) { return (u64)k; });
-        if (s.bin > 0) least_key = first_key(s.bin);
-        __syncthreads();
       }
-      pass_over(false, -1, 0u, least_key);
-      find_bin(s, [&](u64) { return (u64)k; });
-      const int bin = s.bin;
-      const u64 before = s.before, inside = s.inside;
-      if (bin < 0) {  // fewer tokens than k
+      bool have = false, whole = false;  // block 0 has the tokens that matter: all of them from a bin up
+      int n = 0;
+      u64 before = 0ull;
+      if (by_thread && k * cs <= kSMost) {
+        // Few tokens reach the largest of the blocks' bounds (some 10 a block for k = 20, 40 for
+        // 50): they go to block 0 at once, without counts of the whole row.
+        if (t < cs) st_dsmem_s32(dsmem_addr(&s.bound[rank], t), bound);
+        cluster_sync_all();
+        for (int r = 0; r < cs; ++r) bound = max(bound, s.bound[r]);
+        if (bound > 0) {
+          gather(bound, true, 1u, true);
+          n = (int)min((unsigned)ld_dsmem_s32(dsmem_addr(&s.total[(gathers - 1) & 1], 0)), (unsigned)kSMost + 1u);
+          have = whole = n <= kSMost;
+          if (have && rank == 0 && n > 128) {  // those of the bins above the k-th's and of its own
+            const u64 v0 = t < n ? s.item[t] : 0ull, v1 = t + kSThreads < n ? s.item[t + kSThreads] : 0ull;
+            __syncthreads();  // (the counts' place is clear)
+            const int b0 = v0 ? near_bin((unsigned)(v0 >> 32)) : -1, b1 = v1 ? near_bin((unsigned)(v1 >> 32)) : -1;
+            if (b0 >= 0) atomicAdd(&s.low[b0], 1u);
+            if (b1 >= 0) atomicAdd(&s.low[b1], 1u);
+            if (t == 0) s.sent = 0u;
+            __syncthreads();
+            find_bin<true>(s, [&](u64) { return (u64)k; });
+            const int bin = s.bin;
+            n = (int)(s.before + s.inside);
+            if (b0 >= bin) s.item[atomicAdd(&s.sent, 1u)] = v0;
+            if (b1 >= bin) s.item[atomicAdd(&s.sent, 1u)] = v1;
+            __syncthreads();
+            clear();
+          }
+        }
+      }
+      if (!have) {
+        __syncthreads();  // the counts' place is clear
+        pass_over(false, -1, 0u, bound > 0 ? first_key(bound) : 1u);
+        find_bin(s, [&](u64) { return (u64)k; });
+        const int bin = s.bin;
+        const u64 inside = s.inside;
+        before = s.before;
+        if (bin < 0) {  // fewer tokens than k
+          k_open = false;
+        } else if (bin > 0 && inside <= (u64)kSMost) {
+          have = true;
+          whole = before + inside <= (u64)kSMost;
+          n = (int)(whole ? before + inside : inside);
+          gather(bin, whole, 1u, false);
+        }
+      }
+      if (have) {
         k_open = false;
-      } else if (bin > 0 && inside <= (u64)kSMost) {
-        k_open = false;
-        const bool whole = before + inside <= (u64)kSMost;
-        const int n = (int)(whole ? before + inside : inside);
-        gather(bin, whole, 1u);
         unsigned key = 0u, count = 0u;
         u64 cut = 0ull;
         if (whole && !a.probs) {
@@ -602,13 +648,13 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(SampleArgs a) {
             sort_items(n, true);
             int c = k;
             if (by_p) c = min(c, first_reaching(s.weight, c, p_need(s.weight[c - 1])) + 1);
-            int have = 0;
+            int heavy = 0;
             for (int i = t; i < c; i += kSThreads)
-              have += s.weight[i] - (i ? s.weight[i - 1] : 0ull) >= floor_w;
-            have = __reduce_add_sync(0xffffffffu, have);
+              heavy += s.weight[i] - (i ? s.weight[i - 1] : 0ull) >= floor_w;
+            heavy = __reduce_add_sync(0xffffffffu, heavy);
             if (t == 0) s.sent = 0u;
             __syncthreads();
-            if (lane == 0 && have) atomicAdd(&s.sent, (unsigned)have);
+            if (lane == 0 && heavy) atomicAdd(&s.sent, (unsigned)heavy);
             __syncthreads();
             c = (int)s.sent;
             const u64 total = s.weight[c - 1];
@@ -678,7 +724,7 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(SampleArgs a) {
       const int bin = s.bin;
       const u64 before = s.before;
       if (bin > 0) {
-        gather(bin, false, max(thr, 1u));
+        gather(bin, false, max(thr, 1u), false);
         const unsigned n = (unsigned)ld_dsmem_s32(dsmem_addr(&s.total[(gathers - 1) & 1], 0));
         if (n <= (unsigned)kSMost) {
           p_open = false;

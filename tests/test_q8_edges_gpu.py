@@ -450,3 +450,35 @@ def test_sampling_from_the_largest_vocabulary(dtype, spread):
         slack = 2.0 ** -30
         assert (low <= u[:, None].double() + slack).all() and (c.gather(1, got) >= u[:, None].double() - slack).all()
         assert (kept.gather(1, got) > 0).all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("V", [3000, 40001, 152064])
+@pytest.mark.parametrize("spread", [0.001, 1.0, 30.0])
+def test_sampling_from_the_first_few(dtype, V, spread):
+    """Numbers of kept tokens around those that decide how they are found, for logits that hardly
+    differ (and often tie), usual ones and steep ones."""
+    ks = [2, 3, 20, 63, 64, 65, 128, 129, 255, 256, 257, 400]
+    M = len(ks)
+    g = torch.Generator(device=DEV)
+    g.manual_seed(8)
+    x = (torch.empty(M, V, device=DEV).normal_(generator=g) * spread).to(DTYPES[dtype])
+    u = torch.rand(M, device=DEV, generator=g)
+    k = torch.tensor(ks, dtype=torch.int32, device=DEV)
+    prob = torch.empty(M, device=DEV)
+    got = B.kvs_sample_logits(x, u, top_k=k, token_probs=prob).long()[:, None]
+    order = torch.sort(x.double(), dim=1, descending=True, stable=True)[1]
+    ranked = torch.softmax(x.double(), 1).gather(1, order) * (torch.arange(V, device=DEV) < k[:, None])
+    w = torch.zeros(M, V, dtype=torch.float64, device=DEV).scatter_(1, order, ranked)
+    w /= w.sum(1, keepdim=True)
+    c = w.cumsum(1)
+    p = w.gather(1, got)
+    # weights to 2^-37 of themselves, those below 2^-45 of the largest as zero
+    assert (p > 0).all()
+    assert (c.gather(1, got) - p <= u[:, None].double() + 2.0 ** -30).all()
+    assert (c.gather(1, got) >= u[:, None].double() - 2.0 ** -30).all()
+    within(prob, p[:, 0], p[:, 0] * 2.0 ** -23 + 2.0 ** -44)
+    probs = torch.empty(M, V, device=DEV)
+    again = B.kvs_sample_logits(x, u, top_k=k, probs=probs).long()[:, None]
+    assert torch.equal(got, again)
+    within(probs, w, w * 2.0 ** -21 + 2.0 ** -44)
