@@ -880,7 +880,10 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(SampleArgs a) {
     }
     __syncthreads();  // the keys may be replaced
   }
-  // (a cluster barrier follows every access to another block's memory)
+  // Where a small k sent the tokens to block 0 at once, every block has read their number there
+  // with no barrier behind it; a cluster barrier follows every other access to another block's
+  // memory.  No block leaves before all have read.  (Block 0, which finishes such a row, is last.)
+  cluster_sync_all();
 }
 
 struct SampleInfo {
