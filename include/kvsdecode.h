@@ -728,13 +728,14 @@ int kvs_rope_scatter_paged_q8(const void *q, int64_t q_stride, const void *k, in
 /*
  * kvs_paged_attention_q8 -- kvs_paged_attention over an 8-bit cache: K and V
  * rows are the values that the cache's numbers and scales stand for (scales of
- * V below 2^-60 count as 2^-60).  The numbers are exact in the products
+ * V below 2^-60 count as 2^-60, and those below 2^-60 of a larger one in the same
+ * sequence may count as that much).  The numbers are exact in the products
  * (float16 operands, float32 sums); a row of q is brought to 2^15 by a power of
  * two first, and elements below 2^-28 of its largest one may lose bits there
  * (float32 rows go in as two parts of 22 bits together).  Weights: decode
- * steps and float32 as two float16 parts; chunks in 16 bits rounded to float16,
- * and those below 2^-30 of a row's largest may count as zero in the product
- * with v.  In chunks of 16-bit rows, too, bfloat16 elements of q below 2^-88 may
+ * steps and float32 as two float16 parts; chunks in 16 bits rounded to float16.
+ * Times V's scale, those below 2^-30 of a row's largest may count as zero in the
+ * product with v; the sum of the weights has all.  In chunks of 16-bit rows, too, bfloat16 elements of q below 2^-88 may
  * lose bits, and where scales are no powers of two a number goes into the
  * products times its scale over the largest of its 128 keys, rounded to float16.
  * Live rows and scales must be finite.

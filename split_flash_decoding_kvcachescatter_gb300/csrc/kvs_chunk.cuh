@@ -153,6 +153,11 @@ struct Pieces {
 __device__ __forceinline__ float piece_weight(float m, float mx) {
   return ex2(m - (mx == neg_inf_f() ? 0.f : mx));
 }
+// ls + the share of its sum l.
+template <bool kFar>
+__device__ __forceinline__ float add_piece(float ls, float l, float m, float mx) {
+  return add_sum<kFar>(ls, l, m - (mx == neg_inf_f() ? 0.f : mx), kFar ? 0.f : piece_weight(m, mx));
+}
 
 // The two tiles of a unit: tokens, key tiles that each attends, and those of
 // this block's column.
@@ -165,7 +170,10 @@ struct CTile {
 // joined with theirs by the block that completes it.  By the tile's four warps
 // (thread t has row t: live, token tok of the tile, running maximum m and sum l,
 // accumulators at tm_o); false when a wait ran out.
-template <typename T, int D, bool kStaged, class Barrier>
+// kFar (8-bit pages): sums as add_sum's (kvs_paged.cuh), and units of more than two pieces join
+// from memory alone: each 100 instructions here cost that kernel's loops time, which fill
+// the instruction cache (4096 tokens over 8192 382 us with the two ways, 349 with one).
+template <typename T, int D, bool kStaged, bool kFar, class Barrier>
 __device__ __forceinline__ bool finish_tile(T *out, long long out_stride, const volatile CUnit *ud,
                                             const CTile &tl, int x, int t, int lane, bool live,
                                             int tok, int G, int b, uint32_t tm_o, float m, float l,
@@ -200,13 +208,14 @@ __device__ __forceinline__ bool finish_tile(T *out, long long out_stride, const 
     // joins them with the accumulator it still holds in TMEM.
     if (t == 0) {
       const unsigned long long v = ld_acquire_u64(ctr);
-      s_last[x] = (unsigned)(v >> 32) == tag && (unsigned)v + add == (unsigned)tl.nt;
+      s_last[x] = (unsigned)(v >> 32) == tag && (unsigned)v + add == (unsigned)tl.nt &&
+                  (!kFar || pc.b2 == pc.b1 + 1);
     }
     if (!wg_barrier()) return false;
     if (s_last[x]) {
       __threadfence();
       if (t == 0) *ctr = 0ull;  // (no other block will look; a replayed graph uses the tag again)
-      if (pc.b2 == pc.b1 + 1) {  // two pieces, the usual unit: all loads first
+      if (kFar || pc.b2 == pc.b1 + 1) {  // two pieces, the usual unit: all loads first
         const int oc = b == pc.b1 ? pc.b2 : pc.b1;
         const float2 om = __ldcg(pc.ml(oc, t));
 #pragma unroll 1
@@ -216,7 +225,8 @@ __device__ __forceinline__ bool finish_tile(T *out, long long out_stride, const 
           for (int v = 0; v < 16; ++v) q[v] = __ldcg(pc.acc(oc, t, ch * 64 + 4 * v));
           const float mx = fmaxf(m, om.x);
           const float wo = piece_weight(om.x, mx), ww = piece_weight(m, mx);
-          const float ls = b == pc.b1 ? fmaf(wo, om.y, ww * l) : fmaf(ww, l, wo * om.y);
+          const float ls = b == pc.b1 ? add_piece<kFar>(add_piece<kFar>(0.f, l, m, mx), om.y, om.x, mx)
+                                      : add_piece<kFar>(add_piece<kFar>(0.f, om.y, om.x, mx), l, m, mx);
           const float inv = 1.f / ls;
 #pragma unroll
           for (int hc = 0; hc < 2; ++hc) {
@@ -239,7 +249,7 @@ __device__ __forceinline__ bool finish_tile(T *out, long long out_stride, const 
       float ls = 0.f;
       for (int c = pc.b1; c <= pc.b2; ++c) {
         const float2 ml = c == b ? make_float2(m, l) : __ldcg(pc.ml(c, t));
-        ls = fmaf(piece_weight(ml.x, mx), ml.y, ls);
+        ls = add_piece<kFar>(ls, ml.y, ml.x, mx);
       }
       const float inv = 1.f / ls;
 #pragma unroll 1
@@ -299,7 +309,7 @@ __device__ __forceinline__ bool finish_tile(T *out, long long out_stride, const 
         for (int c = pc.b1; c <= pc.b2; ++c) mx = fmaxf(mx, __ldcg(pc.ml(c, t)).x);
         for (int c = pc.b1; c <= pc.b2; ++c) {
           const float2 ml = __ldcg(pc.ml(c, t));
-          ls = fmaf(piece_weight(ml.x, mx), ml.y, ls);
+          ls = add_piece<kFar>(ls, ml.y, ml.x, mx);
         }
         const float inv = 1.f / ls;
 #pragma unroll 1

@@ -223,7 +223,7 @@ __device__ __forceinline__ void put_state(const typename P::Rows &w, float *acc,
 }
 
 // Columns d .. d + 3 of row r joined over the W warps' states.
-template <int D, int W, int ROWS>
+template <int D, int W, int ROWS, bool kFar>
 __device__ __forceinline__ void join_states(const float *acc0, const float2 *ml0, int r, int d,
                                             float4 &acc, float &mx, float &ls) {
   mx = neg_inf_f();
@@ -241,7 +241,7 @@ __device__ __forceinline__ void join_states(const float *acc0, const float2 *ml0
     acc.y = fmaf(wgt, v.y, acc.y);
     acc.z = fmaf(wgt, v.z, acc.z);
     acc.w = fmaf(wgt, v.w, acc.w);
-    ls = fmaf(wgt, ml.y, ls);  // (a NaN sum stays one also under a zero weight)
+    ls = add_sum<kFar>(ls, ml.y, ml.x - mz, wgt);  // (a NaN sum stays one also under a zero weight)
   }
 }
 
@@ -377,7 +377,7 @@ __global__ void __launch_bounds__((DGeo<P, P::kRings>::THREADS), 1)
         const int r = e / (D / 4), d = (e - r * (D / 4)) * 4;
         float4 acc;
         float mx, ls;
-        join_states<D, W, C::ROWS>(macc, mml, r, d, acc, mx, ls);
+        join_states<D, W, C::ROWS, P::kScaled>(macc, mml, r, d, acc, mx, ls);
         if (whole) {
           const float inv = 1.f / ls;
           const int tok = r / G;
@@ -408,7 +408,8 @@ __global__ void __launch_bounds__((DGeo<P, P::kRings>::THREADS), 1)
             const int r = e / (D / 4), d = (e - r * (D / 4)) * 4;
             float4 acc;
             float ls;
-            merge_pieces(slots, paged_slot_floats(kDRows, D), 2 * kDRows + r * D + d, r, b1, b2, acc, ls);
+            merge_pieces<P::kScaled>(slots, paged_slot_floats(kDRows, D), 2 * kDRows + r * D + d, r, b1,
+                                     b2, acc, ls);
             const float inv = 1.f / ls;
             const int tok = r / G;
             store4<T>(orow + (long long)tok * out_stride + (r - tok * G) * D + d,
@@ -533,7 +534,7 @@ __global__ void __launch_bounds__(2 * W * 32, 4 / W)
       const int r = e / (D / 4), d = (e - r * (D / 4)) * 4;
       float4 acc;
       float mx, ls;
-      join_states<D, W, C::ROWS>(macc, mml, r, d, acc, mx, ls);
+      join_states<D, W, C::ROWS, P::kScaled>(macc, mml, r, d, acc, mx, ls);
       *reinterpret_cast<float4 *>(macc + r * (D + 4) + d) = acc;
       if (d == 0) *reinterpret_cast<float2 *>(smem + r * 8) = make_float2(mx, ls);
     }
@@ -565,7 +566,7 @@ __global__ void __launch_bounds__(2 * W * 32, 4 / W)
         acc.y = fmaf(wgt, v[k].y, acc.y);
         acc.z = fmaf(wgt, v[k].z, acc.z);
         acc.w = fmaf(wgt, v[k].w, acc.w);
-        ls = fmaf(wgt, ml[k].y, ls);
+        ls = add_sum<P::kScaled>(ls, ml[k].y, ml[k].x - mx, wgt);
       }
     }
     const float inv = 1.f / ls;

@@ -239,12 +239,26 @@ __device__ __forceinline__ bool next_unit(const PagedArgs &a, Unit &u, const Uni
   return false;
 }
 
+// ls + l 2^d for a piece's sum l and d <= 0, w = 2^d.  kFar: d may be below float32's exponents
+// and l that much above 1 (kvs_rows_q8.cuh).
+template <bool kFar>
+__device__ __forceinline__ float add_sum(float ls, float l, float d, float w) {
+  if constexpr (kFar) {
+    float h;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(h) : "f"(0.5f * d));
+    return fmaf(h, h * l, ls);
+  } else {
+    return fmaf(w, l, ls);
+  }
+}
+
 // Four accumulator columns of one row, merged over a unit's pieces in column
 // order: range b1's piece began the unit (its slot 2 b1 + 1), those of ranges
 // b1 + 1 .. b2 continue it (slots 2 b).  A slot of `stride` floats has the
 // row's (m, l) at float2 `r` and its accumulators at float `at`.  Pieces are
 // taken eight at a time, all loads of a batch before the first is used, so a
 // batch costs one L2 round trip.
+template <bool kFar = false>
 static __device__ __forceinline__ void merge_pieces(const float *slots, size_t stride, int at,
                                                     int r, int b1, int b2, float4 &acc, float &l) {
   constexpr int kBatch = 8;
@@ -269,7 +283,7 @@ static __device__ __forceinline__ void merge_pieces(const float *slots, size_t s
     const float mz = mn == neg_inf_f() ? 0.f : mn;
     const float w = exp2f(m - mz);
     acc = make_float4(acc.x * w, acc.y * w, acc.z * w, acc.w * w);
-    l *= w;
+    l = kFar ? add_sum<true>(0.f, l, m - mz, w) : l * w;
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
       if (c + j <= b2) {
@@ -278,7 +292,7 @@ static __device__ __forceinline__ void merge_pieces(const float *slots, size_t s
         acc.y = fmaf(wj, v[j].y, acc.y);
         acc.z = fmaf(wj, v[j].z, acc.z);
         acc.w = fmaf(wj, v[j].w, acc.w);
-        l = fmaf(wj, ml[j].y, l);  // (a NaN sum stays one also under a zero weight)
+        l = add_sum<kFar>(l, ml[j].y, ml[j].x - mz, wj);  // (a NaN sum stays one also under a zero weight)
       }
     }
     m = mn;

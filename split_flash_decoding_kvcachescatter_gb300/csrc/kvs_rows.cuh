@@ -101,8 +101,8 @@ __device__ __forceinline__ void join_pieces(typename P::Rows &w, const float *sl
       v[j] = c == own ? make_float4(w.o[j][0], w.o[j][1], w.o[j][2], w.o[j][3])
                       : __ldcg(slot(c) + (j + 1) * kThreads);
     const float wt[2] = {ex2f(ml.x - mz[0]), ex2f(ml.z - mz[1])};
-    ls[0] = fmaf(wt[0], ml.y, ls[0]);  // (a NaN sum stays one also under a zero weight)
-    ls[1] = fmaf(wt[1], ml.w, ls[1]);
+    ls[0] = add_sum<P::kScaled>(ls[0], ml.y, ml.x - mz[0], wt[0]);  // (a NaN sum stays one also under a zero weight)
+    ls[1] = add_sum<P::kScaled>(ls[1], ml.w, ml.z - mz[1], wt[1]);
 #pragma unroll
     for (int j = 0; j < D / 8; ++j) {
       acc[j][0] = fmaf(wt[0], v[j].x, acc[j][0]);

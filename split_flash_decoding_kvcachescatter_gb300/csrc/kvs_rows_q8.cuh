@@ -11,8 +11,15 @@
 //          float32 rows as a high and a low part (22 bits).
 //   output (sum 2^x_j sv_b f_j) / (sum 2^x_j).  The running reference m is the
 //          maximum of x_j + log2 sv_b, and w_j = 2^(x_j + log2 sv_b - m) is the weight
-//          of f_j, at most 2^kLift, however the scales differ; the sum takes
+//          of f_j, at most 2^kLift, however the scales differ; the sum l takes
 //          w_j / sv_b.  Weights go into the product as a high and a low float16 part.
+// Scales of V reach up to 2^100, so a w_j could be below float32's range although w_j / sv_b
+// counts in the sum, and m may move by more than that range:
+//  - scales under 2^-60 of the largest so far count as that much: what they stand for is
+//    nothing beside it.  A w_j below 2^-126 is then less than 2^-76 of the sum: with sv* the
+//    scale of the key that made m, l >= 2^kLift / sv*, and w_j / sv_b < 2^-126 2^60 / sv*.
+//  - the sum is multiplied by 2^(m - m') in two steps of half the exponent: l is 2^-90 at
+//    least, a step 2^-86.
 #pragma once
 
 #include <cstdint>
@@ -38,10 +45,13 @@ __device__ __forceinline__ uint4 lds_u4(uint32_t addr) {
   return v;
 }
 
-// log2 of a scale of V, and its reciprocal; scales under 2^-60 count as 2^-60 (what
-// they stand for is nothing beside any other value, and 1 / scale stays in range).
+// The least that scales of V count as: 2^-60, so that 1 / scale stays in range, and 2^-60 of
+// the largest so far.
+constexpr float kLeastScale = 8.673617379884035e-19f;
+__device__ __forceinline__ float least_scale(float largest) { return kLeastScale * fmaxf(largest, 1.f); }
+
+// log2 of a scale of V (2^-60 at least), and its reciprocal.
 __device__ __forceinline__ void value_scale(float sv, float &lg, float &inv) {
-  sv = fmaxf(sv, 8.673617379884035e-19f);
   const unsigned u = __float_as_uint(sv);
   const float mant = __uint_as_float((u & 0x7fffffu) | 0x3f800000u);
   lg = (float)((int)(u >> 23) - 127) + (mant == 1.f ? 0.f : __log2f(mant));
@@ -92,6 +102,7 @@ struct RowsQ8 {
   float fac[2];  // of the rows' scores
   float o[D / 8][4];
   float m[2], l[2];
+  float svmax;  // the largest scale of V so far
   int lane;
 
   __device__ __forceinline__ void start(const T *q, long long q_stride, int w, int rows, int G,
@@ -102,6 +113,7 @@ struct RowsQ8 {
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
     const bool few = kFewForm && rows <= 8;
+    svmax = 0.f;
 #pragma unroll
     for (int hh = 0; hh < 2; ++hh) {
       m[hh] = neg_inf_f();
@@ -187,9 +199,12 @@ struct RowsQ8 {
     constexpr int HH = kFew ? 1 : 2;
     float lg[NB], inv[NB];
 #pragma unroll
+    for (int b = 0; b < NB; ++b) svmax = fmaxf(svmax, scales[NB + b]);
+    const float least = least_scale(svmax);
+#pragma unroll
     for (int b = 0; b < NB; ++b) {
       const float ks = scales[b] * sl2;
-      value_scale(scales[NB + b], lg[b], inv[b]);
+      value_scale(fmaxf(scales[NB + b], least), lg[b], inv[b]);
 #pragma unroll
       for (int j = 2 * b; j < 2 * b + 2; ++j)
 #pragma unroll
@@ -215,10 +230,11 @@ struct RowsQ8 {
       x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
       const float mn = fmaxf(m[hh], x - kLift);
       const float mb = mn == neg_inf_f() ? 0.f : mn;  // (no key so far: every weight is 2^-inf = 0)
-      alpha[hh] = ex2f(m[hh] - mb);
+      const float ah = ex2f(0.5f * (m[hh] - mb));
+      alpha[hh] = ah * ah;
       moved |= mn != m[hh];
       m[hh] = mn;
-      l[hh] *= alpha[hh];
+      l[hh] = l[hh] * ah * ah;
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
         const float up = lg[b] - mb;

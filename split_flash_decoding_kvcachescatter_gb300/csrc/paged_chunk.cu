@@ -537,7 +537,7 @@ __global__ void __launch_bounds__(kCThreads, 1)
         }
         tc_fence_after();
         // (the unit is read again there: in registers it would crowd out the row)
-        if (!finish_tile<T, D, true>(out, out_stride, &units[nq % kCUnits], tl, x, t, lane, live, tok, G, b,
+        if (!finish_tile<T, D, true, false>(out, out_stride, &units[nq % kCUnits], tl, x, t, lane, live, tok, G, b,
                                tm_o, m, l, stg, slots, counters, tag, epoch, d_status, s_last,
                                wg_barrier)) {
           failed = true;

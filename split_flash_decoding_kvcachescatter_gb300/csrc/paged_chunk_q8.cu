@@ -27,10 +27,10 @@
 // What bounds it: the turning.  A pair of tiles moves about 320 KB through shared
 // memory (pages in and out, float16 in, and what the products read), the pages come
 // from L2 with as many bytes on their way as the rings hold, and eight warps convert.
-// 4096 rows of 32 query heads on 8 kv heads of 128 behind 4096 keys: 343 us, where
+// 4096 rows of 32 query heads on 8 kv heads of 128 behind 4096 keys: 349 us, where
 // paged_chunk.cu takes about 255 for pages in 16 bits.
 // Measured at that shape: rings of a whole tile and rows that leave without a staging
-// area 343 us, 8 KB of staging and three quarters 402; two quarters a step 487; a
+// area 343 us at the time, 8 KB of staging and three quarters 402; two quarters a step 487; a
 // warp that copies for the turning ones 566 to 646; pages read straight into
 // registers 701; mma.sync units as the decode steps' 2966.
 
@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(kCqThreads, 1)
       const int tok = live ? t / G : tl.ntok - 1;
       const int last = f.p + tl.tok0 + tok;  // the row's last key
       const int first_last = f.p + tl.tok0;  // the tile's first row's
-      float m = neg_inf_f(), l = 0.f, fac = 1.f;
+      float m = neg_inf_f(), l = 0.f, fac = 1.f, lgmax = 0.f;
       for (int n = tl.lo; n < tl.hi; ++n) {
         const uint32_t ph = (uint32_t)(sb + n - tl.lo) & 1u;
         const int kt = kt0 + n - f.t_lo;
@@ -264,7 +264,10 @@ __global__ void __launch_bounds__(kCqThreads, 1)
           fac = __uint_as_float((unsigned)qfac[(nq & 1) * 256 + x * 128 + t] << 23);
         }
         const CqScales &sc = scales[kt % SR];
-        const float f = fac * sc.score, lg = sc.lg, inv = sc.inv;  // (f > 0)
+        const float f = fac * sc.score, lg0 = sc.lg;  // (f > 0)
+        // (2^-60 of the largest scale so far at the least: kvs_rows_q8.cuh)
+        lgmax = fmaxf(lgmax, lg0);
+        const float lg = fmaxf(lg0, lgmax - 60.f), inv = lg > lg0 ? ex2(-lg) : sc.inv;
         float r[kCN];
         tmem_ld64(tm_s, *reinterpret_cast<float(*)[64]>(&r[0]));
         tmem_ld64(tm_s + 64, *reinterpret_cast<float(*)[64]>(&r[64]));
@@ -288,7 +291,8 @@ __global__ void __launch_bounds__(kCqThreads, 1)
         // the reference moves only when the row's grows by more than 2^kCRescale
         // (rows that do not exist hold anything: they never ask for a rescale)
         const float m_ref = cm > m + kCRescale ? cm : m;
-        const float alpha = (m == neg_inf_f() || !live) ? 1.f : ex2(m - m_ref);
+        const float ah = (m == neg_inf_f() || !live) ? 1.f : ex2(0.5f * (m - m_ref)), alpha = ah * ah;
+        l = l * ah * ah;  // (in two steps: kvs_rows_q8.cuh)
         // P_x and O_x are free once the product before has read and written them
         if (n > tl.lo) {
           if (!__all_sync(0xffffffffu, mbar_wait<kPoll>(&pvdone[x], ph ^ 1u, abort))) {
@@ -324,7 +328,7 @@ __global__ void __launch_bounds__(kCqThreads, 1)
           }
           tmem_st16u(tm_p + ch * 16, w);
         }
-        l = fmaf((ls[0].x + ls[1].x) + (ls[0].y + ls[1].y), inv, l * alpha);
+        l = fmaf((ls[0].x + ls[1].x) + (ls[0].y + ls[1].y), inv, l);
         m = m_ref;
         tmem_wait_st();
         tc_fence_before();
@@ -342,7 +346,7 @@ __global__ void __launch_bounds__(kCqThreads, 1)
         }
         tc_fence_after();
         // (the unit is read again there: in registers it would crowd out the row)
-        if (!finish_tile<T, D, false>(out, out_stride, &units[nq % kCUnits], tl, x, t, lane, live, tok, G, b,
+        if (!finish_tile<T, D, false, true>(out, out_stride, &units[nq % kCUnits], tl, x, t, lane, live, tok, G, b,
                                tm_o, m, l, nullptr, slots, counters, tag, epoch, d_status, s_last,
                                wg_barrier)) {
           failed = true;
@@ -625,7 +629,7 @@ __global__ void __launch_bounds__(kCqThreads, 1)
       float most = a.scale;
 #pragma unroll
       for (int o = 4; o >= 1; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-      most = fmaxf(most, 8.673617379884035e-19f);  // 2^-60
+      most = fmaxf(most, kLeastScale);  // 2^-60
       float inv = __uint_as_float((254u << 23) - __float_as_uint(most));
       if (__float_as_uint(most) & 0x7fffffu) inv = 1.f / most;  // (no power of two)
       const __half2 by_h = __float2half2_rn(a.scale * inv);
