@@ -699,8 +699,8 @@ typedef struct kvs_paged_cache_q8 {
  * the rotation and q_out are the same; rotated k (in float32, not rounded to
  * the type) and v are rounded to the cache's numbers.  For every block (16
  * positions of a kv head) that gets rows, k and v apart, with a = the largest
- * |element| of the new rows:
- *     s = the least power of two with a <= 448 s, 2^-60 at least
+ * finite |element| of the new rows:
+ *     s = the least power of two with a <= 448 s, 2^-60 at least, 2^100 at most
  *     a new row is the first of its block: scale = s
  *     older rows are in it:                scale = max(s, old scale), and where
  *         that has grown, numbers of the older rows (those before the
@@ -711,8 +711,9 @@ typedef struct kvs_paged_cache_q8 {
  * whether its rows came in one call or in many, and its numbers only below
  * 2^-6.  Numbers and scales of no other rows and blocks are written.  A page
  * that gets rows, or whose last block holds the rows before them, must not be
- * shared by another sequence.  A NaN stays one and does not count for the
- * scale; infinities become the largest number.
+ * shared by another sequence.  A NaN stays one, and what is larger than 448 times
+ * its block's scale, infinities among it, becomes 448 (or -448); neither NaN nor
+ * infinities count for the scale.
  *
  *   q, k, v, q_out, inv_freq, rot_dim, scale  as for kvs_rope_scatter_paged
  *   dtype  kvs_dtype of q, k, v and q_out

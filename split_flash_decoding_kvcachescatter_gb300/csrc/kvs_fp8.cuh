@@ -16,13 +16,20 @@ namespace kvs {
 
 constexpr int kScaleBlock = 16;       // positions that share a scale
 constexpr int kLeastScaleExp = -60;   // no scale is below 2^-60
+constexpr int kMostScaleExp = 100;    // or above 2^100: 448 2^100 leaves room in float32
 
-// The least k >= -60 with most <= 448 2^k, as 2^k; most >= 0 (a NaN counts as 0).
+// The least k with most <= 448 2^k, -60 at least and 100 at most, as 2^k; most >= 0 (a NaN
+// counts as 0).
 __device__ __forceinline__ float scale_for(float most) {
   const unsigned u = __float_as_uint(most > 0.f ? most : 0.f);
   // most = 1.f 2^e and 448 = 1.75 2^8
   const int k = (int)(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
-  return __uint_as_float((unsigned)(max(k, kLeastScaleExp) + 127) << 23);
+  return __uint_as_float((unsigned)(min(max(k, kLeastScaleExp), kMostScaleExp) + 127) << 23);
+}
+
+// The larger of most and |x|; an infinity is passed over (0 x is NaN) as NaN is.
+__device__ __forceinline__ float finite_max(float most, float x) {
+  return fmaxf(most, fmaf(x, 0.f, fabsf(x)));
 }
 
 // Two numbers to e4m3 (nearest, ties to even; past 448 they become 448), a in the low byte.

@@ -3,8 +3,8 @@
 // launch.
 //
 // Mathematics: the rotation as in rope_scatter.cu.  A block of 16 positions of a
-// kv head shares a scale, the least power of two 2^k (k >= -60) that keeps every
-// row written to it within 448 2^k; its rows are rounded to e4m3 after division by
+// kv head shares a scale, the least power of two 2^k (-60 <= k <= 100) that keeps every
+// finite element written to it within 448 2^k; its rows are rounded to e4m3 after division by
 // it, which is exact.  Where a block holds older rows its scale can only grow, and
 // its older numbers are then divided by the growth and rounded again (exact down
 // to 2^-6, the end of e4m3's normal range).
@@ -214,8 +214,8 @@ __global__ void __launch_bounds__(kRqThreads)
       each(src, stride, is_k, [&](int, int, const float(&fx)[VE], const float(&fy)[VE], bool pair) {
 #pragma unroll
         for (int e = 0; e < VE; ++e) {
-          most = fmaxf(most, fabsf(fx[e]));
-          if (pair) most = fmaxf(most, fabsf(fy[e]));
+          most = finite_max(most, fx[e]);
+          if (pair) most = finite_max(most, fy[e]);
         }
       });
 #pragma unroll
@@ -472,8 +472,20 @@ __global__ void __launch_bounds__(kWThreads, sizeof(T) == 4 ? 3 : 4)
 #pragma unroll
           for (int e = 0; e < VE; ++e) most = fmaxf(most, fabsf(f[u][e]));
     }
-    // (sizes are ordered as integers; a NaN was passed over)
-    const unsigned top = __reduce_max_sync(0xffffffffu, __float_as_uint(most));
+    // (sizes are ordered as integers; a NaN was passed over, and infinities are once there are
+    // some: finite_max for all takes 42.3 us where this takes 41.4)
+    unsigned top = __reduce_max_sync(0xffffffffu, __float_as_uint(most));
+    if (top == 0x7f800000u) {
+      most = 0.f;
+#pragma unroll
+      for (int u = 0; u < UV; ++u) {
+        const int tok = is_k ? kt + 32 / PV * (u % U) : vt + 32 / kOfRow * u;
+        if (tok < mine)
+#pragma unroll
+          for (int e = 0; e < VE; ++e) most = finite_max(most, f[u][e]);
+      }
+      top = __reduce_max_sync(0xffffffffu, __float_as_uint(most));
+    }
     if (lane == 0) s_most[warp] = __uint_as_float(top);
     __syncthreads();
     if (!works || bad_page) continue;
