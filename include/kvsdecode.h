@@ -845,9 +845,10 @@ typedef struct kvs_sample_rules {
  *   rules        in   HOST struct of device pointers, or NULL: none
  *   token_ids    out  [M] int32, device, or NULL
  *   token_probs  out  [M] float32, device, or NULL
- *   probs        out  [M] rows of vocab_size float32, probs_stride apart, or NULL;
- *                     must not overlap logits
- * No output may overlap another one or the inputs.
+ *   probs        out  [M] rows of vocab_size float32, probs_stride apart, or NULL
+ * No output may overlap another one or the inputs, but token_ids or token_probs may
+ * take the uniforms' place (the same address).  OVERLAP is given for all of this but
+ * token_ids or token_probs over logits, which is not looked for.
  * Errors: DIMS (M < 0, vocab_size < 1, a stride too small), NULL (logits, uniforms,
  * or all three outputs), ALIGN, UNSUPPORTED (dtype; a vocabulary of more than 2^19
  * tokens; more than 2^30 rows), OVERLAP, LAUNCH.  M = 0 enqueues nothing.

@@ -1028,10 +1028,15 @@ def kvs_sample_logits(logits, uniforms, token_ids=None, temperature=None, top_k=
         0 if top_k is None else _vector(top_k, "top_k", i32, M, dev),
         0 if top_p is None else _vector(top_p, "top_p", f32, M, dev),
         0 if min_p is None else _vector(min_p, "min_p", f32, M, dev))
+    lp, ip = logits.data_ptr(), _vector(token_ids, "token_ids", i32, M, dev)
+    op = 0 if token_probs is None else _vector(token_probs, "token_probs", f32, M, dev)
+    row, step = V * logits.element_size(), ls * logits.element_size()
+    for p in (ip, op):  # (the library looks for every other overlap)
+        at = p - lp
+        if p and -4 * M < at < (M - 1) * step + row and not (row <= at % step <= step - 4 * M):
+            raise ValueError("kvs_sample_logits: token_ids and token_probs must not overlap logits")
     rc = lib().kvs_sample_logits(
-        logits.data_ptr(), ls, dt, M, V, _vector(uniforms, "uniforms", f32, M, dev), rules,
-        _vector(token_ids, "token_ids", i32, M, dev),
-        0 if token_probs is None else _vector(token_probs, "token_probs", f32, M, dev), pp, ps,
+        lp, ls, dt, M, V, _vector(uniforms, "uniforms", f32, M, dev), rules, ip, op, pp, ps,
         _get_stream(dev) if stream is None else _stream(stream))
     if rc != KVS_OK:
         raise KvsError(rc, "kvs_sample_logits")

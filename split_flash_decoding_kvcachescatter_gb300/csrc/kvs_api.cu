@@ -757,8 +757,20 @@ int kvs_sample_logits(const void *logits, int64_t logits_stride, int dtype, int 
                         (const void *)probs, (const void *)r.temperature, (const void *)r.top_k,
                         (const void *)r.top_p, (const void *)r.min_p})
     if (!aligned(p, 4)) return KVS_ERR_ALIGN;
-  if (probs && rows_overlap(row_span(logits, logits_stride, vocab_size, dtype),
-                            row_span(probs, probs_stride, vocab_size, KVS_F32), M))
+  // Outputs against the inputs and one another (a NULL meets nothing).
+  auto vec = [](const void *p) { return row_span(p, 1, 1, KVS_F32); };
+  auto meet = [&](const RowSpan &x, const RowSpan &y) { return x.at && y.at && rows_overlap(x, y, M); };
+  const RowSpan all = row_span(probs, probs_stride, vocab_size, KVS_F32);
+  if (meet(all, row_span(logits, logits_stride, vocab_size, dtype))) return KVS_ERR_OVERLAP;
+  for (const void *p : {(const void *)r.temperature, (const void *)r.top_k, (const void *)r.top_p,
+                        (const void *)r.min_p, (const void *)uniforms}) {
+    // (a row's id or probability may take its random number's place: it is read long before)
+    const bool in_place = p == uniforms;
+    if (meet(all, vec(p)) || (!(in_place && p == token_ids) && meet(vec(token_ids), vec(p))) ||
+        (!(in_place && p == token_probs) && meet(vec(token_probs), vec(p))))
+      return KVS_ERR_OVERLAP;
+  }
+  if (meet(all, vec(token_ids)) || meet(all, vec(token_probs)) || meet(vec(token_ids), vec(token_probs)))
     return KVS_ERR_OVERLAP;
   return kvs::launch_sample(logits, logits_stride, dtype, M, vocab_size, uniforms, r, token_ids,
                             token_probs, probs, probs_stride, reinterpret_cast<cudaStream_t>(stream));

@@ -40,3 +40,34 @@ def test_rows_of_a_small_top_k_in_flight_together(dtype, M, V, k):
     for g, o in zip(got, odds):
         assert torch.equal(g, want.expand(40, M))
         assert torch.equal(o, o[:1].expand(40, M))
+
+
+@pytest.mark.parametrize("M", [1, 5, 700])
+def test_a_row_s_result_in_its_random_number_s_place(M):
+    x = logits(M, 9000, seed=41)
+    k = torch.tensor([(0, 30, 1)[m % 3] for m in range(M)], dtype=torch.int32, device=DEV)
+    u = torch.tensor(uniforms(M, 42), device=DEV)
+    odds = torch.empty(M, device=DEV)
+    want = B.kvs_sample_logits(x, u, top_k=k, token_probs=odds)
+    a, b = u.clone(), u.clone()
+    B.kvs_sample_logits(x, a, token_ids=a.view(torch.int32), top_k=k)
+    assert torch.equal(a.view(torch.int32), want)
+    got = B.kvs_sample_logits(x, b, top_k=k, token_probs=b)
+    assert torch.equal(got, want) and torch.equal(b, odds)
+
+
+def test_the_binding_refuses_results_over_logits():
+    wide = torch.zeros(4, 128, device=DEV)
+    x, u = wide[:, :100], torch.zeros(4, device=DEV)
+    flat = wide.view(-1)
+    for at in (0, 3, 97, 128, 3 * 128 + 99):  # the first, a row's end, the next row, the last element
+        with pytest.raises(ValueError, match="logits"):
+            B.kvs_sample_logits(x, u, token_ids=flat[at:at + 4].view(torch.int32))
+        with pytest.raises(ValueError, match="logits"):
+            B.kvs_sample_logits(x, u, token_probs=flat[at:at + 4])
+    for at in (100, 124, 3 * 128 + 100):  # behind a row
+        assert B.kvs_sample_logits(x, u, token_ids=flat[at:at + 4].view(torch.int32)).tolist() == [0] * 4
+    for other in ("uniforms", "temperature", "top_p", "min_p"):
+        v = torch.full((5,), 0.5, device=DEV)
+        with pytest.raises(B.KvsError):
+            B.kvs_sample_logits(**{**dict(logits=x, uniforms=u), other: v[:4]}, token_probs=v[1:])
