@@ -151,6 +151,25 @@ __device__ __forceinline__ u64 share_of(float f, u64 x, bool &left) {
   return (lo >> s) | (hi << (64 - s));
 }
 
+// w / total for w <= 2^45, total < 2^64, to a rounding of float32 (2^-24 and 2^-44 of itself):
+// the reciprocal and w as sums of two floats, the product's first term exact.
+struct Divider {
+  float ih, il;
+  __device__ __forceinline__ explicit Divider(u64 total) {
+    const float th = __ull2float_rn(total);
+    const float tl = __ll2float_rn((long long)(total - (u64)th));  // (total <= 2^63: th is, too)
+    ih = __frcp_rn(th);
+    il = __fmul_rn(ih, __fmaf_rn(-ih, tl, __fmaf_rn(-ih, th, 1.f)));
+  }
+  __device__ __forceinline__ float operator()(u64 w) const {
+    const float a = __fmul_rn(__uint2float_rn((unsigned)(w >> 22)), 4194304.f);
+    const float b = __uint2float_rn((unsigned)w & 0x3fffffu);  // (both exact)
+    const float wh = __fadd_rn(a, b), wl = __fsub_rn(b, __fsub_rn(wh, a));
+    const float p = __fmul_rn(wh, ih);
+    return __fadd_rn(p, __fmaf_rn(wl, ih, __fmaf_rn(wh, il, __fmaf_rn(wh, ih, -p))));
+  }
+};
+
 struct alignas(16) SampleShared {  // (the keys lie behind it)
   // this block's amounts (tokens or weight), by bin; or the tokens it sends to block 0
   union {
@@ -675,7 +694,7 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(SampleArgs a) {
             if (t == 0) {
               const u64 w = s.item[i] - (i ? s.item[i - 1] : 0ull);
               if (a.ids) a.ids[m] = (int)~(unsigned)(s.out[i] >> 32);
-              if (a.token_probs) a.token_probs[m] = (float)((double)w / (double)total);
+              if (a.token_probs) a.token_probs[m] = Divider(total)(w);
             }
             __syncthreads();
             clear();
@@ -840,7 +859,7 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(SampleArgs a) {
         }
         if (here && at <= mark && mark < at + w) {
           if (a.ids) a.ids[m] = lo + j;
-          if (a.token_probs) a.token_probs[m] = (float)((double)w / (double)total);
+          if (a.token_probs) a.token_probs[m] = Divider(total)(w);
         }
         at += w;
       }
@@ -850,7 +869,7 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(SampleArgs a) {
       // ties up to position `cut` of the slice are kept; all of them where the last kept
       // one lies in a later block
       const int cut = s.cut >= 0 ? s.cut : seen_first + ctot <= kept ? n : -1;
-      const float inv = 1.f / __ull2float_rn(total);
+      const Divider share(total);
       float *to = a.probs + (long long)m * a.probs_stride + lo;
       auto prob = [&](int j, unsigned key) {
         u64 w = 0ull;
@@ -860,7 +879,7 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(SampleArgs a) {
         } else if (key == thr && key && j <= cut) {
           w = kept ? thr_w : 0ull;
         }
-        return __ull2float_rn(w) * inv;
+        return w ? share(w) : 0.f;
       };
       if ((reinterpret_cast<uintptr_t>(to) & 15u) == 0u) {
         for (int j = 4 * t; j < n; j += 4 * kSThreads) {

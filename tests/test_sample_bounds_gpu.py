@@ -71,3 +71,31 @@ def test_the_binding_refuses_results_over_logits():
         v = torch.full((5,), 0.5, device=DEV)
         with pytest.raises(B.KvsError):
             B.kvs_sample_logits(**{**dict(logits=x, uniforms=u), other: v[:4]}, token_probs=v[1:])
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("V", [50, 5000, 152064])
+def test_a_token_s_probability_is_one_number(dtype, V):
+    """The token's probability, the one of its place among all, and that of the call without all."""
+    M = 64
+    x = logits(M, V, dtype, seed=43)
+    u = torch.tensor(uniforms(M, 44), device=DEV)
+    k = torch.tensor([(0, 50, 7, 400)[m % 4] for m in range(M)], dtype=torch.int32, device=DEV)
+    p = torch.tensor([(1.0, 0.9)[m // 4 % 2] for m in range(M)], device=DEV)
+    odds, alone, probs = (torch.empty(M, device=DEV), torch.empty(M, device=DEV), torch.empty(M, V, device=DEV))
+    ids = B.kvs_sample_logits(x, u, top_k=k, top_p=p, token_probs=odds, probs=probs)
+    B.kvs_sample_logits(x, u, top_k=k, top_p=p, token_probs=alone)
+    assert torch.equal(odds, probs.gather(1, ids.long()[:, None])[:, 0])
+    assert torch.equal(odds, alone)
+    # one rounding to float32: weights are off by 2^-37 of themselves and 2^-45 of the largest, of
+    # which the sum has at most that many, and all of it once more for the sum
+    host = x.double()
+    order = torch.argsort(host, dim=1, descending=True, stable=True)
+    w = torch.exp(host - host.amax(1, keepdim=True))
+    kk = torch.where(k > 0, k, V).long()
+    rank = torch.empty_like(order).scatter_(1, order, torch.arange(V, device=DEV).expand(M, V))
+    w = torch.where(rank < kk[:, None], w, 0)
+    plain = p == 1
+    want = (w / w.sum(1, keepdim=True))[plain]
+    over = (probs[plain].double() - want).abs() - want * (2.0 ** -24 + 2.0 ** -35) - 2.0 ** -45 * (1 + V * want)
+    assert (over <= 0).all()
