@@ -828,9 +828,12 @@ int kvs_process_logits(const void *logits, int64_t logits_stride, void *out, int
  * token_probs[m] is that token's weight over the sum of the kept ones, probs[m][j]
  * the same for every id (0 for those not kept).  NaN and -inf are never drawn; a row
  * without anything above -inf gives token 0 and probabilities 0; where a logit is
- * +inf, those tokens share the row.  Weights below 2^-45 of the largest count as 0;
- * others are computed to 2^-37 of themselves and summed exactly, so the result does
- * not depend on the order of anything.
+ * +inf, those tokens share the row.  Weights are whole multiples of 2^-44 of the
+ * largest, off by 2^-37 of themselves and 2^-45 of the largest at most (so those below
+ * that count as 0), and summed exactly: the result does not depend on the order of
+ * anything, and another token than the formulas' is drawn only where u, p or l lies so
+ * near to a border: u and p within 2^-36 + vocab_size 2^-44.  Probabilities are rounded
+ * to float32 once.
  */
 typedef struct kvs_sample_rules {
   const float *temperature; /* device [M], or NULL: 1 */

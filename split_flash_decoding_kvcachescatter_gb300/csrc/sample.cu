@@ -11,9 +11,11 @@
 // first id at which the running sum of kept weights, in the order of ids, exceeds u
 // times their sum.
 //
-// Weights are integers, w 2^44 rounded, computed to 2^-37 of themselves (below), so
+// Weights are integers, w 2^44 computed to 2^-37 of itself (below) and rounded, so
 // sums are exact whatever their order, and a token is drawn wrongly only where u falls
-// within about 2^-37 of a border between two tokens.
+// within 2^-36 + V 2^-44 of a border between two tokens: the sum up to a border and that of
+// the row are each off by 2^-37 of themselves and by V roundings of 2^-45 of the largest
+// weight.  (More bits a weight would not fit: 2^19 tokens of 2^44 make 2^63.)
 //
 // A thread-block cluster takes a row; block r owns an equal slice of the ids and keeps
 // their logits in shared memory.  One histogram over the distance from the largest
@@ -106,7 +108,8 @@ struct Weigher {
   // e^((x - top) / T) 2^44.  y = (x - top) log2(e) / T as a sum of two floats (off by
   // 2^-46 of it); y = n + i / 256 + r with |r| <= 2^-9; z = 2^r - 1 = e^(r ln 2) - 1 by its
   // series: the first term in two floats, the others, below 2^-19, in one; then 2^(i / 256)
-  // (1 + z) in integers, z in units of 2^-40.  Off by 2^-37 of itself at most.
+  // (1 + z) in integers, z in units of 2^-40.  Off by 2^-37 of itself at most, and the last
+  // shift by half a unit.
   __device__ __forceinline__ u64 operator()(unsigned key) const {
     if (key == 0u) return 0ull;
     const float x = Keys<T>::logit(key);

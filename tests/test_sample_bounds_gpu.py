@@ -99,3 +99,67 @@ def test_a_token_s_probability_is_one_number(dtype, V):
     want = (w / w.sum(1, keepdim=True))[plain]
     over = (probs[plain].double() - want).abs() - want * (2.0 ** -24 + 2.0 ** -35) - 2.0 ** -45 * (1 + V * want)
     assert (over <= 0).all()
+
+
+def tail_rows(V, low, high, seed, M):
+    """One token of weight 1 behind V - 1 others of weights 2^-high to 2^-low, their exact weights."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    e = low + (high - low) * torch.rand(V, generator=g, device=DEV, dtype=torch.float64)
+    x = (-e * 0.6931471805599453).float()
+    x[V - 1] = 0.0
+    return x.expand(M, V).contiguous(), torch.exp(x.double())
+
+
+@pytest.mark.parametrize("V", [4097, 152064, 2 ** 19])
+@pytest.mark.parametrize("low,high", [(40, 46), (44.4, 44.4), (45.2, 45.2), (30, 46)])
+def test_long_tails_of_the_smallest_weights(V, low, high):
+    """A weight is off by 2^-37 of itself and 2^-45 of the largest, so borders between tokens are by
+    2^-36 + V 2^-44 and probabilities by what follows; many weights near the end all at once."""
+    M = 96
+    x, w = tail_rows(V, low, high, 51, M)
+    run = torch.cumsum(w, 0)
+    total = run[-1]
+    # random numbers within the tail, and some behind it
+    u = (torch.rand(M, generator=torch.Generator().manual_seed(52), dtype=torch.float64).to(DEV) * 1.25 *
+         (run[-2] / total)).float()
+    probs, odds = torch.empty(M, V, device=DEV), torch.empty(M, device=DEV)
+    ids = B.kvs_sample_logits(x, u, token_probs=odds, probs=probs).long()
+    eps = 2.0 ** -36 + V * 2.0 ** -44
+    below = torch.where(ids > 0, run[(ids - 1).clamp_min(0)], 0) / total
+    assert (below - eps <= u.double()).all() and (u.double() <= run[ids] / total + eps).all()
+    want = (w / total).expand(M, V)
+    err = want * (2.0 ** -24 + 2.0 ** -35) + 2.0 ** -45 * (1 + V * want)
+    assert ((probs.double() - want).abs() <= err).all()
+    assert torch.equal(odds, probs.gather(1, ids[:, None])[:, 0])
+
+
+@pytest.mark.parametrize("V", [4097, 152064])
+def test_min_p_near_the_end_of_the_weights(V):
+    M = 4
+    x, w = tail_rows(V, 40, 46, 53, M)
+    least = torch.tensor([2.0 ** -41, 2.0 ** -43.5, 2.0 ** -44, 2.0 ** -45], device=DEV)
+    probs = torch.empty(M, V, device=DEV)
+    B.kvs_sample_logits(x, torch.zeros(M, device=DEV), min_p=least, probs=probs)
+    for m in range(M):
+        slack = w * 2.0 ** -37 + 2.0 ** -45
+        kept = probs[m] > 0
+        cut = float(least[m])
+        assert kept[w - slack > cut].all() and not kept[w + slack < cut].any()
+
+
+def test_top_p_over_a_tail_near_the_end_of_the_weights():
+    """The shortest run from the front, within what the sums of a large vocabulary may be off."""
+    V = 2 ** 19
+    x, w = tail_rows(V, 40, 46, 54, 3)
+    order = torch.argsort(x[0], descending=True, stable=True)
+    run = torch.cumsum(w[order], 0)
+    share = (run[[V // 5, V // 2, V - 1000]] / run[-1]).float().clamp_max(1 - 2.0 ** -24)
+    probs = torch.empty(3, V, device=DEV)
+    B.kvs_sample_logits(x, torch.zeros(3, device=DEV), top_p=share, probs=probs)
+    eps = 2.0 ** -36 + V * 2.0 ** -44
+    for m in range(3):
+        kept = probs[m, order] > 0
+        n, p = int(kept.sum()), float(share[m])
+        assert p < 1 and kept[:n].all()
+        assert run[n - 1] / run[-1] >= p - eps and (n == 1 or run[n - 2] / run[-1] < p + eps)
