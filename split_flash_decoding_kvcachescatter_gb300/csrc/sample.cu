@@ -591,23 +591,15 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(SampleArgs a) {
       k_open = p_open = false;
     }
     if (k_open && near) {
-      // Where this block alone has k maxima of groups of its tokens, the k-th of those is at
+      // Where this block alone has k maxima of its threads' tokens, the k-th of those is at
       // most the row's k-th logit: what lies in lower bins than it need not be counted.
-      // (Each count is a shared-memory atomic on a place of its own, some 17 cycles a warp.)
-      const bool by_thread = 2 * k <= kSThreads;  // groups: a thread's tokens, or a vector's
+      // (Each count is a shared-memory atomic on a place of its own, some 17 cycles a warp.
+      // For larger k the maxima of vectors bound it too, but cost more than they spare: one row
+      // of 152,064, k = 300 26.3 us with them, 24.4 without.)
+      const bool by_thread = 2 * k <= kSThreads;
       int bound = 0;
-      if (by_thread || 4 * k <= vecs) {
-        if (by_thread) {
-          if (own_most) atomicAdd(&s.low[near_bin(own_most)], 1u);
-        } else {
-          for (int j = t; j < vecs; j += kSThreads) {
-            const Vec<Key, VE> v = *reinterpret_cast<const Vec<Key, VE> *>(keys + j * VE);
-            unsigned w = v.e[0];
-#pragma unroll
-            for (int e = 1; e < VE; ++e) w = max(w, (unsigned)v.e[e]);
-            if (w) atomicAdd(&s.low[near_bin(w)], 1u);
-          }
-        }
+      if (by_thread) {
+        if (own_most) atomicAdd(&s.low[near_bin(own_most)], 1u);
         __syncthreads();
         find_bin<true>(s, [&](u64) { return (u64)k; });
         bound = max(s.bin, 0);
@@ -627,6 +619,8 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(SampleArgs a) {
           gather(bound, true, 1u, true);
           n = (int)min((unsigned)ld_dsmem_s32(dsmem_addr(&s.total[(gathers - 1) & 1], 0)), (unsigned)kSMost + 1u);
           have = whole = n <= kSMost;
+          // (128 and less are sorted as they are.  One row of 152,064, k = 20 and 50: 12.0 and 12.6
+          // us from 65 or from 129 on, 14.6 and 12.7 from 257 on, 14.7 and 18.5 never.)
           if (have && rank == 0 && n > 128) {  // those of the bins above the k-th's and of its own
             const u64 v0 = t < n ? s.item[t] : 0ull, v1 = t + kSThreads < n ? s.item[t + kSThreads] : 0ull;
             __syncthreads();  // (the counts' place is clear)
@@ -983,6 +977,15 @@ int launch_sample_impl(SampleArgs a, cudaStream_t stream) {
   };
   // The largest cluster whose clusters for all M rows are resident at once, with
   // slices of 2048 ids or more; where none is, the smallest whose slices fit.
+  // Slices, us at least 512, 1024, 2048, 4096, 8192 ids under top-p 0.9: one row of 9000
+  // 15.3, 14.5, 15.9, 19.1, 25.1, of 32,001 17.1, 17.1, 18.7, 23.2, 34.1; nine of 32,001
+  // 23.3, 23.3, 19.5, 24.4, 35.9.
+  // More rows than are resident: few large blocks keep more of the SM's shared memory busy
+  // where the vocabulary lets two a block be, and lose where a block takes an SM for itself.
+  // us by the rule and by clusters of 8, 152,064 in float32, top-p 0.95, a top-k for every
+  // other row: 36 rows 64 and 64, 38 83 and 66, 64 136 and 102, 128 212 and 171; top_k 50
+  // for all: 38 35 and 30, 128 92 and 78; in bfloat16 without a top-k: 38 107 and 95, 64 110
+  // and 127, 100 253 and 186; 32,001 in bfloat16: 38 35 and 41, 64 37 and 54, 128 55 and 100.
   auto resident = [&](int k) { return bytes_of(k) > si->smem ? 0 : si->active[bytes_of(k) <= si->two][k]; };
   int k = si->top;
   while (k >= 0 && (a.M > resident(k) || (a.V >> k) < 2048)) --k;
