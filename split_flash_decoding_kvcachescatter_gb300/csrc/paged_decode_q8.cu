@@ -29,7 +29,19 @@ struct PagesQ8 : LinesQ8<D_, RowsQ8<Type, D_>::KT> {
   // as PlainPages'; 32 sequences of up to 8192 keys in bfloat16 took 66.3 us at 96 KB, 58.3 at 192,
   // 60.6 at 384, 65.6 at 768
   static constexpr int kFixBytes = 192 << 10;
+  // us by clusters and by equal ranges, bfloat16, all of full length, H 32 / 8, D 128:
+  //   sequences x keys       1x16384   4x8192  16x2048  32x1024  64x1024  32x2048  64x2048  16x4096
+  //   KB a block                 256      512      512      256      256      512      512     1024
+  //   clusters                  19.1     19.9     19.6     24.1     46.2     37.6     73.3     33.0
+  //   equal ranges              19.7     22.4     24.8     27.0     42.1     36.4     60.8     33.6
+  //   1/8 to all, clusters      14.4     19.3     18.7     20.5     37.1     30.9     53.6     32.5
+  //   the same, ranges          17.5     19.1     20.7     23.2     35.3     29.4     46.0     26.8
+  // (H 14 / 2, D 64, 16 x 16384, 512 KB: 20.8 and 22.5, 20.1 and 18.0.)  Twice as much a block
+  // loses up to a fifth where lengths differ, half as much 5 us for one to 16 sequences.
   static constexpr long long kBlockBytes = 512 << 10;
+  // us with half a block an SM and with a whole one, 64 x 256, 512, 1024, 2048 keys: 20.5, 29.2,
+  // 45.5, 77.9 and 24.7, 32.1, 46.2, 73.3; of 1/8 to all 19.2, 25.7, 39.1, 63.5 and 23.6, 27.9,
+  // 37.1, 53.6 (64, 128, 256, 512 KB a unit)
   static constexpr long long kShortBytes = 128 << 10;
 };
 
