@@ -60,10 +60,4 @@ __device__ __forceinline__ void st_dsmem_u64(uint32_t a, unsigned long long v) {
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(a), "l"(v) : "memory");
 }
 
-__device__ __forceinline__ unsigned long long ld_dsmem_u64(uint32_t a) {
-  unsigned long long v;
-  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(a));
-  return v;
-}
-
 }  // namespace kvs

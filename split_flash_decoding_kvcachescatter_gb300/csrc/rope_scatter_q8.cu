@@ -225,6 +225,7 @@ __global__ void __launch_bounds__(kRqThreads)
         scale = old;
       } else {
         if (in > 0) requantise(reinterpret_cast<unsigned *>(block), in * a.D / 4, lane, 32, old / scale);
+        __syncwarp();  // every lane has read the old scale
         if (lane == 0) *scale_at = scale;
       }
       const float inv = 1.f / scale;
