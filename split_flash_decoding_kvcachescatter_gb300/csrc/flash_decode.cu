@@ -255,11 +255,17 @@ __device__ __forceinline__ Run next_run(const Run &r, long long remaining, const
 // owns (query head, float4 column) outputs and takes the runs in batches of
 // MB, issuing all of a batch's loads -- (m, l) and accumulator -- before it
 // uses any, so a batch costs one L2 round trip.
+//
+// The warps meet at `mbar`, the consumers' barrier, in its phase `mphase` and an even
+// number of phases on, in bounded waits: a warp whose own wait just before ran out is
+// gone, although the others' found the phase complete, and a barrier of the hardware
+// would never open without it.  False when a wait ran out.
 // ---------------------------------------------------------------------------
-template <int D, int G, int NW>
-__device__ __noinline__ void merge_runs(const WsView &ws, float *out, int i, int g, int M, int Hkv,
+template <int D, int G, int NW, bool kPoll>
+__device__ __noinline__ bool merge_runs(const WsView &ws, float *out, int i, int g, int M, int Hkv,
                            long long S, int L, long long R, int P, int chunk, int cost,
-                           unsigned char *scratch) {
+                           unsigned char *scratch, uint64_t *mbar, uint32_t mphase,
+                           volatile int *abort) {
   constexpr int LPR = D / 4;
   constexpr int NT = NW * 32;
   constexpr int NE = (G * LPR + NT - 1) / NT;
@@ -268,6 +274,14 @@ __device__ __noinline__ void merge_runs(const WsView &ws, float *out, int i, int
   int *s_n = s_list + kMergeWindow;
   const int t = threadIdx.x;
   const int lane = t & 31;
+  auto meet = [&]() -> bool {  // (every lane the same: see consumers_barrier)
+    __syncwarp();
+    if (lane == 0) mbar_arrive(mbar);
+    bool got = mbar_wait<kPoll>(mbar, mphase, abort);
+    if (kPoll) got = __all_sync(0xffffffffu, got);
+    mphase ^= 1u;
+    return got;
+  };
   const int H = Hkv * G;
   const int n = (L + chunk - 1) / chunk;
   const long long c0 = S + cost;  // cost row where chunk 0 of (i, g) starts
@@ -306,7 +320,7 @@ __device__ __noinline__ void merge_runs(const WsView &ws, float *out, int i, int
       if (sl >= 0) s_list[__popc(ballot & ((1u << lane) - 1u))] = sl;
       if (lane == 0) *s_n = __popc(ballot);
     }
-    consumer_sync(NT);
+    if (!meet()) return false;
     const int nb = *s_n;
     for (int r0 = 0; r0 < nb; r0 += MB) {
       const int nr = min(MB, nb - r0);
@@ -351,7 +365,7 @@ __device__ __noinline__ void merge_runs(const WsView &ws, float *out, int i, int
         mq[q] = mb;
       }
     }
-    consumer_sync(NT);  // every thread has read the list before it is rewritten
+    if (!meet()) return false;  // every thread has read the list before it is rewritten
   }
   float4 *o4 = reinterpret_cast<float4 *>(out) + ((size_t)i * H + (size_t)g * G) * LPR;
 #pragma unroll
@@ -362,6 +376,7 @@ __device__ __noinline__ void merge_runs(const WsView &ws, float *out, int i, int
       o4[e] = make_float4(a[q].x * inv, a[q].y * inv, a[q].z * inv, a[q].w * inv);
     }
   }
+  return true;
 }
 
 // ---------------------------------------------------------------------------
@@ -659,8 +674,11 @@ __global__ void __launch_bounds__(Geo<D, G>::THREADS, 2)
       if (!consumers_barrier()) return;
       if (*s_last) {  // every run of (i, g) is in: merge them
         __threadfence();
-        merge_runs<D, G, C::NW>(ws, out, i_seq, g_kv, M, Hkv, dsc.S, dsc.L, R, P, chunk, kCost,
-                                smem + C::OFF_MACC);
+        if (!merge_runs<D, G, C::NW, kPoll>(ws, out, i_seq, g_kv, M, Hkv, dsc.S, dsc.L, R, P, chunk,
+                                            kCost, smem + C::OFF_MACC, mbar, mphase, abort)) {
+          if (lane == 0) give_up(abort, d_status, ws.epoch);
+          return;
+        }
       }
     }
     tile_reset<G>(acc, m_run, l_lane);  // the next run starts from nothing
