@@ -152,7 +152,7 @@ __device__ __forceinline__ void drain_ring(const Rings &rg, int ring, uint32_t n
 }
 
 // The ring's tiles of [t_lo, t_hi) against the warp's rows; n as in
-// fill_ring.  False when a wait ran out; poison: a bad page was among them.
+// fill_rings.  False when a wait ran out; poison: a bad page was among them.
 template <class P, int W, bool kPoll, bool kFew>
 __device__ __forceinline__ bool consume_tiles(typename P::Rows &w, const Rings &rg, int ring, int t_lo,
                                              int t_hi, int keys, const int (&reach)[2], float sl2,

@@ -1,5 +1,5 @@
 // paged_attention.cu -- attention of a ragged batch's new tokens over a paged
-// KV cache: the choice of kernel, and the kernel for chunks in float32.
+// KV cache: the choice of kernel, and chunks in float32 (the kernel: kvs_rows.cuh).
 //
 // Mathematics: flash attention over a split key axis.  For a row (token,
 // query head) and a set of keys, (m, l, acc) = (max s_j, sum 2^(s_j - m),
@@ -19,11 +19,11 @@
 //
 // Kernels: rows that a unit's 16 can hold (max_new G <= 16: a decode step)
 // paged_decode.cu; more rows in 16 bits paged_chunk.cu (tcgen05); more rows
-// in float32 the one here, on mma.sync: float32 as three TF32 products of a
+// in float32 kvs_rows.cuh's, on mma.sync: float32 as three TF32 products of a
 // high and a low part (hi hi + hi lo + lo hi), off by 2^-21 of it at most (lo lo 2^-22,
 // a lost bit of each lo 2^-23).
 //
-// Measured (the one here): 1001 new tokens of three sequences over up to 2048, H 14 / 2, D 64:
+// Measured (chunks in float32): 1001 new tokens of three sequences over up to 2048, H 14 / 2, D 64:
 // 57 to 74 us by the positions (65 us at 3.7 GFLOP, whose three TF32 products
 // would take 36 us at the 303 TFLOP/s that mma.sync reaches here; splitting the
 // operands and the softmax take the rest).  At positions where it took 82 us:

@@ -12,7 +12,8 @@
 // the scales differ; a tile's share of the row sum is its weights' sum over V's scale.
 // bfloat16 rows of q are brought to 2^15 by a power of two (exact down to 2^-28 of
 // the row's largest element).  Weights are rounded to float16 for the product: they
-// keep 11 bits for bfloat16 too.
+// keep 11 bits for bfloat16 too.  (A second part of them, as the decode steps have, would
+// take 128 columns of tensor memory, of which heads of 128 leave none.)
 //
 // Block (20 warps, one block an SM):
 //   warps 0-3, 4-7  softmax of tile A and of tile B

@@ -19,7 +19,7 @@
 // The other kernel, for any head: a warp a head of a 16-position block at a time, the rows
 // of K and V read twice.
 // Measured (32 query heads on 8 kv heads of 128, bfloat16): 8192 rows of prompts 41 us, 66% of
-// what a copy of the same bytes takes; by the other kernel 82; 16 rows a warp 64, eight of them
+// what a copy of the same bytes takes; by the other kernel 82 (with 64 or 32 of 128 turned, too); 16 rows a warp 64, eight of them
 // with q's angles made by every warp 72 to 78.  A decode step of 32 tokens: 3.2 us, a launch
 // and four dependent reads.
 

@@ -30,8 +30,8 @@
 //
 // Bound: bytes (a row is read once); what it takes is a chain of short phases (a cluster
 // barrier each 0.6 us) and, without a top-k, the instructions of a weight for every token.
-// Measured: one row of 152,064 in float32 17 us, 32 rows 57, 67 of 32,001 in bfloat16 36, 24 of
-// 152,064 in float16 with all probabilities 55.  By digits of the bits alone, 64-bit atomics
+// Measured: one row of 152,064 in float32 17 us (23 by other rules), 32 rows 56, 67 of 32,001 in
+// bfloat16 36, 24 of 152,064 in float16 with all probabilities 55.  By digits of the bits alone, 64-bit atomics
 // for the weights 73 (one row) and 229 (32), pairs of 32-bit ones 39 and 77; the histogram over
 // the distance 19 and 65; weights in fewer steps, one thread for 1 / T and bounds that spare
 // the counting 18 and 58.  (Small k by the row's histogram: one row 18.)
